@@ -362,6 +362,134 @@ MSA_API msa_status msa_vs_expand(const msa_shape* shape, const msa_vs_index* ind
                          int32_t u_count, int32_t range_cap, int32_t col_cap, int32_t* range_cnt,
                          int32_t* ranges, int32_t* col_cnt, int32_t* cols, void* stream);
 
+/* ---------------------------------------------------------------- paged KV cache
+ * What a prefill needs before it (queries and keys normed, rotated and laid
+ * out) and a decode step after it (a cache and the attention that reads it).
+ * No counterpart in the pages, which stop at the prefill: "KV is written in
+ * full" (MInference page) is all they say of the cache.
+ *
+ * A cache is a pool of pages: K and V [num_pages, Hkv, page_size, d_h] bf16,
+ * page_size 16, 32, 64 or 128 tokens (else MSA_ERR_UNSUPPORTED).  ("Page", as
+ * a block is a 64-row attention block here.)  Token x of request b lies in row
+ * x % page_size of page page_table[b][x / page_size]; its slot is
+ * page * page_size + row.  num_pages * page_size < 2^31. */
+typedef struct {
+  void* k; /* [num_pages, Hkv, page_size, d_h] bf16 */
+  void* v;
+  int32_t num_pages, page_size;
+} msa_kv_pages;
+
+/* The requests that share a pool of pages, and its free pages (device buffers
+ * owned by the caller).  A page belongs to at most one request. */
+typedef struct {
+  int32_t n_seqs, num_pages, page_size;
+  int32_t max_pages;    /* columns of page_table */
+  int32_t* page_table;  /* [n_seqs, max_pages]; entries at or above ceil(seq_len / page_size) are unspecified */
+  int32_t* seq_len;     /* [n_seqs] tokens held */
+  int32_t* free_pages;  /* [num_pages] stack: the first state[0] entries are free */
+  int32_t* state;       /* [4]: free pages, requests the last call refused, 0, 0 (start: {count, 0, 0, 0}) */
+} msa_page_pool;
+
+/* Take every request of the pool from seq_len to new_len, in one launch with
+ * no host synchronisation (the lengths stay on the device).  Growing requests
+ * are granted pages, shrinking ones (finished: 0; rejected drafted tokens)
+ * give pages back, in (request, page) order: pages given back are granted
+ * first, then the top of the stack down; what is left over goes on top, first
+ * released uppermost, so growing and shrinking by the same amounts restores
+ * the stack exactly.  page_table, seq_len, free_pages and state are updated.
+ *
+ * A request is refused (its length, pages and tokens stay as they were, and
+ * state[1] counts it) when it needs pages and the pages needed by the requests
+ * up to and including it exceed the free and released ones; when its new
+ * tokens do not fit (below); or when a length is negative or above max_pages *
+ * page_size (this also sets MSA_ERR_INDEX for the next poll, as do a page id
+ * outside the pool and a pool whose tables and stack together hold more than
+ * num_pages pages, of which nothing is changed).
+ *
+ * Token outputs (slots NULL: none).  seq_tokens = T > 0: padded, token i of
+ * request s at s * T + i of [n_seqs, T] outputs, and a request that grows by more than T
+ * is refused (and MSA_ERR_INDEX set).  seq_tokens = 0: packed, at cu_new[s] + i of [tok_cap] outputs,
+ * requests refused from the first whose tokens would end above tok_cap.
+ *   slots      cache slot of each new token, -1 where there is none
+ *   positions  (nullable) old length + i, or + depth[index] when depth is
+ *              given (a drafted tree's token sits at its depth); -1 where none
+ *   cu_new     (nullable) [n_seqs + 1] new tokens of the requests before
+ * new_len, depth and the outputs must not overlap the pool.  At most 8192
+ * requests (else MSA_ERR_UNSUPPORTED).  Calls on one pool must be ordered. */
+MSA_API msa_status msa_build_page_tables(const msa_page_pool* pool, const int32_t* new_len, const int32_t* depth,
+                                         int32_t seq_tokens, int32_t tok_cap, int32_t* cu_new, int32_t* slots,
+                                         int32_t* positions, void* stream);
+
+/* How msa_qk_norm_rope treats a head.  The pointers to weights are device
+ * memory, inv_freq is a host array that the call reads before it returns. */
+typedef struct {
+  int32_t norm;         /* 1: x / sqrt(mean(x^2) + eps) * weight per head of q and k; 0: none */
+  float eps;            /* >= 0 */
+  const void* q_weight; /* [d_h] bf16, NULL: ones */
+  const void* k_weight;
+  int32_t rot_dim;      /* leading columns that rotate: a multiple of 16 in [0, d_h] */
+  int32_t interleaved;  /* pairs (2i, 2i+1); 0: pairs (i, i + rot_dim/2) */
+  double theta;         /* angle of pair i = position * theta^(-2i / rot_dim); <= 0: 10000 */
+  const double* inv_freq; /* [rot_dim / 2] instead of theta's, or NULL */
+  float rot_scale;      /* factor on cosine and sine; 0: 1 */
+} msa_rope_cfg;
+
+/* Norm of every query and key head and rotation by position, from the
+ * projection's token-major rows into the layouts this library reads, one pass,
+ * fp32 with one rounding (the normed value is not rounded before it rotates).
+ * Input token t = b * n + i: query heads at q_in + t * q_stride (elements), Hq
+ * consecutive heads of d_h; k_in and v_in likewise with Hkv heads (parts of
+ * one fused row have its length as stride; strides multiples of 8, bases
+ * 16-byte aligned).  v_in may be NULL (then v and pages must be).
+ *   q         [B, Hq, n, d_h]
+ *   k, v      [B, Hkv, n, d_h] (nullable when pages are given)
+ *   pages     (nullable) K and V also go to the cache at slots[t]; a negative
+ *             slot is not stored, one outside the pool neither, and the next
+ *             poll returns MSA_ERR_INDEX
+ *   positions [B * n], any int32 (angles are exact to about 2^-31 turns
+ *             wherever the position lies); NULL: the index in the sequence
+ * Outputs must not overlap inputs. */
+MSA_API msa_status msa_qk_norm_rope(const msa_shape* shape, const msa_rope_cfg* cfg, const void* q_in,
+                                    int64_t q_stride, const void* k_in, int64_t k_stride, const void* v_in,
+                                    int64_t v_stride, const int32_t* positions, void* q, void* k, void* v,
+                                    const msa_kv_pages* pages, const int32_t* slots, void* stream);
+
+/* The same for packed sequences of different lengths: input token t =
+ * cu_seqlens[s] + i (host array, as for msa_prefill_layer_varlen), outputs in
+ * the varlen layout (sequence s one [H, n_s, d_h] block at element H *
+ * cu_seqlens[s] * d_h).  shape gives Hq, Hkv and d_h. */
+MSA_API msa_status msa_qk_norm_rope_varlen(const msa_shape* shape, const int32_t* cu_seqlens, int32_t n_seqs,
+                                           const msa_rope_cfg* cfg, const void* q_in, int64_t q_stride,
+                                           const void* k_in, int64_t k_stride, const void* v_in, int64_t v_stride,
+                                           const int32_t* positions, void* q, void* k, void* v,
+                                           const msa_kv_pages* pages, const int32_t* slots, void* stream);
+
+/* Workspace bytes of msa_attn_tree (0 on an invalid shape). */
+MSA_API size_t msa_attn_tree_workspace(const msa_shape* shape);
+
+/* Attention of drafted tokens over the paged cache: shape.B requests, shape.n
+ * rows each (1: plain decode; at most 1024).  Request b holds L = seq_len[b]
+ * tokens in its pages, the last T = tree_len[b] (NULL: n) of them the drafted
+ * ones (their K and V are in the cache already).  Row i < T of query head h
+ * attends the L - T context keys and the drafted keys j < T whose bit j is set
+ * in its mask; every key enters the softmax once.
+ *   q, o        [B, Hq, n, d_h]; lse [B, Hq, n] or NULL.  Rows >= T are neither
+ *               read nor written; a row without keys gives o = 0, lse = -inf
+ *   tree_mask   [n, ceil(n / 32)] words per request, word x bit y = drafted key
+ *               32 x + y, mask_stride words from one request to the next (0:
+ *               one mask for all); NULL: j <= i (a chain)
+ * page_table [B, max_pages]; pages may hold anything past a request's last
+ * token, but the K and V of its L tokens must be finite.  A request with T
+ * outside [0, n] or L outside [T, max_pages * page_size] is skipped, a page id
+ * outside the pool is not followed; either makes the next poll return
+ * MSA_ERR_INDEX (outputs of the call are then undefined).  Lengths stay on the
+ * device: a captured call follows them.  The workspace need not be
+ * initialised; calls that overlap in time need their own.  Deterministic. */
+MSA_API msa_status msa_attn_tree(const msa_shape* shape, const void* q, const msa_kv_pages* pages,
+                                 const int32_t* page_table, int32_t max_pages, const int32_t* seq_len,
+                                 const int32_t* tree_len, const uint32_t* tree_mask, int64_t mask_stride, void* o,
+                                 float* lse, void* ws, size_t ws_bytes, void* stream);
+
 /* Failure detection (no counterpart in the pages).  Synchronise `stream`,
  * read and clear the device error word of the current device.  Returns MSA_OK, MSA_ERR_DEVICE_TIMEOUT, MSA_ERR_INDEX or
  * MSA_ERR_CUDA. */

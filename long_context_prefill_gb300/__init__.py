@@ -31,7 +31,8 @@ EXPORTS = ("msa_status_string", "msa_vs_index_workspace", "msa_block_index_works
            "msa_vs_expand", "msa_poll_device_status", "msa_build_block_index_static",
            "msa_check_wait_timeout", "msa_attn_dense", "msa_layer_varlen_workspace", "msa_prefill_layer_varlen",
            "msa_layer_attend_rows", "msa_merge_attention", "msa_captured_mass", "msa_layer_varlen_indices",
-           "msa_layer_attend_stats")
+           "msa_layer_attend_stats", "msa_build_page_tables", "msa_qk_norm_rope", "msa_qk_norm_rope_varlen",
+           "msa_attn_tree_workspace", "msa_attn_tree")
 
 
 class MsaError(RuntimeError):
@@ -55,6 +56,24 @@ class VSIndexC(ctypes.Structure):
     _fields_ = [("vertical", ctypes.c_void_p), ("vertical_cnt", ctypes.c_void_p), ("slash", ctypes.c_void_p),
                 ("slash_cnt", ctypes.c_void_p), ("vertical_bits", ctypes.c_void_p), ("slash_bits", ctypes.c_void_p),
                 ("slash_cover", ctypes.c_void_p), ("v_cap", ctypes.c_int32), ("s_cap", ctypes.c_int32)]
+
+
+class KVPagesC(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32)]
+
+
+class PagePoolC(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("page_table", ctypes.c_void_p), ("seq_len", ctypes.c_void_p),
+                ("free_pages", ctypes.c_void_p), ("state", ctypes.c_void_p)]
+
+
+class RopeCfgC(ctypes.Structure):
+    _fields_ = [("norm", ctypes.c_int32), ("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("theta", ctypes.c_double), ("inv_freq", ctypes.POINTER(ctypes.c_double)),
+                ("rot_scale", ctypes.c_float)]
 
 
 _lib = None
@@ -123,6 +142,17 @@ def load(path: str = LIB_PATH):
             lib.msa_captured_mass.argtypes = [ctypes.c_int64, ctypes.c_int64, P, P, P, P]
             lib.msa_build_block_index_static.restype = st
             lib.msa_build_block_index_static.argtypes = [P, P, P, P, i32, i32, i32, P, P, P]
+            i64 = ctypes.c_int64
+            lib.msa_build_page_tables.restype = st
+            lib.msa_build_page_tables.argtypes = [P, P, P, i32, i32, P, P, P, P]
+            lib.msa_qk_norm_rope.restype = st
+            lib.msa_qk_norm_rope.argtypes = [P, P, P, i64, P, i64, P, i64, P, P, P, P, P, P, P]
+            lib.msa_qk_norm_rope_varlen.restype = st
+            lib.msa_qk_norm_rope_varlen.argtypes = [P, P, i32, P, P, i64, P, i64, P, i64, P, P, P, P, P, P, P]
+            lib.msa_attn_tree_workspace.restype = sz
+            lib.msa_attn_tree_workspace.argtypes = [P]
+            lib.msa_attn_tree.restype = st
+            lib.msa_attn_tree.argtypes = [P, P, P, P, i32, P, P, P, i64, P, P, P, sz, P]
             _lib = lib
     return _lib
 
@@ -609,6 +639,291 @@ def captured_mass(lse_sparse, lse_dense, stream=None):
     _check(load().msa_captured_mass(heads, n, _ptr(lse_sparse), _ptr(lse_dense), _ptr(mass), _stream(stream)),
            "msa_captured_mass")
     return mass
+
+
+# ----------------------------------------------------------------- paged KV cache
+def _launch(device, stream, body):
+    """body(raw stream) with `device` current, on `stream` (None: the device's
+    current one); what body allocates belongs to that stream."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return body(torch.cuda.current_stream(device).cuda_stream)
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream: on {stream.device}, expected {device}")
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        return body(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _pages(k_pages, v_pages, Hkv=None, d=None, device=None):
+    """Check the two page tensors [num_pages, Hkv, page_size, d]; returns their C view."""
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+        raise ValueError("k_pages: a 4-d tensor [num_pages, Hkv, page_size, d] is required")
+    N, H, P, dd = k_pages.shape
+    want = (N, H if Hkv is None else Hkv, P, dd if d is None else d)
+    _want(k_pages, "k_pages", torch.bfloat16, want, device=device)
+    if v_pages is None:
+        raise ValueError("v_pages: a torch.Tensor is required")
+    _want(v_pages, "v_pages", torch.bfloat16, want, device=k_pages.device)
+    return KVPagesC(k_pages.data_ptr(), v_pages.data_ptr(), N, P)
+
+
+class PagePool:
+    """The requests that share a pool of cache pages (msa_page_pool): page_table
+    [n_seqs, max_pages], seq_len [n_seqs], free_pages [num_pages] (a stack) and
+    state [4], int32 tensors that build_page_tables updates in place."""
+
+    def __init__(self, page_table, seq_len, free_pages, state, page_size: int):
+        if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+            raise ValueError("page_table: a 2-d tensor [n_seqs, max_pages] is required")
+        if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
+            raise ValueError("free_pages: a 1-d tensor [num_pages] is required")
+        S, width = page_table.shape
+        dev = page_table.device
+        _want(page_table, "page_table", torch.int32)
+        for t, what, shape in ((seq_len, "seq_len", (S,)), (free_pages, "free_pages", tuple(free_pages.shape)),
+                               (state, "state", (4,))):
+            if t is None:
+                raise ValueError(f"{what}: a torch.Tensor is required")
+            _want(t, what, torch.int32, shape, device=dev)
+        self.page_table, self.seq_len, self.free_pages, self.state = page_table, seq_len, free_pages, state
+        self.page_size = int(page_size)
+        self._c = PagePoolC(S, free_pages.shape[0], self.page_size, width, page_table.data_ptr(), seq_len.data_ptr(),
+                            free_pages.data_ptr(), state.data_ptr())
+
+    @staticmethod
+    def empty(n_seqs: int, max_pages: int, num_pages: int, page_size: int, device) -> "PagePool":
+        """A pool of num_pages free pages and n_seqs requests without tokens."""
+        i32 = dict(dtype=torch.int32, device=device)
+        state = torch.zeros(4, **i32)
+        state[0] = num_pages
+        return PagePool(torch.full((n_seqs, max_pages), -1, **i32), torch.zeros(n_seqs, **i32),
+                        torch.arange(num_pages - 1, -1, -1, **i32), state, page_size)
+
+
+def build_page_tables(pool: PagePool, new_len, seq_tokens: int = 0, tok_cap: int = 0, depth=None, cu_new=None,
+                      slots=None, positions=None, stream=None):
+    """msa_build_page_tables: every request of the pool from its length to
+    new_len [n_seqs].  Returns (cu_new, slots, positions): with seq_tokens = T
+    [n_seqs * T] padded, with tok_cap [tok_cap] packed token outputs, with
+    neither None (a call that only resizes)."""
+    S, dev = pool._c.n_seqs, pool.page_table.device
+    if new_len is None:
+        raise ValueError("new_len: a torch.Tensor is required")
+    _want(new_len, "new_len", torch.int32, (S,), device=dev)
+    seq_tokens, tok_cap = int(seq_tokens), int(tok_cap)
+    if seq_tokens < 0 or tok_cap < 0:
+        raise ValueError("seq_tokens, tok_cap: must not be negative")
+    total = S * seq_tokens if seq_tokens else tok_cap
+    if not total and not (slots is None and positions is None and depth is None):
+        raise ValueError("slots, positions, depth: need seq_tokens or tok_cap")
+    if depth is not None and depth.numel() != total:
+        raise ValueError(f"depth: {depth.numel()} elements, expected {total}")
+    _want(depth, "depth", torch.int32, device=dev)
+    _want(cu_new, "cu_new", torch.int32, (S + 1,), device=dev)
+    _want(slots, "slots", torch.int32, (total,), device=dev)
+    _want(positions, "positions", torch.int32, (total,), device=dev)
+    _cuda(page_table=pool.page_table)
+    lib = load()
+
+    def body(s):
+        cu = torch.empty(S + 1, dtype=torch.int32, device=dev) if cu_new is None else cu_new
+        sl, ps = slots, positions
+        if total:
+            sl = torch.empty(total, dtype=torch.int32, device=dev) if sl is None else sl
+            ps = torch.empty(total, dtype=torch.int32, device=dev) if ps is None else ps
+        _check(lib.msa_build_page_tables(ctypes.byref(pool._c), new_len.data_ptr(), _at(depth), seq_tokens, tok_cap,
+                                         cu.data_ptr(), _at(sl), _at(ps), s), "msa_build_page_tables")
+        return cu, sl, ps
+
+    return _launch(dev, stream, body)
+
+
+class RopeCfg:
+    """How qk_norm_rope treats a head (msa_rope_cfg); see rope_cfg()."""
+
+    def __init__(self, c, q_weight, k_weight, inv_freq):
+        self.c, self.q_weight, self.k_weight, self.inv_freq = c, q_weight, k_weight, inv_freq
+
+    def check(self, d, device):
+        _want(self.q_weight, "q_weight", torch.bfloat16, (d,), device=device)
+        _want(self.k_weight, "k_weight", torch.bfloat16, (d,), device=device)
+
+
+def rope_cfg(rot_dim: int, theta: float = 10000.0, interleaved: bool = False, norm: bool = False, eps: float = 1e-6,
+             q_weight=None, k_weight=None, inv_freq=None, rot_scale: float = 1.0) -> RopeCfg:
+    """Rotation of the first rot_dim columns by position * theta^(-2i / rot_dim)
+    (or by the rot_dim / 2 angles per position of the sequence inv_freq), after
+    an RMS norm with weights [d] (None: ones) when norm is set."""
+    arr = None
+    if inv_freq is not None:
+        vals = [float(x) for x in inv_freq]
+        if len(vals) != int(rot_dim) // 2:
+            raise ValueError(f"inv_freq: {len(vals)} values, expected {int(rot_dim) // 2}")
+        arr = (ctypes.c_double * len(vals))(*vals)
+    c = RopeCfgC(1 if norm else 0, float(eps), _at(q_weight), _at(k_weight), int(rot_dim), 1 if interleaved else 0,
+                 float(theta), arr, float(rot_scale))
+    return RopeCfg(c, q_weight, k_weight, arr)
+
+
+def _token_rows(t, what, lead, device):
+    """Token stride (elements) of a token-major tensor [*lead, H, d] whose heads are contiguous within a token."""
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{what}: dtype {t.dtype}, expected {torch.bfloat16}")
+    if tuple(t.shape[:-2]) != tuple(lead):
+        raise ValueError(f"{what}: leading dimensions {tuple(t.shape[:-2])}, expected {tuple(lead)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{what}: on {t.device}, expected {device}")
+    H, d = t.shape[-2:]
+    st = t.stride()
+    if (d > 1 and st[-1] != 1) or (H > 1 and st[-2] != d):
+        raise ValueError(f"{what}: the heads of a token must be contiguous")
+    step, size = H * d, 1  # tokens must lie at one stride through every leading dimension
+    found = None
+    for n, s in zip(reversed(t.shape[:-2]), reversed(st[:-2])):
+        if n > 1:
+            if found is None:
+                found = s
+            elif s != found * size:
+                raise ValueError(f"{what}: tokens must lie at one stride")
+            size *= n
+    return step if found is None else found
+
+
+def _norm_rope(call, name, lead, out_shape, dims, q_in, k_in, v_in, cfg, positions, q, k, v, k_pages, v_pages, slots,
+               layer_kv, stream):
+    Hq, Hkv, d = dims
+    dev = q_in.device
+    tokens = 1
+    for x in lead:
+        tokens *= int(x)
+    qs, ks = _token_rows(q_in, "q_in", lead, None), _token_rows(k_in, "k_in", lead, dev)
+    if tuple(k_in.shape[-2:]) != (Hkv, d):
+        raise ValueError(f"k_in: heads {tuple(k_in.shape[-2:])}, expected {(Hkv, d)}")
+    vs = 0
+    if v_in is not None:
+        vs = _token_rows(v_in, "v_in", lead, dev)
+        if tuple(v_in.shape[-2:]) != (Hkv, d):
+            raise ValueError(f"v_in: heads {tuple(v_in.shape[-2:])}, expected {(Hkv, d)}")
+    cfg.check(d, dev)
+    pages = None if k_pages is None else _pages(k_pages, v_pages, Hkv, d, dev)
+    if positions is not None and positions.numel() != tokens:
+        raise ValueError(f"positions: {positions.numel()} elements, expected {tokens}")
+    if slots is not None and slots.numel() != tokens:
+        raise ValueError(f"slots: {slots.numel()} elements, expected {tokens}")
+    _want(positions, "positions", torch.int32, device=dev)
+    _want(slots, "slots", torch.int32, device=dev)
+    _want(q, "q", torch.bfloat16, out_shape(Hq), device=dev)
+    _want(k, "k", torch.bfloat16, out_shape(Hkv), device=dev)
+    _want(v, "v", torch.bfloat16, out_shape(Hkv), device=dev)
+    _cuda(q_in=q_in)
+
+    def body(s):
+        def new(H):
+            return torch.empty(out_shape(H), dtype=torch.bfloat16, device=dev)
+
+        qo = new(Hq) if q is None else q
+        ko = new(Hkv) if k is None and layer_kv else k
+        vo = new(Hkv) if v is None and layer_kv and v_in is not None else v
+        _check(call(ctypes.byref(cfg.c), q_in.data_ptr(), qs, k_in.data_ptr(), ks, _at(v_in), vs, _at(positions),
+                    qo.data_ptr(), _at(ko), _at(vo), None if pages is None else ctypes.byref(pages), _at(slots), s),
+               name)
+        return qo, ko, vo
+
+    return _launch(dev, stream, body)
+
+
+def qk_norm_rope(q_in, k_in, v_in, cfg: RopeCfg, positions=None, q=None, k=None, v=None, k_pages=None, v_pages=None,
+                 slots=None, layer_kv: bool = True, stream=None):
+    """msa_qk_norm_rope: q_in [B, n, Hq, d], k_in / v_in [B, n, Hkv, d] (views
+    of the projection's rows) to (q [B, Hq, n, d], k, v [B, Hkv, n, d]) and,
+    with k_pages / v_pages and slots, into the cache.  layer_kv=False leaves k
+    and v to the cache alone (returned as given, or None)."""
+    for t, what in ((q_in, "q_in"), (k_in, "k_in")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise ValueError(f"{what}: a 4-d tensor [B, n, H, d] is required")
+    B, n, Hq, d = q_in.shape
+    Hkv = k_in.shape[2]
+    sh = Shape(B, Hq, Hkv, n, d, 0.0)
+    lib = load()
+    return _norm_rope(lambda *a: lib.msa_qk_norm_rope(ctypes.byref(sh), *a), "msa_qk_norm_rope", (B, n),
+                      lambda H: (B, H, n, d), (Hq, Hkv, d), q_in, k_in, v_in, cfg, positions, q, k, v, k_pages,
+                      v_pages, slots, layer_kv, stream)
+
+
+def qk_norm_rope_varlen(q_in, k_in, v_in, cu_seqlens, cfg: RopeCfg, positions=None, q=None, k=None, v=None,
+                        k_pages=None, v_pages=None, slots=None, layer_kv: bool = True, stream=None):
+    """msa_qk_norm_rope_varlen: packed q_in [tokens, Hq, d], k_in / v_in
+    [tokens, Hkv, d] to flat buffers in the varlen layout (see pack_varlen)
+    and, as for qk_norm_rope, the cache."""
+    for t, what in ((q_in, "q_in"), (k_in, "k_in")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            raise ValueError(f"{what}: a 3-d tensor [tokens, H, d] is required")
+    cu = [int(x) for x in cu_seqlens]
+    tokens, Hq, d = q_in.shape
+    Hkv = k_in.shape[1]
+    if len(cu) < 2 or cu[-1] != tokens:
+        raise ValueError(f"cu_seqlens: must end at the {tokens} tokens of q_in")
+    arr = (ctypes.c_int32 * len(cu))(*cu)
+    sh = Shape(1, Hq, Hkv, 1, d, 0.0)
+    lib = load()
+    return _norm_rope(lambda *a: lib.msa_qk_norm_rope_varlen(ctypes.byref(sh), arr, len(cu) - 1, *a),
+                      "msa_qk_norm_rope_varlen", (tokens,), lambda H: (tokens * H * d,), (Hq, Hkv, d), q_in, k_in,
+                      v_in, cfg, positions, q, k, v, k_pages, v_pages, slots, layer_kv, stream)
+
+
+def attn_tree(q, k_pages, v_pages, page_table, seq_len, tree_len=None, tree_mask=None, o=None, lse=None, scale=None,
+              ws=None, stream=None):
+    """msa_attn_tree: drafted tokens (n = 1: a decode step) q [B, Hq, n, d] over
+    the paged cache; seq_len [B] counts the drafted tokens.  tree_len [B];
+    tree_mask [B, n, ceil(n/32)] or, for all requests, [n, ceil(n/32)] int32
+    words (None: a chain).  Returns o.  ws: a uint8 workspace of at least
+    attn_tree_workspace(...) bytes (None: one is allocated for the call)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q: a 4-d tensor [B, Hq, n, d] is required")
+    B, Hq, n, d = q.shape
+    dev = q.device
+    _want(q, "q", torch.bfloat16)
+    pages = _pages(k_pages, v_pages, None, d, dev)
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table: a 2-d tensor [B, max_pages] is required")
+    width = page_table.shape[1]
+    words = (n + 31) // 32
+    _want(page_table, "page_table", torch.int32, (B, width), device=dev)
+    if seq_len is None:
+        raise ValueError("seq_len: a torch.Tensor is required")
+    _want(seq_len, "seq_len", torch.int32, (B,), device=dev)
+    _want(tree_len, "tree_len", torch.int32, (B,), device=dev)
+    stride = 0
+    if tree_mask is not None:
+        shared = tree_mask.dim() == 2
+        _want(tree_mask, "tree_mask", torch.int32, (n, words) if shared else (B, n, words), device=dev)
+        stride = 0 if shared else n * words
+    _want(o, "o", torch.bfloat16, (B, Hq, n, d), device=dev)
+    _want(lse, "lse", torch.float32, (B, Hq, n), device=dev)
+    _want(ws, "ws", torch.uint8, device=dev)
+    _cuda(q=q)
+    lib = load()
+    sh = Shape(B, Hq, k_pages.shape[1], n, d, float(scale) if scale else 0.0)
+
+    def body(s):
+        out = torch.empty_like(q) if o is None else o
+        w = ws
+        if w is None:
+            w = torch.empty(max(int(lib.msa_attn_tree_workspace(ctypes.byref(sh))), 1), dtype=torch.uint8, device=dev)
+        _check(lib.msa_attn_tree(ctypes.byref(sh), q.data_ptr(), ctypes.byref(pages), page_table.data_ptr(), width,
+                                 seq_len.data_ptr(), _at(tree_len), _at(tree_mask), stride, out.data_ptr(), _at(lse),
+                                 w.data_ptr(), w.numel(), s), "msa_attn_tree")
+        return out
+
+    return _launch(dev, stream, body)
+
+
+def attn_tree_workspace(B, Hq, Hkv, n, d) -> int:
+    """Workspace bytes of attn_tree (0: unsupported shape)."""
+    return int(load().msa_attn_tree_workspace(ctypes.byref(Shape(B, Hq, Hkv, n, d, 0.0))))
 
 
 def kernel_launches() -> int:

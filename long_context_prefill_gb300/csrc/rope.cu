@@ -1,0 +1,367 @@
+// Norms of queries and keys for each head with the position rotation, from the
+// projection's token-major rows into the layouts the library reads: the
+// head-major layer tensors and, in the same pass, the pages of a KV cache.
+//
+// Per head row x of d_h values: y = x / sqrt(mean(x^2) + eps) * w (when the
+// norm is on), then the first rot_dim columns turn by position: the pair
+// (a, b) = (i, i + rot/2), or (2i, 2i+1) when interleaved, becomes
+// (a cos - b sin, b cos + a sin) with the angle position * f_i.  V is moved
+// unchanged.  Everything is fp32 and rounded to bf16 once, at the store: the
+// normed value is not rounded before the rotation.
+//
+// Angles.  An fp32 product position * f_i has an error of 0.06 rad at a
+// position of a million.  The host turns f_i into F = f_i / (2 pi) in units of
+// 2^-64 turns; position * F in 64-bit integers wraps exactly at whole turns,
+// and its top 32 bits are the angle to 2^-31 half turns, whatever the position.
+//
+// What bounds it: HBM, every value read once and written once per
+// destination.  A lane holds both members of its pairs (two 16-byte chunks, a
+// head in 8 lanes for d_h = 128), so the rotation needs no exchange and the
+// norm three shuffles; the cosines of a token are computed once per CTA and
+// serve all its heads.
+#include <cuda_bf16.h>
+#include <math.h>
+#include <string.h>
+
+#include <vector>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace msa {
+
+msa_status check_shape(const msa_shape* s);
+msa_status check_page_geometry(int32_t num_pages, int32_t page_size);
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTokens = 8;    // tokens of a CTA
+constexpr int kMaxBatch = 1024;  // sequences of a launch
+
+struct RopeArgs {
+  const __nv_bfloat16 *q, *k, *v;     // token-major inputs
+  int64_t q_stride, k_stride, v_stride;  // elements from one token to the next
+  int32_t Hq, Hkv, has_v;
+  int32_t tok0, tok1;  // tokens of this launch
+  int32_t n;           // tokens of a sequence (uniform batch), 0: varlen, `cu`
+  int32_t per_cta;
+  const int32_t* positions;
+  const __nv_bfloat16 *q_w, *k_w;
+  int32_t norm, rot, interleaved;
+  float eps, rot_scale;
+  __nv_bfloat16 *qo, *ko, *vo;  // layer layout (ko, vo may be null)
+  __nv_bfloat16 *kp, *vp;       // pages (may be null)
+  const int32_t* slots;
+  int32_t page_shift, num_pages;
+  int* err;
+};
+
+struct RopeTables {
+  uint64_t turn[64];               // f_i in 2^-64 turns
+  int32_t count;                   // varlen: sequences of this launch
+  int32_t cu[kMaxBatch + 1];       // their first tokens
+};
+
+struct Token {
+  int32_t seq0, n, i;  // first token and length of its sequence, index in it
+  int32_t slot;        // cache slot, < 0: not stored
+};
+
+// 16 values of a head: chunks c0 and c1 of 8.  In the rotated columns chunk 0
+// holds the first and chunk 1 the second members of 8 pairs (half-split), or
+// both hold whole pairs (interleaved).
+__device__ __forceinline__ void unpack8(uint4 u, float* f) {
+  const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&u);
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const float2 t = __bfloat1622float2(p[x]);
+    f[2 * x] = t.x;
+    f[2 * x + 1] = t.y;
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float* f) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                    pack_bf16x2(f[6], f[7]));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeArgs A, const __grid_constant__ RopeTables T) {
+  constexpr int kLanes = D / 16;               // lanes of a head
+  constexpr int kHeads = kThreads / kLanes;    // heads in flight per CTA
+  __shared__ float2 cs[kMaxTokens][D / 2];
+  __shared__ Token toks[kMaxTokens];
+  const int tid = threadIdx.x;
+  const int H = A.Hq + A.Hkv * (1 + A.has_v);
+  const int first = A.tok0 + blockIdx.x * A.per_cta;
+  const int cnt = min(A.per_cta, A.tok1 - first);
+  const int half = A.rot >> 1;
+  const int l = tid % kLanes;
+  // this lane's two chunks
+  const bool rotated = 16 * l < A.rot;
+  const int c0 = rotated ? 8 * l : 16 * l, c1 = rotated ? half + 8 * l : 16 * l + 8;
+
+  auto load = [&](int u, uint4& x0, uint4& x1) {
+    const int t = u / H, h = u - t * H;
+    const __nv_bfloat16* src;
+    if (h < A.Hq) src = A.q + (first + t) * A.q_stride + h * D;
+    else if (h < A.Hq + A.Hkv) src = A.k + (first + t) * A.k_stride + (h - A.Hq) * D;
+    else src = A.v + (first + t) * A.v_stride + (h - A.Hq - A.Hkv) * D;
+    x0 = __ldcs(reinterpret_cast<const uint4*>(src + c0));
+    x1 = __ldcs(reinterpret_cast<const uint4*>(src + c1));
+  };
+  const int units = cnt * H;
+  int u = tid / kLanes;
+  uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
+  if (u < units) load(u, x0, x1);  // in flight while the angles are computed
+
+  if (tid < cnt) {
+    const int tk = first + tid;
+    Token k;
+    if (A.n) {
+      k.seq0 = tk / A.n * A.n;
+      k.n = A.n;
+    } else {
+      const int s = seq_search(T.count, [&](int x) { return T.cu[x]; }, tk);
+      k.seq0 = T.cu[s];
+      k.n = T.cu[s + 1] - T.cu[s];
+    }
+    k.i = tk - k.seq0;
+    k.slot = -1;
+    if (A.slots) {
+      k.slot = A.slots[tk];
+      if (k.slot >= 0 && (k.slot >> A.page_shift) >= A.num_pages) {
+        atomicCAS(A.err, 0, (int)kErrIndex);
+        k.slot = -1;
+      }
+    }
+    toks[tid] = k;
+  }
+  if (half)
+    for (int x = tid; x < cnt * half; x += kThreads) {
+      const int t = x / half, p = x - t * half, tk = first + t;
+      int pos;
+      if (A.positions) pos = A.positions[tk];
+      else if (A.n) pos = tk % A.n;
+      else pos = tk - T.cu[seq_search(T.count, [&](int y) { return T.cu[y]; }, tk)];
+      const uint64_t turns = (uint64_t)(int64_t)pos * T.turn[p];
+      float s, c;
+      sincospif((float)(int32_t)(turns >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31 half turns
+      cs[t][p] = make_float2(c * A.rot_scale, s * A.rot_scale);
+    }
+  __syncthreads();
+
+  while (u < units) {
+    const int nu = u + kHeads;
+    uint4 y0 = make_uint4(0, 0, 0, 0), y1 = y0;
+    if (nu < units) load(nu, y0, y1);
+    const int t = u / H, h = u - t * H;
+    const Token tk = toks[t];
+    const bool is_v = h >= A.Hq + A.Hkv, is_q = h < A.Hq;
+    if (!is_v) {
+      float a[8], b[8];
+      unpack8(x0, a);
+      unpack8(x1, b);
+      if (A.norm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) ss += a[x] * a[x] + b[x] * b[x];
+        const unsigned group = (kLanes == 8 ? 0xFFu : 0xFu) << ((tid & 31) / kLanes * kLanes);
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
+        const float r = 1.f / sqrtf(ss * (1.f / D) + A.eps);
+        const __nv_bfloat16* w = is_q ? A.q_w : A.k_w;
+        float w0[8], w1[8];
+        if (w) {
+          unpack8(__ldg(reinterpret_cast<const uint4*>(w + c0)), w0);
+          unpack8(__ldg(reinterpret_cast<const uint4*>(w + c1)), w1);
+        }
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          a[x] = a[x] * r * (w ? w0[x] : 1.f);
+          b[x] = b[x] * r * (w ? w1[x] : 1.f);
+        }
+      }
+      if (rotated) {
+        if (A.interleaved) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float2 e = cs[t][4 * l + x], f = cs[t][(half >> 1) + 4 * l + x];
+            const float p = a[2 * x], q = a[2 * x + 1], v = b[2 * x], w = b[2 * x + 1];
+            a[2 * x] = p * e.x - q * e.y;
+            a[2 * x + 1] = q * e.x + p * e.y;
+            b[2 * x] = v * f.x - w * f.y;
+            b[2 * x + 1] = w * f.x + v * f.y;
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const float2 e = cs[t][8 * l + x];
+            const float p = a[x], q = b[x];
+            a[x] = p * e.x - q * e.y;
+            b[x] = q * e.x + p * e.y;
+          }
+        }
+      }
+      x0 = pack8(a);
+      x1 = pack8(b);
+    }
+    const int kh = is_q ? h : is_v ? h - A.Hq - A.Hkv : h - A.Hq;
+    const int64_t heads = is_q ? A.Hq : A.Hkv;
+    __nv_bfloat16* out = is_q ? A.qo : is_v ? A.vo : A.ko;
+    if (out) {
+      __nv_bfloat16* dst = out + (heads * tk.seq0 + (int64_t)kh * tk.n + tk.i) * D;
+      *reinterpret_cast<uint4*>(dst + c0) = x0;
+      *reinterpret_cast<uint4*>(dst + c1) = x1;
+    }
+    __nv_bfloat16* pages = is_v ? A.vp : A.kp;
+    if (!is_q && pages && tk.slot >= 0) {
+      const int64_t page = tk.slot >> A.page_shift;
+      const int off = tk.slot & ((1 << A.page_shift) - 1);
+      __nv_bfloat16* dst = pages + (((page * A.Hkv + kh) << A.page_shift) + off) * D;
+      *reinterpret_cast<uint4*>(dst + c0) = x0;
+      *reinterpret_cast<uint4*>(dst + c1) = x1;
+    }
+    u = nu;
+    x0 = y0;
+    x1 = y1;
+  }
+}
+
+bool aligned(const void* p, size_t a, bool required) {
+  if (!p) return !required;
+  return reinterpret_cast<uintptr_t>(p) % a == 0;
+}
+
+// f in units of 2^-64 turns: the fraction of f / (2 pi) (whole turns change nothing).
+uint64_t turns64(double f) {
+  double t = f * 0.15915494309189533577;
+  t -= floor(t);
+  const double hi = floor(t * 4294967296.0);
+  const double lo = floor((t * 4294967296.0 - hi) * 4294967296.0);
+  return ((uint64_t)hi << 32) + (uint64_t)lo;
+}
+
+msa_status norm_rope(const msa_shape& s, const int32_t* cu, int32_t n_seqs, const msa_rope_cfg* cfg, const void* q_in,
+                     int64_t q_stride, const void* k_in, int64_t k_stride, const void* v_in, int64_t v_stride,
+                     const int32_t* positions, void* q, void* k, void* v, const msa_kv_pages* pages,
+                     const int32_t* slots, int64_t tokens, cudaStream_t stream) {
+  if (!cfg) return MSA_ERR_INVALID_ARG;
+  if (cfg->rot_dim < 0 || cfg->rot_dim > s.d_h || !(cfg->eps >= 0.f) || isinf(cfg->eps)) return MSA_ERR_INVALID_ARG;
+  if (cfg->norm != 0 && cfg->norm != 1) return MSA_ERR_INVALID_ARG;
+  if (cfg->rot_dim % 16) return MSA_ERR_UNSUPPORTED;
+  const double theta = cfg->theta > 0.0 ? cfg->theta : 10000.0;
+  if (!(cfg->theta == cfg->theta) || isinf(theta) || !isfinite(cfg->rot_scale)) return MSA_ERR_INVALID_ARG;
+  if (!aligned(q_in, 16, true) || !aligned(k_in, 16, true) || !aligned(v_in, 16, false) || !aligned(q, 16, true) ||
+      !aligned(k, 16, false) || !aligned(v, 16, false) || !aligned(positions, 4, false) ||
+      !aligned(slots, 4, false) || !aligned(cfg->q_weight, 16, false) || !aligned(cfg->k_weight, 16, false))
+    return MSA_ERR_INVALID_ARG;
+  if (q_stride < (int64_t)s.Hq * s.d_h || k_stride < (int64_t)s.Hkv * s.d_h ||
+      (v_in && v_stride < (int64_t)s.Hkv * s.d_h))
+    return MSA_ERR_INVALID_ARG;
+  if (q_stride % 8 || k_stride % 8 || (v_in && v_stride % 8)) return MSA_ERR_INVALID_ARG;
+  if (!k && !pages) return MSA_ERR_INVALID_ARG;          // the keys would go nowhere
+  if (v_in ? !v && !pages : v || pages) return MSA_ERR_INVALID_ARG;  // values come and go together
+  if (q == q_in || q == k_in || (v_in && q == v_in) || (k && (k == q_in || k == k_in || k == v_in)) ||
+      (v && (v == q_in || v == k_in || v == v_in)))
+    return MSA_ERR_INVALID_ARG;  // rows move: not in place
+  RopeArgs a;
+  memset(&a, 0, sizeof(a));
+  if (pages) {
+    const msa_status geo = check_page_geometry(pages->num_pages, pages->page_size);
+    if (geo != MSA_OK) return geo;
+    if (!slots || !aligned(pages->k, 16, true) || !aligned(pages->v, 16, true)) return MSA_ERR_INVALID_ARG;
+    a.kp = static_cast<__nv_bfloat16*>(pages->k);
+    a.vp = static_cast<__nv_bfloat16*>(pages->v);
+    a.slots = slots;
+    a.page_shift = __builtin_ctz((unsigned)pages->page_size);
+    a.num_pages = pages->num_pages;
+  } else if (slots) {
+    return MSA_ERR_INVALID_ARG;
+  }
+  if (tokens >= ((int64_t)1 << 31) - kMaxTokens) return MSA_ERR_UNSUPPORTED;
+  RopeTables t;
+  memset(&t, 0, sizeof(t));
+  for (int i = 0; i < cfg->rot_dim / 2; ++i) {
+    const double f = cfg->inv_freq ? cfg->inv_freq[i] : pow(theta, -2.0 * i / cfg->rot_dim);
+    if (!isfinite(f)) return MSA_ERR_INVALID_ARG;
+    t.turn[i] = turns64(f);
+  }
+  if (tokens == 0) return MSA_OK;
+  a.q = static_cast<const __nv_bfloat16*>(q_in);
+  a.k = static_cast<const __nv_bfloat16*>(k_in);
+  a.v = static_cast<const __nv_bfloat16*>(v_in);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.Hq = s.Hq;
+  a.Hkv = s.Hkv;
+  a.has_v = v_in != nullptr;
+  a.n = cu ? 0 : s.n;
+  a.positions = positions;
+  a.q_w = static_cast<const __nv_bfloat16*>(cfg->q_weight);
+  a.k_w = static_cast<const __nv_bfloat16*>(cfg->k_weight);
+  a.norm = cfg->norm;
+  a.rot = cfg->rot_dim;
+  a.interleaved = cfg->interleaved;
+  a.eps = cfg->eps;
+  a.rot_scale = cfg->rot_scale == 0.f ? 1.f : cfg->rot_scale;
+  a.qo = static_cast<__nv_bfloat16*>(q);
+  a.ko = static_cast<__nv_bfloat16*>(k);
+  a.vo = static_cast<__nv_bfloat16*>(v);
+  a.err = device_error_word();
+  if (!a.err) return MSA_ERR_CUDA;
+  // one token per CTA while there are few (latency), more when they fill the GPU several times over
+  int64_t per = tokens / (152 * 8);
+  a.per_cta = (int)(per < 1 ? 1 : per > kMaxTokens ? kMaxTokens : per);
+  for (int s0 = 0; s0 < (cu ? n_seqs : 1); s0 += kMaxBatch) {
+    a.tok0 = 0;
+    a.tok1 = (int32_t)tokens;
+    if (cu) {
+      t.count = n_seqs - s0 < kMaxBatch ? n_seqs - s0 : kMaxBatch;
+      for (int x = 0; x <= t.count; ++x) t.cu[x] = cu[s0 + x];
+      a.tok0 = t.cu[0];
+      a.tok1 = t.cu[t.count];
+    }
+    if (a.tok1 <= a.tok0) continue;
+    const unsigned grid = (unsigned)ceil_div((int64_t)a.tok1 - a.tok0, a.per_cta);
+    if (s.d_h == 128) norm_rope_kernel<128><<<grid, kThreads, 0, stream>>>(a, t);
+    else norm_rope_kernel<64><<<grid, kThreads, 0, stream>>>(a, t);
+    note_launch();
+    if (cudaGetLastError() != cudaSuccess) return MSA_ERR_CUDA;
+  }
+  return MSA_OK;
+}
+
+}  // namespace
+
+}  // namespace msa
+
+using namespace msa;
+
+extern "C" msa_status msa_qk_norm_rope(const msa_shape* shape, const msa_rope_cfg* cfg, const void* q_in,
+                                       int64_t q_stride, const void* k_in, int64_t k_stride, const void* v_in,
+                                       int64_t v_stride, const int32_t* positions, void* q, void* k, void* v,
+                                       const msa_kv_pages* pages, const int32_t* slots, void* stream) {
+  const msa_status st = check_shape(shape);
+  if (st != MSA_OK) return st;
+  return norm_rope(*shape, nullptr, 0, cfg, q_in, q_stride, k_in, k_stride, v_in, v_stride, positions, q, k, v, pages,
+                   slots, (int64_t)shape->B * shape->n, (cudaStream_t)stream);
+}
+
+extern "C" msa_status msa_qk_norm_rope_varlen(const msa_shape* shape, const int32_t* cu_seqlens, int32_t n_seqs,
+                                              const msa_rope_cfg* cfg, const void* q_in, int64_t q_stride,
+                                              const void* k_in, int64_t k_stride, const void* v_in, int64_t v_stride,
+                                              const int32_t* positions, void* q, void* k, void* v,
+                                              const msa_kv_pages* pages, const int32_t* slots, void* stream) {
+  if (!shape || !cu_seqlens || n_seqs < 1 || cu_seqlens[0] != 0) return MSA_ERR_INVALID_ARG;
+  msa_shape s = *shape;
+  s.B = 1;
+  s.n = 1;
+  const msa_status st = check_shape(&s);
+  if (st != MSA_OK) return st;
+  for (int x = 0; x < n_seqs; ++x)
+    if (cu_seqlens[x + 1] < cu_seqlens[x]) return MSA_ERR_INVALID_ARG;
+  return norm_rope(s, cu_seqlens, n_seqs, cfg, q_in, q_stride, k_in, k_stride, v_in, v_stride, positions, q, k, v,
+                   pages, slots, cu_seqlens[n_seqs], (cudaStream_t)stream);
+}

@@ -1,0 +1,252 @@
+"""Per-head norms of queries and keys with the rotation (msa_qk_norm_rope).
+
+CPU: host checks.  GPU: every value against the formula in 64 bits, within the
+fp32 bound of paged_ref.norm_rope and one bf16 rounding; V and the cache's
+other rows bit for bit."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import long_context_prefill_gb300 as msa
+from paged_ref import check_rounded, norm_rope
+
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from long_context_prefill_gb300 import build
+    build.build()
+    return msa.load()
+
+
+def test_refusals(lib):
+    P = ctypes.c_void_p
+    inv, uns = msa.MSA_ERR_INVALID_ARG, msa.MSA_ERR_UNSUPPORTED
+    a = {k: P(0x100000 * (x + 1)) for x, k in enumerate(("q_in", "k_in", "v_in", "pos", "q", "k", "v", "slots"))}
+
+    def call(shape=None, cfg=None, qs=512, ks=256, vs=256, pages=None, **kw):
+        sh = dict(B=1, Hq=4, Hkv=2, n=8, d_h=128, scale=0.0)
+        sh.update(shape or {})
+        c = dict(norm=1, eps=1e-6, q_weight=None, k_weight=None, rot_dim=128, interleaved=0, theta=1e4, inv_freq=None,
+                 rot_scale=1.0)
+        c.update(cfg or {})
+        x = dict(a, slots=None)
+        x.update(kw)
+        return lib.msa_qk_norm_rope(ctypes.byref(msa.Shape(**sh)), ctypes.byref(msa.RopeCfgC(**c)), x["q_in"], qs,
+                                    x["k_in"], ks, x["v_in"], vs, x["pos"], x["q"], x["k"], x["v"],
+                                    None if pages is None else ctypes.byref(pages), x["slots"], None)
+
+    assert call(shape=dict(d_h=96)) == uns
+    assert call(shape=dict(Hq=3)) == inv
+    assert call(cfg=dict(rot_dim=24)) == uns
+    assert call(cfg=dict(rot_dim=144)) == inv
+    assert call(cfg=dict(rot_dim=-16)) == inv
+    assert call(cfg=dict(norm=2)) == inv
+    assert call(cfg=dict(eps=-1.0)) == inv
+    assert call(cfg=dict(eps=float("nan"))) == inv
+    assert call(cfg=dict(theta=float("inf"))) == inv
+    assert call(cfg=dict(theta=float("nan"))) == inv
+    assert call(cfg=dict(rot_scale=float("nan"))) == inv
+    bad = (ctypes.c_double * 64)(*([float("nan")] * 64))
+    assert call(cfg=dict(inv_freq=bad)) == inv
+    assert call(qs=504) == inv
+    assert call(ks=260) == inv  # not a multiple of 8 elements
+    assert call(q_in=P(0x100008)) == inv
+    assert call(q_in=None) == inv
+    assert call(k=None, v=None) == inv                     # no destination
+    assert call(v=None) == inv                             # values read and dropped
+    assert call(v_in=None) == inv                          # values written from nothing
+    assert call(q=a["q_in"]) == inv                        # in place
+    assert call(slots=a["slots"]) == inv                   # slots without pages
+    pages = msa.KVPagesC(0x10000000, 0x20000000, 8, 16)
+    assert call(pages=pages) == inv                        # pages without slots
+    assert call(pages=msa.KVPagesC(0x10000000, 0x20000000, 8, 24), slots=a["slots"]) == uns
+    assert call(pages=msa.KVPagesC(0x10000000, None, 8, 16), slots=a["slots"]) == inv
+    sh, c = msa.Shape(1, 4, 2, 1, 128, 0.0), msa.rope_cfg(128).c
+
+    def varlen(cu):
+        arr = (ctypes.c_int32 * len(cu))(*cu)
+        return lib.msa_qk_norm_rope_varlen(ctypes.byref(sh), arr, len(cu) - 1, ctypes.byref(c), a["q_in"], 512,
+                                           a["k_in"], 256, a["v_in"], 256, None, a["q"], a["k"], a["v"], None, None,
+                                           None)
+    assert varlen([1, 5]) == inv
+    assert varlen([0, 5, 4]) == inv
+    assert varlen([0, 0, 0]) == msa.MSA_OK  # nothing to do
+
+
+def test_binding_refusals():
+    x = torch.zeros(2, 5, 8, 64, dtype=BF)
+    q, k, v = x.split([4, 2, 2], 2)
+    cfg = msa.rope_cfg(64, norm=True, q_weight=torch.ones(64, dtype=BF))
+    for call, what in [
+        (lambda: msa.qk_norm_rope(q, k, v, cfg), "q_in: must be on a CUDA device"),
+        (lambda: msa.qk_norm_rope(q[0], k, v, cfg), "q_in: a 4-d"),
+        (lambda: msa.qk_norm_rope(q, k[:, :4], v, cfg), "k_in: leading"),
+        (lambda: msa.qk_norm_rope(q, k, v[..., :1, :], cfg), "v_in: heads"),
+        (lambda: msa.qk_norm_rope(q.float(), k, v, cfg), "q_in: dtype"),
+        (lambda: msa.qk_norm_rope(q[..., ::2, :], k, v, cfg), "q_in: the heads"),
+        (lambda: msa.qk_norm_rope(q[:, ::2], k[:, ::2], v[:, :3], cfg), "tokens must lie at one stride"),
+        (lambda: msa.qk_norm_rope(q, k, v, msa.rope_cfg(64, norm=True, q_weight=torch.ones(32, dtype=BF))), "q_weight: shape"),
+        (lambda: msa.qk_norm_rope(q, k, v, cfg, positions=torch.zeros(9, dtype=torch.int32)), "positions: 9 elements"),
+        (lambda: msa.qk_norm_rope(q, k, v, cfg, q=torch.zeros(2, 4, 4, 64, dtype=BF)), "q: shape"),
+        (lambda: msa.qk_norm_rope(q, k, v, cfg, k_pages=torch.zeros(3, 2, 16, 64, dtype=BF)), "v_pages: a torch"),
+        (lambda: msa.qk_norm_rope_varlen(q[0], k[0], v[0], [0, 4], cfg), "cu_seqlens: must end"),
+        (lambda: msa.rope_cfg(64, inv_freq=[1.0] * 31), "inv_freq: 31 values"),
+    ]:
+        with pytest.raises(ValueError, match=what):
+            call()
+
+
+def _freq(rot, theta=10000.0):
+    return [theta ** (-2 * i / rot) for i in range(rot // 2)] if rot else []
+
+
+def _inputs(tok, Hq, Hkv, d, seed, pad=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(tok, (Hq + 2 * Hkv) * d + pad, generator=g, device="cuda") * 3
+    x = x.to(BF)
+    w = (1 + 0.5 * torch.randn(2, d, generator=g, device="cuda")).to(BF)
+    q, k, v = (t.unflatten(1, (-1, d)) for t in x[:, :(Hq + 2 * Hkv) * d].split([Hq * d, Hkv * d, Hkv * d], 1))
+    return q, k, v, w
+
+
+def _check(got, x, w, cfgd, pos, what):
+    y, slack = norm_rope(x, w, cfgd["norm"], cfgd["eps"], cfgd["rot"], cfgd["freq"], cfgd["inter"], pos,
+                         cfgd.get("scale", 1.0))
+    check_rounded(got, y, slack, what)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rot", [0, 16, 48, None])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("norm", [False, True])
+def test_layer_and_cache(cuda_lib, d, rot, inter, norm):
+    rot = d if rot is None else rot
+    B, n, Hq, Hkv, page = 3, 37, 6, 2, 16
+    tok = B * n
+    q, k, v, w = _inputs(tok, Hq, Hkv, d, d + rot, pad=24)
+    rng = np.random.default_rng(rot)
+    pos = torch.from_numpy(rng.integers(0, 1 << 20, tok).astype(np.int32)).cuda()
+    slots = torch.from_numpy(rng.permutation(tok + 40)[:tok].astype(np.int32)).cuda()
+    slots[5] = -1  # a padding token: not stored
+    N = -(-(tok + 40) // page)
+    cfg = msa.rope_cfg(rot, interleaved=inter, norm=norm, eps=1e-5, q_weight=w[0], k_weight=w[1])
+    kp, vp = (torch.full((N, Hkv, page, d), float("nan"), dtype=BF, device="cuda") for _ in range(2))
+    shaped = [t.unflatten(0, (B, n)) for t in (q, k, v)]
+    qo, ko, vo = msa.qk_norm_rope(*shaped, cfg, positions=pos, k_pages=kp, v_pages=vp, slots=slots)
+    assert cuda_lib.poll_device_status() == 0
+    c = dict(norm=norm, eps=1e-5, rot=rot, freq=_freq(rot), inter=inter)
+    back = lambda t: t.transpose(1, 2).reshape(tok, -1, d)  # noqa: E731
+    _check(back(qo), q, w[0], c, pos, "q")
+    _check(back(ko), k, w[1], c, pos, "k")
+    assert torch.equal(back(vo), v)
+    keep = torch.arange(tok, device="cuda") != 5
+    rows = lambda t: t.transpose(1, 2).reshape(-1, Hkv, d)  # noqa: E731
+    assert torch.equal(rows(kp)[slots[keep].long()], back(ko)[keep])
+    assert torch.equal(rows(vp)[slots[keep].long()], v[keep])
+    other = torch.ones(N * page, dtype=torch.bool, device="cuda")
+    other[slots[keep].long()] = False
+    assert bool(rows(kp)[other].isnan().all()) and bool(rows(vp)[other].isnan().all())  # left as they were
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,d,lens", [(5, 1, 64, [1]), (8, 8, 128, [3, 0, 130, 1, 64]), (4, 2, 128, [700, 0, 0, 1]),
+                                           (32, 8, 128, [257, 1000])])
+def test_varlen_layout(cuda_lib, Hq, Hkv, d, lens):
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    tok = int(cu[-1])
+    q, k, v, w = _inputs(tok, Hq, Hkv, d, tok)
+    cfg = msa.rope_cfg(d, theta=500000.0, norm=True, q_weight=w[0])  # k: no weight
+    qo, ko, vo = msa.qk_norm_rope_varlen(q, k, v, cu, cfg)
+    pos = torch.cat([torch.arange(x) for x in lens]).int().cuda()
+    c = dict(norm=True, eps=1e-6, rot=d, freq=_freq(d, 500000.0), inter=False)
+    for t, x, ww, H in ((qo, q, w[0], Hq), (ko, k, None, Hkv)):
+        seqs = msa.unpack_varlen(t, H, cu, d)
+        _check(torch.cat([s.transpose(0, 1) for s in seqs]), x, ww, c, pos, "varlen")
+    assert torch.equal(torch.cat([s.transpose(0, 1) for s in msa.unpack_varlen(vo, Hkv, cu, d)]), v)
+
+
+@pytest.mark.gpu
+def test_many_sequences(cuda_lib):
+    """More sequences than one launch's table holds."""
+    rng = np.random.default_rng(3)
+    lens = rng.integers(0, 4, 2500)
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    tok = int(cu[-1])
+    q, k, v, w = _inputs(tok, 2, 1, 64, 9)
+    qo, ko, vo = msa.qk_norm_rope_varlen(q, k, v, cu, msa.rope_cfg(64))
+    pos = torch.from_numpy(np.concatenate([np.arange(x) for x in lens]).astype(np.int32)).cuda()
+    c = dict(norm=False, eps=0.0, rot=64, freq=_freq(64), inter=False)
+    _check(torch.cat([s.transpose(0, 1) for s in msa.unpack_varlen(qo, 2, cu, 64)]), q, None, c, pos, "q")
+
+
+@pytest.mark.gpu
+def test_far_positions_given_angles_and_factor(cuda_lib):
+    """Angles of positions up to 2^31 - 1, negative ones, angles above a turn, a factor on the rotation."""
+    tok, Hq, Hkv, d = 64, 4, 2, 128
+    q, k, v, w = _inputs(tok, Hq, Hkv, d, 77)
+    rng = np.random.default_rng(7)
+    p = rng.integers(-(1 << 31), 1 << 31, tok)
+    p[:4] = [0, (1 << 31) - 1, -(1 << 31), -1]
+    pos = torch.from_numpy(p.astype(np.int32)).cuda()
+    # multiples of 2^-20: position * f is exact in 64 bits, so the reference has the true angle
+    freq = (rng.integers(-(1 << 22), 1 << 22, d // 2) / 2.0 ** 20).tolist()
+    cfg = msa.rope_cfg(d, inv_freq=freq, rot_scale=1.25)
+    qo, _, _ = msa.qk_norm_rope(*(t[None] for t in (q, k, v)), cfg, positions=pos)
+    # the reference's cos reduces an angle of up to 2^33 by pi in 64 bits: exact to its last bit
+    y, slack = norm_rope(q, None, False, 0.0, d, freq, False, pos, 1.25)
+    # f / (2 pi): two roundings of 2^-53, so position * f is off by at most 4 * 2^-52 * 2^31 = 2^-19 rad
+    slack = 2 * slack  # which was the pair's size times 2^-19 (32 * 2^-24) already
+    check_rounded(qo[0].transpose(0, 1), y, slack, "far")
+
+
+@pytest.mark.gpu
+def test_zeros_infinities_and_bad_slots(cuda_lib):
+    tok, Hq, Hkv, d, page = 8, 2, 1, 64, 16
+    q, k, v, w = _inputs(tok, Hq, Hkv, d, 5)
+    q[0, 0] = 0
+    q[1, 1, 3] = float("inf")
+    q[2, 0, 9] = float("nan")
+    cfg = msa.rope_cfg(d, norm=True, eps=0.0)
+    kp, vp = (torch.zeros(2, Hkv, page, d, dtype=BF, device="cuda") for _ in range(2))
+    slots = torch.arange(tok, dtype=torch.int32, device="cuda")
+    slots[3], slots[4] = 32, 1 << 30  # behind the pool
+    qo, ko, _ = msa.qk_norm_rope(*(t[None] for t in (q, k, v)), cfg, k_pages=kp, v_pages=vp, slots=slots)
+    assert cuda_lib.poll_device_status() == msa.MSA_ERR_INDEX
+    assert cuda_lib.poll_device_status() == 0
+    assert torch.equal(kp[0, 0, 5:8], ko[0, 0, 5:8]) and not bool(kp[0, 0, 3:5].any()) and not bool(kp[1].any())
+    assert bool(qo[0, 0, 0].isnan().all())     # 0 / 0: a zero row without eps
+    assert bool(qo[0, 1, 1].isnan().any()) and bool(qo[0, 0, 2].isnan().all())
+    good = torch.ones(Hq, tok, dtype=torch.bool, device="cuda")
+    good[0, 0] = good[1, 1] = good[0, 2] = False
+    assert bool(qo[0][good].isfinite().all())  # a bad row stays its own
+
+
+@pytest.mark.gpu
+def test_streams_and_capture(cuda_lib):
+    tok, Hq, Hkv, d = 19, 4, 2, 128
+    q, k, v, w = _inputs(tok, Hq, Hkv, d, 6)
+    x = [t[None] for t in (q, k, v)]
+    cfg = msa.rope_cfg(d, norm=True, q_weight=w[0], k_weight=w[1])
+    want = msa.qk_norm_rope(*x, cfg)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = msa.qk_norm_rope(*x, cfg, stream=side)
+    side.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    out = [torch.zeros_like(t) for t in want]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        msa.qk_norm_rope(*x, cfg, q=out[0], k=out[1], v=out[2])
+    for _ in range(2):
+        for t in out:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want):
+            assert torch.equal(a, b)
