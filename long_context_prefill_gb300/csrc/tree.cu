@@ -54,7 +54,7 @@ float effective_scale(const msa_shape& s);
 
 namespace {
 
-constexpr int kCtas = 152;  // parts of the line of tiles
+constexpr int kCtas = 152;  // parts of the line of tiles, if it has as many tiles
 constexpr int kThreads = 384;
 constexpr int kCleanWarp = 8, kMmaWarp0 = 9, kLoaderWarp = 10, kMmaWarp1 = 11;
 constexpr int kSegSlots = 4;
@@ -161,7 +161,8 @@ __device__ __forceinline__ bool request(const TreeArgs& A, int b, int& L, int& T
   return !bad && T > 0;
 }
 __device__ __forceinline__ int key_tiles(int L) { return (L + 127) >> 7; }
-__device__ __forceinline__ int64_t part_begin(int64_t W, int c) { return W * c / kCtas; }
+__device__ __forceinline__ int parts(int64_t W) { return W < kCtas ? (int)W : kCtas; }
+__device__ __forceinline__ int64_t part_begin(int64_t W, int c) { return W < kCtas ? c : W * c / kCtas; }
 
 template <int D, bool kTwo>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -207,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (w < warp) base += wsum[w];
       W += wsum[w];
     }
-    const int64_t lo = part_begin(W, blockIdx.x);
+    const int64_t lo = part_begin(W, blockIdx.x);  // at or above W in a CTA without a part
     int64_t at = base + inc - mine;
     if (threadIdx.x == 0) { start[0] = 0; start[1] = 0; start[2] = W; }
     __syncthreads();
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t W = start[2], lo = part_begin(W, blockIdx.x), hi = part_begin(W, blockIdx.x + 1);
   const int first_b = (int)start[0];
   const int64_t first_tile = start[1];
-  if (lo >= hi) return;  // the whole CTA agrees; nothing is held yet
+  if ((int)blockIdx.x >= parts(W)) return;  // the whole CTA agrees; nothing is held yet
 
   if (warp == 0) {
     tmem_alloc(const_cast<uint32_t*>(&misc[0]), kTmemCols);
@@ -705,7 +706,8 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeArgs 
   const int64_t W = A.prefix[A.B], p0 = A.prefix[b], p1 = A.prefix[b + 1];
   if (p1 == p0) return;
   const int64_t tiles = (p1 - p0) / items, s0 = p0 + item * tiles, s1 = s0 + tiles;
-  const int c0 = (int)(((s0 + 1) * kCtas - 1) / W), c1 = (int)((s1 * kCtas - 1) / W);
+  const int G = parts(W);  // part c holds tile x: the largest c with W c / G <= x
+  const int c0 = (int)(((s0 + 1) * G - 1) / W), c1 = (int)((s1 * G - 1) / W);
   if (c0 == c1) return;  // one CTA finished it
   const int rb = item % A.RB, kvh = item / A.RB;
   const int width = min(256, A.R - 256 * rb), full = min(256, A.R);
@@ -714,24 +716,46 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeArgs 
   const int c4 = e / width, rw = e - c4 * width, rr = 256 * rb + rw;
   const int T = A.tree_len ? A.tree_len[b] : A.n;
   if (rr % A.n >= T) return;
-  auto slot = [&](int c) { return (int64_t)(2 * c + (part_begin(W, c) > s0 ? 0 : 1)); };
-  float m = -INFINITY;
-  for (int c = c0; c <= c1; ++c)
-    if (part_begin(W, c) < part_begin(W, c + 1)) m = fmaxf(m, A.part_ml[slot(c) * full + rw].x);
-  const float ref = m == -INFINITY ? 0.f : m;
-  float l = 0.f;
+  auto slot = [&](int c) { return (int64_t)(2 * c + (c == c0 ? 1 : 0)); };  // the first part starts the item
+  // one pass, kAhead parts at a time: their loads are all in flight before the first is used
+  constexpr int kAhead = 8;
+  float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = c0; c <= c1; ++c) {
-    if (part_begin(W, c) >= part_begin(W, c + 1)) continue;
-    const int64_t sl = slot(c);
-    const float2 x = A.part_ml[sl * full + rw];
-    const float4 y = A.part[sl * (D / 4) * full + (int64_t)c4 * width + rw];
-    const float w = ex2(x.x - ref);
-    l += w * x.y;
-    o.x += w * y.x;
-    o.y += w * y.y;
-    o.z += w * y.z;
-    o.w += w * y.w;
+  const float2* ml = A.part_ml + rw;
+  const float4* part = A.part + (int64_t)c4 * width + rw;
+  for (int c = c0; c <= c1; c += kAhead) {
+    float2 x[kAhead];
+    float4 y[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int64_t sl = slot(min(c + k, c1));
+      x[k] = ml[sl * full];
+      y[k] = part[sl * (D / 4) * full];
+    }
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (c + k > c1) x[k] = make_float2(-INFINITY, 0.f);
+      top = fmaxf(top, x[k].x);
+    }
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float keep = ex2(m - ref);
+    m = top;
+    l *= keep;
+    o.x *= keep;
+    o.y *= keep;
+    o.z *= keep;
+    o.w *= keep;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (c + k > c1) continue;  // a repeated last part carries nothing (its values may be NaN)
+      const float w = ex2(x[k].x - ref);
+      l += w * x[k].y;
+      o.x += w * y[k].x;
+      o.y += w * y[k].y;
+      o.z += w * y[k].z;
+      o.w += w * y[k].w;
+    }
   }
   const bool some = !(l == 0.f);
   const float inv = some ? 1.f / l : 0.f;
