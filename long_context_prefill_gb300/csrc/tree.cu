@@ -60,7 +60,10 @@ constexpr int kCleanWarp = 8, kMmaWarp0 = 9, kLoaderWarp = 10, kMmaWarp1 = 11;
 constexpr int kSegSlots = 4;
 constexpr int kSegReaders = 11;  // 8 softmax warps, 2 issuers, the cleaner
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0, kColO = 256;  // S of group X at 128 X (P over its first 64), O at 256 + 128 X
+// TMEM columns.  Up to 128 rows: S of group X at 128 X, P over its first 64.
+// Above: one S that the groups use in turn, P of group X at 128 + 64 X.  O of
+// group X at 256 + 128 X.
+constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
 constexpr int kPChunk = 4;
 constexpr uint32_t kIdleNs = 64;
@@ -98,7 +101,9 @@ enum {
   kBarODone = 8,                    // [2]
   kBarOFree = 10,                   // [2]
   kBarML = 12,
-  kBarSegFull = 13,                 // [kSegSlots]
+  kBarSFree = 13,                   // kTwo: the scores are in registers
+  kBarPV = 14,                      // [2] kTwo: the group's last P has been used
+  kBarSegFull = 16,                 // [kSegSlots]
   kBarSegEmpty = kBarSegFull + kSegSlots,
   kBarRing = kBarSegEmpty + kSegSlots  // full[kSlots], empty[kSlots], ready[kSlots]
 };
@@ -236,20 +241,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 32 * kMmaWarp0) {
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars[kBarQFull + x], 1);
-      mbar_init(&bars[kBarQEmpty + x], 2);
+      mbar_init(&bars[kBarQEmpty + x], kTwo ? 1 : 2);
       mbar_init(&bars[kBarSFull + x], 1);
       mbar_init(&bars[kBarPFull + x], 4);
       mbar_init(&bars[kBarODone + x], 1);
       mbar_init(&bars[kBarOFree + x], 4);
+      mbar_init(&bars[kBarPV + x], 1);
     }
     mbar_init(&bars[kBarML], 4);
+    mbar_init(&bars[kBarSFree], 4);
     for (int s = 0; s < kSegSlots; ++s) {
       mbar_init(&bars[kBarSegFull + s], 1);
       mbar_init(&bars[kBarSegEmpty + s], kSegReaders);
     }
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&bFull[s], 1);
-      mbar_init(&bEmpty[s], kTwo ? 2 : 1);
+      mbar_init(&bEmpty[s], 1);
       mbar_init(&bReady[s], 1);
     }
     misc[2] = 0;
@@ -271,9 +278,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     return g.b >= 0;
   };
   auto ready = [&](int idx) { return mbar_wait(&bReady[idx % kSlots], (idx / kSlots) & 1); };
+  constexpr uint32_t id_qk = idesc_bf16_f32(128, 128, false, false);
+  constexpr uint32_t id_pv = idesc_bf16_f32(128, D, false, true);
+  constexpr uint64_t kTileDesc = Ly::kTile >> 4;
+  const uint64_t dq = sdesc_sw128(smem_u32(sm + Ly::kQ), 16, 1024);
+  const uint64_t dk = sdesc_sw128(smem_u32(sm + Ly::kRing), 16, 1024);     // + slot * kTileDesc
+  const uint64_t dv = sdesc_sw128(smem_u32(sm + Ly::kRing), 16384, 1024);
+  auto issue_qk = [&](uint32_t d, uint64_t q0, uint64_t k0) {  // S = Q K^T of one tile, by one thread
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      const uint64_t off = (uint64_t)((kk >> 2) * 1024 + (kk & 3) * 2);
+      mma_bf16_ss(d, q0 + off, k0 + off, id_qk, kk > 0 ? 1u : 0u);
+    }
+  };
+  auto issue_pv_mma = [&](uint32_t d, uint32_t p, uint64_t v0, bool first) {  // O (+)= P V
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+      mma_bf16_ts(d, p + 8 * kk, v0 + (uint64_t)(kk * 128), id_pv, (!first || kk > 0) ? 1u : 0u);
+  };
   // rows of softmax group X in the 256-row block rb (one group's rows serve both groups unless kTwo)
   auto group_rows = [&](int rb, int X) { return min(128, A.R - 256 * rb - (kTwo ? 128 * X : 0)); };
 
+  // the block starts with 3 x 128 threads x 168 registers; the softmax threads (a row's 128 scores each) take
+  // 208 and the others' 72: 2 x 208 + 72 <= 3 x 168
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == kLoaderWarp) {
     // ------------------------------------------------------------ loader
     const uint64_t policy = A.RB == 1 ? policy_evict_first() : policy_evict_last();
@@ -401,24 +430,81 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) mbar_arrive(&bReady[st]);
       }
-  } else if (warp == kMmaWarp0 || warp == kMmaWarp1) {
+  } else if (kTwo && warp == kMmaWarp0) {
+    // ------------------------------------------------------------ scores of both groups
+    int tile = 0, use = 0;  // tiles so far, uses of S so far
+    Seg g;
+    for (int s = 0; next_seg(s, g); ++s) {
+      if (!mbar_wait(&bars[kBarQFull], s & 1)) { ok = false; break; }
+      for (int t = g.t0; t < g.t1 && ok; ++t, ++tile) {
+        const int kst = 2 * tile % kSlots;
+        if (misc[2] || !ready(2 * tile)) { ok = false; break; }
+#pragma unroll
+        for (int X = 0; X < 2; ++X) {
+          if (group_rows(g.rb, X) <= 0) continue;
+          if (use > 0 && !mbar_wait(&bars[kBarSFree], (use - 1) & 1)) { ok = false; break; }
+          ++use;
+          tc_fence_after();
+          if (lane == 0) {
+            issue_qk(tmem + kColS, dq + (uint64_t)X * kTileDesc, dk + (uint64_t)kst * kTileDesc);
+            mma_commit(&bars[kBarSFull + X]);
+          }
+          __syncwarp();
+        }
+        if (ok && lane == 0) mma_commit(&bEmpty[kst]);
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (lane == 0) mma_commit(&bars[kBarQEmpty]);
+      __syncwarp();
+    }
+  } else if (kTwo) {
+    // ------------------------------------------------------------ O += P V of both groups
+    int tile = 0, seen[2] = {0, 0};  // tiles so far, P's of each group
+    Seg g;
+    for (int s = 0; next_seg(s, g); ++s) {
+      // O_X of the segment before has been read: its first PV here, or (no rows) its end, waits for that
+      auto o_free = [&](int X) { return s == 0 || mbar_wait(&bars[kBarOFree + X], (s - 1) & 1); };
+      for (int t = g.t0; t < g.t1 && ok; ++t, ++tile) {
+        const int vst = (2 * tile + 1) % kSlots;
+        if (misc[2] || !ready(2 * tile + 1)) { ok = false; break; }
+#pragma unroll
+        for (int X = 0; X < 2; ++X) {
+          if (group_rows(g.rb, X) <= 0) continue;
+          if (t == g.t0 && !o_free(X)) { ok = false; break; }
+          if (!mbar_wait(&bars[kBarPFull + X], seen[X] & 1)) { ok = false; break; }
+          ++seen[X];
+          tc_fence_after();
+          if (lane == 0) {
+            issue_pv_mma(tmem + kColO + 128 * X, tmem + kColP + 64 * X, dv + (uint64_t)vst * kTileDesc, t == g.t0);
+            mma_commit(&bars[kBarPV + X]);
+          }
+          __syncwarp();
+        }
+        if (ok && lane == 0) mma_commit(&bEmpty[vst]);
+        __syncwarp();
+      }
+      if (!ok) break;
+      for (int X = 0; X < 2; ++X)
+        if (group_rows(g.rb, X) <= 0 && !o_free(X)) ok = false;
+      if (!ok) break;
+      if (lane == 0) {
+        mma_commit(&bars[kBarODone]);
+        mma_commit(&bars[kBarODone + 1]);
+      }
+      __syncwarp();
+    }
+  } else if (!kTwo) {
     // ------------------------------------------------------------ MMA issuer of group X
     const int X = warp == kMmaWarp0 ? 0 : 1;
-    constexpr uint32_t id_qk = idesc_bf16_f32(128, 128, false, false);
-    constexpr uint32_t id_pv = idesc_bf16_f32(128, D, false, true);
-    constexpr uint64_t kTileDesc = Ly::kTile >> 4;
-    const uint64_t dq = sdesc_sw128(smem_u32(sm + Ly::kQ), 16, 1024);
-    const uint64_t dk = sdesc_sw128(smem_u32(sm + Ly::kRing), 16, 1024);
-    const uint64_t dv = sdesc_sw128(smem_u32(sm + Ly::kRing), 16384, 1024);
     const uint32_t tS = tmem + kColS + 128 * X, tO = tmem + kColO + 128 * X;
     int tile0 = 0;   // CTA tile index of the segment's first tile
     int pphase = 0;  // tiles whose P this issuer has waited for
     Seg g;
     for (int s = 0; next_seg(s, g); ++s) {
-      const int nq = kTwo ? 1 : 2, buf = s % nq, nt = g.t1 - g.t0;
-      const uint64_t q0 = dq + (uint64_t)(kTwo ? X : buf) * kTileDesc;
-      const bool active = !kTwo || group_rows(g.rb, X) > 0;
-      if (!mbar_wait(&bars[kBarQFull + buf], (s / nq) & 1)) { ok = false; break; }
+      const int buf = s & 1, nt = g.t1 - g.t0;
+      const uint64_t q0 = dq + (uint64_t)buf * kTileDesc;
+      if (!mbar_wait(&bars[kBarQFull + buf], (s >> 1) & 1)) { ok = false; break; }
       int pending = -1;
       bool first = true;
       // O_X of the segment before has been read: its first PV here, or its end, waits for that
@@ -431,10 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ready(vidx)) return false;
         tc_fence_after();
         if (lane == 0) {
-          const uint64_t v0 = dv + (uint64_t)vst * kTileDesc;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ts(tO, tS + 8 * kk, v0 + (uint64_t)(kk * 128), id_pv, (!first || kk > 0) ? 1u : 0u);
+          issue_pv_mma(tO, tS, dv + (uint64_t)vst * kTileDesc, first);
           mma_commit(&bEmpty[vst]);
         }
         __syncwarp();
@@ -442,34 +525,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         pending = -1;
         return true;
       };
-      for (int t = kTwo ? 0 : X; t < nt; t += kTwo ? 1 : 2) {
+      for (int t = X; t < nt; t += 2) {
         if (misc[2]) { ok = false; break; }
         const int kidx = 2 * (tile0 + t), kst = kidx % kSlots;
         if (pending >= 0 && !issue_pv()) { ok = false; break; }
         if (!ready(kidx)) { ok = false; break; }
         tc_fence_after();
-        if (active) {
-          if (lane == 0) {
-            const uint64_t k0 = dk + (uint64_t)kst * kTileDesc;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t off = (uint64_t)((kk >> 2) * 1024 + (kk & 3) * 2);
-              mma_bf16_ss(tS, q0 + off, k0 + off, id_qk, kk > 0 ? 1u : 0u);
-            }
-            mma_commit(&bars[kBarSFull + X]);
-            mma_commit(&bEmpty[kst]);
-          }
-          __syncwarp();
-          pending = tile0 + t;
-        } else {  // no rows: release both tiles
-          const int vst = (kidx + 1) % kSlots;
-          if (!ready(kidx + 1)) { ok = false; break; }
-          if (lane == 0) {
-            mbar_arrive(&bEmpty[kst]);
-            mbar_arrive(&bEmpty[vst]);
-          }
-          __syncwarp();
+        if (lane == 0) {
+          issue_qk(tS, q0, dk + (uint64_t)kst * kTileDesc);
+          mma_commit(&bars[kBarSFull + X]);
+          mma_commit(&bEmpty[kst]);
         }
+        __syncwarp();
+        pending = tile0 + t;
       }
       if (!ok) break;
       if (lane == 0) mma_commit(&bars[kBarQEmpty + buf]);  // every S of this segment
@@ -479,11 +547,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       tile0 += nt;
     }
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ------------------------------------------------------------ softmax group X
     const int X = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    const uint32_t tS = tmem + lane_base + kColS + 128 * X, tO = tmem + lane_base + kColO + 128 * X;
+    const uint32_t tS = tmem + lane_base + kColS + (kTwo ? 0 : 128 * X), tO = tmem + lane_base + kColO + 128 * X;
+    const uint32_t tP = kTwo ? tmem + lane_base + kColP + 64 * X : tS;
     const float c2 = A.scale_log2;
     int seen = 0;  // tiles of this group so far (phase of S)
     Seg g;
@@ -524,14 +595,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (!mbar_wait(&bars[kBarSFull + X], seen & 1)) { ok = false; break; }
-          ++seen;
           tc_fence_after();
+          float sv[128];
           if (warp_in) {
-            float sv[128];
             uint32_t* u = reinterpret_cast<uint32_t*>(sv);
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(u + 32 * c));
             tmem_ld_wait();
+          }
+          if (kTwo) {  // the scores are in registers: S is free for the other group's
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kBarSFree]);
+          }
+          // kTwo: P and O of this group are its own once the product with its last P is done
+          auto pv_done = [&]() -> bool {
+            if (!kTwo || seen == 0) return true;
+            if (!mbar_wait(&bars[kBarPV + X], (seen - 1) & 1)) return false;
+            tc_fence_after();
+            return true;
+          };
+          if (warp_in) {
             if (masked) {
 #pragma unroll
               for (int k = 0; k < 128; ++k) sv[k] = ((vw[k >> 5] >> (k & 31)) & 1u) ? sv[k] : -INFINITY;
@@ -558,6 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float mref = (m_used == -INFINITY) ? 0.f : m_used;
             const uint64_t c2x2 = pk2(c2, c2), negm = pk2(-mref, -mref);
             uint64_t acc[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
+            if (!pv_done()) { ok = false; break; }
             // P rounded to bf16 for the second MMA (its operand type is V's); the row sum keeps fp32
 #pragma unroll
             for (int h = 0; h < 64 / kPChunk; ++h) {
@@ -574,13 +659,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 up2(p, p0, p1);
                 pk[k] = pack_bf16x2(p0, p1);
               }
-              tmem_st4(tS + kPChunk * h, pk);
+              tmem_st4(tP + kPChunk * h, pk);
             }
             float a0, a1, a2, a3;
             up2(acc[0], a0, a1);
             up2(acc[1], a2, a3);
             l = l * alpha + ((a0 + a1) + (a2 + a3));
-            if (any && !first) {  // O_X: its previous PV completed before S was ready
+            if (any && !first) {  // O_X: its previous PV has completed (before S was ready, or waited for)
 #pragma unroll 1
               for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
@@ -593,7 +678,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tmem_st_wait();
             first = false;
+          } else if (!pv_done()) {
+            ok = false;
+            break;
           }
+          ++seen;
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[kBarPFull + X]);
