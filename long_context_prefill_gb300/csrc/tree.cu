@@ -56,7 +56,7 @@ namespace {
 
 constexpr int kCtas = 152;  // parts of the line of tiles, if it has as many tiles
 constexpr int kThreads = 384;
-constexpr int kCleanWarp = 8, kMmaWarp0 = 9, kLoaderWarp = 10, kMmaWarp1 = 11;
+constexpr int kCleanWarp = 8, kMmaWarp0 = 9, kLoaderWarp = 10;  // 11: the other issuer
 constexpr int kSegSlots = 4;
 constexpr int kSegReaders = 11;  // 8 softmax warps, 2 issuers, the cleaner
 constexpr uint32_t kTmemCols = 512;
@@ -98,9 +98,9 @@ enum {
   kBarQEmpty = 2,                   // [2]
   kBarSFull = 4,                    // [2]
   kBarPFull = 6,                    // [2]
-  kBarODone = 8,                    // [2]
-  kBarOFree = 10,                   // [2]
-  kBarML = 12,
+  kBarODone = 8,                    // [2] every product of the group's segment is done (kTwo: of a group without rows)
+  kBarOFree = 10,                   // [2] O of the segment has been read
+  kBarML = 12,                      // maxima and sums of both groups are written
   kBarSFree = 13,                   // kTwo: the scores are in registers
   kBarPV = 14,                      // [2] kTwo: the group's last P has been used
   kBarSegFull = 16,                 // [kSegSlots]
@@ -116,11 +116,10 @@ struct Lay {
   static constexpr int kRing = 2 * kTile;
   static constexpr int kSeg = kRing + kSlots * kTile;
   static constexpr int kML = kSeg + kSegSlots * (int)sizeof(Seg);
-  static constexpr int kBars = kML + 128 * 8;
+  static constexpr int kBars = kML + 2 * 128 * 8;
   static constexpr int kNumBars = kBarRing + 3 * kSlots;
   static constexpr int kMisc = kBars + kNumBars * 8;  // [0] TMEM base, [2] abort
-  static constexpr int kTotal = kMisc + 16;
-  static constexpr int kAlloc = kTotal + 1024;
+  static constexpr int kAlloc = kMisc + 16;
   static_assert(kAlloc <= 227 * 1024 && kAlloc > 120 * 1024, "shared memory: one CTA per SM");
 };
 
@@ -174,8 +173,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tree_attn_kernel(const __grid_constant__ TreeMaps M, const TreeArgs A) {
   using Ly = Lay<D>;
   constexpr int kSlots = Ly::kSlots;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t sm[];  // swizzled tiles start on 1 KB
+  if (smem_u32(sm) & 1023) {
+    if (threadIdx.x == 0) atomicCAS(A.err, 0, (int)kErrTimeout);
+    return;
+  }
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Ly::kBars);
   uint64_t* bFull = bars + kBarRing;
   uint64_t* bEmpty = bFull + kSlots;
@@ -187,56 +189,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- this CTA's part [lo, hi) of the line of tiles, and the request it starts in
-  const int items = A.Hkv * A.RB;  // items of a request
-  int64_t* wsum = reinterpret_cast<int64_t*>(sm + Ly::kRing);  // scratch until the pipeline starts
-  int64_t* start = wsum + 16;                                  // [0] request, [1] its first tile, [2] all tiles
-  {
-    const int per = (A.B + kThreads - 1) / kThreads;
-    const int b0 = min(A.B, (int)threadIdx.x * per), b1 = min(A.B, b0 + per);
-    int64_t mine = 0;
-    int L, T;
-    bool bad;
-    for (int b = b0; b < b1; ++b)
-      if (request(A, b, L, T, bad)) mine += (int64_t)items * key_tiles(L);
-    int64_t inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    if (lane == 31) wsum[warp] = inc;
-    __syncthreads();
-    int64_t base = 0, W = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) base += wsum[w];
-      W += wsum[w];
-    }
-    const int64_t lo = part_begin(W, blockIdx.x);  // at or above W in a CTA without a part
-    int64_t at = base + inc - mine;
-    if (threadIdx.x == 0) { start[0] = 0; start[1] = 0; start[2] = W; }
-    __syncthreads();
-    for (int b = b0; b < b1; ++b) {
-      const int64_t t = request(A, b, L, T, bad) ? (int64_t)items * key_tiles(L) : 0;
-      if (at <= lo && lo < at + t) { start[0] = b; start[1] = at; }
-      if (blockIdx.x == 0) {
-        A.prefix[b] = at;
-        if (bad) atomicCAS(A.err, 0, (int)kErrIndex);
-      }
-      at += t;
-    }
-    if (blockIdx.x == 0 && threadIdx.x == 0) A.prefix[A.B] = W;
-    __syncthreads();
-  }
-  const int64_t W = start[2], lo = part_begin(W, blockIdx.x), hi = part_begin(W, blockIdx.x + 1);
-  const int first_b = (int)start[0];
-  const int64_t first_tile = start[1];
-  if ((int)blockIdx.x >= parts(W)) return;  // the whole CTA agrees; nothing is held yet
-
   if (warp == 0) {
     tmem_alloc(const_cast<uint32_t*>(&misc[0]), kTmemCols);
     tmem_relinquish();
+  }
+  if (threadIdx.x == 32 * kLoaderWarp) {
+    tma_prefetch_desc(&M.q);
+    tma_prefetch_desc(&M.k);
+    tma_prefetch_desc(&M.v);
   }
   if (threadIdx.x == 32 * kMmaWarp0) {
     for (int x = 0; x < 2; ++x) {
@@ -245,10 +205,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars[kBarSFull + x], 1);
       mbar_init(&bars[kBarPFull + x], 4);
       mbar_init(&bars[kBarODone + x], 1);
-      mbar_init(&bars[kBarOFree + x], 4);
+      mbar_init(&bars[kBarOFree + x], kTwo ? 4 : 8);
       mbar_init(&bars[kBarPV + x], 1);
     }
-    mbar_init(&bars[kBarML], 4);
+    mbar_init(&bars[kBarML], 8);
     mbar_init(&bars[kBarSFree], 4);
     for (int s = 0; s < kSegSlots; ++s) {
       mbar_init(&bars[kBarSegFull + s], 1);
@@ -262,10 +222,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     misc[2] = 0;
     fence_mbar_init();
   }
+  // ---- this CTA's part [lo, hi) of the line of tiles, and the request it starts in
+  const int items = A.Hkv * A.RB;  // items of a request
+  int64_t* wsum = reinterpret_cast<int64_t*>(sm + Ly::kRing);  // scratch until the pipeline starts
+  int64_t* start = wsum + 16;                                  // [0] request, [1] its first tile
+  int64_t W = 0;                                               // all tiles
+  {
+    const int per = (A.B + kThreads - 1) / kThreads;
+    const int b0 = min(A.B, (int)threadIdx.x * per), b1 = min(A.B, b0 + per);
+    auto tiles = [&](int b) -> int64_t {
+      int L, T;
+      bool bad;
+      const bool live = request(A, b, L, T, bad);
+      if (bad && blockIdx.x == 0) atomicCAS(A.err, 0, (int)kErrIndex);
+      return live ? (int64_t)items * key_tiles(L) : 0;
+    };
+    int64_t own = 0, mine = 0;  // of the last request, of all of this thread's
+    for (int b = b0; b < b1; ++b) mine += own = tiles(b);
+    int64_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    int64_t base = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) base += wsum[w];
+      W += wsum[w];
+    }
+    const int64_t lo = part_begin(W, blockIdx.x);  // at or above W in a CTA without a part
+    int64_t at = base + inc - mine;
+    for (int b = b0; b < b1; ++b) {
+      const int64_t t = per == 1 ? own : tiles(b);
+      if (at <= lo && lo < at + t) { start[0] = b; start[1] = at; }
+      if (blockIdx.x == 0) A.prefix[b] = at;
+      at += t;
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) A.prefix[A.B] = W;
+  }
+  const int64_t lo = part_begin(W, blockIdx.x), hi = part_begin(W, blockIdx.x + 1);
   fence_proxy_async_smem();  // the scratch above lies in the ring that TMA fills
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if ((int)blockIdx.x >= parts(W)) {  // no part
+    if (warp == 0) tmem_dealloc(misc[0], kTmemCols);
+    return;
+  }
+  const int first_b = (int)start[0];
+  const int64_t first_tile = start[1];
   const uint32_t tmem = misc[0];
 
   // Segment s of this CTA as the readers see it; false: no more, or gave up.
@@ -306,11 +314,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kLoaderWarp) {
     // ------------------------------------------------------------ loader
     const uint64_t policy = A.RB == 1 ? policy_evict_first() : policy_evict_last();
-    if (lane == 0) {
-      tma_prefetch_desc(&M.q);
-      tma_prefetch_desc(&M.k);
-      tma_prefetch_desc(&M.v);
-    }
     const int pshift = 7 - A.page_shift, pp = 1 << pshift;  // pages of a tile
     const int P = 1 << A.page_shift;
     int64_t at = first_tile;  // first tile of item 0 of request b
@@ -484,15 +487,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && lane == 0) mma_commit(&bEmpty[vst]);
         __syncwarp();
       }
+      for (int X = 0; X < 2 && ok; ++X)
+        if (group_rows(g.rb, X) <= 0) {
+          ok = o_free(X);
+          if (ok && lane == 0) mbar_arrive(&bars[kBarODone + X]);
+          __syncwarp();
+        }
       if (!ok) break;
-      for (int X = 0; X < 2; ++X)
-        if (group_rows(g.rb, X) <= 0 && !o_free(X)) ok = false;
-      if (!ok) break;
-      if (lane == 0) {
-        mma_commit(&bars[kBarODone]);
-        mma_commit(&bars[kBarODone + 1]);
-      }
-      __syncwarp();
     }
   } else if (!kTwo) {
     // ------------------------------------------------------------ MMA issuer of group X
@@ -557,6 +558,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tP = kTwo ? tmem + lane_base + kColP + 64 * X : tS;
     const float c2 = A.scale_log2;
     int seen = 0;  // tiles of this group so far (phase of S)
+    int idle = 0;  // segments without rows for this group
+    // kTwo: P and O of this group are its own once the product with its last P is done
+    auto pv_done = [&]() -> bool {
+      if (!kTwo || seen == 0) return true;
+      if (!mbar_wait(&bars[kBarPV + X], (seen - 1) & 1)) return false;
+      tc_fence_after();
+      return true;
+    };
     Seg g;
     for (int s = 0; next_seg(s, g); ++s) {
       const int rows = group_rows(g.rb, X);
@@ -602,19 +611,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(u + 32 * c));
             tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int k = 0; k < 128; ++k) sv[k] = 0.f;
           }
           if (kTwo) {  // the scores are in registers: S is free for the other group's
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[kBarSFree]);
           }
-          // kTwo: P and O of this group are its own once the product with its last P is done
-          auto pv_done = [&]() -> bool {
-            if (!kTwo || seen == 0) return true;
-            if (!mbar_wait(&bars[kBarPV + X], (seen - 1) & 1)) return false;
-            tc_fence_after();
-            return true;
-          };
           if (warp_in) {
             if (masked) {
 #pragma unroll
@@ -689,84 +694,75 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       if (!ok) break;
 
-      // ---- the segment's end: O / l and LSE, or the part's unnormalised state
-      if (!kTwo && X == 1) {  // group 0 joins: hand over this group's maximum and sum
-        if (s > 0 && !mbar_wait(&bars[kBarOFree + 1], (s - 1) & 1)) { ok = false; break; }
-        ml[r] = make_float2(m_used, l);
+      // ---- the segment's end: O / l and LSE, or the part's unnormalised state.
+      // O goes to registers first, so that the next segment's products may start
+      // while it is written.  Up to 128 rows, each group takes half of the
+      // columns of both groups' O.
+      constexpr int kCols = kTwo ? D : D / 2;  // columns that a thread writes
+      const int col0 = kTwo ? 0 : X * kCols;
+      float ov[kCols];
+      if (kTwo) {
+        if (rows > 0 ? !pv_done() : !mbar_wait(&bars[kBarODone + X], idle++ & 1)) { ok = false; break; }
+        // every warp loads, with rows or not: values defined on one path only would stay live around the loop
+#pragma unroll
+        for (int c = 0; c < kCols / 32; ++c) tmem_ld32(tO + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(ov + 32 * c));
+        tmem_ld_wait();
+      } else {
+        if (s > 0 && !mbar_wait(&bars[kBarOFree], (s - 1) & 1)) { ok = false; break; }  // ml has been read
+        ml[128 * X + r] = make_float2(m_used, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[kBarML]);
-        continue;
-      }
-      const bool both = !kTwo && nt > 1;
-      float w0 = 1.f, w1 = 0.f;
-      if (!kTwo) {
-        if (!mbar_wait(&bars[kBarML], s & 1)) { ok = false; break; }
-        if (both) {
-          const float2 o1 = ml[r];
-          const float m = fmaxf(m_used, o1.x);
-          const float ref = m == -INFINITY ? 0.f : m;
-          w0 = ex2(m_used - ref);
-          w1 = ex2(o1.x - ref);
-          l = l * w0 + o1.y * w1;
-          m_used = m;
+        if (!mbar_wait(&bars[kBarML], s & 1) || !mbar_wait(&bars[kBarODone], s & 1) ||
+            !mbar_wait(&bars[kBarODone + 1], s & 1)) {
+          ok = false;
+          break;
         }
-        if (!mbar_wait(&bars[kBarODone + 1], s & 1)) { ok = false; break; }
-      }
-      if (!mbar_wait(&bars[kBarODone + X], s & 1)) { ok = false; break; }
-      tc_fence_after();
-      if (warp_in) {
-        const bool whole = g.t0 == 0 && g.t1 == g.tiles;
-        const int64_t grow = (int64_t)(g.b * A.Hq + g.kvh * (A.Hq / A.Hkv)) * A.n + rr;
-        const bool some = !(l == 0.f);  // an attended key (a NaN among them shows in l)
-        const float inv = whole && some ? 1.f / l : 0.f;
-        const int width = min(256, A.R - 256 * g.rb);  // rows of the block
-        const int64_t slot = 2 * blockIdx.x + (g.t0 > 0 ? 0 : 1);
-        const int rw = rr - 256 * g.rb;
-        float4* part = A.part + slot * (D / 4) * min(256, A.R) + rw;
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          __syncwarp();
-          uint32_t o[32];
-          tmem_ld32(tO + 32 * c, o);
-          if (both) {
-            uint32_t q[32];
-            tmem_ld32(tO + 128 + 32 * c, q);
-            tmem_ld_wait();
+        tc_fence_after();
+        const float2 s0 = ml[r], s1 = ml[128 + r];
+        const float m = fmaxf(s0.x, s1.x), ref = m == -INFINITY ? 0.f : m;
+        const float w0 = ex2(s0.x - ref), w1 = ex2(s1.x - ref);
+        m_used = m;
+        l = s0.y * w0 + s1.y * w1;
+        const uint32_t t0 = tmem + lane_base + kColO + col0;
 #pragma unroll
-            for (int x = 0; x < 32; ++x)
-              o[x] = __float_as_uint(__uint_as_float(o[x]) * w0 + __uint_as_float(q[x]) * w1);
-          } else {
-            tmem_ld_wait();
-          }
-          if (!row_ok) continue;
-          if (whole) {
-            uint4* dst = reinterpret_cast<uint4*>(A.o + grow * D + 32 * c);
+        for (int c = 0; c < kCols / 32; ++c) {
+          uint32_t q[32];
+          tmem_ld32(t0 + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(ov + 32 * c));
+          tmem_ld32(t0 + 128 + 32 * c, q);
+          tmem_ld_wait();
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              uint32_t pk[4];
-#pragma unroll
-              for (int y = 0; y < 4; ++y)
-                pk[y] = pack_bf16x2(__uint_as_float(o[8 * x + 2 * y]) * inv, __uint_as_float(o[8 * x + 2 * y + 1]) * inv);
-              dst[x] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            }
-          } else {
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              part[(int64_t)(8 * c + x) * width] =
-                  make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]), __uint_as_float(o[4 * x + 2]),
-                              __uint_as_float(o[4 * x + 3]));
-          }
-        }
-        if (row_ok) {
-          if (!whole) A.part_ml[slot * min(256, A.R) + rw] = make_float2(m_used, l);
-          else if (A.lse) A.lse[grow] = some ? (m_used + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+          for (int x = 0; x < 32; ++x)  // a group without a tile has no O
+            ov[32 * c + x] = ov[32 * c + x] * w0 + (nt > 1 ? __uint_as_float(q[x]) * w1 : 0.f);
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&bars[kBarOFree + X]);
+        mbar_arrive(&bars[kBarOFree + (kTwo ? X : 0)]);
         if (!kTwo) mbar_arrive(&bars[kBarOFree + 1]);
+      }
+      if (!row_ok) continue;
+      const bool some = !(l == 0.f);  // an attended key (a NaN among them shows in l)
+      if (g.t0 == 0 && g.t1 == g.tiles) {
+        const int64_t grow = (int64_t)(g.b * A.Hq + g.kvh * (A.Hq / A.Hkv)) * A.n + rr;
+        const float inv = some ? 1.f / l : 0.f;
+        uint4* dst = reinterpret_cast<uint4*>(A.o + grow * D + col0);
+#pragma unroll
+        for (int x = 0; x < kCols / 8; ++x) {
+          uint32_t pk[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) pk[y] = pack_bf16x2(ov[8 * x + 2 * y] * inv, ov[8 * x + 2 * y + 1] * inv);
+          dst[x] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        }
+        if (A.lse && col0 == 0) A.lse[grow] = some ? (m_used + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+      } else {
+        const int width = min(256, A.R - 256 * g.rb), full = min(256, A.R), rw = rr - 256 * g.rb;
+        const int64_t slot = 2 * blockIdx.x + (g.t0 > 0 ? 0 : 1);
+        float4* part = A.part + slot * (D / 4) * full + (int64_t)(col0 / 4) * width + rw;
+#pragma unroll
+        for (int x = 0; x < kCols / 4; ++x, part += width)
+          *part = make_float4(ov[4 * x], ov[4 * x + 1], ov[4 * x + 2], ov[4 * x + 3]);
+        if (col0 == 0) A.part_ml[slot * full + rw] = make_float2(m_used, l);
       }
     }
   }
