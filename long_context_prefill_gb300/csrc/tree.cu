@@ -70,7 +70,7 @@ constexpr uint32_t kIdleNs = 64;
 constexpr int kMaxDrafts = 1024;
 
 struct TreeArgs {
-  int32_t B, Hq, Hkv, n, R, RB, page_shift, max_pages, num_pages, words;
+  int32_t B, Hq, Hkv, n, R, RB, page_shift, max_pages, num_pages, words, q_box;
   const int32_t *table, *seq_len, *tree_len;
   const uint32_t* mask;
   int64_t mask_stride;  // words between the masks of two requests (0: one mask for all)
@@ -84,7 +84,7 @@ struct TreeArgs {
 };
 
 struct TreeMaps {
-  CUtensorMap q, k, v;  // [rows, d] views, boxes of 64 columns x 16 rows (q), x page_size rows (k, v)
+  CUtensorMap q, k, v;  // [rows, d] views, boxes of 64 columns x q_box rows (q), x page_size rows (k, v)
 };
 
 // The part of one item that a CTA processes: tiles t0 .. t1 of its `tiles`.
@@ -355,6 +355,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&bars[kBarSegFull + s % kSegSlots]);
       }
       if (g.b < 0) break;
+      // ---- Q rows (their load overlaps the page entries')
+      {
+        const int nq = kTwo ? 1 : 2, buf = s % nq;
+        if (!mbar_wait_idle(&bars[kBarQEmpty + buf], ((s / nq) & 1) ^ 1, kIdleNs)) { ok = false; break; }
+        const int rows = min(kTwo ? 256 : 128, A.R - 256 * g.rb), boxes = (rows + A.q_box - 1) / A.q_box;
+        uint64_t* full = &bars[kBarQFull + buf];
+        if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(boxes * A.q_box * D * 2));
+        __syncwarp();
+        const int qrow = (g.b * A.Hq + g.kvh * (A.Hq / A.Hkv)) * A.n + 256 * g.rb;
+        if (lane < boxes * (D / 64)) {  // at most 8
+          const int c = lane & (D / 64 - 1), r = lane / (D / 64) * A.q_box;
+          tma_load_3d(sm + Ly::kQ + (kTwo ? r >> 7 : buf) * Ly::kTile + c * 16384 + (r & 127) * 128, &M.q, full, 64 * c,
+                      qrow + r, 0);
+        }
+      }
       // ---- pages of the first tiles: lane x holds entry base + x, and base + 32 + x ahead
       const int32_t* row = A.table + (int64_t)g.b * A.max_pages;
       const int np = (g.L + P - 1) >> A.page_shift;
@@ -368,21 +383,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       int base = g.t0 << pshift;
       int ids = entry(base + lane), ahead = entry(base + 32 + lane);
-      // ---- Q rows
-      {
-        const int nq = kTwo ? 1 : 2, buf = s % nq;
-        if (!mbar_wait_idle(&bars[kBarQEmpty + buf], ((s / nq) & 1) ^ 1, kIdleNs)) { ok = false; break; }
-        const int rows = min(kTwo ? 256 : 128, A.R - 256 * g.rb), boxes = (rows + 15) >> 4;
-        uint64_t* full = &bars[kBarQFull + buf];
-        if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(boxes * 16 * D * 2));
-        __syncwarp();
-        const int qrow = (g.b * A.Hq + g.kvh * (A.Hq / A.Hkv)) * A.n + 256 * g.rb;
-        for (int x = lane; x < boxes * (D / 64); x += 32) {
-          const int c = x & (D / 64 - 1), r = x / (D / 64);
-          tma_load_3d(sm + Ly::kQ + (kTwo ? r >> 3 : buf) * Ly::kTile + c * 16384 + (r & 7) * 2048, &M.q, full, 64 * c,
-                      qrow + 16 * r, 0);
-        }
-      }
       // ---- K and V tiles
       for (int t = g.t0; t < g.t1 && ok; ++t) {
         int off = (t << pshift) - base;
@@ -944,6 +944,8 @@ extern "C" msa_status msa_attn_tree(const msa_shape* shape, const void* q, const
   a.n = shape->n;
   a.R = shape->Hq / shape->Hkv * shape->n;
   a.RB = (a.R + 255) / 256;
+  // a load costs about 100 cycles whatever its size: few of them, and few rows that are not the group's
+  a.q_box = a.R <= 16 ? 16 : a.R <= 32 ? 32 : 64;
   a.page_shift = __builtin_ctz((unsigned)pages->page_size);
   a.max_pages = max_pages;
   a.num_pages = pages->num_pages;
@@ -964,7 +966,7 @@ extern "C" msa_status msa_attn_tree(const msa_shape* shape, const void* q, const
   if (!a.err) return MSA_ERR_CUDA;
   TreeMaps maps;
   const int64_t krows = (int64_t)pages->num_pages * shape->Hkv * pages->page_size;
-  if (!make_bf16_map(&maps.q, q, 1, (int64_t)shape->B * shape->Hq * shape->n, shape->d_h, 16) ||
+  if (!make_bf16_map(&maps.q, q, 1, (int64_t)shape->B * shape->Hq * shape->n, shape->d_h, a.q_box) ||
       !make_bf16_map(&maps.k, pages->k, 1, krows, shape->d_h, pages->page_size) ||
       !make_bf16_map(&maps.v, pages->v, 1, krows, shape->d_h, pages->page_size))
     return MSA_ERR_CUDA;
