@@ -15,17 +15,17 @@
 // all of them, rows that do not exist costing nothing but idle lanes.
 //
 // Split.  The tiles of 128 keys of all (request, KV head, 256-row block) items
-// form one line, cut into equal parts, one per CTA and SM: no CTA has more
-// than one tile above another's, whatever the lengths.  An item that lies in
-// one part is finished there; of one that is cut, each part leaves its
+// form one line, cut into equal parts, one per softmax group (below): no group
+// has more than one tile above another's, whatever the lengths.  An item that
+// lies in one part is finished there; of one that is cut, each part leaves its
 // unnormalised sum, maximum and row sum in the workspace, and a second kernel
 // (launched early, waiting for the first) joins them in key order, so results
 // do not depend on timing.
 //
-// A CTA (12 warps):
+// A CTA (12 warps, one CTA per SM):
 //   warp 10    loader: walks the parts' segments, publishes their descriptors,
 //              loads Q rows and the K and V pages of every tile by TMA into a
-//              ring (K and V tiles alternate);
+//              ring (K and V tiles alternate; two parts' tiles take turns);
 //   warp 8     waits for the ring's tiles one after another and declares each
 //              ready; in a request's last V tile it first zeroes the rows past
 //              the end: pages may hold anything there, and a weight of zero
@@ -34,14 +34,22 @@
 //              not take the phase of a slot's earlier use for the one it waits
 //              for.  With declarations in order, the tile it saw last proves
 //              every earlier use of the slot over);
-//   warps 9/11 MMA issuers of the two softmax groups;
+//   warps 9/11 MMA issuers;
 //   warps 0-7  softmax groups X = 0, 1 (4 warps each, thread = row = TMEM lane).
-// Up to 128 rows (kTwo false): the groups take turns on the key tiles, each
-// with its own running maximum, sum and O, joined at the segment's end.  Above (kTwo):
-// group X owns rows 128 X .. of the 256-row block, and both see every tile.
+// Three row layouts (Rows):
+//   kFew   up to 64 rows: the groups work on parts of their own; group 1 has its
+//          rows in TMEM lanes 64 .., so that the groups' warps sit on different
+//          schedulers, and Q is double-buffered.  A group's chain (scores,
+//          softmax, values) takes longer than a tile takes out of HBM; two
+//          chains side by side do not;
+//   kMany  up to 128 rows: the same with all lanes and one Q buffer a group;
+//   kTwo   above: one part per CTA, group X owns rows 128 X .. of the 256-row
+//          block, and both use every tile.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <string.h>
+
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -54,14 +62,14 @@ float effective_scale(const msa_shape& s);
 
 namespace {
 
-constexpr int kCtas = 152;  // parts of the line of tiles, if it has as many tiles
+constexpr int kCtas = 152;
 constexpr int kThreads = 384;
 constexpr int kCleanWarp = 8, kMmaWarp0 = 9, kLoaderWarp = 10;  // 11: the other issuer
-constexpr int kSegSlots = 4;
-constexpr int kSegReaders = 11;  // 8 softmax warps, 2 issuers, the cleaner
+constexpr int kSegSlots = 3;
+enum Rows { kFew = 0, kMany = 1, kTwo = 2 };
 constexpr uint32_t kTmemCols = 512;
-// TMEM columns.  Up to 128 rows: S of group X at 128 X, P over its first 64.
-// Above: one S that the groups use in turn, P of group X at 128 + 64 X.  O of
+// TMEM columns.  kFew, kMany: S of group X at 128 X, P over its first 64.
+// kTwo: one S that the groups use in turn, P of group X at 128 + 64 X.  O of
 // group X at 256 + 128 X.
 constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
@@ -70,15 +78,15 @@ constexpr uint32_t kIdleNs = 64;
 constexpr int kMaxDrafts = 1024;
 
 struct TreeArgs {
-  int32_t B, Hq, Hkv, n, R, RB, page_shift, max_pages, num_pages, words, q_box;
+  int32_t B, Hq, Hkv, n, R, RB, page_shift, max_pages, num_pages, words, q_box, max_parts;
   const int32_t *table, *seq_len, *tree_len;
   const uint32_t* mask;
   int64_t mask_stride;  // words between the masks of two requests (0: one mask for all)
   __nv_bfloat16* o;
   float* lse;
   int64_t* prefix;  // [B + 1] tiles of the requests before
-  float4* part;     // [2 kCtas][d/4][rows] unnormalised O of the cut items
-  float2* part_ml;  // [2 kCtas][rows] their maximum (log2) and row sum
+  float4* part;     // [2 max_parts][d/4][rows] unnormalised O of the cut items
+  float2* part_ml;  // [2 max_parts][rows] their maximum (log2) and row sum
   float scale_log2;
   int* err;
 };
@@ -87,36 +95,35 @@ struct TreeMaps {
   CUtensorMap q, k, v;  // [rows, d] views, boxes of 64 columns x q_box rows (q), x page_size rows (k, v)
 };
 
-// The part of one item that a CTA processes: tiles t0 .. t1 of its `tiles`.
+// The piece of one item that lies in a part: tiles t0 .. t1 of its `tiles`.
 struct Seg {
   int32_t b, kvh, rb, t0, t1, tiles;  // b < 0: no more
   int32_t L, T;
 };
 
+// Barriers; [X]: per group (kTwo: segments and Q once, at X = 0)
 enum {
-  kBarQFull = 0,                    // [2]
-  kBarQEmpty = 2,                   // [2]
-  kBarSFull = 4,                    // [2]
-  kBarPFull = 6,                    // [2]
-  kBarODone = 8,                    // [2] every product of the group's segment is done (kTwo: of a group without rows)
-  kBarOFree = 10,                   // [2] O of the segment has been read
-  kBarML = 12,                      // maxima and sums of both groups are written
-  kBarSFree = 13,                   // kTwo: the scores are in registers
-  kBarPV = 14,                      // [2] kTwo: the group's last P has been used
-  kBarSegFull = 16,                 // [kSegSlots]
-  kBarSegEmpty = kBarSegFull + kSegSlots,
-  kBarRing = kBarSegEmpty + kSegSlots  // full[kSlots], empty[kSlots], ready[kSlots]
+  kBarQFull = 0,                         // [X][2 buffers]
+  kBarQEmpty = 4,                        // [X][2]
+  kBarSFull = 8,                         // [X] scores are in TMEM
+  kBarPFull = 10,                        // [X] weights are in TMEM
+  kBarODone = 12,                        // [X] every product of the segment is done (kTwo: of a group without rows)
+  kBarOFree = 14,                        // [X] O of the segment has been read
+  kBarPV = 16,                           // [X] kTwo: the group's last P has been used
+  kBarSFree = 18,                        // kTwo: the scores are in registers
+  kBarSegFull = 19,                      // [X][kSegSlots]
+  kBarSegEmpty = kBarSegFull + 2 * kSegSlots,
+  kBarRing = kBarSegEmpty + 2 * kSegSlots  // full[kSlots], empty[kSlots], ready[kSlots]
 };
 
 template <int D>
 struct Lay {
   static constexpr int kTile = 128 * D * 2;
   static constexpr int kSlots = 5 * (128 / D);
-  static constexpr int kQ = 0;  // two Q tiles: two segments' (one row tile each) or one segment's two
+  static constexpr int kQ = 0;  // two Q tiles, one per group (kFew: of two 64-row buffers)
   static constexpr int kRing = 2 * kTile;
   static constexpr int kSeg = kRing + kSlots * kTile;
-  static constexpr int kML = kSeg + kSegSlots * (int)sizeof(Seg);
-  static constexpr int kBars = kML + 2 * 128 * 8;
+  static constexpr int kBars = kSeg + 2 * kSegSlots * (int)sizeof(Seg);
   static constexpr int kNumBars = kBarRing + 3 * kSlots;
   static constexpr int kMisc = kBars + kNumBars * 8;  // [0] TMEM base, [2] abort
   static constexpr int kAlloc = kMisc + 16;
@@ -165,14 +172,20 @@ __device__ __forceinline__ bool request(const TreeArgs& A, int b, int& L, int& T
   return !bad && T > 0;
 }
 __device__ __forceinline__ int key_tiles(int L) { return (L + 127) >> 7; }
-__device__ __forceinline__ int parts(int64_t W) { return W < kCtas ? (int)W : kCtas; }
-__device__ __forceinline__ int64_t part_begin(int64_t W, int c) { return W < kCtas ? c : W * c / kCtas; }
+// The line of W tiles in G = min(W, max_parts) parts; CTA c's groups take parts c and kCtas + c.
+__device__ __forceinline__ int parts(int64_t W, int most) { return W < most ? (int)W : most; }
+__device__ __forceinline__ int64_t part_begin(int64_t W, int most, int p) { return W < most ? p : W * p / most; }
 
-template <int D, bool kTwo>
+template <int D, Rows kRows>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_attn_kernel(const __grid_constant__ TreeMaps M, const TreeArgs A) {
   using Ly = Lay<D>;
+  constexpr bool kPair = kRows == kTwo;
   constexpr int kSlots = Ly::kSlots;
+  constexpr int kMost = kPair ? kCtas : 2 * kCtas;  // parts (A.max_parts)
+  constexpr int kGroupWarps = kRows == kFew ? 2 : 4;
+  constexpr int kSegReaders = kPair ? 11 : kGroupWarps + 2;  // softmax warps, issuer(s), the cleaner
+  constexpr int kQBufs = kRows == kFew ? 2 : 1;
   extern __shared__ __align__(1024) uint8_t sm[];  // swizzled tiles start on 1 KB
   if (smem_u32(sm) & 1023) {
     if (threadIdx.x == 0) atomicCAS(A.err, 0, (int)kErrTimeout);
@@ -182,8 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bFull = bars + kBarRing;
   uint64_t* bEmpty = bFull + kSlots;
   uint64_t* bReady = bEmpty + kSlots;
-  Seg* segs = reinterpret_cast<Seg*>(sm + Ly::kSeg);
-  float2* ml = reinterpret_cast<float2*>(sm + Ly::kML);
+  Seg* segs = reinterpret_cast<Seg*>(sm + Ly::kSeg);  // [2][kSegSlots]
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(sm + Ly::kMisc);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -199,18 +211,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&M.v);
   }
   if (threadIdx.x == 32 * kMmaWarp0) {
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < 4; ++x) {
       mbar_init(&bars[kBarQFull + x], 1);
-      mbar_init(&bars[kBarQEmpty + x], kTwo ? 1 : 2);
+      mbar_init(&bars[kBarQEmpty + x], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
       mbar_init(&bars[kBarSFull + x], 1);
-      mbar_init(&bars[kBarPFull + x], 4);
+      mbar_init(&bars[kBarPFull + x], kGroupWarps);
       mbar_init(&bars[kBarODone + x], 1);
-      mbar_init(&bars[kBarOFree + x], kTwo ? 4 : 8);
+      mbar_init(&bars[kBarOFree + x], kGroupWarps);
       mbar_init(&bars[kBarPV + x], 1);
     }
-    mbar_init(&bars[kBarML], 8);
     mbar_init(&bars[kBarSFree], 4);
-    for (int s = 0; s < kSegSlots; ++s) {
+    for (int s = 0; s < 2 * kSegSlots; ++s) {
       mbar_init(&bars[kBarSegFull + s], 1);
       mbar_init(&bars[kBarSegEmpty + s], kSegReaders);
     }
@@ -222,10 +235,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     misc[2] = 0;
     fence_mbar_init();
   }
-  // ---- this CTA's part [lo, hi) of the line of tiles, and the request it starts in
+  // ---- this CTA's parts of the line of tiles, and the requests they start in
   const int items = A.Hkv * A.RB;  // items of a request
   int64_t* wsum = reinterpret_cast<int64_t*>(sm + Ly::kRing);  // scratch until the pipeline starts
-  int64_t* start = wsum + 16;                                  // [0] request, [1] its first tile
+  int64_t* start = wsum + 16;                                  // [X][2]: request, its first tile
   int64_t W = 0;                                               // all tiles
   {
     const int per = (A.B + kThreads - 1) / kThreads;
@@ -253,43 +266,64 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (w < warp) base += wsum[w];
       W += wsum[w];
     }
-    const int64_t lo = part_begin(W, blockIdx.x);  // at or above W in a CTA without a part
     int64_t at = base + inc - mine;
     for (int b = b0; b < b1; ++b) {
       const int64_t t = per == 1 ? own : tiles(b);
-      if (at <= lo && lo < at + t) { start[0] = b; start[1] = at; }
+#pragma unroll
+      for (int X = 0; X < (kPair ? 1 : 2); ++X) {
+        const int64_t lo = part_begin(W, kMost, blockIdx.x + kCtas * X);  // at or above W: no part
+        if (at <= lo && lo < at + t) { start[2 * X] = b; start[2 * X + 1] = at; }
+      }
       if (blockIdx.x == 0) A.prefix[b] = at;
       at += t;
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) A.prefix[A.B] = W;
   }
-  const int64_t lo = part_begin(W, blockIdx.x), hi = part_begin(W, blockIdx.x + 1);
+  const int G = parts(W, kMost);
+  // tiles of this CTA's parts; tile k of group X is tile turn(X, k) of the ring (the parts' tiles take turns)
+  int64_t begin[2] = {0, 0};
+  int cnt[2] = {0, 0};
+#pragma unroll
+  for (int X = 0; X < (kPair ? 1 : 2); ++X) {
+    const int p = blockIdx.x + kCtas * X;
+    if (p < G) {
+      begin[X] = part_begin(W, kMost, p);
+      cnt[X] = (int)(part_begin(W, kMost, p + 1) - begin[X]);
+    }
+  }
+  const int both = min(cnt[0], cnt[1]);
+  auto turn = [&](int X, int k) { return kPair ? k : k < both ? 2 * k + X : both + k; };
+  auto owner = [&](int j) { return kPair ? 0 : j < 2 * both ? j & 1 : cnt[0] > cnt[1] ? 0 : 1; };
   fence_proxy_async_smem();  // the scratch above lies in the ring that TMA fills
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if ((int)blockIdx.x >= parts(W)) {  // no part
+  if ((int)blockIdx.x >= G) {  // no part
     if (warp == 0) tmem_dealloc(misc[0], kTmemCols);
     return;
   }
-  const int first_b = (int)start[0];
-  const int64_t first_tile = start[1];
   const uint32_t tmem = misc[0];
 
-  // Segment s of this CTA as the readers see it; false: no more, or gave up.
+  // Segment s of group X's part as its readers see it; false: no more, or gave up.
   bool ok = true;
-  auto next_seg = [&](int s, Seg& g) -> bool {
-    if (misc[2] || !mbar_wait(&bars[kBarSegFull + s % kSegSlots], (s / kSegSlots) & 1)) { ok = false; return false; }
-    g = segs[s % kSegSlots];
+  auto next_seg = [&](int X, int s, Seg& g) -> bool {
+    const int slot = (kPair ? 0 : X * kSegSlots) + s % kSegSlots;
+    if (misc[2] || !mbar_wait(&bars[kBarSegFull + slot], (s / kSegSlots) & 1)) { ok = false; return false; }
+    g = segs[slot];
     __syncwarp();
-    if (lane == 0) mbar_arrive(&bars[kBarSegEmpty + s % kSegSlots]);
+    if (lane == 0) mbar_arrive(&bars[kBarSegEmpty + slot]);
     return g.b >= 0;
   };
   auto ready = [&](int idx) { return mbar_wait(&bReady[idx % kSlots], (idx / kSlots) & 1); };
+  // Q of group X, buffer buf.  The MMA reads 128 rows from 64 X above it in kFew (group 1's rows come to lanes 64 ..);
+  // rows that are not the group's hold anything and only reach their own lanes.
+  auto q_at = [&](int X, int buf) { return Ly::kQ + X * Ly::kTile + buf * 8192; };
   constexpr uint32_t id_qk = idesc_bf16_f32(128, 128, false, false);
   constexpr uint32_t id_pv = idesc_bf16_f32(128, D, false, true);
   constexpr uint64_t kTileDesc = Ly::kTile >> 4;
-  const uint64_t dq = sdesc_sw128(smem_u32(sm + Ly::kQ), 16, 1024);
+  auto q_desc = [&](int X, int buf) {
+    return sdesc_sw128(smem_u32(sm + q_at(X, buf)) - (kRows == kFew ? 8192u * X : 0u), 16, 1024);
+  };
   const uint64_t dk = sdesc_sw128(smem_u32(sm + Ly::kRing), 16, 1024);     // + slot * kTileDesc
   const uint64_t dv = sdesc_sw128(smem_u32(sm + Ly::kRing), 16384, 1024);
   auto issue_qk = [&](uint32_t d, uint64_t q0, uint64_t k0) {  // S = Q K^T of one tile, by one thread
@@ -304,140 +338,177 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int kk = 0; kk < 8; ++kk)
       mma_bf16_ts(d, p + 8 * kk, v0 + (uint64_t)(kk * 128), id_pv, (!first || kk > 0) ? 1u : 0u);
   };
-  // rows of softmax group X in the 256-row block rb (one group's rows serve both groups unless kTwo)
-  auto group_rows = [&](int rb, int X) { return min(128, A.R - 256 * rb - (kTwo ? 128 * X : 0)); };
+  // rows of softmax group X in the 256-row block rb
+  auto group_rows = [&](int rb, int X) { return min(128, A.R - 256 * rb - (kPair ? 128 * X : 0)); };
 
   // the block starts with 3 x 128 threads x 168 registers; the softmax threads (a row's 128 scores each) take
-  // 208 and the others' 72: 2 x 208 + 72 <= 3 x 168
+  // 192 and the others' 120: 2 x 192 + 120 = 3 x 168
   if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-  if (warp == kLoaderWarp) {
-    // ------------------------------------------------------------ loader
-    const uint64_t policy = A.RB == 1 ? policy_evict_first() : policy_evict_last();
-    const int pshift = 7 - A.page_shift, pp = 1 << pshift;  // pages of a tile
-    const int P = 1 << A.page_shift;
-    int64_t at = first_tile;  // first tile of item 0 of request b
-    int64_t pos = lo;
-    int idx = 0, s = 0;  // ring index (2 per tile), segment
-    int b = first_b;
-    for (; ok; ++s) {
-      // ---- next segment
-      Seg g;
-      g.b = -1;
-      if (pos < hi) {
-        int L = 0, T = 0;
-        bool bad;
-        int64_t t = 0;
-        for (; b < A.B; ++b) {  // pos < hi <= W: a request holding it exists
-          t = request(A, b, L, T, bad) ? (int64_t)items * key_tiles(L) : 0;
-          if (pos < at + t) break;
-          at += t;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+    if (warp == kLoaderWarp) {
+      // ---------------------------------------------------------- loader
+      const uint64_t policy = A.RB == 1 ? policy_evict_first() : policy_evict_last();
+      const int pshift = 7 - A.page_shift, pp = 1 << pshift;  // pages of a tile
+      const int P = 1 << A.page_shift;
+      struct Stream {
+        int64_t at, pos, hi;  // first tile of request b, next segment's first tile, the part's end
+        int b, s, t;          // request, segments so far, next tile of the segment
+        Seg g;
+        int base, ids, ahead;  // lane x holds the page of entry base + x, and of base + 32 + x
+      };
+      auto publish = [&](int X, int s, const Seg& g) -> bool {
+        const int slot = X * kSegSlots + s % kSegSlots;
+        if (misc[2] || !mbar_wait_idle(&bars[kBarSegEmpty + slot], ((s / kSegSlots) & 1) ^ 1, kIdleNs)) return false;
+        if (lane == 0) {
+          segs[slot] = g;
+          mbar_arrive(&bars[kBarSegFull + slot]);
         }
-        if (b >= A.B) { ok = false; break; }
-        g.b = b;
-        g.L = L;
-        g.T = T;
-        g.tiles = key_tiles(L);
-        const int item = (int)((pos - at) / g.tiles);
-        g.kvh = item / A.RB;
-        g.rb = item - g.kvh * A.RB;
-        g.t0 = (int)(pos - at - (int64_t)item * g.tiles);
-        const int64_t left = hi - pos;
-        g.t1 = left < g.tiles - g.t0 ? g.t0 + (int)left : g.tiles;
-        pos += g.t1 - g.t0;
-      }
-      if (misc[2] || !mbar_wait_idle(&bars[kBarSegEmpty + s % kSegSlots], ((s / kSegSlots) & 1) ^ 1, kIdleNs)) {
-        ok = false;
-        break;
-      }
-      if (lane == 0) {
-        segs[s % kSegSlots] = g;
-        mbar_arrive(&bars[kBarSegFull + s % kSegSlots]);
-      }
-      if (g.b < 0) break;
-      // ---- Q rows (their load overlaps the page entries')
-      {
-        const int nq = kTwo ? 1 : 2, buf = s % nq;
-        if (!mbar_wait_idle(&bars[kBarQEmpty + buf], ((s / nq) & 1) ^ 1, kIdleNs)) { ok = false; break; }
-        const int rows = min(kTwo ? 256 : 128, A.R - 256 * g.rb), boxes = (rows + A.q_box - 1) / A.q_box;
-        uint64_t* full = &bars[kBarQFull + buf];
-        if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(boxes * A.q_box * D * 2));
-        __syncwarp();
-        const int qrow = (g.b * A.Hq + g.kvh * (A.Hq / A.Hkv)) * A.n + 256 * g.rb;
-        if (lane < boxes * (D / 64)) {  // at most 8
-          const int c = lane & (D / 64 - 1), r = lane / (D / 64) * A.q_box;
-          tma_load_3d(sm + Ly::kQ + (kTwo ? r >> 7 : buf) * Ly::kTile + c * 16384 + (r & 127) * 128, &M.q, full, 64 * c,
-                      qrow + r, 0);
-        }
-      }
-      // ---- pages of the first tiles: lane x holds entry base + x, and base + 32 + x ahead
-      const int32_t* row = A.table + (int64_t)g.b * A.max_pages;
-      const int np = (g.L + P - 1) >> A.page_shift;
-      auto entry = [&](int p) {
-        int page = p < np ? row[p] : 0;
+        return true;
+      };
+      auto entry = [&](const Seg& g, int p) {
+        const int np = (g.L + P - 1) >> A.page_shift;
+        int page = p < np ? A.table[(int64_t)g.b * A.max_pages + p] : 0;
         if ((unsigned)page >= (unsigned)A.num_pages) {  // skipped: an existing page stands in, the call has failed
           atomicCAS(A.err, 0, (int)kErrIndex);
           page = 0;
         }
         return page;
       };
-      int base = g.t0 << pshift;
-      int ids = entry(base + lane), ahead = entry(base + 32 + lane);
-      // ---- K and V tiles
-      for (int t = g.t0; t < g.t1 && ok; ++t) {
-        int off = (t << pshift) - base;
-        if (off >= 32) {
-          base += 32;
-          off -= 32;
-          ids = ahead;
-          ahead = entry(base + 32 + lane);
+      // The next segment of a stream: its descriptor, its Q rows, its first page entries.
+      auto open = [&](Stream& S, int X) -> bool {
+        Seg& g = S.g;
+        bool bad;
+        int64_t t = 0;
+        for (; S.b < A.B; ++S.b) {  // pos < hi <= W: a request holding it exists
+          t = request(A, S.b, g.L, g.T, bad) ? (int64_t)items * key_tiles(g.L) : 0;
+          if (S.pos < S.at + t) break;
+          S.at += t;
         }
-        const int have = min(pp, np - (t << pshift));  // pages of this tile that hold keys
+        if (S.b >= A.B) return false;
+        g.b = S.b;
+        g.tiles = key_tiles(g.L);
+        const int item = (int)((S.pos - S.at) / g.tiles);
+        g.kvh = item / A.RB;
+        g.rb = item - g.kvh * A.RB;
+        g.t0 = (int)(S.pos - S.at - (int64_t)item * g.tiles);
+        const int64_t left = S.hi - S.pos;
+        g.t1 = left < g.tiles - g.t0 ? g.t0 + (int)left : g.tiles;
+        S.pos += g.t1 - g.t0;
+        S.t = g.t0;
+        if (!publish(X, S.s, g)) return false;
+        const int buf = S.s % kQBufs;
+        if (!mbar_wait_idle(&bars[kBarQEmpty + 2 * X + buf], ((S.s / kQBufs) & 1) ^ 1, kIdleNs)) return false;
+        ++S.s;
+        const int rows = min(kPair ? 256 : 128, A.R - 256 * g.rb), boxes = (rows + A.q_box - 1) / A.q_box;
+        uint64_t* full = &bars[kBarQFull + 2 * X + buf];
+        if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(boxes * A.q_box * D * 2));
+        __syncwarp();
+        const int qrow = (g.b * A.Hq + g.kvh * (A.Hq / A.Hkv)) * A.n + 256 * g.rb;
+        if (lane < boxes * (D / 64)) {  // at most 8
+          const int c = lane & (D / 64 - 1), r = lane / (D / 64) * A.q_box;
+          tma_load_3d(sm + q_at(kPair ? r >> 7 : X, buf) + c * 16384 + (r & 127) * 128, &M.q, full, 64 * c, qrow + r, 0);
+        }
+        S.base = g.t0 << pshift;
+        S.ids = entry(g, S.base + lane);
+        S.ahead = entry(g, S.base + 32 + lane);
+        return true;
+      };
+      int issued = 0;  // loads into the ring so far
+      // Ring tile j: the next tile of a stream.
+      auto step = [&](Stream& S, int X, int j) -> bool {
+        if ((S.s == 0 || S.t == S.g.t1) && !open(S, X)) return false;
+        int off = (S.t << pshift) - S.base;
+        if (off >= 32) {
+          S.base += 32;
+          off -= 32;
+          S.ids = S.ahead;
+          S.ahead = entry(S.g, S.base + 32 + lane);
+        }
+        const int np = (S.g.L + P - 1) >> A.page_shift;
+        const int have = min(pp, np - (S.t << pshift));  // pages of this tile that hold keys
         const int c = lane >> 3, x = lane & 7;
-        const int page = __shfl_sync(0xFFFFFFFFu, ids, (off + x) & 31);
-        const int krow = (page * A.Hkv + g.kvh) << A.page_shift;
+        const int krow = (__shfl_sync(0xFFFFFFFFu, S.ids, (off + x) & 31) * A.Hkv + S.g.kvh) << A.page_shift;
 #pragma unroll
-        for (int is_v = 0; is_v < 2; ++is_v, ++idx) {
-          const int st = idx % kSlots;
-          if (misc[2] || !mbar_wait_idle(&bEmpty[st], ((idx / kSlots) & 1) ^ 1, kIdleNs)) {
-            ok = false;
-            break;  // before ++idx: nothing was loaded into this slot
-          }
+        for (int is_v = 0; is_v < 2; ++is_v) {
+          const int idx = 2 * j + is_v, st = idx % kSlots;
+          if (misc[2] || !mbar_wait_idle(&bEmpty[st], ((idx / kSlots) & 1) ^ 1, kIdleNs)) return false;
           if (lane == 0) mbar_arrive_expect_tx(&bFull[st], (uint32_t)(have * P * D * 2));
           __syncwarp();
+          issued = idx + 1;
           if (c < D / 64 && x < have)
-            tma_load_3d_hint(sm + Ly::kRing + st * Ly::kTile + c * 16384 + x * P * 128, is_v ? &M.v : &M.k,
-                             &bFull[st], 64 * c, krow, 0, policy);
+            tma_load_3d_hint(sm + Ly::kRing + st * Ly::kTile + c * 16384 + x * P * 128, is_v ? &M.v : &M.k, &bFull[st],
+                             64 * c, krow, 0, policy);
         }
+        ++S.t;
+        return true;
+      };
+      // the two streams change places in registers, so that the code above exists once
+      Stream S, other;
+      S.at = start[1], S.pos = begin[0], S.hi = begin[0] + cnt[0], S.b = (int)start[0], S.s = S.t = 0;
+      other.at = start[3], other.pos = begin[1], other.hi = begin[1] + cnt[1], other.b = (int)start[2];
+      other.s = other.t = 0;
+      __syncwarp();  // every lane has read the scratch that the first load overwrites
+      Seg end;
+      end.b = -1;
+      int X = 0;
+      if (!kPair && cnt[1] == 0) ok = publish(1, 0, end);  // an idle group leaves at once
+      for (int j = 0; j < cnt[0] + cnt[1] && ok; ++j) {
+        if (owner(j) != X) {
+          const Stream t = S;
+          S = other;
+          other = t;
+          X ^= 1;
+        }
+        ok = step(S, X, j);
       }
-    }
-    if (!ok)  // gave up: the copies in flight land before the shared memory goes
-      for (int x = max(0, idx - kSlots); x < idx; ++x) mbar_wait(&bFull[x % kSlots], (x / kSlots) & 1);
-  } else if (warp == kCleanWarp) {
-    // ------------------------------------------------------------ tiles in order, rows past a request's end
-    int idx = 0;
-    Seg g;
-    for (int s = 0; next_seg(s, g); ++s)
-      for (int t = 2 * g.t0; t < 2 * g.t1; ++t, ++idx) {  // K and V of every tile
-        const int st = idx % kSlots;
-        if (misc[2] || !mbar_wait(&bFull[st], (idx / kSlots) & 1)) { ok = false; break; }
-        const int keys = g.L - 64 * (t & ~1);
-        if ((t & 1) && keys < 128) {
-          uint8_t* v = sm + Ly::kRing + st * Ly::kTile;
-          for (int x = keys * 8 + lane; x < 1024; x += 32)
+      if (ok) ok = publish(X, S.s, end);
+      if (!kPair && ok && cnt[1] > 0) ok = publish(X ^ 1, other.s, end);
+      if (!ok)  // gave up: the copies in flight land before the shared memory goes
+        for (int x = max(0, issued - kSlots); x < issued; ++x) mbar_wait(&bFull[x % kSlots], (x / kSlots) & 1);
+    } else if (warp == kCleanWarp) {
+      // ---------------------------------------------------------- tiles in order, rows past a request's end
+      struct Walk {
+        int b_end, L, t, s;  // end of the segment, keys of its request, next tile, segments so far
+      };
+      Walk w = {0, 0, 0, 0}, other = {0, 0, 0, 0};
+      int X = 0;
+      for (int j = 0; j < cnt[0] + cnt[1] && ok; ++j) {
+        if (owner(j) != X) {
+          const Walk t = w;
+          w = other;
+          other = t;
+          X ^= 1;
+        }
+        if (w.t == w.b_end) {
+          Seg g;
+          if (!next_seg(X, w.s++, g)) { ok = false; break; }
+          w.t = g.t0;
+          w.b_end = g.t1;
+          w.L = g.L;
+        }
+        const int keys = w.L - 128 * w.t++;
+#pragma unroll 1
+        for (int idx = 2 * j; idx < 2 * j + 2; ++idx) {
+          const int st = idx % kSlots;
+          if (misc[2] || !mbar_wait(&bFull[st], (idx / kSlots) & 1)) { ok = false; break; }
+          if ((idx & 1) && keys < 128) {
+            uint8_t* v = sm + Ly::kRing + st * Ly::kTile;
+#pragma unroll 1
+            for (int x = keys * 8 + lane; x < 1024; x += 32)
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-              *reinterpret_cast<uint4*>(v + c * 16384 + x * 16) = make_uint4(0u, 0u, 0u, 0u);
-          fence_proxy_async_smem();
-          __syncwarp();
+              for (int c = 0; c < D / 64; ++c)
+                *reinterpret_cast<uint4*>(v + c * 16384 + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive(&bReady[st]);
         }
-        if (lane == 0) mbar_arrive(&bReady[st]);
       }
-  } else if (kTwo && warp == kMmaWarp0) {
+    } else if (kPair && warp == kMmaWarp0) {
     // ------------------------------------------------------------ scores of both groups
     int tile = 0, use = 0;  // tiles so far, uses of S so far
     Seg g;
-    for (int s = 0; next_seg(s, g); ++s) {
+    for (int s = 0; next_seg(0, s, g); ++s) {
       if (!mbar_wait(&bars[kBarQFull], s & 1)) { ok = false; break; }
       for (int t = g.t0; t < g.t1 && ok; ++t, ++tile) {
         const int kst = 2 * tile % kSlots;
@@ -449,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++use;
           tc_fence_after();
           if (lane == 0) {
-            issue_qk(tmem + kColS, dq + (uint64_t)X * kTileDesc, dk + (uint64_t)kst * kTileDesc);
+            issue_qk(tmem + kColS, q_desc(X, 0), dk + (uint64_t)kst * kTileDesc);
             mma_commit(&bars[kBarSFull + X]);
           }
           __syncwarp();
@@ -461,11 +532,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mma_commit(&bars[kBarQEmpty]);
       __syncwarp();
     }
-  } else if (kTwo) {
+    } else if (kPair) {
     // ------------------------------------------------------------ O += P V of both groups
     int tile = 0, seen[2] = {0, 0};  // tiles so far, P's of each group
     Seg g;
-    for (int s = 0; next_seg(s, g); ++s) {
+    for (int s = 0; next_seg(0, s, g); ++s) {
       // O_X of the segment before has been read: its first PV here, or (no rows) its end, waits for that
       auto o_free = [&](int X) { return s == 0 || mbar_wait(&bars[kBarOFree + X], (s - 1) & 1); };
       for (int t = g.t0; t < g.t1 && ok; ++t, ++tile) {
@@ -495,198 +566,236 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       if (!ok) break;
     }
-  } else if (!kTwo) {
-    // ------------------------------------------------------------ MMA issuer of group X
-    const int X = warp == kMmaWarp0 ? 0 : 1;
-    const uint32_t tS = tmem + kColS + 128 * X, tO = tmem + kColO + 128 * X;
-    int tile0 = 0;   // CTA tile index of the segment's first tile
-    int pphase = 0;  // tiles whose P this issuer has waited for
-    Seg g;
-    for (int s = 0; next_seg(s, g); ++s) {
-      const int buf = s & 1, nt = g.t1 - g.t0;
-      const uint64_t q0 = dq + (uint64_t)buf * kTileDesc;
-      if (!mbar_wait(&bars[kBarQFull + buf], (s >> 1) & 1)) { ok = false; break; }
-      int pending = -1;
-      bool first = true;
-      // O_X of the segment before has been read: its first PV here, or its end, waits for that
-      auto o_free = [&]() -> bool { return s == 0 || mbar_wait(&bars[kBarOFree + X], (s - 1) & 1); };
-      auto issue_pv = [&]() -> bool {
-        if (first && !o_free()) return false;
-        const int vidx = 2 * pending + 1, vst = vidx % kSlots;
-        if (!mbar_wait(&bars[kBarPFull + X], pphase & 1)) return false;
-        ++pphase;
-        if (!ready(vidx)) return false;
-        tc_fence_after();
-        if (lane == 0) {
-          issue_pv_mma(tO, tS, dv + (uint64_t)vst * kTileDesc, first);
-          mma_commit(&bEmpty[vst]);
+    } else {
+      // ---------------------------------------------------------- MMA issuer of group X
+      const int X = warp == kMmaWarp0 ? 0 : 1;
+      const uint32_t tS = tmem + kColS + 128 * X, tO = tmem + kColO + 128 * X;
+      int k = 0;  // tiles of this group so far
+      Seg g;
+      for (int s = 0; next_seg(X, s, g); ++s) {
+        const int buf = s % kQBufs;
+        const uint64_t q0 = q_desc(X, buf);
+        if (!mbar_wait(&bars[kBarQFull + 2 * X + buf], (s / kQBufs) & 1)) { ok = false; break; }
+        // O += P V of the group's tile k - 1 (the segment's first product waits until O of the one before is read)
+        auto issue_pv = [&](bool first) -> bool {
+          if (first && s > 0 && !mbar_wait(&bars[kBarOFree + X], (s - 1) & 1)) return false;
+          if (!mbar_wait(&bars[kBarPFull + X], (k - 1) & 1)) return false;
+          const int vidx = 2 * turn(X, k - 1) + 1, vst = vidx % kSlots;
+          if (!ready(vidx)) return false;
+          tc_fence_after();
+          if (lane == 0) {
+            issue_pv_mma(tO, tS, dv + (uint64_t)vst * kTileDesc, first);
+            mma_commit(&bEmpty[vst]);
+          }
+          __syncwarp();
+          return true;
+        };
+        for (int t = g.t0; t < g.t1; ++t, ++k) {
+          if (misc[2] || (t > g.t0 && !issue_pv(t == g.t0 + 1))) { ok = false; break; }
+          const int kidx = 2 * turn(X, k), kst = kidx % kSlots;
+          if (!ready(kidx)) { ok = false; break; }
+          tc_fence_after();
+          if (lane == 0) {
+            issue_qk(tS, q0, dk + (uint64_t)kst * kTileDesc);
+            mma_commit(&bars[kBarSFull + X]);
+            mma_commit(&bEmpty[kst]);
+            if (t + 1 == g.t1) mma_commit(&bars[kBarQEmpty + 2 * X + buf]);
+          }
+          __syncwarp();
         }
+        if (!ok || !issue_pv(g.t1 == g.t0 + 1)) { ok = false; break; }
+        if (lane == 0) mma_commit(&bars[kBarODone + X]);
         __syncwarp();
-        first = false;
-        pending = -1;
-        return true;
-      };
-      for (int t = X; t < nt; t += 2) {
-        if (misc[2]) { ok = false; break; }
-        const int kidx = 2 * (tile0 + t), kst = kidx % kSlots;
-        if (pending >= 0 && !issue_pv()) { ok = false; break; }
-        if (!ready(kidx)) { ok = false; break; }
-        tc_fence_after();
-        if (lane == 0) {
-          issue_qk(tS, q0, dk + (uint64_t)kst * kTileDesc);
-          mma_commit(&bars[kBarSFull + X]);
-          mma_commit(&bEmpty[kst]);
-        }
-        __syncwarp();
-        pending = tile0 + t;
       }
-      if (!ok) break;
-      if (lane == 0) mma_commit(&bars[kBarQEmpty + buf]);  // every S of this segment
-      __syncwarp();
-      if (pending >= 0 ? !issue_pv() : first && !o_free()) { ok = false; break; }
-      if (lane == 0) mma_commit(&bars[kBarODone + X]);
-      __syncwarp();
-      tile0 += nt;
     }
-  }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     // ------------------------------------------------------------ softmax group X
-    const int X = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const int X = warp >> 2, quarter = warp & 3;
+    const bool used = kRows != kFew || X == quarter >> 1;  // kFew: warps 0, 1 and 6, 7
+    const int lane0 = 32 * quarter - (kRows == kFew ? 64 * X : 0), r = lane0 + lane;  // row of lane 0, of this thread
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    const uint32_t tS = tmem + lane_base + kColS + (kTwo ? 0 : 128 * X), tO = tmem + lane_base + kColO + 128 * X;
-    const uint32_t tP = kTwo ? tmem + lane_base + kColP + 64 * X : tS;
-    const float c2 = A.scale_log2;
+    const uint32_t tS = tmem + lane_base + kColS + (kPair ? 0 : 128 * X), tO = tmem + lane_base + kColO + 128 * X;
+    const uint32_t tP = kPair ? tmem + lane_base + kColP + 64 * X : tS;
     int seen = 0;  // tiles of this group so far (phase of S)
     int idle = 0;  // segments without rows for this group
     // kTwo: P and O of this group are its own once the product with its last P is done
     auto pv_done = [&]() -> bool {
-      if (!kTwo || seen == 0) return true;
+      if (!kPair || seen == 0) return true;
       if (!mbar_wait(&bars[kBarPV + X], (seen - 1) & 1)) return false;
       tc_fence_after();
       return true;
     };
     Seg g;
-    for (int s = 0; next_seg(s, g); ++s) {
+    for (int s = 0; used && next_seg(X, s, g); ++s) {
       const int rows = group_rows(g.rb, X);
-      const int rr = 256 * g.rb + (kTwo ? 128 * X : 0) + r;  // row within the KV group
+      const int rr = 256 * g.rb + (kPair ? 128 * X : 0) + r;  // row within the KV group
       const bool row_in = r < rows;
-      const bool warp_in = 32 * quarter < rows;
+      const bool warp_in = lane0 < rows;
       const int i = rr % A.n;  // drafted token of this row
       const bool row_ok = row_in && i < g.T;
       const int C = g.L - g.T;
       const uint32_t* mrow = A.mask ? A.mask + g.b * A.mask_stride + (int64_t)i * A.words : nullptr;
-      const int nt = g.t1 - g.t0;
+      // bit k: this row attends key key0 + k (keys from the end of the context on; lanes without a row see all)
+      auto mask32 = [&](int key0) -> uint32_t {
+        const int rel = key0 - C;  // drafted index of bit 0 (negative: context)
+        if (rel <= -32 || !row_ok) return ~0u;
+        if (!mrow) return low_mask32(min(i + 1, g.T) - rel);
+        const int w0 = rel >> 5, sh = rel & 31;  // floor for negative rel
+        const uint32_t a = (w0 >= 0 && w0 < A.words) ? __ldg(mrow + w0) : 0u;
+        const uint32_t c = (w0 + 1 < A.words) ? __ldg(mrow + w0 + 1) : 0u;
+        const uint32_t bits = __funnelshift_r(a, c, sh) & low_mask32(g.T - rel);
+        return rel < 0 ? bits | low_mask32(-rel) : bits;
+      };
       float m_used = -INFINITY, l = 0.f;
-      bool first = true;
-      if (rows > 0)
-        for (int t = kTwo ? 0 : X; t < nt; t += kTwo ? 1 : 2) {
-          if (misc[2]) { ok = false; break; }
-          const int key0 = 128 * (g.t0 + t);
-          const bool masked = key0 + 128 > C;
-          uint32_t vw[4] = {~0u, ~0u, ~0u, ~0u};
-          if (masked && row_ok) {
+      bool first = true;      // no product into O yet
+      bool alpha_any = false;  // a row of the warp raises its reference
+      const float c2 = A.scale_log2;
+      auto load64 = [&](uint32_t t, float* sv) {
+        uint32_t* u = reinterpret_cast<uint32_t*>(sv);
+        tmem_ld32(t, *reinterpret_cast<uint32_t(*)[32]>(u));
+        tmem_ld32(t + 32, *reinterpret_cast<uint32_t(*)[32]>(u + 32));
+        tmem_ld_wait();
+      };
+      auto max64 = [&](const float* sv, float m) -> float {
+        float mx[8];
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const int rel = key0 + 32 * w - C;  // drafted index of bit 0 (negative: context)
-              if (rel <= -32) continue;
-              uint32_t bits;
-              if (!mrow) {
-                bits = low_mask32(min(i + 1, g.T) - rel);
-              } else {
-                const int w0 = rel >> 5, sh = rel & 31;  // floor for negative rel
-                const uint32_t a = (w0 >= 0 && w0 < A.words) ? __ldg(mrow + w0) : 0u;
-                const uint32_t c = (w0 + 1 < A.words) ? __ldg(mrow + w0 + 1) : 0u;
-                bits = __funnelshift_r(a, c, sh) & low_mask32(g.T - rel);
-                if (rel < 0) bits |= low_mask32(-rel);
-              }
-              vw[w] = bits;
-            }
+        for (int x = 0; x < 8; ++x) mx[x] = max3f(sv[x], sv[8 + x], sv[16 + x]);
+#pragma unroll
+        for (int k = 24; k < 56; k += 16)
+#pragma unroll
+          for (int x = 0; x < 8; ++x) mx[x] = max3f(mx[x], sv[k + x], sv[k + 8 + x]);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) mx[x] = fmaxf(mx[x], sv[56 + x]);
+        return fmaxf(max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])), m);
+      };
+      // A tile's maximum: the reference rises when it has to by more than 2^8; returns the factor for what was summed.
+      auto raise = [&](float mt) -> float {
+        const float m_new = fmaxf(m_used, mt * c2);
+        // lanes without a row hold whatever shared memory held: they have no vote, or runs would differ
+        alpha_any = __any_sync(0xFFFFFFFFu, row_ok && m_new > m_used + kRescaleThreshold);
+        if (!alpha_any || m_new == -INFINITY) return 1.f;
+        const float alpha = (m_used == -INFINITY) ? 0.f : ex2(m_used - m_new);
+        m_used = m_new;
+        return alpha;
+      };
+      // 64 weights e^{s - reference}: bf16 for the second product (its operand type is V's), their sum in fp32
+      auto weights = [&](const float* sv, uint32_t t, uint64_t (&acc)[2]) {
+        const float mref = (m_used == -INFINITY) ? 0.f : m_used;
+        const uint64_t c2x2 = pk2(c2, c2), negm = pk2(-mref, -mref);
+#pragma unroll
+        for (int h = 0; h < 32 / kPChunk; ++h) {
+          uint32_t pk[kPChunk];
+#pragma unroll
+          for (int k = 0; k < kPChunk; ++k) {
+            const int e = 2 * kPChunk * h + 2 * k;
+            float x0, x1, p0, p1;
+            up2(fma2(pk2(sv[e], sv[e + 1]), c2x2, negm), x0, x1);
+            const uint64_t p = pk2(ex2(x0), ex2(x1));
+            acc[k & 1] = add2(acc[k & 1], p);
+            up2(p, p0, p1);
+            pk[k] = pack_bf16x2(p0, p1);
           }
+          tmem_st4(t + kPChunk * h, pk);
+        }
+      };
+      auto add_row = [&](const uint64_t (&acc)[2], float alpha) {
+        float a0, a1, a2, a3;
+        up2(acc[0], a0, a1);
+        up2(acc[1], a2, a3);
+        l = l * alpha + ((a0 + a1) + (a2 + a3));
+      };
+      auto rescale = [&](float alpha) {  // O: its previous product is done (before S was ready, or waited for)
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tO + 32 * c, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+          tmem_st32(tO + 32 * c, o);
+        }
+      };
+      if (rows > 0)
+        for (int t = g.t0; t < g.t1; ++t) {
+          if (misc[2]) { ok = false; break; }
+          const int key0 = 128 * t;
+          const bool masked = key0 + 128 > C;
           if (!mbar_wait(&bars[kBarSFull + X], seen & 1)) { ok = false; break; }
           tc_fence_after();
-          float sv[128];
-          if (warp_in) {
-            uint32_t* u = reinterpret_cast<uint32_t*>(sv);
+          if constexpr (kPair) {
+            float sv[128];
+            if (warp_in) {
+              uint32_t* u = reinterpret_cast<uint32_t*>(sv);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(u + 32 * c));
-            tmem_ld_wait();
-          } else {
+              for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(u + 32 * c));
+              tmem_ld_wait();
+            } else {
 #pragma unroll
-            for (int k = 0; k < 128; ++k) sv[k] = 0.f;
-          }
-          if (kTwo) {  // the scores are in registers: S is free for the other group's
-            tc_fence_before();
+              for (int k = 0; k < 128; ++k) sv[k] = 0.f;
+            }
+            tc_fence_before();  // the scores are in registers: S is free for the other group's
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[kBarSFree]);
-          }
-          if (warp_in) {
-            if (masked) {
+            if (warp_in) {
+              if (masked) {
 #pragma unroll
-              for (int k = 0; k < 128; ++k) sv[k] = ((vw[k >> 5] >> (k & 31)) & 1u) ? sv[k] : -INFINITY;
-            }
-            float mx[8];
+                for (int c = 0; c < 4; ++c) {
+                  const uint32_t vw = mask32(key0 + 32 * c);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) mx[x] = max3f(sv[x], sv[8 + x], sv[16 + x]);
-#pragma unroll
-            for (int k = 24; k < 120; k += 16)
-#pragma unroll
-              for (int x = 0; x < 8; ++x) mx[x] = max3f(mx[x], sv[k + x], sv[k + 8 + x]);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) mx[x] = fmaxf(mx[x], sv[120 + x]);
-            const float mt = max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
-            const float m_new = fmaxf(m_used, mt * c2);
-            // lanes without a row hold whatever shared memory held: they have no vote, or runs would differ
-            const bool need = row_ok && m_new > m_used + kRescaleThreshold;
-            const bool any = __any_sync(0xFFFFFFFFu, need);
-            float alpha = 1.f;
-            if (any && m_new != -INFINITY) {
-              alpha = (m_used == -INFINITY) ? 0.f : ex2(m_used - m_new);
-              m_used = m_new;
-            }
-            const float mref = (m_used == -INFINITY) ? 0.f : m_used;
-            const uint64_t c2x2 = pk2(c2, c2), negm = pk2(-mref, -mref);
-            uint64_t acc[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
-            if (!pv_done()) { ok = false; break; }
-            // P rounded to bf16 for the second MMA (its operand type is V's); the row sum keeps fp32
-#pragma unroll
-            for (int h = 0; h < 64 / kPChunk; ++h) {
-              uint32_t pk[kPChunk];
-#pragma unroll
-              for (int k = 0; k < kPChunk; ++k) {
-                const int e = 2 * kPChunk * h + 2 * k;
-                const uint64_t x = fma2(pk2(sv[e], sv[e + 1]), c2x2, negm);
-                float x0, x1;
-                up2(x, x0, x1);
-                const uint64_t p = pk2(ex2(x0), ex2(x1));
-                acc[k & 1] = add2(acc[k & 1], p);
-                float p0, p1;
-                up2(p, p0, p1);
-                pk[k] = pack_bf16x2(p0, p1);
+                  for (int k = 0; k < 32; ++k) sv[32 * c + k] = ((vw >> k) & 1u) ? sv[32 * c + k] : -INFINITY;
+                }
               }
-              tmem_st4(tP + kPChunk * h, pk);
+              const float alpha = raise(max64(sv, max64(sv + 64, -INFINITY)));
+              ok = pv_done();  // P and O may be written
+              uint64_t acc[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
+              weights(sv, tP, acc);
+              weights(sv + 64, tP + 32, acc);
+              add_row(acc, alpha);
+              if (alpha_any && !first) rescale(alpha);
+              tmem_st_wait();
+              first = false;
+            } else {
+              ok = pv_done();
             }
-            float a0, a1, a2, a3;
-            up2(acc[0], a0, a1);
-            up2(acc[1], a2, a3);
-            l = l * alpha + ((a0 + a1) + (a2 + a3));
-            if (any && !first) {  // O_X: its previous PV has completed (before S was ready, or waited for)
+          } else if (warp_in) {
+            // Two passes over the scores in TMEM, half a tile at a time: the rolled loops keep the code of all roles
+            // within the instruction cache, which 128 scores in registers at once do not (a third of the fetches
+            // missed, and one warp a scheduler has nothing to hide that with).
+            if (masked) {  // masked scores are put back as -inf
 #pragma unroll 1
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32(tO + 32 * c, o);
+              for (int c = 0; c < 4; ++c) {
+                uint32_t u[32];
+                const uint32_t vw = mask32(key0 + 32 * c);
+                tmem_ld32(tS + 32 * c, u);
                 tmem_ld_wait();
 #pragma unroll
-                for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
-                tmem_st32(tO + 32 * c, o);
+                for (int k = 0; k < 32; ++k) u[k] = ((vw >> k) & 1u) ? u[k] : 0xFF800000u;
+                tmem_st32(tS + 32 * c, u);
               }
+              tmem_st_wait();
             }
+            float mt = -INFINITY;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              float sv[64];
+              load64(tS + 64 * h, sv);
+              mt = max64(sv, mt);
+            }
+            const float alpha = raise(mt);
+            uint64_t acc[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {  // P of half 0 lies over its scores, that of half 1 as well
+              float sv[64];
+              load64(tS + 64 * h, sv);
+              weights(sv, tP + 32 * h, acc);
+            }
+            add_row(acc, alpha);
+            if (alpha_any && !first) rescale(alpha);
             tmem_st_wait();
             first = false;
-          } else if (!pv_done()) {
-            ok = false;
-            break;
           }
+          if (!ok) break;
           ++seen;
           tc_fence_before();
           __syncwarp();
@@ -696,73 +805,62 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // ---- the segment's end: O / l and LSE, or the part's unnormalised state.
       // O goes to registers first, so that the next segment's products may start
-      // while it is written.  Up to 128 rows, each group takes half of the
-      // columns of both groups' O.
-      constexpr int kCols = kTwo ? D : D / 2;  // columns that a thread writes
-      const int col0 = kTwo ? 0 : X * kCols;
-      float ov[kCols];
-      if (kTwo) {
-        if (rows > 0 ? !pv_done() : !mbar_wait(&bars[kBarODone + X], idle++ & 1)) { ok = false; break; }
+      // while it is written.
+      if (kPair && rows > 0 ? !pv_done()
+                            : !mbar_wait(&bars[kBarODone + X], (kPair ? idle++ : s) & 1)) { ok = false; break; }
+      tc_fence_after();
+      const bool whole = g.t0 == 0 && g.t1 == g.tiles;
+      const bool some = !(l == 0.f);  // an attended key (a NaN among them shows in l)
+      const int64_t grow = (int64_t)(g.b * A.Hq + g.kvh * (A.Hq / A.Hkv)) * A.n + rr;
+      const float inv = some ? 1.f / l : 0.f;
+      const int width = min(256, A.R - 256 * g.rb), full = min(256, A.R), rw = rr - 256 * g.rb;
+      const int64_t slot = 2 * (blockIdx.x + (kPair ? 0 : kCtas * X)) + (g.t0 > 0 ? 0 : 1);
+      float4* part = A.part + slot * (D / 4) * full + rw;
+      // N columns from c0 on
+      auto write = [&](const float* ov, int c0, auto N) {
+        if (!row_ok) return;
+        if (whole) {
+          uint4* dst = reinterpret_cast<uint4*>(A.o + grow * D + c0);
+#pragma unroll
+          for (int x = 0; x < N / 8; ++x) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) pk[y] = pack_bf16x2(ov[8 * x + 2 * y] * inv, ov[8 * x + 2 * y + 1] * inv);
+            dst[x] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < N / 4; ++x, part += width)
+            *part = make_float4(ov[4 * x], ov[4 * x + 1], ov[4 * x + 2], ov[4 * x + 3]);
+        }
+      };
+      if constexpr (kPair) {
+        float ov[D];
         // every warp loads, with rows or not: values defined on one path only would stay live around the loop
 #pragma unroll
-        for (int c = 0; c < kCols / 32; ++c) tmem_ld32(tO + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(ov + 32 * c));
+        for (int c = 0; c < D / 32; ++c) tmem_ld32(tO + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(ov + 32 * c));
         tmem_ld_wait();
-      } else {
-        if (s > 0 && !mbar_wait(&bars[kBarOFree], (s - 1) & 1)) { ok = false; break; }  // ml has been read
-        ml[128 * X + r] = make_float2(m_used, l);
+        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kBarML]);
-        if (!mbar_wait(&bars[kBarML], s & 1) || !mbar_wait(&bars[kBarODone], s & 1) ||
-            !mbar_wait(&bars[kBarODone + 1], s & 1)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const float2 s0 = ml[r], s1 = ml[128 + r];
-        const float m = fmaxf(s0.x, s1.x), ref = m == -INFINITY ? 0.f : m;
-        const float w0 = ex2(s0.x - ref), w1 = ex2(s1.x - ref);
-        m_used = m;
-        l = s0.y * w0 + s1.y * w1;
-        const uint32_t t0 = tmem + lane_base + kColO + col0;
-#pragma unroll
-        for (int c = 0; c < kCols / 32; ++c) {
-          uint32_t q[32];
-          tmem_ld32(t0 + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(ov + 32 * c));
-          tmem_ld32(t0 + 128 + 32 * c, q);
-          tmem_ld_wait();
-#pragma unroll
-          for (int x = 0; x < 32; ++x)  // a group without a tile has no O
-            ov[32 * c + x] = ov[32 * c + x] * w0 + (nt > 1 ? __uint_as_float(q[x]) * w1 : 0.f);
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&bars[kBarOFree + (kTwo ? X : 0)]);
-        if (!kTwo) mbar_arrive(&bars[kBarOFree + 1]);
-      }
-      if (!row_ok) continue;
-      const bool some = !(l == 0.f);  // an attended key (a NaN among them shows in l)
-      if (g.t0 == 0 && g.t1 == g.tiles) {
-        const int64_t grow = (int64_t)(g.b * A.Hq + g.kvh * (A.Hq / A.Hkv)) * A.n + rr;
-        const float inv = some ? 1.f / l : 0.f;
-        uint4* dst = reinterpret_cast<uint4*>(A.o + grow * D + col0);
-#pragma unroll
-        for (int x = 0; x < kCols / 8; ++x) {
-          uint32_t pk[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) pk[y] = pack_bf16x2(ov[8 * x + 2 * y] * inv, ov[8 * x + 2 * y + 1] * inv);
-          dst[x] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-        }
-        if (A.lse && col0 == 0) A.lse[grow] = some ? (m_used + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+        if (lane == 0) mbar_arrive(&bars[kBarOFree + X]);
+        write(ov, 0, std::integral_constant<int, D>());
       } else {
-        const int width = min(256, A.R - 256 * g.rb), full = min(256, A.R), rw = rr - 256 * g.rb;
-        const int64_t slot = 2 * blockIdx.x + (g.t0 > 0 ? 0 : 1);
-        float4* part = A.part + slot * (D / 4) * full + (int64_t)(col0 / 4) * width + rw;
-#pragma unroll
-        for (int x = 0; x < kCols / 4; ++x, part += width)
-          *part = make_float4(ov[4 * x], ov[4 * x + 1], ov[4 * x + 2], ov[4 * x + 3]);
-        if (col0 == 0) A.part_ml[slot * full + rw] = make_float2(m_used, l);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 64) {
+          float ov[64];
+          __syncwarp();
+          load64(tO + c, ov);
+          if (c + 64 == D) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kBarOFree + X]);
+          }
+          write(ov, c, std::integral_constant<int, 64>());
+        }
+      }
+      if (row_ok) {
+        if (!whole) A.part_ml[slot * full + rw] = make_float2(m_used, l);
+        else if (A.lse) A.lse[grow] = some ? (m_used + __log2f(l)) * 0.69314718055994531f : -INFINITY;
       }
     }
   }
@@ -791,7 +889,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeArgs 
   const int64_t W = A.prefix[A.B], p0 = A.prefix[b], p1 = A.prefix[b + 1];
   if (p1 == p0) return;
   const int64_t tiles = (p1 - p0) / items, s0 = p0 + item * tiles, s1 = s0 + tiles;
-  const int G = parts(W);  // part c holds tile x: the largest c with W c / G <= x
+  const int G = parts(W, A.max_parts);  // part c holds tile x: the largest c with W c / G <= x
   const int c0 = (int)(((s0 + 1) * G - 1) / W), c1 = (int)((s1 * G - 1) / W);
   if (c0 == c1) return;  // one CTA finished it
   const int rb = item % A.RB, kvh = item / A.RB;
@@ -855,13 +953,14 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 struct TreeWs {
   size_t prefix, ml, part, total;
 };
+int max_parts(int64_t R) { return R > 128 ? kCtas : 2 * kCtas; }
 TreeWs tree_ws(const msa_shape& s) {
-  const int64_t R = (int64_t)(s.Hq / s.Hkv) * s.n, full = R < 256 ? R : 256;
+  const int64_t R = (int64_t)(s.Hq / s.Hkv) * s.n, rows = 2 * max_parts(R) * (R < 256 ? R : 256);
   TreeWs w;
   w.prefix = 0;
   w.ml = align256((size_t)(s.B + 1) * 8);
-  w.part = align256(w.ml + (size_t)(2 * kCtas * full) * 8);
-  w.total = align256(w.part + (size_t)(2 * kCtas * full) * s.d_h * 4);
+  w.part = align256(w.ml + (size_t)rows * 8);
+  w.total = align256(w.part + (size_t)rows * s.d_h * 4);
   return w;
 }
 
@@ -880,9 +979,9 @@ bool aligned(const void* p, size_t a, bool required) {
   return reinterpret_cast<uintptr_t>(p) % a == 0;
 }
 
-template <int D, bool kTwo>
+template <int D, Rows kRows>
 msa_status launch_tree(const TreeMaps& maps, const TreeArgs& a, bool join, cudaStream_t stream) {
-  auto kern = tree_attn_kernel<D, kTwo>;
+  auto kern = tree_attn_kernel<D, kRows>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::kAlloc) != cudaSuccess)
     return MSA_ERR_CUDA;
   kern<<<kCtas, kThreads, Lay<D>::kAlloc, stream>>>(maps, a);
@@ -944,6 +1043,7 @@ extern "C" msa_status msa_attn_tree(const msa_shape* shape, const void* q, const
   a.n = shape->n;
   a.R = shape->Hq / shape->Hkv * shape->n;
   a.RB = (a.R + 255) / 256;
+  a.max_parts = max_parts(a.R);
   // a load costs about 100 cycles whatever its size: few of them, and few rows that are not the group's
   a.q_box = a.R <= 16 ? 16 : a.R <= 32 ? 32 : 64;
   a.page_shift = __builtin_ctz((unsigned)pages->page_size);
@@ -973,7 +1073,8 @@ extern "C" msa_status msa_attn_tree(const msa_shape* shape, const void* q, const
   // a table of at most 128 keys holds no item of two tiles: none is cut
   const bool join = (int64_t)max_pages * pages->page_size > 128;
   cudaStream_t stm = (cudaStream_t)stream;
-  if (a.R > 128)
-    return shape->d_h == 128 ? launch_tree<128, true>(maps, a, join, stm) : launch_tree<64, true>(maps, a, join, stm);
-  return shape->d_h == 128 ? launch_tree<128, false>(maps, a, join, stm) : launch_tree<64, false>(maps, a, join, stm);
+  const bool d128 = shape->d_h == 128;
+  if (a.R <= 64) return d128 ? launch_tree<128, kFew>(maps, a, join, stm) : launch_tree<64, kFew>(maps, a, join, stm);
+  if (a.R <= 128) return d128 ? launch_tree<128, kMany>(maps, a, join, stm) : launch_tree<64, kMany>(maps, a, join, stm);
+  return d128 ? launch_tree<128, kTwo>(maps, a, join, stm) : launch_tree<64, kTwo>(maps, a, join, stm);
 }
