@@ -99,6 +99,7 @@ struct TreeMaps {
 struct Seg {
   int32_t b, kvh, rb, t0, t1, tiles;  // b < 0: no more
   int32_t L, T;
+  int32_t r0, r1;  // tiles that its result covers: t0, t1, or more where both groups' segments are joined
 };
 
 // Barriers; [X]: per group (kTwo: segments and Q once, at X = 0)
@@ -111,7 +112,8 @@ enum {
   kBarOFree = 14,                        // [X] O of the segment has been read
   kBarPV = 16,                           // [X] kTwo: the group's last P has been used
   kBarSFree = 18,                        // kTwo: the scores are in registers
-  kBarSegFull = 19,                      // [X][kSegSlots]
+  kBarML = 19,                           // kMany: both groups' maxima and sums are written
+  kBarSegFull = 20,                      // [X][kSegSlots]
   kBarSegEmpty = kBarSegFull + 2 * kSegSlots,
   kBarRing = kBarSegEmpty + 2 * kSegSlots  // full[kSlots], empty[kSlots], ready[kSlots]
 };
@@ -123,7 +125,8 @@ struct Lay {
   static constexpr int kQ = 0;  // two Q tiles, one per group (kFew: of two 64-row buffers)
   static constexpr int kRing = 2 * kTile;
   static constexpr int kSeg = kRing + kSlots * kTile;
-  static constexpr int kBars = kSeg + 2 * kSegSlots * (int)sizeof(Seg);
+  static constexpr int kML = kSeg + 2 * kSegSlots * (int)sizeof(Seg);  // kMany: [2][128] maximum and row sum
+  static constexpr int kBars = kML + 2 * 128 * 8;
   static constexpr int kNumBars = kBarRing + 3 * kSlots;
   static constexpr int kMisc = kBars + kNumBars * 8;  // [0] TMEM base, [2] abort
   static constexpr int kAlloc = kMisc + 16;
@@ -172,9 +175,19 @@ __device__ __forceinline__ bool request(const TreeArgs& A, int b, int& L, int& T
   return !bad && T > 0;
 }
 __device__ __forceinline__ int key_tiles(int L) { return (L + 127) >> 7; }
-// The line of W tiles in G = min(W, max_parts) parts; CTA c's groups take parts c and kCtas + c.
+// The line of W tiles in G = min(W, max_parts) parts.  CTA c's groups take parts 2 c and 2 c + 1 if there are
+// max_parts of them (of two per CTA), else parts c and kCtas + c.
 __device__ __forceinline__ int parts(int64_t W, int most) { return W < most ? (int)W : most; }
+__device__ __forceinline__ int part_of(int64_t W, int most, int cta, int X) {
+  return most > kCtas && W >= most ? 2 * cta + X : cta + kCtas * X;
+}
 __device__ __forceinline__ int64_t part_begin(int64_t W, int most, int p) { return W < most ? p : W * p / most; }
+
+// kMany, all parts present: the odd part of a CTA that lies within one item [s0, s1) which its even part reaches too
+// is joined with it in the CTA.
+__device__ __forceinline__ bool joined_in_cta(bool many, int64_t W, int most, int p, int64_t s0, int64_t s1) {
+  return many && W >= most && (p & 1) && part_begin(W, most, p) > s0 && part_begin(W, most, p + 1) <= s1;
+}
 
 template <int D, Rows kRows>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -223,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars[kBarPV + x], 1);
     }
     mbar_init(&bars[kBarSFree], 4);
+    mbar_init(&bars[kBarML], 8);
     for (int s = 0; s < 2 * kSegSlots; ++s) {
       mbar_init(&bars[kBarSegFull + s], 1);
       mbar_init(&bars[kBarSegEmpty + s], kSegReaders);
@@ -271,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t t = per == 1 ? own : tiles(b);
 #pragma unroll
       for (int X = 0; X < (kPair ? 1 : 2); ++X) {
-        const int64_t lo = part_begin(W, kMost, blockIdx.x + kCtas * X);  // at or above W: no part
+        const int64_t lo = part_begin(W, kMost, part_of(W, kMost, blockIdx.x, X));  // at or above W: no part
         if (at <= lo && lo < at + t) { start[2 * X] = b; start[2 * X + 1] = at; }
       }
       if (blockIdx.x == 0) A.prefix[b] = at;
@@ -285,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int cnt[2] = {0, 0};
 #pragma unroll
   for (int X = 0; X < (kPair ? 1 : 2); ++X) {
-    const int p = blockIdx.x + kCtas * X;
+    const int p = part_of(W, kMost, blockIdx.x, X);
     if (p < G) {
       begin[X] = part_begin(W, kMost, p);
       cnt[X] = (int)(part_begin(W, kMost, p + 1) - begin[X]);
@@ -393,6 +407,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         g.t0 = (int)(S.pos - S.at - (int64_t)item * g.tiles);
         const int64_t left = S.hi - S.pos;
         g.t1 = left < g.tiles - g.t0 ? g.t0 + (int)left : g.tiles;
+        g.r0 = g.t0;
+        g.r1 = g.t1;
+        if (kRows == kMany) {
+          const int64_t i0 = S.at + (int64_t)item * g.tiles;
+          const int p = part_of(W, kMost, blockIdx.x, 1);
+          // (of the even part only its last segment reaches the item)
+          if (joined_in_cta(true, W, kMost, p, i0, i0 + g.tiles)) {
+            g.r0 = (int)max((int64_t)0, begin[0] - i0);
+            g.r1 = (int)(begin[1] + cnt[1] - i0);
+          }
+        }
         S.pos += g.t1 - g.t0;
         S.t = g.t0;
         if (!publish(X, S.s, g)) return false;
@@ -809,13 +834,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (kPair && rows > 0 ? !pv_done()
                             : !mbar_wait(&bars[kBarODone + X], (kPair ? idle++ : s) & 1)) { ok = false; break; }
       tc_fence_after();
-      const bool whole = g.t0 == 0 && g.t1 == g.tiles;
+      const bool joins = kRows == kMany && (g.r0 != g.t0 || g.r1 != g.t1);
+      float w0 = 1.f, w1 = 0.f;
+      if (joins) {  // both groups' last segments, once per CTA: each takes half of the columns of both O's
+        float2* ml = reinterpret_cast<float2*>(sm + Ly::kML);
+        ml[128 * X + r] = make_float2(m_used, l);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kBarML]);  // and every product into this group's O is done
+        if (!mbar_wait(&bars[kBarML], 0)) { ok = false; break; }
+        tc_fence_after();
+        const float2 a = ml[r], b = ml[128 + r];
+        const float m = fmaxf(a.x, b.x), ref = m == -INFINITY ? 0.f : m;
+        w0 = ex2(a.x - ref);
+        w1 = ex2(b.x - ref);
+        m_used = m;
+        l = a.y * w0 + b.y * w1;
+      }
+      const bool whole = g.r0 == 0 && g.r1 == g.tiles;
       const bool some = !(l == 0.f);  // an attended key (a NaN among them shows in l)
       const int64_t grow = (int64_t)(g.b * A.Hq + g.kvh * (A.Hq / A.Hkv)) * A.n + rr;
       const float inv = some ? 1.f / l : 0.f;
       const int width = min(256, A.R - 256 * g.rb), full = min(256, A.R), rw = rr - 256 * g.rb;
-      const int64_t slot = 2 * (blockIdx.x + (kPair ? 0 : kCtas * X)) + (g.t0 > 0 ? 0 : 1);
-      float4* part = A.part + slot * (D / 4) * full + rw;
+      const int64_t slot = 2 * part_of(W, kMost, blockIdx.x, kPair || joins ? 0 : X) + (g.r0 > 0 ? 0 : 1);
       // N columns from c0 on
       auto write = [&](const float* ov, int c0, auto N) {
         if (!row_ok) return;
@@ -829,6 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             dst[x] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
           }
         } else {
+          float4* part = A.part + slot * (D / 4) * full + (int64_t)(c0 / 4) * width + rw;
 #pragma unroll
           for (int x = 0; x < N / 4; ++x, part += width)
             *part = make_float4(ov[4 * x], ov[4 * x + 1], ov[4 * x + 2], ov[4 * x + 3]);
@@ -844,6 +886,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[kBarOFree + X]);
         write(ov, 0, std::integral_constant<int, D>());
+      } else if (joins) {
+#pragma unroll 1
+        for (int c = X * (D / 2); c < (X + 1) * (D / 2); c += 32) {
+          float ov[32], q[32];
+          __syncwarp();
+          tmem_ld32(tmem + lane_base + kColO + c, *reinterpret_cast<uint32_t(*)[32]>(ov));
+          tmem_ld32(tmem + lane_base + kColO + 128 + c, *reinterpret_cast<uint32_t(*)[32]>(q));
+          tmem_ld_wait();
+#pragma unroll
+          for (int x = 0; x < 32; ++x) ov[x] = ov[x] * w0 + q[x] * w1;
+          write(ov, c, std::integral_constant<int, 32>());
+        }
       } else {
 #pragma unroll 1
         for (int c = 0; c < D; c += 64) {
@@ -858,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           write(ov, c, std::integral_constant<int, 64>());
         }
       }
-      if (row_ok) {
+      if (row_ok && (!joins || X == 0)) {
         if (!whole) A.part_ml[slot * full + rw] = make_float2(m_used, l);
         else if (A.lse) A.lse[grow] = some ? (m_used + __log2f(l)) * 0.69314718055994531f : -INFINITY;
       }
@@ -891,7 +945,14 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeArgs 
   const int64_t tiles = (p1 - p0) / items, s0 = p0 + item * tiles, s1 = s0 + tiles;
   const int G = parts(W, A.max_parts);  // part c holds tile x: the largest c with W c / G <= x
   const int c0 = (int)(((s0 + 1) * G - 1) / W), c1 = (int)((s1 * G - 1) / W);
-  if (c0 == c1) return;  // one CTA finished it
+  // Its parts: c0, the ones from c0 + lead on by `step`, and c1 where those leave it out.  (kMany, all parts present:
+  // an odd part that was joined in its CTA stands in the slot of the even one; only c0 and c1 can be odd and not.)
+  const bool pairs = A.R > 64 && A.R <= 128 && W >= 2 * kCtas;
+  const int step = pairs ? 2 : 1, lead = pairs && !(c0 & 1) ? 2 : 1;
+  const int inner = c0 + lead <= c1 ? (c1 - c0 - lead) / step + 1 : 0;
+  const bool tail = pairs && (c1 & 1) && c1 != c0 && !joined_in_cta(true, W, 2 * kCtas, c1, s0, s1);
+  const int n = 1 + inner + (tail ? 1 : 0);
+  if (n == 1) return;  // one CTA finished it
   const int rb = item % A.RB, kvh = item / A.RB;
   const int width = min(256, A.R - 256 * rb), full = min(256, A.R);
   const int e = blockIdx.y * kJoinThreads + threadIdx.x;
@@ -899,28 +960,31 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeArgs 
   const int c4 = e / width, rw = e - c4 * width, rr = 256 * rb + rw;
   const int T = A.tree_len ? A.tree_len[b] : A.n;
   if (rr % A.n >= T) return;
-  auto slot = [&](int c) { return (int64_t)(2 * c + (c == c0 ? 1 : 0)); };  // the first part starts the item
+  auto slot = [&](int k) {  // of its k-th part; the first one starts the item
+    return (int64_t)(k == 0 ? 2 * c0 + 1 : 2 * (k <= inner ? c0 + lead + step * (k - 1) : c1));
+  };
   // one pass, kAhead parts at a time: their loads are all in flight before the first is used
   constexpr int kAhead = 8;
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   const float2* ml = A.part_ml + rw;
   const float4* part = A.part + (int64_t)c4 * width + rw;
-  for (int c = c0; c <= c1; c += kAhead) {
+  for (int c = 0; c < n; c += kAhead) {
     float2 x[kAhead];
     float4 y[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const int64_t sl = slot(min(c + k, c1));
-      x[k] = ml[sl * full];
-      y[k] = part[sl * (D / 4) * full];
+      x[k] = make_float2(-INFINITY, 0.f);
+      y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c + k < n) {
+        const int64_t sl = slot(c + k);
+        x[k] = ml[sl * full];
+        y[k] = part[sl * (D / 4) * full];
+      }
     }
     float top = m;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (c + k > c1) x[k] = make_float2(-INFINITY, 0.f);
-      top = fmaxf(top, x[k].x);
-    }
+    for (int k = 0; k < kAhead; ++k) top = fmaxf(top, x[k].x);
     const float ref = top == -INFINITY ? 0.f : top;
     const float keep = ex2(m - ref);
     m = top;
@@ -931,7 +995,6 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeArgs 
     o.w *= keep;
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      if (c + k > c1) continue;  // a repeated last part carries nothing (its values may be NaN)
       const float w = ex2(x[k].x - ref);
       l += w * x[k].y;
       o.x += w * y[k].x;
