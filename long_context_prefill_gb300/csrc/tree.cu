@@ -63,10 +63,10 @@ float effective_scale(const msa_shape& s);
 namespace {
 
 constexpr int kCtas = 152;
-constexpr int kThreads = 384;
-constexpr int kCleanWarp = 8, kMmaWarp0 = 9, kLoaderWarp = 10;  // 11: the other issuer
+constexpr int kCleanWarp = 8, kMmaWarp0 = 9, kLoaderWarp = 10, kMmaWarp1 = 11;
 constexpr int kSegSlots = 3;
 enum Rows { kFew = 0, kMany = 1, kTwo = 2 };
+constexpr int threads_of(Rows r) { return r == kMany ? 512 : 384; }
 constexpr uint32_t kTmemCols = 512;
 // TMEM columns.  kFew, kMany: S of group X at 128 X, P over its first 64.
 // kTwo: one S that the groups use in turn, P of group X at 128 + 64 X.  O of
@@ -190,14 +190,22 @@ __device__ __forceinline__ bool joined_in_cta(bool many, int64_t W, int most, in
 }
 
 template <int D, Rows kRows>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_of(kRows), 1)
     tree_attn_kernel(const __grid_constant__ TreeMaps M, const TreeArgs A) {
   using Ly = Lay<D>;
   constexpr bool kPair = kRows == kTwo;
+  constexpr int kThreads = threads_of(kRows);
+  // From 8 boxes a K or V tile on (small pages) a second loader warp takes half of them, in kFew one of the softmax
+  // warps without rows, in kMany one more warp: a box costs its warp about 100 cycles, and 16-token pages make 32 of
+  // them a tile, more than the tile takes out of HBM (decode of 256 short requests 96 -> 84 us, d_h 64 143 -> 124 us).
+  // With fewer the second warp costs more than it takes over (d_h 64 in 64-token pages: 118 us without, 125 us with
+  // it).  kTwo is not bound by its loads.
+  constexpr int kHelperWarp = kRows == kFew ? 2 : 12;
+  const int loaders = !kPair && (128 >> A.page_shift) * (D / 64) >= 8 ? 2 : 1;
   constexpr int kSlots = Ly::kSlots;
   constexpr int kMost = kPair ? kCtas : 2 * kCtas;  // parts (A.max_parts)
   constexpr int kGroupWarps = kRows == kFew ? 2 : 4;
-  constexpr int kSegReaders = kPair ? 11 : kGroupWarps + 2;  // softmax warps, issuer(s), the cleaner
+  constexpr int kSegReaders = kPair ? 11 : kGroupWarps + 2;  // softmax warps, issuer(s), the cleaner (and the helper)
   constexpr int kQBufs = kRows == kFew ? 2 : 1;
   extern __shared__ __align__(1024) uint8_t sm[];  // swizzled tiles start on 1 KB
   if (smem_u32(sm) & 1023) {
@@ -239,10 +247,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars[kBarML], 8);
     for (int s = 0; s < 2 * kSegSlots; ++s) {
       mbar_init(&bars[kBarSegFull + s], 1);
-      mbar_init(&bars[kBarSegEmpty + s], kSegReaders);
+      mbar_init(&bars[kBarSegEmpty + s], kSegReaders + loaders - 1);
     }
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&bFull[s], 1);
+      mbar_init(&bFull[s], loaders);
       mbar_init(&bEmpty[s], 1);
       mbar_init(&bReady[s], 1);
     }
@@ -355,12 +363,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   // rows of softmax group X in the 256-row block rb
   auto group_rows = [&](int rb, int X) { return min(128, A.R - 256 * rb - (kPair ? 128 * X : 0)); };
 
-  // the block starts with 3 x 128 threads x 168 registers; the softmax threads (a row's 128 scores each) take
-  // 192 and the others' 120: 2 x 192 + 120 = 3 x 168
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
-    if (warp == kLoaderWarp) {
-      // ---------------------------------------------------------- loader
+  // kTwo: the block starts with 3 x 128 threads x 168 registers; the softmax threads (a row's 128 scores each) take
+  // 192 and the others 120: 2 x 192 + 120 = 3 x 168
+  if (warp >= 8 || (kRows == kFew && warp == kHelperWarp)) {
+    if (kPair) asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+    if (warp == kLoaderWarp || (loaders > 1 && warp == kHelperWarp)) {
+      // ---------------------------------------------------------- loader and helper
+      const int share = warp == kLoaderWarp ? 0 : 1;  // takes boxes share, share + loaders, ..
       const uint64_t policy = A.RB == 1 ? policy_evict_first() : policy_evict_last();
       const int pshift = 7 - A.page_shift, pp = 1 << pshift;  // pages of a tile
       const int P = 1 << A.page_shift;
@@ -391,48 +400,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The next segment of a stream: its descriptor, its Q rows, its first page entries.
       auto open = [&](Stream& S, int X) -> bool {
         Seg& g = S.g;
-        bool bad;
-        int64_t t = 0;
-        for (; S.b < A.B; ++S.b) {  // pos < hi <= W: a request holding it exists
-          t = request(A, S.b, g.L, g.T, bad) ? (int64_t)items * key_tiles(g.L) : 0;
-          if (S.pos < S.at + t) break;
-          S.at += t;
-        }
-        if (S.b >= A.B) return false;
-        g.b = S.b;
-        g.tiles = key_tiles(g.L);
-        const int item = (int)((S.pos - S.at) / g.tiles);
-        g.kvh = item / A.RB;
-        g.rb = item - g.kvh * A.RB;
-        g.t0 = (int)(S.pos - S.at - (int64_t)item * g.tiles);
-        const int64_t left = S.hi - S.pos;
-        g.t1 = left < g.tiles - g.t0 ? g.t0 + (int)left : g.tiles;
-        g.r0 = g.t0;
-        g.r1 = g.t1;
-        if (kRows == kMany) {
-          const int64_t i0 = S.at + (int64_t)item * g.tiles;
-          const int p = part_of(W, kMost, blockIdx.x, 1);
-          // (of the even part only its last segment reaches the item)
-          if (joined_in_cta(true, W, kMost, p, i0, i0 + g.tiles)) {
-            g.r0 = (int)max((int64_t)0, begin[0] - i0);
-            g.r1 = (int)(begin[1] + cnt[1] - i0);
+        if (share > 0) {
+          if (!next_seg(X, S.s, g)) return false;
+        } else {
+          bool bad;
+          int64_t t = 0;
+          for (; S.b < A.B; ++S.b) {  // pos < hi <= W: a request holding it exists
+            t = request(A, S.b, g.L, g.T, bad) ? (int64_t)items * key_tiles(g.L) : 0;
+            if (S.pos < S.at + t) break;
+            S.at += t;
+          }
+          if (S.b >= A.B) return false;
+          g.b = S.b;
+          g.tiles = key_tiles(g.L);
+          const int item = (int)((S.pos - S.at) / g.tiles);
+          g.kvh = item / A.RB;
+          g.rb = item - g.kvh * A.RB;
+          g.t0 = (int)(S.pos - S.at - (int64_t)item * g.tiles);
+          const int64_t left = S.hi - S.pos;
+          g.t1 = left < g.tiles - g.t0 ? g.t0 + (int)left : g.tiles;
+          g.r0 = g.t0;
+          g.r1 = g.t1;
+          if (kRows == kMany) {
+            const int64_t i0 = S.at + (int64_t)item * g.tiles;
+            const int p = part_of(W, kMost, blockIdx.x, 1);
+            // (of the even part only its last segment reaches the item)
+            if (joined_in_cta(true, W, kMost, p, i0, i0 + g.tiles)) {
+              g.r0 = (int)max((int64_t)0, begin[0] - i0);
+              g.r1 = (int)(begin[1] + cnt[1] - i0);
+            }
+          }
+          S.pos += g.t1 - g.t0;
+          if (!publish(X, S.s, g)) return false;
+          const int buf = S.s % kQBufs;
+          if (!mbar_wait_idle(&bars[kBarQEmpty + 2 * X + buf], ((S.s / kQBufs) & 1) ^ 1, kIdleNs)) return false;
+          const int rows = min(kPair ? 256 : 128, A.R - 256 * g.rb), boxes = (rows + A.q_box - 1) / A.q_box;
+          uint64_t* full = &bars[kBarQFull + 2 * X + buf];
+          if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(boxes * A.q_box * D * 2));
+          __syncwarp();
+          const int qrow = (g.b * A.Hq + g.kvh * (A.Hq / A.Hkv)) * A.n + 256 * g.rb;
+          if (lane < boxes * (D / 64)) {  // at most 8
+            const int c = lane & (D / 64 - 1), r = lane / (D / 64) * A.q_box;
+            tma_load_3d(sm + q_at(kPair ? r >> 7 : X, buf) + c * 16384 + (r & 127) * 128, &M.q, full, 64 * c, qrow + r, 0);
           }
         }
-        S.pos += g.t1 - g.t0;
-        S.t = g.t0;
-        if (!publish(X, S.s, g)) return false;
-        const int buf = S.s % kQBufs;
-        if (!mbar_wait_idle(&bars[kBarQEmpty + 2 * X + buf], ((S.s / kQBufs) & 1) ^ 1, kIdleNs)) return false;
         ++S.s;
-        const int rows = min(kPair ? 256 : 128, A.R - 256 * g.rb), boxes = (rows + A.q_box - 1) / A.q_box;
-        uint64_t* full = &bars[kBarQFull + 2 * X + buf];
-        if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(boxes * A.q_box * D * 2));
-        __syncwarp();
-        const int qrow = (g.b * A.Hq + g.kvh * (A.Hq / A.Hkv)) * A.n + 256 * g.rb;
-        if (lane < boxes * (D / 64)) {  // at most 8
-          const int c = lane & (D / 64 - 1), r = lane / (D / 64) * A.q_box;
-          tma_load_3d(sm + q_at(kPair ? r >> 7 : X, buf) + c * 16384 + (r & 127) * 128, &M.q, full, 64 * c, qrow + r, 0);
-        }
+        S.t = g.t0;
         S.base = g.t0 << pshift;
         S.ids = entry(g, S.base + lane);
         S.ahead = entry(g, S.base + 32 + lane);
@@ -450,17 +463,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           S.ahead = entry(S.g, S.base + 32 + lane);
         }
         const int np = (S.g.L + P - 1) >> A.page_shift;
-        const int have = min(pp, np - (S.t << pshift));  // pages of this tile that hold keys
-        const int c = lane >> 3, x = lane & 7;
+        const int boxes = min(pp, np - (S.t << pshift)) * (D / 64);  // pages of this tile that hold keys, by 64 columns
+        const int box = lane * loaders + share, c = box & (D / 64 - 1), x = box / (D / 64);
+        const uint32_t bytes = (uint32_t)(((boxes - share + loaders - 1) >> (loaders - 1)) * P * 128);
         const int krow = (__shfl_sync(0xFFFFFFFFu, S.ids, (off + x) & 31) * A.Hkv + S.g.kvh) << A.page_shift;
 #pragma unroll
         for (int is_v = 0; is_v < 2; ++is_v) {
           const int idx = 2 * j + is_v, st = idx % kSlots;
           if (misc[2] || !mbar_wait_idle(&bEmpty[st], ((idx / kSlots) & 1) ^ 1, kIdleNs)) return false;
-          if (lane == 0) mbar_arrive_expect_tx(&bFull[st], (uint32_t)(have * P * D * 2));
+          if (lane == 0) mbar_arrive_expect_tx(&bFull[st], bytes);
           __syncwarp();
           issued = idx + 1;
-          if (c < D / 64 && x < have)
+          if (box < boxes)
             tma_load_3d_hint(sm + Ly::kRing + st * Ly::kTile + c * 16384 + x * P * 128, is_v ? &M.v : &M.k, &bFull[st],
                              64 * c, krow, 0, policy);
         }
@@ -476,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Seg end;
       end.b = -1;
       int X = 0;
-      if (!kPair && cnt[1] == 0) ok = publish(1, 0, end);  // an idle group leaves at once
+      if (!kPair && share == 0 && cnt[1] == 0) ok = publish(1, 0, end);  // an idle group leaves at once
       for (int j = 0; j < cnt[0] + cnt[1] && ok; ++j) {
         if (owner(j) != X) {
           const Stream t = S;
@@ -486,8 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ok = step(S, X, j);
       }
-      if (ok) ok = publish(X, S.s, end);
-      if (!kPair && ok && cnt[1] > 0) ok = publish(X ^ 1, other.s, end);
+      if (ok && share == 0) ok = publish(X, S.s, end) && (kPair || cnt[1] == 0 || publish(X ^ 1, other.s, end));
       if (!ok)  // gave up: the copies in flight land before the shared memory goes
         for (int x = max(0, issued - kSlots); x < issued; ++x) mbar_wait(&bFull[x % kSlots], (x / kSlots) & 1);
     } else if (warp == kCleanWarp) {
@@ -530,68 +543,68 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (kPair && warp == kMmaWarp0) {
-    // ------------------------------------------------------------ scores of both groups
-    int tile = 0, use = 0;  // tiles so far, uses of S so far
-    Seg g;
-    for (int s = 0; next_seg(0, s, g); ++s) {
-      if (!mbar_wait(&bars[kBarQFull], s & 1)) { ok = false; break; }
-      for (int t = g.t0; t < g.t1 && ok; ++t, ++tile) {
-        const int kst = 2 * tile % kSlots;
-        if (misc[2] || !ready(2 * tile)) { ok = false; break; }
+      // ------------------------------------------------------------ scores of both groups
+      int tile = 0, use = 0;  // tiles so far, uses of S so far
+      Seg g;
+      for (int s = 0; next_seg(0, s, g); ++s) {
+        if (!mbar_wait(&bars[kBarQFull], s & 1)) { ok = false; break; }
+        for (int t = g.t0; t < g.t1 && ok; ++t, ++tile) {
+          const int kst = 2 * tile % kSlots;
+          if (misc[2] || !ready(2 * tile)) { ok = false; break; }
 #pragma unroll
-        for (int X = 0; X < 2; ++X) {
-          if (group_rows(g.rb, X) <= 0) continue;
-          if (use > 0 && !mbar_wait(&bars[kBarSFree], (use - 1) & 1)) { ok = false; break; }
-          ++use;
-          tc_fence_after();
-          if (lane == 0) {
-            issue_qk(tmem + kColS, q_desc(X, 0), dk + (uint64_t)kst * kTileDesc);
-            mma_commit(&bars[kBarSFull + X]);
+          for (int X = 0; X < 2; ++X) {
+            if (group_rows(g.rb, X) <= 0) continue;
+            if (use > 0 && !mbar_wait(&bars[kBarSFree], (use - 1) & 1)) { ok = false; break; }
+            ++use;
+            tc_fence_after();
+            if (lane == 0) {
+              issue_qk(tmem + kColS, q_desc(X, 0), dk + (uint64_t)kst * kTileDesc);
+              mma_commit(&bars[kBarSFull + X]);
+            }
+            __syncwarp();
           }
+          if (ok && lane == 0) mma_commit(&bEmpty[kst]);
           __syncwarp();
         }
-        if (ok && lane == 0) mma_commit(&bEmpty[kst]);
+        if (!ok) break;
+        if (lane == 0) mma_commit(&bars[kBarQEmpty]);
         __syncwarp();
       }
-      if (!ok) break;
-      if (lane == 0) mma_commit(&bars[kBarQEmpty]);
-      __syncwarp();
-    }
     } else if (kPair) {
-    // ------------------------------------------------------------ O += P V of both groups
-    int tile = 0, seen[2] = {0, 0};  // tiles so far, P's of each group
-    Seg g;
-    for (int s = 0; next_seg(0, s, g); ++s) {
-      // O_X of the segment before has been read: its first PV here, or (no rows) its end, waits for that
-      auto o_free = [&](int X) { return s == 0 || mbar_wait(&bars[kBarOFree + X], (s - 1) & 1); };
-      for (int t = g.t0; t < g.t1 && ok; ++t, ++tile) {
-        const int vst = (2 * tile + 1) % kSlots;
-        if (misc[2] || !ready(2 * tile + 1)) { ok = false; break; }
+      // ------------------------------------------------------------ O += P V of both groups
+      int tile = 0, seen[2] = {0, 0};  // tiles so far, P's of each group
+      Seg g;
+      for (int s = 0; next_seg(0, s, g); ++s) {
+        // O_X of the segment before has been read: its first PV here, or (no rows) its end, waits for that
+        auto o_free = [&](int X) { return s == 0 || mbar_wait(&bars[kBarOFree + X], (s - 1) & 1); };
+        for (int t = g.t0; t < g.t1 && ok; ++t, ++tile) {
+          const int vst = (2 * tile + 1) % kSlots;
+          if (misc[2] || !ready(2 * tile + 1)) { ok = false; break; }
 #pragma unroll
-        for (int X = 0; X < 2; ++X) {
-          if (group_rows(g.rb, X) <= 0) continue;
-          if (t == g.t0 && !o_free(X)) { ok = false; break; }
-          if (!mbar_wait(&bars[kBarPFull + X], seen[X] & 1)) { ok = false; break; }
-          ++seen[X];
-          tc_fence_after();
-          if (lane == 0) {
-            issue_pv_mma(tmem + kColO + 128 * X, tmem + kColP + 64 * X, dv + (uint64_t)vst * kTileDesc, t == g.t0);
-            mma_commit(&bars[kBarPV + X]);
+          for (int X = 0; X < 2; ++X) {
+            if (group_rows(g.rb, X) <= 0) continue;
+            if (t == g.t0 && !o_free(X)) { ok = false; break; }
+            if (!mbar_wait(&bars[kBarPFull + X], seen[X] & 1)) { ok = false; break; }
+            ++seen[X];
+            tc_fence_after();
+            if (lane == 0) {
+              issue_pv_mma(tmem + kColO + 128 * X, tmem + kColP + 64 * X, dv + (uint64_t)vst * kTileDesc, t == g.t0);
+              mma_commit(&bars[kBarPV + X]);
+            }
+            __syncwarp();
           }
+          if (ok && lane == 0) mma_commit(&bEmpty[vst]);
           __syncwarp();
         }
-        if (ok && lane == 0) mma_commit(&bEmpty[vst]);
-        __syncwarp();
+        for (int X = 0; X < 2 && ok; ++X)
+          if (group_rows(g.rb, X) <= 0) {
+            ok = o_free(X);
+            if (ok && lane == 0) mbar_arrive(&bars[kBarODone + X]);
+            __syncwarp();
+          }
+        if (!ok) break;
       }
-      for (int X = 0; X < 2 && ok; ++X)
-        if (group_rows(g.rb, X) <= 0) {
-          ok = o_free(X);
-          if (ok && lane == 0) mbar_arrive(&bars[kBarODone + X]);
-          __syncwarp();
-        }
-      if (!ok) break;
-    }
-    } else {
+    } else if (!kPair && (warp == kMmaWarp0 || warp == kMmaWarp1)) {
       // ---------------------------------------------------------- MMA issuer of group X
       const int X = warp == kMmaWarp0 ? 0 : 1;
       const uint32_t tS = tmem + kColS + 128 * X, tO = tmem + kColO + 128 * X;
@@ -634,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    if (kPair) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     // ------------------------------------------------------------ softmax group X
     const int X = warp >> 2, quarter = warp & 3;
     const bool used = kRows != kFew || X == quarter >> 1;  // kFew: warps 0, 1 and 6, 7
@@ -1047,7 +1060,7 @@ msa_status launch_tree(const TreeMaps& maps, const TreeArgs& a, bool join, cudaS
   auto kern = tree_attn_kernel<D, kRows>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::kAlloc) != cudaSuccess)
     return MSA_ERR_CUDA;
-  kern<<<kCtas, kThreads, Lay<D>::kAlloc, stream>>>(maps, a);
+  kern<<<kCtas, threads_of(kRows), Lay<D>::kAlloc, stream>>>(maps, a);
   note_launch();
   if (cudaGetLastError() != cudaSuccess) return MSA_ERR_CUDA;
   if (!join) return MSA_OK;
