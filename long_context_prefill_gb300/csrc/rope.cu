@@ -36,7 +36,12 @@ msa_status check_page_geometry(int32_t num_pages, int32_t page_size);
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 8;    // tokens of a CTA
+constexpr int kMaxTokens = 16;   // tokens of a CTA
+#ifndef PERSM
+#define PERSM 8
+#define MOST 8
+#endif
+constexpr int kPerSm = PERSM, kMost = MOST;
 constexpr int kMaxBatch = 1024;  // sequences of a launch
 
 struct RopeArgs {
@@ -68,28 +73,61 @@ struct Token {
   int32_t slot;        // cache slot, < 0: not stored
 };
 
-// 16 values of a head: chunks c0 and c1 of 8.  In the rotated columns chunk 0
-// holds the first and chunk 1 the second members of 8 pairs (half-split), or
-// both hold whole pairs (interleaved).
-__device__ __forceinline__ void unpack8(uint4 u, float* f) {
-  const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&u);
+// Two fp32 values in one 64-bit register pair, for the packed f32x2 instructions.
+__device__ __forceinline__ uint64_t pk2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void up2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// 8 bf16 values (16 bytes) as four pairs
+__device__ __forceinline__ void unpack8(uint4 u, uint64_t (&f)[4]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int x = 0; x < 4; ++x) f[x] = pk2(__uint_as_float(w[x] << 16), __uint_as_float(w[x] & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint4 pack8(const uint64_t (&f)[4]) {
+  uint32_t w[4];
 #pragma unroll
   for (int x = 0; x < 4; ++x) {
-    const float2 t = __bfloat1622float2(p[x]);
-    f[2 * x] = t.x;
-    f[2 * x + 1] = t.y;
+    float a, b;
+    up2(f[x], a, b);
+    w[x] = pack_bf16x2(a, b);
   }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ uint4 pack8(const float* f) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
+// 8 floats of shared memory as four pairs: floats 0 .. 3 at p, 4 .. 7 at q
+__device__ __forceinline__ void load8(const float* p, const float* q, uint64_t (&f)[4]) {
+  const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(p), b = *reinterpret_cast<const ulonglong2*>(q);
+  f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
 }
 
+// A lane's 16 values of a head: chunks c0 and c1 of 8.  In the rotated columns
+// chunk 0 holds the first and chunk 1 the second members of 8 pairs
+// (half-split), or both hold whole pairs (interleaved).
+//
+// 65 % of the issue slots with scalar arithmetic, at 5.2 TB/s for 32K tokens of
+// 48 heads of 128; so the arithmetic is in packed pairs.
 template <int D>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeArgs A, const __grid_constant__ RopeTables T) {
   constexpr int kLanes = D / 16;               // lanes of a head
   constexpr int kHeads = kThreads / kLanes;    // heads in flight per CTA
-  __shared__ float2 cs[kMaxTokens][D / 2];
+  // Shared tables hold what a lane reads as two float4, and those of the lanes of a head side by side (no two lanes
+  // on one bank): value x of lane l at 4 (l + (x / 4) lanes) + x % 4.
+  __shared__ __align__(16) float cosines[kMaxTokens][D / 2], sines[kMaxTokens][D / 2];
+  __shared__ __align__(16) float weights[2][2][D / 2];  // [q or k][chunk]
   __shared__ Token toks[kMaxTokens];
   const int tid = threadIdx.x;
   const int H = A.Hq + A.Hkv * (1 + A.has_v);
@@ -100,9 +138,16 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeArgs A, c
   // this lane's two chunks
   const bool rotated = 16 * l < A.rot;
   const int c0 = rotated ? 8 * l : 16 * l, c1 = rotated ? half + 8 * l : 16 * l + 8;
+  const int rl = A.rot >> 4;  // lanes of a head that rotate, 8 pairs each
+  auto at = [&](int lane, int x, int lanes) { return 4 * (lane + (x >> 2) * lanes) + (x & 3); };
+  // position of pair p: value x of the lane whose chunks hold it (interleaved: 4 pairs in each chunk)
+  auto pair_at = [&](int p) {
+    if (!A.interleaved) return at(p >> 3, p & 7, rl);
+    const int second = p >= (half >> 1), q = second ? p - (half >> 1) : p;
+    return at(q >> 2, (q & 3) + 4 * second, rl);
+  };
 
-  auto load = [&](int u, uint4& x0, uint4& x1) {
-    const int t = u / H, h = u - t * H;
+  auto load = [&](int t, int h, uint4& x0, uint4& x1) {
     const __nv_bfloat16* src;
     if (h < A.Hq) src = A.q + (first + t) * A.q_stride + h * D;
     else if (h < A.Hq + A.Hkv) src = A.k + (first + t) * A.k_stride + (h - A.Hq) * D;
@@ -110,10 +155,20 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeArgs A, c
     x0 = __ldcs(reinterpret_cast<const uint4*>(src + c0));
     x1 = __ldcs(reinterpret_cast<const uint4*>(src + c1));
   };
-  const int units = cnt * H;
-  int u = tid / kLanes;
+  int t = 0, h = tid / kLanes;  // token and head of this lane
+  auto next = [&](int& t, int& h) {
+    h += kHeads;
+    while (h >= H) {
+      h -= H;
+      ++t;
+    }
+  };
+  while (h >= H) {
+    h -= H;
+    ++t;
+  }
   uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
-  if (u < units) load(u, x0, x1);  // in flight while the angles are computed
+  if (t < cnt) load(t, h, x0, x1);  // in flight while the angles are computed
 
   if (tid < cnt) {
     const int tk = first + tid;
@@ -137,6 +192,14 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeArgs A, c
     }
     toks[tid] = k;
   }
+  if (A.norm && tid < 2 * kLanes) {  // this lane's weights of a query (tid < kLanes) or key head
+    const __nv_bfloat16* w = tid < kLanes ? A.q_w : A.k_w;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      weights[tid / kLanes][0][at(l, x, kLanes)] = w ? __bfloat162float(w[c0 + x]) : 1.f;
+      weights[tid / kLanes][1][at(l, x, kLanes)] = w ? __bfloat162float(w[c1 + x]) : 1.f;
+    }
+  }
   if (half)
     for (int x = tid; x < cnt * half; x += kThreads) {
       const int t = x / half, p = x - t * half, tk = first + t;
@@ -147,59 +210,72 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeArgs A, c
       const uint64_t turns = (uint64_t)(int64_t)pos * T.turn[p];
       float s, c;
       sincospif((float)(int32_t)(turns >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31 half turns
-      cs[t][p] = make_float2(c * A.rot_scale, s * A.rot_scale);
+      cosines[t][pair_at(p)] = c * A.rot_scale;
+      sines[t][pair_at(p)] = s * A.rot_scale;
     }
   __syncthreads();
 
-  while (u < units) {
-    const int nu = u + kHeads;
+  while (t < cnt) {
+    int nt = t, nh = h;
+    next(nt, nh);
     uint4 y0 = make_uint4(0, 0, 0, 0), y1 = y0;
-    if (nu < units) load(nu, y0, y1);
-    const int t = u / H, h = u - t * H;
+    if (nt < cnt) load(nt, nh, y0, y1);
     const Token tk = toks[t];
     const bool is_v = h >= A.Hq + A.Hkv, is_q = h < A.Hq;
     if (!is_v) {
-      float a[8], b[8];
+      uint64_t a[4], b[4];
       unpack8(x0, a);
       unpack8(x1, b);
       if (A.norm) {
-        float ss = 0.f;
+        uint64_t sum = pk2(0.f, 0.f);
 #pragma unroll
-        for (int x = 0; x < 8; ++x) ss += a[x] * a[x] + b[x] * b[x];
+        for (int x = 0; x < 4; ++x) sum = fma2(b[x], b[x], fma2(a[x], a[x], sum));
+        float s0, s1;
+        up2(sum, s0, s1);
+        float ss = s0 + s1;
         const unsigned group = (kLanes == 8 ? 0xFFu : 0xFu) << ((tid & 31) / kLanes * kLanes);
 #pragma unroll
         for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
-        const float r = 1.f / sqrtf(ss * (1.f / D) + A.eps);
-        const __nv_bfloat16* w = is_q ? A.q_w : A.k_w;
-        float w0[8], w1[8];
-        if (w) {
-          unpack8(__ldg(reinterpret_cast<const uint4*>(w + c0)), w0);
-          unpack8(__ldg(reinterpret_cast<const uint4*>(w + c1)), w1);
-        }
+        const float r = rsqrtf(ss * (1.f / D) + A.eps);
+        const uint64_t rr = pk2(r, r);
+        uint64_t w[4];
+        const float* wa = &weights[is_q ? 0 : 1][0][4 * l];
+        load8(wa, wa + 4 * kLanes, w);
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          a[x] = a[x] * r * (w ? w0[x] : 1.f);
-          b[x] = b[x] * r * (w ? w1[x] : 1.f);
-        }
+        for (int x = 0; x < 4; ++x) a[x] = mul2(mul2(a[x], rr), w[x]);
+        load8(wa + D / 2, wa + D / 2 + 4 * kLanes, w);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) b[x] = mul2(mul2(b[x], rr), w[x]);
       }
       if (rotated) {
+        uint64_t c[4], s[4];
+        load8(&cosines[t][4 * l], &cosines[t][4 * (l + rl)], c);
+        load8(&sines[t][4 * l], &sines[t][4 * (l + rl)], s);
         if (A.interleaved) {
+          auto turn = [&](uint64_t v, float c, float s) {  // (p, q) -> (p c - q s, q c + p s)
+            float p, q;
+            up2(v, p, q);
+            return fma2(v, pk2(c, c), mul2(pk2(-q, p), pk2(s, s)));
+          };
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float2 e = cs[t][4 * l + x], f = cs[t][(half >> 1) + 4 * l + x];
-            const float p = a[2 * x], q = a[2 * x + 1], v = b[2 * x], w = b[2 * x + 1];
-            a[2 * x] = p * e.x - q * e.y;
-            a[2 * x + 1] = q * e.x + p * e.y;
-            b[2 * x] = v * f.x - w * f.y;
-            b[2 * x + 1] = w * f.x + v * f.y;
+          for (int x = 0; x < 2; ++x) {
+            float c0, c1, s0, s1;
+            up2(c[x], c0, c1);
+            up2(s[x], s0, s1);
+            a[2 * x] = turn(a[2 * x], c0, s0);
+            a[2 * x + 1] = turn(a[2 * x + 1], c1, s1);
+            up2(c[2 + x], c0, c1);
+            up2(s[2 + x], s0, s1);
+            b[2 * x] = turn(b[2 * x], c0, s0);
+            b[2 * x + 1] = turn(b[2 * x + 1], c1, s1);
           }
         } else {
+          const uint64_t minus = pk2(-1.f, -1.f);
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const float2 e = cs[t][8 * l + x];
-            const float p = a[x], q = b[x];
-            a[x] = p * e.x - q * e.y;
-            b[x] = q * e.x + p * e.y;
+          for (int x = 0; x < 4; ++x) {
+            const uint64_t p = a[x];
+            a[x] = fma2(p, c[x], mul2(mul2(b[x], s[x]), minus));
+            b[x] = fma2(b[x], c[x], mul2(p, s[x]));
           }
         }
       }
@@ -222,7 +298,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeArgs A, c
       *reinterpret_cast<uint4*>(dst + c0) = x0;
       *reinterpret_cast<uint4*>(dst + c1) = x1;
     }
-    u = nu;
+    t = nt;
+    h = nh;
     x0 = y0;
     x1 = y1;
   }
@@ -311,9 +388,12 @@ msa_status norm_rope(const msa_shape& s, const int32_t* cu, int32_t n_seqs, cons
   a.vo = static_cast<__nv_bfloat16*>(v);
   a.err = device_error_word();
   if (!a.err) return MSA_ERR_CUDA;
-  // one token per CTA while there are few (latency), more when they fill the GPU several times over
-  int64_t per = tokens / (152 * 8);
-  a.per_cta = (int)(per < 1 ? 1 : per > kMaxTokens ? kMaxTokens : per);
+  // few tokens per CTA while there are few (latency; but heads for every lane), more when they fill the GPU several
+  // times over
+  const int64_t heads = s.Hq + s.Hkv * (v_in ? 2 : 1), lanes = kThreads / (s.d_h / 16);
+  int64_t per = tokens / (152 * kPerSm);
+  if (per < lanes / heads) per = lanes / heads;
+  a.per_cta = (int)(per < 1 ? 1 : per > kMost ? kMost : per);
   for (int s0 = 0; s0 < (cu ? n_seqs : 1); s0 += kMaxBatch) {
     a.tok0 = 0;
     a.tok1 = (int32_t)tokens;
