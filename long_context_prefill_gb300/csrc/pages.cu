@@ -27,7 +27,7 @@ msa_status check_page_geometry(int32_t num_pages, int32_t page_size);
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kMaxRequests = 8192;  // four int32 per request in shared memory
+constexpr int kMaxRequests = 8192;  // five int32 per request in shared memory
 constexpr int kMaxCtas = 152;
 
 struct PageArgs {
@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const PageArgs A) 
   int32_t* s_gr = sm + (A.S + 1);    // pages granted before
   int32_t* s_rel = s_gr + (A.S + 1); // pages released before
   int32_t* s_len = s_rel + (A.S + 1);  // length after the call
+  int32_t* s_old = s_len + (A.S + 1);  // and before
 
   const int tid = threadIdx.x, up = (1 << A.shift) - 1;
   const int most = A.max_pages << A.shift;
@@ -102,9 +103,7 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const PageArgs A) 
   // ---- what every request asks for, and who is served
   const int per = (A.S + kThreads - 1) / kThreads, s0 = min(A.S, tid * per), s1 = min(A.S, s0 + per);
   const bool tokens = A.slots != nullptr;
-  auto ask = [&](int s, int& old, int& len) -> Sum3 {
-    old = A.seq_len[s];
-    len = A.new_len[s];
+  auto ask = [&](int old, int& len) -> Sum3 {
     Sum3 v = {0, 0, 0};
     if (!sane || len < 0 || len > most || old < 0 || old > most || (tokens && A.T && len - old > A.T)) {
       len = -1;
@@ -116,12 +115,16 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const PageArgs A) 
   };
   Sum3 mine = {0, 0, 0}, all;
   for (int s = s0; s < s1; ++s) {
-    int old, len;
-    const Sum3 v = ask(s, old, len);
+    const int old = A.seq_len[s];
+    int len = A.new_len[s];
+    const Sum3 v = ask(old, len);
     if (len < 0) atomicCAS(A.err, 0, (int)kErrIndex);
+    s_old[s] = old;
+    s_len[s] = len;
     mine.tok += v.tok; mine.grow += v.grow; mine.rel += v.rel;
   }
   Sum3 run = block_exclusive(mine, part, all);
+  const Sum3 start = run;
   // a pool whose tables and stack hold more pages than it has is left as it is
   const int64_t avail = count + all.rel;
   const bool fits = sane && avail <= A.N;
@@ -130,8 +133,9 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const PageArgs A) 
   mine = {0, 0, 0};
   int refused = 0;
   for (int s = s0; s < s1; ++s) {
-    int old, len;
-    const Sum3 v = ask(s, old, len);
+    const int old = s_old[s];
+    int len = s_len[s];
+    const Sum3 v = ask(old, len);
     run.tok += v.tok; run.grow += v.grow;
     const bool ok = fits && len >= 0 && (v.grow == 0 || run.grow <= avail) &&
                     (!tokens || A.T || v.tok == 0 || run.tok <= A.cap);
@@ -142,11 +146,12 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const PageArgs A) 
     else ++refused;
   }
   if (refused) atomicAdd(&s_refused, refused);
-  Sum3 fin;
-  run = block_exclusive(mine, part, fin);
+  Sum3 fin = all;
+  if (__syncthreads_or(refused)) run = block_exclusive(mine, part, fin);  // without the refused ones
+  else run = start;
   const int G = (int)fin.grow;
   for (int s = s0; s < s1; ++s) {
-    const int old = A.seq_len[s], len = s_len[s];
+    const int old = s_old[s], len = s_len[s];
     s_tok[s] = (int)run.tok;
     s_gr[s] = (int)run.grow;
     if (len > old) { run.tok += len - old; run.grow += pages(len) - pages(old); }
@@ -166,40 +171,71 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const PageArgs A) 
   };
   auto granted = [&](int g) { return checked(g < R ? released(g) : A.stack[count - 1 - (g - R)]); };
 
-  // ---- granted pages into the table, released ones that stay free onto the stack
-  for (int g = gtid; g < G; g += gsize) {
-    const int s = find(s_gr, A.S, g);
-    A.table[(int64_t)s * A.max_pages + pages(A.seq_len[s]) + (g - s_gr[s])] = granted(g);
+  // ---- granted pages into the table, released ones that stay free onto the stack: four a thread, loads first
+  for (int g0 = 4 * gtid; g0 < G; g0 += 4 * gsize) {
+    int page[4], s = find(s_gr, A.S, g0);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) page[x] = g0 + x < G ? granted(g0 + x) : 0;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (g0 + x >= G) break;
+      while (s + 1 < A.S && s_gr[s + 1] <= g0 + x) ++s;
+      A.table[(int64_t)s * A.max_pages + pages(s_old[s]) + (g0 + x - s_gr[s])] = page[x];
+    }
   }
-  for (int r = G + gtid; r < R; r += gsize) {
-    A.stack[count + R - 1 - r] = checked(released(r));  // below N: count + R <= N
+  for (int r0 = G + 4 * gtid; r0 < R; r0 += 4 * gsize) {
+    int page[4], s = find(s_rel, A.S, r0);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      page[x] = 0;
+      if (r0 + x >= R) continue;
+      while (s + 1 < A.S && s_rel[s + 1] <= r0 + x) ++s;
+      page[x] = A.table[(int64_t)s * A.max_pages + pages(s_len[s]) + (r0 + x - s_rel[s])];
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (r0 + x < R) A.stack[count + R - 1 - (r0 + x)] = checked(page[x]);  // below N: count + R <= N
   }
   // ---- slots and positions of the new tokens
   if (A.cu)
     for (int s = gtid; s <= A.S; s += gsize) A.cu[s] = s_tok[s];
   if (tokens) {
+    // four tokens a thread: one search, a page entry for each page they touch, 16-byte stores
     const int total = A.T ? A.S * A.T : A.cap;
-    for (int t = gtid; t < total; t += gsize) {
-      int s, i;
-      bool live;
-      if (A.T) {
-        s = t / A.T;
-        i = t - s * A.T;
-        live = i < s_tok[s + 1] - s_tok[s];
-      } else {
-        live = t < s_tok[A.S];
-        s = live ? find(s_tok, A.S, t) : 0;
-        i = t - s_tok[s];
+    for (int t0 = 4 * gtid; t0 < total; t0 += 4 * gsize) {
+      int slot[4], pos[4];
+      int s = A.T ? t0 / A.T : t0 < s_tok[A.S] ? find(s_tok, A.S, t0) : A.S;
+      int i = s < A.S ? t0 - (A.T ? s * A.T : s_tok[s]) : 0;
+      int held = -1, page = -1;  // page index and page of the token before, if it was of the same request
+#pragma unroll
+      for (int x = 0; x < 4; ++x, ++i) {
+        slot[x] = pos[x] = -1;
+        // (requests without tokens are passed over in the packed form)
+        while (s < A.S && i >= (A.T ? A.T : s_tok[s + 1] - s_tok[s])) {
+          i = 0;
+          ++s;
+          held = -1;
+        }
+        if (s >= A.S || t0 + x >= total || (A.T && i >= s_tok[s + 1] - s_tok[s])) continue;
+        const int old = s_old[s], at = old + i, p = at >> A.shift, po = pages(old);
+        if (p != held) {
+          page = p < po ? checked(A.table[(int64_t)s * A.max_pages + p]) : granted(s_gr[s] + p - po);
+          held = p;
+        }
+        if (page >= 0) slot[x] = (page << A.shift) + (at & up);
+        pos[x] = old + (A.depth ? A.depth[t0 + x] : i);
       }
-      int slot = -1, pos = -1;
-      if (live) {
-        const int old = A.seq_len[s], at = old + i, p = at >> A.shift, po = pages(old);
-        const int page = p < po ? checked(A.table[(int64_t)s * A.max_pages + p]) : granted(s_gr[s] + p - po);
-        if (page >= 0) slot = (page << A.shift) + (at & up);
-        pos = old + (A.depth ? A.depth[t] : i);
-      }
-      A.slots[t] = slot;
-      if (A.pos) A.pos[t] = pos;
+      auto store = [&](int32_t* to, const int (&v)[4]) {
+        if (t0 + 4 <= total && (reinterpret_cast<uintptr_t>(to) & 15) == 0) {
+          *reinterpret_cast<int4*>(to + t0) = make_int4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (t0 + x < total) to[t0 + x] = v[x];
+        }
+      };
+      store(A.slots, slot);
+      if (A.pos) store(A.pos, pos);
     }
   }
 
@@ -274,12 +310,15 @@ extern "C" msa_status msa_build_page_tables(const msa_page_pool* pool, const int
   a.pos = positions;
   a.err = device_error_word();
   if (!a.err) return MSA_ERR_CUDA;
-  // pages that may move are not known here: at most the tables hold, or the pool
-  const int64_t moved = (int64_t)a.S * a.max_pages < a.N ? (int64_t)a.S * a.max_pages : a.N;
+  // How many pages move is not known here.  A call with tokens takes about what those need; one without mostly gives
+  // back: at most what the tables hold, or the pool.  Four a thread and round, one CTA (and no ticket) where it can do.
   const int64_t tok = !slots ? 0 : seq_tokens ? (int64_t)a.S * seq_tokens : tok_cap;
-  const int64_t want = ((tok > moved ? tok : moved) + 4 * kThreads - 1) / (4 * kThreads);
-  const int grid = (int)(want < 1 ? 1 : want > kMaxCtas ? kMaxCtas : want);
-  const int smem = 4 * (a.S + 1) * (int)sizeof(int32_t);
+  const int64_t held = (int64_t)a.S * a.max_pages < a.N ? (int64_t)a.S * a.max_pages : a.N;
+  const int64_t moved = slots ? tok / pool->page_size + a.S : held;
+  const int64_t want = (tok / 4 + moved / 4 + kThreads - 1) / kThreads;
+  const int most = slots ? kMaxCtas : 24;  // every CTA scans all requests: more of them cost more than they move
+  const int grid = (int)(want < 1 ? 1 : want > most ? most : want);
+  const int smem = 5 * (a.S + 1) * (int)sizeof(int32_t);
   if (smem > 48 * 1024 && cudaFuncSetAttribute(page_table_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
                               cudaSuccess)
     return MSA_ERR_CUDA;
