@@ -642,31 +642,51 @@ def captured_mass(lse_sparse, lse_dense, stream=None):
 
 
 # ----------------------------------------------------------------- paged KV cache
-def _launch(device, stream, body):
-    """body(raw stream) with `device` current, on `stream` (None: the device's
-    current one); what body allocates belongs to that stream."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return body(torch.cuda.current_stream(device).cuda_stream)
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream: on {stream.device}, expected {device}")
-    with torch.cuda.device(device), torch.cuda.stream(stream):
-        return body(torch.cuda.current_stream(device).cuda_stream)
+# These run once per decode step: their checks take a fast path (one test per
+# tensor) and call _want only to name what is wrong.
+def _elsewhere(device, stream) -> bool:
+    """The call is not for the current stream of the current device."""
+    return stream is not None or device.index != torch._C._cuda_getDevice()
+
+
+class _on:
+    """`device` current, on `stream` (None: the device's current one); what is allocated inside belongs to that stream."""
+
+    def __init__(self, device, stream):
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream: on {stream.device}, expected {device}")
+        self.device, self.stream = torch.cuda.device(device), torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self.device.__enter__()
+        self.stream.__enter__()
+
+    def __exit__(self, *exc):
+        self.stream.__exit__(*exc)
+        self.device.__exit__(*exc)
+
+
+def _same(t, what, dtype, shape, device):
+    """_want for a tensor that is mostly right."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        if t is None:
+            raise ValueError(f"{what}: a torch.Tensor is required")
+        _want(t, what, dtype, shape, device=device)
 
 
 def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _pages(k_pages, v_pages, Hkv=None, d=None, device=None):
-    """Check the two page tensors [num_pages, Hkv, page_size, d]; returns their C view."""
+def _pages(k_pages, v_pages, Hkv, d, device):
+    """Check the two page tensors [num_pages, Hkv, page_size, d] (Hkv None: any); returns their C view."""
     if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
         raise ValueError("k_pages: a 4-d tensor [num_pages, Hkv, page_size, d] is required")
-    N, H, P, dd = k_pages.shape
-    want = (N, H if Hkv is None else Hkv, P, dd if d is None else d)
-    _want(k_pages, "k_pages", torch.bfloat16, want, device=device)
-    if v_pages is None:
-        raise ValueError("v_pages: a torch.Tensor is required")
-    _want(v_pages, "v_pages", torch.bfloat16, want, device=k_pages.device)
+    N, H, P, _ = k_pages.shape
+    want = (N, H if Hkv is None else Hkv, P, d)
+    _same(k_pages, "k_pages", torch.bfloat16, want, device)
+    _same(v_pages, "v_pages", torch.bfloat16, want, device)
     return KVPagesC(k_pages.data_ptr(), v_pages.data_ptr(), N, P)
 
 
@@ -683,11 +703,9 @@ class PagePool:
         S, width = page_table.shape
         dev = page_table.device
         _want(page_table, "page_table", torch.int32)
-        for t, what, shape in ((seq_len, "seq_len", (S,)), (free_pages, "free_pages", tuple(free_pages.shape)),
-                               (state, "state", (4,))):
-            if t is None:
-                raise ValueError(f"{what}: a torch.Tensor is required")
-            _want(t, what, torch.int32, shape, device=dev)
+        _same(seq_len, "seq_len", torch.int32, (S,), dev)
+        _want(free_pages, "free_pages", torch.int32, device=dev)
+        _same(state, "state", torch.int32, (4,), dev)
         self.page_table, self.seq_len, self.free_pages, self.state = page_table, seq_len, free_pages, state
         self.page_size = int(page_size)
         self._c = PagePoolC(S, free_pages.shape[0], self.page_size, width, page_table.data_ptr(), seq_len.data_ptr(),
@@ -710,35 +728,39 @@ def build_page_tables(pool: PagePool, new_len, seq_tokens: int = 0, tok_cap: int
     [n_seqs * T] padded, with tok_cap [tok_cap] packed token outputs, with
     neither None (a call that only resizes)."""
     S, dev = pool._c.n_seqs, pool.page_table.device
-    if new_len is None:
-        raise ValueError("new_len: a torch.Tensor is required")
-    _want(new_len, "new_len", torch.int32, (S,), device=dev)
-    seq_tokens, tok_cap = int(seq_tokens), int(tok_cap)
+    _same(new_len, "new_len", torch.int32, (S,), dev)
     if seq_tokens < 0 or tok_cap < 0:
         raise ValueError("seq_tokens, tok_cap: must not be negative")
     total = S * seq_tokens if seq_tokens else tok_cap
     if not total and not (slots is None and positions is None and depth is None):
         raise ValueError("slots, positions, depth: need seq_tokens or tok_cap")
-    if depth is not None and depth.numel() != total:
-        raise ValueError(f"depth: {depth.numel()} elements, expected {total}")
-    _want(depth, "depth", torch.int32, device=dev)
-    _want(cu_new, "cu_new", torch.int32, (S + 1,), device=dev)
-    _want(slots, "slots", torch.int32, (total,), device=dev)
-    _want(positions, "positions", torch.int32, (total,), device=dev)
+    if depth is not None:
+        if depth.numel() != total:
+            raise ValueError(f"depth: {depth.numel()} elements, expected {total}")
+        _want(depth, "depth", torch.int32, device=dev)
+    if cu_new is not None:
+        _same(cu_new, "cu_new", torch.int32, (S + 1,), dev)
+    if slots is not None:
+        _same(slots, "slots", torch.int32, (total,), dev)
+    if positions is not None:
+        _same(positions, "positions", torch.int32, (total,), dev)
     _cuda(page_table=pool.page_table)
-    lib = load()
-
-    def body(s):
-        cu = torch.empty(S + 1, dtype=torch.int32, device=dev) if cu_new is None else cu_new
-        sl, ps = slots, positions
-        if total:
-            sl = torch.empty(total, dtype=torch.int32, device=dev) if sl is None else sl
-            ps = torch.empty(total, dtype=torch.int32, device=dev) if ps is None else ps
-        _check(lib.msa_build_page_tables(ctypes.byref(pool._c), new_len.data_ptr(), _at(depth), seq_tokens, tok_cap,
-                                         cu.data_ptr(), _at(sl), _at(ps), s), "msa_build_page_tables")
-        return cu, sl, ps
-
-    return _launch(dev, stream, body)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return build_page_tables(pool, new_len, seq_tokens, tok_cap, depth, cu_new, slots, positions)
+    if cu_new is None:
+        cu_new = torch.empty(S + 1, dtype=torch.int32, device=dev)
+    if total:
+        if slots is None:
+            slots = torch.empty(total, dtype=torch.int32, device=dev)
+        if positions is None:
+            positions = torch.empty(total, dtype=torch.int32, device=dev)
+    st = load().msa_build_page_tables(ctypes.byref(pool._c), new_len.data_ptr(), _at(depth), int(seq_tokens),
+                                      int(tok_cap), cu_new.data_ptr(), _at(slots), _at(positions),
+                                      torch._C._cuda_getCurrentRawStream(dev.index))
+    if st:
+        raise MsaError(st, "msa_build_page_tables")
+    return cu_new, slots, positions
 
 
 class RopeCfg:
@@ -748,8 +770,10 @@ class RopeCfg:
         self.c, self.q_weight, self.k_weight, self.inv_freq = c, q_weight, k_weight, inv_freq
 
     def check(self, d, device):
-        _want(self.q_weight, "q_weight", torch.bfloat16, (d,), device=device)
-        _want(self.k_weight, "k_weight", torch.bfloat16, (d,), device=device)
+        if self.q_weight is not None:
+            _same(self.q_weight, "q_weight", torch.bfloat16, (d,), device)
+        if self.k_weight is not None:
+            _same(self.k_weight, "k_weight", torch.bfloat16, (d,), device)
 
 
 def rope_cfg(rot_dim: int, theta: float = 10000.0, interleaved: bool = False, norm: bool = False, eps: float = 1e-6,
@@ -768,71 +792,56 @@ def rope_cfg(rot_dim: int, theta: float = 10000.0, interleaved: bool = False, no
     return RopeCfg(c, q_weight, k_weight, arr)
 
 
-def _token_rows(t, what, lead, device):
+def _token_rows(t, what, lead, heads, device):
     """Token stride (elements) of a token-major tensor [*lead, H, d] whose heads are contiguous within a token."""
-    if t.dtype != torch.bfloat16:
+    if not isinstance(t, torch.Tensor) or t.dim() != len(lead) + 2:
+        raise ValueError(f"{what}: a {len(lead) + 2}-d tensor [..., H, d] is required")
+    if t.dtype is not torch.bfloat16:
         raise ValueError(f"{what}: dtype {t.dtype}, expected {torch.bfloat16}")
-    if tuple(t.shape[:-2]) != tuple(lead):
-        raise ValueError(f"{what}: leading dimensions {tuple(t.shape[:-2])}, expected {tuple(lead)}")
-    if device is not None and t.device != device:
+    shape = t.shape
+    if shape[:-2] != lead:
+        raise ValueError(f"{what}: leading dimensions {tuple(shape[:-2])}, expected {tuple(lead)}")
+    if shape[-2:] != heads:
+        raise ValueError(f"{what}: heads {tuple(shape[-2:])}, expected {heads}")
+    if t.device != device:
         raise ValueError(f"{what}: on {t.device}, expected {device}")
-    H, d = t.shape[-2:]
+    H, d = heads
     st = t.stride()
     if (d > 1 and st[-1] != 1) or (H > 1 and st[-2] != d):
         raise ValueError(f"{what}: the heads of a token must be contiguous")
-    step, size = H * d, 1  # tokens must lie at one stride through every leading dimension
-    found = None
-    for n, s in zip(reversed(t.shape[:-2]), reversed(st[:-2])):
-        if n > 1:
-            if found is None:
-                found = s
-            elif s != found * size:
-                raise ValueError(f"{what}: tokens must lie at one stride")
-            size *= n
-    return step if found is None else found
+    if len(lead) == 1:
+        return st[0] if lead[0] > 1 else H * d
+    B, n = lead
+    if B > 1 and n > 1 and st[0] != n * st[1]:
+        raise ValueError(f"{what}: tokens must lie at one stride")
+    return st[1] if n > 1 else st[0] if B > 1 else H * d
 
 
-def _norm_rope(call, name, lead, out_shape, dims, q_in, k_in, v_in, cfg, positions, q, k, v, k_pages, v_pages, slots,
-               layer_kv, stream):
+def _rope_args(lead, out, dims, q_in, k_in, v_in, cfg, positions, q, k, v, k_pages, v_pages, slots):
+    """Check everything; returns (token strides of q_in, k_in and v_in, C view of the pages or None)."""
     Hq, Hkv, d = dims
     dev = q_in.device
-    tokens = 1
-    for x in lead:
-        tokens *= int(x)
-    qs, ks = _token_rows(q_in, "q_in", lead, None), _token_rows(k_in, "k_in", lead, dev)
-    if tuple(k_in.shape[-2:]) != (Hkv, d):
-        raise ValueError(f"k_in: heads {tuple(k_in.shape[-2:])}, expected {(Hkv, d)}")
-    vs = 0
-    if v_in is not None:
-        vs = _token_rows(v_in, "v_in", lead, dev)
-        if tuple(v_in.shape[-2:]) != (Hkv, d):
-            raise ValueError(f"v_in: heads {tuple(v_in.shape[-2:])}, expected {(Hkv, d)}")
+    qs = _token_rows(q_in, "q_in", lead, (Hq, d), dev)
+    ks = _token_rows(k_in, "k_in", lead, (Hkv, d), dev)
+    vs = 0 if v_in is None else _token_rows(v_in, "v_in", lead, (Hkv, d), dev)
     cfg.check(d, dev)
     pages = None if k_pages is None else _pages(k_pages, v_pages, Hkv, d, dev)
-    if positions is not None and positions.numel() != tokens:
-        raise ValueError(f"positions: {positions.numel()} elements, expected {tokens}")
-    if slots is not None and slots.numel() != tokens:
-        raise ValueError(f"slots: {slots.numel()} elements, expected {tokens}")
-    _want(positions, "positions", torch.int32, device=dev)
-    _want(slots, "slots", torch.int32, device=dev)
-    _want(q, "q", torch.bfloat16, out_shape(Hq), device=dev)
-    _want(k, "k", torch.bfloat16, out_shape(Hkv), device=dev)
-    _want(v, "v", torch.bfloat16, out_shape(Hkv), device=dev)
+    if positions is not None or slots is not None:
+        tokens = lead[0] if len(lead) == 1 else lead[0] * lead[1]
+        for t, what in ((positions, "positions"), (slots, "slots")):
+            if t is not None and not (t.dtype is torch.int32 and t.numel() == tokens and t.device == dev
+                                      and t.is_contiguous()):
+                if t.numel() != tokens:
+                    raise ValueError(f"{what}: {t.numel()} elements, expected {tokens}")
+                _want(t, what, torch.int32, device=dev)
+    if q is not None:
+        _same(q, "q", torch.bfloat16, out[0], dev)
+    if k is not None:
+        _same(k, "k", torch.bfloat16, out[1], dev)
+    if v is not None:
+        _same(v, "v", torch.bfloat16, out[1], dev)
     _cuda(q_in=q_in)
-
-    def body(s):
-        def new(H):
-            return torch.empty(out_shape(H), dtype=torch.bfloat16, device=dev)
-
-        qo = new(Hq) if q is None else q
-        ko = new(Hkv) if k is None and layer_kv else k
-        vo = new(Hkv) if v is None and layer_kv and v_in is not None else v
-        _check(call(ctypes.byref(cfg.c), q_in.data_ptr(), qs, k_in.data_ptr(), ks, _at(v_in), vs, _at(positions),
-                    qo.data_ptr(), _at(ko), _at(vo), None if pages is None else ctypes.byref(pages), _at(slots), s),
-               name)
-        return qo, ko, vo
-
-    return _launch(dev, stream, body)
+    return qs, ks, vs, pages
 
 
 def qk_norm_rope(q_in, k_in, v_in, cfg: RopeCfg, positions=None, q=None, k=None, v=None, k_pages=None, v_pages=None,
@@ -845,12 +854,27 @@ def qk_norm_rope(q_in, k_in, v_in, cfg: RopeCfg, positions=None, q=None, k=None,
         if not isinstance(t, torch.Tensor) or t.dim() != 4:
             raise ValueError(f"{what}: a 4-d tensor [B, n, H, d] is required")
     B, n, Hq, d = q_in.shape
-    Hkv = k_in.shape[2]
-    sh = Shape(B, Hq, Hkv, n, d, 0.0)
-    lib = load()
-    return _norm_rope(lambda *a: lib.msa_qk_norm_rope(ctypes.byref(sh), *a), "msa_qk_norm_rope", (B, n),
-                      lambda H: (B, H, n, d), (Hq, Hkv, d), q_in, k_in, v_in, cfg, positions, q, k, v, k_pages,
-                      v_pages, slots, layer_kv, stream)
+    Hkv, dev = k_in.shape[2], q_in.device
+    kv = (B, Hkv, n, d)
+    qs, ks, vs, pages = _rope_args((B, n), ((B, Hq, n, d), kv), (Hq, Hkv, d), q_in, k_in, v_in, cfg, positions, q, k, v,
+                                   k_pages, v_pages, slots)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return qk_norm_rope(q_in, k_in, v_in, cfg, positions, q, k, v, k_pages, v_pages, slots, layer_kv)
+    if q is None:
+        q = torch.empty((B, Hq, n, d), dtype=torch.bfloat16, device=dev)
+    if layer_kv:
+        if k is None:
+            k = torch.empty(kv, dtype=torch.bfloat16, device=dev)
+        if v is None and v_in is not None:
+            v = torch.empty(kv, dtype=torch.bfloat16, device=dev)
+    st = load().msa_qk_norm_rope(ctypes.byref(Shape(B, Hq, Hkv, n, d, 0.0)), ctypes.byref(cfg.c), q_in.data_ptr(), qs,
+                                 k_in.data_ptr(), ks, _at(v_in), vs, _at(positions), q.data_ptr(), _at(k), _at(v),
+                                 None if pages is None else ctypes.byref(pages), _at(slots),
+                                 torch._C._cuda_getCurrentRawStream(dev.index))
+    if st:
+        raise MsaError(st, "msa_qk_norm_rope")
+    return q, k, v
 
 
 def qk_norm_rope_varlen(q_in, k_in, v_in, cu_seqlens, cfg: RopeCfg, positions=None, q=None, k=None, v=None,
@@ -863,15 +887,30 @@ def qk_norm_rope_varlen(q_in, k_in, v_in, cu_seqlens, cfg: RopeCfg, positions=No
             raise ValueError(f"{what}: a 3-d tensor [tokens, H, d] is required")
     cu = [int(x) for x in cu_seqlens]
     tokens, Hq, d = q_in.shape
-    Hkv = k_in.shape[1]
+    Hkv, dev = k_in.shape[1], q_in.device
     if len(cu) < 2 or cu[-1] != tokens:
         raise ValueError(f"cu_seqlens: must end at the {tokens} tokens of q_in")
-    arr = (ctypes.c_int32 * len(cu))(*cu)
-    sh = Shape(1, Hq, Hkv, 1, d, 0.0)
-    lib = load()
-    return _norm_rope(lambda *a: lib.msa_qk_norm_rope_varlen(ctypes.byref(sh), arr, len(cu) - 1, *a),
-                      "msa_qk_norm_rope_varlen", (tokens,), lambda H: (tokens * H * d,), (Hq, Hkv, d), q_in, k_in,
-                      v_in, cfg, positions, q, k, v, k_pages, v_pages, slots, layer_kv, stream)
+    qn, kn = tokens * Hq * d, tokens * Hkv * d
+    qs, ks, vs, pages = _rope_args((tokens,), ((qn,), (kn,)), (Hq, Hkv, d), q_in, k_in, v_in, cfg, positions, q, k, v,
+                                   k_pages, v_pages, slots)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return qk_norm_rope_varlen(q_in, k_in, v_in, cu, cfg, positions, q, k, v, k_pages, v_pages, slots, layer_kv)
+    if q is None:
+        q = torch.empty(qn, dtype=torch.bfloat16, device=dev)
+    if layer_kv:
+        if k is None:
+            k = torch.empty(kn, dtype=torch.bfloat16, device=dev)
+        if v is None and v_in is not None:
+            v = torch.empty(kn, dtype=torch.bfloat16, device=dev)
+    st = load().msa_qk_norm_rope_varlen(ctypes.byref(Shape(1, Hq, Hkv, 1, d, 0.0)), (ctypes.c_int32 * len(cu))(*cu),
+                                        len(cu) - 1, ctypes.byref(cfg.c), q_in.data_ptr(), qs, k_in.data_ptr(), ks,
+                                        _at(v_in), vs, _at(positions), q.data_ptr(), _at(k), _at(v),
+                                        None if pages is None else ctypes.byref(pages), _at(slots),
+                                        torch._C._cuda_getCurrentRawStream(dev.index))
+    if st:
+        raise MsaError(st, "msa_qk_norm_rope_varlen")
+    return q, k, v
 
 
 def attn_tree(q, k_pages, v_pages, page_table, seq_len, tree_len=None, tree_mask=None, o=None, lse=None, scale=None,
@@ -890,35 +929,38 @@ def attn_tree(q, k_pages, v_pages, page_table, seq_len, tree_len=None, tree_mask
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table: a 2-d tensor [B, max_pages] is required")
     width = page_table.shape[1]
-    words = (n + 31) // 32
-    _want(page_table, "page_table", torch.int32, (B, width), device=dev)
-    if seq_len is None:
-        raise ValueError("seq_len: a torch.Tensor is required")
-    _want(seq_len, "seq_len", torch.int32, (B,), device=dev)
-    _want(tree_len, "tree_len", torch.int32, (B,), device=dev)
+    _same(page_table, "page_table", torch.int32, (B, width), dev)
+    _same(seq_len, "seq_len", torch.int32, (B,), dev)
+    if tree_len is not None:
+        _same(tree_len, "tree_len", torch.int32, (B,), dev)
     stride = 0
     if tree_mask is not None:
+        words = (n + 31) // 32
         shared = tree_mask.dim() == 2
-        _want(tree_mask, "tree_mask", torch.int32, (n, words) if shared else (B, n, words), device=dev)
+        _same(tree_mask, "tree_mask", torch.int32, (n, words) if shared else (B, n, words), dev)
         stride = 0 if shared else n * words
-    _want(o, "o", torch.bfloat16, (B, Hq, n, d), device=dev)
-    _want(lse, "lse", torch.float32, (B, Hq, n), device=dev)
-    _want(ws, "ws", torch.uint8, device=dev)
+    if o is not None:
+        _same(o, "o", torch.bfloat16, (B, Hq, n, d), dev)
+    if lse is not None:
+        _same(lse, "lse", torch.float32, (B, Hq, n), dev)
+    if ws is not None:
+        _want(ws, "ws", torch.uint8, device=dev)
     _cuda(q=q)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return attn_tree(q, k_pages, v_pages, page_table, seq_len, tree_len, tree_mask, o, lse, scale, ws)
     lib = load()
-    sh = Shape(B, Hq, k_pages.shape[1], n, d, float(scale) if scale else 0.0)
-
-    def body(s):
-        out = torch.empty_like(q) if o is None else o
-        w = ws
-        if w is None:
-            w = torch.empty(max(int(lib.msa_attn_tree_workspace(ctypes.byref(sh))), 1), dtype=torch.uint8, device=dev)
-        _check(lib.msa_attn_tree(ctypes.byref(sh), q.data_ptr(), ctypes.byref(pages), page_table.data_ptr(), width,
-                                 seq_len.data_ptr(), _at(tree_len), _at(tree_mask), stride, out.data_ptr(), _at(lse),
-                                 w.data_ptr(), w.numel(), s), "msa_attn_tree")
-        return out
-
-    return _launch(dev, stream, body)
+    sh = ctypes.byref(Shape(B, Hq, k_pages.shape[1], n, d, float(scale) if scale else 0.0))
+    if o is None:
+        o = torch.empty_like(q)
+    if ws is None:
+        ws = torch.empty(lib.msa_attn_tree_workspace(sh) or 1, dtype=torch.uint8, device=dev)
+    st = lib.msa_attn_tree(sh, q.data_ptr(), ctypes.byref(pages), page_table.data_ptr(), width, seq_len.data_ptr(),
+                           _at(tree_len), _at(tree_mask), stride, o.data_ptr(), _at(lse), ws.data_ptr(), ws.numel(),
+                           torch._C._cuda_getCurrentRawStream(dev.index))
+    if st:
+        raise MsaError(st, "msa_attn_tree")
+    return o
 
 
 def attn_tree_workspace(B, Hq, Hkv, n, d) -> int:
