@@ -44,7 +44,20 @@
 //          chains side by side do not;
 //   kMany  up to 128 rows: the same with all lanes and one Q buffer a group;
 //   kTwo   above: one part per CTA, group X owns rows 128 X .. of the 256-row
-//          block, and both use every tile.
+//          block, and both use every tile.  One warp issues the scores of both,
+//          one the products with V; the scores of a group go to one shared TMEM
+//          tile that is free again once they are in its registers, so a group's
+//          next scores do not wait for its product with V.
+//
+// Measured (captured, 40 heads of 128 as 32 / 8): decode of 64 requests of 1K to
+// 16K tokens 192 us (6.6 TB/s, 0.98 of the measured copy rate), a million-token
+// context with 5 drafted tokens 593 us (7.2 TB/s), 128K with a tree of 32 (128
+// rows) 94 us (0.84 of the floor), 16 trees of up to 48 (192 rows) over 4K to
+// 32K 174 us (0.69: the two groups' softmax takes 1900 cycles of a scheduler's
+// 3040 a tile, and the products with Q read 8 KB of shared memory per 64 cycles,
+// its whole rate, beside the loads that land there).  Tried and slower there: a
+// score tile per group with P over it 194 us, turns of the groups on a scheduler
+// 192 to 253 us, scores by halves of 64 keys 208 us.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <string.h>
@@ -889,17 +902,7 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
             *part = make_float4(ov[4 * x], ov[4 * x + 1], ov[4 * x + 2], ov[4 * x + 3]);
         }
       };
-      if constexpr (kPair) {
-        float ov[D];
-        // every warp loads, with rows or not: values defined on one path only would stay live around the loop
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) tmem_ld32(tO + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(ov + 32 * c));
-        tmem_ld_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kBarOFree + X]);
-        write(ov, 0, std::integral_constant<int, D>());
-      } else if (joins) {
+      if (joins) {
 #pragma unroll 1
         for (int c = X * (D / 2); c < (X + 1) * (D / 2); c += 32) {
           float ov[32], q[32];

@@ -204,19 +204,36 @@ def test_rows_without_keys_and_shared_mask(cuda_lib, n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("Hq,Hkv,n", [(4, 1, 1), (4, 1, 17), (4, 1, 50), (6, 2, 100)])
-def test_long_contexts_are_cut_and_joined(cuda_lib, Hq, Hkv, n):
+def test_long_contexts_are_cut_and_joined(cuda_lib, Hq, Hkv, n, d):
     """One long request cut over all CTAs beside short ones; the same bits on every run."""
     rng = np.random.default_rng(n)
     lens = [60001, 5, 4097, 130]
     tls = [n, min(n, 5), max(1, n // 3), n]
     masks = np.stack([tree_bits(rng, n) for _ in lens])
-    c = Case(Hq, Hkv, n, 128, 64, lens, 40 + n, tls=tls, masks=masks, peak=6.0)
+    c = Case(Hq, Hkv, n, d, 64, lens, 40 + n, tls=tls, masks=masks, peak=6.0)
     out = c.run()
     assert cuda_lib.poll_device_status() == 0
     c.check(out, what="long")
     again = c.run()
     assert torch.equal(out[0], again[0]) and torch.equal(out[1], again[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("Hq,Hkv,n", [(4, 2, 1), (4, 2, 20), (4, 1, 32), (8, 2, 40)])
+def test_items_across_many_cuts(cuda_lib, Hq, Hkv, n, page):
+    """Requests of a few to a few hundred tiles, so that parts begin and end anywhere in items: single tiles, items
+    cut once, items over many parts, parts over many items; every row layout."""
+    rng = np.random.default_rng(7 * n)
+    lens = (n + np.exp(rng.uniform(0, math.log(30000), 24))).astype(int)
+    tls = rng.integers(1, n + 1, len(lens))
+    masks = np.stack([tree_bits(rng, n) for _ in lens])
+    c = Case(Hq, Hkv, n, 128, page, lens, 60 + n, tls=tls, masks=masks, peak=4.0)
+    out = c.run()
+    assert cuda_lib.poll_device_status() == 0
+    c.check(out, what="cuts")
 
 
 @pytest.mark.gpu
