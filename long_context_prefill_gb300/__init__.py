@@ -744,7 +744,8 @@ def build_page_tables(pool: PagePool, new_len, seq_tokens: int = 0, tok_cap: int
         _same(slots, "slots", torch.int32, (total,), dev)
     if positions is not None:
         _same(positions, "positions", torch.int32, (total,), dev)
-    _cuda(page_table=pool.page_table)
+    if not pool.page_table.is_cuda:
+        _cuda(page_table=pool.page_table)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return build_page_tables(pool, new_len, seq_tokens, tok_cap, depth, cu_new, slots, positions)
@@ -792,55 +793,63 @@ def rope_cfg(rot_dim: int, theta: float = 10000.0, interleaved: bool = False, no
     return RopeCfg(c, q_weight, k_weight, arr)
 
 
-def _token_rows(t, what, lead, heads, device):
+def _token_rows(t, what, lead, H, d, device):
     """Token stride (elements) of a token-major tensor [*lead, H, d] whose heads are contiguous within a token."""
-    if not isinstance(t, torch.Tensor) or t.dim() != len(lead) + 2:
-        raise ValueError(f"{what}: a {len(lead) + 2}-d tensor [..., H, d] is required")
-    if t.dtype is not torch.bfloat16:
-        raise ValueError(f"{what}: dtype {t.dtype}, expected {torch.bfloat16}")
-    shape = t.shape
-    if shape[:-2] != lead:
-        raise ValueError(f"{what}: leading dimensions {tuple(shape[:-2])}, expected {tuple(lead)}")
-    if shape[-2:] != heads:
-        raise ValueError(f"{what}: heads {tuple(shape[-2:])}, expected {heads}")
-    if t.device != device:
+    want = (*lead, H, d)
+    if not (isinstance(t, torch.Tensor) and t.shape == want and t.dtype is torch.bfloat16 and t.device == device):
+        if not isinstance(t, torch.Tensor) or t.dim() != len(want):
+            raise ValueError(f"{what}: a {len(want)}-d tensor [..., H, d] is required")
+        if t.dtype is not torch.bfloat16:
+            raise ValueError(f"{what}: dtype {t.dtype}, expected {torch.bfloat16}")
+        if t.shape[:-2] != lead:
+            raise ValueError(f"{what}: leading dimensions {tuple(t.shape[:-2])}, expected {tuple(lead)}")
+        if t.shape != want:
+            raise ValueError(f"{what}: heads {tuple(t.shape[-2:])}, expected {(H, d)}")
         raise ValueError(f"{what}: on {t.device}, expected {device}")
-    H, d = heads
     st = t.stride()
     if (d > 1 and st[-1] != 1) or (H > 1 and st[-2] != d):
         raise ValueError(f"{what}: the heads of a token must be contiguous")
     if len(lead) == 1:
         return st[0] if lead[0] > 1 else H * d
     B, n = lead
-    if B > 1 and n > 1 and st[0] != n * st[1]:
-        raise ValueError(f"{what}: tokens must lie at one stride")
-    return st[1] if n > 1 else st[0] if B > 1 else H * d
+    if n > 1:
+        if B > 1 and st[0] != n * st[1]:
+            raise ValueError(f"{what}: tokens must lie at one stride")
+        return st[1]
+    return st[0] if B > 1 else H * d
+
+
+def _per_token(t, what, tokens, device):
+    """One int32 per token, in any shape."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.numel() == tokens and t.device == device
+            and t.is_contiguous()):
+        if isinstance(t, torch.Tensor) and t.numel() != tokens:
+            raise ValueError(f"{what}: {t.numel()} elements, expected {tokens}")
+        _want(t, what, torch.int32, device=device)
 
 
 def _rope_args(lead, out, dims, q_in, k_in, v_in, cfg, positions, q, k, v, k_pages, v_pages, slots):
     """Check everything; returns (token strides of q_in, k_in and v_in, C view of the pages or None)."""
     Hq, Hkv, d = dims
     dev = q_in.device
-    qs = _token_rows(q_in, "q_in", lead, (Hq, d), dev)
-    ks = _token_rows(k_in, "k_in", lead, (Hkv, d), dev)
-    vs = 0 if v_in is None else _token_rows(v_in, "v_in", lead, (Hkv, d), dev)
+    qs = _token_rows(q_in, "q_in", lead, Hq, d, dev)
+    ks = _token_rows(k_in, "k_in", lead, Hkv, d, dev)
+    vs = 0 if v_in is None else _token_rows(v_in, "v_in", lead, Hkv, d, dev)
     cfg.check(d, dev)
     pages = None if k_pages is None else _pages(k_pages, v_pages, Hkv, d, dev)
-    if positions is not None or slots is not None:
-        tokens = lead[0] if len(lead) == 1 else lead[0] * lead[1]
-        for t, what in ((positions, "positions"), (slots, "slots")):
-            if t is not None and not (t.dtype is torch.int32 and t.numel() == tokens and t.device == dev
-                                      and t.is_contiguous()):
-                if t.numel() != tokens:
-                    raise ValueError(f"{what}: {t.numel()} elements, expected {tokens}")
-                _want(t, what, torch.int32, device=dev)
+    tokens = lead[0] if len(lead) == 1 else lead[0] * lead[1]
+    if positions is not None:
+        _per_token(positions, "positions", tokens, dev)
+    if slots is not None:
+        _per_token(slots, "slots", tokens, dev)
     if q is not None:
         _same(q, "q", torch.bfloat16, out[0], dev)
     if k is not None:
         _same(k, "k", torch.bfloat16, out[1], dev)
     if v is not None:
         _same(v, "v", torch.bfloat16, out[1], dev)
-    _cuda(q_in=q_in)
+    if not q_in.is_cuda:
+        _cuda(q_in=q_in)
     return qs, ks, vs, pages
 
 
@@ -945,7 +954,8 @@ def attn_tree(q, k_pages, v_pages, page_table, seq_len, tree_len=None, tree_mask
         _same(lse, "lse", torch.float32, (B, Hq, n), dev)
     if ws is not None:
         _want(ws, "ws", torch.uint8, device=dev)
-    _cuda(q=q)
+    if not q.is_cuda:
+        _cuda(q=q)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return attn_tree(q, k_pages, v_pages, page_table, seq_len, tree_len, tree_mask, o, lse, scale, ws)
