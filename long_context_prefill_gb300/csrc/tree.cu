@@ -947,20 +947,45 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
   }
 }
 
-// Joins the parts of the items that the line's cuts went through, in key
-// order.  Grid: (items, chunks of a block's rows x d/4 values).
-constexpr int kJoinThreads = 128;
+// Joins the parts of the items that the line's cuts went through, in a fixed
+// order.  Latency bounds it (a few parts of a few KB for each of a few items), so
+// where there is little to join, the eight warps of a CTA share an item's parts:
+// warp k takes parts k, k + 8, .. of a chunk of 32 float4 of the block's rows, four
+// parts' loads in flight, and the first joins the eight.  One request of 5000
+// tokens in 38 parts a head: 26 us with a warp per chunk, 19 us so; 16 requests
+// with trees of 48: 174 us with a warp per chunk, 234 us so, as most CTAs only find
+// out that they have nothing to do.  Grid: (items, chunks / chunks of a CTA).
+constexpr int join_warps(int share) { return share > 1 ? share : 4; }
 
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeArgs A) {
+// a / b for a >= 0, b > 0, in 32 bits where they suffice (64-bit division takes some hundred cycles)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
+struct Joined {
+  float m, l;
+  float4 o;
+};
+// x and y joined; either may be empty (m = -inf, the rest 0)
+__device__ __forceinline__ Joined join2(const Joined& x, const Joined& y) {
+  const float m = fmaxf(x.m, y.m), ref = m == -INFINITY ? 0.f : m;
+  const float a = ex2(x.m - ref), b = ex2(y.m - ref);
+  return {m, x.l * a + y.l * b,
+          make_float4(x.o.x * a + y.o.x * b, x.o.y * a + y.o.y * b, x.o.z * a + y.o.z * b, x.o.w * a + y.o.w * b)};
+}
+
+template <int D, int kShare>
+__global__ void __launch_bounds__(32 * join_warps(kShare)) tree_join_kernel(const TreeArgs A) {
+  __shared__ Joined joined[kShare][32];  // (kShare = 1: unused)
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int items = A.Hkv * A.RB;
+  const int items = A.Hkv * A.RB, lane = threadIdx.x & 31;
+  const int warp = (threadIdx.x >> 5) % kShare;  // of those that share a chunk
   const int b = (int)(blockIdx.x / items), item = (int)(blockIdx.x % items);
   const int64_t W = A.prefix[A.B], p0 = A.prefix[b], p1 = A.prefix[b + 1];
   if (p1 == p0) return;
-  const int64_t tiles = (p1 - p0) / items, s0 = p0 + item * tiles, s1 = s0 + tiles;
+  const int64_t tiles = quotient(p1 - p0, items), s0 = p0 + item * tiles, s1 = s0 + tiles;
   const int G = parts(W, A.max_parts);  // part c holds tile x: the largest c with W c / G <= x
-  const int c0 = (int)(((s0 + 1) * G - 1) / W), c1 = (int)((s1 * G - 1) / W);
+  const int c0 = (int)quotient((s0 + 1) * G - 1, W), c1 = (int)quotient(s1 * G - 1, W);
   // Its parts: c0, the ones from c0 + lead on by `step`, and c1 where those leave it out.  (kMany, all parts present:
   // an odd part that was joined in its CTA stands in the slot of the even one; only c0 and c1 can be odd and not.)
   const bool pairs = A.R > 64 && A.R <= 128 && W >= 2 * kCtas;
@@ -969,62 +994,59 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeArgs 
   const bool tail = pairs && (c1 & 1) && c1 != c0 && !joined_in_cta(true, W, 2 * kCtas, c1, s0, s1);
   const int n = 1 + inner + (tail ? 1 : 0);
   if (n == 1) return;  // one CTA finished it
-  const int rb = item % A.RB, kvh = item / A.RB;
-  const int width = min(256, A.R - 256 * rb), full = min(256, A.R);
-  const int e = blockIdx.y * kJoinThreads + threadIdx.x;
-  if (e >= width * (D / 4)) return;
-  const int c4 = e / width, rw = e - c4 * width, rr = 256 * rb + rw;
-  const int T = A.tree_len ? A.tree_len[b] : A.n;
-  if (rr % A.n >= T) return;
   auto slot = [&](int k) {  // of its k-th part; the first one starts the item
     return (int64_t)(k == 0 ? 2 * c0 + 1 : 2 * (k <= inner ? c0 + lead + step * (k - 1) : c1));
   };
-  // one pass, kAhead parts at a time: their loads are all in flight before the first is used
-  constexpr int kAhead = 8;
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int rb = item % A.RB, kvh = item / A.RB;
+  const int width = min(256, A.R - 256 * rb), full = min(256, A.R);
+  const int e = (blockIdx.y * (join_warps(kShare) / kShare) + (threadIdx.x >> 5) / kShare) * 32 + lane, c4 = e / width, rw = e - c4 * width, rr = 256 * rb + rw;
+  const bool there = e < width * (D / 4) && rr % A.n < (A.tree_len ? A.tree_len[b] : A.n);
   const float2* ml = A.part_ml + rw;
   const float4* part = A.part + (int64_t)c4 * width + rw;
-  for (int c = 0; c < n; c += kAhead) {
-    float2 x[kAhead];
-    float4 y[kAhead];
+  Joined s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  constexpr int kAhead = kShare > 1 ? 4 : 8;
+  for (int c = warp; c < n; c += kAhead * kShare) {
+    Joined x[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      x[k] = make_float2(-INFINITY, 0.f);
-      y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (c + k < n) {
-        const int64_t sl = slot(c + k);
-        x[k] = ml[sl * full];
-        y[k] = part[sl * (D / 4) * full];
+      x[k] = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+      if (there && c + k * kShare < n) {
+        const int64_t sl = slot(c + k * kShare);
+        const float2 state = ml[sl * full];
+        x[k].m = state.x;
+        x[k].l = state.y;
+        x[k].o = part[sl * (D / 4) * full];
       }
     }
-    float top = m;
+    // as join2 for all of them at once
+    float top = s.m;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) top = fmaxf(top, x[k].x);
-    const float ref = top == -INFINITY ? 0.f : top;
-    const float keep = ex2(m - ref);
-    m = top;
-    l *= keep;
-    o.x *= keep;
-    o.y *= keep;
-    o.z *= keep;
-    o.w *= keep;
+    for (int k = 0; k < kAhead; ++k) top = fmaxf(top, x[k].m);
+    const float ref = top == -INFINITY ? 0.f : top, keep = ex2(s.m - ref);
+    s = {top, s.l * keep, make_float4(s.o.x * keep, s.o.y * keep, s.o.z * keep, s.o.w * keep)};
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const float w = ex2(x[k].x - ref);
-      l += w * x[k].y;
-      o.x += w * y[k].x;
-      o.y += w * y[k].y;
-      o.z += w * y[k].z;
-      o.w += w * y[k].w;
+      const float w = ex2(x[k].m - ref);
+      s.l += w * x[k].l;
+      s.o.x += w * x[k].o.x;
+      s.o.y += w * x[k].o.y;
+      s.o.z += w * x[k].o.z;
+      s.o.w += w * x[k].o.w;
     }
   }
-  const bool some = !(l == 0.f);
-  const float inv = some ? 1.f / l : 0.f;
+  if (kShare > 1) {
+    joined[warp][lane] = s;
+    __syncthreads();
+  }
+  if (warp > 0 || !there) return;
+#pragma unroll
+  for (int k = 1; k < kShare; ++k) s = join2(s, joined[k][lane]);
+  const bool some = !(s.l == 0.f);
+  const float inv = some ? 1.f / s.l : 0.f;
   const int64_t grow = (int64_t)(b * A.Hq + kvh * (A.Hq / A.Hkv)) * A.n + rr;
   *reinterpret_cast<uint2*>(A.o + grow * D + 4 * c4) =
-      make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-  if (c4 == 0 && A.lse) A.lse[grow] = some ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+      make_uint2(pack_bf16x2(s.o.x * inv, s.o.y * inv), pack_bf16x2(s.o.z * inv, s.o.w * inv));
+  if (c4 == 0 && A.lse) A.lse[grow] = some ? (s.m + __log2f(s.l)) * 0.69314718055994531f : -INFINITY;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -1074,12 +1096,16 @@ msa_status launch_tree(const TreeMaps& maps, const TreeArgs& a, bool join, cudaS
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   const int full = a.R < 256 ? a.R : 256;
-  cfg.gridDim = dim3((unsigned)(a.B * a.Hkv * a.RB), (unsigned)ceil_div((int64_t)full * (D / 4), kJoinThreads));
-  cfg.blockDim = dim3(kJoinThreads);
+  const int64_t items = (int64_t)a.B * a.Hkv * a.RB, chunks = ceil_div((int64_t)full * (D / 4), 32);
+  const bool share = items * chunks <= 8 * kCtas;  // a CTA per chunk, all of them resident at once
+  cfg.gridDim = dim3((unsigned)items, (unsigned)(share ? chunks : ceil_div(chunks, join_warps(1))));
+  cfg.blockDim = dim3(32 * join_warps(share ? 8 : 1));
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, tree_join_kernel<D>, a) != cudaSuccess) return MSA_ERR_CUDA;
+  if ((share ? cudaLaunchKernelEx(&cfg, tree_join_kernel<D, 8>, a)
+             : cudaLaunchKernelEx(&cfg, tree_join_kernel<D, 1>, a)) != cudaSuccess)
+    return MSA_ERR_CUDA;
   note_launch();
   return MSA_OK;
 }
