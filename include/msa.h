@@ -403,8 +403,8 @@ typedef struct {
  * up to and including it exceed the free and released ones; when its new
  * tokens do not fit (below); or when a length is negative or above max_pages *
  * page_size (this also sets MSA_ERR_INDEX for the next poll, as do a page id
- * outside the pool and a pool whose tables and stack together hold more than
- * num_pages pages, of which nothing is changed).
+ * outside the pool and a pool whose free pages and those given back together
+ * are more than num_pages, of which nothing is changed).
  *
  * Token outputs (slots NULL: none).  seq_tokens = T > 0: padded, token i of
  * request s at s * T + i of [n_seqs, T] outputs, and a request that grows by more than T
@@ -415,7 +415,7 @@ typedef struct {
  *              given (a drafted tree's token sits at its depth); -1 where none
  *   cu_new     (nullable) [n_seqs + 1] new tokens of the requests before
  * new_len, depth and the outputs must not overlap the pool.  At most 8192
- * requests (else MSA_ERR_UNSUPPORTED).  Calls on one pool must be ordered. */
+ * requests and 2^31 - 2^19 token outputs (else MSA_ERR_UNSUPPORTED).  Calls on one pool must be ordered. */
 MSA_API msa_status msa_build_page_tables(const msa_page_pool* pool, const int32_t* new_len, const int32_t* depth,
                                          int32_t seq_tokens, int32_t tok_cap, int32_t* cu_new, int32_t* slots,
                                          int32_t* positions, void* stream);

@@ -29,6 +29,8 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kMaxRequests = 8192;  // five int32 per request in shared memory
 constexpr int kMaxCtas = 152;
+constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - (1 << 19);  // an index may step one round past the last token
+static_assert(4 * kMaxCtas * kThreads < 1 << 19, "indexes within int32");
 
 struct PageArgs {
   int32_t S, N, shift, max_pages, T, cap;
@@ -284,7 +286,7 @@ extern "C" msa_status msa_build_page_tables(const msa_page_pool* pool, const int
   const msa_status geo = check_page_geometry(pool->num_pages, pool->page_size);
   if (geo != MSA_OK) return geo;
   if (pool->n_seqs > kMaxRequests || (int64_t)pool->max_pages * pool->page_size >= ((int64_t)1 << 31) ||
-      (int64_t)pool->n_seqs * seq_tokens >= ((int64_t)1 << 31))
+      (int64_t)pool->n_seqs * seq_tokens >= kMaxTokens || tok_cap >= kMaxTokens)
     return MSA_ERR_UNSUPPORTED;
   if (!aligned4(pool->page_table, true) || !aligned4(pool->seq_len, true) || !aligned4(pool->free_pages, true) ||
       !aligned4(pool->state, true) || !aligned4(new_len, true) || !aligned4(depth, false) ||

@@ -74,6 +74,8 @@ def test_refusals(lib):
     assert call(new=ctypes.c_void_p(0x30000)) == inv  # the pool's own lengths
     assert call(T=-1) == inv
     assert call(cap=-1) == inv
+    assert call(slots=P, T=(1 << 29) - 1) == uns  # 2^31 - 4 token outputs
+    assert call(slots=P, cap=(1 << 31) - 1) == uns
     assert call(pos=P) == inv    # positions without slots
     assert call(depth=P) == inv
 
