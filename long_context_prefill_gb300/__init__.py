@@ -836,7 +836,7 @@ def _rope_args(lead, out, dims, q_in, k_in, v_in, cfg, positions, q, k, v, k_pag
     ks = _token_rows(k_in, "k_in", lead, Hkv, d, dev)
     vs = 0 if v_in is None else _token_rows(v_in, "v_in", lead, Hkv, d, dev)
     cfg.check(d, dev)
-    pages = None if k_pages is None else _pages(k_pages, v_pages, Hkv, d, dev)
+    pages = None if k_pages is None and v_pages is None else _pages(k_pages, v_pages, Hkv, d, dev)
     tokens = lead[0] if len(lead) == 1 else lead[0] * lead[1]
     if positions is not None:
         _per_token(positions, "positions", tokens, dev)
@@ -945,7 +945,7 @@ def attn_tree(q, k_pages, v_pages, page_table, seq_len, tree_len=None, tree_mask
     stride = 0
     if tree_mask is not None:
         words = (n + 31) // 32
-        shared = tree_mask.dim() == 2
+        shared = isinstance(tree_mask, torch.Tensor) and tree_mask.dim() == 2
         _same(tree_mask, "tree_mask", torch.int32, (n, words) if shared else (B, n, words), dev)
         stride = 0 if shared else n * words
     if o is not None:

@@ -92,6 +92,7 @@ def test_binding_refusals():
         (lambda: msa.attn_tree(q, kp, kp, table, lens, tree_len=lens.float()), "tree_len: dtype"),
         (lambda: msa.attn_tree(q, kp, kp, table, lens, tree_mask=torch.zeros(2, 2, 1, **i32)), "tree_mask: shape"),
         (lambda: msa.attn_tree(q, kp, kp, table, lens, tree_mask=torch.zeros(3, 2, **i32)), "tree_mask: shape"),
+        (lambda: msa.attn_tree(q, kp, kp, table, lens, tree_mask=[[1]] * 3), "tree_mask: a torch.Tensor"),
         (lambda: msa.attn_tree(q, kp, kp, table, lens, lse=torch.zeros(2, 4, 2)), "lse: shape"),
         (lambda: msa.attn_tree(q, kp, kp, table, lens, ws=torch.zeros(8)), "ws: dtype"),
     ]:

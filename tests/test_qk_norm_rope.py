@@ -93,6 +93,7 @@ def test_binding_refusals():
         (lambda: msa.qk_norm_rope(q, k, v, cfg, positions=torch.zeros(9, dtype=torch.int32)), "positions: 9 elements"),
         (lambda: msa.qk_norm_rope(q, k, v, cfg, q=torch.zeros(2, 4, 4, 64, dtype=BF)), "q: shape"),
         (lambda: msa.qk_norm_rope(q, k, v, cfg, k_pages=torch.zeros(3, 2, 16, 64, dtype=BF)), "v_pages: a torch"),
+        (lambda: msa.qk_norm_rope(q, k, v, cfg, v_pages=torch.zeros(3, 2, 16, 64, dtype=BF)), "k_pages: a 4-d"),
         (lambda: msa.qk_norm_rope_varlen(q[0], k[0], v[0], [0, 4], cfg), "cu_seqlens: must end"),
         (lambda: msa.rope_cfg(64, inv_freq=[1.0] * 31), "inv_freq: 31 values"),
     ]:
