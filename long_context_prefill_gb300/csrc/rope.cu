@@ -23,8 +23,6 @@
 #include <math.h>
 #include <string.h>
 
-#include <vector>
-
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -326,6 +324,7 @@ msa_status norm_rope(const msa_shape& s, const int32_t* cu, int32_t n_seqs, cons
   if (cfg->rot_dim % 16) return MSA_ERR_UNSUPPORTED;
   const double theta = cfg->theta > 0.0 ? cfg->theta : 10000.0;
   if (!(cfg->theta == cfg->theta) || isinf(theta) || !isfinite(cfg->rot_scale)) return MSA_ERR_INVALID_ARG;
+  if (tokens == 0) return MSA_OK;  // empty tensors need no address
   if (!aligned(q_in, 16, true) || !aligned(k_in, 16, true) || !aligned(v_in, 16, false) || !aligned(q, 16, true) ||
       !aligned(k, 16, false) || !aligned(v, 16, false) || !aligned(positions, 4, false) ||
       !aligned(slots, 4, false) || !aligned(cfg->q_weight, 16, false) || !aligned(cfg->k_weight, 16, false))
@@ -361,7 +360,6 @@ msa_status norm_rope(const msa_shape& s, const int32_t* cu, int32_t n_seqs, cons
     if (!isfinite(f)) return MSA_ERR_INVALID_ARG;
     t.turn[i] = turns64(f);
   }
-  if (tokens == 0) return MSA_OK;
   a.q = static_cast<const __nv_bfloat16*>(q_in);
   a.k = static_cast<const __nv_bfloat16*>(k_in);
   a.v = static_cast<const __nv_bfloat16*>(v_in);

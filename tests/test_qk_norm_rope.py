@@ -75,6 +75,9 @@ def test_refusals(lib):
     assert varlen([1, 5]) == inv
     assert varlen([0, 5, 4]) == inv
     assert varlen([0, 0, 0]) == msa.MSA_OK  # nothing to do
+    a = dict.fromkeys(a)
+    assert varlen([0, 0, 0]) == msa.MSA_OK  # empty tensors have no address
+    assert varlen([0, 5]) == inv
 
 
 def test_binding_refusals():
