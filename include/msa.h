@@ -443,9 +443,9 @@ typedef struct {
  * 16-byte aligned).  v_in may be NULL (then v and pages must be).
  *   q         [B, Hq, n, d_h]
  *   k, v      [B, Hkv, n, d_h] (nullable when pages are given)
- *   pages     (nullable) K and V also go to the cache at slots[t]; a negative
- *             slot is not stored, one outside the pool neither, and the next
- *             poll returns MSA_ERR_INDEX
+ *   pages     (nullable) K and V also go to the cache at slots[t], each slot
+ *             named at most once; a negative slot is not stored, one outside
+ *             the pool neither, and the next poll returns MSA_ERR_INDEX
  *   positions [B * n], any int32 (angles are exact to about 2^-31 turns
  *             wherever the position lies); NULL: the index in the sequence
  * Outputs must not overlap inputs. */
@@ -473,7 +473,7 @@ MSA_API size_t msa_attn_tree_workspace(const msa_shape* shape);
  * ones (their K and V are in the cache already).  Row i < T of query head h
  * attends the L - T context keys and the drafted keys j < T whose bit j is set
  * in its mask; every key enters the softmax once.
- *   q, o        [B, Hq, n, d_h]; lse [B, Hq, n] or NULL.  Rows >= T are neither
+ *   q, o        [B, Hq, n, d_h], not overlapping; lse [B, Hq, n] or NULL.  Rows >= T are neither
  *               read nor written; a row without keys gives o = 0, lse = -inf
  *   tree_mask   [n, ceil(n / 32)] words per request, word x bit y = drafted key
  *               32 x + y, mask_stride words from one request to the next (0:

@@ -50,9 +50,10 @@
 //          next scores do not wait for its product with V.
 //
 // Measured (captured, 40 heads of 128 as 32 / 8): decode of 64 requests of 1K to
-// 16K tokens 192 us (6.6 TB/s, 0.98 of the measured copy rate), a million-token
-// context with 5 drafted tokens 593 us (7.2 TB/s), 128K with a tree of 32 (128
-// rows) 94 us (0.84 of the floor), 16 trees of up to 48 (192 rows) over 4K to
+// 16K tokens 188 to 193 us (6.7 TB/s, 0.98 of the measured copy rate), a
+// million-token context with 5 drafted tokens 590 us (7.3 TB/s), 128K with a tree
+// of 32 (128 rows) 88 to 91 us (0.88 of the floor), one request of 300 tokens
+// 9.5 us (two kernels' latency), 16 trees of up to 48 (192 rows) over 4K to
 // 32K 174 us (0.69: the two groups' softmax takes 1900 cycles of a scheduler's
 // 3040 a tile, and the products with Q read 8 KB of shared memory per 64 cycles,
 // its whole rate, beside the loads that land there).  Tried and slower there: a
@@ -999,7 +1000,9 @@ __global__ void __launch_bounds__(32 * join_warps(kShare)) tree_join_kernel(cons
   };
   const int rb = item % A.RB, kvh = item / A.RB;
   const int width = min(256, A.R - 256 * rb), full = min(256, A.R);
-  const int e = (blockIdx.y * (join_warps(kShare) / kShare) + (threadIdx.x >> 5) / kShare) * 32 + lane, c4 = e / width, rw = e - c4 * width, rr = 256 * rb + rw;
+  constexpr int kChunks = join_warps(kShare) / kShare;  // chunks of a CTA
+  const int e = (blockIdx.y * kChunks + (threadIdx.x >> 5) / kShare) * 32 + lane;
+  const int c4 = e / width, rw = e - c4 * width, rr = 256 * rb + rw;
   const bool there = e < width * (D / 4) && rr % A.n < (A.tree_len ? A.tree_len[b] : A.n);
   const float2* ml = A.part_ml + rw;
   const float4* part = A.part + (int64_t)c4 * width + rw;
