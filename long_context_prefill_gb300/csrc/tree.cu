@@ -54,7 +54,7 @@
 // million-token context with 5 drafted tokens 590 us (7.3 TB/s), 128K with a tree
 // of 32 (128 rows) 88 to 91 us (0.88 of the floor), one request of 300 tokens
 // 9.5 us (two kernels' latency), 16 trees of up to 48 (192 rows) over 4K to
-// 32K 174 us (0.69: the two groups' softmax takes 1900 cycles of a scheduler's
+// 32K 164 us (0.73: the two groups' softmax takes 1900 cycles of a scheduler's
 // 3040 a tile, and the products with Q read 8 KB of shared memory per 64 cycles,
 // its whole rate, beside the loads that land there).  Tried and slower there: a
 // score tile per group with P over it 194 us, turns of the groups on a scheduler
@@ -91,6 +91,8 @@ constexpr int kPChunk = 4;
 constexpr uint32_t kIdleNs = 64;
 constexpr int kMaxDrafts = 1024;
 
+struct Cut;
+
 struct TreeArgs {
   int32_t B, Hq, Hkv, n, R, RB, page_shift, max_pages, num_pages, words, q_box, max_parts;
   const int32_t *table, *seq_len, *tree_len;
@@ -98,7 +100,8 @@ struct TreeArgs {
   int64_t mask_stride;  // words between the masks of two requests (0: one mask for all)
   __nv_bfloat16* o;
   float* lse;
-  int64_t* prefix;  // [B + 1] tiles of the requests before
+  int32_t* count;   // parts of the line
+  Cut* cuts;        // [max_parts] what they cut
   float4* part;     // [2 max_parts][d/4][rows] unnormalised O of the cut items
   float2* part_ml;  // [2 max_parts][rows] their maximum (log2) and row sum
   float scale_log2;
@@ -114,6 +117,13 @@ struct Seg {
   int32_t b, kvh, rb, t0, t1, tiles;  // b < 0: no more
   int32_t L, T;
   int32_t r0, r1;  // tiles that its result covers: t0, t1, or more where both groups' segments are joined
+};
+
+// The item that a part's beginning cuts, if this is the first cut through it: n parts, the first in slot `first` of
+// the workspace, k = 1 .. inner in slots base + step k, another one in `tail`.
+struct __align__(16) Cut {
+  int32_t n;  // 1 or less: nothing to join
+  int32_t b, item, inner, first, base, step, tail;
 };
 
 // Barriers; [X]: per group (kTwo: segments and Q once, at X = 0)
@@ -203,6 +213,36 @@ __device__ __forceinline__ bool joined_in_cta(bool many, int64_t W, int most, in
   return many && W >= most && (p & 1) && part_begin(W, most, p) > s0 && part_begin(W, most, p + 1) <= s1;
 }
 
+// a / b for a >= 0, b > 0, in 32 bits where they suffice (64-bit division takes some hundred cycles)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
+// What the beginning of part p cuts, which lies in request b, whose tiles begin at `at`.
+template <Rows kRows, int kMost>
+__device__ void note_cut(const TreeArgs& A, int64_t W, int p, int b, int64_t at) {
+  const int64_t lo = part_begin(W, kMost, p);
+  const int tiles = key_tiles(A.seq_len[b]);
+  const int64_t item = quotient(lo - at, tiles), s0 = at + item * tiles, s1 = s0 + tiles;
+  Cut c = {0, b, (int32_t)item, 0, 0, 0, 0, 0};
+  if (lo > s0 && part_begin(W, kMost, p - 1) <= s0) {
+    // kMany, all parts present: an odd part that was joined in its CTA stands in the slot of the even one; only the
+    // first and the last part of an item can be odd and not
+    const bool pairs = kRows == kMany && W >= kMost;
+    const int c0 = p - 1, c1 = (int)quotient(s1 * parts(W, kMost) - 1, W);  // the largest part that begins below s1
+    const int lead = pairs && !(c0 & 1) ? 2 : 1;
+    const bool tail = pairs && (c1 & 1) && c1 != c0 && !joined_in_cta(true, W, kMost, c1, s0, s1);
+    c.step = pairs ? 2 : 1;
+    c.inner = c0 + lead <= c1 ? (c1 - c0 - lead) / c.step + 1 : 0;
+    c.n = 1 + c.inner + (tail ? 1 : 0);
+    c.first = 2 * c0 + 1;
+    c.base = 2 * (c0 + lead - c.step);
+    c.step *= 2;
+    c.tail = 2 * c1;
+  }
+  A.cuts[p] = c;
+}
+
 template <int D, Rows kRows>
 __global__ void __launch_bounds__(threads_of(kRows), 1)
     tree_attn_kernel(const __grid_constant__ TreeMaps M, const TreeArgs A) {
@@ -224,6 +264,7 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
   extern __shared__ __align__(1024) uint8_t sm[];  // swizzled tiles start on 1 KB
   if (smem_u32(sm) & 1023) {
     if (threadIdx.x == 0) atomicCAS(A.err, 0, (int)kErrTimeout);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *A.count = 0;  // nothing to join
     return;
   }
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Ly::kBars);
@@ -273,7 +314,7 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
   }
   // ---- this CTA's parts of the line of tiles, and the requests they start in
   const int items = A.Hkv * A.RB;  // items of a request
-  int64_t* wsum = reinterpret_cast<int64_t*>(sm + Ly::kRing);  // scratch until the pipeline starts
+  int64_t* wsum = reinterpret_cast<int64_t*>(sm + Ly::kML);    // (used again at the end, for maxima and sums)
   int64_t* start = wsum + 16;                                  // [X][2]: request, its first tile
   int64_t W = 0;                                               // all tiles
   {
@@ -310,12 +351,11 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
         const int64_t lo = part_begin(W, kMost, part_of(W, kMost, blockIdx.x, X));  // at or above W: no part
         if (at <= lo && lo < at + t) { start[2 * X] = b; start[2 * X + 1] = at; }
       }
-      if (blockIdx.x == 0) A.prefix[b] = at;
       at += t;
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) A.prefix[A.B] = W;
   }
   const int G = parts(W, kMost);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *A.count = G;
   // tiles of this CTA's parts; tile k of group X is tile turn(X, k) of the ring (the parts' tiles take turns)
   int64_t begin[2] = {0, 0};
   int cnt[2] = {0, 0};
@@ -330,7 +370,6 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
   const int both = min(cnt[0], cnt[1]);
   auto turn = [&](int X, int k) { return kPair ? k : k < both ? 2 * k + X : both + k; };
   auto owner = [&](int j) { return kPair ? 0 : j < 2 * both ? j & 1 : cnt[0] > cnt[1] ? 0 : 1; };
-  fence_proxy_async_smem();  // the scratch above lies in the ring that TMA fills
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -500,7 +539,6 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
       S.at = start[1], S.pos = begin[0], S.hi = begin[0] + cnt[0], S.b = (int)start[0], S.s = S.t = 0;
       other.at = start[3], other.pos = begin[1], other.hi = begin[1] + cnt[1], other.b = (int)start[2];
       other.s = other.t = 0;
-      __syncwarp();  // every lane has read the scratch that the first load overwrites
       Seg end;
       end.b = -1;
       int X = 0;
@@ -524,6 +562,8 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
       };
       Walk w = {0, 0, 0, 0}, other = {0, 0, 0, 0};
       int X = 0;
+      if (lane < 2 && (lane ? cnt[1] : cnt[0]) > 0)  // what the parts cut, for the second kernel
+        note_cut<kRows, kMost>(A, W, part_of(W, kMost, blockIdx.x, lane), (int)start[2 * lane], start[2 * lane + 1]);
       for (int j = 0; j < cnt[0] + cnt[1] && ok; ++j) {
         if (owner(j) != X) {
           const Walk t = w;
@@ -949,120 +989,156 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
 }
 
 // Joins the parts of the items that the line's cuts went through, in a fixed
-// order.  Latency bounds it (a few parts of a few KB for each of a few items), so
-// where there is little to join, the eight warps of a CTA share an item's parts:
-// warp k takes parts k, k + 8, .. of a chunk of 32 float4 of the block's rows, four
-// parts' loads in flight, and the first joins the eight.  One request of 5000
-// tokens in 38 parts a head: 26 us with a warp per chunk, 19 us so; 16 requests
-// with trees of 48: 174 us with a warp per chunk, 234 us so, as most CTAs only find
-// out that they have nothing to do.  Grid: (items, chunks / chunks of a CTA).
-constexpr int join_warps(int share) { return share > 1 ? share : 4; }
+// order.  Latency bounds it where there is little to join, and else what the parts
+// hold (up to 40 MB, in the L2).  There are fewer cuts than parts, so each CTA looks
+// through all of them (those that are the first through their item stand for it)
+// and takes its share of the cut items' chunks, however many items there are; with a grid over the items most CTAs find nothing to do: 152 requests of
+// 1072 tokens with 192 rows 167 us so, 211 us with it.
+//   kShare = 1: a thread takes 16 columns of a row, two parts in flight, a chunk is
+//     a warp's width of those;
+//   kShare = 8, where items have four parts or more each and there is a CTA's worth of
+//     room for every chunk: 4 columns, the eight warps of a CTA divide a chunk's
+//     parts, four in flight each (one request of 5000 tokens in 38 parts a head:
+//     18 us, 26 us with kShare = 1; with more chunks than that, 2 requests with 256
+//     rows over 20000 tokens, 60 us, 50 us with kShare = 1).
+constexpr int kJoinThreads = 256, kJoinCols = 16;
+constexpr int join_per_sm(int share) { return share > 1 ? 4 : 3; }
 
-// a / b for a >= 0, b > 0, in 32 bits where they suffice (64-bit division takes some hundred cycles)
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
-}
-
-struct Joined {
-  float m, l;
-  float4 o;
-};
-// x and y joined; either may be empty (m = -inf, the rest 0)
-__device__ __forceinline__ Joined join2(const Joined& x, const Joined& y) {
-  const float m = fmaxf(x.m, y.m), ref = m == -INFINITY ? 0.f : m;
-  const float a = ex2(x.m - ref), b = ex2(y.m - ref);
-  return {m, x.l * a + y.l * b,
-          make_float4(x.o.x * a + y.o.x * b, x.o.y * a + y.o.y * b, x.o.z * a + y.o.z * b, x.o.w * a + y.o.w * b)};
-}
-
-template <int D, int kShare>
-__global__ void __launch_bounds__(32 * join_warps(kShare)) tree_join_kernel(const TreeArgs A) {
-  __shared__ Joined joined[kShare][32];  // (kShare = 1: unused)
+template <int D, Rows kRows, int kShare>
+__global__ void __launch_bounds__(kJoinThreads, join_per_sm(kShare)) tree_join_kernel(const TreeArgs A) {
+  constexpr int kMost = kRows == kTwo ? kCtas : 2 * kCtas, kWarps = kJoinThreads / 32, kWords = (kMost + 31) / 32;
+  constexpr int kCols = kShare > 1 ? 4 : kJoinCols, kAhead = kShare > 1 ? 4 : 2;
+  static_assert(kShare == 1 || kShare == kWarps, "a chunk per warp or CTA");
+  __shared__ unsigned found[kWords];
+  __shared__ float joined[kShare][kCols + 2][32];  // (kShare = 1: unused)
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int items = A.Hkv * A.RB, lane = threadIdx.x & 31;
-  const int warp = (threadIdx.x >> 5) % kShare;  // of those that share a chunk
-  const int b = (int)(blockIdx.x / items), item = (int)(blockIdx.x % items);
-  const int64_t W = A.prefix[A.B], p0 = A.prefix[b], p1 = A.prefix[b + 1];
-  if (p1 == p0) return;
-  const int64_t tiles = quotient(p1 - p0, items), s0 = p0 + item * tiles, s1 = s0 + tiles;
-  const int G = parts(W, A.max_parts);  // part c holds tile x: the largest c with W c / G <= x
-  const int c0 = (int)quotient((s0 + 1) * G - 1, W), c1 = (int)quotient(s1 * G - 1, W);
-  // Its parts: c0, the ones from c0 + lead on by `step`, and c1 where those leave it out.  (kMany, all parts present:
-  // an odd part that was joined in its CTA stands in the slot of the even one; only c0 and c1 can be odd and not.)
-  const bool pairs = A.R > 64 && A.R <= 128 && W >= 2 * kCtas;
-  const int step = pairs ? 2 : 1, lead = pairs && !(c0 & 1) ? 2 : 1;
-  const int inner = c0 + lead <= c1 ? (c1 - c0 - lead) / step + 1 : 0;
-  const bool tail = pairs && (c1 & 1) && c1 != c0 && !joined_in_cta(true, W, 2 * kCtas, c1, s0, s1);
-  const int n = 1 + inner + (tail ? 1 : 0);
-  if (n == 1) return;  // one CTA finished it
-  auto slot = [&](int k) {  // of its k-th part; the first one starts the item
-    return (int64_t)(k == 0 ? 2 * c0 + 1 : 2 * (k <= inner ? c0 + lead + step * (k - 1) : c1));
-  };
-  const int rb = item % A.RB, kvh = item / A.RB;
-  const int width = min(256, A.R - 256 * rb), full = min(256, A.R);
-  constexpr int kChunks = join_warps(kShare) / kShare;  // chunks of a CTA
-  const int e = (blockIdx.y * kChunks + (threadIdx.x >> 5) / kShare) * 32 + lane;
-  const int c4 = e / width, rw = e - c4 * width, rr = 256 * rb + rw;
-  const bool there = e < width * (D / 4) && rr % A.n < (A.tree_len ? A.tree_len[b] : A.n);
-  const float2* ml = A.part_ml + rw;
-  const float4* part = A.part + (int64_t)c4 * width + rw;
-  Joined s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-  constexpr int kAhead = kShare > 1 ? 4 : 8;
-  for (int c = warp; c < n; c += kAhead * kShare) {
-    Joined x[kAhead];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int full = min(256, A.R), chunks = (full * (D / kCols) + 31) / 32;
+  const int G = *A.count;
+  for (int x = warp; x < kWords; x += kWarps) {
+    const int p = 32 * x + lane, n = A.cuts[min(p, kMost - 1)].n;
+    const unsigned f = __ballot_sync(0xFFFFFFFFu, p < G && n > 1);  // (behind G: of another call)
+    if (lane == 0) found[x] = f;
+  }
+  __syncthreads();
+  const int first = blockIdx.x + (kShare > 1 ? 0 : warp * gridDim.x), step = gridDim.x * (kWarps / kShare);
+  for (int u = first;; u += step) {
+    // the cut that stands for this chunk's item
+    int left = u / chunks, p = -1;
+    const int e = 32 * (u - left * chunks) + lane;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      x[k] = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-      if (there && c + k * kShare < n) {
-        const int64_t sl = slot(c + k * kShare);
-        const float2 state = ml[sl * full];
-        x[k].m = state.x;
-        x[k].l = state.y;
-        x[k].o = part[sl * (D / 4) * full];
+    for (int x = 0; x < kWords; ++x) {
+      const unsigned f = found[x];
+      const int here = __popc(f);
+      if (left >= 0 && left < here) {
+        const bool mine = (f >> lane & 1u) && __popc(f & ((1u << lane) - 1u)) == left;
+        p = 32 * x + __ffs(__ballot_sync(0xFFFFFFFFu, mine)) - 1;
       }
+      left -= here;
     }
-    // as join2 for all of them at once
-    float top = s.m;
+    if (p < 0) return;  // no more
+    const Cut it = A.cuts[p];
+    const int rb = it.item % A.RB, kvh = it.item / A.RB;
+    const int width = min(256, A.R - 256 * rb);
+    const int c = e / width, rw = e - c * width, rr = 256 * rb + rw;  // group of columns, row of the block
+    const bool there = e < width * (D / kCols);
+    const int T = A.tree_len ? A.tree_len[it.b] : A.n;
+    const float2* ml = A.part_ml + rw;
+    const float4* part = A.part + (int64_t)(kCols / 4 * c) * width + rw;
+    float m = -INFINITY, l = 0.f, o[kCols];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) top = fmaxf(top, x[k].m);
-    const float ref = top == -INFINITY ? 0.f : top, keep = ex2(s.m - ref);
-    s = {top, s.l * keep, make_float4(s.o.x * keep, s.o.y * keep, s.o.z * keep, s.o.w * keep)};
+    for (int x = 0; x < kCols; ++x) o[x] = 0.f;
+    if (there)
+      for (int y0 = kShare > 1 ? warp : 0; y0 < it.n; y0 += kAhead * kShare) {
+        float2 state[kAhead];
+        float4 v[kAhead][kCols / 4];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const float w = ex2(x[k].m - ref);
-      s.l += w * x[k].l;
-      s.o.x += w * x[k].o.x;
-      s.o.y += w * x[k].o.y;
-      s.o.z += w * x[k].o.z;
-      s.o.w += w * x[k].o.w;
+        for (int k = 0; k < kAhead; ++k) {
+          const int y = y0 + k * kShare;
+          state[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+          for (int x = 0; x < kCols / 4; ++x) v[k][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (y < it.n) {
+            const int64_t slot = y == 0 ? it.first : y <= it.inner ? it.base + it.step * y : it.tail;
+            state[k] = ml[slot * full];
+#pragma unroll
+            for (int x = 0; x < kCols / 4; ++x) v[k][x] = part[slot * (D / 4) * full + x * width];
+          }
+        }
+        float top = m;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) top = fmaxf(top, state[k].x);
+        const float ref = top == -INFINITY ? 0.f : top, keep = ex2(m - ref);
+        m = top;
+        l *= keep;
+#pragma unroll
+        for (int x = 0; x < kCols; ++x) o[x] *= keep;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const float w = ex2(state[k].x - ref);
+          l += w * state[k].y;
+#pragma unroll
+          for (int x = 0; x < kCols / 4; ++x) {
+            o[4 * x] += w * v[k][x].x;
+            o[4 * x + 1] += w * v[k][x].y;
+            o[4 * x + 2] += w * v[k][x].z;
+            o[4 * x + 3] += w * v[k][x].w;
+          }
+        }
+      }
+    if (kShare > 1) {
+      joined[warp][0][lane] = m;
+      joined[warp][1][lane] = l;
+#pragma unroll
+      for (int x = 0; x < kCols; ++x) joined[warp][2 + x][lane] = o[x];
+      __syncthreads();
+      if (warp == 0) {
+#pragma unroll
+        for (int k = 1; k < kShare; ++k) m = fmaxf(m, joined[k][0][lane]);
+        const float ref = m == -INFINITY ? 0.f : m;
+        l = 0.f;
+#pragma unroll
+        for (int x = 0; x < kCols; ++x) o[x] = 0.f;
+#pragma unroll
+        for (int k = 0; k < kShare; ++k) {
+          const float w = ex2(joined[k][0][lane] - ref);
+          l += w * joined[k][1][lane];
+#pragma unroll
+          for (int x = 0; x < kCols; ++x) o[x] += w * joined[k][2 + x][lane];
+        }
+      }
+      __syncthreads();
     }
-  }
-  if (kShare > 1) {
-    joined[warp][lane] = s;
-    __syncthreads();
-  }
-  if (warp > 0 || !there) return;
+    if ((kShare > 1 && warp > 0) || !there || rr % A.n >= T) continue;  // (rows not drafted: parts hold anything)
+    const bool some = !(l == 0.f);
+    const float inv = some ? 1.f / l : 0.f;
+    const int64_t grow = (int64_t)(it.b * A.Hq + kvh * (A.Hq / A.Hkv)) * A.n + rr;
+    uint32_t w[kCols / 2];
 #pragma unroll
-  for (int k = 1; k < kShare; ++k) s = join2(s, joined[k][lane]);
-  const bool some = !(s.l == 0.f);
-  const float inv = some ? 1.f / s.l : 0.f;
-  const int64_t grow = (int64_t)(b * A.Hq + kvh * (A.Hq / A.Hkv)) * A.n + rr;
-  *reinterpret_cast<uint2*>(A.o + grow * D + 4 * c4) =
-      make_uint2(pack_bf16x2(s.o.x * inv, s.o.y * inv), pack_bf16x2(s.o.z * inv, s.o.w * inv));
-  if (c4 == 0 && A.lse) A.lse[grow] = some ? (s.m + __log2f(s.l)) * 0.69314718055994531f : -INFINITY;
+    for (int x = 0; x < kCols / 2; ++x) w[x] = pack_bf16x2(o[2 * x] * inv, o[2 * x + 1] * inv);
+    __nv_bfloat16* dst = A.o + grow * D + kCols * c;
+    if constexpr (kCols == 4) {
+      *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int x = 0; x < kCols / 2; x += 4)
+        *reinterpret_cast<uint4*>(dst + 2 * x) = make_uint4(w[x], w[x + 1], w[x + 2], w[x + 3]);
+    }
+    if (c == 0 && A.lse) A.lse[grow] = some ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+  }
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct TreeWs {
-  size_t prefix, ml, part, total;
+  size_t cuts, ml, part, total;
 };
 int max_parts(int64_t R) { return R > 128 ? kCtas : 2 * kCtas; }
 TreeWs tree_ws(const msa_shape& s) {
   const int64_t R = (int64_t)(s.Hq / s.Hkv) * s.n, rows = 2 * max_parts(R) * (R < 256 ? R : 256);
   TreeWs w;
-  w.prefix = 0;
-  w.ml = align256((size_t)(s.B + 1) * 8);
+  w.cuts = 16;  // behind their count
+  w.ml = align256(w.cuts + max_parts(R) * sizeof(Cut));
   w.part = align256(w.ml + (size_t)rows * 8);
   w.total = align256(w.part + (size_t)rows * s.d_h * 4);
   return w;
@@ -1099,15 +1175,19 @@ msa_status launch_tree(const TreeMaps& maps, const TreeArgs& a, bool join, cudaS
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   const int full = a.R < 256 ? a.R : 256;
-  const int64_t items = (int64_t)a.B * a.Hkv * a.RB, chunks = ceil_div((int64_t)full * (D / 4), 32);
-  const bool share = items * chunks <= 8 * kCtas;  // a CTA per chunk, all of them resident at once
-  cfg.gridDim = dim3((unsigned)items, (unsigned)(share ? chunks : ceil_div(chunks, join_warps(1))));
-  cfg.blockDim = dim3(32 * join_warps(share ? 8 : 1));
+  const int64_t items = (int64_t)a.B * a.Hkv * a.RB, most = items < a.max_parts ? items : a.max_parts - 1;  // cut ones
+  const int64_t split = items * ceil_div((int64_t)full * (D / 4), 32);  // chunks, if their parts are divided
+  const bool share = 4 * items <= a.max_parts && split <= 8 * kCtas;
+  // (kShare = 1 has a chunk per warp, but few chunks go to all SMs first)
+  const int64_t ctas = share ? split : most * ceil_div((int64_t)full * (D / kJoinCols), 32);
+  const int fit = join_per_sm(share ? 8 : 1) * kCtas;
+  cfg.gridDim = dim3((unsigned)(ctas < fit ? ctas : fit));
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if ((share ? cudaLaunchKernelEx(&cfg, tree_join_kernel<D, 8>, a)
-             : cudaLaunchKernelEx(&cfg, tree_join_kernel<D, 1>, a)) != cudaSuccess)
+  if ((share ? cudaLaunchKernelEx(&cfg, tree_join_kernel<D, kRows, 8>, a)
+             : cudaLaunchKernelEx(&cfg, tree_join_kernel<D, kRows, 1>, a)) != cudaSuccess)
     return MSA_ERR_CUDA;
   note_launch();
   return MSA_OK;
@@ -1166,7 +1246,8 @@ extern "C" msa_status msa_attn_tree(const msa_shape* shape, const void* q, const
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
   uint8_t* base = static_cast<uint8_t*>(ws);
-  a.prefix = reinterpret_cast<int64_t*>(base + w.prefix);
+  a.count = reinterpret_cast<int32_t*>(base);
+  a.cuts = reinterpret_cast<Cut*>(base + w.cuts);
   a.part_ml = reinterpret_cast<float2*>(base + w.ml);
   a.part = reinterpret_cast<float4*>(base + w.part);
   a.scale_log2 = effective_scale(*shape) * 1.4426950408889634f;
