@@ -34,7 +34,7 @@ msa_status check_page_geometry(int32_t num_pages, int32_t page_size);
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 8;    // tokens of a CTA: 4 and 16 measured 1 % and 7 % slower on 32K tokens
+constexpr int kMaxTokens = 8;    // tokens of a CTA: 5 and 16 measured 1 % and 6 % slower on 32K tokens
 constexpr int kPerSm = 8;        // CTAs per SM below which they take fewer tokens
 constexpr int kMaxBatch = 1024;  // sequences of a launch
 
@@ -113,10 +113,12 @@ __device__ __forceinline__ void load8(const float* p, const float* q, uint64_t (
 // (half-split), or both hold whole pairs (interleaved).
 //
 // With scalar arithmetic the issue slots were 65 % taken at 5.2 TB/s, so it is in
-// packed pairs: 32K tokens of 40 + 8 heads of 128 into layer and cache in 162 us,
-// 5.8 TB/s (0.86 of the measured copy rate), 64 tokens of a decode step in 3.5 us.
+// packed pairs; and a lane keeps the loads of its next two heads in flight (with one
+// the 4 CTAs an SM's registers hold had too little on the way: 162 us).  32K tokens
+// of 32 + 8 + 8 heads of 128 into layer and cache take 152 us, 6.2 TB/s (0.91 of the
+// measured copy rate), 105K tokens 457 us (0.97), 64 tokens of a decode step 3.7 us.
 template <int D>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeArgs A, const __grid_constant__ RopeTables T) {
+__global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const RopeArgs A, const __grid_constant__ RopeTables T) {
   constexpr int kLanes = D / 16;               // lanes of a head
   constexpr int kHeads = kThreads / kLanes;    // heads in flight per CTA
   // Shared tables hold what a lane reads as two float4, and those of the lanes of a head side by side (no two lanes
@@ -164,6 +166,10 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeArgs A, c
   }
   uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
   if (t < cnt) load(t, h, x0, x1);  // in flight while the angles are computed
+  uint4 y0 = make_uint4(0, 0, 0, 0), y1 = y0;  // and its next one
+  int nt = t, nh = h;
+  next(nt, nh);
+  if (nt < cnt) load(nt, nh, y0, y1);
 
   if (tid < cnt) {
     const int tk = first + tid;
@@ -211,10 +217,10 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeArgs A, c
   __syncthreads();
 
   while (t < cnt) {
-    int nt = t, nh = h;
-    next(nt, nh);
-    uint4 y0 = make_uint4(0, 0, 0, 0), y1 = y0;
-    if (nt < cnt) load(nt, nh, y0, y1);
+    int mt = nt, mh = nh;
+    next(mt, mh);
+    uint4 z0 = make_uint4(0, 0, 0, 0), z1 = z0;
+    if (mt < cnt) load(mt, mh, z0, z1);
     const Token tk = toks[t];
     const bool is_v = h >= A.Hq + A.Hkv, is_q = h < A.Hq;
     if (!is_v) {
@@ -297,6 +303,10 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeArgs A, c
     h = nh;
     x0 = y0;
     x1 = y1;
+    nt = mt;
+    nh = mh;
+    y0 = z0;
+    y1 = z1;
   }
 }
 
