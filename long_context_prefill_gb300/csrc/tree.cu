@@ -996,18 +996,18 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
 // 1072 tokens with 192 rows 167 us so, 211 us with it.
 //   kShare = 1: a thread takes 16 columns of a row, two parts in flight, a chunk is
 //     a warp's width of those;
-//   kShare = 8, where items have four parts or more each and there is a CTA's worth of
-//     room for every chunk: 4 columns, the eight warps of a CTA divide a chunk's
-//     parts, four in flight each (one request of 5000 tokens in 38 parts a head:
-//     18 us, 26 us with kShare = 1; with more chunks than that, 2 requests with 256
-//     rows over 20000 tokens, 60 us, 50 us with kShare = 1).
-constexpr int kJoinThreads = 256, kJoinCols = 16;
-constexpr int join_per_sm(int share) { return share > 1 ? 4 : 3; }
+//   kShare = 8, where items have four parts or more each and about every chunk has an
+//     idle CTA: 8 columns, the eight warps of a CTA divide a chunk's parts, four in
+//     flight each (one request of 5000 tokens in 38 parts a head: 18 us, 26 us with
+//     kShare = 1; with more chunks than four an SM, 4 requests with 64 rows over 8000
+//     tokens, 36 us, 33 us with kShare = 1).
+constexpr int kJoinThreads = 256, kJoinPerSm = 3;
+constexpr int join_cols(int share) { return share > 1 ? 8 : 16; }
 
 template <int D, Rows kRows, int kShare>
-__global__ void __launch_bounds__(kJoinThreads, join_per_sm(kShare)) tree_join_kernel(const TreeArgs A) {
+__global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) tree_join_kernel(const TreeArgs A) {
   constexpr int kMost = kRows == kTwo ? kCtas : 2 * kCtas, kWarps = kJoinThreads / 32, kWords = (kMost + 31) / 32;
-  constexpr int kCols = kShare > 1 ? 4 : kJoinCols, kAhead = kShare > 1 ? 4 : 2;
+  constexpr int kCols = join_cols(kShare), kAhead = kShare > 1 ? 4 : 2;
   static_assert(kShare == 1 || kShare == kWarps, "a chunk per warp or CTA");
   __shared__ unsigned found[kWords];
   __shared__ float joined[kShare][kCols + 2][32];  // (kShare = 1: unused)
@@ -1117,13 +1117,9 @@ __global__ void __launch_bounds__(kJoinThreads, join_per_sm(kShare)) tree_join_k
 #pragma unroll
     for (int x = 0; x < kCols / 2; ++x) w[x] = pack_bf16x2(o[2 * x] * inv, o[2 * x + 1] * inv);
     __nv_bfloat16* dst = A.o + grow * D + kCols * c;
-    if constexpr (kCols == 4) {
-      *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-    } else {
 #pragma unroll
-      for (int x = 0; x < kCols / 2; x += 4)
-        *reinterpret_cast<uint4*>(dst + 2 * x) = make_uint4(w[x], w[x + 1], w[x + 2], w[x + 3]);
-    }
+    for (int x = 0; x < kCols / 2; x += 4)
+      *reinterpret_cast<uint4*>(dst + 2 * x) = make_uint4(w[x], w[x + 1], w[x + 2], w[x + 3]);
     if (c == 0 && A.lse) A.lse[grow] = some ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
   }
 }
@@ -1176,12 +1172,11 @@ msa_status launch_tree(const TreeMaps& maps, const TreeArgs& a, bool join, cudaS
   memset(&cfg, 0, sizeof(cfg));
   const int full = a.R < 256 ? a.R : 256;
   const int64_t items = (int64_t)a.B * a.Hkv * a.RB, most = items < a.max_parts ? items : a.max_parts - 1;  // cut ones
-  const int64_t split = items * ceil_div((int64_t)full * (D / 4), 32);  // chunks, if their parts are divided
-  const bool share = 4 * items <= a.max_parts && split <= 8 * kCtas;
+  const int64_t split = items * ceil_div((int64_t)full * (D / join_cols(8)), 32);  // chunks, if their parts are divided
+  const bool share = 4 * items <= a.max_parts && split <= 4 * kCtas;
   // (kShare = 1 has a chunk per warp, but few chunks go to all SMs first)
-  const int64_t ctas = share ? split : most * ceil_div((int64_t)full * (D / kJoinCols), 32);
-  const int fit = join_per_sm(share ? 8 : 1) * kCtas;
-  cfg.gridDim = dim3((unsigned)(ctas < fit ? ctas : fit));
+  const int64_t ctas = share ? split : most * ceil_div((int64_t)full * (D / join_cols(1)), 32);
+  cfg.gridDim = dim3((unsigned)(ctas < kJoinPerSm * kCtas ? ctas : kJoinPerSm * kCtas));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cfg.attrs = &attr;
