@@ -43,7 +43,7 @@ struct RopeArgs {
   int64_t q_stride, k_stride, v_stride;  // elements from one token to the next
   int32_t Hq, Hkv, has_v;
   int32_t tok0, tok1;  // tokens of this launch
-  int32_t n;           // tokens of a sequence (uniform batch), 0: varlen, `cu`
+  int32_t n;           // tokens of a sequence (uniform batch)
   int32_t per_cta;
   const int32_t* positions;
   const __nv_bfloat16 *q_w, *k_w;
@@ -54,13 +54,18 @@ struct RopeArgs {
   const int32_t* slots;
   int32_t page_shift, num_pages;
   int* err;
+  uint64_t turn[64];  // f_i in 2^-64 turns
 };
 
-struct RopeTables {
-  uint64_t turn[64];               // f_i in 2^-64 turns
-  int32_t count;                   // varlen: sequences of this launch
-  int32_t cu[kMaxBatch + 1];       // their first tokens
+// Varlen: the sequences of a launch and their first tokens.  (4 KB of parameters, which a uniform batch does not pay
+// for: they cost its call 0.5 us on the host.)
+template <bool kVarlen>
+struct Seqs {
+  int32_t count;
+  int32_t cu[kMaxBatch + 1];
 };
+template <>
+struct Seqs<false> {};
 
 struct Token {
   int32_t seq0, n, i;  // first token and length of its sequence, index in it
@@ -115,10 +120,11 @@ __device__ __forceinline__ void load8(const float* p, const float* q, uint64_t (
 // With scalar arithmetic the issue slots were 65 % taken at 5.2 TB/s, so it is in
 // packed pairs; and a lane keeps the loads of its next two heads in flight (with one
 // the 4 CTAs an SM's registers hold had too little on the way: 162 us).  32K tokens
-// of 32 + 8 + 8 heads of 128 into layer and cache take 152 us, 6.2 TB/s (0.91 of the
-// measured copy rate), 105K tokens 457 us (0.97), 64 tokens of a decode step 3.7 us.
-template <int D>
-__global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const RopeArgs A, const __grid_constant__ RopeTables T) {
+// of 32 + 8 + 8 heads of 128 into layer and cache take 151 us, 6.2 TB/s (0.91 of the
+// measured copy rate), 105K tokens 458 us (0.97), 64 tokens of a decode step 3.5 us.
+template <int D, bool kVarlen>
+__global__ void __launch_bounds__(kThreads, 4)
+    norm_rope_kernel(const __grid_constant__ RopeArgs A, const __grid_constant__ Seqs<kVarlen> T) {
   constexpr int kLanes = D / 16;               // lanes of a head
   constexpr int kHeads = kThreads / kLanes;    // heads in flight per CTA
   // Shared tables hold what a lane reads as two float4, and those of the lanes of a head side by side (no two lanes
@@ -174,13 +180,13 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const RopeArgs A
   if (tid < cnt) {
     const int tk = first + tid;
     Token k;
-    if (A.n) {
-      k.seq0 = tk / A.n * A.n;
-      k.n = A.n;
-    } else {
+    if constexpr (kVarlen) {
       const int s = seq_search(T.count, [&](int x) { return T.cu[x]; }, tk);
       k.seq0 = T.cu[s];
       k.n = T.cu[s + 1] - T.cu[s];
+    } else {
+      k.seq0 = tk / A.n * A.n;
+      k.n = A.n;
     }
     k.i = tk - k.seq0;
     k.slot = -1;
@@ -206,9 +212,9 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const RopeArgs A
       const int t = x / half, p = x - t * half, tk = first + t;
       int pos;
       if (A.positions) pos = A.positions[tk];
-      else if (A.n) pos = tk % A.n;
-      else pos = tk - T.cu[seq_search(T.count, [&](int y) { return T.cu[y]; }, tk)];
-      const uint64_t turns = (uint64_t)(int64_t)pos * T.turn[p];
+      else if constexpr (kVarlen) pos = tk - T.cu[seq_search(T.count, [&](int y) { return T.cu[y]; }, tk)];
+      else pos = tk % A.n;
+      const uint64_t turns = (uint64_t)(int64_t)pos * A.turn[p];
       float s, c;
       sincospif((float)(int32_t)(turns >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31 half turns
       cosines[t][pair_at(p)] = c * A.rot_scale;
@@ -363,12 +369,10 @@ msa_status norm_rope(const msa_shape& s, const int32_t* cu, int32_t n_seqs, cons
     return MSA_ERR_INVALID_ARG;
   }
   if (tokens >= ((int64_t)1 << 31) - kMaxTokens) return MSA_ERR_UNSUPPORTED;
-  RopeTables t;
-  memset(&t, 0, sizeof(t));
   for (int i = 0; i < cfg->rot_dim / 2; ++i) {
     const double f = cfg->inv_freq ? cfg->inv_freq[i] : pow(theta, -2.0 * i / cfg->rot_dim);
     if (!isfinite(f)) return MSA_ERR_INVALID_ARG;
-    t.turn[i] = turns64(f);
+    a.turn[i] = turns64(f);
   }
   a.q = static_cast<const __nv_bfloat16*>(q_in);
   a.k = static_cast<const __nv_bfloat16*>(k_in);
@@ -379,7 +383,7 @@ msa_status norm_rope(const msa_shape& s, const int32_t* cu, int32_t n_seqs, cons
   a.Hq = s.Hq;
   a.Hkv = s.Hkv;
   a.has_v = v_in != nullptr;
-  a.n = cu ? 0 : s.n;
+  a.n = s.n;
   a.positions = positions;
   a.q_w = static_cast<const __nv_bfloat16*>(cfg->q_weight);
   a.k_w = static_cast<const __nv_bfloat16*>(cfg->k_weight);
@@ -399,21 +403,28 @@ msa_status norm_rope(const msa_shape& s, const int32_t* cu, int32_t n_seqs, cons
   int64_t per = tokens / (152 * kPerSm);
   if (per < lanes / heads) per = lanes / heads;
   a.per_cta = (int)(per < 1 ? 1 : per > kMaxTokens ? kMaxTokens : per);
-  for (int s0 = 0; s0 < (cu ? n_seqs : 1); s0 += kMaxBatch) {
-    a.tok0 = 0;
-    a.tok1 = (int32_t)tokens;
-    if (cu) {
-      t.count = n_seqs - s0 < kMaxBatch ? n_seqs - s0 : kMaxBatch;
-      for (int x = 0; x <= t.count; ++x) t.cu[x] = cu[s0 + x];
-      a.tok0 = t.cu[0];
-      a.tok1 = t.cu[t.count];
-    }
-    if (a.tok1 <= a.tok0) continue;
+  auto launch = [&](auto kernel, const auto& seqs) {
     const unsigned grid = (unsigned)ceil_div((int64_t)a.tok1 - a.tok0, a.per_cta);
-    if (s.d_h == 128) norm_rope_kernel<128><<<grid, kThreads, 0, stream>>>(a, t);
-    else norm_rope_kernel<64><<<grid, kThreads, 0, stream>>>(a, t);
+    kernel<<<grid, kThreads, 0, stream>>>(a, seqs);
     note_launch();
-    if (cudaGetLastError() != cudaSuccess) return MSA_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess;
+  };
+  if (!cu) {
+    a.tok1 = (int32_t)tokens;
+    const bool ok = s.d_h == 128 ? launch(norm_rope_kernel<128, false>, Seqs<false>())
+                                 : launch(norm_rope_kernel<64, false>, Seqs<false>());
+    return ok ? MSA_OK : MSA_ERR_CUDA;
+  }
+  Seqs<true> t;
+  memset(&t, 0, sizeof(t));
+  for (int s0 = 0; s0 < n_seqs; s0 += kMaxBatch) {
+    t.count = n_seqs - s0 < kMaxBatch ? n_seqs - s0 : kMaxBatch;
+    for (int x = 0; x <= t.count; ++x) t.cu[x] = cu[s0 + x];
+    a.tok0 = t.cu[0];
+    a.tok1 = t.cu[t.count];
+    if (a.tok1 <= a.tok0) continue;
+    const bool ok = s.d_h == 128 ? launch(norm_rope_kernel<128, true>, t) : launch(norm_rope_kernel<64, true>, t);
+    if (!ok) return MSA_ERR_CUDA;
   }
   return MSA_OK;
 }
