@@ -238,6 +238,23 @@ def test_items_across_many_cuts(cuda_lib, Hq, Hkv, n, page):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,n,d,lens", [(16, 2, 100, 128, [12001, 300, 5000]), (4, 1, 200, 64, [9000]),
+                                             (4, 1, 200, 128, [5000, 1000]), (3, 1, 100, 64, [200, 7000])])
+def test_row_blocks_are_cut_and_joined(cuda_lib, Hq, Hkv, n, d, lens):
+    """More than 256 rows a KV group, the last block of them partly filled, each block cut on its own: few long items
+    and many; a request whose tree is shorter than its rows."""
+    rng = np.random.default_rng(n + d)
+    tls = [n, n // 2, n][:len(lens)]
+    masks = np.stack([tree_bits(rng, n) for _ in lens])
+    c = Case(Hq, Hkv, n, d, 32, lens, 90 + n, tls=tls, masks=masks, peak=4.0)
+    out = c.run()
+    assert cuda_lib.poll_device_status() == 0
+    c.check(out, what="row blocks")
+    again = c.run()
+    assert torch.equal(out[0], again[0]) and torch.equal(out[1], again[1])
+
+
+@pytest.mark.gpu
 def test_large_scores_across_tiles(cuda_lib):
     """Scores that grow along the keys (every tile raises the maximum by tens) and fall again."""
     c = Case(4, 2, 3, 128, 32, [900, 4000], 13)
