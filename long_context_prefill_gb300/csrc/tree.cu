@@ -718,13 +718,15 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
       tc_fence_after();
       return true;
     };
+    const int i_first = r % A.n;  // (a block of rows other than the first is kTwo's)
     Seg g;
     for (int s = 0; used && next_seg(X, s, g); ++s) {
-      const int rows = group_rows(g.rb, X);
-      const int rr = 256 * g.rb + (kPair ? 128 * X : 0) + r;  // row within the KV group
+      const int rb = kPair ? g.rb : 0;
+      const int rows = group_rows(rb, X);
+      const int rr = 256 * rb + (kPair ? 128 * X : 0) + r;  // row within the KV group
       const bool row_in = r < rows;
       const bool warp_in = lane0 < rows;
-      const int i = rr % A.n;  // drafted token of this row
+      const int i = kPair ? rr % A.n : i_first;  // drafted token of this row
       const bool row_ok = row_in && i < g.T;
       const int C = g.L - g.T;
       const uint32_t* mrow = A.mask ? A.mask + g.b * A.mask_stride + (int64_t)i * A.words : nullptr;
@@ -854,6 +856,7 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
             // Two passes over the scores in TMEM, half a tile at a time: the rolled loops keep the code of all roles
             // within the instruction cache, which 128 scores in registers at once do not (a third of the fetches
             // missed, and one warp a scheduler has nothing to hide that with).
+            float mt = -INFINITY;
             if (masked) {  // masked scores are put back as -inf
 #pragma unroll 1
               for (int c = 0; c < 4; ++c) {
@@ -862,17 +865,20 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
                 tmem_ld32(tS + 32 * c, u);
                 tmem_ld_wait();
 #pragma unroll
-                for (int k = 0; k < 32; ++k) u[k] = ((vw >> k) & 1u) ? u[k] : 0xFF800000u;
+                for (int k = 0; k < 32; ++k) {
+                  u[k] = ((vw >> k) & 1u) ? u[k] : 0xFF800000u;
+                  mt = fmaxf(mt, __uint_as_float(u[k]));
+                }
                 tmem_st32(tS + 32 * c, u);
               }
               tmem_st_wait();
-            }
-            float mt = -INFINITY;
+            } else {
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-              float sv[64];
-              load64(tS + 64 * h, sv);
-              mt = max64(sv, mt);
+              for (int h = 0; h < 2; ++h) {
+                float sv[64];
+                load64(tS + 64 * h, sv);
+                mt = max64(sv, mt);
+              }
             }
             const float alpha = raise(mt);
             uint64_t acc[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
@@ -922,7 +928,7 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
       const bool some = !(l == 0.f);  // an attended key (a NaN among them shows in l)
       const int64_t grow = (int64_t)(g.b * A.Hq + g.kvh * (A.Hq / A.Hkv)) * A.n + rr;
       const float inv = some ? 1.f / l : 0.f;
-      const int width = min(256, A.R - 256 * g.rb), full = min(256, A.R), rw = rr - 256 * g.rb;
+      const int width = min(256, A.R - 256 * rb), full = min(256, A.R), rw = rr - 256 * rb;
       const int64_t slot = 2 * part_of(W, kMost, blockIdx.x, kPair || joins ? 0 : X) + (g.r0 > 0 ? 0 : 1);
       // N columns from c0 on
       auto write = [&](const float* ov, int c0, auto N) {
