@@ -23,9 +23,10 @@
 // do not depend on timing.
 //
 // A CTA (12 warps, one CTA per SM):
-//   warp 10    loader: walks the parts' segments, publishes their descriptors,
-//              loads Q rows and the K and V pages of every tile by TMA into a
-//              ring (K and V tiles alternate; two parts' tiles take turns);
+//   warp 10    loader of group 0's part (kTwo: of the CTA's) and one more warp for
+//              group 1's: walk its segments, publish their descriptors, load Q
+//              rows and the K and V pages of every tile by TMA into one ring (K
+//              and V tiles alternate; the two parts' tiles take turns);
 //   warp 8     waits for the ring's tiles one after another and declares each
 //              ready; in a request's last V tile it first zeroes the rows past
 //              the end: pages may hold anything there, and a weight of zero
@@ -152,8 +153,8 @@ struct Lay {
   static constexpr int kML = kSeg + 2 * kSegSlots * (int)sizeof(Seg);  // kMany: [2][128] maximum and row sum
   static constexpr int kBars = kML + 2 * 128 * 8;
   static constexpr int kNumBars = kBarRing + 3 * kSlots;
-  static constexpr int kMisc = kBars + kNumBars * 8;  // [0] TMEM base, [2] abort
-  static constexpr int kAlloc = kMisc + 16;
+  static constexpr int kMisc = kBars + kNumBars * 8;  // [0] TMEM base, [2] abort, [4 + X] tiles loaded
+  static constexpr int kAlloc = kMisc + 32;
   static_assert(kAlloc <= 227 * 1024 && kAlloc > 120 * 1024, "shared memory: one CTA per SM");
 };
 
@@ -249,17 +250,15 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
   using Ly = Lay<D>;
   constexpr bool kPair = kRows == kTwo;
   constexpr int kThreads = threads_of(kRows);
-  // From 8 boxes a K or V tile on (small pages) a second loader warp takes half of them, in kFew one of the softmax
-  // warps without rows, in kMany one more warp: a box costs its warp about 100 cycles, and 16-token pages make 32 of
-  // them a tile, more than the tile takes out of HBM (decode of 256 short requests 96 -> 84 us, d_h 64 143 -> 124 us).
-  // With fewer the second warp costs more than it takes over (d_h 64 in 64-token pages: 118 us without, 125 us with
-  // it).  kTwo is not bound by its loads.
-  constexpr int kHelperWarp = kRows == kFew ? 2 : 12;
-  const int loaders = !kPair && (128 >> A.page_shift) * (D / 64) >= 8 ? 2 : 1;
+  // Each group's part has a loader of its own (kFew: the second one is a softmax warp without rows): opening a segment
+  // (lengths, division, page entries, Q) takes one about 3000 cycles, a tile's boxes up to 1700, and short requests
+  // need both every other tile.  With one loader for both parts 256 requests of 100 to 1000 tokens take 81 us instead
+  // of 77 (16-token pages 83 instead of 77), 512 of 20 to 400 tokens 93 instead of 86, long ones the same.
+  constexpr int kLoaderWarp1 = kRows == kFew ? 2 : 12;
   constexpr int kSlots = Ly::kSlots;
   constexpr int kMost = kPair ? kCtas : 2 * kCtas;  // parts (A.max_parts)
   constexpr int kGroupWarps = kRows == kFew ? 2 : 4;
-  constexpr int kSegReaders = kPair ? 11 : kGroupWarps + 2;  // softmax warps, issuer(s), the cleaner (and the helper)
+  constexpr int kSegReaders = kPair ? 11 : kGroupWarps + 2;  // softmax warps, issuer(s), the cleaner
   constexpr int kQBufs = kRows == kFew ? 2 : 1;
   extern __shared__ __align__(1024) uint8_t sm[];  // swizzled tiles start on 1 KB
   if (smem_u32(sm) & 1023) {
@@ -302,14 +301,14 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
     mbar_init(&bars[kBarML], 8);
     for (int s = 0; s < 2 * kSegSlots; ++s) {
       mbar_init(&bars[kBarSegFull + s], 1);
-      mbar_init(&bars[kBarSegEmpty + s], kSegReaders + loaders - 1);
+      mbar_init(&bars[kBarSegEmpty + s], kSegReaders);
     }
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&bFull[s], loaders);
+      mbar_init(&bFull[s], 1);
       mbar_init(&bEmpty[s], 1);
       mbar_init(&bReady[s], 1);
     }
-    misc[2] = 0;
+    misc[2] = misc[4] = misc[5] = 0;
     fence_mbar_init();
   }
   // ---- this CTA's parts of the line of tiles, and the requests they start in
@@ -418,21 +417,21 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
 
   // kTwo: the block starts with 3 x 128 threads x 168 registers; the softmax threads (a row's 128 scores each) take
   // 192 and the others 120: 2 x 192 + 120 = 3 x 168
-  if (warp >= 8 || (kRows == kFew && warp == kHelperWarp)) {
+  if (warp >= 8 || (kRows == kFew && warp == kLoaderWarp1)) {
     if (kPair) asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
-    if (warp == kLoaderWarp || (loaders > 1 && warp == kHelperWarp)) {
-      // ---------------------------------------------------------- loader and helper
-      const int share = warp == kLoaderWarp ? 0 : 1;  // takes boxes share, share + loaders, ..
+    if (warp == kLoaderWarp || (!kPair && warp == kLoaderWarp1)) {
+      // ---------------------------------------------------------- loader of group X's part (kTwo: of the CTA's)
+      const int X = warp == kLoaderWarp ? 0 : 1;
       const uint64_t policy = A.RB == 1 ? policy_evict_first() : policy_evict_last();
       const int pshift = 7 - A.page_shift, pp = 1 << pshift;  // pages of a tile
       const int P = 1 << A.page_shift;
-      struct Stream {
-        int64_t at, pos, hi;  // first tile of request b, next segment's first tile, the part's end
-        int b, s, t;          // request, segments so far, next tile of the segment
-        Seg g;
-        int base, ids, ahead;  // lane x holds the page of entry base + x, and of base + 32 + x
-      };
-      auto publish = [&](int X, int s, const Seg& g) -> bool {
+      const int count = X ? cnt[1] : cnt[0];
+      int64_t at = start[2 * X + 1], pos = X ? begin[1] : begin[0];  // first tile of request b, of the next segment
+      const int64_t hi = pos + count;                                // the part's end
+      int b = (int)start[2 * X], s = 0, t = 0;        // request, segments so far, next tile of the segment
+      Seg g;
+      int base, ids, ahead;  // lane x holds the page of entry base + x, and of base + 32 + x
+      auto publish = [&](const Seg& g) -> bool {
         const int slot = X * kSegSlots + s % kSegSlots;
         if (misc[2] || !mbar_wait_idle(&bars[kBarSegEmpty + slot], ((s / kSegSlots) & 1) ^ 1, kIdleNs)) return false;
         if (lane == 0) {
@@ -450,111 +449,107 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
         }
         return page;
       };
-      // The next segment of a stream: its descriptor, its Q rows, its first page entries.
-      auto open = [&](Stream& S, int X) -> bool {
-        Seg& g = S.g;
-        if (share > 0) {
-          if (!next_seg(X, S.s, g)) return false;
-        } else {
-          bool bad;
-          int64_t t = 0;
-          for (; S.b < A.B; ++S.b) {  // pos < hi <= W: a request holding it exists
-            t = request(A, S.b, g.L, g.T, bad) ? (int64_t)items * key_tiles(g.L) : 0;
-            if (S.pos < S.at + t) break;
-            S.at += t;
-          }
-          if (S.b >= A.B) return false;
-          g.b = S.b;
-          g.tiles = key_tiles(g.L);
-          const int item = (int)((S.pos - S.at) / g.tiles);
-          g.kvh = item / A.RB;
-          g.rb = item - g.kvh * A.RB;
-          g.t0 = (int)(S.pos - S.at - (int64_t)item * g.tiles);
-          const int64_t left = S.hi - S.pos;
-          g.t1 = left < g.tiles - g.t0 ? g.t0 + (int)left : g.tiles;
-          g.r0 = g.t0;
-          g.r1 = g.t1;
-          if (kRows == kMany) {
-            const int64_t i0 = S.at + (int64_t)item * g.tiles;
-            const int p = part_of(W, kMost, blockIdx.x, 1);
-            // (of the even part only its last segment reaches the item)
-            if (joined_in_cta(true, W, kMost, p, i0, i0 + g.tiles)) {
-              g.r0 = (int)max((int64_t)0, begin[0] - i0);
-              g.r1 = (int)(begin[1] + cnt[1] - i0);
-            }
-          }
-          S.pos += g.t1 - g.t0;
-          if (!publish(X, S.s, g)) return false;
-          const int buf = S.s % kQBufs;
-          if (!mbar_wait_idle(&bars[kBarQEmpty + 2 * X + buf], ((S.s / kQBufs) & 1) ^ 1, kIdleNs)) return false;
-          const int rows = min(kPair ? 256 : 128, A.R - 256 * g.rb), boxes = (rows + A.q_box - 1) / A.q_box;
-          uint64_t* full = &bars[kBarQFull + 2 * X + buf];
-          if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(boxes * A.q_box * D * 2));
-          __syncwarp();
-          const int qrow = (g.b * A.Hq + g.kvh * (A.Hq / A.Hkv)) * A.n + 256 * g.rb;
-          if (lane < boxes * (D / 64)) {  // at most 8
-            const int c = lane & (D / 64 - 1), r = lane / (D / 64) * A.q_box;
-            tma_load_3d(sm + q_at(kPair ? r >> 7 : X, buf) + c * 16384 + (r & 127) * 128, &M.q, full, 64 * c, qrow + r, 0);
+      // The next segment: its descriptor, its Q rows, its first page entries.
+      auto open = [&]() -> bool {
+        bool bad;
+        int64_t tiles = 0;
+        for (; b < A.B; ++b) {  // pos < hi <= W: a request holding it exists
+          tiles = request(A, b, g.L, g.T, bad) ? (int64_t)items * key_tiles(g.L) : 0;
+          if (pos < at + tiles) break;
+          at += tiles;
+        }
+        if (b >= A.B) return false;
+        g.b = b;
+        g.tiles = key_tiles(g.L);
+        const int item = (int)quotient(pos - at, g.tiles);
+        g.kvh = item / A.RB;
+        g.rb = item - g.kvh * A.RB;
+        g.t0 = (int)(pos - at - (int64_t)item * g.tiles);
+        const int64_t left = hi - pos;
+        g.t1 = left < g.tiles - g.t0 ? g.t0 + (int)left : g.tiles;
+        g.r0 = g.t0;
+        g.r1 = g.t1;
+        if (kRows == kMany) {
+          const int64_t i0 = at + (int64_t)item * g.tiles;
+          const int p = part_of(W, kMost, blockIdx.x, 1);
+          // (of the even part only its last segment reaches the item)
+          if (joined_in_cta(true, W, kMost, p, i0, i0 + g.tiles)) {
+            g.r0 = (int)max((int64_t)0, begin[0] - i0);
+            g.r1 = (int)(begin[1] + cnt[1] - i0);
           }
         }
-        ++S.s;
-        S.t = g.t0;
-        S.base = g.t0 << pshift;
-        S.ids = entry(g, S.base + lane);
-        S.ahead = entry(g, S.base + 32 + lane);
+        pos += g.t1 - g.t0;
+        if (!publish(g)) return false;
+        const int buf = s % kQBufs;
+        if (!mbar_wait_idle(&bars[kBarQEmpty + 2 * X + buf], ((s / kQBufs) & 1) ^ 1, kIdleNs)) return false;
+        const int rows = min(kPair ? 256 : 128, A.R - 256 * g.rb), boxes = (rows + A.q_box - 1) / A.q_box;
+        uint64_t* full = &bars[kBarQFull + 2 * X + buf];
+        if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(boxes * A.q_box * D * 2));
+        __syncwarp();
+        const int qrow = (g.b * A.Hq + g.kvh * (A.Hq / A.Hkv)) * A.n + 256 * g.rb;
+        if (lane < boxes * (D / 64)) {  // at most 8
+          const int c = lane & (D / 64 - 1), r = lane / (D / 64) * A.q_box;
+          uint8_t* to = sm + q_at(kPair ? r >> 7 : X, buf) + c * 16384 + (r & 127) * 128;
+          tma_load_3d(to, &M.q, full, 64 * c, qrow + r, 0);
+        }
+        ++s;
+        t = g.t0;
+        base = g.t0 << pshift;
+        ids = entry(g, base + lane);
+        ahead = entry(g, base + 32 + lane);
         return true;
       };
-      int issued = 0;  // loads into the ring so far
-      // Ring tile j: the next tile of a stream.
-      auto step = [&](Stream& S, int X, int j) -> bool {
-        if ((S.s == 0 || S.t == S.g.t1) && !open(S, X)) return false;
-        int off = (S.t << pshift) - S.base;
+      // Before a slot's wait: the use of the slot before is loaded, if that is the other loader's task, so that the
+      // phase waited for is of that use and not of the one before it.
+      auto loaded = [&](int idx) -> bool {
+        const int j = idx >> 1;
+        if (kPair || idx < 0 || owner(j) == X) return true;
+        const int k = j < 2 * both ? j >> 1 : j - both;  // the other's tile
+        if ((int)misc[4 + (X ^ 1)] > k) return true;
+        const uint64_t since = global_timer_ns();
+        while ((int)misc[4 + (X ^ 1)] <= k)
+          if (misc[2] || global_timer_ns() - since > MSA_WAIT_LIMIT_NS) return false;
+        return true;
+      };
+      int issued = 0;  // the ring's loads up to here are past
+      // the part's tile k
+      auto step = [&](int k) -> bool {
+        if ((s == 0 || t == g.t1) && !open()) return false;
+        int off = (t << pshift) - base;
         if (off >= 32) {
-          S.base += 32;
+          base += 32;
           off -= 32;
-          S.ids = S.ahead;
-          S.ahead = entry(S.g, S.base + 32 + lane);
+          ids = ahead;
+          ahead = entry(g, base + 32 + lane);
         }
-        const int np = (S.g.L + P - 1) >> A.page_shift;
-        const int boxes = min(pp, np - (S.t << pshift)) * (D / 64);  // pages of this tile that hold keys, by 64 columns
-        const int box = lane * loaders + share, c = box & (D / 64 - 1), x = box / (D / 64);
-        const uint32_t bytes = (uint32_t)(((boxes - share + loaders - 1) >> (loaders - 1)) * P * 128);
-        const int krow = (__shfl_sync(0xFFFFFFFFu, S.ids, (off + x) & 31) * A.Hkv + S.g.kvh) << A.page_shift;
+        const int np = (g.L + P - 1) >> A.page_shift;
+        const int boxes = min(pp, np - (t << pshift)) * (D / 64);  // pages of this tile that hold keys, by 64 columns
+        const int c = lane & (D / 64 - 1), x = lane / (D / 64);
+        const int krow = (__shfl_sync(0xFFFFFFFFu, ids, (off + x) & 31) * A.Hkv + g.kvh) << A.page_shift;
 #pragma unroll
         for (int is_v = 0; is_v < 2; ++is_v) {
-          const int idx = 2 * j + is_v, st = idx % kSlots;
-          if (misc[2] || !mbar_wait_idle(&bEmpty[st], ((idx / kSlots) & 1) ^ 1, kIdleNs)) return false;
-          if (lane == 0) mbar_arrive_expect_tx(&bFull[st], bytes);
+          const int idx = 2 * turn(X, k) + is_v, st = idx % kSlots;
+          if (misc[2] || !loaded(idx - kSlots)) return false;
+          if (!mbar_wait_idle(&bEmpty[st], ((idx / kSlots) & 1) ^ 1, kIdleNs)) return false;
+          if (lane == 0) mbar_arrive_expect_tx(&bFull[st], (uint32_t)(boxes * P * 128));
           __syncwarp();
           issued = idx + 1;
-          if (box < boxes)
+          if (lane < boxes)
             tma_load_3d_hint(sm + Ly::kRing + st * Ly::kTile + c * 16384 + x * P * 128, is_v ? &M.v : &M.k, &bFull[st],
                              64 * c, krow, 0, policy);
         }
-        ++S.t;
+        __syncwarp();
+        if (!kPair && lane == 0) misc[4 + X] = k + 1;
+        ++t;
         return true;
       };
-      // the two streams change places in registers, so that the code above exists once
-      Stream S, other;
-      S.at = start[1], S.pos = begin[0], S.hi = begin[0] + cnt[0], S.b = (int)start[0], S.s = S.t = 0;
-      other.at = start[3], other.pos = begin[1], other.hi = begin[1] + cnt[1], other.b = (int)start[2];
-      other.s = other.t = 0;
+      for (int k = 0; k < count && ok; ++k) ok = step(k);
       Seg end;
       end.b = -1;
-      int X = 0;
-      if (!kPair && share == 0 && cnt[1] == 0) ok = publish(1, 0, end);  // an idle group leaves at once
-      for (int j = 0; j < cnt[0] + cnt[1] && ok; ++j) {
-        if (owner(j) != X) {
-          const Stream t = S;
-          S = other;
-          other = t;
-          X ^= 1;
-        }
-        ok = step(S, X, j);
-      }
-      if (ok && share == 0) ok = publish(X, S.s, end) && (kPair || cnt[1] == 0 || publish(X ^ 1, other.s, end));
+      if (ok) ok = publish(end);
       if (!ok)  // gave up: the copies in flight land before the shared memory goes
-        for (int x = max(0, issued - kSlots); x < issued; ++x) mbar_wait(&bFull[x % kSlots], (x / kSlots) & 1);
+        for (int x = max(0, issued - kSlots); x < issued; ++x)
+          if (owner(x >> 1) == X) mbar_wait(&bFull[x % kSlots], (x / kSlots) & 1);
     } else if (warp == kCleanWarp) {
       // ---------------------------------------------------------- tiles in order, rows past a request's end
       struct Walk {
@@ -998,8 +993,9 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
 // order.  Latency bounds it where there is little to join, and else what the parts
 // hold (up to 40 MB, in the L2).  There are fewer cuts than parts, so each CTA looks
 // through all of them (those that are the first through their item stand for it)
-// and takes its share of the cut items' chunks, however many items there are; with a grid over the items most CTAs find nothing to do: 152 requests of
-// 1072 tokens with 192 rows 167 us so, 211 us with it.
+// and takes its share of the cut items' chunks, however many items there are; with
+// a grid over the items most CTAs find nothing to do: 152 requests of 1072 tokens
+// with 192 rows 167 us so, 211 us with it.
 //   kShare = 1: a thread takes 16 columns of a row, two parts in flight, a chunk is
 //     a warp's width of those;
 //   kShare = 8, where items have four parts or more each and about every chunk has an
@@ -1265,6 +1261,7 @@ extern "C" msa_status msa_attn_tree(const msa_shape* shape, const void* q, const
   cudaStream_t stm = (cudaStream_t)stream;
   const bool d128 = shape->d_h == 128;
   if (a.R <= 64) return d128 ? launch_tree<128, kFew>(maps, a, join, stm) : launch_tree<64, kFew>(maps, a, join, stm);
-  if (a.R <= 128) return d128 ? launch_tree<128, kMany>(maps, a, join, stm) : launch_tree<64, kMany>(maps, a, join, stm);
+  if (a.R <= 128)
+    return d128 ? launch_tree<128, kMany>(maps, a, join, stm) : launch_tree<64, kMany>(maps, a, join, stm);
   return d128 ? launch_tree<128, kTwo>(maps, a, join, stm) : launch_tree<64, kTwo>(maps, a, join, stm);
 }
