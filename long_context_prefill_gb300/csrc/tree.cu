@@ -899,10 +899,16 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
       // ---- the segment's end: O / l and LSE, or the part's unnormalised state.
       // O goes to registers first, so that the next segment's products may start
       // while it is written.
+      const bool joins = kRows == kMany && (g.r0 != g.t0 || g.r1 != g.t1);
+      const bool whole = g.r0 == 0 && g.r1 == g.tiles;
+      const int64_t grow = (int64_t)(g.b * A.Hq + g.kvh * (A.Hq / A.Hkv)) * A.n + rr;
+      const int width = min(256, A.R - 256 * rb), full = min(256, A.R), rw = rr - 256 * rb;
+      const int64_t slot = 2 * part_of(W, kMost, blockIdx.x, kPair || joins ? 0 : X) + (g.r0 > 0 ? 0 : 1);
+      bool some = !(l == 0.f);  // an attended key (a NaN among them shows in l)
+      float inv = some ? 1.f / l : 0.f;
       if (kPair && rows > 0 ? !pv_done()
                             : !mbar_wait(&bars[kBarODone + X], (kPair ? idle++ : s) & 1)) { ok = false; break; }
       tc_fence_after();
-      const bool joins = kRows == kMany && (g.r0 != g.t0 || g.r1 != g.t1);
       float w0 = 1.f, w1 = 0.f;
       if (joins) {  // both groups' last segments, once per CTA: each takes half of the columns of both O's
         float2* ml = reinterpret_cast<float2*>(sm + Ly::kML);
@@ -918,13 +924,9 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
         w1 = ex2(b.x - ref);
         m_used = m;
         l = a.y * w0 + b.y * w1;
+        some = !(l == 0.f);
+        inv = some ? 1.f / l : 0.f;
       }
-      const bool whole = g.r0 == 0 && g.r1 == g.tiles;
-      const bool some = !(l == 0.f);  // an attended key (a NaN among them shows in l)
-      const int64_t grow = (int64_t)(g.b * A.Hq + g.kvh * (A.Hq / A.Hkv)) * A.n + rr;
-      const float inv = some ? 1.f / l : 0.f;
-      const int width = min(256, A.R - 256 * rb), full = min(256, A.R), rw = rr - 256 * rb;
-      const int64_t slot = 2 * part_of(W, kMost, blockIdx.x, kPair || joins ? 0 : X) + (g.r0 > 0 ? 0 : 1);
       // N columns from c0 on
       auto write = [&](const float* ov, int c0, auto N) {
         if (!row_ok) return;
