@@ -11,14 +11,15 @@
 //   pages r >= G go to stack[count + R - 1 - r];  count' = count + R - G.
 // Growing and then shrinking by the same amounts restores the stack exactly.
 //
-// What bounds it: latency.  A decode step of 64 requests moves about 2 KB (4.3 us),
-// the prefill of 64 prompts with pages of 16 moves 2.8 MB (6.1 us), a step of 1021
-// requests' trees 0.6 MB (8.4 us).  So one launch does everything: every CTA scans
-// all requests on its own (a few KB out of L2, cheaper than a second launch that
-// waits for the first) and fills its share of the tables.  No entry that one CTA
-// reads is written by another (grants go to table entries at or above a request's
-// old page count, pushes to stack entries at or above `count`), except the lengths
-// and the count themselves: the CTA that finishes last, by a ticket, writes those.
+// What bounds it: latency.  A decode step of 64 requests moves about 2 KB (4.3 to
+// 5.1 us), the prefill of 64 prompts with pages of 16 moves 2.8 MB (6.1 us), a step
+// of 1021 requests' trees 0.6 MB (8.4 us).  So one launch does everything: every CTA
+// scans all requests on its own (a few KB out of L2, cheaper than a second launch
+// that waits for the first) and fills its share of the tables.  No entry that one
+// CTA reads is written by another (grants go to table entries at or above a
+// request's old page count, pushes to stack entries at or above `count`), except the
+// lengths and the count themselves: the CTA that finishes last, by a ticket, writes
+// those.
 #include "internal.h"
 
 namespace msa {

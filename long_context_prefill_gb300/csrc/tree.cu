@@ -50,16 +50,18 @@
 //          tile that is free again once they are in its registers, so a group's
 //          next scores do not wait for its product with V.
 //
-// Measured (captured, 40 heads of 128 as 32 / 8): decode of 64 requests of 1K to
-// 16K tokens 188 to 193 us (6.7 TB/s, 0.98 of the measured copy rate), a
-// million-token context with 5 drafted tokens 590 us (7.3 TB/s), 128K with a tree
-// of 32 (128 rows) 88 to 91 us (0.88 of the floor), one request of 300 tokens
-// 9.5 us (two kernels' latency), 16 trees of up to 48 (192 rows) over 4K to
-// 32K 164 us (0.73: the two groups' softmax takes 1900 cycles of a scheduler's
-// 3040 a tile, and the products with Q read 8 KB of shared memory per 64 cycles,
-// its whole rate, beside the loads that land there).  Tried and slower there: a
-// score tile per group with P over it 194 us, turns of the groups on a scheduler
-// 192 to 253 us, scores by halves of 64 keys 208 us.
+// Measured (captured, 32 / 8 heads of 128): decode of 64 requests of 1K to 16K
+// tokens 188 to 191 us (6.7 TB/s, 0.98 of the measured copy rate), of 256 requests
+// of 100 to 1000 tokens 76.5 us (floor 58), a million-token context with 5 drafted
+// tokens 585 us (7.3 TB/s), 128K with a tree of 32 (128 rows) 88 to 90 us (0.89 of
+// the floor), 16 trees of up to 48 (192 rows) over 4K to 32K 164 us (0.73); one
+// request of 2047 tokens with 2 / 1 heads of 64 10 us (two kernels' latency).  kTwo
+// takes 1.70 us a tile (1.47 at HBM speed): the groups' scores go through one TMEM
+// tile in turn, 560 to 1000 cycles from the reading of one's to the issue of the
+// other's and 950 to compute them (1400 where a product with V runs beside).  Tried
+// and slower there (against 162 to 174 us): a score tile per group with P over it
+// 194 us, turns of the groups on a scheduler 192 to 253 us, scores by halves of 64
+// keys 208 us, products held back while scores are computed 175 us.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <string.h>
