@@ -443,13 +443,12 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
         return true;
       };
       auto entry = [&](const Seg& g, int p) {
-        const int np = (g.L + P - 1) >> A.page_shift;
-        int page = p < np ? A.table[(int64_t)g.b * A.max_pages + p] : 0;
-        if ((unsigned)page >= (unsigned)A.num_pages) {  // skipped: an existing page stands in, the call has failed
-          atomicCAS(A.err, 0, (int)kErrIndex);
-          page = 0;
-        }
-        return page;
+        return p < (g.L + P - 1) >> A.page_shift ? A.table[(int64_t)g.b * A.max_pages + p] : 0;
+      };
+      auto checked = [&](int page) {
+        if ((unsigned)page < (unsigned)A.num_pages) return page;
+        atomicCAS(A.err, 0, (int)kErrIndex);  // skipped: an existing page stands in, the call has failed
+        return 0;
       };
       // The next segment: its descriptor, its Q rows, its first page entries.
       auto open = [&]() -> bool {
@@ -481,6 +480,10 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
           }
         }
         pos += g.t1 - g.t0;
+        t = g.t0;
+        base = g.t0 << pshift;
+        ids = entry(g, base + lane);  // on their way until the Q rows are
+        ahead = entry(g, base + 32 + lane);
         if (!publish(g)) return false;
         const int buf = s % kQBufs;
         if (!mbar_wait_idle(&bars[kBarQEmpty + 2 * X + buf], ((s / kQBufs) & 1) ^ 1, kIdleNs)) return false;
@@ -495,10 +498,8 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
           tma_load_3d(to, &M.q, full, 64 * c, qrow + r, 0);
         }
         ++s;
-        t = g.t0;
-        base = g.t0 << pshift;
-        ids = entry(g, base + lane);
-        ahead = entry(g, base + 32 + lane);
+        ids = checked(ids);
+        ahead = checked(ahead);
         return true;
       };
       // Before a slot's wait: the use of the slot before is loaded, if that is the other loader's task, so that the
@@ -522,7 +523,7 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
           base += 32;
           off -= 32;
           ids = ahead;
-          ahead = entry(g, base + 32 + lane);
+          ahead = checked(entry(g, base + 32 + lane));
         }
         const int np = (g.L + P - 1) >> A.page_shift;
         const int boxes = min(pp, np - (t << pshift)) * (D / 64);  // pages of this tile that hold keys, by 64 columns
