@@ -735,9 +735,7 @@ def build_page_tables(pool: PagePool, new_len, seq_tokens: int = 0, tok_cap: int
     if not total and not (slots is None and positions is None and depth is None):
         raise ValueError("slots, positions, depth: need seq_tokens or tok_cap")
     if depth is not None:
-        if depth.numel() != total:
-            raise ValueError(f"depth: {depth.numel()} elements, expected {total}")
-        _want(depth, "depth", torch.int32, device=dev)
+        _per_token(depth, "depth", total, dev)
     if cu_new is not None:
         _same(cu_new, "cu_new", torch.int32, (S + 1,), dev)
     if slots is not None:

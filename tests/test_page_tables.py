@@ -89,6 +89,7 @@ def test_binding_refusals():
         (lambda: msa.build_page_tables(pool, new.long()), "new_len: dtype"),
         (lambda: msa.build_page_tables(pool, new, slots=new), "need seq_tokens"),
         (lambda: msa.build_page_tables(pool, new, seq_tokens=2, depth=new), "depth: 4 elements"),
+        (lambda: msa.build_page_tables(pool, new, seq_tokens=1, depth=[0] * 4), "depth: a torch.Tensor"),
         (lambda: msa.build_page_tables(pool, new, tok_cap=6, slots=new), "slots: shape"),
         (lambda: msa.build_page_tables(pool, new, tok_cap=-6), "tok_cap"),
         (lambda: msa.build_page_tables(pool, new), "page_table: must be on a CUDA device"),
