@@ -33,6 +33,9 @@ constexpr int kMaxRequests = 8192;  // five int32 per request in shared memory
 constexpr int kMaxCtas = 152;
 constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - (1 << 19);  // an index may step one round past the last token
 static_assert(4 * kMaxCtas * kThreads < 1 << 19, "indexes within int32");
+constexpr int scan_bytes(int requests) { return 5 * (requests + 1) * (int)sizeof(int32_t); }
+constexpr int kStaticBytes = 1024;  // at least the kernel's static shared memory
+static_assert(scan_bytes(kMaxRequests) + kStaticBytes <= 227 * 1024, "shared memory budget");
 
 struct PageArgs {
   int32_t S, N, shift, max_pages, T, cap;
@@ -90,6 +93,7 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const PageArgs A) 
   extern __shared__ int32_t sm[];
   __shared__ Sum3 part[kThreads / 32];
   __shared__ int s_last, s_refused;
+  static_assert(sizeof(part) + sizeof(s_last) + sizeof(s_refused) <= kStaticBytes, "static shared memory");
   int32_t* s_tok = sm;               // tokens of the requests before
   int32_t* s_gr = sm + (A.S + 1);    // pages granted before
   int32_t* s_rel = s_gr + (A.S + 1); // pages released before
@@ -323,9 +327,12 @@ extern "C" msa_status msa_build_page_tables(const msa_page_pool* pool, const int
   const int64_t moved = slots ? tok / pool->page_size + a.S : held;
   const int64_t want = (tok / 4 + moved / 4 + kThreads - 1) / kThreads;
   const int grid = (int)(want < 1 ? 1 : want > kMaxCtas ? kMaxCtas : want);
-  const int smem = 5 * (a.S + 1) * (int)sizeof(int32_t);
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(page_table_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-                              cudaSuccess)
+  const int smem = scan_bytes(a.S);
+  // The default limit of 48 KB counts the kernel's static bytes too.  It is raised to the same size whatever the call,
+  // so that it holds for calls of other sizes from other host threads.
+  if (smem + kStaticBytes > 48 * 1024 &&
+      cudaFuncSetAttribute(page_table_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, scan_bytes(kMaxRequests)) !=
+          cudaSuccess)
     return MSA_ERR_CUDA;
   page_table_kernel<<<grid, kThreads, smem, (cudaStream_t)stream>>>(a);
   note_launch();

@@ -4,6 +4,10 @@ CPU: the reference itself (growing and rolling back restores the pool) and the
 host checks.  GPU: every table, stack, slot and position equal to the reference's,
 over grow, shrink, mixed, refused and repeated calls."""
 import ctypes
+import os
+import subprocess
+import sys
+import threading
 
 import numpy as np
 import pytest
@@ -11,6 +15,8 @@ import torch
 
 import long_context_prefill_gb300 as msa
 from paged_ref import resize
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def _pool(rng, S, width, N, lens, page):
@@ -207,4 +213,55 @@ def test_captured_steps_follow_the_lengths(cuda_lib):
         torch.cuda.synchronize()
         assert slots.tolist() == ws and pos.tolist() == wp and pool.seq_len.tolist() == lens, step
     assert pool.page_table.tolist() == table and pool.state.tolist() == state
+    assert cuda_lib.poll_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sizes", [[2437, 2438, 2456, 2457, 8192], [8192, 2438]])
+def test_many_requests_in_a_fresh_process(cuda_lib, sizes):
+    """Tables of up to the 8192 requests a pool may have, around the size whose scans need more shared memory than a
+    kernel has by default; each size as the first of its kind in a process, and after a larger one."""
+    code = f"""
+import sys
+sys.path[:0] = {[ROOT, os.path.join(ROOT, "tests")]!r}
+import torch
+import long_context_prefill_gb300 as msa
+from paged_ref import resize
+for S in {sizes}:
+    pool = msa.PagePool.empty(S, 3, 2 * S, 16, "cuda")
+    table, lens, stack, state = [[-1] * 3 for _ in range(S)], [0] * S, list(range(2 * S - 1, -1, -1)), [2 * S, 0, 0, 0]
+    for new in ([(7 * s) % 33 for s in range(S)], [(5 * s) % 49 for s in range(S)], [0] * S):
+        got = msa.build_page_tables(pool, torch.tensor(new, dtype=torch.int32, device="cuda"), tok_cap=24 * S)
+        want = resize(table, lens, stack, state, new, 16, tok_cap=24 * S)
+        assert [t.tolist() for t in got] == list(want), S
+        assert pool.seq_len.tolist() == lens and pool.free_pages.tolist() == stack and pool.state.tolist() == state, S
+        assert pool.page_table.tolist() == table, S
+assert msa.poll_device_status() == 0
+"""
+    run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0, run.stderr[-2000:]
+
+
+@pytest.mark.gpu
+def test_pools_of_different_sizes_from_two_threads(cuda_lib):
+    """Two host threads, each with its own pool and stream, of sizes that need different amounts of shared memory."""
+    def work(S, failed):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                pool = msa.PagePool.empty(S, 2, 2 * S, 16, "cuda")
+                lens = [torch.full((S,), x, dtype=torch.int32, device="cuda") for x in (17, 0)]
+                for x in range(400):
+                    msa.build_page_tables(pool, lens[x & 1])
+                msa.build_page_tables(pool, lens[0])
+                assert bool((pool.seq_len == 17).all()) and pool.state.tolist() == [0, 0, 0, 0]
+        except Exception as e:  # noqa: BLE001  (a thread's failure is the test's)
+            failed.append((S, e))
+
+    failed = []
+    threads = [threading.Thread(target=work, args=(S, failed)) for S in (2600, 8192)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
     assert cuda_lib.poll_device_status() == 0
