@@ -156,7 +156,9 @@ struct Lay {
   static constexpr int kBars = kML + 2 * 128 * 8;
   static constexpr int kNumBars = kBarRing + 3 * kSlots;
   static constexpr int kMisc = kBars + kNumBars * 8;  // [0] TMEM base, [2] abort, [4 + X] tiles loaded
-  static constexpr int kAlloc = kMisc + 32;
+  static constexpr int kStart = kMisc + 32;           // [X][2] int64: request in which a part begins, its first tile
+  static constexpr int kAlloc = kStart + 32;
+  static_assert(kStart % 8 == 0 && kML % 8 == 0, "int64 in shared memory");
   static_assert(kAlloc <= 227 * 1024 && kAlloc > 120 * 1024, "shared memory: one CTA per SM");
 };
 
@@ -315,8 +317,11 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
   }
   // ---- this CTA's parts of the line of tiles, and the requests they start in
   const int items = A.Hkv * A.RB;  // items of a request
-  int64_t* wsum = reinterpret_cast<int64_t*>(sm + Ly::kML);    // (used again at the end, for maxima and sums)
-  int64_t* start = wsum + 16;                                  // [X][2]: request, its first tile
+  // The warps' sums lie where kMany's maxima and sums come at the end: they are read before the __syncthreads below, and
+  // those are written by the roles behind it.  `start` is read by the loaders and the cleaner as they begin, and group 0
+  // may have its maxima while the loader of group 1 has not begun yet: it has bytes of its own.
+  int64_t* wsum = reinterpret_cast<int64_t*>(sm + Ly::kML);
+  int64_t* start = reinterpret_cast<int64_t*>(sm + Ly::kStart);
   int64_t W = 0;                                               // all tiles
   {
     const int per = (A.B + kThreads - 1) / kThreads;

@@ -481,3 +481,21 @@ def test_prefill_draft_verify_together(cuda_lib):
     msa.build_page_tables(pool, torch.zeros(2, **i32))
     assert pool.state.tolist() == [150, 0, 0, 0] and sorted(pool.free_pages.tolist()) == list(range(150))
     assert math.isfinite(float(oc.float().sum()))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("tiles", [303, 304, 305, 400, 606, 607, 608])
+def test_parts_of_one_and_two_tiles(cuda_lib, tiles, d):
+    """65 to 128 rows a KV head over about as many tiles as there are parts: a CTA's first group is done after one tile,
+    and joins with the second; one item over all parts, and items that begin inside them."""
+    rng = np.random.default_rng(tiles)
+    for lens in ([128 * tiles - 5], [128 * (tiles - 7) - 100, 128 * 2, 128 * 5 - 60]):
+        n = 20  # 80 rows
+        masks = np.stack([tree_bits(rng, n) for _ in lens])
+        c = Case(4, 1, n, d, 64, lens, 10 + tiles, tls=[n, 3, n][:len(lens)], masks=masks)
+        out = c.run()
+        assert cuda_lib.poll_device_status() == 0
+        c.check(out, what=f"{tiles} tiles")
+        again = c.run()
+        assert torch.equal(out[0], again[0]) and torch.equal(out[1], again[1])
