@@ -92,6 +92,7 @@ constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
 constexpr int kPChunk = 4;
 constexpr uint32_t kIdleNs = 64;
+constexpr uint64_t kDrainNs = MSA_WAIT_LIMIT_NS / 16;  // a CTA that gave up: for each copy and product in flight
 constexpr int kMaxDrafts = 1024;
 
 struct Cut;
@@ -140,7 +141,8 @@ enum {
   kBarPV = 16,                           // [X] kTwo: the group's last P has been used
   kBarSFree = 18,                        // kTwo: the scores are in registers
   kBarML = 19,                           // kMany: both groups' maxima and sums are written
-  kBarSegFull = 20,                      // [X][kSegSlots]
+  kBarDrain = 20,                        // [issuer] after giving up: its products are done
+  kBarSegFull = 22,                      // [X][kSegSlots]
   kBarSegEmpty = kBarSegFull + 2 * kSegSlots,
   kBarRing = kBarSegEmpty + 2 * kSegSlots  // full[kSlots], empty[kSlots], ready[kSlots]
 };
@@ -155,9 +157,10 @@ struct Lay {
   static constexpr int kML = kSeg + 2 * kSegSlots * (int)sizeof(Seg);  // kMany: [2][128] maximum and row sum
   static constexpr int kBars = kML + 2 * 128 * 8;
   static constexpr int kNumBars = kBarRing + 3 * kSlots;
-  static constexpr int kMisc = kBars + kNumBars * 8;  // [0] TMEM base, [2] abort, [4 + X] tiles loaded
+  static constexpr int kMisc = kBars + kNumBars * 8;  // [0] TMEM base, [2] abort, [4 + X] tiles loaded, [6 + X] Q's asked for
   static constexpr int kStart = kMisc + 32;           // [X][2] int64: request in which a part begins, its first tile
-  static constexpr int kAlloc = kStart + 32;
+  static constexpr int kLast = kStart + 32;           // [X][kSlots] the last ring load of loader X into a slot, -1: none
+  static constexpr int kAlloc = kLast + 2 * kSlots * 4;
   static_assert(kStart % 8 == 0 && kML % 8 == 0, "int64 in shared memory");
   static_assert(kAlloc <= 227 * 1024 && kAlloc > 120 * 1024, "shared memory: one CTA per SM");
 };
@@ -276,6 +279,7 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
   uint64_t* bReady = bEmpty + kSlots;
   Seg* segs = reinterpret_cast<Seg*>(sm + Ly::kSeg);  // [2][kSegSlots]
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(sm + Ly::kMisc);
+  volatile int* lasts = reinterpret_cast<volatile int*>(sm + Ly::kLast);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -300,6 +304,7 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
       mbar_init(&bars[kBarODone + x], 1);
       mbar_init(&bars[kBarOFree + x], kGroupWarps);
       mbar_init(&bars[kBarPV + x], 1);
+      mbar_init(&bars[kBarDrain + x], 1);
     }
     mbar_init(&bars[kBarSFree], 4);
     mbar_init(&bars[kBarML], 8);
@@ -436,6 +441,7 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
       int64_t at = start[2 * X + 1], pos = X ? begin[1] : begin[0];  // first tile of request b, of the next segment
       const int64_t hi = pos + count;                                // the part's end
       int b = (int)start[2 * X], s = 0, t = 0;        // request, segments so far, next tile of the segment
+      int last = -1, asked = 0;  // the last ring load into slot `lane`; segments whose Q was asked for
       Seg g;
       int base, ids, ahead;  // lane x holds the page of entry base + x, and of base + 32 + x
       auto publish = [&](const Seg& g) -> bool {
@@ -495,6 +501,7 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
         const int rows = min(kPair ? 256 : 128, A.R - 256 * g.rb), boxes = (rows + A.q_box - 1) / A.q_box;
         uint64_t* full = &bars[kBarQFull + 2 * X + buf];
         if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(boxes * A.q_box * D * 2));
+        ++asked;
         __syncwarp();
         const int qrow = (g.b * A.Hq + g.kvh * (A.Hq / A.Hkv)) * A.n + 256 * g.rb;
         if (lane < boxes * (D / 64)) {  // at most 8
@@ -519,7 +526,6 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
           if (misc[2] || global_timer_ns() - since > MSA_WAIT_LIMIT_NS) return false;
         return true;
       };
-      int issued = 0;  // the ring's loads up to here are past
       // the part's tile k
       auto step = [&](int k) -> bool {
         if ((s == 0 || t == g.t1) && !open()) return false;
@@ -541,7 +547,7 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
           if (!mbar_wait_idle(&bEmpty[st], ((idx / kSlots) & 1) ^ 1, kIdleNs)) return false;
           if (lane == 0) mbar_arrive_expect_tx(&bFull[st], (uint32_t)(boxes * P * 128));
           __syncwarp();
-          issued = idx + 1;
+          last = lane == st ? idx : last;
           if (lane < boxes)
             tma_load_3d_hint(sm + Ly::kRing + st * Ly::kTile + c * 16384 + x * P * 128, is_v ? &M.v : &M.k, &bFull[st],
                              64 * c, krow, 0, policy);
@@ -555,9 +561,8 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
       Seg end;
       end.b = -1;
       if (ok) ok = publish(end);
-      if (!ok)  // gave up: the copies in flight land before the shared memory goes
-        for (int x = max(0, issued - kSlots); x < issued; ++x)
-          if (owner(x >> 1) == X) mbar_wait(&bFull[x % kSlots], (x / kSlots) & 1);
+      if (lane < kSlots) lasts[X * kSlots + lane] = last;
+      if (lane == 0) misc[6 + X] = asked;
     } else if (warp == kCleanWarp) {
       // ---------------------------------------------------------- tiles in order, rows past a request's end
       struct Walk {
@@ -1027,6 +1032,24 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
 
   tc_fence_before();
   __syncthreads();
+  if (misc[2]) {
+    // A role gave up, so others may have left copies and products in flight that nobody waited for, whether or not they
+    // gave up themselves: those end before the CTA's shared memory and TMEM go.
+    if (warp == kMmaWarp0 || warp == kMmaWarp1) {
+      uint64_t* drained = &bars[kBarDrain + (warp == kMmaWarp0 ? 0 : 1)];
+      if (lane == 0) mma_commit(drained);
+      mbar_wait(drained, 0, kDrainNs);
+    } else if (warp == kLoaderWarp || (!kPair && warp == kLoaderWarp1)) {
+      const int X = warp == kLoaderWarp ? 0 : 1, asked = misc[6 + X];
+      for (int x = max(0, asked - kQBufs); x < asked; ++x)
+        mbar_wait(&bars[kBarQFull + 2 * X + x % kQBufs], (x / kQBufs) & 1, kDrainNs);
+      // A slot's last load only: the one before had landed and been used.
+      const int x = lane < kSlots ? lasts[X * kSlots + lane] : -1;
+      if (x >= 0 && (kPair || x > lasts[(X ^ 1) * kSlots + lane])) mbar_wait(&bFull[lane], (x / kSlots) & 1, kDrainNs);
+      __syncwarp();
+    }
+    __syncthreads();
+  }
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
