@@ -693,23 +693,47 @@ def _pages(k_pages, v_pages, Hkv, d, device):
 class PagePool:
     """The requests that share a pool of cache pages (msa_page_pool): page_table
     [n_seqs, max_pages], seq_len [n_seqs], free_pages [num_pages] (a stack) and
-    state [4], int32 tensors that build_page_tables updates in place."""
+    state [4], int32 tensors that build_page_tables updates in place.  They may
+    be replaced: each call checks and uses the ones that are there."""
 
     def __init__(self, page_table, seq_len, free_pages, state, page_size: int):
-        if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        self.__dict__.update(page_table=page_table, seq_len=seq_len, free_pages=free_pages, state=state,
+                             page_size=int(page_size), _held=None)
+        self.view()
+
+    def __setattr__(self, name, value):
+        self.__dict__[name] = value
+        self.__dict__["_held"] = None
+
+    def view(self):
+        """The tensors' C view."""
+        return self._hold()[0]
+
+    def _hold(self):
+        """(C view, n_seqs, device, addresses, storages), checked anew when a tensor was replaced or its memory was.
+        The storages are held so that an address which was checked is not another tensor's."""
+        held = self._held
+        if held is not None and held[3] == (self.page_table.data_ptr(), self.seq_len.data_ptr(),
+                                            self.free_pages.data_ptr(), self.state.data_ptr()):
+            return held
+        table, lens, stack, state = self.page_table, self.seq_len, self.free_pages, self.state
+        if not isinstance(table, torch.Tensor) or table.dim() != 2:
             raise ValueError("page_table: a 2-d tensor [n_seqs, max_pages] is required")
-        if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
+        if not isinstance(stack, torch.Tensor) or stack.dim() != 1:
             raise ValueError("free_pages: a 1-d tensor [num_pages] is required")
-        S, width = page_table.shape
-        dev = page_table.device
-        _want(page_table, "page_table", torch.int32)
-        _same(seq_len, "seq_len", torch.int32, (S,), dev)
-        _want(free_pages, "free_pages", torch.int32, device=dev)
+        S, width = table.shape
+        N, dev = stack.shape[0], table.device
+        _same(table, "page_table", torch.int32, (S, width), dev)
+        _same(lens, "seq_len", torch.int32, (S,), dev)
+        _same(stack, "free_pages", torch.int32, (N,), dev)
         _same(state, "state", torch.int32, (4,), dev)
-        self.page_table, self.seq_len, self.free_pages, self.state = page_table, seq_len, free_pages, state
-        self.page_size = int(page_size)
-        self._c = PagePoolC(S, free_pages.shape[0], self.page_size, width, page_table.data_ptr(), seq_len.data_ptr(),
-                            free_pages.data_ptr(), state.data_ptr())
+        if not 0 < self.page_size < 1 << 31:
+            raise ValueError(f"page_size: {self.page_size}")
+        at = (table.data_ptr(), lens.data_ptr(), stack.data_ptr(), state.data_ptr())
+        held = (PagePoolC(S, N, self.page_size, width, *at), S, dev, at, table.untyped_storage(), lens.untyped_storage(),
+                stack.untyped_storage(), state.untyped_storage())
+        self.__dict__["_held"] = held
+        return held
 
     @staticmethod
     def empty(n_seqs: int, max_pages: int, num_pages: int, page_size: int, device) -> "PagePool":
@@ -727,7 +751,7 @@ def build_page_tables(pool: PagePool, new_len, seq_tokens: int = 0, tok_cap: int
     new_len [n_seqs].  Returns (cu_new, slots, positions): with seq_tokens = T
     [n_seqs * T] padded, with tok_cap [tok_cap] packed token outputs, with
     neither None (a call that only resizes)."""
-    S, dev = pool._c.n_seqs, pool.page_table.device
+    c, S, dev = pool._hold()[:3]
     _same(new_len, "new_len", torch.int32, (S,), dev)
     if seq_tokens < 0 or tok_cap < 0:
         raise ValueError("seq_tokens, tok_cap: must not be negative")
@@ -742,7 +766,7 @@ def build_page_tables(pool: PagePool, new_len, seq_tokens: int = 0, tok_cap: int
         _same(slots, "slots", torch.int32, (total,), dev)
     if positions is not None:
         _same(positions, "positions", torch.int32, (total,), dev)
-    if not pool.page_table.is_cuda:
+    if not new_len.is_cuda:
         _cuda(page_table=pool.page_table)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
@@ -754,7 +778,7 @@ def build_page_tables(pool: PagePool, new_len, seq_tokens: int = 0, tok_cap: int
             slots = torch.empty(total, dtype=torch.int32, device=dev)
         if positions is None:
             positions = torch.empty(total, dtype=torch.int32, device=dev)
-    st = load().msa_build_page_tables(ctypes.byref(pool._c), new_len.data_ptr(), _at(depth), int(seq_tokens),
+    st = load().msa_build_page_tables(ctypes.byref(c), new_len.data_ptr(), _at(depth), int(seq_tokens),
                                       int(tok_cap), cu_new.data_ptr(), _at(slots), _at(positions),
                                       torch._C._cuda_getCurrentRawStream(dev.index))
     if st:

@@ -265,3 +265,48 @@ def test_pools_of_different_sizes_from_two_threads(cuda_lib):
         t.join()
     assert not failed, failed
     assert cuda_lib.poll_device_status() == 0
+
+
+def test_pool_follows_its_tensors():
+    """A tensor put in another's place, or one whose storage was replaced, is the one that the next call uses; one that
+    does not fit is refused by name."""
+    pool = msa.PagePool.empty(4, 8, 64, 16, "cpu")
+    i32 = dict(dtype=torch.int32)
+    old = [pool.page_table, pool.seq_len, pool.free_pages, pool.state]
+    pool.page_table, pool.seq_len = torch.zeros(4, 9, **i32), torch.ones(4, **i32)
+    pool.free_pages, pool.state = torch.zeros(70, **i32), torch.zeros(4, **i32)
+    c = pool.view()
+    assert (c.n_seqs, c.num_pages, c.page_size, c.max_pages) == (4, 70, 16, 9)
+    assert [c.page_table, c.seq_len, c.free_pages, c.state] == [
+        t.data_ptr() for t in (pool.page_table, pool.seq_len, pool.free_pages, pool.state)]
+    assert all(t.data_ptr() != getattr(c, k) for t, k in zip(old, ("page_table", "seq_len", "free_pages", "state")))
+    pool.seq_len.data = torch.full((4,), 5, **i32)
+    assert pool.view().seq_len == pool.seq_len.data_ptr()
+    new = torch.zeros(4, **i32)
+    for name, bad, what in [("seq_len", torch.zeros(3, **i32), "seq_len: shape"), ("state", torch.zeros(4), "state: dtype"),
+                            ("free_pages", new[None], "free_pages: a 1-d"), ("page_table", new, "page_table: a 2-d"),
+                            ("page_table", torch.zeros(4, 9, **i32).t(), "page_table: must be contiguous"),
+                            ("page_size", 1 << 32, "page_size")]:
+        keep = getattr(pool, name)
+        setattr(pool, name, bad)
+        with pytest.raises(ValueError, match=what):
+            msa.build_page_tables(pool, new)
+        setattr(pool, name, keep)
+    pool.seq_len.data = torch.zeros(3, **i32)
+    with pytest.raises(ValueError, match="seq_len: shape"):
+        msa.build_page_tables(pool, new)
+
+
+@pytest.mark.gpu
+def test_pool_with_a_tensor_replaced(cuda_lib):
+    pool = msa.PagePool.empty(2, 4, 8, 16, "cuda")
+    first = pool.seq_len
+    pool.seq_len = torch.zeros(2, dtype=torch.int32, device="cuda")
+    msa.build_page_tables(pool, torch.tensor([20, 3], dtype=torch.int32, device="cuda"))
+    assert pool.seq_len.tolist() == [20, 3] and first.tolist() == [0, 0]
+    second = pool.seq_len.detach()  # keeps the storage
+    pool.seq_len.data = torch.tensor([20, 3], dtype=torch.int32, device="cuda")
+    msa.build_page_tables(pool, torch.tensor([33, 0], dtype=torch.int32, device="cuda"))
+    assert pool.seq_len.tolist() == [33, 0] and second.tolist() == [20, 3]
+    assert pool.state.tolist() == [5, 0, 0, 0]
+    assert cuda_lib.poll_device_status() == 0
