@@ -787,16 +787,19 @@ def build_page_tables(pool: PagePool, new_len, seq_tokens: int = 0, tok_cap: int
 
 
 class RopeCfg:
-    """How qk_norm_rope treats a head (msa_rope_cfg); see rope_cfg()."""
+    """How qk_norm_rope treats a head (msa_rope_cfg); see rope_cfg().  q_weight and k_weight may be replaced: each call
+    checks and uses the ones that are there."""
 
     def __init__(self, c, q_weight, k_weight, inv_freq):
         self.c, self.q_weight, self.k_weight, self.inv_freq = c, q_weight, k_weight, inv_freq
 
     def check(self, d, device):
-        if self.q_weight is not None:
-            _same(self.q_weight, "q_weight", torch.bfloat16, (d,), device)
-        if self.k_weight is not None:
-            _same(self.k_weight, "k_weight", torch.bfloat16, (d,), device)
+        q, k, c = self.q_weight, self.k_weight, self.c
+        if q is not None:
+            _same(q, "q_weight", torch.bfloat16, (d,), device)
+        if k is not None:
+            _same(k, "k_weight", torch.bfloat16, (d,), device)
+        c.q_weight, c.k_weight = _at(q), _at(k)
 
 
 def rope_cfg(rot_dim: int, theta: float = 10000.0, interleaved: bool = False, norm: bool = False, eps: float = 1e-6,
@@ -810,7 +813,7 @@ def rope_cfg(rot_dim: int, theta: float = 10000.0, interleaved: bool = False, no
         if len(vals) != int(rot_dim) // 2:
             raise ValueError(f"inv_freq: {len(vals)} values, expected {int(rot_dim) // 2}")
         arr = (ctypes.c_double * len(vals))(*vals)
-    c = RopeCfgC(1 if norm else 0, float(eps), _at(q_weight), _at(k_weight), int(rot_dim), 1 if interleaved else 0,
+    c = RopeCfgC(1 if norm else 0, float(eps), None, None, int(rot_dim), 1 if interleaved else 0,
                  float(theta), arr, float(rot_scale))
     return RopeCfg(c, q_weight, k_weight, arr)
 

@@ -254,3 +254,27 @@ def test_streams_and_capture(cuda_lib):
         torch.cuda.synchronize()
         for a, b in zip(out, want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_weights_replaced_in_a_config(cuda_lib):
+    """A config follows its weights: another tensor in their place, new storage of the same tensor."""
+    q, k, v, w = _inputs(9, 4, 2, 128, 8)
+    x = [t[None] for t in (q, k, v)]
+    cfg = msa.rope_cfg(128, norm=True, q_weight=w[0].clone(), k_weight=w[1].clone())
+    first = (cfg.q_weight, cfg.k_weight.detach())  # keeps the storages
+    cfg.q_weight = 2 * w[0]
+    cfg.k_weight.data = 4 * w[1]
+    got = msa.qk_norm_rope(*x, cfg)
+    want = msa.qk_norm_rope(*x, msa.rope_cfg(128, norm=True, q_weight=2 * w[0], k_weight=4 * w[1]))
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    cfg.q_weight = None
+    got = msa.qk_norm_rope(*x, cfg)
+    want = msa.qk_norm_rope(*x, msa.rope_cfg(128, norm=True, k_weight=4 * w[1]))
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    cfg.k_weight.data = torch.ones(64, dtype=BF, device="cuda")
+    with pytest.raises(ValueError, match="k_weight: shape"):
+        msa.qk_norm_rope(*x, cfg)
+    assert first[0].shape == first[1].shape
