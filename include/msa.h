@@ -446,8 +446,10 @@ typedef struct {
  *   pages     (nullable) K and V also go to the cache at slots[t], each slot
  *             named at most once; a negative slot is not stored, one outside
  *             the pool neither, and the next poll returns MSA_ERR_INDEX
- *   positions [B * n], any int32 (angles are exact to about 2^-31 turns
- *             wherever the position lies); NULL: the index in the sequence
+ *   positions [B * n], any int32; NULL: the index in the sequence.  An angle,
+ *             position times the f_i that is given or theta's in double, is off
+ *             by about 2^-26 turns at most wherever the position lies (fp32 in half
+ *             turns; |f_i| < 2^30)
  * Outputs must not overlap inputs. */
 MSA_API msa_status msa_qk_norm_rope(const msa_shape* shape, const msa_rope_cfg* cfg, const void* q_in,
                                     int64_t q_stride, const void* k_in, int64_t k_stride, const void* v_in,

@@ -12,7 +12,9 @@
 // Angles.  An fp32 product position * f_i has an error of 0.06 rad at a
 // position of a million.  The host turns f_i into F = f_i / (2 pi) in units of
 // 2^-64 turns; position * F in 64-bit integers wraps exactly at whole turns,
-// and its top 32 bits are the angle to 2^-31 half turns, whatever the position.
+// and its top 32 bits are the angle to 2^-31 turns, whatever the position.  It
+// is rounded to fp32 half turns in [-1, 1) for the sine and cosine: to 2^-26
+// turns at worst, and relative to the angle where that is near a whole turn.
 //
 // What bounds it: HBM, every value read once and written once per
 // destination.  A lane holds both members of its pairs (two 16-byte chunks, a
@@ -321,13 +323,17 @@ bool aligned(const void* p, size_t a, bool required) {
   return reinterpret_cast<uintptr_t>(p) % a == 0;
 }
 
-// f in units of 2^-64 turns: the fraction of f / (2 pi) (whole turns change nothing).
+// The fraction of x >= 0 in units of 2^-64 (exact: a double less its whole part is one, and has no more than 64 bits
+// above 2^-64).
+uint64_t fraction64(double x) { return (uint64_t)((x - floor(x)) * 0x1p64); }
+
+// f in units of 2^-64 turns: the fraction of f / (2 pi) (whole turns change nothing).  1 / (2 pi) in two doubles and the
+// product's rounding error by fma: off by two units at most as long as |f| < 2^30.
 uint64_t turns64(double f) {
-  double t = f * 0.15915494309189533577;
-  t -= floor(t);
-  const double hi = floor(t * 4294967296.0);
-  const double lo = floor((t * 4294967296.0 - hi) * 4294967296.0);
-  return ((uint64_t)hi << 32) + (uint64_t)lo;
+  constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;
+  const double a = fabs(f), p = a * kHi, e = fma(a, kHi, -p) + a * kLo;
+  const uint64_t t = fraction64(p) + (e < 0.0 ? 0 - fraction64(-e) : fraction64(e));
+  return f < 0.0 ? 0 - t : t;
 }
 
 msa_status norm_rope(const msa_shape& s, const int32_t* cu, int32_t n_seqs, const msa_rope_cfg* cfg, const void* q_in,

@@ -4,6 +4,7 @@ CPU: host checks.  GPU: every value against the formula in 64 bits, within the
 fp32 bound of paged_ref.norm_rope and one bf16 rounding; V and the cache's
 other rows bit for bit."""
 import ctypes
+import math
 
 import numpy as np
 import pytest
@@ -278,3 +279,55 @@ def test_weights_replaced_in_a_config(cuda_lib):
     with pytest.raises(ValueError, match="k_weight: shape"):
         msa.qk_norm_rope(*x, cfg)
     assert first[0].shape == first[1].shape
+
+
+def _inverse_two_pi(bits):
+    """2^bits / (2 pi), rounded down (Machin's formula in integers)."""
+    one = 1 << (bits + 80)
+
+    def atan_inverse(x):
+        term, total, k = one // x, one // x, 1
+        while term:
+            term //= -x * x
+            k += 2
+            total += term // k
+        return total
+
+    pi = 4 * (4 * atan_inverse(5) - atan_inverse(239))  # pi 2^(bits + 80)
+    return (one << bits) // (2 * pi)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("size", [-8, 0, 18])
+def test_angles_near_whole_turns_at_far_positions(cuda_lib, size, sign):
+    """The angle itself at positions up to 2^31, where it lies within 2^-18 turns of a whole turn, so that the sine that
+    comes out is the angle: the reference is position * f / (2 pi) in exact integers."""
+    d, tok = 128, 64
+    rng = np.random.default_rng(size + 50)
+    unit = _inverse_two_pi(64 + 200)
+    # unrounded doubles of about 2^size
+    freq = [sign * float(x) * 2.0 ** size for x in rng.uniform(0.5, 1.0, d // 2)]
+    turn = []  # f / (2 pi) in 2^-64 turns
+    for f in freq:
+        num, den = f.as_integer_ratio()
+        turn.append((num * unit // (den << 200)) % (1 << 64))
+    turn = np.array(turn, np.uint64)
+    pos = np.zeros(tok, np.int64)
+    for t in range(tok):  # token t: a position where pair t comes close to a whole turn
+        p = rng.integers(1 << 30, 1 << 31, 1 << 20) * rng.choice([-1, 1], 1 << 20)
+        near = np.abs((p.astype(np.uint64) * turn[t]).view(np.int64).astype(np.float64))
+        pos[t] = p[np.argmin(np.where(near < 2.0 ** 41, np.inf, near))]
+    x = torch.zeros(1, tok, 1, d, dtype=BF, device="cuda")
+    x[..., d // 2:] = 1  # (0, 1) -> (-sin, cos)
+    cfg = msa.rope_cfg(d, inv_freq=freq)
+    q, _, _ = msa.qk_norm_rope(x, x, x, cfg, positions=torch.from_numpy(pos.astype(np.int32)).cuda())
+    u = (pos.astype(np.uint64)[:, None] * turn[None]).view(np.int64) / 2.0 ** 63  # half turns in [-1, 1)
+    u = torch.from_numpy(u).cuda()
+    ref = torch.cat([-torch.sin(math.pi * u), torch.cos(math.pi * u)], 1)
+    near = torch.diagonal(u).abs()
+    assert bool((near < 2.0 ** -17).all())
+    # 32 bits of a turn, cut off (2^-31 half turns; the 64-bit product: 2^31 units of 2^-64 turns, 2^-32 half turns), then rounded to fp32; the
+    # sine or cosine of that to 2 steps
+    slack = math.pi * (1.5 * 2.0 ** -31 + u.abs() * 2.0 ** -24)
+    check_rounded(q[0, 0], ref, torch.cat([slack, slack], 1) + ref.abs() * 2.0 ** -22, "far angles")
