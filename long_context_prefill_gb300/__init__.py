@@ -756,6 +756,8 @@ def build_page_tables(pool: PagePool, new_len, seq_tokens: int = 0, tok_cap: int
     if seq_tokens < 0 or tok_cap < 0:
         raise ValueError("seq_tokens, tok_cap: must not be negative")
     total = S * seq_tokens if seq_tokens else tok_cap
+    if total >> 31 or tok_cap >> 31:
+        raise ValueError("seq_tokens, tok_cap: more than 2^31 - 1 token outputs")
     if not total and not (slots is None and positions is None and depth is None):
         raise ValueError("slots, positions, depth: need seq_tokens or tok_cap")
     if depth is not None:

@@ -310,3 +310,12 @@ def test_pool_with_a_tensor_replaced(cuda_lib):
     assert pool.seq_len.tolist() == [33, 0] and second.tolist() == [20, 3]
     assert pool.state.tolist() == [5, 0, 0, 0]
     assert cuda_lib.poll_device_status() == 0
+
+
+def test_token_counts_beyond_32_bits_are_refused():
+    """Counts that the library's 32-bit arguments would cut off (to 0: no tokens at all)."""
+    pool = msa.PagePool.empty(1, 8, 64, 16, "cpu")
+    new = torch.zeros(1, dtype=torch.int32)
+    for kw in (dict(seq_tokens=1 << 32), dict(tok_cap=1 << 32), dict(seq_tokens=1 << 31), dict(tok_cap=(1 << 33) + 5)):
+        with pytest.raises(ValueError, match="seq_tokens, tok_cap: more than"):
+            msa.build_page_tables(pool, new, **kw)
