@@ -450,7 +450,7 @@ typedef struct {
  *             position times the f_i that is given or theta's in double, is off
  *             by about 2^-26 turns at most wherever the position lies (fp32 in half
  *             turns; |f_i| < 2^30)
- * Outputs must not overlap inputs. */
+ * Outputs must not overlap inputs or each other. */
 MSA_API msa_status msa_qk_norm_rope(const msa_shape* shape, const msa_rope_cfg* cfg, const void* q_in,
                                     int64_t q_stride, const void* k_in, int64_t k_stride, const void* v_in,
                                     int64_t v_stride, const int32_t* positions, void* q, void* k, void* v,

@@ -357,9 +357,14 @@ msa_status norm_rope(const msa_shape& s, const int32_t* cu, int32_t n_seqs, cons
   if (q_stride % 8 || k_stride % 8 || (v_in && v_stride % 8)) return MSA_ERR_INVALID_ARG;
   if (!k && !pages) return MSA_ERR_INVALID_ARG;          // the keys would go nowhere
   if (v_in ? !v && !pages : v || pages) return MSA_ERR_INVALID_ARG;  // values come and go together
-  if (q == q_in || q == k_in || (v_in && q == v_in) || (k && (k == q_in || k == k_in || k == v_in)) ||
-      (v && (v == q_in || v == k_in || v == v_in)))
-    return MSA_ERR_INVALID_ARG;  // rows move: not in place
+  // rows move: not in place, nor two outputs in one
+  const void* outs[5] = {q, k, v, pages ? pages->k : nullptr, pages ? pages->v : nullptr};
+  for (int x = 0; x < 5; ++x) {
+    if (!outs[x]) continue;
+    if (outs[x] == q_in || outs[x] == k_in || outs[x] == v_in) return MSA_ERR_INVALID_ARG;
+    for (int y = 0; y < x; ++y)
+      if (outs[x] == outs[y]) return MSA_ERR_INVALID_ARG;
+  }
   RopeArgs a;
   memset(&a, 0, sizeof(a));
   if (pages) {

@@ -331,3 +331,22 @@ def test_angles_near_whole_turns_at_far_positions(cuda_lib, size, sign):
     # sine or cosine of that to 2 steps
     slack = math.pi * (1.5 * 2.0 ** -31 + u.abs() * 2.0 ** -24)
     check_rounded(q[0, 0], ref, torch.cat([slack, slack], 1) + ref.abs() * 2.0 ** -22, "far angles")
+
+
+def test_outputs_in_one_place_are_refused(lib):
+    """Two outputs, or an output and an input, at one address: which value stays would be chance."""
+    P = ctypes.c_void_p
+    names = ("q_in", "k_in", "v_in", "q", "k", "v", "k_pages", "v_pages")
+    sh, c = msa.Shape(1, 4, 4, 8, 128, 0.0), msa.rope_cfg(128).c
+
+    def call(**same):
+        a = {k: 0x100000 * (x + 1) for x, k in enumerate(names)}
+        a.update({k: a[v] for k, v in same.items()})
+        pages = msa.KVPagesC(a["k_pages"], a["v_pages"], 8, 16)
+        return lib.msa_qk_norm_rope(ctypes.byref(sh), ctypes.byref(c), P(a["q_in"]), 512, P(a["k_in"]), 512, P(a["v_in"]),
+                                    512, None, P(a["q"]), P(a["k"]), P(a["v"]), ctypes.byref(pages), P(0x1000), None)
+
+    outs = names[3:]
+    for x, out in enumerate(outs):
+        for other in names[:3] + outs[:x]:
+            assert call(**{out: other}) == msa.MSA_ERR_INVALID_ARG, (out, other)
