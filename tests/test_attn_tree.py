@@ -499,3 +499,52 @@ def test_parts_of_one_and_two_tiles(cuda_lib, tiles, d):
         c.check(out, what=f"{tiles} tiles")
         again = c.run()
         assert torch.equal(out[0], again[0]) and torch.equal(out[1], again[1])
+
+
+def _guarded(nbytes):
+    """A workspace of exactly nbytes between guards, all bytes 0xFF (as fp32: NaN; as int32: -1)."""
+    whole = torch.full((nbytes + 512,), 255, dtype=torch.uint8, device="cuda")
+    return whole, whole[256:256 + nbytes]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv,n", [(4, 2, 1), (4, 1, 16), (4, 1, 20), (4, 1, 32), (4, 1, 48), (6, 1, 100)])
+def test_workspace_of_the_stated_size(cuda_lib, Hq, Hkv, n, d):
+    """Every row layout, items cut many times and not at all: the stated bytes suffice, need no value before the call
+    and give the bits of a workspace that the call allocates."""
+    rng = np.random.default_rng(n + d)
+    lens = [50001, n, n + 700, n + 4000]
+    tls = [n, n, max(1, n // 2), 1]
+    masks = np.stack([tree_bits(rng, n) for _ in lens])
+    c = Case(Hq, Hkv, n, d, 32, lens, 5 + n, tls=tls, masks=masks, peak=4.0)
+    whole, ws = _guarded(msa.attn_tree_workspace(len(lens), Hq, Hkv, n, d))
+    out = c.run(ws=ws)
+    assert cuda_lib.poll_device_status() == 0
+    c.check(out, what="workspace")
+    assert bool((whole[:256] == 255).all()) and bool((whole[-256:] == 255).all())
+    own = c.run()
+    assert torch.equal(out[0], own[0]) and torch.equal(out[1], own[1])
+
+
+@pytest.mark.gpu
+def test_workspace_reused_by_other_shapes(cuda_lib):
+    """One workspace for calls of different shapes and row layouts one after another, each after calls that left more
+    parts and cuts in it, fewer, and other ones."""
+    rng = np.random.default_rng(17)
+    cases = []
+    for Hq, Hkv, n, d, lens in [(4, 1, 32, 128, [60000, 900]), (4, 1, 32, 128, [200, 129]), (4, 2, 3, 64, [30000, 7, 5000]),
+                                (4, 1, 50, 128, [20000] * 3), (8, 8, 1, 128, [40, 300]), (4, 1, 50, 128, [260]),
+                                (4, 1, 20, 64, [300] * 40)]:
+        masks = np.stack([tree_bits(rng, n) for _ in lens])
+        cases.append(Case(Hq, Hkv, n, d, 64, lens, 70 + n, masks=masks))
+    need = max(msa.attn_tree_workspace(len(c.lens), *(c.q.shape[1], c.k.shape[1], *c.q.shape[2:])) for c in cases)
+    whole, ws = _guarded(need)
+    want = [c.run() for c in cases]
+    for x in list(range(len(cases))) + rng.permutation(np.repeat(np.arange(len(cases)), 3)).tolist():
+        got = cases[x].run(ws=ws)
+        assert torch.equal(got[0], want[x][0]) and torch.equal(got[1], want[x][1]), x
+    assert cuda_lib.poll_device_status() == 0
+    for c, w in zip(cases, want):
+        c.check(w, what="reused")
+    assert bool((whole[:256] == 255).all()) and bool((whole[-256:] == 255).all())

@@ -319,3 +319,23 @@ def test_token_counts_beyond_32_bits_are_refused():
     for kw in (dict(seq_tokens=1 << 32), dict(tok_cap=1 << 32), dict(seq_tokens=1 << 31), dict(tok_cap=(1 << 33) + 5)):
         with pytest.raises(ValueError, match="seq_tokens, tok_cap: more than"):
             msa.build_page_tables(pool, new, **kw)
+
+
+@pytest.mark.gpu
+def test_tables_on_a_given_stream(cuda_lib):
+    """Calls ordered on a stream other than the current one."""
+    rng = np.random.default_rng(19)
+    lists = _pool(rng, 70, 40, 4000, rng.integers(0, 300, 70).tolist(), 16)
+    b = Both(lists, 16)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        new = [x + int(rng.integers(0, 100)) for x in b.lens]
+        t = torch.tensor(new, dtype=torch.int32, device="cuda")
+        side.wait_stream(torch.cuda.current_stream())
+        got = msa.build_page_tables(b.pool, t, tok_cap=7000, stream=side)
+        side.synchronize()
+        want = resize(b.table, b.lens, b.stack, b.state, new, 16, tok_cap=7000)
+        assert [x.tolist() for x in got] == list(want)
+        assert b.pool.page_table.tolist() == b.table and b.pool.seq_len.tolist() == b.lens
+    assert cuda_lib.poll_device_status() == 0

@@ -350,3 +350,52 @@ def test_outputs_in_one_place_are_refused(lib):
     for x, out in enumerate(outs):
         for other in names[:3] + outs[:x]:
             assert call(**{out: other}) == msa.MSA_ERR_INVALID_ARG, (out, other)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("varlen", [False, True])
+def test_many_tokens_of_full_heads(cuda_lib, varlen):
+    """32 / 8 heads of 128 and enough tokens that a CTA takes eight, the last one fewer: into layer and cache."""
+    Hq, Hkv, d, page = 32, 8, 128, 64
+    lens = [4099, 1, 0, 6000, 903] if varlen else [10003]
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    tok = int(cu[-1])
+    q, k, v, w = _inputs(tok, Hq, Hkv, d, 12)
+    rng = np.random.default_rng(12)
+    N = -(-tok // page) + 2
+    slots = torch.from_numpy(rng.permutation(N * page)[:tok].astype(np.int32)).cuda()
+    kp, vp = (torch.full((N, Hkv, page, d), float("nan"), dtype=BF, device="cuda") for _ in range(2))
+    cfg = msa.rope_cfg(d, theta=500000.0, norm=True, q_weight=w[0], k_weight=w[1])
+    where = dict(k_pages=kp, v_pages=vp, slots=slots)
+    if varlen:
+        outs = msa.qk_norm_rope_varlen(q, k, v, cu, cfg, **where)
+        outs = [torch.cat([s.transpose(0, 1) for s in msa.unpack_varlen(t, H, cu, d)])
+                for t, H in zip(outs, (Hq, Hkv, Hkv))]
+    else:
+        outs = [t[0].transpose(0, 1) for t in msa.qk_norm_rope(*(t[None] for t in (q, k, v)), cfg, **where)]
+    assert cuda_lib.poll_device_status() == 0
+    pos = torch.cat([torch.arange(x) for x in lens]).int().cuda()
+    c = dict(norm=True, eps=1e-6, rot=d, freq=_freq(d, 500000.0), inter=False)
+    _check(outs[0], q, w[0], c, pos, "q")
+    _check(outs[1], k, w[1], c, pos, "k")
+    assert torch.equal(outs[2], v)
+    rows = lambda t: t.transpose(1, 2).reshape(-1, Hkv, d)  # noqa: E731
+    assert torch.equal(rows(kp)[slots.long()], outs[1]) and torch.equal(rows(vp)[slots.long()], v)
+    other = torch.ones(N * page, dtype=torch.bool, device="cuda")
+    other[slots.long()] = False
+    assert bool(rows(kp)[other].isnan().all()) and bool(rows(vp)[other].isnan().all())
+
+
+@pytest.mark.gpu
+def test_packed_tokens_on_a_given_stream(cuda_lib):
+    lens = [5, 0, 300, 17]
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    q, k, v, w = _inputs(int(cu[-1]), 4, 2, 64, 14)
+    cfg = msa.rope_cfg(64, norm=True, q_weight=w[0], k_weight=w[1])
+    want = msa.qk_norm_rope_varlen(q, k, v, cu, cfg)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = msa.qk_norm_rope_varlen(q, k, v, cu, cfg, stream=side)
+    side.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
