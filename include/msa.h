@@ -474,7 +474,9 @@ MSA_API size_t msa_attn_tree_workspace(const msa_shape* shape);
  * tokens in its pages, the last T = tree_len[b] (NULL: n) of them the drafted
  * ones (their K and V are in the cache already).  Row i < T of query head h
  * attends the L - T context keys and the drafted keys j < T whose bit j is set
- * in its mask; every key enters the softmax once.
+ * in its mask; every key enters the softmax once.  Scores, softmax statistics
+ * and sums are fp32; a weight is rounded to bf16 for its product with V, as in
+ * the prefill's attention.
  *   q, o        [B, Hq, n, d_h], not overlapping; lse [B, Hq, n] or NULL.  Rows >= T are neither
  *               read nor written; a row without keys gives o = 0, lse = -inf
  *   tree_mask   [n, ceil(n / 32)] words per request, word x bit y = drafted key

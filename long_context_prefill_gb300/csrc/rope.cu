@@ -103,7 +103,7 @@ __device__ __forceinline__ void load8(const float* p, const float* q, uint64_t (
 // With scalar arithmetic the issue slots were 65 % taken at 5.2 TB/s, so it is in
 // packed pairs; and a lane keeps the loads of its next two heads in flight (with one
 // the 4 CTAs an SM's registers hold had too little on the way: 162 us).  32K tokens
-// of 32 + 8 + 8 heads of 128 into layer and cache take 151 us, 6.2 TB/s (0.91 of the
+// of 32 + 8 + 8 heads of 128 into layer and cache take 151 us, 6.2 TB/s (0.92 of the
 // measured copy rate), 105K tokens 458 us (0.97), 64 tokens of a decode step 3.5 us.
 template <int D, bool kVarlen>
 __global__ void __launch_bounds__(kThreads, 4)
