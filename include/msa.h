@@ -494,6 +494,87 @@ MSA_API msa_status msa_attn_tree(const msa_shape* shape, const void* q, const ms
                                  const int32_t* tree_len, const uint32_t* tree_mask, int64_t mask_stride, void* o,
                                  float* lse, void* ws, size_t ws_bytes, void* stream);
 
+/* A sliding window with a few first tokens that stay visible: what an A-shape
+ * head (eq.(3)) sees of the cache.  Row i of a request stands at position
+ * p_i = L - T + i or, when depth is given, L - T + depth[b][i] (a drafted
+ * tree's token sits at its depth; clamped to [0, n)).  It sees context key j when
+ * j < sink or j > p_i - window.  Of the drafted keys it sees those that its
+ * mask names; without a mask (and then without depths) the chain's j <= i,
+ * under the same rule. */
+typedef struct {
+  int32_t sink;         /* >= 0 */
+  int32_t window;       /* >= 1 */
+  const int32_t* depth; /* [B, n] device memory, or NULL: i */
+} msa_tree_window;
+
+/* msa_attn_tree through a window (not NULL).  Keys that no row of a request
+ * can see, sink .. L - T - window, are not read: their pages may hold
+ * anything and the table's entries of pages with no other keys are
+ * unspecified, so a rolling cache can give them back.  Workspace:
+ * msa_attn_tree_workspace. */
+MSA_API msa_status msa_attn_tree_window(const msa_shape* shape, const void* q, const msa_kv_pages* pages,
+                                        const int32_t* page_table, int32_t max_pages, const int32_t* seq_len,
+                                        const int32_t* tree_len, const uint32_t* tree_mask, int64_t mask_stride,
+                                        const msa_tree_window* window, void* o, float* lse, void* ws, size_t ws_bytes,
+                                        void* stream);
+
+/* ---------------------------------------------------------------- 4-bit cache
+ * The same cache with K and V in 4.5 bits a value.  16 neighbouring channels
+ * of a token and head form a block: each value is an e2m1 number (0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6 and their negatives; code 8 is the sign) times the block's
+ * e4m3 scale times the tensor's scale (k_scale, v_scale).  A block x is held
+ * as scale = RN(max |x| / (6 tensor scale)) (at most 448) and codes
+ * RN(x / (scale tensor scale)), to the nearest with ties to even, of the
+ * exact x (a key after norm and rotation, not rounded before); a block whose
+ * scale rounds to zero is held as zeros.
+ *
+ * data: [num_pages, Hkv] units pairs, K's and V's, of page_size * (d_h / 2 +
+ * d_h / 16) bytes each: codes [d_h / 32][page_size][16] (byte y of chunk c:
+ * channel 32 c + 2 y in the low four bits, 32 c + 2 y + 1 in the high ones),
+ * then scales [page_size][d_h / 16].  Page tables, slots and pools as for
+ * the bf16 cache. */
+typedef struct {
+  void* data; /* 16-byte aligned */
+  int32_t num_pages, page_size;
+  float k_scale, v_scale; /* powers of two from 2^-40 to 2^40; 0: 1 */
+} msa_kv4_pages;
+
+/* msa_qk_norm_rope and its varlen form with the 4-bit cache in place of the
+ * bf16 pages (pages, slots and v_in are required; k and v, nullable, are the
+ * layer's in bf16, not the cached values).  What a slot holds is what the
+ * definition gives in fp64. */
+MSA_API msa_status msa_qk_norm_rope_kv4(const msa_shape* shape, const msa_rope_cfg* cfg, const void* q_in,
+                                        int64_t q_stride, const void* k_in, int64_t k_stride, const void* v_in,
+                                        int64_t v_stride, const int32_t* positions, void* q, void* k, void* v,
+                                        const msa_kv4_pages* pages, const int32_t* slots, void* stream);
+MSA_API msa_status msa_qk_norm_rope_varlen_kv4(const msa_shape* shape, const int32_t* cu_seqlens, int32_t n_seqs,
+                                               const msa_rope_cfg* cfg, const void* q_in, int64_t q_stride,
+                                               const void* k_in, int64_t k_stride, const void* v_in,
+                                               int64_t v_stride, const int32_t* positions, void* q, void* k, void* v,
+                                               const msa_kv4_pages* pages, const int32_t* slots, void* stream);
+
+/* Cached tokens back in the layer's layout, so that a prefill can continue a
+ * cached prefix: the first min(seq_len[b], shape.n) tokens of each of shape.B
+ * requests to k, v [B, Hkv, n, d_h] (bf16, exactly the values held); rows
+ * behind them are not written.  Hq of the shape is not used (set it to Hkv).
+ * A length outside [0, max_pages * page_size] is skipped, a page id outside
+ * the pool is not followed; either makes the next poll return MSA_ERR_INDEX. */
+MSA_API msa_status msa_kv4_gather(const msa_shape* shape, const msa_kv4_pages* pages, const int32_t* page_table,
+                                  int32_t max_pages, const int32_t* seq_len, void* k, void* v, void* stream);
+
+/* Workspace bytes of msa_attn_tree_kv4 (0 on an invalid shape). */
+MSA_API size_t msa_attn_tree_kv4_workspace(const msa_shape* shape);
+
+/* msa_attn_tree over the 4-bit cache, through a window or (window NULL) not.
+ * The products take the held values exactly and q exactly (fp16 operands, q
+ * scaled by a power of two per row: what is below 2^-30 of the row's largest
+ * value is rounded); a weight is rounded to fp16 for its product with V. */
+MSA_API msa_status msa_attn_tree_kv4(const msa_shape* shape, const void* q, const msa_kv4_pages* pages,
+                                     const int32_t* page_table, int32_t max_pages, const int32_t* seq_len,
+                                     const int32_t* tree_len, const uint32_t* tree_mask, int64_t mask_stride,
+                                     const msa_tree_window* window, void* o, float* lse, void* ws, size_t ws_bytes,
+                                     void* stream);
+
 /* Failure detection (no counterpart in the pages).  Synchronise `stream`,
  * read and clear the device error word of the current device.  Returns MSA_OK, MSA_ERR_DEVICE_TIMEOUT, MSA_ERR_INDEX or
  * MSA_ERR_CUDA. */

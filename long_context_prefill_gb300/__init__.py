@@ -32,7 +32,8 @@ EXPORTS = ("msa_status_string", "msa_vs_index_workspace", "msa_block_index_works
            "msa_check_wait_timeout", "msa_attn_dense", "msa_layer_varlen_workspace", "msa_prefill_layer_varlen",
            "msa_layer_attend_rows", "msa_merge_attention", "msa_captured_mass", "msa_layer_varlen_indices",
            "msa_layer_attend_stats", "msa_build_page_tables", "msa_qk_norm_rope", "msa_qk_norm_rope_varlen",
-           "msa_attn_tree_workspace", "msa_attn_tree")
+           "msa_attn_tree_workspace", "msa_attn_tree", "msa_attn_tree_window", "msa_qk_norm_rope_kv4",
+           "msa_qk_norm_rope_varlen_kv4", "msa_kv4_gather", "msa_attn_tree_kv4_workspace", "msa_attn_tree_kv4")
 
 
 class MsaError(RuntimeError):
@@ -67,6 +68,15 @@ class PagePoolC(ctypes.Structure):
     _fields_ = [("n_seqs", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("max_pages", ctypes.c_int32), ("page_table", ctypes.c_void_p), ("seq_len", ctypes.c_void_p),
                 ("free_pages", ctypes.c_void_p), ("state", ctypes.c_void_p)]
+
+
+class TreeWindowC(ctypes.Structure):
+    _fields_ = [("sink", ctypes.c_int32), ("window", ctypes.c_int32), ("depth", ctypes.c_void_p)]
+
+
+class KV4PagesC(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
 
 
 class RopeCfgC(ctypes.Structure):
@@ -153,6 +163,18 @@ def load(path: str = LIB_PATH):
             lib.msa_attn_tree_workspace.argtypes = [P]
             lib.msa_attn_tree.restype = st
             lib.msa_attn_tree.argtypes = [P, P, P, P, i32, P, P, P, i64, P, P, P, sz, P]
+            lib.msa_attn_tree_window.restype = st
+            lib.msa_attn_tree_window.argtypes = [P, P, P, P, i32, P, P, P, i64, P, P, P, P, sz, P]
+            lib.msa_qk_norm_rope_kv4.restype = st
+            lib.msa_qk_norm_rope_kv4.argtypes = lib.msa_qk_norm_rope.argtypes
+            lib.msa_qk_norm_rope_varlen_kv4.restype = st
+            lib.msa_qk_norm_rope_varlen_kv4.argtypes = lib.msa_qk_norm_rope_varlen.argtypes
+            lib.msa_kv4_gather.restype = st
+            lib.msa_kv4_gather.argtypes = [P, P, P, i32, P, P, P, P]
+            lib.msa_attn_tree_kv4_workspace.restype = sz
+            lib.msa_attn_tree_kv4_workspace.argtypes = [P]
+            lib.msa_attn_tree_kv4.restype = st
+            lib.msa_attn_tree_kv4.argtypes = [P, P, P, P, i32, P, P, P, i64, P, P, P, P, sz, P]
             _lib = lib
     return _lib
 
@@ -855,15 +877,21 @@ def _per_token(t, what, tokens, device):
         _want(t, what, torch.int32, device=device)
 
 
-def _rope_args(lead, out, dims, q_in, k_in, v_in, cfg, positions, q, k, v, k_pages, v_pages, slots):
-    """Check everything; returns (token strides of q_in, k_in and v_in, C view of the pages or None)."""
+def _rope_args(lead, out, dims, q_in, k_in, v_in, cfg, positions, q, k, v, pages, slots):
+    """Check everything; returns (token strides of q_in, k_in and v_in, C view of the pages or None).  pages: KV4Pages,
+    or the pair k_pages, v_pages."""
     Hq, Hkv, d = dims
     dev = q_in.device
     qs = _token_rows(q_in, "q_in", lead, Hq, d, dev)
     ks = _token_rows(k_in, "k_in", lead, Hkv, d, dev)
     vs = 0 if v_in is None else _token_rows(v_in, "v_in", lead, Hkv, d, dev)
     cfg.check(d, dev)
-    pages = None if k_pages is None and v_pages is None else _pages(k_pages, v_pages, Hkv, d, dev)
+    if isinstance(pages, KV4Pages):
+        if slots is None or v_in is None:
+            raise ValueError(f"{'slots' if slots is None else 'v_in'}: a torch.Tensor is required")
+        pages = pages.view(Hkv, d, dev)
+    else:
+        pages = None if pages[0] is None and pages[1] is None else _pages(*pages, Hkv, d, dev)
     tokens = lead[0] if len(lead) == 1 else lead[0] * lead[1]
     if positions is not None:
         _per_token(positions, "positions", tokens, dev)
@@ -880,23 +908,19 @@ def _rope_args(lead, out, dims, q_in, k_in, v_in, cfg, positions, q, k, v, k_pag
     return qs, ks, vs, pages
 
 
-def qk_norm_rope(q_in, k_in, v_in, cfg: RopeCfg, positions=None, q=None, k=None, v=None, k_pages=None, v_pages=None,
-                 slots=None, layer_kv: bool = True, stream=None):
-    """msa_qk_norm_rope: q_in [B, n, Hq, d], k_in / v_in [B, n, Hkv, d] (views
-    of the projection's rows) to (q [B, Hq, n, d], k, v [B, Hkv, n, d]) and,
-    with k_pages / v_pages and slots, into the cache.  layer_kv=False leaves k
-    and v to the cache alone (returned as given, or None)."""
+def _norm_rope(name, q_in, k_in, v_in, cfg, positions, q, k, v, pages, slots, layer_kv, stream):
+    """qk_norm_rope and qk_norm_rope_kv4, of which `name` is the C name."""
     for t, what in ((q_in, "q_in"), (k_in, "k_in")):
         if not isinstance(t, torch.Tensor) or t.dim() != 4:
             raise ValueError(f"{what}: a 4-d tensor [B, n, H, d] is required")
     B, n, Hq, d = q_in.shape
     Hkv, dev = k_in.shape[2], q_in.device
     kv = (B, Hkv, n, d)
-    qs, ks, vs, pages = _rope_args((B, n), ((B, Hq, n, d), kv), (Hq, Hkv, d), q_in, k_in, v_in, cfg, positions, q, k, v,
-                                   k_pages, v_pages, slots)
+    qs, ks, vs, held = _rope_args((B, n), ((B, Hq, n, d), kv), (Hq, Hkv, d), q_in, k_in, v_in, cfg, positions, q, k, v,
+                                  pages, slots)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
-            return qk_norm_rope(q_in, k_in, v_in, cfg, positions, q, k, v, k_pages, v_pages, slots, layer_kv)
+            return _norm_rope(name, q_in, k_in, v_in, cfg, positions, q, k, v, pages, slots, layer_kv, None)
     if q is None:
         q = torch.empty((B, Hq, n, d), dtype=torch.bfloat16, device=dev)
     if layer_kv:
@@ -904,34 +928,31 @@ def qk_norm_rope(q_in, k_in, v_in, cfg: RopeCfg, positions=None, q=None, k=None,
             k = torch.empty(kv, dtype=torch.bfloat16, device=dev)
         if v is None and v_in is not None:
             v = torch.empty(kv, dtype=torch.bfloat16, device=dev)
-    st = load().msa_qk_norm_rope(ctypes.byref(Shape(B, Hq, Hkv, n, d, 0.0)), ctypes.byref(cfg.c), q_in.data_ptr(), qs,
-                                 k_in.data_ptr(), ks, _at(v_in), vs, _at(positions), q.data_ptr(), _at(k), _at(v),
-                                 None if pages is None else ctypes.byref(pages), _at(slots),
-                                 torch._C._cuda_getCurrentRawStream(dev.index))
+    st = getattr(load(), name)(ctypes.byref(Shape(B, Hq, Hkv, n, d, 0.0)), ctypes.byref(cfg.c), q_in.data_ptr(), qs,
+                               k_in.data_ptr(), ks, _at(v_in), vs, _at(positions), q.data_ptr(), _at(k), _at(v),
+                               None if held is None else ctypes.byref(held), _at(slots),
+                               torch._C._cuda_getCurrentRawStream(dev.index))
     if st:
-        raise MsaError(st, "msa_qk_norm_rope")
+        raise MsaError(st, name)
     return q, k, v
 
 
-def qk_norm_rope_varlen(q_in, k_in, v_in, cu_seqlens, cfg: RopeCfg, positions=None, q=None, k=None, v=None,
-                        k_pages=None, v_pages=None, slots=None, layer_kv: bool = True, stream=None):
-    """msa_qk_norm_rope_varlen: packed q_in [tokens, Hq, d], k_in / v_in
-    [tokens, Hkv, d] to flat buffers in the varlen layout (see pack_varlen)
-    and, as for qk_norm_rope, the cache."""
+def _norm_rope_varlen(name, q_in, k_in, v_in, cu, cfg, positions, q, k, v, pages, slots, layer_kv, stream):
+    """The packed forms, of which `name` is the C name."""
     for t, what in ((q_in, "q_in"), (k_in, "k_in")):
         if not isinstance(t, torch.Tensor) or t.dim() != 3:
             raise ValueError(f"{what}: a 3-d tensor [tokens, H, d] is required")
-    cu = [int(x) for x in cu_seqlens]
+    cu = [int(x) for x in cu]
     tokens, Hq, d = q_in.shape
     Hkv, dev = k_in.shape[1], q_in.device
     if len(cu) < 2 or cu[-1] != tokens:
         raise ValueError(f"cu_seqlens: must end at the {tokens} tokens of q_in")
     qn, kn = tokens * Hq * d, tokens * Hkv * d
-    qs, ks, vs, pages = _rope_args((tokens,), ((qn,), (kn,)), (Hq, Hkv, d), q_in, k_in, v_in, cfg, positions, q, k, v,
-                                   k_pages, v_pages, slots)
+    qs, ks, vs, held = _rope_args((tokens,), ((qn,), (kn,)), (Hq, Hkv, d), q_in, k_in, v_in, cfg, positions, q, k, v,
+                                  pages, slots)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
-            return qk_norm_rope_varlen(q_in, k_in, v_in, cu, cfg, positions, q, k, v, k_pages, v_pages, slots, layer_kv)
+            return _norm_rope_varlen(name, q_in, k_in, v_in, cu, cfg, positions, q, k, v, pages, slots, layer_kv, None)
     if q is None:
         q = torch.empty(qn, dtype=torch.bfloat16, device=dev)
     if layer_kv:
@@ -939,29 +960,140 @@ def qk_norm_rope_varlen(q_in, k_in, v_in, cu_seqlens, cfg: RopeCfg, positions=No
             k = torch.empty(kn, dtype=torch.bfloat16, device=dev)
         if v is None and v_in is not None:
             v = torch.empty(kn, dtype=torch.bfloat16, device=dev)
-    st = load().msa_qk_norm_rope_varlen(ctypes.byref(Shape(1, Hq, Hkv, 1, d, 0.0)), (ctypes.c_int32 * len(cu))(*cu),
-                                        len(cu) - 1, ctypes.byref(cfg.c), q_in.data_ptr(), qs, k_in.data_ptr(), ks,
-                                        _at(v_in), vs, _at(positions), q.data_ptr(), _at(k), _at(v),
-                                        None if pages is None else ctypes.byref(pages), _at(slots),
-                                        torch._C._cuda_getCurrentRawStream(dev.index))
+    st = getattr(load(), name)(ctypes.byref(Shape(1, Hq, Hkv, 1, d, 0.0)), (ctypes.c_int32 * len(cu))(*cu),
+                               len(cu) - 1, ctypes.byref(cfg.c), q_in.data_ptr(), qs, k_in.data_ptr(), ks,
+                               _at(v_in), vs, _at(positions), q.data_ptr(), _at(k), _at(v),
+                               None if held is None else ctypes.byref(held), _at(slots),
+                               torch._C._cuda_getCurrentRawStream(dev.index))
     if st:
-        raise MsaError(st, "msa_qk_norm_rope_varlen")
+        raise MsaError(st, name)
     return q, k, v
 
 
-def attn_tree(q, k_pages, v_pages, page_table, seq_len, tree_len=None, tree_mask=None, o=None, lse=None, scale=None,
-              ws=None, stream=None):
-    """msa_attn_tree: drafted tokens (n = 1: a decode step) q [B, Hq, n, d] over
-    the paged cache; seq_len [B] counts the drafted tokens.  tree_len [B];
-    tree_mask [B, n, ceil(n/32)] or, for all requests, [n, ceil(n/32)] int32
-    words (None: a chain).  Returns o.  ws: a uint8 workspace of at least
-    attn_tree_workspace(...) bytes (None: one is allocated for the call)."""
+def qk_norm_rope(q_in, k_in, v_in, cfg: RopeCfg, positions=None, q=None, k=None, v=None, k_pages=None, v_pages=None,
+                 slots=None, layer_kv: bool = True, stream=None):
+    """msa_qk_norm_rope: q_in [B, n, Hq, d], k_in / v_in [B, n, Hkv, d] (views
+    of the projection's rows) to (q [B, Hq, n, d], k, v [B, Hkv, n, d]) and,
+    with k_pages / v_pages and slots, into the cache.  layer_kv=False leaves k
+    and v to the cache alone (returned as given, or None)."""
+    return _norm_rope("msa_qk_norm_rope", q_in, k_in, v_in, cfg, positions, q, k, v, (k_pages, v_pages), slots,
+                      layer_kv, stream)
+
+
+def qk_norm_rope_varlen(q_in, k_in, v_in, cu_seqlens, cfg: RopeCfg, positions=None, q=None, k=None, v=None,
+                        k_pages=None, v_pages=None, slots=None, layer_kv: bool = True, stream=None):
+    """msa_qk_norm_rope_varlen: packed q_in [tokens, Hq, d], k_in / v_in
+    [tokens, Hkv, d] to flat buffers in the varlen layout (see pack_varlen)
+    and, as for qk_norm_rope, the cache."""
+    return _norm_rope_varlen("msa_qk_norm_rope_varlen", q_in, k_in, v_in, cu_seqlens, cfg, positions, q, k, v,
+                             (k_pages, v_pages), slots, layer_kv, stream)
+
+
+class KV4Pages:
+    """A pool of 4-bit cache pages (msa_kv4_pages): data, uint8 [num_pages, Hkv,
+    kv4_page_bytes(page_size, d)], for heads of d channels, and the tensors'
+    scales, powers of two.  data may be replaced: each call checks and uses the
+    tensor that is there."""
+
+    def __init__(self, data, page_size: int, d: int, k_scale: float = 1.0, v_scale: float = 1.0):
+        self.data, self.page_size, self.d = data, int(page_size), int(d)
+        self.k_scale, self.v_scale = float(k_scale), float(v_scale)
+        if not self.k_scale > 0 or not self.v_scale > 0:
+            raise ValueError("k_scale, v_scale: must be positive")
+        if not isinstance(data, torch.Tensor) or data.dim() != 3:
+            raise ValueError("data: a 3-d tensor [num_pages, Hkv, bytes] is required")
+
+    @staticmethod
+    def empty(num_pages: int, Hkv: int, page_size: int, d: int, device, k_scale: float = 1.0,
+              v_scale: float = 1.0) -> "KV4Pages":
+        """A pool whose values are all zero."""
+        data = torch.zeros(num_pages, Hkv, kv4_page_bytes(page_size, d), dtype=torch.uint8, device=device)
+        return KV4Pages(data, page_size, d, k_scale, v_scale)
+
+    def view(self, Hkv, d, device):
+        """C view of the pages, checked against Hkv heads (None: any) of d channels on `device`."""
+        t = self.data
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            raise ValueError("data: a 3-d tensor [num_pages, Hkv, bytes] is required")
+        if d != self.d:
+            raise ValueError(f"pages: heads of {self.d} channels, expected {d}")
+        N, H, _ = t.shape
+        _same(t, "data", torch.uint8, (N, H if Hkv is None else Hkv, kv4_page_bytes(self.page_size, d)), device)
+        return KV4PagesC(t.data_ptr(), N, self.page_size, self.k_scale, self.v_scale)
+
+
+def kv4_page_bytes(page_size: int, d: int) -> int:
+    """Bytes that the K and V of one page and head take in a 4-bit cache."""
+    return 2 * int(page_size) * (int(d) // 2 + int(d) // 16)
+
+
+def _kv4(pages):
+    if not isinstance(pages, KV4Pages):
+        raise ValueError("pages: KV4Pages are required")
+    return pages
+
+
+def qk_norm_rope_kv4(q_in, k_in, v_in, cfg: RopeCfg, pages: KV4Pages, slots, positions=None, q=None, k=None, v=None,
+                     layer_kv: bool = False, stream=None):
+    """msa_qk_norm_rope_kv4: as qk_norm_rope, K and V into the slots of a 4-bit
+    cache.  layer_kv=True also returns them in bf16 in the layer's layout (not
+    the cached values: see kv4_gather)."""
+    return _norm_rope("msa_qk_norm_rope_kv4", q_in, k_in, v_in, cfg, positions, q, k, v, _kv4(pages), slots, layer_kv,
+                      stream)
+
+
+def qk_norm_rope_varlen_kv4(q_in, k_in, v_in, cu_seqlens, cfg: RopeCfg, pages: KV4Pages, slots, positions=None, q=None,
+                            k=None, v=None, layer_kv: bool = False, stream=None):
+    """msa_qk_norm_rope_varlen_kv4: the packed form of qk_norm_rope_kv4."""
+    return _norm_rope_varlen("msa_qk_norm_rope_varlen_kv4", q_in, k_in, v_in, cu_seqlens, cfg, positions, q, k, v,
+                             _kv4(pages), slots, layer_kv, stream)
+
+
+def kv4_gather(pages: KV4Pages, page_table, seq_len, n: int, k=None, v=None, stream=None):
+    """msa_kv4_gather: the first min(seq_len[b], n) cached tokens of every
+    request to (k, v) [B, Hkv, n, d] bf16; the rows behind them keep what a
+    given k and v hold, and are zero otherwise."""
+    data = _kv4(pages).data
+    dev, H, d, n = data.device, data.shape[1], pages.d, int(n)
+    c = pages.view(None, d, dev)
+    if n < 1 or n >> 31:
+        raise ValueError(f"n: {n}")
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table: a 2-d tensor [B, max_pages] is required")
+    B, width = page_table.shape
+    _same(page_table, "page_table", torch.int32, (B, width), dev)
+    _same(seq_len, "seq_len", torch.int32, (B,), dev)
+    if k is not None:
+        _same(k, "k", torch.bfloat16, (B, H, n, d), dev)
+    if v is not None:
+        _same(v, "v", torch.bfloat16, (B, H, n, d), dev)
+    if not data.is_cuda:
+        _cuda(data=data)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return kv4_gather(pages, page_table, seq_len, n, k, v)
+    if k is None:
+        k = torch.zeros(B, H, n, d, dtype=torch.bfloat16, device=dev)
+    if v is None:
+        v = torch.zeros(B, H, n, d, dtype=torch.bfloat16, device=dev)
+    st = load().msa_kv4_gather(ctypes.byref(Shape(B, H, H, n, d, 0.0)), ctypes.byref(c), page_table.data_ptr(), width,
+                               seq_len.data_ptr(), k.data_ptr(), v.data_ptr(),
+                               torch._C._cuda_getCurrentRawStream(dev.index))
+    if st:
+        raise MsaError(st, "msa_kv4_gather")
+    return k, v
+
+
+def _query(q):
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q: a 4-d tensor [B, Hq, n, d] is required")
+    _want(q, "q", torch.bfloat16)
+
+
+def _tree_args(q, page_table, seq_len, tree_len, tree_mask, depth, o, lse, ws):
+    """Check what the attentions of drafted tokens share; returns (columns of the page table, stride of the masks)."""
     B, Hq, n, d = q.shape
     dev = q.device
-    _want(q, "q", torch.bfloat16)
-    pages = _pages(k_pages, v_pages, None, d, dev)
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table: a 2-d tensor [B, max_pages] is required")
     width = page_table.shape[1]
@@ -975,6 +1107,8 @@ def attn_tree(q, k_pages, v_pages, page_table, seq_len, tree_len=None, tree_mask
         shared = isinstance(tree_mask, torch.Tensor) and tree_mask.dim() == 2
         _same(tree_mask, "tree_mask", torch.int32, (n, words) if shared else (B, n, words), dev)
         stride = 0 if shared else n * words
+    if depth is not None:
+        _same(depth, "depth", torch.int32, (B, n), dev)
     if o is not None:
         _same(o, "o", torch.bfloat16, (B, Hq, n, d), dev)
     if lse is not None:
@@ -983,6 +1117,33 @@ def attn_tree(q, k_pages, v_pages, page_table, seq_len, tree_len=None, tree_mask
         _want(ws, "ws", torch.uint8, device=dev)
     if not q.is_cuda:
         _cuda(q=q)
+    return width, stride
+
+
+def _window(sink, window, depth, tree_mask):
+    """Check a window (its depth needs a mask); returns (sink, window)."""
+    sink, window = int(sink), int(window)
+    if sink < 0 or sink >> 31:
+        raise ValueError(f"sink: {sink}")
+    if window < 1 or window >> 31:
+        raise ValueError(f"window: {window}")
+    if depth is not None and tree_mask is None:
+        raise ValueError("depth: needs a tree_mask")
+    return sink, window
+
+
+def attn_tree(q, k_pages, v_pages, page_table, seq_len, tree_len=None, tree_mask=None, o=None, lse=None, scale=None,
+              ws=None, stream=None):
+    """msa_attn_tree: drafted tokens (n = 1: a decode step) q [B, Hq, n, d] over
+    the paged cache; seq_len [B] counts the drafted tokens.  tree_len [B];
+    tree_mask [B, n, ceil(n/32)] or, for all requests, [n, ceil(n/32)] int32
+    words (None: a chain).  Returns o.  ws: a uint8 workspace of at least
+    attn_tree_workspace(...) bytes (None: one is allocated for the call)."""
+    _query(q)
+    B, Hq, n, d = q.shape
+    dev = q.device
+    pages = _pages(k_pages, v_pages, None, d, dev)
+    width, stride = _tree_args(q, page_table, seq_len, tree_len, tree_mask, None, o, lse, ws)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return attn_tree(q, k_pages, v_pages, page_table, seq_len, tree_len, tree_mask, o, lse, scale, ws)
@@ -1000,9 +1161,77 @@ def attn_tree(q, k_pages, v_pages, page_table, seq_len, tree_len=None, tree_mask
     return o
 
 
+def attn_tree_window(q, k_pages, v_pages, page_table, seq_len, sink: int, window: int, tree_len=None, tree_mask=None,
+                     depth=None, o=None, lse=None, scale=None, ws=None, stream=None):
+    """msa_attn_tree_window: attn_tree through a sliding window of `window`
+    keys that keeps the first `sink` tokens visible.  depth [B, n] int32: how
+    far behind the context each token of a masked tree stands (None: its
+    index).  Pages that no row sees may be gone."""
+    _query(q)
+    B, Hq, n, d = q.shape
+    dev = q.device
+    pages = _pages(k_pages, v_pages, None, d, dev)
+    seen = _window(sink, window, depth, tree_mask)
+    width, stride = _tree_args(q, page_table, seq_len, tree_len, tree_mask, depth, o, lse, ws)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return attn_tree_window(q, k_pages, v_pages, page_table, seq_len, sink, window, tree_len, tree_mask, depth,
+                                    o, lse, scale, ws)
+    lib = load()
+    sh = ctypes.byref(Shape(B, Hq, k_pages.shape[1], n, d, float(scale) if scale else 0.0))
+    win = TreeWindowC(*seen, _at(depth))
+    if o is None:
+        o = torch.empty_like(q)
+    if ws is None:
+        ws = torch.empty(lib.msa_attn_tree_workspace(sh) or 1, dtype=torch.uint8, device=dev)
+    st = lib.msa_attn_tree_window(sh, q.data_ptr(), ctypes.byref(pages), page_table.data_ptr(), width,
+                                  seq_len.data_ptr(), _at(tree_len), _at(tree_mask), stride, ctypes.byref(win),
+                                  o.data_ptr(), _at(lse), ws.data_ptr(), ws.numel(),
+                                  torch._C._cuda_getCurrentRawStream(dev.index))
+    if st:
+        raise MsaError(st, "msa_attn_tree_window")
+    return o
+
+
+def attn_tree_kv4(q, pages: KV4Pages, page_table, seq_len, sink: int = 0, window: int = 0, tree_len=None,
+                  tree_mask=None, depth=None, o=None, lse=None, scale=None, ws=None, stream=None):
+    """msa_attn_tree_kv4: attn_tree over a 4-bit cache; with window > 0 as
+    attn_tree_window (0: every key, and then no sink and no depth)."""
+    _query(q)
+    B, Hq, n, d = q.shape
+    dev = q.device
+    held = _kv4(pages).view(None, d, dev)
+    if not window and (sink or depth is not None):
+        raise ValueError("sink, depth: need a window")
+    seen = _window(sink, window, depth, tree_mask) if window else None
+    width, stride = _tree_args(q, page_table, seq_len, tree_len, tree_mask, depth, o, lse, ws)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return attn_tree_kv4(q, pages, page_table, seq_len, sink, window, tree_len, tree_mask, depth, o, lse, scale,
+                                 ws)
+    lib = load()
+    sh = ctypes.byref(Shape(B, Hq, pages.data.shape[1], n, d, float(scale) if scale else 0.0))
+    win = ctypes.byref(TreeWindowC(*seen, _at(depth))) if seen else None
+    if o is None:
+        o = torch.empty_like(q)
+    if ws is None:
+        ws = torch.empty(lib.msa_attn_tree_kv4_workspace(sh) or 1, dtype=torch.uint8, device=dev)
+    st = lib.msa_attn_tree_kv4(sh, q.data_ptr(), ctypes.byref(held), page_table.data_ptr(), width, seq_len.data_ptr(),
+                               _at(tree_len), _at(tree_mask), stride, win, o.data_ptr(), _at(lse), ws.data_ptr(),
+                               ws.numel(), torch._C._cuda_getCurrentRawStream(dev.index))
+    if st:
+        raise MsaError(st, "msa_attn_tree_kv4")
+    return o
+
+
 def attn_tree_workspace(B, Hq, Hkv, n, d) -> int:
     """Workspace bytes of attn_tree (0: unsupported shape)."""
     return int(load().msa_attn_tree_workspace(ctypes.byref(Shape(B, Hq, Hkv, n, d, 0.0))))
+
+
+def attn_tree_kv4_workspace(B, Hq, Hkv, n, d) -> int:
+    """Workspace bytes of attn_tree_kv4 (0: unsupported shape)."""
+    return int(load().msa_attn_tree_kv4_workspace(ctypes.byref(Shape(B, Hq, Hkv, n, d, 0.0))))
 
 
 def kernel_launches() -> int:

@@ -26,6 +26,7 @@
 #include <string.h>
 
 #include "internal.h"
+#include "kv4.cuh"
 #include "ptx.cuh"
 
 namespace msa {
@@ -53,6 +54,8 @@ struct RopeArgs {
   float eps, rot_scale;
   __nv_bfloat16 *qo, *ko, *vo;  // layer layout (ko, vo may be null)
   __nv_bfloat16 *kp, *vp;       // pages (may be null)
+  uint8_t* kv4;                 // or 4-bit pages
+  float k_inv, v_inv;           // 1 / their scales (powers of two)
   const int32_t* slots;
   int32_t page_shift, num_pages;
   int* err;
@@ -72,6 +75,7 @@ struct Seqs<false> {};
 struct Token {
   int32_t seq0, n, i;  // first token and length of its sequence, index in it
   int32_t slot;        // cache slot, < 0: not stored
+  int32_t pos;         // kKv4
 };
 
 // 8 bf16 values (16 bytes) as four pairs
@@ -96,6 +100,68 @@ __device__ __forceinline__ void load8(const float* p, const float* q, uint64_t (
   f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
 }
 
+// ---------------------------------------------------------------- 4-bit pages
+// A block of 16 channels is held as e2m1 codes and an e4m3 scale: scale = RN(max |x| / 6), code = RN(x / scale), both
+// ties to even and of the exact x.  V is exact: a quotient x / scale of 8 by 4 significant bits is a border of two codes
+// or at least 2^-8 of it away (a border times a scale has 7 bits), so rounding it to 2^-12 gives the borders back that
+// the reciprocal's error moved.  K is rounded here in fp32 first, to 2^-19 of its pair's size (32 half steps), so its
+// blocks are rounded twice, from both ends of that range; where the two differ (0.2 % of the heads) they are computed
+// again in fp64.  What the cache holds is then what the definition gives in 64 bits, whatever order a kernel sums in.
+
+// Value `c` of the key head at `x` in fp64; r: the norm's factor.
+__device__ __noinline__ double key64(const RopeArgs& A, const __nv_bfloat16* x, int c, int pos, double r) {
+  auto normed = [&](int i) {
+    const double v = (double)__bfloat162float(x[i]);
+    return A.norm ? v * r * (A.k_w ? (double)__bfloat162float(A.k_w[i]) : 1.0) : v;
+  };
+  if (c >= A.rot) return normed(c);
+  const int half = A.rot >> 1, p = A.interleaved ? c >> 1 : c % half;
+  const bool second = A.interleaved ? c & 1 : c >= half;
+  const double own = normed(c), other = normed(A.interleaved ? c ^ 1 : second ? c - half : c + half);
+  double s, co;
+  sincospi((double)(int64_t)((uint64_t)(int64_t)pos * A.turn[p]) * 0x1p-63, &s, &co);
+  return (own * co + (second ? other : -other) * s) * (double)A.rot_scale;
+}
+
+// x >= 0 cut to fp32 with its last bit set where something was cut: rounds to fewer bits as x itself does.
+__device__ __forceinline__ float sticky(double x) {
+  const float f = __double2float_rz(x);
+  return (double)f == x ? f : __uint_as_float(__float_as_uint(f) | 1u);
+}
+
+// Rounds the block v of 16 values to codes (two per byte) and a scale.  margin: how far off they may be.  Returns
+// whether the scale (bit 16) or a code (bits 0 .. 15) may not be that of the exact values.
+__device__ __forceinline__ uint32_t round_block(const float (&v)[16], float inv, float margin, uint2& codes,
+                                                uint32_t& scale) {
+  float a = 0.f;
+#pragma unroll
+  for (int x = 0; x < 16; ++x) a = fmaxf(a, fabsf(v[x]));
+  const float step = 2.384185791015625e-07f;  // 2^-22: the quotient's rounding
+  const float q = a * inv / 6.f, off = margin * inv;
+  scale = e4m3_of(q);
+  uint32_t unsure = 0;
+  if (margin > 0.f && e4m3_of(fmaxf(q - off * 0.25f - q * step, 0.f)) != e4m3_of(q + off * 0.25f + q * step)) unsure = 1u << 16;
+  const float s = e4m3_value(scale), r = s > 0.f ? inv / s : 0.f;
+  const float e = s > 0.f ? off / s + 4.f * step : 0.f;
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int x = 0; x < 16; x += 2) {
+    uint32_t c;
+    if (margin > 0.f) {
+      const float t0 = fabsf(v[x]) * r, t1 = fabsf(v[x + 1]) * r;
+      c = e2m1x2_of(t0 + e, t1 + e);
+      const uint32_t d = c ^ e2m1x2_of(fmaxf(t0 - e, 0.f), fmaxf(t1 - e, 0.f));
+      unsure |= (d & 0xFu ? 1u << x : 0u) | (d & 0xF0u ? 2u << x : 0u);
+    } else {
+      c = e2m1x2_of(fmaf(fabsf(v[x]), r, 3072.f) - 3072.f, fmaf(fabsf(v[x + 1]), r, 3072.f) - 3072.f);
+    }
+    c |= (__float_as_uint(v[x]) >> 28 & 8u) | (__float_as_uint(v[x + 1]) >> 24 & 0x80u);
+    w[x >> 3] |= c << (4 * (x & 7));
+  }
+  codes = make_uint2(w[0], w[1]);
+  return unsure;
+}
+
 // A lane's 16 values of a head: chunks c0 and c1 of 8.  In the rotated columns
 // chunk 0 holds the first and chunk 1 the second members of 8 pairs
 // (half-split), or both hold whole pairs (interleaved).
@@ -105,7 +171,7 @@ __device__ __forceinline__ void load8(const float* p, const float* q, uint64_t (
 // the 4 CTAs an SM's registers hold had too little on the way: 162 us).  32K tokens
 // of 32 + 8 + 8 heads of 128 into layer and cache take 151 us, 6.2 TB/s (0.92 of the
 // measured copy rate), 105K tokens 458 us (0.97), 64 tokens of a decode step 3.5 us.
-template <int D, bool kVarlen>
+template <int D, bool kVarlen, bool kKv4>
 __global__ void __launch_bounds__(kThreads, 4)
     norm_rope_kernel(const __grid_constant__ RopeArgs A, const __grid_constant__ Seqs<kVarlen> T) {
   constexpr int kLanes = D / 16;               // lanes of a head
@@ -115,6 +181,8 @@ __global__ void __launch_bounds__(kThreads, 4)
   __shared__ __align__(16) float cosines[kMaxTokens][D / 2], sines[kMaxTokens][D / 2];
   __shared__ __align__(16) float weights[2][2][D / 2];  // [q or k][chunk]
   __shared__ Token toks[kMaxTokens];
+  // kKv4: heads on their way from a lane's chunks to its block of 16 channels (rows apart by 4 banks)
+  __shared__ __align__(16) float blocks[kKv4 ? kHeads : 1][kKv4 ? D + 4 : 4];
   const int tid = threadIdx.x;
   const int H = A.Hq + A.Hkv * (1 + A.has_v);
   const int first = A.tok0 + blockIdx.x * A.per_cta;
@@ -172,6 +240,7 @@ __global__ void __launch_bounds__(kThreads, 4)
       k.n = A.n;
     }
     k.i = tk - k.seq0;
+    if constexpr (kKv4) k.pos = A.positions ? A.positions[tk] : k.i;
     k.slot = -1;
     if (A.slots) {
       k.slot = A.slots[tk];
@@ -212,6 +281,8 @@ __global__ void __launch_bounds__(kThreads, 4)
     if (mt < cnt) load(mt, mh, z0, z1);
     const Token tk = toks[t];
     const bool is_v = h >= A.Hq + A.Hkv, is_q = h < A.Hq;
+    const unsigned group = (kLanes == 8 ? 0xFFu : 0xFu) << ((tid & 31) / kLanes * kLanes);  // lanes of this head
+    float size = 0.f;  // kKv4: the largest |a| + |b| of the head's pairs
     if (!is_v) {
       uint64_t a[4], b[4];
       unpack8(x0, a);
@@ -223,7 +294,6 @@ __global__ void __launch_bounds__(kThreads, 4)
         float s0, s1;
         up2(sum, s0, s1);
         float ss = s0 + s1;
-        const unsigned group = (kLanes == 8 ? 0xFFu : 0xFu) << ((tid & 31) / kLanes * kLanes);
 #pragma unroll
         for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
         const float r = rsqrtf(ss * (1.f / D) + A.eps);
@@ -236,6 +306,19 @@ __global__ void __launch_bounds__(kThreads, 4)
         load8(wa + D / 2, wa + D / 2 + 4 * kLanes, w);
 #pragma unroll
         for (int x = 0; x < 4; ++x) b[x] = mul2(mul2(b[x], rr), w[x]);
+      }
+      if (kKv4 && !is_q) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          float a0, a1, b0, b1;
+          up2(a[x], a0, a1);
+          up2(b[x], b0, b1);
+          size = fmaxf(size, fmaxf(fabsf(a0), fabsf(a1)) + fmaxf(fabsf(b0), fabsf(b1)));
+          if (A.interleaved) size = fmaxf(size, fmaxf(fabsf(a0) + fabsf(a1), fabsf(b0) + fabsf(b1)));
+        }
+        size *= fmaxf(1.f, fabsf(A.rot_scale));
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1) size = fmaxf(size, __shfl_xor_sync(group, size, o));
       }
       if (rotated) {
         uint64_t c[4], s[4];
@@ -271,6 +354,14 @@ __global__ void __launch_bounds__(kThreads, 4)
       }
       x0 = pack8(a);
       x1 = pack8(b);
+      if (kKv4 && !is_q) {
+        float* row = blocks[tid / kLanes];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          *reinterpret_cast<ulonglong2*>(row + c0 + 4 * x) = make_ulonglong2(a[2 * x], a[2 * x + 1]);
+          *reinterpret_cast<ulonglong2*>(row + c1 + 4 * x) = make_ulonglong2(b[2 * x], b[2 * x + 1]);
+        }
+      }
     }
     const int kh = is_q ? h : is_v ? h - A.Hq - A.Hkv : h - A.Hq;
     const int64_t heads = is_q ? A.Hq : A.Hkv;
@@ -280,8 +371,69 @@ __global__ void __launch_bounds__(kThreads, 4)
       __stcs(reinterpret_cast<uint4*>(dst + c0), x0);
       __stcs(reinterpret_cast<uint4*>(dst + c1), x1);
     }
+    if (kKv4 && !is_q && tk.slot >= 0) {
+      // V's chunks to blocks as well, so that a lane has channels 16 l .. 16 l + 15
+      float v[16];
+      float* row = blocks[tid / kLanes];
+      if (is_v) {
+        uint64_t a[4], b[4];
+        unpack8(x0, a);
+        unpack8(x1, b);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          *reinterpret_cast<ulonglong2*>(row + c0 + 4 * x) = make_ulonglong2(a[2 * x], a[2 * x + 1]);
+          *reinterpret_cast<ulonglong2*>(row + c1 + 4 * x) = make_ulonglong2(b[2 * x], b[2 * x + 1]);
+        }
+      }
+      __syncwarp(group);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) *reinterpret_cast<float4*>(v + 4 * x) = *reinterpret_cast<float4*>(row + 16 * l + 4 * x);
+      __syncwarp(group);
+      const float inv = is_v ? A.v_inv : A.k_inv;
+      uint2 codes;
+      uint32_t scale;
+      const bool exact = is_v || (!A.norm && 16 * l >= A.rot);  // neither normed nor turned
+      const uint32_t unsure = round_block(v, inv, exact ? 0.f : size * 1.9073486328125e-06f, codes, scale);  // 2^-19
+      if (__any_sync(group, unsure != 0)) {  // K only
+        const __nv_bfloat16* src = A.k + (first + t) * A.k_stride + kh * D;
+        double ss = 0.0;
+#pragma unroll 1
+        for (int x = 0; x < 16; ++x) {
+          const double y = (double)__bfloat162float(src[16 * l + x]);
+          ss += y * y;
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
+        if (unsure) {
+          const double r = A.norm ? 1.0 / sqrt(ss / D + (double)A.eps) : 1.0;
+          const int pos = tk.pos;
+          if (unsure >> 16) {
+            double a = 0.0;
+#pragma unroll 1
+            for (int x = 0; x < 16; ++x) a = fmax(a, fabs(key64(A, src, 16 * l + x, pos, r)));
+            scale = e4m3_of(sticky(a * (double)inv / 6.0));
+          }
+          const float s = e4m3_value(scale);
+#pragma unroll 1
+          for (int x = 0; x < 16; ++x) {
+            if (!(unsure >> 16) && !(unsure >> x & 1u)) continue;
+            const double y = key64(A, src, 16 * l + x, pos, r);
+            const uint32_t c = (e2m1x2_of(s > 0.f ? sticky(fabs(y) * (double)inv / (double)s) : 0.f, 0.f) & 7u) | (y < 0.0 ? 8u : 0u);
+            const int sh = 4 * (x & 7);
+            uint32_t& w = x < 8 ? codes.x : codes.y;
+            w = (w & ~(0xFu << sh)) | c << sh;
+          }
+        }
+        __syncwarp(group);
+      }
+      const int off = tk.slot & ((1 << A.page_shift) - 1);
+      const int64_t size4 = (int64_t)kv4_unit<D>() << A.page_shift;
+      uint8_t* unit = A.kv4 + (((int64_t)(tk.slot >> A.page_shift) * A.Hkv + kh) * 2 + (is_v ? 1 : 0)) * size4;
+      *reinterpret_cast<uint2*>(unit + ((((l >> 1) << A.page_shift) + off) << 4) + 8 * (l & 1)) = codes;
+      unit[((D / 2) << A.page_shift) + off * (D / 16) + l] = (uint8_t)scale;
+    }
     __nv_bfloat16* pages = is_v ? A.vp : A.kp;
-    if (!is_q && pages && tk.slot >= 0) {
+    if (!kKv4 && !is_q && pages && tk.slot >= 0) {
       const int64_t page = tk.slot >> A.page_shift;
       const int off = tk.slot & ((1 << A.page_shift) - 1);
       __nv_bfloat16* dst = pages + (((page * A.Hkv + kh) << A.page_shift) + off) * D;
@@ -320,7 +472,7 @@ uint64_t turns64(double f) {
 msa_status norm_rope(const msa_shape& s, const int32_t* cu, int32_t n_seqs, const msa_rope_cfg* cfg, const void* q_in,
                      int64_t q_stride, const void* k_in, int64_t k_stride, const void* v_in, int64_t v_stride,
                      const int32_t* positions, void* q, void* k, void* v, const msa_kv_pages* pages,
-                     const int32_t* slots, int64_t tokens, cudaStream_t stream) {
+                     const msa_kv4_pages* kv4, const int32_t* slots, int64_t tokens, cudaStream_t stream) {
   if (!cfg) return MSA_ERR_INVALID_ARG;
   if (cfg->rot_dim < 0 || cfg->rot_dim > s.d_h || !(cfg->eps >= 0.f) || isinf(cfg->eps)) return MSA_ERR_INVALID_ARG;
   if (cfg->norm != 0 && cfg->norm != 1) return MSA_ERR_INVALID_ARG;
@@ -336,10 +488,10 @@ msa_status norm_rope(const msa_shape& s, const int32_t* cu, int32_t n_seqs, cons
       (v_in && v_stride < (int64_t)s.Hkv * s.d_h))
     return MSA_ERR_INVALID_ARG;
   if (q_stride % 8 || k_stride % 8 || (v_in && v_stride % 8)) return MSA_ERR_INVALID_ARG;
-  if (!k && !pages) return MSA_ERR_INVALID_ARG;          // the keys would go nowhere
-  if (v_in ? !v && !pages : v || pages) return MSA_ERR_INVALID_ARG;  // values come and go together
+  if (!k && !pages && !kv4) return MSA_ERR_INVALID_ARG;  // the keys would go nowhere
+  if (v_in ? !v && !pages && !kv4 : v || pages || kv4) return MSA_ERR_INVALID_ARG;  // values come and go together
   // rows move: not in place, nor two outputs in one
-  const void* outs[5] = {q, k, v, pages ? pages->k : nullptr, pages ? pages->v : nullptr};
+  const void* outs[5] = {q, k, v, pages ? pages->k : kv4 ? kv4->data : nullptr, pages ? pages->v : nullptr};
   for (int x = 0; x < 5; ++x) {
     if (!outs[x]) continue;
     if (outs[x] == q_in || outs[x] == k_in || outs[x] == v_in) return MSA_ERR_INVALID_ARG;
@@ -357,6 +509,16 @@ msa_status norm_rope(const msa_shape& s, const int32_t* cu, int32_t n_seqs, cons
     a.slots = slots;
     a.page_shift = __builtin_ctz((unsigned)pages->page_size);
     a.num_pages = pages->num_pages;
+  } else if (kv4) {
+    const msa_status ok = check_kv4_pages(kv4);
+    if (ok != MSA_OK) return ok;
+    if (!slots) return MSA_ERR_INVALID_ARG;
+    a.kv4 = static_cast<uint8_t*>(kv4->data);
+    a.k_inv = 1.f / kv4_scale(kv4->k_scale);
+    a.v_inv = 1.f / kv4_scale(kv4->v_scale);
+    a.slots = slots;
+    a.page_shift = __builtin_ctz((unsigned)kv4->page_size);
+    a.num_pages = kv4->num_pages;
   } else if (slots) {
     return MSA_ERR_INVALID_ARG;
   }
@@ -403,8 +565,10 @@ msa_status norm_rope(const msa_shape& s, const int32_t* cu, int32_t n_seqs, cons
   };
   if (!cu) {
     a.tok1 = (int32_t)tokens;
-    const bool ok = s.d_h == 128 ? launch(norm_rope_kernel<128, false>, Seqs<false>())
-                                 : launch(norm_rope_kernel<64, false>, Seqs<false>());
+    const bool ok = kv4 ? (s.d_h == 128 ? launch(norm_rope_kernel<128, false, true>, Seqs<false>())
+                                        : launch(norm_rope_kernel<64, false, true>, Seqs<false>()))
+                        : (s.d_h == 128 ? launch(norm_rope_kernel<128, false, false>, Seqs<false>())
+                                        : launch(norm_rope_kernel<64, false, false>, Seqs<false>()));
     return ok ? MSA_OK : MSA_ERR_CUDA;
   }
   Seqs<true> t;
@@ -415,7 +579,10 @@ msa_status norm_rope(const msa_shape& s, const int32_t* cu, int32_t n_seqs, cons
     a.tok0 = t.cu[0];
     a.tok1 = t.cu[t.count];
     if (a.tok1 <= a.tok0) continue;
-    const bool ok = s.d_h == 128 ? launch(norm_rope_kernel<128, true>, t) : launch(norm_rope_kernel<64, true>, t);
+    const bool ok = kv4 ? (s.d_h == 128 ? launch(norm_rope_kernel<128, true, true>, t)
+                                        : launch(norm_rope_kernel<64, true, true>, t))
+                        : (s.d_h == 128 ? launch(norm_rope_kernel<128, true, false>, t)
+                                        : launch(norm_rope_kernel<64, true, false>, t));
     if (!ok) return MSA_ERR_CUDA;
   }
   return MSA_OK;
@@ -427,21 +594,22 @@ msa_status norm_rope(const msa_shape& s, const int32_t* cu, int32_t n_seqs, cons
 
 using namespace msa;
 
-extern "C" msa_status msa_qk_norm_rope(const msa_shape* shape, const msa_rope_cfg* cfg, const void* q_in,
-                                       int64_t q_stride, const void* k_in, int64_t k_stride, const void* v_in,
-                                       int64_t v_stride, const int32_t* positions, void* q, void* k, void* v,
-                                       const msa_kv_pages* pages, const int32_t* slots, void* stream) {
+namespace {
+
+msa_status uniform(const msa_shape* shape, const msa_rope_cfg* cfg, const void* q_in, int64_t q_stride,
+                   const void* k_in, int64_t k_stride, const void* v_in, int64_t v_stride, const int32_t* positions,
+                   void* q, void* k, void* v, const msa_kv_pages* pages, const msa_kv4_pages* kv4,
+                   const int32_t* slots, void* stream) {
   const msa_status st = check_shape(shape);
   if (st != MSA_OK) return st;
   return norm_rope(*shape, nullptr, 0, cfg, q_in, q_stride, k_in, k_stride, v_in, v_stride, positions, q, k, v, pages,
-                   slots, (int64_t)shape->B * shape->n, (cudaStream_t)stream);
+                   kv4, slots, (int64_t)shape->B * shape->n, (cudaStream_t)stream);
 }
 
-extern "C" msa_status msa_qk_norm_rope_varlen(const msa_shape* shape, const int32_t* cu_seqlens, int32_t n_seqs,
-                                              const msa_rope_cfg* cfg, const void* q_in, int64_t q_stride,
-                                              const void* k_in, int64_t k_stride, const void* v_in, int64_t v_stride,
-                                              const int32_t* positions, void* q, void* k, void* v,
-                                              const msa_kv_pages* pages, const int32_t* slots, void* stream) {
+msa_status varlen(const msa_shape* shape, const int32_t* cu_seqlens, int32_t n_seqs, const msa_rope_cfg* cfg,
+                  const void* q_in, int64_t q_stride, const void* k_in, int64_t k_stride, const void* v_in,
+                  int64_t v_stride, const int32_t* positions, void* q, void* k, void* v, const msa_kv_pages* pages,
+                  const msa_kv4_pages* kv4, const int32_t* slots, void* stream) {
   if (!shape || !cu_seqlens || n_seqs < 1 || cu_seqlens[0] != 0) return MSA_ERR_INVALID_ARG;
   msa_shape s = *shape;
   s.B = 1;
@@ -451,5 +619,44 @@ extern "C" msa_status msa_qk_norm_rope_varlen(const msa_shape* shape, const int3
   for (int x = 0; x < n_seqs; ++x)
     if (cu_seqlens[x + 1] < cu_seqlens[x]) return MSA_ERR_INVALID_ARG;
   return norm_rope(s, cu_seqlens, n_seqs, cfg, q_in, q_stride, k_in, k_stride, v_in, v_stride, positions, q, k, v,
-                   pages, slots, cu_seqlens[n_seqs], (cudaStream_t)stream);
+                   pages, kv4, slots, cu_seqlens[n_seqs], (cudaStream_t)stream);
+}
+
+}  // namespace
+
+extern "C" msa_status msa_qk_norm_rope(const msa_shape* shape, const msa_rope_cfg* cfg, const void* q_in,
+                                       int64_t q_stride, const void* k_in, int64_t k_stride, const void* v_in,
+                                       int64_t v_stride, const int32_t* positions, void* q, void* k, void* v,
+                                       const msa_kv_pages* pages, const int32_t* slots, void* stream) {
+  return uniform(shape, cfg, q_in, q_stride, k_in, k_stride, v_in, v_stride, positions, q, k, v, pages, nullptr, slots,
+                 stream);
+}
+
+extern "C" msa_status msa_qk_norm_rope_varlen(const msa_shape* shape, const int32_t* cu_seqlens, int32_t n_seqs,
+                                              const msa_rope_cfg* cfg, const void* q_in, int64_t q_stride,
+                                              const void* k_in, int64_t k_stride, const void* v_in, int64_t v_stride,
+                                              const int32_t* positions, void* q, void* k, void* v,
+                                              const msa_kv_pages* pages, const int32_t* slots, void* stream) {
+  return varlen(shape, cu_seqlens, n_seqs, cfg, q_in, q_stride, k_in, k_stride, v_in, v_stride, positions, q, k, v,
+                pages, nullptr, slots, stream);
+}
+
+extern "C" msa_status msa_qk_norm_rope_kv4(const msa_shape* shape, const msa_rope_cfg* cfg, const void* q_in,
+                                           int64_t q_stride, const void* k_in, int64_t k_stride, const void* v_in,
+                                           int64_t v_stride, const int32_t* positions, void* q, void* k, void* v,
+                                           const msa_kv4_pages* pages, const int32_t* slots, void* stream) {
+  if (!pages || !v_in) return MSA_ERR_INVALID_ARG;
+  return uniform(shape, cfg, q_in, q_stride, k_in, k_stride, v_in, v_stride, positions, q, k, v, nullptr, pages, slots,
+                 stream);
+}
+
+extern "C" msa_status msa_qk_norm_rope_varlen_kv4(const msa_shape* shape, const int32_t* cu_seqlens, int32_t n_seqs,
+                                                  const msa_rope_cfg* cfg, const void* q_in, int64_t q_stride,
+                                                  const void* k_in, int64_t k_stride, const void* v_in,
+                                                  int64_t v_stride, const int32_t* positions, void* q, void* k,
+                                                  void* v, const msa_kv4_pages* pages, const int32_t* slots,
+                                                  void* stream) {
+  if (!pages || !v_in) return MSA_ERR_INVALID_ARG;
+  return varlen(shape, cu_seqlens, n_seqs, cfg, q_in, q_stride, k_in, k_stride, v_in, v_stride, positions, q, k, v,
+                nullptr, pages, slots, stream);
 }

@@ -1179,16 +1179,6 @@ TreeWs tree_ws(const msa_shape& s) {
   return w;
 }
 
-msa_status check_tree_shape(const msa_shape* s) {
-  const msa_status st = check_shape(s);
-  if (st != MSA_OK) return st;
-  const int64_t rows = (int64_t)s->B * s->Hq * s->n;
-  const int64_t R = (int64_t)(s->Hq / s->Hkv) * s->n, RB = (R + 255) / 256;
-  if (s->n > kMaxDrafts || rows + 256 >= ((int64_t)1 << 31)) return MSA_ERR_UNSUPPORTED;
-  if ((int64_t)s->B * s->Hkv * RB >= ((int64_t)1 << 31)) return MSA_ERR_UNSUPPORTED;
-  return MSA_OK;
-}
-
 bool aligned(const void* p, size_t a, bool required) {
   if (!p) return !required;
   return reinterpret_cast<uintptr_t>(p) % a == 0;
@@ -1228,6 +1218,16 @@ msa_status launch_tree(const TreeMaps& maps, const TreeArgs& a, bool join, cudaS
 }
 
 }  // namespace
+
+msa_status check_tree_shape(const msa_shape* s) {
+  const msa_status st = check_shape(s);
+  if (st != MSA_OK) return st;
+  const int64_t rows = (int64_t)s->B * s->Hq * s->n;
+  const int64_t R = (int64_t)(s->Hq / s->Hkv) * s->n, RB = (R + 255) / 256;
+  if (s->n > kMaxDrafts || rows + 256 >= ((int64_t)1 << 31)) return MSA_ERR_UNSUPPORTED;
+  if ((int64_t)s->B * s->Hkv * RB >= ((int64_t)1 << 31)) return MSA_ERR_UNSUPPORTED;
+  return MSA_OK;
+}
 
 }  // namespace msa
 

@@ -103,9 +103,11 @@ def check_rounded(got, ref, slack, what):
 
 
 # ------------------------------------------------------------------ attention over pages
-def attend(q, k, v, seen, scale):
+def attend(q, k, v, seen, scale, half=BF16_HALF, floor=0.0):
     """q [H, rows, d], k / v [L, d] of one KV head, seen [rows, L]: (o, lse) in
-    float64 and bounds on the kernel's errors in them.
+    float64 and bounds on the kernel's errors in them.  half: half a step of the
+    type that weights are rounded to; floor: what a weight may be off by
+    absolutely, as a share of the row's largest one.
 
     Scores: d exact bf16 products summed in fp32, at most d steps of 2^-23 (an
     accumulator that truncates) of the absolute sum; delta, in nats, is that
@@ -122,7 +124,9 @@ def attend(q, k, v, seen, scale):
     o = torch.einsum("hrl,ld->hrd", p, v)
     a = torch.einsum("hrl,ld->hrd", p, v.abs())
     delta = q.shape[-1] * 2.0 ** -23 * size.masked_fill(~seen, 0.0).amax(-1) + 2.0 ** -20
-    o_tol = a * (BF16_HALF + 2 * delta[..., None] + L * 2.0 ** -23) + BF16_HALF * o.abs() + 2.0 ** -100
+    o_tol = a * (half + 2 * delta[..., None] + L * 2.0 ** -23) + BF16_HALF * o.abs() + 2.0 ** -100
+    if floor:
+        o_tol += floor * p.amax(-1, keepdim=True) * (seen.any(0)[:, None] * v.abs()).sum(0)
     lse_tol = delta + L * 2.0 ** -23 + 2.0 ** -21 * (1 + torch.where(torch.isinf(lse), 0.0, lse.abs()))
     return o, lse, o_tol, lse_tol
 
@@ -182,3 +186,93 @@ def check_tree(q, k_pages, v_pages, table, lens, tls, masks, o, lse, o0, lse0, s
             assert bool((e <= to).all()), f"{what}: request {b} head {h}: o off by {float((e - to).max()):.3e} above {float(to.max()):.3e}"
             e = torch.where(none, 0.0, gl - rl).abs()
             assert bool((e <= tl).all()), f"{what}: request {b} head {h}: lse off by {float(e.max()):.3e}"
+
+
+# ------------------------------------------------------------------ windows
+def seen_keys(L, T, mask=None, depth=None, sink=0, window=0):
+    """[T, L] bool: the keys that each drafted row of a request sees (window 0: no window)."""
+    C = L - T
+    seen = np.ones((T, L), bool)
+    seen[:, C:] = np.tril(np.ones((T, T), bool)) if mask is None else np.asarray(mask)[:T, :T]
+    if window:
+        for i in range(T):
+            p = C + (i if depth is None else int(depth[i]))
+            end = p - window + 1 if mask is None else min(C, p - window + 1)  # a mask decides on the drafted keys
+            if end > sink:
+                seen[i, sink:end] = False
+    return seen
+
+
+def check_rows(q, keys, values, lens, tls, seen, o, lse, o0, lse0, scale=None, what="", **weights):
+    """Every row of an attention over a cache.  keys(b, h), values(b, h): [L, d]; seen(b): [T, L] bool; o0 / lse0: what
+    the outputs held before.  Keys that no row sees may hold anything."""
+    B, Hq, n, d = q.shape
+    scale = 1 / math.sqrt(d) if scale is None else scale
+    for b in range(B):
+        L, T = int(lens[b]), int(tls[b])
+        assert torch.equal(o[b, :, T:], o0[b, :, T:]) and torch.equal(lse[b, :, T:], lse0[b, :, T:]), f"{what}: rows behind request {b}"
+        if T == 0:
+            continue
+        see = torch.from_numpy(np.ascontiguousarray(seen(b))).to(q.device)
+        use = torch.nonzero(see.any(0))[:, 0]  # the others do not matter
+        Hkv = keys(b, None)
+        g = Hq // Hkv
+        for h in range(Hkv):
+            k, v = keys(b, h)[use], values(b, h)[use]
+            ro, rl, to, tl = attend(q[b, h * g:(h + 1) * g, :T], k, v, see[:, use], scale, **weights)
+            go, gl = o[b, h * g:(h + 1) * g, :T].double(), lse[b, h * g:(h + 1) * g, :T].double()
+            none = torch.isinf(rl)
+            assert torch.equal(torch.isneginf(gl), none), f"{what}: rows without keys, request {b} head {h}"
+            assert bool((go[none] == 0).all()), f"{what}: output of rows without keys, request {b} head {h}"
+            e = (go - ro).abs()
+            assert bool((e <= to).all()), f"{what}: request {b} head {h}: o off by {float((e - to).max()):.3e} above {float(to.max()):.3e}"
+            e = torch.where(none, 0.0, gl - rl).abs()
+            assert bool((e <= tl).all()), f"{what}: request {b} head {h}: lse off by {float(e.max()):.3e}"
+
+
+# ------------------------------------------------------------------ the 4-bit cache
+E2M1 = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]
+
+# fp16 weights: half a step relative (torch.finfo(torch.float16).eps / 2), and where they are subnormal half a step of
+# 2^-24 absolutely, with a row's largest weight held at 2^7 or more
+KV4_WEIGHTS = dict(half=2.0 ** -11, floor=2.0 ** -32)
+
+
+def kv4_round(x, scale=1.0):
+    """fp64 x [.., d] rounded to the 4-bit cache's blocks: (values, codes uint8 [.., d], e4m3 bytes [.., d/16])."""
+    b = x.double().unflatten(-1, (-1, 16)) / scale
+    a = (b.abs().amax(-1, keepdim=True) / 6).clamp(max=448.0)
+    e = torch.frexp(a)[1].clamp(min=-5) - 1  # a in [2^e, 2^(e+1)), subnormal below 2^-6
+    step = torch.exp2(e.double() - 3)
+    s = torch.round(a / step) * step
+    t = torch.where(s > 0, b.abs() / s, 0.0)
+    unit = torch.where(t < 2, 0.5, torch.where(t < 4, 1.0, 2.0))
+    m = (torch.round(t / unit) * unit).clamp(max=6.0)  # torch.round: ties to even, which are the even codes
+    neg = torch.signbit(b)
+    table = torch.tensor(E2M1, dtype=torch.float64, device=x.device)
+    codes = torch.bucketize(m, table).to(torch.uint8) | neg.to(torch.uint8) << 3
+    return ((torch.where(neg, -m, m) * s * scale).flatten(-2), codes.flatten(-2),
+            s[..., 0].float().to(torch.float8_e4m3fn).view(torch.uint8))
+
+
+def kv4_values(data, page, d, k_scale=1.0, v_scale=1.0):
+    """The values that pages uint8 [.., bytes] hold: K and V, fp64 [.., page, d] (a NaN scale: NaN)."""
+    out = []
+    half, size = page * d // 2, page * (d // 2 + d // 16)
+    table = torch.tensor(E2M1 + [-x for x in E2M1], dtype=torch.float64, device=data.device)
+    for x, g in ((data[..., :size], k_scale), (data[..., size:], v_scale)):
+        c = x[..., :half].unflatten(-1, (d // 32, page, 16)).transpose(-3, -2)
+        c = torch.stack([c & 15, c >> 4], -1).flatten(-3)
+        s = x[..., half:].contiguous().view(torch.float8_e4m3fn).double().unflatten(-1, (page, d // 16))
+        out.append(table[c.int()] * s.repeat_interleave(16, -1) * g)
+    return out
+
+
+def kv4_store(data, page, d, which, slots, codes, scales):
+    """Write tokens' codes [tokens, Hkv, d] and scales [tokens, Hkv, d/16] to their slots of K (which = 0) or V (1)."""
+    half, size = page * d // 2, page * (d // 2 + d // 16)
+    x = data[..., which * size:(which + 1) * size]
+    pg, off = slots // page, slots % page
+    c = codes.unflatten(-1, (d // 32, 16, 2))
+    x[..., :half].unflatten(-1, (d // 32, page, 16))[pg, :, :, off] = c[..., 0] | c[..., 1] << 4
+    x[..., half:].unflatten(-1, (page, d // 16))[pg, :, off] = scales
