@@ -1,6 +1,5 @@
-// Attention of drafted tokens over a paged cache held in 4 bits, and through a
-// window that keeps the first tokens over either cache: the plain kernel, one
-// CTA per row, its warps taking keys in turn, joined at the end.
+// Attention of drafted tokens over a paged cache held in 4 bits: the plain
+// kernel, one CTA per row, its warps taking keys in turn, joined at the end.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <string.h>
@@ -198,19 +197,4 @@ extern "C" msa_status msa_attn_tree_kv4(const msa_shape* shape, const void* q, c
   if (st != MSA_OK) return st;
   return rows(shape, q, nullptr, pages, page_table, max_pages, seq_len, tree_len, tree_mask, mask_stride, window, o, lse,
               ws, ws_bytes, msa_attn_tree_kv4_workspace(shape), stream);
-}
-
-extern "C" msa_status msa_attn_tree_window(const msa_shape* shape, const void* q, const msa_kv_pages* pages,
-                                           const int32_t* page_table, int32_t max_pages, const int32_t* seq_len,
-                                           const int32_t* tree_len, const uint32_t* tree_mask, int64_t mask_stride,
-                                           const msa_tree_window* window, void* o, float* lse, void* ws,
-                                           size_t ws_bytes, void* stream) {
-  msa_status st = check_tree_shape(shape);
-  if (st != MSA_OK) return st;
-  if (!pages || !window) return MSA_ERR_INVALID_ARG;
-  st = check_page_geometry(pages->num_pages, pages->page_size);
-  if (st != MSA_OK) return st;
-  if (!aligned(pages->k, 16, true) || !aligned(pages->v, 16, true)) return MSA_ERR_INVALID_ARG;
-  return rows(shape, q, pages, nullptr, page_table, max_pages, seq_len, tree_len, tree_mask, mask_stride, window, o, lse,
-              ws, ws_bytes, msa_attn_tree_workspace(shape), stream);
 }

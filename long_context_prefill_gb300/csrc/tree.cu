@@ -62,24 +62,14 @@
 // and slower there (against 162 to 174 us): a score tile per group with P over it
 // 194 us, turns of the groups on a scheduler 192 to 253 us, scores by halves of 64
 // keys 208 us, products held back while scores are computed 175 us.
-#include <cuda_bf16.h>
-#include <math.h>
-#include <string.h>
-
 #include <type_traits>
 
-#include "internal.h"
-#include "ptx.cuh"
+#include "tree.cuh"
 
 namespace msa {
 
-msa_status check_shape(const msa_shape* s);
-msa_status check_page_geometry(int32_t num_pages, int32_t page_size);
-float effective_scale(const msa_shape& s);
-
 namespace {
 
-constexpr int kCtas = 152;
 constexpr int kCleanWarp = 8, kMmaWarp0 = 9, kLoaderWarp = 10, kMmaWarp1 = 11;
 constexpr int kSegSlots = 3;
 enum Rows { kFew = 0, kMany = 1, kTwo = 2 };
@@ -95,39 +85,8 @@ constexpr uint32_t kIdleNs = 64;
 constexpr uint64_t kDrainNs = MSA_WAIT_LIMIT_NS / 16;  // a CTA that gave up: for each copy and product in flight
 constexpr int kMaxDrafts = 1024;
 
-struct Cut;
-
-struct TreeArgs {
-  int32_t B, Hq, Hkv, n, R, RB, page_shift, max_pages, num_pages, words, q_box, max_parts;
-  const int32_t *table, *seq_len, *tree_len;
-  const uint32_t* mask;
-  int64_t mask_stride;  // words between the masks of two requests (0: one mask for all)
-  __nv_bfloat16* o;
-  float* lse;
-  int32_t* count;   // parts of the line
-  Cut* cuts;        // [max_parts] what they cut
-  float4* part;     // [2 max_parts][d/4][rows] unnormalised O of the cut items
-  float2* part_ml;  // [2 max_parts][rows] their maximum (log2) and row sum
-  float scale_log2;
-  int* err;
-};
-
 struct TreeMaps {
   CUtensorMap q, k, v;  // [rows, d] views, boxes of 64 columns x q_box rows (q), x page_size rows (k, v)
-};
-
-// The piece of one item that lies in a part: tiles t0 .. t1 of its `tiles`.
-struct Seg {
-  int32_t b, kvh, rb, t0, t1, tiles;  // b < 0: no more
-  int32_t L, T;
-  int32_t r0, r1;  // tiles that its result covers: t0, t1, or more where both groups' segments are joined
-};
-
-// The item that a part's beginning cuts, if this is the first cut through it: n parts, the first in slot `first` of
-// the workspace, k = 1 .. inner in slots base + step k, another one in `tail`.
-struct __align__(16) Cut {
-  int32_t n;  // 1 or less: nothing to join
-  int32_t b, item, inner, first, base, step, tail;
 };
 
 // Barriers; [X]: per group (kTwo: segments and Q once, at X = 0)
@@ -165,60 +124,8 @@ struct Lay {
   static_assert(kAlloc <= 227 * 1024 && kAlloc > 120 * 1024, "shared memory: one CTA per SM");
 };
 
-// Keys and drafted tokens of request b; false (nothing to compute) when it has
-// none or its numbers break the contract (flagged once by the loader).
-__device__ __forceinline__ bool request(const TreeArgs& A, int b, int& L, int& T, bool& bad) {
-  L = A.seq_len[b];
-  T = A.tree_len ? A.tree_len[b] : A.n;
-  bad = T < 0 || T > A.n || L < T || L > ((int64_t)A.max_pages << A.page_shift);
-  return !bad && T > 0;
-}
-__device__ __forceinline__ int key_tiles(int L) { return (L + 127) >> 7; }
-// The line of W tiles in G = min(W, max_parts) parts.  CTA c's groups take parts 2 c and 2 c + 1 if there are
-// max_parts of them (of two per CTA), else parts c and kCtas + c.
-__device__ __forceinline__ int parts(int64_t W, int most) { return W < most ? (int)W : most; }
-__device__ __forceinline__ int part_of(int64_t W, int most, int cta, int X) {
-  return most > kCtas && W >= most ? 2 * cta + X : cta + kCtas * X;
-}
-__device__ __forceinline__ int64_t part_begin(int64_t W, int most, int p) { return W < most ? p : W * p / most; }
-
-// kMany, all parts present: the odd part of a CTA that lies within one item [s0, s1) which its even part reaches too
-// is joined with it in the CTA.
-__device__ __forceinline__ bool joined_in_cta(bool many, int64_t W, int most, int p, int64_t s0, int64_t s1) {
-  return many && W >= most && (p & 1) && part_begin(W, most, p) > s0 && part_begin(W, most, p + 1) <= s1;
-}
-
-// a / b for a >= 0, b > 0, in 32 bits where they suffice (64-bit division takes some hundred cycles)
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
-}
-
-// What the beginning of part p cuts, which lies in request b, whose tiles begin at `at`.
-template <Rows kRows, int kMost>
-__device__ void note_cut(const TreeArgs& A, int64_t W, int p, int b, int64_t at) {
-  const int64_t lo = part_begin(W, kMost, p);
-  const int tiles = key_tiles(A.seq_len[b]);
-  const int64_t item = quotient(lo - at, tiles), s0 = at + item * tiles, s1 = s0 + tiles;
-  Cut c = {0, b, (int32_t)item, 0, 0, 0, 0, 0};
-  if (lo > s0 && part_begin(W, kMost, p - 1) <= s0) {
-    // kMany, all parts present: an odd part that was joined in its CTA stands in the slot of the even one; only the
-    // first and the last part of an item can be odd and not
-    const bool pairs = kRows == kMany && W >= kMost;
-    const int c0 = p - 1, c1 = (int)quotient(s1 * parts(W, kMost) - 1, W);  // the largest part that begins below s1
-    const int lead = pairs && !(c0 & 1) ? 2 : 1;
-    const bool tail = pairs && (c1 & 1) && c1 != c0 && !joined_in_cta(true, W, kMost, c1, s0, s1);
-    c.step = pairs ? 2 : 1;
-    c.inner = c0 + lead <= c1 ? (c1 - c0 - lead) / c.step + 1 : 0;
-    c.n = 1 + c.inner + (tail ? 1 : 0);
-    c.first = 2 * c0 + 1;
-    c.base = 2 * (c0 + lead - c.step);
-    c.step *= 2;
-    c.tail = 2 * c1;
-  }
-  A.cuts[p] = c;
-}
-
-template <int D, Rows kRows>
+// kWin: through a window (msa_attn_tree_window); tiles without a key that some row sees are not in the line.
+template <int D, Rows kRows, bool kWin>
 __global__ void __launch_bounds__(threads_of(kRows), 1)
     tree_attn_kernel(const __grid_constant__ TreeMaps M, const TreeArgs A) {
   using Ly = Lay<D>;
@@ -303,7 +210,7 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
       bool bad;
       const bool live = request(A, b, L, T, bad);
       if (bad && blockIdx.x == 0) atomicCAS(A.err, 0, (int)kErrIndex);
-      return live ? (int64_t)items * key_tiles(L) : 0;
+      return live ? (int64_t)items * span_of<kWin>(A, L, T).tiles : 0;
     };
     int64_t own = 0, mine = 0;  // of the last request, of all of this thread's
     for (int b = b0; b < b1; ++b) mine += own = tiles(b);
@@ -410,7 +317,8 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
       int b = (int)start[2 * X], s = 0, t = 0;        // request, segments so far, next tile of the segment
       int last = -1, asked = 0;  // the last ring load into slot `lane`; segments whose Q was asked for
       Seg g;
-      int base, ids, ahead;  // lane x holds the page of entry base + x, and of base + 32 + x
+      Span span;
+      int base, ids, ahead;  // lane x holds the page of entry base + x, and of base + 32 + x (counted along the line)
       auto publish = [&](const Seg& g) -> bool {
         const int slot = X * kSegSlots + s % kSegSlots;
         if (misc[2] || !mbar_wait_idle(&bars[kBarSegEmpty + slot], ((s / kSegSlots) & 1) ^ 1, kIdleNs)) return false;
@@ -421,6 +329,10 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
         return true;
       };
       auto entry = [&](const Seg& g, int p) {
+        if (kWin) {
+          p = (span.tile(p >> pshift) << pshift) + (p & (pp - 1));
+          if (span.gone(p, A.page_shift)) return 0;  // an existing page stands in
+        }
         return p < (g.L + P - 1) >> A.page_shift ? A.table[(int64_t)g.b * A.max_pages + p] : 0;
       };
       auto checked = [&](int page) {
@@ -433,13 +345,15 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
         bool bad;
         int64_t tiles = 0;
         for (; b < A.B; ++b) {  // pos < hi <= W: a request holding it exists
-          tiles = request(A, b, g.L, g.T, bad) ? (int64_t)items * key_tiles(g.L) : 0;
+          const bool live = request(A, b, g.L, g.T, bad);
+          span = span_of<kWin>(A, g.L, g.T);
+          tiles = live ? (int64_t)items * span.tiles : 0;
           if (pos < at + tiles) break;
           at += tiles;
         }
         if (b >= A.B) return false;
         g.b = b;
-        g.tiles = key_tiles(g.L);
+        g.tiles = span.tiles;
         const int item = (int)quotient(pos - at, g.tiles);
         g.kvh = item / A.RB;
         g.rb = item - g.kvh * A.RB;
@@ -504,7 +418,7 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
           ahead = checked(entry(g, base + 32 + lane));
         }
         const int np = (g.L + P - 1) >> A.page_shift;
-        const int boxes = min(pp, np - (t << pshift)) * (D / 64);  // pages of this tile that hold keys, by 64 columns
+        const int boxes = min(pp, np - (span.tile(t) << pshift)) * (D / 64);  // pages of this tile that hold keys, by 64 columns
         const int c = lane & (D / 64 - 1), x = lane / (D / 64);
         const int krow = (__shfl_sync(0xFFFFFFFFu, ids, (off + x) & 31) * A.Hkv + g.kvh) << A.page_shift;
 #pragma unroll
@@ -534,11 +448,12 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
       // ---------------------------------------------------------- tiles in order, rows past a request's end
       struct Walk {
         int b_end, L, t, s;  // end of the segment, keys of its request, next tile, segments so far
+        Span span;
       };
-      Walk w = {0, 0, 0, 0}, other = {0, 0, 0, 0};
+      Walk w = {0, 0, 0, 0, {}}, other = {0, 0, 0, 0, {}};
       int X = 0;
       if (lane < 2 && (lane ? cnt[1] : cnt[0]) > 0)  // what the parts cut, for the second kernel
-        note_cut<kRows, kMost>(A, W, part_of(W, kMost, blockIdx.x, lane), (int)start[2 * lane], start[2 * lane + 1]);
+        note_cut<kRows == kMany, kMost, kWin>(A, W, part_of(W, kMost, blockIdx.x, lane), (int)start[2 * lane], start[2 * lane + 1]);
       for (int j = 0; j < cnt[0] + cnt[1] && ok; ++j) {
         if (owner(j) != X) {
           const Walk t = w;
@@ -552,19 +467,26 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
           w.t = g.t0;
           w.b_end = g.t1;
           w.L = g.L;
+          w.span = span_of<kWin>(A, g.L, g.T);
         }
-        const int keys = w.L - 128 * w.t++;
+        const int key0 = w.span.key0(w.t++), keys = w.L - key0;
+        // rows of the tile that hold keys which no row sees (below 0, above 127: none)
+        const int h0 = max(0, w.span.hole - key0), h1 = min(128, w.span.lo - key0);
 #pragma unroll 1
         for (int idx = 2 * j; idx < 2 * j + 2; ++idx) {
           const int st = idx % kSlots;
           if (misc[2] || !mbar_wait(&bFull[st], (idx / kSlots) & 1)) { ok = false; break; }
-          if ((idx & 1) && keys < 128) {
+          if ((idx & 1) && (keys < 128 || (kWin && h0 < h1))) {
             uint8_t* v = sm + Ly::kRing + st * Ly::kTile;
+            auto zero = [&](int r0, int r1) {
 #pragma unroll 1
-            for (int x = keys * 8 + lane; x < 1024; x += 32)
+              for (int x = r0 * 8 + lane; x < r1 * 8; x += 32)
 #pragma unroll
-              for (int c = 0; c < D / 64; ++c)
-                *reinterpret_cast<uint4*>(v + c * 16384 + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+                for (int c = 0; c < D / 64; ++c)
+                  *reinterpret_cast<uint4*>(v + c * 16384 + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+            };
+            zero(keys, 128);
+            if (kWin) zero(h0, h1);
             fence_proxy_async_smem();
             __syncwarp();
           }
@@ -706,15 +628,19 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
       const int C = g.L - g.T;
       const uint32_t* mrow = A.mask ? A.mask + g.b * A.mask_stride + (int64_t)i * A.words : nullptr;
       // bit k: this row attends key key0 + k (keys from the end of the context on; lanes without a row see all)
+      const Span span = span_of<kWin>(A, g.L, g.T);
+      const int end = kWin ? behind(A, g.b, i, C) : 0;  // keys sink .. end - 1 are outside this row's window
       auto mask32 = [&](int key0) -> uint32_t {
         const int rel = key0 - C;  // drafted index of bit 0 (negative: context)
-        if (rel <= -32 || !row_ok) return ~0u;
-        if (!mrow) return low_mask32(min(i + 1, g.T) - rel);
+        if (!row_ok) return ~0u;
+        const uint32_t in = kWin ? ~(low_mask32(end - key0) & ~low_mask32(A.sink - key0)) : ~0u;
+        if (rel <= -32) return in;
+        if (!mrow) return low_mask32(min(i + 1, g.T) - rel) & in;
         const int w0 = rel >> 5, sh = rel & 31;  // floor for negative rel
         const uint32_t a = (w0 >= 0 && w0 < A.words) ? __ldg(mrow + w0) : 0u;
         const uint32_t c = (w0 + 1 < A.words) ? __ldg(mrow + w0 + 1) : 0u;
         const uint32_t bits = __funnelshift_r(a, c, sh) & low_mask32(g.T - rel);
-        return rel < 0 ? bits | low_mask32(-rel) : bits;
+        return (rel < 0 ? bits | low_mask32(-rel) : bits) & in;
       };
       float m_used = -INFINITY, l = 0.f;
       bool first = true;      // no product into O yet
@@ -791,8 +717,9 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
       if (rows > 0)
         for (int t = g.t0; t < g.t1; ++t) {
           if (misc[2]) { ok = false; break; }
-          const int key0 = 128 * t;
-          const bool masked = key0 + 128 > C;
+          const int key0 = span.key0(t);
+          // (kWin: the last row's window begins at C + n - A.window at most)
+          const bool masked = key0 + 128 > C || (kWin && key0 + 128 > A.sink && key0 < (int64_t)C + A.n - A.window);
           if (!mbar_wait(&bars[kBarSFull + X], seen & 1)) { ok = false; break; }
           tc_fence_after();
           if constexpr (kPair) {
@@ -1026,145 +953,6 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
   }
 }
 
-// Joins the parts of the items that the line's cuts went through, in a fixed
-// order.  Latency bounds it where there is little to join, and else what the parts
-// hold (up to 40 MB, in the L2).  There are fewer cuts than parts, so each CTA looks
-// through all of them (those that are the first through their item stand for it)
-// and takes its share of the cut items' chunks, however many items there are; with
-// a grid over the items most CTAs find nothing to do: 152 requests of 1072 tokens
-// with 192 rows 167 us so, 211 us with it.
-//   kShare = 1: a thread takes 16 columns of a row, two parts in flight, a chunk is
-//     a warp's width of those;
-//   kShare = 8, where items have four parts or more each and about every chunk has an
-//     idle CTA: 8 columns, the eight warps of a CTA divide a chunk's parts, four in
-//     flight each (one request of 5000 tokens in 38 parts a head: 18 us, 26 us with
-//     kShare = 1; with more chunks than four an SM, 4 requests with 64 rows over 8000
-//     tokens, 36 us, 33 us with kShare = 1).
-constexpr int kJoinThreads = 256, kJoinPerSm = 3;
-constexpr int join_cols(int share) { return share > 1 ? 8 : 16; }
-
-template <int D, Rows kRows, int kShare>
-__global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) tree_join_kernel(const TreeArgs A) {
-  constexpr int kMost = kRows == kTwo ? kCtas : 2 * kCtas, kWarps = kJoinThreads / 32, kWords = (kMost + 31) / 32;
-  constexpr int kCols = join_cols(kShare), kAhead = kShare > 1 ? 4 : 2;
-  static_assert(kShare == 1 || kShare == kWarps, "a chunk per warp or CTA");
-  __shared__ unsigned found[kWords];
-  __shared__ float joined[kShare][kCols + 2][32];  // (kShare = 1: unused)
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int full = min(256, A.R), chunks = (full * (D / kCols) + 31) / 32;
-  const int G = *A.count;
-  for (int x = warp; x < kWords; x += kWarps) {
-    const int p = 32 * x + lane, n = A.cuts[min(p, kMost - 1)].n;
-    const unsigned f = __ballot_sync(0xFFFFFFFFu, p < G && n > 1);  // (behind G: of another call)
-    if (lane == 0) found[x] = f;
-  }
-  __syncthreads();
-  const int first = blockIdx.x + (kShare > 1 ? 0 : warp * gridDim.x), step = gridDim.x * (kWarps / kShare);
-  for (int u = first;; u += step) {
-    // the cut that stands for this chunk's item
-    int left = u / chunks, p = -1;
-    const int e = 32 * (u - left * chunks) + lane;
-#pragma unroll
-    for (int x = 0; x < kWords; ++x) {
-      const unsigned f = found[x];
-      const int here = __popc(f);
-      if (left >= 0 && left < here) {
-        const bool mine = (f >> lane & 1u) && __popc(f & ((1u << lane) - 1u)) == left;
-        p = 32 * x + __ffs(__ballot_sync(0xFFFFFFFFu, mine)) - 1;
-      }
-      left -= here;
-    }
-    if (p < 0) return;  // no more
-    const Cut it = A.cuts[p];
-    const int rb = it.item % A.RB, kvh = it.item / A.RB;
-    const int width = min(256, A.R - 256 * rb);
-    const int c = e / width, rw = e - c * width, rr = 256 * rb + rw;  // group of columns, row of the block
-    const bool there = e < width * (D / kCols);
-    const int T = A.tree_len ? A.tree_len[it.b] : A.n;
-    const float2* ml = A.part_ml + rw;
-    const float4* part = A.part + (int64_t)(kCols / 4 * c) * width + rw;
-    float m = -INFINITY, l = 0.f, o[kCols];
-#pragma unroll
-    for (int x = 0; x < kCols; ++x) o[x] = 0.f;
-    if (there)
-      for (int y0 = kShare > 1 ? warp : 0; y0 < it.n; y0 += kAhead * kShare) {
-        float2 state[kAhead];
-        float4 v[kAhead][kCols / 4];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          const int y = y0 + k * kShare;
-          state[k] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-          for (int x = 0; x < kCols / 4; ++x) v[k][x] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (y < it.n) {
-            const int64_t slot = y == 0 ? it.first : y <= it.inner ? it.base + it.step * y : it.tail;
-            state[k] = ml[slot * full];
-#pragma unroll
-            for (int x = 0; x < kCols / 4; ++x) v[k][x] = part[slot * (D / 4) * full + x * width];
-          }
-        }
-        float top = m;
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) top = fmaxf(top, state[k].x);
-        const float ref = top == -INFINITY ? 0.f : top, keep = ex2(m - ref);
-        m = top;
-        l *= keep;
-#pragma unroll
-        for (int x = 0; x < kCols; ++x) o[x] *= keep;
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          const float w = ex2(state[k].x - ref);
-          l += w * state[k].y;
-#pragma unroll
-          for (int x = 0; x < kCols / 4; ++x) {
-            o[4 * x] += w * v[k][x].x;
-            o[4 * x + 1] += w * v[k][x].y;
-            o[4 * x + 2] += w * v[k][x].z;
-            o[4 * x + 3] += w * v[k][x].w;
-          }
-        }
-      }
-    if (kShare > 1) {
-      joined[warp][0][lane] = m;
-      joined[warp][1][lane] = l;
-#pragma unroll
-      for (int x = 0; x < kCols; ++x) joined[warp][2 + x][lane] = o[x];
-      __syncthreads();
-      if (warp == 0) {
-#pragma unroll
-        for (int k = 1; k < kShare; ++k) m = fmaxf(m, joined[k][0][lane]);
-        const float ref = m == -INFINITY ? 0.f : m;
-        l = 0.f;
-#pragma unroll
-        for (int x = 0; x < kCols; ++x) o[x] = 0.f;
-#pragma unroll
-        for (int k = 0; k < kShare; ++k) {
-          const float w = ex2(joined[k][0][lane] - ref);
-          l += w * joined[k][1][lane];
-#pragma unroll
-          for (int x = 0; x < kCols; ++x) o[x] += w * joined[k][2 + x][lane];
-        }
-      }
-      __syncthreads();
-    }
-    if ((kShare > 1 && warp > 0) || !there || rr % A.n >= T) continue;  // (rows not drafted: parts hold anything)
-    const bool some = !(l == 0.f);
-    const float inv = some ? 1.f / l : 0.f;
-    const int64_t grow = (int64_t)(it.b * A.Hq + kvh * (A.Hq / A.Hkv)) * A.n + rr;
-    uint32_t w[kCols / 2];
-#pragma unroll
-    for (int x = 0; x < kCols / 2; ++x) w[x] = pack_bf16x2(o[2 * x] * inv, o[2 * x + 1] * inv);
-    __nv_bfloat16* dst = A.o + grow * D + kCols * c;
-#pragma unroll
-    for (int x = 0; x < kCols / 2; x += 4)
-      *reinterpret_cast<uint4*>(dst + 2 * x) = make_uint4(w[x], w[x + 1], w[x + 2], w[x + 3]);
-    if (c == 0 && A.lse) A.lse[grow] = some ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
-  }
-}
-
-size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
-
 struct TreeWs {
   size_t cuts, ml, part, total;
 };
@@ -1179,42 +967,15 @@ TreeWs tree_ws(const msa_shape& s) {
   return w;
 }
 
-bool aligned(const void* p, size_t a, bool required) {
-  if (!p) return !required;
-  return reinterpret_cast<uintptr_t>(p) % a == 0;
-}
-
-template <int D, Rows kRows>
+template <int D, Rows kRows, bool kWin>
 msa_status launch_tree(const TreeMaps& maps, const TreeArgs& a, bool join, cudaStream_t stream) {
-  auto kern = tree_attn_kernel<D, kRows>;
+  auto kern = tree_attn_kernel<D, kRows, kWin>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::kAlloc) != cudaSuccess)
     return MSA_ERR_CUDA;
   kern<<<kCtas, threads_of(kRows), Lay<D>::kAlloc, stream>>>(maps, a);
   note_launch();
   if (cudaGetLastError() != cudaSuccess) return MSA_ERR_CUDA;
-  if (!join) return MSA_OK;
-  cudaLaunchAttribute attr;
-  memset(&attr, 0, sizeof(attr));
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof(cfg));
-  const int full = a.R < 256 ? a.R : 256;
-  const int64_t items = (int64_t)a.B * a.Hkv * a.RB, most = items < a.max_parts ? items : a.max_parts - 1;  // cut ones
-  const int64_t split = items * ceil_div((int64_t)full * (D / join_cols(8)), 32);  // chunks, if their parts are divided
-  const bool share = 4 * items <= a.max_parts && split <= 4 * kCtas;
-  // (kShare = 1 has a chunk per warp, but few chunks go to all SMs first)
-  const int64_t ctas = share ? split : most * ceil_div((int64_t)full * (D / join_cols(1)), 32);
-  cfg.gridDim = dim3((unsigned)(ctas < kJoinPerSm * kCtas ? ctas : kJoinPerSm * kCtas));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if ((share ? cudaLaunchKernelEx(&cfg, tree_join_kernel<D, kRows, 8>, a)
-             : cudaLaunchKernelEx(&cfg, tree_join_kernel<D, kRows, 1>, a)) != cudaSuccess)
-    return MSA_ERR_CUDA;
-  note_launch();
-  return MSA_OK;
+  return join ? launch_join<D, kRows == kTwo ? kCtas : 2 * kCtas, 256>(a, stream) : MSA_OK;
 }
 
 }  // namespace
@@ -1237,10 +998,19 @@ extern "C" size_t msa_attn_tree_workspace(const msa_shape* shape) {
   return check_tree_shape(shape) == MSA_OK ? tree_ws(*shape).total : 0;
 }
 
-extern "C" msa_status msa_attn_tree(const msa_shape* shape, const void* q, const msa_kv_pages* pages,
-                                    const int32_t* page_table, int32_t max_pages, const int32_t* seq_len,
-                                    const int32_t* tree_len, const uint32_t* tree_mask, int64_t mask_stride, void* o,
-                                    float* lse, void* ws, size_t ws_bytes, void* stream) {
+namespace {
+
+template <bool kWin>
+msa_status launch_rows(const TreeMaps& maps, const TreeArgs& a, bool d128, bool join, cudaStream_t stm) {
+  if (a.R <= 64) return d128 ? launch_tree<128, kFew, kWin>(maps, a, join, stm) : launch_tree<64, kFew, kWin>(maps, a, join, stm);
+  if (a.R <= 128) return d128 ? launch_tree<128, kMany, kWin>(maps, a, join, stm) : launch_tree<64, kMany, kWin>(maps, a, join, stm);
+  return d128 ? launch_tree<128, kTwo, kWin>(maps, a, join, stm) : launch_tree<64, kTwo, kWin>(maps, a, join, stm);
+}
+
+msa_status attn_tree(const msa_shape* shape, const void* q, const msa_kv_pages* pages, const int32_t* page_table,
+                     int32_t max_pages, const int32_t* seq_len, const int32_t* tree_len, const uint32_t* tree_mask,
+                     int64_t mask_stride, const msa_tree_window* window, void* o, float* lse, void* ws,
+                     size_t ws_bytes, void* stream) {
   msa_status st = check_tree_shape(shape);
   if (st != MSA_OK) return st;
   if (!pages || max_pages < 1) return MSA_ERR_INVALID_ARG;
@@ -1255,6 +1025,7 @@ extern "C" msa_status msa_attn_tree(const msa_shape* shape, const void* q, const
   if (tree_mask && mask_stride != 0 && mask_stride < (int64_t)shape->n * words) return MSA_ERR_INVALID_ARG;
   if ((int64_t)pages->num_pages * pages->page_size * shape->Hkv + 256 >= ((int64_t)1 << 31)) return MSA_ERR_UNSUPPORTED;
   if ((int64_t)max_pages * pages->page_size >= ((int64_t)1 << 31) - 256) return MSA_ERR_UNSUPPORTED;
+  if (window && !window_ok(window, tree_mask)) return MSA_ERR_INVALID_ARG;
   const TreeWs w = tree_ws(*shape);
   if (ws_bytes < w.total) return MSA_ERR_WORKSPACE_TOO_SMALL;
   TreeArgs a;
@@ -1285,6 +1056,11 @@ extern "C" msa_status msa_attn_tree(const msa_shape* shape, const void* q, const
   a.part_ml = reinterpret_cast<float2*>(base + w.ml);
   a.part = reinterpret_cast<float4*>(base + w.part);
   a.scale_log2 = effective_scale(*shape) * 1.4426950408889634f;
+  if (window) {
+    a.sink = window->sink;
+    a.window = window->window;
+    a.depth = window->depth;
+  }
   a.err = device_error_word();
   if (!a.err) return MSA_ERR_CUDA;
   TreeMaps maps;
@@ -1297,8 +1073,25 @@ extern "C" msa_status msa_attn_tree(const msa_shape* shape, const void* q, const
   const bool join = (int64_t)max_pages * pages->page_size > 128;
   cudaStream_t stm = (cudaStream_t)stream;
   const bool d128 = shape->d_h == 128;
-  if (a.R <= 64) return d128 ? launch_tree<128, kFew>(maps, a, join, stm) : launch_tree<64, kFew>(maps, a, join, stm);
-  if (a.R <= 128)
-    return d128 ? launch_tree<128, kMany>(maps, a, join, stm) : launch_tree<64, kMany>(maps, a, join, stm);
-  return d128 ? launch_tree<128, kTwo>(maps, a, join, stm) : launch_tree<64, kTwo>(maps, a, join, stm);
+  return window ? launch_rows<true>(maps, a, d128, join, stm) : launch_rows<false>(maps, a, d128, join, stm);
+}
+
+}  // namespace
+
+extern "C" msa_status msa_attn_tree(const msa_shape* shape, const void* q, const msa_kv_pages* pages,
+                                    const int32_t* page_table, int32_t max_pages, const int32_t* seq_len,
+                                    const int32_t* tree_len, const uint32_t* tree_mask, int64_t mask_stride, void* o,
+                                    float* lse, void* ws, size_t ws_bytes, void* stream) {
+  return attn_tree(shape, q, pages, page_table, max_pages, seq_len, tree_len, tree_mask, mask_stride, nullptr, o, lse,
+                   ws, ws_bytes, stream);
+}
+
+extern "C" msa_status msa_attn_tree_window(const msa_shape* shape, const void* q, const msa_kv_pages* pages,
+                                           const int32_t* page_table, int32_t max_pages, const int32_t* seq_len,
+                                           const int32_t* tree_len, const uint32_t* tree_mask, int64_t mask_stride,
+                                           const msa_tree_window* window, void* o, float* lse, void* ws,
+                                           size_t ws_bytes, void* stream) {
+  if (!window) return MSA_ERR_INVALID_ARG;
+  return attn_tree(shape, q, pages, page_table, max_pages, seq_len, tree_len, tree_mask, mask_stride, window, o, lse,
+                   ws, ws_bytes, stream);
 }

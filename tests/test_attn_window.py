@@ -213,6 +213,22 @@ def test_many_requests_cut_anywhere(cuda_lib, n, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [1, 20, 40])
+def test_window_over_everything_is_the_whole(cuda_lib, n):
+    """A window or a sink that covers every key: the bits of attn_tree."""
+    rng = np.random.default_rng(n)
+    lens = [n, 5000, 333]
+    masks = np.stack([tree_bits(rng, n) for _ in lens])
+    for sink, window in ((0, 1 << 30), (6000, 1), (2600, 2600)):
+        c = Case(4, 1, n, 128, 32, lens, sink, window, 3, masks=masks)
+        o, lse, _, _ = c.run()
+        ref_l = torch.empty_like(lse)
+        ref = msa.attn_tree(c.q, c.k, c.v, c.table_dev, c.lens_dev, tree_mask=c.words, lse=ref_l)
+        assert cuda_lib.poll_device_status() == 0
+        assert torch.equal(o, ref) and torch.equal(lse, ref_l), (sink, window)
+
+
+@pytest.mark.gpu
 def test_a_window_agrees_with_the_ashape_prefill(cuda_lib):
     """Every row of a prompt through the cache sees what an A-shape head of the prefill sees."""
     n, Hq, Hkv, d, page, sink, window = 1000, 4, 2, 128, 16, 64, 200
