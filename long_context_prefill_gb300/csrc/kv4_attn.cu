@@ -1,181 +1,790 @@
-// Attention of drafted tokens over a paged cache held in 4 bits: the plain
-// kernel, one CTA per row, its warps taking keys in turn, joined at the end.
-#include <cuda_bf16.h>
-#include <math.h>
-#include <string.h>
-
-#include "internal.h"
+// Attention of drafted tokens over a paged cache held in 4 bits (decode,
+// speculative trees, windows), sm_103a.
+//
+// What it computes: msa_attn_tree's o_i = Σ_j e^{s_ij} v_j / Σ_j e^{s_ij} over
+// keys and values that are e2m1 codes times e4m3 scales of 16 channels.
+//
+// What bounds it: HBM, 144 bytes a key and KV head (d = 128) where the bf16 cache
+// has 512; at that rate an SM has about 790 cycles for a tile of 128 keys, so
+// nothing else may cost more.  Codes become fp16 (exact: 6 bits) for the tensor
+// core; the products are turned round so that the few query rows are the
+// narrow side:
+//   S^T [128 keys x N rows] = K Q^T   A = K in TMEM, where the threads that
+//                                     decode it put it: it passes shared memory
+//                                     once, as codes
+//   O^T [d x N] += V^T P^T            A = V in shared memory, [key][channel]
+// N = 16, 32 or 64 rows; a group of more rows is cut into blocks of 64 (with
+// bf16's layout, rows as the wide side, a tile of one row costs as much softmax
+// as one of 32: a warp's lanes are rows).  Softmax threads are keys: all lanes
+// work whatever the number of rows, and a weight goes to shared memory as it is
+// made.  q is fp16 too: a power of two per row (undone in the scores) brings its
+// largest value to 2^14, so that every bf16 down to 2^-30 of it is exact.  Weights are
+// rounded to fp16 at 2^7 times their share of the reference, a maximum that
+// rises when a score passes it by 2^8.
+//
+// Split: as tree.cu's (tree.cuh), one part of the line of tiles per CTA.
+//
+// A CTA (16 warps, one CTA per SM):
+//   warps 0-3    softmax (thread = key = TMEM lane), the segment's output
+//   warps 4-7    decode K: shared memory -> registers -> TMEM (two buffers)
+//   warps 8-11   decode V: shared memory -> registers -> shared memory (two
+//                buffers); rows that no query sees become zeros (their pages
+//                may hold anything)
+//   warp 12      loader: walks the part's segments, a bulk copy per page and
+//                head (K and V lie side by side) into a ring of tiles
+//   warp 13      issues the products
+//   warps 14-15  Q of the next segment to fp16
 #include "kv4.cuh"
-#include "ptx.cuh"
+#include "tree.cuh"
 
 namespace msa {
 
-msa_status check_tree_shape(const msa_shape* s);
-msa_status check_page_geometry(int32_t num_pages, int32_t page_size);
-float effective_scale(const msa_shape& s);
-
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kBlock = 64;  // rows of an item
+constexpr int kThreads = 512;
+constexpr int kDecodeK = 4, kDecodeV = 8, kLoader = 12, kIssuer = 13, kQWarp = 14;
+constexpr int kSegSlots = 3;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColK = 0, kColS = 128, kColO = 256;  // K and S: two buffers of 64 columns
+constexpr float kTop = 7.f, kRaise = 8.f;                // log2: weight of the reference, how far a score may pass it
+constexpr uint32_t kIdleNs = 64;
+constexpr uint64_t kDrainNs = MSA_WAIT_LIMIT_NS / 16;
 
-struct RowArgs {
-  int32_t B, Hq, Hkv, n, page_shift, max_pages, num_pages, words, sink, window;
-  const int32_t *table, *seq_len, *tree_len, *depth;
-  const uint32_t* mask;
-  int64_t mask_stride;
-  const __nv_bfloat16 *q, *k, *v;
-  const uint8_t* data;
-  float k_scale, v_scale;
-  __nv_bfloat16* o;
-  float* lse;
-  float scale_log2;
-  int* err;
+// [2]: buffers
+enum {
+  kBarKFull = 0,     // [2] K is in TMEM
+  kBarQK = 2,        // [2] scores are in TMEM, K is free
+  kBarSEmpty = 4,    // [2] scores are in registers
+  kBarVFull = 6,     // [2] V is in shared memory
+  kBarPFull = 8,     // [2] weights are in shared memory
+  kBarPV = 10,       // [2] the product is done: V and weights are free
+  kBarQFull = 12,    // [2] Q of the segment
+  kBarQEmpty = 14,   // [2] its products are done, its factors have been read
+  kBarGroup = 16,    // the softmax warps among themselves
+  kBarDrain = 17,    // after giving up: the products are done
+  kBarSegFull = 18,  // [kSegSlots]
+  kBarSegEmpty = kBarSegFull + kSegSlots,
+  kBarRing = kBarSegEmpty + kSegSlots  // full[kStages], empty[kStages]
 };
 
-template <int D, bool kKv4>
-__global__ void __launch_bounds__(32 * kWarps) attn_rows_kernel(const RowArgs A) {
-  constexpr int kPer = D / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = blockIdx.x;
-  const int b = (int)(row / ((int64_t)A.Hq * A.n)), hq = (int)(row / A.n % A.Hq), i = (int)(row % A.n);
-  const int kvh = hq / (A.Hq / A.Hkv);
-  const int L = A.seq_len[b], T = A.tree_len ? A.tree_len[b] : A.n;
-  if (T < 0 || T > A.n || L < T || L > ((int64_t)A.max_pages << A.page_shift)) {
-    if (threadIdx.x == 0) atomicCAS(A.err, 0, (int)kErrIndex);
+template <int D>
+struct Lay4 {
+  static constexpr int kUnit = D / 2 + D / 16;   // bytes of a token, K or V
+  static constexpr int kStage = 2 * 128 * kUnit;
+  static constexpr int kStages = 4 * (128 / D);
+  static constexpr int kTile = 128 * D * 2;      // a tile of V in fp16
+  static constexpr int kQTile = kBlock * D * 2;
+  static constexpr int kPTile = 128 * kBlock * 2;
+  static constexpr int kV = 0, kP = kV + 2 * kTile, kQ = kP + 2 * kPTile, kRaw = kQ + 2 * kQTile;
+  static constexpr int kSeg = kRaw + kStages * kStage;
+  static constexpr int kRows = (kSeg + kSegSlots * (int)sizeof(Seg) + 15) / 16 * 16;
+  // per row: factors [2], rows [2], window ends [2], reciprocals [2], references, factors of a raise, maxima [4], sums [4]
+  static constexpr int kWsum = kRows + 18 * kBlock * 4;
+  static constexpr int kBars = kWsum + 16 * 8;
+  static constexpr int kMisc = kBars + (kBarRing + 2 * kStages) * 8;  // [0] TMEM base, [2] abort, [3] tiles asked for, [4] flags [2]
+  static constexpr int kStart = kMisc + 32;
+  static constexpr int kAlloc = kStart + 16;
+  static_assert(kRows % 16 == 0 && kWsum % 8 == 0 && kStart % 8 == 0 && kRaw % 16 == 0, "alignment");
+  static_assert(kAlloc <= 227 * 1024 && kAlloc > 120 * 1024, "shared memory: one CTA per SM");
+};
+
+struct Kv4Args {
+  TreeArgs t;
+  const __nv_bfloat16* q;
+  const uint8_t* data;
+  float v_scale;
+};
+
+// Instruction descriptor, kind::f16 with fp16 inputs and an fp32 accumulator (fields as in idesc_bf16_f32).
+constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn_major, bool b_mn_major) {
+  return idesc_bf16_f32(M, N, a_mn_major, b_mn_major) & ~((1u << 7) | (1u << 10));
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ float warp_max(float x) {  // a NaN among others is left out
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  return m;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// A token's codes and scales of K or V: chunk c of 16 bytes at code + c * step.
+template <int D>
+struct Row4 {
+  uint4 code[D / 32];
+  uint32_t scale[D / 64];
+  __device__ __forceinline__ void load(const uint8_t* codes, int step, const uint8_t* scales) {
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) code[c] = *reinterpret_cast<const uint4*>(codes + c * step);
+    if constexpr (D == 128) {
+      const uint2 s = *reinterpret_cast<const uint2*>(scales);
+      scale[0] = s.x;
+      scale[1] = s.y;
+    } else {
+      scale[0] = *reinterpret_cast<const uint32_t*>(scales);
+    }
+  }
+  // 32 channels as 16 fp16 pairs
+  __device__ __forceinline__ void chunk(int c, uint32_t (&r)[16]) const {
+    const uint32_t two = f16x2_of_e4m3x2(scale[c >> 1] >> (16 * (c & 1)));
+    const uint32_t s0 = __byte_perm(two, 0, 0x1010), s1 = __byte_perm(two, 0, 0x3232);
+    f16_of_codes(code[c].x, s0, *reinterpret_cast<uint32_t(*)[4]>(r));
+    f16_of_codes(code[c].y, s0, *reinterpret_cast<uint32_t(*)[4]>(r + 4));
+    f16_of_codes(code[c].z, s1, *reinterpret_cast<uint32_t(*)[4]>(r + 8));
+    f16_of_codes(code[c].w, s1, *reinterpret_cast<uint32_t(*)[4]>(r + 12));
+  }
+};
+
+// Sums l[0 .. n) over the warp; each step halves what a lane keeps: 64 rows end as rows 2 lane and 2 lane + 1 in l[0] and
+// l[1], 32 as row `lane`, 16 as row lane / 2 in l[0].
+template <int n, int o>
+__device__ __forceinline__ void lane_sums(float* l, int lane) {
+  if constexpr (n > 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int x = 0; x < n / 2; ++x) {
+      const float give = up ? l[x] : l[x + n / 2], keep = up ? l[x + n / 2] : l[x];
+      l[x] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+    }
+  } else {
+    l[0] += __shfl_xor_sync(0xFFFFFFFFu, l[0], o);
+  }
+  if constexpr (o > 1) lane_sums<(n > 1 ? n / 2 : 1), o / 2>(l, lane);
+}
+
+template <int D, int kN, bool kWin>
+__global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_constant__ Kv4Args X) {
+  using Ly = Lay4<D>;
+  constexpr int kStages = Ly::kStages;
+  constexpr bool kWide = kN == 64;  // the softmax threads' scores and sums take more registers than an equal share
+  const TreeArgs& A = X.t;
+  extern __shared__ __align__(1024) uint8_t sm[];  // swizzled tiles start on 1 KB
+  if (smem_u32(sm) & 1023) {
+    if (threadIdx.x == 0) atomicCAS(A.err, 0, (int)kErrTimeout);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *A.count = 0;  // nothing to join
     return;
   }
-  if (i >= T) return;
-  const int C = L - T;
-  float q[kPer], o[kPer], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int x = 0; x < kPer; ++x) {
-    q[x] = __bfloat162float(A.q[row * D + kPer * lane + x]);
-    o[x] = 0.f;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Ly::kBars);
+  uint64_t* bFull = bars + kBarRing;
+  uint64_t* bEmpty = bFull + kStages;
+  Seg* segs = reinterpret_cast<Seg*>(sm + Ly::kSeg);
+  float* rowf = reinterpret_cast<float*>(sm + Ly::kRows);  // [2][kBlock]
+  volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(sm + Ly::kMisc);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (warp == 0) {
+    tmem_alloc(const_cast<uint32_t*>(&misc[0]), kTmemCols);
+    tmem_relinquish();
   }
-  const int e = A.depth ? min(max(A.depth[(int64_t)b * A.n + i], 0), A.n - 1) : i;
-  int64_t hole1 = A.window ? (int64_t)C + e - A.window + 1 : 0;  // keys sink .. hole1 - 1 are not seen
-  if (A.mask && hole1 > C) hole1 = C;
-  for (int j = warp; j < L; j += kWarps) {
-    if (j >= A.sink && j < hole1) continue;
-    if (j >= C) {
-      const int x = j - C;
-      if (A.mask ? !(A.mask[b * A.mask_stride + (int64_t)i * A.words + (x >> 5)] >> (x & 31) & 1u) : x > i) continue;
+  if (threadIdx.x == 32 * kIssuer) {
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&bars[kBarKFull + x], 4);
+      mbar_init(&bars[kBarQK + x], 1);
+      mbar_init(&bars[kBarSEmpty + x], 4);
+      mbar_init(&bars[kBarVFull + x], 4);
+      mbar_init(&bars[kBarPFull + x], 4);
+      mbar_init(&bars[kBarPV + x], 1);
+      mbar_init(&bars[kBarQFull + x], 2);
+      mbar_init(&bars[kBarQEmpty + x], 5);
     }
-    const int page = A.table[(int64_t)b * A.max_pages + (j >> A.page_shift)], r = j & ((1 << A.page_shift) - 1);
-    if ((unsigned)page >= (unsigned)A.num_pages) {
-      if (lane == 0) atomicCAS(A.err, 0, (int)kErrIndex);
-      continue;
+    mbar_init(&bars[kBarGroup], 4);
+    mbar_init(&bars[kBarDrain], 1);
+    for (int s = 0; s < kSegSlots; ++s) {
+      mbar_init(&bars[kBarSegFull + s], 1);
+      mbar_init(&bars[kBarSegEmpty + s], 11);  // softmax, V, issuer, Q
     }
-    float k[kPer], v[kPer];
-    if constexpr (kKv4) {
-      const int64_t unit = (int64_t)kv4_unit<D>() << A.page_shift;
-      const uint8_t* u = A.data + ((int64_t)page * A.Hkv + kvh) * 2 * unit;
-#pragma unroll
-      for (int x = 0; x < kPer; ++x) {
-        const int c = kPer * lane + x;
-        const int64_t at = ((((int64_t)(c >> 5) << A.page_shift) + r) << 4) + (c & 31) / 2;
-        const int64_t sc = ((int64_t)(D / 2) << A.page_shift) + r * (D / 16) + c / 16;
-        uint32_t y[4];
-        f16_of_codes(u[at] >> (4 * (c & 1)) & 15u, f16x2_of_e4m3x2(u[sc]), y);
-        k[x] = __half2float(__ushort_as_half((unsigned short)y[0])) * A.k_scale;
-        f16_of_codes(u[unit + at] >> (4 * (c & 1)) & 15u, f16x2_of_e4m3x2(u[unit + sc]), y);
-        v[x] = __half2float(__ushort_as_half((unsigned short)y[0])) * A.v_scale;
-      }
-    } else {
-      const int64_t at = ((((int64_t)page * A.Hkv + kvh) << A.page_shift) + r) * D + kPer * lane;
-#pragma unroll
-      for (int x = 0; x < kPer; ++x) {
-        k[x] = __bfloat162float(A.k[at + x]);
-        v[x] = __bfloat162float(A.v[at + x]);
-      }
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&bFull[s], 1);
+      mbar_init(&bEmpty[s], 8);
     }
-    float s = 0.f;
-#pragma unroll
-    for (int x = 0; x < kPer; ++x) s = fmaf(q[x], k[x], s);
-#pragma unroll
-    for (int w = 16; w; w >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, w);
-    s *= A.scale_log2;
-    const float top = fmaxf(m, s), keep = ex2(m - top), p = ex2(s - top);
-    m = top;
-    l = l * keep + p;
-#pragma unroll
-    for (int x = 0; x < kPer; ++x) o[x] = fmaf(p, v[x], o[x] * keep);
+    misc[2] = misc[3] = 0;
+    misc[4] = misc[5] = 0xFFFFFFFFu;
+    fence_mbar_init();
   }
-  __shared__ float part[kWarps][D], ml[kWarps][2];
+  // ---- this CTA's part of the line of tiles, and the request it starts in
+  const int items = A.Hkv * A.RB;  // items of a request
+  int64_t* wsum = reinterpret_cast<int64_t*>(sm + Ly::kWsum);
+  int64_t* start = reinterpret_cast<int64_t*>(sm + Ly::kStart);
+  int64_t W = 0;  // all tiles
+  {
+    const int per = (A.B + kThreads - 1) / kThreads;
+    const int b0 = min(A.B, (int)threadIdx.x * per), b1 = min(A.B, b0 + per);
+    auto tiles = [&](int b) -> int64_t {
+      int L, T;
+      bool bad;
+      const bool live = request(A, b, L, T, bad);
+      if (bad && blockIdx.x == 0) atomicCAS(A.err, 0, (int)kErrIndex);
+      return live ? (int64_t)items * span_of<kWin>(A, L, T).tiles : 0;
+    };
+    int64_t own = 0, mine = 0;
+    for (int b = b0; b < b1; ++b) mine += own = tiles(b);
+    int64_t inc = mine;
 #pragma unroll
-  for (int x = 0; x < kPer; ++x) part[warp][kPer * lane + x] = o[x];
-  if (lane == 0) ml[warp][0] = m, ml[warp][1] = l;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    int64_t base = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) base += wsum[w];
+      W += wsum[w];
+    }
+    int64_t at = base + inc - mine;
+    const int64_t lo = part_begin(W, kCtas, blockIdx.x);  // at or above W: no part
+    for (int b = b0; b < b1; ++b) {
+      const int64_t t = per == 1 ? own : tiles(b);
+      if (at <= lo && lo < at + t) { start[0] = b; start[1] = at; }
+      at += t;
+    }
+  }
+  const int G = parts(W, kCtas);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *A.count = G;
+  const int64_t begin = part_begin(W, kCtas, blockIdx.x);
+  const int cnt = (int)blockIdx.x < G ? (int)(part_begin(W, kCtas, blockIdx.x + 1) - begin) : 0;
+  tc_fence_before();
   __syncthreads();
-  if (threadIdx.x >= D) return;
-  float top = -INFINITY, sum = 0.f, out = 0.f;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w][0]);
-  const float ref = top == -INFINITY ? 0.f : top;
-  for (int w = 0; w < kWarps; ++w) {
-    const float f = ex2(ml[w][0] - ref);
-    sum += f * ml[w][1];
-    out += f * part[w][threadIdx.x];
+  tc_fence_after();
+  if (cnt == 0) {  // no part
+    if (warp == 0) tmem_dealloc(misc[0], kTmemCols);
+    return;
   }
-  A.o[row * D + threadIdx.x] = __float2bfloat16(sum == 0.f ? 0.f : out / sum);
-  if (threadIdx.x == 0 && A.lse) A.lse[row] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;
-}
+  const uint32_t tmem = misc[0];
 
-bool aligned(const void* p, size_t a, bool required) {
-  if (!p) return !required;
-  return reinterpret_cast<uintptr_t>(p) % a == 0;
-}
+  // Segment s of the part as its readers see it; false: no more, or gave up.
+  bool ok = true;
+  auto next_seg = [&](int s, Seg& g) -> bool {
+    const int slot = s % kSegSlots;
+    if (misc[2] || !mbar_wait(&bars[kBarSegFull + slot], (s / kSegSlots) & 1)) { ok = false; return false; }
+    g = segs[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[kBarSegEmpty + slot]);
+    return g.b >= 0;
+  };
+  // Tile j of the part is in buffer j & 1: use number j >> 1 of it.
+  auto used_before = [&](int bar, int j) {  // what frees the buffer for tile j has happened
+    return j < 2 || mbar_wait(&bars[bar + (j & 1)], ((j >> 1) - 1) & 1);
+  };
+  auto done = [&](int bar, int j) { return mbar_wait(&bars[bar + (j & 1)], (j >> 1) & 1); };
+  // where the token of row r of a tile lies in a stage: K's codes; V's unit is one page's tokens further
+  const int P = 1 << A.page_shift;
+  auto codes_at = [&](int r) { return (r >> A.page_shift) * 2 * P * Ly::kUnit + (r & (P - 1)) * 16; };
+  auto scales_at = [&](int r) { return (r >> A.page_shift) * 2 * P * Ly::kUnit + P * (D / 2) + (r & (P - 1)) * (D / 16); };
 
-msa_status rows(const msa_shape* shape, const void* q, const msa_kv_pages* pages, const msa_kv4_pages* kv4,
-                const int32_t* page_table, int32_t max_pages, const int32_t* seq_len, const int32_t* tree_len,
-                const uint32_t* tree_mask, int64_t mask_stride, const msa_tree_window* window, void* o, float* lse,
-                void* ws, size_t ws_bytes, size_t need, void* stream) {
-  const int32_t num_pages = pages ? pages->num_pages : kv4->num_pages, page_size = pages ? pages->page_size : kv4->page_size;
-  if (max_pages < 1) return MSA_ERR_INVALID_ARG;
-  if (!aligned(q, 16, true) || !aligned(o, 16, true) || !aligned(page_table, 4, true) || !aligned(seq_len, 4, true) ||
-      !aligned(tree_len, 4, false) || !aligned(tree_mask, 4, false) || !aligned(lse, 4, false) || !aligned(ws, 16, true))
-    return MSA_ERR_INVALID_ARG;
-  if (q == o) return MSA_ERR_INVALID_ARG;
-  const int32_t words = (shape->n + 31) / 32;
-  if (tree_mask && mask_stride != 0 && mask_stride < (int64_t)shape->n * words) return MSA_ERR_INVALID_ARG;
-  if (window && (window->sink < 0 || window->window < 1 || !aligned(window->depth, 4, false) || (window->depth && !tree_mask)))
-    return MSA_ERR_INVALID_ARG;
-  if ((int64_t)num_pages * page_size * shape->Hkv + 256 >= ((int64_t)1 << 31)) return MSA_ERR_UNSUPPORTED;
-  if ((int64_t)max_pages * page_size >= ((int64_t)1 << 31) - 256) return MSA_ERR_UNSUPPORTED;
-  if (ws_bytes < need) return MSA_ERR_WORKSPACE_TOO_SMALL;
-  RowArgs a;
-  memset(&a, 0, sizeof(a));
-  a.B = shape->B;
-  a.Hq = shape->Hq;
-  a.Hkv = shape->Hkv;
-  a.n = shape->n;
-  a.page_shift = __builtin_ctz((unsigned)page_size);
-  a.max_pages = max_pages;
-  a.num_pages = num_pages;
-  a.words = words;
-  if (window) a.sink = window->sink, a.window = window->window, a.depth = window->depth;
-  a.table = page_table;
-  a.seq_len = seq_len;
-  a.tree_len = tree_len;
-  a.mask = tree_mask;
-  a.mask_stride = mask_stride;
-  a.q = static_cast<const __nv_bfloat16*>(q);
-  if (pages) {
-    a.k = static_cast<const __nv_bfloat16*>(pages->k);
-    a.v = static_cast<const __nv_bfloat16*>(pages->v);
+  if (warp >= 4) {
+    if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    if (warp < kDecodeV) {
+      // ------------------------------------------------------------ K to TMEM
+      const int r = 32 * (warp - kDecodeK) + lane;
+      const uint32_t to = tmem + ((uint32_t)(32 * (warp - kDecodeK)) << 16) + kColK;
+      for (int j = 0; j < cnt && ok; ++j) {
+        const int st = j % kStages;
+        if (misc[2] || !mbar_wait(&bFull[st], (j / kStages) & 1)) { ok = false; break; }
+        const uint8_t* raw = sm + Ly::kRaw + st * Ly::kStage;
+        Row4<D> row;
+        row.load(raw + codes_at(r), 16 * P, raw + scales_at(r));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bEmpty[st]);
+        if (!used_before(kBarQK, j)) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t w[16];
+          row.chunk(c, w);
+          tmem_st16(to + 64 * (j & 1) + 16 * c, w);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kBarKFull + (j & 1)]);
+      }
+    } else if (warp < kLoader) {
+      // ------------------------------------------------------------ V to shared memory
+      const int r = 32 * (warp - kDecodeV) + lane;
+      int j = 0;
+      Seg g;
+      for (int s = 0; j < cnt && next_seg(s, g); ++s) {
+        const Span span = span_of<kWin>(A, g.L, g.T);
+        for (int t = g.t0; t < g.t1 && ok; ++t, ++j) {
+          const int st = j % kStages;
+          if (misc[2] || !mbar_wait(&bFull[st], (j / kStages) & 1)) { ok = false; break; }
+          const uint8_t* raw = sm + Ly::kRaw + st * Ly::kStage + P * Ly::kUnit;
+          Row4<D> row;
+          row.load(raw + codes_at(r), 16 * P, raw + scales_at(r));
+          const int key = span.key0(t) + r;
+          if (key >= g.L || (kWin && key >= span.hole && key < span.lo)) {  // seen by no row: zeros
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) row.code[c] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) row.scale[c] = 0;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bEmpty[st]);
+          if (!used_before(kBarPV, j)) { ok = false; break; }
+          uint8_t* v = sm + Ly::kV + (j & 1) * Ly::kTile;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t w[16];
+            row.chunk(c, w);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              *reinterpret_cast<uint4*>(v + (c >> 1) * 16384 + sw128_offset(r, 4 * (c & 1) + x)) =
+                  make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[kBarVFull + (j & 1)]);
+        }
+        if (!ok) break;
+      }
+    } else if (warp == kLoader) {
+      // ------------------------------------------------------------ loader
+      const uint64_t policy = A.RB == 1 ? policy_evict_first() : policy_evict_last();
+      const int pshift = 7 - A.page_shift, pp = 1 << pshift;  // pages of a tile
+      const uint32_t page_bytes = 2 * P * Ly::kUnit;
+      int64_t at = start[1], pos = begin;  // first tile of request b, of the next segment
+      const int64_t hi = begin + cnt;
+      int b = (int)start[0], s = 0, t = 0;
+      Seg g = {};
+      Span span = {};
+      int base = 0, ids = 0, ahead = 0;  // lane x holds the page of entry base + x, and of base + 32 + x (along the line)
+      auto publish = [&](const Seg& g) -> bool {
+        const int slot = s % kSegSlots;
+        if (misc[2] || !mbar_wait_idle(&bars[kBarSegEmpty + slot], ((s / kSegSlots) & 1) ^ 1, kIdleNs)) return false;
+        if (lane == 0) {
+          segs[slot] = g;
+          mbar_arrive(&bars[kBarSegFull + slot]);
+        }
+        return true;
+      };
+      // -1: not read
+      auto entry = [&](int p) {
+        p = (span.tile(p >> pshift) << pshift) + (p & (pp - 1));
+        if (p >= (g.L + P - 1) >> A.page_shift || (kWin && span.gone(p, A.page_shift))) return -1;
+        const int page = A.table[(int64_t)g.b * A.max_pages + p];
+        if ((unsigned)page < (unsigned)A.num_pages) return page;
+        atomicCAS(A.err, 0, (int)kErrIndex);  // not followed: an existing page stands in, the call has failed
+        return 0;
+      };
+      auto open = [&]() -> bool {
+        bool bad;
+        int64_t tiles = 0;
+        for (; b < A.B; ++b) {
+          const bool live = request(A, b, g.L, g.T, bad);
+          span = span_of<kWin>(A, g.L, g.T);
+          tiles = live ? (int64_t)items * span.tiles : 0;
+          if (pos < at + tiles) break;
+          at += tiles;
+        }
+        if (b >= A.B) return false;
+        g.b = b;
+        g.tiles = span.tiles;
+        const int item = (int)quotient(pos - at, g.tiles);
+        g.kvh = item / A.RB;
+        g.rb = item - g.kvh * A.RB;
+        g.t0 = (int)(pos - at - (int64_t)item * g.tiles);
+        const int64_t left = hi - pos;
+        g.t1 = left < g.tiles - g.t0 ? g.t0 + (int)left : g.tiles;
+        g.r0 = g.t0;
+        g.r1 = g.t1;
+        pos += g.t1 - g.t0;
+        t = g.t0;
+        base = g.t0 << pshift;
+        if (!publish(g)) return false;
+        ++s;
+        ids = entry(base + lane);
+        ahead = entry(base + 32 + lane);
+        return true;
+      };
+      for (int j = 0; j < cnt && ok; ++j) {
+        if ((s == 0 || t == g.t1) && !open()) { ok = false; break; }
+        int off = (t << pshift) - base;
+        if (off >= 32) {
+          base += 32;
+          off -= 32;
+          ids = ahead;
+          ahead = entry(base + 32 + lane);
+        }
+        const int page = __shfl_sync(0xFFFFFFFFu, ids, (off + lane) & 31);
+        const bool mine = lane < pp && page >= 0;
+        const uint32_t copies = __popc(__ballot_sync(0xFFFFFFFFu, mine));
+        const int st = j % kStages;
+        if (misc[2] || !mbar_wait_idle(&bEmpty[st], ((j / kStages) & 1) ^ 1, kIdleNs)) { ok = false; break; }
+        if (lane == 0) mbar_arrive_expect_tx(&bFull[st], copies * page_bytes);
+        __syncwarp();
+        if (mine)
+          bulk_load(sm + Ly::kRaw + st * Ly::kStage + lane * page_bytes,
+                    X.data + ((int64_t)page * A.Hkv + g.kvh) * page_bytes, page_bytes, &bFull[st], policy);
+        __syncwarp();
+        if (lane == 0) misc[3] = j + 1;
+        ++t;
+      }
+      Seg end;
+      end.b = -1;
+      if (ok) ok = publish(end);
+    } else if (warp == kIssuer) {
+      // ------------------------------------------------------------ products
+      constexpr uint32_t id_qk = idesc_f16_f32(128, kN, false, false);
+      constexpr uint32_t id_pv = idesc_f16_f32(128, kN, true, true);  // (d = 64: rows 64 .. of O^T hold anything)
+      const uint64_t dq = sdesc_sw128(smem_u32(sm + Ly::kQ), 16, 1024);
+      const uint64_t dv = sdesc_sw128(smem_u32(sm + Ly::kV), 16384, 1024);
+      const uint64_t dp = sdesc_sw128(smem_u32(sm + Ly::kP), 16384, 1024);
+      auto issue_pv = [&](int j, bool first) -> bool {
+        if (!done(kBarPFull, j) || !done(kBarVFull, j)) return false;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t v = dv + (uint64_t)((j & 1) * (Ly::kTile >> 4)), p = dp + (uint64_t)((j & 1) * (Ly::kPTile >> 4));
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_bf16_ss(tmem + kColO, v + (uint64_t)(kk * 128), p + (uint64_t)(kk * 128), id_pv, (!first || kk > 0) ? 1u : 0u);
+          mma_commit(&bars[kBarPV + (j & 1)]);
+        }
+        __syncwarp();
+        return true;
+      };
+      int j = 0;
+      bool first = true;  // tile j - 1 is its segment's first
+      Seg g;
+      for (int s = 0; j < cnt && next_seg(s, g); ++s) {
+        if (!mbar_wait(&bars[kBarQFull + (s & 1)], (s >> 1) & 1)) { ok = false; break; }
+        for (int t = g.t0; t < g.t1; ++t, ++j) {
+          if (misc[2] || !done(kBarKFull, j) || !used_before(kBarSEmpty, j)) { ok = false; break; }
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t q = dq + (uint64_t)((s & 1) * (Ly::kQTile >> 4));
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_bf16_ts(tmem + kColS + 64 * (j & 1), tmem + kColK + 64 * (j & 1) + 8 * kk,
+                          q + (uint64_t)((kk >> 2) * (kBlock * 8) + (kk & 3) * 2), id_qk, kk > 0 ? 1u : 0u);
+            mma_commit(&bars[kBarQK + (j & 1)]);
+            if (t + 1 == g.t1) mma_commit(&bars[kBarQEmpty + (s & 1)]);
+          }
+          __syncwarp();
+          if (j > 0 && !issue_pv(j - 1, first)) { ok = false; break; }
+          first = t == g.t0;
+        }
+        if (!ok) break;
+      }
+      if (ok && !issue_pv(cnt - 1, first)) ok = false;
+    } else {
+      // ------------------------------------------------------------ Q to fp16
+      constexpr int kPer = D / 32;
+      if (warp == kQWarp && lane == 0) note_cut<false, kCtas, kWin>(A, W, blockIdx.x, (int)start[0], start[1]);
+      __syncwarp();
+      Seg g;
+      for (int s = 0; next_seg(s, g); ++s) {
+        if (!mbar_wait_idle(&bars[kBarQEmpty + (s & 1)], ((s >> 1) & 1) ^ 1, kIdleNs)) { ok = false; break; }
+        uint8_t* to = sm + Ly::kQ + (s & 1) * Ly::kQTile;
+        float* f = rowf + (s & 1) * kBlock;
+        const int64_t q0 = (int64_t)(g.b * A.Hq + g.kvh * (A.Hq / A.Hkv)) * A.n + kBlock * g.rb;
+        const int ch = kPer * lane;
+#pragma unroll 4
+        for (int r = warp - kQWarp; r < kN; r += 2) {
+          const int rr = kBlock * g.rb + r;
+          if (rr >= A.R || rr % A.n >= g.T) {  // no row: whatever its column holds stays there
+            if (lane == 0) f[r] = 0.f;
+            continue;
+          }
+          const uint32_t* src = reinterpret_cast<const uint32_t*>(X.q + (q0 + r) * D + ch);
+          uint32_t u[kPer / 2];
+#pragma unroll
+          for (int x = 0; x < kPer / 2; ++x) u[x] = __ldg(src + x);
+          uint32_t top = 0;
+#pragma unroll
+          for (int x = 0; x < kPer / 2; ++x) top = max(top, max(u[x] & 0x7FFFu, u[x] >> 16 & 0x7FFFu));
+          top = max(1u, __reduce_max_sync(0xFFFFFFFFu, top) >> 7);  // exponent of the largest value
+          const int up = 141 - (int)top, a = up / 2, c = up - a;      // to 2^14; two factors, since 2^141 is no fp32 number
+          const float fa = __uint_as_float((uint32_t)(127 + a) << 23), fc = __uint_as_float((uint32_t)(127 + c) << 23);
+          uint32_t h[kPer / 2];
+#pragma unroll
+          for (int x = 0; x < kPer / 2; ++x)
+            h[x] = pack_f16x2(__uint_as_float(u[x] << 16) * fa * fc, __uint_as_float(u[x] & 0xFFFF0000u) * fa * fc);
+          uint8_t* dst = to + (ch >> 6) * (kBlock * 128) + sw128_offset(r, (ch & 63) >> 3) + (ch & 7) * 2;
+#pragma unroll
+          for (int x = 0; x < kPer / 2; ++x) reinterpret_cast<uint32_t*>(dst)[x] = h[x];
+          if (lane == 0)
+            f[r] = A.scale_log2 * __uint_as_float((uint32_t)(127 - a) << 23) * __uint_as_float((uint32_t)(127 - c) << 23);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kBarQFull + (s & 1)]);
+      }
+    }
   } else {
-    a.data = static_cast<const uint8_t*>(kv4->data);
-    a.k_scale = kv4_scale(kv4->k_scale);
-    a.v_scale = kv4_scale(kv4->v_scale);
+    if (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ------------------------------------------------------------ softmax: thread = key
+    const int tid = threadIdx.x;
+    const uint32_t lane_base = (uint32_t)(32 * warp) << 16;
+    int* rowi = reinterpret_cast<int*>(rowf + 2 * kBlock);  // [2][kBlock] drafted token of the row, -1: no row
+    int* rowend = rowi + 2 * kBlock;                        // [2][kBlock] kWin: end of the keys behind its window
+    float* inv = reinterpret_cast<float*>(rowend + 2 * kBlock);  // [2][kBlock] 1 / row sum, V's scale in it
+    float* nref = inv + 2 * kBlock;                         // kTop - reference
+    float* alpha = nref + kBlock;                           // factors of a raise
+    float* wmax = alpha + kBlock;                           // [4][kBlock]
+    float* wl = wmax + 4 * kBlock;                          // [4][kBlock]
+    int syncs = 0;
+    auto group_sync = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kBarGroup]);
+      return mbar_wait(&bars[kBarGroup], syncs++ & 1);
+    };
+    int j = 0;
+    Seg g;
+    for (int s = 0; j < cnt && next_seg(s, g); ++s) {
+      const Span span = span_of<kWin>(A, g.L, g.T);
+      const int C = g.L - g.T, set = (s & 1) * kBlock;
+      float m_used = -INFINITY;  // of row `tid`
+      if (tid < kN) {
+        const int rr = kBlock * g.rb + tid, i = rr % A.n;
+        rowi[set + tid] = rr < A.R && i < g.T ? i : -1;
+        if (kWin) rowend[set + tid] = behind(A, g.b, i, C);
+      }
+      float l[kN];
+#pragma unroll
+      for (int r = 0; r < kN; ++r) l[r] = 0.f;
+      if (!mbar_wait(&bars[kBarQFull + (s & 1)], (s >> 1) & 1) || !group_sync()) { ok = false; break; }
+      const float* f = rowf + set;
+      for (int t = g.t0; t < g.t1; ++t, ++j) {
+        const int key0 = span.key0(t), key = key0 + tid;
+        const bool masked = key0 + 128 > C || (kWin && key0 + 128 > A.sink && key0 < (int64_t)C + A.n - A.window);
+        if (misc[2] || !done(kBarQK, j)) { ok = false; break; }
+        tc_fence_after();
+        float sv[kN];
+#pragma unroll
+        for (int c = 0; c < kN; c += 16)
+          tmem_ld16(tmem + lane_base + kColS + 64 * (j & 1) + c, reinterpret_cast<uint32_t*>(sv) + c);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kBarSEmpty + (j & 1)]);
+        uint32_t see[(kN + 31) / 32];  // rows that see this key
+#pragma unroll
+        for (int x = 0; x < (kN + 31) / 32; ++x) see[x] = 0xFFFFFFFFu;
+        if (masked) {
+          const int rel = key - C;
+#pragma unroll 1
+          for (int r = 0; r < kN; ++r) {
+            const int i = rowi[set + r];
+            bool in = key < g.L;
+            if (in && rel >= 0)
+              in = A.mask ? i >= 0 && (__ldg(A.mask + g.b * A.mask_stride + (int64_t)i * A.words + (rel >> 5)) >> (rel & 31) & 1u)
+                          : rel <= i;
+            if (kWin && key >= A.sink && key < rowend[set + r]) in = false;
+            if (!in) {
+              if (kN > 32 && r >= 32) see[(kN - 1) / 32] &= ~(1u << (r & 31));
+              else see[0] &= ~(1u << r);
+            }
+          }
+        }
+        // scores in log2 units above the reference, and whether one is too far above
+        bool far = t == g.t0;
+        if (!far) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int r = 0; r < kN; r += 4) {
+            const float4 a = *reinterpret_cast<const float4*>(f + r), n4 = *reinterpret_cast<const float4*>(nref + r);
+            float y[4] = {fmaf(sv[r], a.x, n4.x), fmaf(sv[r + 1], a.y, n4.y), fmaf(sv[r + 2], a.z, n4.z),
+                          fmaf(sv[r + 3], a.w, n4.w)};
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (!(see[(r + x) >> 5] >> ((r + x) & 31) & 1u)) y[x] = -INFINITY;
+            top = fmaxf(max3f(y[0], y[1], y[2]), fmaxf(y[3], top));
+          }
+          far = __any_sync(0xFFFFFFFFu, top > kTop + kRaise);
+          if (far && lane == 0) misc[4 + (syncs & 1)] = syncs;
+          const int at = syncs;
+          if (!group_sync()) { ok = false; break; }
+          far = misc[4 + (at & 1)] == (uint32_t)at;
+        }
+        if (far) {
+          // the rows' maxima over the tile, new references, and what was summed comes to them
+          float mine[(kN + 31) / 32] = {};
+#pragma unroll
+          for (int r = 0; r < kN; ++r) {
+            const float m = warp_max((see[r >> 5] >> (r & 31) & 1u) ? sv[r] * f[r] : -INFINITY);
+            if (lane == (r & 31)) mine[r >> 5] = m;
+          }
+#pragma unroll
+          for (int x = 0; x < (kN + 31) / 32; ++x)
+            if (32 * x + lane < kN) wmax[warp * kBlock + 32 * x + lane] = mine[x];
+          if (!group_sync()) { ok = false; break; }
+          if (tid < kN) {
+            float m = m_used;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) m = fmaxf(m, wmax[w * kBlock + tid]);
+            alpha[tid] = m == m_used ? 1.f : ex2(m_used - m);
+            nref[tid] = kTop - m;  // +inf while the row has met no key: its first one is too far above
+            m_used = m;
+          }
+          if (!group_sync()) { ok = false; break; }
+          if (t > g.t0) {
+#pragma unroll
+            for (int r = 0; r < kN; ++r) l[r] *= alpha[r];
+            if (!done(kBarPV, j - 1)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < kN; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(tmem + lane_base + kColO + c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha[c + x]);
+              tmem_st16(tmem + lane_base + kColO + c, o);
+            }
+            tmem_st_wait();
+          }
+        }
+        if (!used_before(kBarPV, j)) { ok = false; break; }
+        uint8_t* p = sm + Ly::kP + (j & 1) * Ly::kPTile;
+#pragma unroll
+        for (int r = 0; r < kN; r += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int x = 0; x < 8; x += 4) {
+            const float4 a = *reinterpret_cast<const float4*>(f + r + x), n4 = *reinterpret_cast<const float4*>(nref + r + x);
+            float y[4] = {fmaf(sv[r + x], a.x, n4.x), fmaf(sv[r + x + 1], a.y, n4.y), fmaf(sv[r + x + 2], a.z, n4.z),
+                          fmaf(sv[r + x + 3], a.w, n4.w)};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (!(see[(r + x + k) >> 5] >> ((r + x + k) & 31) & 1u)) y[k] = -INFINITY;
+              y[k] = ex2(y[k]);
+              l[r + x + k] += y[k];
+            }
+            w[x / 2] = pack_f16x2(y[0], y[1]);
+            w[x / 2 + 1] = pack_f16x2(y[2], y[3]);
+          }
+          *reinterpret_cast<uint4*>(p + sw128_offset(tid, r >> 3)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kBarPFull + (j & 1)]);
+      }
+      if (!ok) break;
+
+      // ---- the segment's end: row sums over lanes and warps, then O^T (thread = channel)
+      if (lane == 0) mbar_arrive(&bars[kBarQEmpty + (s & 1)]);  // (behind the last barrier of the group: all have read f)
+      lane_sums<kN, 16>(l, lane);
+      if constexpr (kN == 64) *reinterpret_cast<float2*>(wl + warp * kBlock + 2 * lane) = make_float2(l[0], l[1]);
+      else if (kN == 32 || !(lane & 1)) wl[warp * kBlock + (kN == 32 ? lane : lane >> 1)] = l[0];
+      if (!group_sync()) { ok = false; break; }
+      const bool whole = g.r0 == 0 && g.r1 == g.tiles;
+      const int full = min(kBlock, A.R), width = min(kBlock, A.R - kBlock * g.rb);
+      const int64_t slot = 2 * (int64_t)blockIdx.x + (g.r0 > 0 ? 0 : 1);
+      const int64_t grow = (int64_t)(g.b * A.Hq + g.kvh * (A.Hq / A.Hkv)) * A.n + kBlock * g.rb;
+      if (tid < kN) {
+        const float sum = (wl[tid] + wl[kBlock + tid]) + (wl[2 * kBlock + tid] + wl[3 * kBlock + tid]);
+        const bool some = !(sum == 0.f);
+        inv[set + tid] = whole ? (some ? X.v_scale / sum : 0.f) : X.v_scale;
+        if (rowi[set + tid] >= 0) {
+          // (sums are 2^kTop times those of the reference)
+          if (!whole) A.part_ml[slot * full + tid] = make_float2(m_used - kTop, sum);
+          else if (A.lse) A.lse[grow + tid] = some ? (m_used - kTop + __log2f(sum)) * 0.69314718055994531f : -INFINITY;
+        }
+      }
+      if (!group_sync() || !done(kBarPV, j - 1)) { ok = false; break; }
+      tc_fence_after();
+      if (D == 128 || warp < 2) {
+#pragma unroll 1
+        for (int c = 0; c < kN && c < width; c += 16) {
+          uint32_t o[16];
+          tmem_ld16(tmem + lane_base + kColO + c, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            const int r = c + x;
+            if (rowi[set + r] < 0) continue;
+            const float y = __uint_as_float(o[x]) * inv[set + r];
+            if (whole) A.o[(grow + r) * D + tid] = __float2bfloat16(y);
+            else reinterpret_cast<float*>(A.part + slot * (D / 4) * full + (int64_t)(tid >> 2) * width + r)[tid & 3] = y;
+          }
+        }
+      }
+      tc_fence_before();
+    }
   }
-  a.o = static_cast<__nv_bfloat16*>(o);
-  a.lse = lse;
-  a.scale_log2 = effective_scale(*shape) * 1.4426950408889634f;
-  a.err = device_error_word();
-  if (!a.err) return MSA_ERR_CUDA;
-  auto kern = pages ? (shape->d_h == 128 ? attn_rows_kernel<128, false> : attn_rows_kernel<64, false>)
-                    : (shape->d_h == 128 ? attn_rows_kernel<128, true> : attn_rows_kernel<64, true>);
-  kern<<<(unsigned)((int64_t)shape->B * shape->Hq * shape->n), 32 * kWarps, 0, (cudaStream_t)stream>>>(a);
+  if (!ok) {
+    misc[2] = 1;
+    atomicCAS(A.err, 0, (int)kErrTimeout);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (misc[2]) {
+    // A role gave up: copies and products that nobody waited for end before the CTA's shared memory and TMEM go.
+    if (warp == kIssuer) {
+      if (lane == 0) mma_commit(&bars[kBarDrain]);
+      mbar_wait(&bars[kBarDrain], 0, kDrainNs);
+    } else if (warp == kLoader) {
+      const int asked = (int)misc[3];
+      for (int x = max(0, asked - kStages); x < asked; ++x) mbar_wait(&bFull[x % kStages], (x / kStages) & 1, kDrainNs);
+    }
+    __syncthreads();
+  }
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+struct Ws4 {
+  size_t cuts, ml, part, total;
+};
+Ws4 kv4_ws(const msa_shape& s) {
+  const int64_t R = (int64_t)(s.Hq / s.Hkv) * s.n, rows = 2 * kCtas * (R < kBlock ? R : kBlock);
+  Ws4 w;
+  w.cuts = 16;  // behind their count
+  w.ml = align256(w.cuts + kCtas * sizeof(Cut));
+  w.part = align256(w.ml + (size_t)rows * 8);
+  w.total = align256(w.part + (size_t)rows * s.d_h * 4);
+  return w;
+}
+
+template <int D, int kN, bool kWin>
+msa_status launch(const Kv4Args& a, bool join, cudaStream_t stream) {
+  auto kern = kv4_attn_kernel<D, kN, kWin>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay4<D>::kAlloc) != cudaSuccess)
+    return MSA_ERR_CUDA;
+  kern<<<kCtas, kThreads, Lay4<D>::kAlloc, stream>>>(a);
   note_launch();
-  return cudaGetLastError() == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
+  if (cudaGetLastError() != cudaSuccess) return MSA_ERR_CUDA;
+  return join ? launch_join<D, kCtas, kBlock>(a.t, stream) : MSA_OK;
+}
+
+template <int D, bool kWin>
+msa_status launch_rows(const Kv4Args& a, bool join, cudaStream_t stream) {
+  if (a.t.R <= 16) return launch<D, 16, kWin>(a, join, stream);
+  if (a.t.R <= 32) return launch<D, 32, kWin>(a, join, stream);
+  return launch<D, 64, kWin>(a, join, stream);
 }
 
 }  // namespace
@@ -184,7 +793,9 @@ msa_status rows(const msa_shape* shape, const void* q, const msa_kv_pages* pages
 
 using namespace msa;
 
-extern "C" size_t msa_attn_tree_kv4_workspace(const msa_shape* shape) { return msa_attn_tree_workspace(shape); }
+extern "C" size_t msa_attn_tree_kv4_workspace(const msa_shape* shape) {
+  return check_tree_shape(shape) == MSA_OK ? kv4_ws(*shape).total : 0;
+}
 
 extern "C" msa_status msa_attn_tree_kv4(const msa_shape* shape, const void* q, const msa_kv4_pages* pages,
                                         const int32_t* page_table, int32_t max_pages, const int32_t* seq_len,
@@ -195,6 +806,58 @@ extern "C" msa_status msa_attn_tree_kv4(const msa_shape* shape, const void* q, c
   if (st != MSA_OK) return st;
   st = check_kv4_pages(pages);
   if (st != MSA_OK) return st;
-  return rows(shape, q, nullptr, pages, page_table, max_pages, seq_len, tree_len, tree_mask, mask_stride, window, o, lse,
-              ws, ws_bytes, msa_attn_tree_kv4_workspace(shape), stream);
+  if (max_pages < 1) return MSA_ERR_INVALID_ARG;
+  if (!aligned(q, 16, true) || !aligned(o, 16, true) || !aligned(page_table, 4, true) || !aligned(seq_len, 4, true) ||
+      !aligned(tree_len, 4, false) || !aligned(tree_mask, 4, false) || !aligned(lse, 4, false) || !aligned(ws, 16, true))
+    return MSA_ERR_INVALID_ARG;
+  if (q == o) return MSA_ERR_INVALID_ARG;
+  const int32_t words = (shape->n + 31) / 32;
+  if (tree_mask && mask_stride != 0 && mask_stride < (int64_t)shape->n * words) return MSA_ERR_INVALID_ARG;
+  if (window && !window_ok(window, tree_mask)) return MSA_ERR_INVALID_ARG;
+  if ((int64_t)max_pages * pages->page_size >= ((int64_t)1 << 31) - 256) return MSA_ERR_UNSUPPORTED;
+  const Ws4 w = kv4_ws(*shape);
+  if (ws_bytes < w.total) return MSA_ERR_WORKSPACE_TOO_SMALL;
+  Kv4Args a;
+  memset(&a, 0, sizeof(a));
+  TreeArgs& t = a.t;
+  t.B = shape->B;
+  t.Hq = shape->Hq;
+  t.Hkv = shape->Hkv;
+  t.n = shape->n;
+  t.R = shape->Hq / shape->Hkv * shape->n;
+  t.RB = (t.R + kBlock - 1) / kBlock;
+  if ((int64_t)t.B * t.Hkv * t.RB >= ((int64_t)1 << 31)) return MSA_ERR_UNSUPPORTED;
+  t.max_parts = kCtas;
+  t.page_shift = __builtin_ctz((unsigned)pages->page_size);
+  t.max_pages = max_pages;
+  t.num_pages = pages->num_pages;
+  t.words = words;
+  t.table = page_table;
+  t.seq_len = seq_len;
+  t.tree_len = tree_len;
+  t.mask = tree_mask;
+  t.mask_stride = mask_stride;
+  t.o = static_cast<__nv_bfloat16*>(o);
+  t.lse = lse;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  t.count = reinterpret_cast<int32_t*>(base);
+  t.cuts = reinterpret_cast<Cut*>(base + w.cuts);
+  t.part_ml = reinterpret_cast<float2*>(base + w.ml);
+  t.part = reinterpret_cast<float4*>(base + w.part);
+  t.scale_log2 = effective_scale(*shape) * 1.4426950408889634f * kv4_scale(pages->k_scale);
+  if (window) {
+    t.sink = window->sink;
+    t.window = window->window;
+    t.depth = window->depth;
+  }
+  t.err = device_error_word();
+  if (!t.err) return MSA_ERR_CUDA;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.data = static_cast<const uint8_t*>(pages->data);
+  a.v_scale = kv4_scale(pages->v_scale);
+  // a table of at most 128 keys holds no item of two tiles: none is cut
+  const bool join = (int64_t)max_pages * pages->page_size > 128;
+  cudaStream_t stm = (cudaStream_t)stream;
+  if (shape->d_h == 128) return window ? launch_rows<128, true>(a, join, stm) : launch_rows<128, false>(a, join, stm);
+  return window ? launch_rows<64, true>(a, join, stm) : launch_rows<64, false>(a, join, stm);
 }
