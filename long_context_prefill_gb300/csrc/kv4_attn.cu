@@ -458,10 +458,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
       const uint64_t dq = sdesc_sw128(smem_u32(sm + Ly::kQ), 16, 1024);
       const uint64_t dv = sdesc_sw128(smem_u32(sm + Ly::kV), 16384, 1024);
       const uint64_t dp = sdesc_sw128(smem_u32(sm + Ly::kP), 16384, 1024);
+      const bool leader = elect_one();
       auto issue_pv = [&](int j, bool first) -> bool {
         if (!done(kBarPFull, j) || !done(kBarVFull, j)) return false;
         tc_fence_after();
-        if (lane == 0) {
+        if (leader) {
           const uint64_t v = dv + (uint64_t)((j & 1) * (Ly::kTile >> 4)), p = dp + (uint64_t)((j & 1) * (Ly::kPTile >> 4));
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
@@ -479,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
         for (int t = g.t0; t < g.t1; ++t, ++j) {
           if (misc[2] || !done(kBarKFull, j) || !used_before(kBarSEmpty, j)) { ok = false; break; }
           tc_fence_after();
-          if (lane == 0) {
+          if (leader) {
             const uint64_t q = dq + (uint64_t)((s & 1) * (Ly::kQTile >> 4));
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
@@ -511,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
         for (int r = warp - kQWarp; r < kN; r += 2) {
           const int rr = kBlock * g.rb + r;
           if (rr >= A.R || rr % A.n >= g.T) {  // no row: whatever its column holds stays there
-            if (lane == 0) f[r] = 0.f;
+            if (lane == 0) f[r] = 0x1p-126f;
             continue;
           }
           const uint32_t* src = reinterpret_cast<const uint32_t*>(X.q + (q0 + r) * D + ch);
@@ -531,8 +532,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
           uint8_t* dst = to + (ch >> 6) * (kBlock * 128) + sw128_offset(r, (ch & 63) >> 3) + (ch & 7) * 2;
 #pragma unroll
           for (int x = 0; x < kPer / 2; ++x) reinterpret_cast<uint32_t*>(dst)[x] = h[x];
-          if (lane == 0)
-            f[r] = A.scale_log2 * __uint_as_float((uint32_t)(127 - a) << 23) * __uint_as_float((uint32_t)(127 - c) << 23);
+          if (lane == 0)  // (not zero: -inf times it stays -inf)
+            f[r] = fmaxf(0x1p-126f, A.scale_log2 * __uint_as_float((uint32_t)(127 - a) << 23) * __uint_as_float((uint32_t)(127 - c) << 23));
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -552,10 +553,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
     float* wmax = alpha + kBlock;                           // [4][kBlock]
     float* wl = wmax + 4 * kBlock;                          // [4][kBlock]
     int syncs = 0;
-    auto group_sync = [&]() -> bool {
+    auto group_arrive = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kBarGroup]);
-      return mbar_wait(&bars[kBarGroup], syncs++ & 1);
+    };
+    auto group_wait = [&]() { return mbar_wait(&bars[kBarGroup], syncs++ & 1); };
+    auto group_sync = [&]() {
+      group_arrive();
+      return group_wait();
     };
     int j = 0;
     Seg g;
@@ -568,9 +573,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
         rowi[set + tid] = rr < A.R && i < g.T ? i : -1;
         if (kWin) rowend[set + tid] = behind(A, g.b, i, C);
       }
-      float l[kN];
+      uint64_t l[kN / 2];  // sums of this key's lane, rows in pairs
 #pragma unroll
-      for (int r = 0; r < kN; ++r) l[r] = 0.f;
+      for (int r = 0; r < kN / 2; ++r) l[r] = pk2(0.f, 0.f);
       if (!mbar_wait(&bars[kBarQFull + (s & 1)], (s >> 1) & 1) || !group_sync()) { ok = false; break; }
       const float* f = rowf + set;
       for (int t = g.t0; t < g.t1; ++t, ++j) {
@@ -578,19 +583,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
         const bool masked = key0 + 128 > C || (kWin && key0 + 128 > A.sink && key0 < (int64_t)C + A.n - A.window);
         if (misc[2] || !done(kBarQK, j)) { ok = false; break; }
         tc_fence_after();
-        float sv[kN];
-#pragma unroll
-        for (int c = 0; c < kN; c += 16)
-          tmem_ld16(tmem + lane_base + kColS + 64 * (j & 1) + c, reinterpret_cast<uint32_t*>(sv) + c);
-        tmem_ld_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kBarSEmpty + (j & 1)]);
-        uint32_t see[(kN + 31) / 32];  // rows that see this key
-#pragma unroll
-        for (int x = 0; x < (kN + 31) / 32; ++x) see[x] = 0xFFFFFFFFu;
+        uint32_t see[(kN + 31) / 32];  // masked: rows that see this key
         if (masked) {
           const int rel = key - C;
+#pragma unroll
+          for (int x = 0; x < (kN + 31) / 32; ++x) see[x] = 0;
 #pragma unroll 1
           for (int r = 0; r < kN; ++r) {
             const int i = rowi[set + r];
@@ -599,38 +596,55 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
               in = A.mask ? i >= 0 && (__ldg(A.mask + g.b * A.mask_stride + (int64_t)i * A.words + (rel >> 5)) >> (rel & 31) & 1u)
                           : rel <= i;
             if (kWin && key >= A.sink && key < rowend[set + r]) in = false;
-            if (!in) {
-              if (kN > 32 && r >= 32) see[(kN - 1) / 32] &= ~(1u << (r & 31));
-              else see[0] &= ~(1u << r);
-            }
+            if (kN > 32 && r >= 32) see[(kN - 1) / 32] |= (in ? 1u : 0u) << (r & 31);
+            else see[0] |= (in ? 1u : 0u) << (r & 31);
           }
         }
-        // scores in log2 units above the reference, and whether one is too far above
-        bool far = t == g.t0;
-        if (!far) {
+        float y[kN];
+        auto load_scores = [&]() {  // -inf where a row does not see the key
+#pragma unroll
+          for (int c = 0; c < kN; c += 16)
+            tmem_ld16(tmem + lane_base + kColS + 64 * (j & 1) + c, reinterpret_cast<uint32_t*>(y) + c);
+          tmem_ld_wait();
+          if (masked)
+#pragma unroll
+            for (int r = 0; r < kN; ++r) y[r] = (see[r >> 5] >> (r & 31) & 1u) ? y[r] : -INFINITY;
+        };
+        // log2 of the weights; returns the largest
+        auto scale_scores = [&]() -> float {
           float top = -INFINITY;
 #pragma unroll
           for (int r = 0; r < kN; r += 4) {
-            const float4 a = *reinterpret_cast<const float4*>(f + r), n4 = *reinterpret_cast<const float4*>(nref + r);
-            float y[4] = {fmaf(sv[r], a.x, n4.x), fmaf(sv[r + 1], a.y, n4.y), fmaf(sv[r + 2], a.z, n4.z),
-                          fmaf(sv[r + 3], a.w, n4.w)};
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (!(see[(r + x) >> 5] >> ((r + x) & 31) & 1u)) y[x] = -INFINITY;
-            top = fmaxf(max3f(y[0], y[1], y[2]), fmaxf(y[3], top));
+            const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(f + r), b = *reinterpret_cast<const ulonglong2*>(nref + r);
+            up2(fma2(pk2(y[r], y[r + 1]), a.x, b.x), y[r], y[r + 1]);
+            up2(fma2(pk2(y[r + 2], y[r + 3]), a.y, b.y), y[r + 2], y[r + 3]);
+            top = max3f(max3f(y[r], y[r + 1], y[r + 2]), y[r + 3], top);
           }
-          far = __any_sync(0xFFFFFFFFu, top > kTop + kRaise);
-          if (far && lane == 0) misc[4 + (syncs & 1)] = syncs;
+          return top;
+        };
+        auto exponentials = [&]() {
+#pragma unroll
+          for (int r = 0; r < kN; ++r) y[r] = ex2(y[r]);
+        };
+        load_scores();
+        bool far = t == g.t0;
+        if (!far) {
+          // Does one of the four warps' scores pass its reference too far?  The exponentials are under way meanwhile.
+          const float top = scale_scores();
           const int at = syncs;
-          if (!group_sync()) { ok = false; break; }
+          if (__any_sync(0xFFFFFFFFu, top > kTop + kRaise) && lane == 0) misc[4 + (at & 1)] = at;
+          group_arrive();
+          exponentials();
+          if (!group_wait()) { ok = false; break; }
           far = misc[4 + (at & 1)] == (uint32_t)at;
+          if (far) load_scores();
         }
         if (far) {
           // the rows' maxima over the tile, new references, and what was summed comes to them
           float mine[(kN + 31) / 32] = {};
 #pragma unroll
           for (int r = 0; r < kN; ++r) {
-            const float m = warp_max((see[r >> 5] >> (r & 31) & 1u) ? sv[r] * f[r] : -INFINITY);
+            const float m = warp_max(y[r] * f[r]);
             if (lane == (r & 31)) mine[r >> 5] = m;
           }
 #pragma unroll
@@ -642,13 +656,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
 #pragma unroll
             for (int w = 0; w < 4; ++w) m = fmaxf(m, wmax[w * kBlock + tid]);
             alpha[tid] = m == m_used ? 1.f : ex2(m_used - m);
-            nref[tid] = kTop - m;  // +inf while the row has met no key: its first one is too far above
+            nref[tid] = fminf(kTop - m, 3e38f);  // (no key met yet: the first one is too far above)
             m_used = m;
           }
           if (!group_sync()) { ok = false; break; }
           if (t > g.t0) {
 #pragma unroll
-            for (int r = 0; r < kN; ++r) l[r] *= alpha[r];
+            for (int r = 0; r < kN; r += 2) l[r / 2] = mul2(l[r / 2], pk2(alpha[r], alpha[r + 1]));
             if (!done(kBarPV, j - 1)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll 1
@@ -662,25 +676,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
             }
             tmem_st_wait();
           }
+          scale_scores();
+          exponentials();
         }
+        tc_fence_before();  // the scores are in registers
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kBarSEmpty + (j & 1)]);
         if (!used_before(kBarPV, j)) { ok = false; break; }
         uint8_t* p = sm + Ly::kP + (j & 1) * Ly::kPTile;
 #pragma unroll
         for (int r = 0; r < kN; r += 8) {
           uint32_t w[4];
 #pragma unroll
-          for (int x = 0; x < 8; x += 4) {
-            const float4 a = *reinterpret_cast<const float4*>(f + r + x), n4 = *reinterpret_cast<const float4*>(nref + r + x);
-            float y[4] = {fmaf(sv[r + x], a.x, n4.x), fmaf(sv[r + x + 1], a.y, n4.y), fmaf(sv[r + x + 2], a.z, n4.z),
-                          fmaf(sv[r + x + 3], a.w, n4.w)};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (!(see[(r + x + k) >> 5] >> ((r + x + k) & 31) & 1u)) y[k] = -INFINITY;
-              y[k] = ex2(y[k]);
-              l[r + x + k] += y[k];
-            }
-            w[x / 2] = pack_f16x2(y[0], y[1]);
-            w[x / 2 + 1] = pack_f16x2(y[2], y[3]);
+          for (int x = 0; x < 4; ++x) {
+            w[x] = pack_f16x2(y[r + 2 * x], y[r + 2 * x + 1]);
+            l[r / 2 + x] = add2(l[r / 2 + x], pk2(y[r + 2 * x], y[r + 2 * x + 1]));
           }
           *reinterpret_cast<uint4*>(p + sw128_offset(tid, r >> 3)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
@@ -693,9 +703,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
 
       // ---- the segment's end: row sums over lanes and warps, then O^T (thread = channel)
       if (lane == 0) mbar_arrive(&bars[kBarQEmpty + (s & 1)]);  // (behind the last barrier of the group: all have read f)
-      lane_sums<kN, 16>(l, lane);
-      if constexpr (kN == 64) *reinterpret_cast<float2*>(wl + warp * kBlock + 2 * lane) = make_float2(l[0], l[1]);
-      else if (kN == 32 || !(lane & 1)) wl[warp * kBlock + (kN == 32 ? lane : lane >> 1)] = l[0];
+      float sums[kN];
+#pragma unroll
+      for (int r = 0; r < kN; r += 2) up2(l[r / 2], sums[r], sums[r + 1]);
+      lane_sums<kN, 16>(sums, lane);
+      if constexpr (kN == 64) *reinterpret_cast<float2*>(wl + warp * kBlock + 2 * lane) = make_float2(sums[0], sums[1]);
+      else if (kN == 32 || !(lane & 1)) wl[warp * kBlock + (kN == 32 ? lane : lane >> 1)] = sums[0];
       if (!group_sync()) { ok = false; break; }
       const bool whole = g.r0 == 0 && g.r1 == g.tiles;
       const int full = min(kBlock, A.R), width = min(kBlock, A.R - kBlock * g.rb);
@@ -742,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
   if (misc[2]) {
     // A role gave up: copies and products that nobody waited for end before the CTA's shared memory and TMEM go.
     if (warp == kIssuer) {
-      if (lane == 0) mma_commit(&bars[kBarDrain]);
+      if (elect_one()) mma_commit(&bars[kBarDrain]);
       mbar_wait(&bars[kBarDrain], 0, kDrainNs);
     } else if (warp == kLoader) {
       const int asked = (int)misc[3];

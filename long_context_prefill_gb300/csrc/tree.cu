@@ -495,6 +495,7 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
       }
     } else if (kPair && warp == kMmaWarp0) {
       // ------------------------------------------------------------ scores of both groups
+      const bool leader = elect_one();
       int tile = 0, use = 0;  // tiles so far, uses of S so far
       Seg g;
       for (int s = 0; next_seg(0, s, g); ++s) {
@@ -508,21 +509,22 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
             if (use > 0 && !mbar_wait(&bars[kBarSFree], (use - 1) & 1)) { ok = false; break; }
             ++use;
             tc_fence_after();
-            if (lane == 0) {
+            if (leader) {
               issue_qk(tmem + kColS, q_desc(X, 0), dk + (uint64_t)kst * kTileDesc);
               mma_commit(&bars[kBarSFull + X]);
             }
             __syncwarp();
           }
-          if (ok && lane == 0) mma_commit(&bEmpty[kst]);
+          if (ok && leader) mma_commit(&bEmpty[kst]);
           __syncwarp();
         }
         if (!ok) break;
-        if (lane == 0) mma_commit(&bars[kBarQEmpty]);
+        if (leader) mma_commit(&bars[kBarQEmpty]);
         __syncwarp();
       }
     } else if (kPair) {
       // ------------------------------------------------------------ O += P V of both groups
+      const bool leader = elect_one();
       int tile = 0, seen[2] = {0, 0};  // tiles so far, P's of each group
       Seg g;
       for (int s = 0; next_seg(0, s, g); ++s) {
@@ -538,25 +540,26 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
             if (!mbar_wait(&bars[kBarPFull + X], seen[X] & 1)) { ok = false; break; }
             ++seen[X];
             tc_fence_after();
-            if (lane == 0) {
+            if (leader) {
               issue_pv_mma(tmem + kColO + 128 * X, tmem + kColP + 64 * X, dv + (uint64_t)vst * kTileDesc, t == g.t0);
               mma_commit(&bars[kBarPV + X]);
             }
             __syncwarp();
           }
-          if (ok && lane == 0) mma_commit(&bEmpty[vst]);
+          if (ok && leader) mma_commit(&bEmpty[vst]);
           __syncwarp();
         }
         for (int X = 0; X < 2 && ok; ++X)
           if (group_rows(g.rb, X) <= 0) {
             ok = o_free(X);
-            if (ok && lane == 0) mbar_arrive(&bars[kBarODone + X]);
+            if (ok && leader) mbar_arrive(&bars[kBarODone + X]);
             __syncwarp();
           }
         if (!ok) break;
       }
     } else if (!kPair && (warp == kMmaWarp0 || warp == kMmaWarp1)) {
       // ---------------------------------------------------------- MMA issuer of group X
+      const bool leader = elect_one();
       const int X = warp == kMmaWarp0 ? 0 : 1;
       const uint32_t tS = tmem + kColS + 128 * X, tO = tmem + kColO + 128 * X;
       int k = 0;  // tiles of this group so far
@@ -572,7 +575,7 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
           const int vidx = 2 * turn(X, k - 1) + 1, vst = vidx % kSlots;
           if (!ready(vidx)) return false;
           tc_fence_after();
-          if (lane == 0) {
+          if (leader) {
             issue_pv_mma(tO, tS, dv + (uint64_t)vst * kTileDesc, first);
             mma_commit(&bEmpty[vst]);
           }
@@ -584,7 +587,7 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
           const int kidx = 2 * turn(X, k), kst = kidx % kSlots;
           if (!ready(kidx)) { ok = false; break; }
           tc_fence_after();
-          if (lane == 0) {
+          if (leader) {
             issue_qk(tS, q0, dk + (uint64_t)kst * kTileDesc);
             mma_commit(&bars[kBarSFull + X]);
             mma_commit(&bEmpty[kst]);
@@ -593,7 +596,7 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
           __syncwarp();
         }
         if (!ok || !issue_pv(g.t1 == g.t0 + 1)) { ok = false; break; }
-        if (lane == 0) mma_commit(&bars[kBarODone + X]);
+        if (leader) mma_commit(&bars[kBarODone + X]);
         __syncwarp();
       }
     }
@@ -934,7 +937,7 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
     // gave up themselves: those end before the CTA's shared memory and TMEM go.
     if (warp == kMmaWarp0 || warp == kMmaWarp1) {
       uint64_t* drained = &bars[kBarDrain + (warp == kMmaWarp0 ? 0 : 1)];
-      if (lane == 0) mma_commit(drained);
+      if (elect_one()) mma_commit(drained);
       mbar_wait(drained, 0, kDrainNs);
     } else if (warp == kLoaderWarp || (!kPair && warp == kLoaderWarp1)) {
       const int X = warp == kLoaderWarp ? 0 : 1, asked = misc[6 + X];
