@@ -24,16 +24,19 @@
 //
 // Split: as tree.cu's (tree.cuh), one part of the line of tiles per CTA.
 //
-// A CTA (16 warps, one CTA per SM):
-//   warps 0-3    softmax (thread = key = TMEM lane), the segment's output
-//   warps 4-7    decode K: shared memory -> registers -> TMEM (two buffers)
-//   warps 8-11   decode V: shared memory -> registers -> shared memory (two
+// A CTA (20 warps, one CTA per SM):
+//   warps 0-7    softmax (thread = key = TMEM lane) in two groups that take the
+//                tiles in turn, each with its own references, sums and O: a
+//                tile's chain (scores, exponentials, weights) is latency, two of
+//                them side by side are not.  They are joined at a segment's end
+//   warps 8-11   decode K: shared memory -> registers -> TMEM (two buffers)
+//   warps 12-15  decode V: shared memory -> registers -> shared memory (two
 //                buffers); rows that no query sees become zeros (their pages
 //                may hold anything)
-//   warp 12      loader: walks the part's segments, a bulk copy per page and
+//   warp 16      loader: walks the part's segments, a bulk copy per page and
 //                head (K and V lie side by side) into a ring of tiles
-//   warp 13      issues the products
-//   warps 14-15  Q of the next segment to fp16
+//   warp 17      issues the products
+//   warps 18-19  Q of the next segment to fp16
 #include "kv4.cuh"
 #include "tree.cuh"
 
@@ -42,11 +45,11 @@ namespace msa {
 namespace {
 
 constexpr int kBlock = 64;  // rows of an item
-constexpr int kThreads = 512;
-constexpr int kDecodeK = 4, kDecodeV = 8, kLoader = 12, kIssuer = 13, kQWarp = 14;
+constexpr int kThreads = 640;
+constexpr int kDecodeK = 8, kDecodeV = 12, kLoader = 16, kIssuer = 17, kQWarp = 18;
 constexpr int kSegSlots = 3;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColK = 0, kColS = 128, kColO = 256;  // K and S: two buffers of 64 columns
+constexpr uint32_t kColK = 0, kColS = 128, kColO = 256;  // two of 64 columns each
 constexpr float kTop = 7.f, kRaise = 8.f;                // log2: weight of the reference, how far a score may pass it
 constexpr uint32_t kIdleNs = 64;
 constexpr uint64_t kDrainNs = MSA_WAIT_LIMIT_NS / 16;
@@ -61,9 +64,10 @@ enum {
   kBarPV = 10,       // [2] the product is done: V and weights are free
   kBarQFull = 12,    // [2] Q of the segment
   kBarQEmpty = 14,   // [2] its products are done, its factors have been read
-  kBarGroup = 16,    // the softmax warps among themselves
-  kBarDrain = 17,    // after giving up: the products are done
-  kBarSegFull = 18,  // [kSegSlots]
+  kBarGroup = 16,    // [2] the warps of a softmax group among themselves
+  kBarBoth = 18,     // the warps of both
+  kBarDrain = 19,    // after giving up: the products are done
+  kBarSegFull = 20,  // [kSegSlots]
   kBarSegEmpty = kBarSegFull + kSegSlots,
   kBarRing = kBarSegEmpty + kSegSlots  // full[kStages], empty[kStages]
 };
@@ -79,10 +83,11 @@ struct Lay4 {
   static constexpr int kV = 0, kP = kV + 2 * kTile, kQ = kP + 2 * kPTile, kRaw = kQ + 2 * kQTile;
   static constexpr int kSeg = kRaw + kStages * kStage;
   static constexpr int kRows = (kSeg + kSegSlots * (int)sizeof(Seg) + 15) / 16 * 16;
-  // per row: factors [2], rows [2], window ends [2], reciprocals [2], references, factors of a raise, maxima [4], sums [4]
-  static constexpr int kWsum = kRows + 18 * kBlock * 4;
-  static constexpr int kBars = kWsum + 16 * 8;
-  static constexpr int kMisc = kBars + (kBarRing + 2 * kStages) * 8;  // [0] TMEM base, [2] abort, [3] tiles asked for, [4] flags [2]
+  // per row, [segment parity]: factors, rows, window ends; [group]: references, factors of a raise, last references,
+  // factors of O, maxima [warp], sums [warp]
+  static constexpr int kWsum = kRows + (6 + 8 + 16) * kBlock * 4;
+  static constexpr int kBars = kWsum + (kThreads / 32) * 8;
+  static constexpr int kMisc = kBars + (kBarRing + 2 * kStages) * 8;  // [0] TMEM base, [2] abort, [3] tiles asked for, [4] flags [group][2]
   static constexpr int kStart = kMisc + 32;
   static constexpr int kAlloc = kStart + 16;
   static_assert(kRows % 16 == 0 && kWsum % 8 == 0 && kStart % 8 == 0 && kRaw % 16 == 0, "alignment");
@@ -124,6 +129,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -181,7 +191,6 @@ template <int D, int kN, bool kWin>
 __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_constant__ Kv4Args X) {
   using Ly = Lay4<D>;
   constexpr int kStages = Ly::kStages;
-  constexpr bool kWide = kN == 64;  // the softmax threads' scores and sums take more registers than an equal share
   const TreeArgs& A = X.t;
   extern __shared__ __align__(1024) uint8_t sm[];  // swizzled tiles start on 1 KB
   if (smem_u32(sm) & 1023) {
@@ -212,20 +221,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
       mbar_init(&bars[kBarPFull + x], 4);
       mbar_init(&bars[kBarPV + x], 1);
       mbar_init(&bars[kBarQFull + x], 2);
-      mbar_init(&bars[kBarQEmpty + x], 5);
+      mbar_init(&bars[kBarQEmpty + x], 9);
+      mbar_init(&bars[kBarGroup + x], 4);
     }
-    mbar_init(&bars[kBarGroup], 4);
+    mbar_init(&bars[kBarBoth], 8);
     mbar_init(&bars[kBarDrain], 1);
     for (int s = 0; s < kSegSlots; ++s) {
       mbar_init(&bars[kBarSegFull + s], 1);
-      mbar_init(&bars[kBarSegEmpty + s], 11);  // softmax, V, issuer, Q
+      mbar_init(&bars[kBarSegEmpty + s], 15);  // softmax, V, issuer, Q
     }
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bFull[s], 1);
       mbar_init(&bEmpty[s], 8);
     }
     misc[2] = misc[3] = 0;
-    misc[4] = misc[5] = 0xFFFFFFFFu;
+    for (int x = 4; x < 8; ++x) misc[x] = 0xFFFFFFFFu;
     fence_mbar_init();
   }
   // ---- this CTA's part of the line of tiles, and the request it starts in
@@ -300,21 +310,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
   auto codes_at = [&](int r) { return (r >> A.page_shift) * 2 * P * Ly::kUnit + (r & (P - 1)) * 16; };
   auto scales_at = [&](int r) { return (r >> A.page_shift) * 2 * P * Ly::kUnit + P * (D / 2) + (r & (P - 1)) * (D / 16); };
 
-  if (warp >= 4) {
-    if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+  // The softmax threads hold kN scores and sums: the block starts with 5 x 128 threads x 96 registers; 2 x 152 + 3 x 56
+  // and 2 x 128 + 3 x 72 are below 5 x 96
+  if (warp >= kDecodeK) {
+    if (kN == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (kN == 32) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp < kDecodeV) {
       // ------------------------------------------------------------ K to TMEM
       const int r = 32 * (warp - kDecodeK) + lane;
       const uint32_t to = tmem + ((uint32_t)(32 * (warp - kDecodeK)) << 16) + kColK;
-      for (int j = 0; j < cnt && ok; ++j) {
+      Row4<D> row, next;
+      auto fetch = [&](int j) -> bool {  // the codes of tile j: on their way while those of the tile before are decoded
         const int st = j % kStages;
-        if (misc[2] || !mbar_wait(&bFull[st], (j / kStages) & 1)) { ok = false; break; }
+        if (misc[2] || !mbar_wait(&bFull[st], (j / kStages) & 1)) return false;
         const uint8_t* raw = sm + Ly::kRaw + st * Ly::kStage;
-        Row4<D> row;
-        row.load(raw + codes_at(r), 16 * P, raw + scales_at(r));
+        next.load(raw + codes_at(r), 16 * P, raw + scales_at(r));
         __syncwarp();
         if (lane == 0) mbar_arrive(&bEmpty[st]);
-        if (!used_before(kBarQK, j)) { ok = false; break; }
+        return true;
+      };
+      ok = fetch(0);
+      for (int j = 0; j < cnt && ok; ++j) {
+        row = next;
+        if ((j + 1 < cnt && !fetch(j + 1)) || !used_before(kBarQK, j)) { ok = false; break; }
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
@@ -330,41 +348,48 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
     } else if (warp < kLoader) {
       // ------------------------------------------------------------ V to shared memory
       const int r = 32 * (warp - kDecodeV) + lane;
-      int j = 0;
       Seg g;
-      for (int s = 0; j < cnt && next_seg(s, g); ++s) {
-        const Span span = span_of<kWin>(A, g.L, g.T);
-        for (int t = g.t0; t < g.t1 && ok; ++t, ++j) {
-          const int st = j % kStages;
-          if (misc[2] || !mbar_wait(&bFull[st], (j / kStages) & 1)) { ok = false; break; }
-          const uint8_t* raw = sm + Ly::kRaw + st * Ly::kStage + P * Ly::kUnit;
-          Row4<D> row;
-          row.load(raw + codes_at(r), 16 * P, raw + scales_at(r));
-          const int key = span.key0(t) + r;
-          if (key >= g.L || (kWin && key >= span.hole && key < span.lo)) {  // seen by no row: zeros
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) row.code[c] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) row.scale[c] = 0;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bEmpty[st]);
-          if (!used_before(kBarPV, j)) { ok = false; break; }
-          uint8_t* v = sm + Ly::kV + (j & 1) * Ly::kTile;
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t w[16];
-            row.chunk(c, w);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              *reinterpret_cast<uint4*>(v + (c >> 1) * 16384 + sw128_offset(r, 4 * (c & 1) + x)) =
-                  make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[kBarVFull + (j & 1)]);
+      Span span;
+      int s = 0, t = 0;
+      Row4<D> row, next;
+      auto fetch = [&](int j) -> bool {
+        if (j == 0 || t == g.t1) {
+          if (!next_seg(s++, g)) return false;
+          span = span_of<kWin>(A, g.L, g.T);
+          t = g.t0;
         }
-        if (!ok) break;
+        const int st = j % kStages;
+        if (misc[2] || !mbar_wait(&bFull[st], (j / kStages) & 1)) return false;
+        const uint8_t* raw = sm + Ly::kRaw + st * Ly::kStage + P * Ly::kUnit;
+        next.load(raw + codes_at(r), 16 * P, raw + scales_at(r));
+        const int key = span.key0(t++) + r;
+        if (key >= g.L || (kWin && key >= span.hole && key < span.lo)) {  // seen by no row: zeros
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) next.code[c] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) next.scale[c] = 0;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bEmpty[st]);
+        return true;
+      };
+      ok = fetch(0);
+      for (int j = 0; j < cnt && ok; ++j) {
+        row = next;
+        if ((j + 1 < cnt && !fetch(j + 1)) || !used_before(kBarPV, j)) { ok = false; break; }
+        uint8_t* v = sm + Ly::kV + (j & 1) * Ly::kTile;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t w[16];
+          row.chunk(c, w);
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            *reinterpret_cast<uint4*>(v + (c >> 1) * 16384 + sw128_offset(r, 4 * (c & 1) + x)) =
+                make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kBarVFull + (j & 1)]);
       }
     } else if (warp == kLoader) {
       // ------------------------------------------------------------ loader
@@ -466,14 +491,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
           const uint64_t v = dv + (uint64_t)((j & 1) * (Ly::kTile >> 4)), p = dp + (uint64_t)((j & 1) * (Ly::kPTile >> 4));
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ss(tmem + kColO, v + (uint64_t)(kk * 128), p + (uint64_t)(kk * 128), id_pv, (!first || kk > 0) ? 1u : 0u);
+            mma_bf16_ss(tmem + kColO + 64 * (j & 1), v + (uint64_t)(kk * 128), p + (uint64_t)(kk * 128), id_pv, (!first || kk > 0) ? 1u : 0u);
           mma_commit(&bars[kBarPV + (j & 1)]);
         }
         __syncwarp();
         return true;
       };
       int j = 0;
-      bool first = true;  // tile j - 1 is its segment's first
+      bool first = true;  // tile j - 1 is the first of its group in the segment
       Seg g;
       for (int s = 0; j < cnt && next_seg(s, g); ++s) {
         if (!mbar_wait(&bars[kBarQFull + (s & 1)], (s >> 1) & 1)) { ok = false; break; }
@@ -491,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
           }
           __syncwarp();
           if (j > 0 && !issue_pv(j - 1, first)) { ok = false; break; }
-          first = t == g.t0;
+          first = t - g.t0 < 2;
         }
         if (!ok) break;
       }
@@ -541,30 +566,38 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
       }
     }
   } else {
-    if (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    // ------------------------------------------------------------ softmax: thread = key
-    const int tid = threadIdx.x;
-    const uint32_t lane_base = (uint32_t)(32 * warp) << 16;
+    if (kN == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    if (kN == 32) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    // ------------------------------------------------------------ softmax group H: the part's tiles j = H mod 2; thread = key
+    const int H = warp >> 2, w4 = warp & 3, tid = threadIdx.x & 127;
+    const uint32_t lane_base = (uint32_t)(32 * w4) << 16;
     int* rowi = reinterpret_cast<int*>(rowf + 2 * kBlock);  // [2][kBlock] drafted token of the row, -1: no row
     int* rowend = rowi + 2 * kBlock;                        // [2][kBlock] kWin: end of the keys behind its window
-    float* inv = reinterpret_cast<float*>(rowend + 2 * kBlock);  // [2][kBlock] 1 / row sum, V's scale in it
-    float* nref = inv + 2 * kBlock;                         // kTop - reference
-    float* alpha = nref + kBlock;                           // factors of a raise
-    float* wmax = alpha + kBlock;                           // [4][kBlock]
-    float* wl = wmax + 4 * kBlock;                          // [4][kBlock]
-    int syncs = 0;
+    float* rows = reinterpret_cast<float*>(rowend + 2 * kBlock);
+    float* nref = rows + H * kBlock;                        // [2] kTop - reference
+    float* alpha = rows + (2 + H) * kBlock;                 // [2] factors of a raise
+    float* last = rows + 4 * kBlock;                        // [2] references at the segment's end
+    float* fo = rows + 6 * kBlock;                          // [2] factors of O
+    float* wmax = rows + (8 + 4 * H) * kBlock;              // [2][4] maxima
+    float* wl = rows + 16 * kBlock;                         // [2][4] sums
+    int syncs = 0, boths = 0;
     auto group_arrive = [&]() {
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kBarGroup]);
+      if (lane == 0) mbar_arrive(&bars[kBarGroup + H]);
     };
-    auto group_wait = [&]() { return mbar_wait(&bars[kBarGroup], syncs++ & 1); };
+    auto group_wait = [&]() { return mbar_wait(&bars[kBarGroup + H], syncs++ & 1); };
     auto group_sync = [&]() {
       group_arrive();
       return group_wait();
     };
-    int j = 0;
+    auto both_sync = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kBarBoth]);
+      return mbar_wait(&bars[kBarBoth], boths++ & 1);
+    };
+    int j0 = 0;  // the segment's first tile
     Seg g;
-    for (int s = 0; j < cnt && next_seg(s, g); ++s) {
+    for (int s = 0; j0 < cnt && next_seg(s, g); ++s) {
       const Span span = span_of<kWin>(A, g.L, g.T);
       const int C = g.L - g.T, set = (s & 1) * kBlock;
       float m_used = -INFINITY;  // of row `tid`
@@ -578,7 +611,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
       for (int r = 0; r < kN / 2; ++r) l[r] = pk2(0.f, 0.f);
       if (!mbar_wait(&bars[kBarQFull + (s & 1)], (s >> 1) & 1) || !group_sync()) { ok = false; break; }
       const float* f = rowf + set;
-      for (int t = g.t0; t < g.t1; ++t, ++j) {
+      const int tiles = g.t1 - g.t0, first = (j0 ^ H) & 1;  // the group's first tile of them
+      for (int x = first; x < tiles; x += 2) {
+        const int t = g.t0 + x, j = j0 + x;
         const int key0 = span.key0(t), key = key0 + tid;
         const bool masked = key0 + 128 > C || (kWin && key0 + 128 > A.sink && key0 < (int64_t)C + A.n - A.window);
         if (misc[2] || !done(kBarQK, j)) { ok = false; break; }
@@ -627,16 +662,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
           for (int r = 0; r < kN; ++r) y[r] = ex2(y[r]);
         };
         load_scores();
-        bool far = t == g.t0;
+        bool far = x == first;
         if (!far) {
           // Does one of the four warps' scores pass its reference too far?  The exponentials are under way meanwhile.
           const float top = scale_scores();
           const int at = syncs;
-          if (__any_sync(0xFFFFFFFFu, top > kTop + kRaise) && lane == 0) misc[4 + (at & 1)] = at;
+          if (__any_sync(0xFFFFFFFFu, top > kTop + kRaise) && lane == 0) misc[4 + 2 * H + (at & 1)] = at;
           group_arrive();
           exponentials();
           if (!group_wait()) { ok = false; break; }
-          far = misc[4 + (at & 1)] == (uint32_t)at;
+          far = misc[4 + 2 * H + (at & 1)] == (uint32_t)at;
           if (far) load_scores();
         }
         if (far) {
@@ -648,8 +683,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
             if (lane == (r & 31)) mine[r >> 5] = m;
           }
 #pragma unroll
-          for (int x = 0; x < (kN + 31) / 32; ++x)
-            if (32 * x + lane < kN) wmax[warp * kBlock + 32 * x + lane] = mine[x];
+          for (int y = 0; y < (kN + 31) / 32; ++y)
+            if (32 * y + lane < kN) wmax[w4 * kBlock + 32 * y + lane] = mine[y];
           if (!group_sync()) { ok = false; break; }
           if (tid < kN) {
             float m = m_used;
@@ -660,19 +695,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
             m_used = m;
           }
           if (!group_sync()) { ok = false; break; }
-          if (t > g.t0) {
+          if (x > first) {
 #pragma unroll
             for (int r = 0; r < kN; r += 2) l[r / 2] = mul2(l[r / 2], pk2(alpha[r], alpha[r + 1]));
-            if (!done(kBarPV, j - 1)) { ok = false; break; }
+            if (!done(kBarPV, j - 2)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < kN; c += 16) {
               uint32_t o[16];
-              tmem_ld16(tmem + lane_base + kColO + c, o);
+              tmem_ld16(tmem + lane_base + kColO + 64 * H + c, o);
               tmem_ld_wait();
 #pragma unroll
               for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha[c + x]);
-              tmem_st16(tmem + lane_base + kColO + c, o);
+              tmem_st16(tmem + lane_base + kColO + 64 * H + c, o);
             }
             tmem_st_wait();
           }
@@ -707,42 +742,61 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
 #pragma unroll
       for (int r = 0; r < kN; r += 2) up2(l[r / 2], sums[r], sums[r + 1]);
       lane_sums<kN, 16>(sums, lane);
-      if constexpr (kN == 64) *reinterpret_cast<float2*>(wl + warp * kBlock + 2 * lane) = make_float2(sums[0], sums[1]);
-      else if (kN == 32 || !(lane & 1)) wl[warp * kBlock + (kN == 32 ? lane : lane >> 1)] = sums[0];
-      if (!group_sync()) { ok = false; break; }
+      float* own = wl + (4 * H + w4) * kBlock;
+      if constexpr (kN == 64) *reinterpret_cast<float2*>(own + 2 * lane) = make_float2(sums[0], sums[1]);
+      else if (kN == 32 || !(lane & 1)) own[kN == 32 ? lane : lane >> 1] = sums[0];
+      if (tid < kN) last[H * kBlock + tid] = m_used;
+      if (!both_sync()) { ok = false; break; }
       const bool whole = g.r0 == 0 && g.r1 == g.tiles;
       const int full = min(kBlock, A.R), width = min(kBlock, A.R - kBlock * g.rb);
       const int64_t slot = 2 * (int64_t)blockIdx.x + (g.r0 > 0 ? 0 : 1);
       const int64_t grow = (int64_t)(g.b * A.Hq + g.kvh * (A.Hq / A.Hkv)) * A.n + kBlock * g.rb;
-      if (tid < kN) {
-        const float sum = (wl[tid] + wl[kBlock + tid]) + (wl[2 * kBlock + tid] + wl[3 * kBlock + tid]);
+      if (H == 0 && tid < kN) {
+        // both groups' sums and products at the larger reference
+        const float m0 = last[tid], m1 = last[kBlock + tid], m = fmaxf(m0, m1), ref = m == -INFINITY ? 0.f : m;
+        const float f0 = ex2(m0 - ref), f1 = ex2(m1 - ref);
+        const float* x = wl + tid;
+        const float s0 = (x[0] + x[kBlock]) + (x[2 * kBlock] + x[3 * kBlock]);
+        const float s1 = (x[4 * kBlock] + x[5 * kBlock]) + (x[6 * kBlock] + x[7 * kBlock]);
+        const float sum = f0 * s0 + f1 * s1;
         const bool some = !(sum == 0.f);
-        inv[set + tid] = whole ? (some ? X.v_scale / sum : 0.f) : X.v_scale;
+        const float inv = whole ? (some ? X.v_scale / sum : 0.f) : X.v_scale;
+        fo[tid] = f0 * inv;
+        fo[kBlock + tid] = f1 * inv;
         if (rowi[set + tid] >= 0) {
           // (sums are 2^kTop times those of the reference)
-          if (!whole) A.part_ml[slot * full + tid] = make_float2(m_used - kTop, sum);
-          else if (A.lse) A.lse[grow + tid] = some ? (m_used - kTop + __log2f(sum)) * 0.69314718055994531f : -INFINITY;
+          if (!whole) A.part_ml[slot * full + tid] = make_float2(m - kTop, sum);
+          else if (A.lse) A.lse[grow + tid] = some ? (m - kTop + __log2f(sum)) * 0.69314718055994531f : -INFINITY;
         }
       }
-      if (!group_sync() || !done(kBarPV, j - 1)) { ok = false; break; }
+      // the last products of both groups (a segment of one tile has one of them)
+      const int end = j0 + tiles - 1;
+      const bool two = tiles > 1;
+      if (!both_sync() || !done(kBarPV, end) || (two && !done(kBarPV, end - 1))) { ok = false; break; }
       tc_fence_after();
-      if (D == 128 || warp < 2) {
+      const uint32_t oA = tmem + lane_base + kColO + 64 * (end & 1), oB = tmem + lane_base + kColO + 64 * (~end & 1);
+      const float *fA = fo + kBlock * (end & 1), *fB = fo + kBlock * (~end & 1);
+      if (D == 128 || w4 < 2) {
 #pragma unroll 1
-        for (int c = 0; c < kN && c < width; c += 16) {
-          uint32_t o[16];
-          tmem_ld16(tmem + lane_base + kColO + c, o);
+        for (int c = 8 * H; c < kN && c < width; c += 16) {  // the groups take 8 rows in turn
+          uint32_t o[8], q[8];
+          tmem_ld8(oA + c, o);
+          tmem_ld8(oB + c, q);
           tmem_ld_wait();
 #pragma unroll
-          for (int x = 0; x < 16; ++x) {
+          for (int x = 0; x < 8; ++x) {
             const int r = c + x;
             if (rowi[set + r] < 0) continue;
-            const float y = __uint_as_float(o[x]) * inv[set + r];
+            float y = __uint_as_float(o[x]) * fA[r];
+            if (two) y = fmaf(__uint_as_float(q[x]), fB[r], y);
             if (whole) A.o[(grow + r) * D + tid] = __float2bfloat16(y);
             else reinterpret_cast<float*>(A.part + slot * (D / 4) * full + (int64_t)(tid >> 2) * width + r)[tid & 3] = y;
           }
         }
       }
       tc_fence_before();
+      if (!both_sync()) { ok = false; break; }  // O has been read
+      j0 += tiles;
     }
   }
   if (!ok) {
