@@ -45,14 +45,19 @@ namespace msa {
 namespace {
 
 constexpr int kBlock = 64;  // rows of an item
-constexpr int kThreads = 640;
-constexpr int kDecodeK = 8, kDecodeV = 12, kLoader = 16, kIssuer = 17, kQWarp = 18;
-constexpr int kSegSlots = 3;
+constexpr int kSegSlots = 4;
+
+// Warps of a CTA for blocks of up to kR rows.  With 64 rows the softmax threads' scores and sums leave the others few
+// registers, and the softmax is the longer part: K and V are decoded by one group of warps each.
+template <int kR>
+struct Roles {
+  static constexpr int kGroups = kR == 64 ? 1 : 2;  // of four warps that decode K, and V
+  static constexpr int kK = 8, kV = kK + 4 * kGroups, kLoader = kV + 4 * kGroups, kIssueQK = kLoader + 1,
+                       kIssuePV = kLoader + 2, kQ = kLoader + 3, kOut = kLoader + 4, kThreads = 32 * (kOut + 4);
+};
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColK = 0, kColS = 128, kColO = 256;  // two of 64 columns each
+constexpr uint32_t kColK = 0, kColS = 128, kColO = 256;  // two of 64 columns each; O: [segment parity][group]
 constexpr float kTop = 7.f, kRaise = 8.f;                // log2: weight of the reference, how far a score may pass it
-constexpr uint32_t kIdleNs = 64;
-constexpr uint64_t kDrainNs = MSA_WAIT_LIMIT_NS / 16;
 
 // [2]: buffers
 enum {
@@ -65,9 +70,12 @@ enum {
   kBarQFull = 12,    // [2] Q of the segment
   kBarQEmpty = 14,   // [2] its products are done, its factors have been read
   kBarGroup = 16,    // [2] the warps of a softmax group among themselves
-  kBarBoth = 18,     // the warps of both
-  kBarDrain = 19,    // after giving up: the products are done
-  kBarSegFull = 20,  // [kSegSlots]
+  kBarSums = 18,     // [2] a segment's references and sums are written
+  kBarODone = 20,    // [2] its products are done
+  kBarOFree = 22,    // [2] its O and sums have been read
+  kBarOut = 24,      // the output warps among themselves
+  kBarDrain = 25,    // [2] after giving up: an issuer's products are done
+  kBarSegFull = 27,  // [kSegSlots]
   kBarSegEmpty = kBarSegFull + kSegSlots,
   kBarRing = kBarSegEmpty + kSegSlots  // full[kStages], empty[kStages]
 };
@@ -83,14 +91,15 @@ struct Lay4 {
   static constexpr int kV = 0, kP = kV + 2 * kTile, kQ = kP + 2 * kPTile, kRaw = kQ + 2 * kQTile;
   static constexpr int kSeg = kRaw + kStages * kStage;
   static constexpr int kRows = (kSeg + kSegSlots * (int)sizeof(Seg) + 15) / 16 * 16;
-  // per row, [segment parity]: factors, rows, window ends; [group]: references, factors of a raise, last references,
-  // factors of O, maxima [warp], sums [warp]
-  static constexpr int kWsum = kRows + (6 + 8 + 16) * kBlock * 4;
-  static constexpr int kBars = kWsum + (kThreads / 32) * 8;
+  // per row, [segment parity]: factors, rows, window ends; [group]: references, factors of a raise, maxima [warp];
+  // [segment parity][group]: factors of O, last references, sums [warp]
+  static constexpr int kWsum = kRows + (6 + 4 + 8 + 4 + 4 + 16) * kBlock * 4;
+  static constexpr int kBars = kWsum + 32 * 8;
   static constexpr int kMisc = kBars + (kBarRing + 2 * kStages) * 8;  // [0] TMEM base, [2] abort, [3] tiles asked for, [4] flags [group][2]
   static constexpr int kStart = kMisc + 32;
-  static constexpr int kAlloc = kStart + 16;
-  static_assert(kRows % 16 == 0 && kWsum % 8 == 0 && kStart % 8 == 0 && kRaw % 16 == 0, "alignment");
+  static constexpr int kInfo = (kStart + 31) / 16 * 16;  // [kStages] rows of the tile that are seen: not x .. y - 1 nor from z on; w: not all
+  static constexpr int kAlloc = kInfo + kStages * 16;
+  static_assert(kRows % 16 == 0 && kWsum % 8 == 0 && kStart % 8 == 0 && kInfo % 16 == 0 && kRaw % 16 == 0, "alignment");
   static_assert(kAlloc <= 227 * 1024 && kAlloc > 120 * 1024, "shared memory: one CTA per SM");
 };
 
@@ -135,6 +144,11 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
@@ -143,32 +157,50 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
-// A token's codes and scales of K or V: chunk c of 16 bytes at code + c * step.
+// mbar_wait in five instructions: nine roles' loops share the instruction cache, so the bound is a count of polls (of 25
+// cycles at least: 0.2 s) and not a clock.
+constexpr uint32_t kPolls = 1u << 24, kDrainPolls = kPolls / 16;
+__device__ __forceinline__ bool wait4(uint64_t* bar, uint32_t parity, uint32_t polls = kPolls) {
+  for (; polls; --polls)
+    if (mbar_try_wait(bar, parity)) return true;
+  return false;
+}
+
+// 32 channels of a token: 16 bytes of codes and two scales, as 16 fp16 pairs.
+__device__ __forceinline__ void decode32(uint4 codes, uint32_t scales, uint32_t (&r)[16]) {
+  const uint32_t two = f16x2_of_e4m3x2(scales & 0xFFFFu);
+  const uint32_t s0 = __byte_perm(two, 0, 0x1010), s1 = __byte_perm(two, 0, 0x3232);
+  f16_of_codes(codes.x, s0, *reinterpret_cast<uint32_t(*)[4]>(r));
+  f16_of_codes(codes.y, s0, *reinterpret_cast<uint32_t(*)[4]>(r + 4));
+  f16_of_codes(codes.z, s1, *reinterpret_cast<uint32_t(*)[4]>(r + 8));
+  f16_of_codes(codes.w, s1, *reinterpret_cast<uint32_t(*)[4]>(r + 12));
+}
 template <int D>
-struct Row4 {
-  uint4 code[D / 32];
-  uint32_t scale[D / 64];
-  __device__ __forceinline__ void load(const uint8_t* codes, int step, const uint8_t* scales) {
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) code[c] = *reinterpret_cast<const uint4*>(codes + c * step);
-    if constexpr (D == 128) {
-      const uint2 s = *reinterpret_cast<const uint2*>(scales);
-      scale[0] = s.x;
-      scale[1] = s.y;
-    } else {
-      scale[0] = *reinterpret_cast<const uint32_t*>(scales);
-    }
+__device__ __forceinline__ void load_scales(const uint8_t* p, uint32_t (&s)[D / 64]) {
+  if constexpr (D == 128) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    s[0] = x.x;
+    s[1] = x.y;
+  } else {
+    s[0] = *reinterpret_cast<const uint32_t*>(p);
   }
-  // 32 channels as 16 fp16 pairs
-  __device__ __forceinline__ void chunk(int c, uint32_t (&r)[16]) const {
-    const uint32_t two = f16x2_of_e4m3x2(scale[c >> 1] >> (16 * (c & 1)));
-    const uint32_t s0 = __byte_perm(two, 0, 0x1010), s1 = __byte_perm(two, 0, 0x3232);
-    f16_of_codes(code[c].x, s0, *reinterpret_cast<uint32_t(*)[4]>(r));
-    f16_of_codes(code[c].y, s0, *reinterpret_cast<uint32_t(*)[4]>(r + 4));
-    f16_of_codes(code[c].z, s1, *reinterpret_cast<uint32_t(*)[4]>(r + 8));
-    f16_of_codes(code[c].w, s1, *reinterpret_cast<uint32_t(*)[4]>(r + 12));
+}
+
+// The scales of the next 32 channels to the front.
+template <int D>
+__device__ __forceinline__ void next_scales(uint32_t (&s)[D / 64]) {
+  if constexpr (D == 128) {
+    s[0] = __funnelshift_r(s[0], s[1], 16);
+    s[1] >>= 16;
+  } else {
+    s[0] >>= 16;
   }
-};
+}
+template <int D>
+__device__ __forceinline__ void store_zero_scales(uint8_t* p) {
+  if constexpr (D == 128) *reinterpret_cast<uint2*>(p) = make_uint2(0, 0);
+  else *reinterpret_cast<uint32_t*>(p) = 0;
+}
 
 // Sums l[0 .. n) over the warp; each step halves what a lane keeps: 64 rows end as rows 2 lane and 2 lane + 1 in l[0] and
 // l[1], 32 as row `lane`, 16 as row lane / 2 in l[0].
@@ -187,9 +219,12 @@ __device__ __forceinline__ void lane_sums(float* l, int lane) {
   if constexpr (o > 1) lane_sums<(n > 1 ? n / 2 : 1), o / 2>(l, lane);
 }
 
-template <int D, int kN, bool kWin>
-__global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_constant__ Kv4Args X) {
+template <int D, int kR, bool kWin>
+__global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const __grid_constant__ Kv4Args X) {
   using Ly = Lay4<D>;
+  using Ro = Roles<kR>;
+  constexpr int kN = kR < 16 ? 16 : kR;  // rows of a product (columns behind kR hold anything)
+  constexpr int kThreads = Ro::kThreads, kGroups = Ro::kGroups;
   constexpr int kStages = Ly::kStages;
   const TreeArgs& A = X.t;
   extern __shared__ __align__(1024) uint8_t sm[];  // swizzled tiles start on 1 KB
@@ -204,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
   Seg* segs = reinterpret_cast<Seg*>(sm + Ly::kSeg);
   float* rowf = reinterpret_cast<float*>(sm + Ly::kRows);  // [2][kBlock]
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(sm + Ly::kMisc);
+  int4* infos = reinterpret_cast<int4*>(sm + Ly::kInfo);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -212,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
     tmem_alloc(const_cast<uint32_t*>(&misc[0]), kTmemCols);
     tmem_relinquish();
   }
-  if (threadIdx.x == 32 * kIssuer) {
+  if (threadIdx.x == 32 * Ro::kIssueQK) {
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars[kBarKFull + x], 4);
       mbar_init(&bars[kBarQK + x], 1);
@@ -220,15 +256,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
       mbar_init(&bars[kBarVFull + x], 4);
       mbar_init(&bars[kBarPFull + x], 4);
       mbar_init(&bars[kBarPV + x], 1);
-      mbar_init(&bars[kBarQFull + x], 2);
+      mbar_init(&bars[kBarQFull + x], 1);
       mbar_init(&bars[kBarQEmpty + x], 9);
       mbar_init(&bars[kBarGroup + x], 4);
+      mbar_init(&bars[kBarSums + x], 8);
+      mbar_init(&bars[kBarODone + x], 1);
+      mbar_init(&bars[kBarOFree + x], 4);
+      mbar_init(&bars[kBarDrain + x], 1);
     }
-    mbar_init(&bars[kBarBoth], 8);
-    mbar_init(&bars[kBarDrain], 1);
+    mbar_init(&bars[kBarOut], 4);
     for (int s = 0; s < kSegSlots; ++s) {
       mbar_init(&bars[kBarSegFull + s], 1);
-      mbar_init(&bars[kBarSegEmpty + s], 15);  // softmax, V, issuer, Q
+      mbar_init(&bars[kBarSegEmpty + s], 8 + 2 + 1 + 4);  // softmax, issuers, Q, output
     }
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bFull[s], 1);
@@ -294,145 +333,137 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
   bool ok = true;
   auto next_seg = [&](int s, Seg& g) -> bool {
     const int slot = s % kSegSlots;
-    if (misc[2] || !mbar_wait(&bars[kBarSegFull + slot], (s / kSegSlots) & 1)) { ok = false; return false; }
+    if (misc[2] || !wait4(&bars[kBarSegFull + slot], (s / kSegSlots) & 1)) { ok = false; return false; }
     g = segs[slot];
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars[kBarSegEmpty + slot]);
     return g.b >= 0;
   };
-  // Tile j of the part is in buffer j & 1: use number j >> 1 of it.
-  auto used_before = [&](int bar, int j) {  // what frees the buffer for tile j has happened
-    return j < 2 || mbar_wait(&bars[bar + (j & 1)], ((j >> 1) - 1) & 1);
-  };
-  auto done = [&](int bar, int j) { return mbar_wait(&bars[bar + (j & 1)], (j >> 1) & 1); };
+  // Tile j of the part is in buffer j & 1, use number j >> 1 of it; segment s likewise.
+  auto done = [&](int bar, int j) { return wait4(&bars[bar + (j & 1)], (j >> 1) & 1); };
+  auto used_before = [&](int bar, int j) { return wait4(&bars[bar + (j & 1)], ((j >> 1) & 1) ^ 1); };  // (first use: at once)
+  // numbers of the rows (see Lay4)
+  float* rows = rowf;
+  int* rowi = reinterpret_cast<int*>(rows + 2 * kBlock);    // [parity] drafted token of the row, -1: no row
+  int* rowend = reinterpret_cast<int*>(rows + 4 * kBlock);  // [parity] kWin: end of the keys behind its window
+  constexpr int kRowRef = 6 * kBlock, kRowAlpha = 8 * kBlock, kRowMax = 10 * kBlock, kRowFo = 18 * kBlock,
+                kRowLast = 22 * kBlock, kRowSums = 26 * kBlock;
   // where the token of row r of a tile lies in a stage: K's codes; V's unit is one page's tokens further
   const int P = 1 << A.page_shift;
   auto codes_at = [&](int r) { return (r >> A.page_shift) * 2 * P * Ly::kUnit + (r & (P - 1)) * 16; };
   auto scales_at = [&](int r) { return (r >> A.page_shift) * 2 * P * Ly::kUnit + P * (D / 2) + (r & (P - 1)) * (D / 16); };
 
-  // The softmax threads hold kN scores and sums: the block starts with 5 x 128 threads x 96 registers; 2 x 152 + 3 x 56
-  // and 2 x 128 + 3 x 72 are below 5 x 96
-  if (warp >= kDecodeK) {
-    if (kN == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (kN == 32) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp < kDecodeV) {
-      // ------------------------------------------------------------ K to TMEM
-      const int r = 32 * (warp - kDecodeK) + lane;
-      const uint32_t to = tmem + ((uint32_t)(32 * (warp - kDecodeK)) << 16) + kColK;
-      Row4<D> row, next;
-      auto fetch = [&](int j) -> bool {  // the codes of tile j: on their way while those of the tile before are decoded
+  // The softmax threads hold kR scores and sums, so they take registers of the others: the block starts with 8 x 128
+  // threads x 64 (kR = 64: 6 x 128 x 80), and 2 x (88, 104) + 6 x (56, 48) are within 8 x 64, 2 x 144 + 4 x 48 within 6 x 80
+  if (warp >= Ro::kK) {
+    if (kR == 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (kR == 32 || kR == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp < Ro::kLoader) {
+      // ------------------------------------------------------------ K to TMEM, V to shared memory: group H the tiles
+      // j = H mod kGroups.  One loop for both (again for the instruction cache).
+      const bool is_v = warp >= Ro::kV;
+      const int H = ((warp - Ro::kK) >> 2) & (kGroups - 1), q = warp & 3, r = 32 * q + lane;
+      const uint32_t to = tmem + ((uint32_t)(32 * q) << 16) + kColK;
+      uint8_t* const codes0 = sm + Ly::kRaw + (is_v ? P * Ly::kUnit : 0) + codes_at(r);
+      uint8_t* const scales0 = sm + Ly::kRaw + (is_v ? P * Ly::kUnit : 0) + scales_at(r);
+      const uint32_t turn = (r & 7) << 4;  // the 128-byte swizzle of row r
+      const int free_bar = is_v ? kBarPV : kBarQK, full_bar = is_v ? kBarVFull : kBarKFull;
+      for (int j = H; j < cnt; j += kGroups) {
         const int st = j % kStages;
-        if (misc[2] || !mbar_wait(&bFull[st], (j / kStages) & 1)) return false;
-        const uint8_t* raw = sm + Ly::kRaw + st * Ly::kStage;
-        next.load(raw + codes_at(r), 16 * P, raw + scales_at(r));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bEmpty[st]);
-        return true;
-      };
-      ok = fetch(0);
-      for (int j = 0; j < cnt && ok; ++j) {
-        row = next;
-        if ((j + 1 < cnt && !fetch(j + 1)) || !used_before(kBarQK, j)) { ok = false; break; }
+        if (!wait4(&bFull[st], (j / kStages) & 1)) { ok = false; break; }
+        uint8_t* codes = codes0 + st * Ly::kStage;
+        const int4 seen = infos[st];
+        if (is_v && seen.w) {
+          // a row that no query sees is zero, whatever its page holds (its codes and scales here: then it decodes as one)
+          if (r >= seen.z || (r >= seen.x && r < seen.y)) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) *reinterpret_cast<uint4*>(codes + c * 16 * P) = make_uint4(0, 0, 0, 0);
+            store_zero_scales<D>(scales0 + st * Ly::kStage);
+          }
+        }
+        uint32_t scales[D / 64];
+        load_scales<D>(scales0 + st * Ly::kStage, scales);
+        if (!used_before(free_bar, j)) { ok = false; break; }
         tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
+        uint8_t* v = sm + Ly::kV + (j & 1) * Ly::kTile + r * 128;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c, codes += 16 * P) {
           uint32_t w[16];
-          row.chunk(c, w);
-          tmem_st16(to + 64 * (j & 1) + 16 * c, w);
+          decode32(*reinterpret_cast<const uint4*>(codes), scales[0], w);
+          next_scales<D>(scales);
+          if (is_v) {
+            uint8_t* dst = v + (c >> 1) * 16384;
+            const uint32_t at = turn ^ (uint32_t)((c & 1) << 6);
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              *reinterpret_cast<uint4*>(dst + (at ^ (uint32_t)(y << 4))) = make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
+          } else {
+            tmem_st16(to + 64 * (j & 1) + 16 * c, w);
+          }
         }
-        tmem_st_wait();
-        tc_fence_before();
+        if (is_v) {
+          fence_proxy_async_smem();  // V for the products; zeroed codes before the next copy into the stage
+        } else {
+          tmem_st_wait();
+          tc_fence_before();
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kBarKFull + (j & 1)]);
+        if (lane == 0) {
+          mbar_arrive(&bEmpty[st]);
+          mbar_arrive(&bars[full_bar + (j & 1)]);
+        }
       }
-    } else if (warp < kLoader) {
-      // ------------------------------------------------------------ V to shared memory
-      const int r = 32 * (warp - kDecodeV) + lane;
-      Seg g;
-      Span span;
-      int s = 0, t = 0;
-      Row4<D> row, next;
-      auto fetch = [&](int j) -> bool {
-        if (j == 0 || t == g.t1) {
-          if (!next_seg(s++, g)) return false;
-          span = span_of<kWin>(A, g.L, g.T);
-          t = g.t0;
-        }
-        const int st = j % kStages;
-        if (misc[2] || !mbar_wait(&bFull[st], (j / kStages) & 1)) return false;
-        const uint8_t* raw = sm + Ly::kRaw + st * Ly::kStage + P * Ly::kUnit;
-        next.load(raw + codes_at(r), 16 * P, raw + scales_at(r));
-        const int key = span.key0(t++) + r;
-        if (key >= g.L || (kWin && key >= span.hole && key < span.lo)) {  // seen by no row: zeros
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) next.code[c] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c) next.scale[c] = 0;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bEmpty[st]);
-        return true;
-      };
-      ok = fetch(0);
-      for (int j = 0; j < cnt && ok; ++j) {
-        row = next;
-        if ((j + 1 < cnt && !fetch(j + 1)) || !used_before(kBarPV, j)) { ok = false; break; }
-        uint8_t* v = sm + Ly::kV + (j & 1) * Ly::kTile;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t w[16];
-          row.chunk(c, w);
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            *reinterpret_cast<uint4*>(v + (c >> 1) * 16384 + sw128_offset(r, 4 * (c & 1) + x)) =
-                make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kBarVFull + (j & 1)]);
-      }
-    } else if (warp == kLoader) {
+    } else if (warp == Ro::kLoader) {
       // ------------------------------------------------------------ loader
       const uint64_t policy = A.RB == 1 ? policy_evict_first() : policy_evict_last();
       const int pshift = 7 - A.page_shift, pp = 1 << pshift;  // pages of a tile
       const uint32_t page_bytes = 2 * P * Ly::kUnit;
       int64_t at = start[1], pos = begin;  // first tile of request b, of the next segment
       const int64_t hi = begin + cnt;
-      int b = (int)start[0], s = 0, t = 0;
-      Seg g = {};
-      Span span = {};
-      int base = 0, ids = 0, ahead = 0;  // lane x holds the page of entry base + x, and of base + 32 + x (along the line)
+      int b = (int)start[0], s = 0;
+      // A segment is opened while the tiles of the one before are loaded: its Q is converted meanwhile.
+      struct Open {
+        Seg g;
+        Span span;
+        int base, ids, ahead;  // lane x holds the page of entry base + x, and of base + 32 + x (along the line)
+      };
+      Open cur = {}, next = {};
       auto publish = [&](const Seg& g) -> bool {
         const int slot = s % kSegSlots;
-        if (misc[2] || !mbar_wait_idle(&bars[kBarSegEmpty + slot], ((s / kSegSlots) & 1) ^ 1, kIdleNs)) return false;
+        if (misc[2] || !wait4(&bars[kBarSegEmpty + slot], ((s / kSegSlots) & 1) ^ 1)) return false;
         if (lane == 0) {
           segs[slot] = g;
           mbar_arrive(&bars[kBarSegFull + slot]);
         }
+        ++s;
         return true;
       };
       // -1: not read
-      auto entry = [&](int p) {
-        p = (span.tile(p >> pshift) << pshift) + (p & (pp - 1));
-        if (p >= (g.L + P - 1) >> A.page_shift || (kWin && span.gone(p, A.page_shift))) return -1;
-        const int page = A.table[(int64_t)g.b * A.max_pages + p];
+      auto entry = [&](const Open& o, int p) {
+        p = (o.span.tile(p >> pshift) << pshift) + (p & (pp - 1));
+        if (p >= (o.g.L + P - 1) >> A.page_shift || (kWin && o.span.gone(p, A.page_shift))) return -1;
+        const int page = A.table[(int64_t)o.g.b * A.max_pages + p];
         if ((unsigned)page < (unsigned)A.num_pages) return page;
         atomicCAS(A.err, 0, (int)kErrIndex);  // not followed: an existing page stands in, the call has failed
         return 0;
       };
-      auto open = [&]() -> bool {
+      // the segment from `pos` on, or the end's mark
+      auto open = [&](Open& o) -> bool {
+        Seg& g = o.g;
+        g.b = -1;
+        if (pos >= hi) return publish(g);
         bool bad;
         int64_t tiles = 0;
         for (; b < A.B; ++b) {
           const bool live = request(A, b, g.L, g.T, bad);
-          span = span_of<kWin>(A, g.L, g.T);
-          tiles = live ? (int64_t)items * span.tiles : 0;
+          o.span = span_of<kWin>(A, g.L, g.T);
+          tiles = live ? (int64_t)items * o.span.tiles : 0;
           if (pos < at + tiles) break;
           at += tiles;
         }
         if (b >= A.B) return false;
         g.b = b;
-        g.tiles = span.tiles;
+        g.tiles = o.span.tiles;
         const int item = (int)quotient(pos - at, g.tiles);
         g.kvh = item / A.RB;
         g.rb = item - g.kvh * A.RB;
@@ -442,99 +473,113 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
         g.r0 = g.t0;
         g.r1 = g.t1;
         pos += g.t1 - g.t0;
-        t = g.t0;
-        base = g.t0 << pshift;
         if (!publish(g)) return false;
-        ++s;
-        ids = entry(base + lane);
-        ahead = entry(base + 32 + lane);
+        o.base = g.t0 << pshift;
+        o.ids = entry(o, o.base + lane);
+        o.ahead = entry(o, o.base + 32 + lane);
         return true;
       };
+      ok = open(next);
+      int t = 0;
       for (int j = 0; j < cnt && ok; ++j) {
-        if ((s == 0 || t == g.t1) && !open()) { ok = false; break; }
-        int off = (t << pshift) - base;
-        if (off >= 32) {
-          base += 32;
-          off -= 32;
-          ids = ahead;
-          ahead = entry(base + 32 + lane);
+        if (j == 0 || t == cur.g.t1) {
+          cur = next;
+          t = cur.g.t0;
+          if (!open(next)) { ok = false; break; }
         }
-        const int page = __shfl_sync(0xFFFFFFFFu, ids, (off + lane) & 31);
+        int off = (t << pshift) - cur.base;
+        if (off >= 32) {
+          cur.base += 32;
+          off -= 32;
+          cur.ids = cur.ahead;
+          cur.ahead = entry(cur, cur.base + 32 + lane);
+        }
+        const int page = __shfl_sync(0xFFFFFFFFu, cur.ids, (off + lane) & 31);
         const bool mine = lane < pp && page >= 0;
         const uint32_t copies = __popc(__ballot_sync(0xFFFFFFFFu, mine));
         const int st = j % kStages;
-        if (misc[2] || !mbar_wait_idle(&bEmpty[st], ((j / kStages) & 1) ^ 1, kIdleNs)) { ok = false; break; }
-        if (lane == 0) mbar_arrive_expect_tx(&bFull[st], copies * page_bytes);
+        if (!wait4(&bEmpty[st], ((j / kStages) & 1) ^ 1)) { ok = false; break; }
+        if (lane == 0) {
+          const int key0 = cur.span.key0(t), z = min(128, cur.g.L - key0);
+          const int x = max(0, cur.span.hole - key0), y = min(128, cur.span.lo - key0);
+          infos[st] = make_int4(x, y, z, z < 128 || (kWin && x < y));
+          mbar_arrive_expect_tx(&bFull[st], copies * page_bytes);
+        }
         __syncwarp();
         if (mine)
           bulk_load(sm + Ly::kRaw + st * Ly::kStage + lane * page_bytes,
-                    X.data + ((int64_t)page * A.Hkv + g.kvh) * page_bytes, page_bytes, &bFull[st], policy);
+                    X.data + ((int64_t)page * A.Hkv + cur.g.kvh) * page_bytes, page_bytes, &bFull[st], policy);
         __syncwarp();
         if (lane == 0) misc[3] = j + 1;
         ++t;
       }
-      Seg end;
-      end.b = -1;
-      if (ok) ok = publish(end);
-    } else if (warp == kIssuer) {
-      // ------------------------------------------------------------ products
-      constexpr uint32_t id_qk = idesc_f16_f32(128, kN, false, false);
-      constexpr uint32_t id_pv = idesc_f16_f32(128, kN, true, true);  // (d = 64: rows 64 .. of O^T hold anything)
+    } else if (warp == Ro::kIssueQK) {
+      // ------------------------------------------------------------ scores.  (A warp of their own: behind a product
+      // with V that waits for its weights, a group's next scores would come a whole chain later.)
+      constexpr uint32_t id = idesc_f16_f32(128, kN, false, false);
       const uint64_t dq = sdesc_sw128(smem_u32(sm + Ly::kQ), 16, 1024);
-      const uint64_t dv = sdesc_sw128(smem_u32(sm + Ly::kV), 16384, 1024);
-      const uint64_t dp = sdesc_sw128(smem_u32(sm + Ly::kP), 16384, 1024);
       const bool leader = elect_one();
-      auto issue_pv = [&](int j, bool first) -> bool {
-        if (!done(kBarPFull, j) || !done(kBarVFull, j)) return false;
-        tc_fence_after();
-        if (leader) {
-          const uint64_t v = dv + (uint64_t)((j & 1) * (Ly::kTile >> 4)), p = dp + (uint64_t)((j & 1) * (Ly::kPTile >> 4));
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ss(tmem + kColO + 64 * (j & 1), v + (uint64_t)(kk * 128), p + (uint64_t)(kk * 128), id_pv, (!first || kk > 0) ? 1u : 0u);
-          mma_commit(&bars[kBarPV + (j & 1)]);
-        }
-        __syncwarp();
-        return true;
-      };
       int j = 0;
-      bool first = true;  // tile j - 1 is the first of its group in the segment
       Seg g;
       for (int s = 0; j < cnt && next_seg(s, g); ++s) {
-        if (!mbar_wait(&bars[kBarQFull + (s & 1)], (s >> 1) & 1)) { ok = false; break; }
+        if (!wait4(&bars[kBarQFull + (s & 1)], (s >> 1) & 1)) { ok = false; break; }
+        const uint64_t q = dq + (uint64_t)((s & 1) * (Ly::kQTile >> 4));
         for (int t = g.t0; t < g.t1; ++t, ++j) {
-          if (misc[2] || !done(kBarKFull, j) || !used_before(kBarSEmpty, j)) { ok = false; break; }
+          if (!done(kBarKFull, j) || !used_before(kBarSEmpty, j)) { ok = false; break; }
           tc_fence_after();
           if (leader) {
-            const uint64_t q = dq + (uint64_t)((s & 1) * (Ly::kQTile >> 4));
-#pragma unroll
+#pragma unroll 2
             for (int kk = 0; kk < D / 16; ++kk)
               mma_bf16_ts(tmem + kColS + 64 * (j & 1), tmem + kColK + 64 * (j & 1) + 8 * kk,
-                          q + (uint64_t)((kk >> 2) * (kBlock * 8) + (kk & 3) * 2), id_qk, kk > 0 ? 1u : 0u);
+                          q + (uint64_t)((kk >> 2) * (kBlock * 8) + (kk & 3) * 2), id, kk > 0 ? 1u : 0u);
             mma_commit(&bars[kBarQK + (j & 1)]);
             if (t + 1 == g.t1) mma_commit(&bars[kBarQEmpty + (s & 1)]);
           }
           __syncwarp();
-          if (j > 0 && !issue_pv(j - 1, first)) { ok = false; break; }
-          first = t - g.t0 < 2;
         }
         if (!ok) break;
       }
-      if (ok && !issue_pv(cnt - 1, first)) ok = false;
-    } else {
+    } else if (warp == Ro::kIssuePV) {
+      // ------------------------------------------------------------ products with V
+      constexpr uint32_t id = idesc_f16_f32(128, kN, true, true);  // (d = 64: rows 64 .. of O^T hold anything)
+      const uint64_t dv = sdesc_sw128(smem_u32(sm + Ly::kV), 16384, 1024);
+      const uint64_t dp = sdesc_sw128(smem_u32(sm + Ly::kP), 16384, 1024);
+      const bool leader = elect_one();
+      int j = 0;
+      Seg g;
+      for (int s = 0; j < cnt && next_seg(s, g); ++s) {
+        if (!used_before(kBarOFree, s)) { ok = false; break; }
+        const uint32_t o = tmem + kColO + 128 * (s & 1);
+        for (int t = g.t0; t < g.t1; ++t, ++j) {
+          if (!done(kBarVFull, j) || !done(kBarPFull, j)) { ok = false; break; }
+          tc_fence_after();
+          if (leader) {
+            const bool more = t - g.t0 >= 2;  // not the first of its group in the segment
+            const uint64_t v = dv + (uint64_t)((j & 1) * (Ly::kTile >> 4)), p = dp + (uint64_t)((j & 1) * (Ly::kPTile >> 4));
+#pragma unroll 2
+            for (int kk = 0; kk < 8; ++kk)
+              mma_bf16_ss(o + 64 * (j & 1), v + (uint64_t)(kk * 128), p + (uint64_t)(kk * 128), id, (more || kk > 0) ? 1u : 0u);
+            mma_commit(&bars[kBarPV + (j & 1)]);
+            if (t + 1 == g.t1) mma_commit(&bars[kBarODone + (s & 1)]);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+    } else if (warp == Ro::kQ) {
       // ------------------------------------------------------------ Q to fp16
       constexpr int kPer = D / 32;
-      if (warp == kQWarp && lane == 0) note_cut<false, kCtas, kWin>(A, W, blockIdx.x, (int)start[0], start[1]);
+      if (lane == 0) note_cut<false, kCtas, kWin>(A, W, blockIdx.x, (int)start[0], start[1]);
       __syncwarp();
       Seg g;
       for (int s = 0; next_seg(s, g); ++s) {
-        if (!mbar_wait_idle(&bars[kBarQEmpty + (s & 1)], ((s >> 1) & 1) ^ 1, kIdleNs)) { ok = false; break; }
+        if (!wait4(&bars[kBarQEmpty + (s & 1)], ((s >> 1) & 1) ^ 1)) { ok = false; break; }
         uint8_t* to = sm + Ly::kQ + (s & 1) * Ly::kQTile;
         float* f = rowf + (s & 1) * kBlock;
         const int64_t q0 = (int64_t)(g.b * A.Hq + g.kvh * (A.Hq / A.Hkv)) * A.n + kBlock * g.rb;
         const int ch = kPer * lane;
 #pragma unroll 4
-        for (int r = warp - kQWarp; r < kN; r += 2) {
+        for (int r = 0; r < kR; ++r) {
           const int rr = kBlock * g.rb + r;
           if (rr >= A.R || rr % A.n >= g.T) {  // no row: whatever its column holds stays there
             if (lane == 0) f[r] = 0x1p-126f;
@@ -564,36 +609,90 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[kBarQFull + (s & 1)]);
       }
+    } else {
+      // ------------------------------------------------------------ output: both groups' O joined; thread = channel
+      const int w4 = warp & 3, tid = 32 * w4 + lane;
+      const uint32_t lane_base = (uint32_t)(32 * w4) << 16;
+      int outs = 0, j0 = 0;
+      Seg g;
+      for (int s = 0; j0 < cnt && next_seg(s, g); ++s) {
+        const int par = s & 1, set = par * kBlock, tiles = g.t1 - g.t0;
+        float* fo = rows + kRowFo + 2 * set;
+        const bool whole = g.r0 == 0 && g.r1 == g.tiles;
+        const int full = min(kBlock, A.R), width = min(kBlock, A.R - kBlock * g.rb);
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (g.r0 > 0 ? 0 : 1);
+        const int64_t grow = (int64_t)(g.b * A.Hq + g.kvh * (A.Hq / A.Hkv)) * A.n + kBlock * g.rb;
+        if (!done(kBarSums, s)) { ok = false; break; }
+        if (tid < kR) {
+          // both groups' sums and products at the larger reference
+          const float* last = rows + kRowLast + 2 * set + tid;
+          const float m0 = last[0], m1 = last[kBlock], m = fmaxf(m0, m1), ref = m == -INFINITY ? 0.f : m;
+          const float f0 = ex2(m0 - ref), f1 = ex2(m1 - ref);
+          const float* x = rows + kRowSums + 8 * set + tid;
+          const float s0 = (x[0] + x[kBlock]) + (x[2 * kBlock] + x[3 * kBlock]);
+          const float s1 = (x[4 * kBlock] + x[5 * kBlock]) + (x[6 * kBlock] + x[7 * kBlock]);
+          const float sum = f0 * s0 + f1 * s1;
+          const bool some = !(sum == 0.f);
+          const float inv = whole ? (some ? X.v_scale / sum : 0.f) : X.v_scale;
+          fo[tid] = f0 * inv;
+          fo[kBlock + tid] = f1 * inv;
+          if (rowi[set + tid] >= 0) {
+            // (sums are 2^kTop times those of the reference)
+            if (!whole) A.part_ml[slot * full + tid] = make_float2(m - kTop, sum);
+            else if (A.lse) A.lse[grow + tid] = some ? (m - kTop + __log2f(sum)) * 0.69314718055994531f : -INFINITY;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kBarOut]);
+        if (!wait4(&bars[kBarOut], outs++ & 1) || !done(kBarODone, s)) { ok = false; break; }
+        tc_fence_after();
+        // (a segment of one tile has one group's products)
+        const int end = (j0 + tiles - 1) & 1;
+        const bool two = tiles > 1;
+        const uint32_t o0 = tmem + lane_base + kColO + 128 * par;
+        if (D == 128 || w4 < 2) {
+#pragma unroll 1
+          for (int c = 0; c < kR && c < width; c += 8) {
+            uint32_t o[8], q[8];
+            tmem_ld8(o0 + 64 * end + c, o);
+            tmem_ld8(o0 + 64 * (end ^ 1) + c, q);
+            tmem_ld_wait();
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              const int r = c + x;
+              if (rowi[set + r] < 0) continue;
+              float y = __uint_as_float(o[x]) * fo[end * kBlock + r];
+              if (two) y = fmaf(__uint_as_float(q[x]), fo[(end ^ 1) * kBlock + r], y);
+              if (whole) A.o[(grow + r) * D + tid] = __float2bfloat16(y);
+              else reinterpret_cast<float*>(A.part + slot * (D / 4) * full + (int64_t)(tid >> 2) * width + r)[tid & 3] = y;
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kBarOFree + par]);
+        j0 += tiles;
+      }
     }
   } else {
-    if (kN == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-    if (kN == 32) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    if (kR == 16) asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    if (kR == 32) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    if (kR == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
     // ------------------------------------------------------------ softmax group H: the part's tiles j = H mod 2; thread = key
     const int H = warp >> 2, w4 = warp & 3, tid = threadIdx.x & 127;
-    const uint32_t lane_base = (uint32_t)(32 * w4) << 16;
-    int* rowi = reinterpret_cast<int*>(rowf + 2 * kBlock);  // [2][kBlock] drafted token of the row, -1: no row
-    int* rowend = rowi + 2 * kBlock;                        // [2][kBlock] kWin: end of the keys behind its window
-    float* rows = reinterpret_cast<float*>(rowend + 2 * kBlock);
-    float* nref = rows + H * kBlock;                        // [2] kTop - reference
-    float* alpha = rows + (2 + H) * kBlock;                 // [2] factors of a raise
-    float* last = rows + 4 * kBlock;                        // [2] references at the segment's end
-    float* fo = rows + 6 * kBlock;                          // [2] factors of O
-    float* wmax = rows + (8 + 4 * H) * kBlock;              // [2][4] maxima
-    float* wl = rows + 16 * kBlock;                         // [2][4] sums
-    int syncs = 0, boths = 0;
+    const uint32_t lane_base = (uint32_t)(32 * w4) << 16, tS = tmem + lane_base + kColS + 64 * H;
+    float* nref = rows + kRowRef + H * kBlock;
+    float* alpha = rows + kRowAlpha + H * kBlock;
+    float* wmax = rows + kRowMax + 4 * H * kBlock;
+    int syncs = 0;
     auto group_arrive = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kBarGroup + H]);
     };
-    auto group_wait = [&]() { return mbar_wait(&bars[kBarGroup + H], syncs++ & 1); };
+    auto group_wait = [&]() { return wait4(&bars[kBarGroup + H], syncs++ & 1); };
     auto group_sync = [&]() {
       group_arrive();
       return group_wait();
-    };
-    auto both_sync = [&]() {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kBarBoth]);
-      return mbar_wait(&bars[kBarBoth], boths++ & 1);
     };
     int j0 = 0;  // the segment's first tile
     Seg g;
@@ -601,56 +700,64 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
       const Span span = span_of<kWin>(A, g.L, g.T);
       const int C = g.L - g.T, set = (s & 1) * kBlock;
       float m_used = -INFINITY;  // of row `tid`
-      if (tid < kN) {
+      if (!used_before(kBarOFree, s)) { ok = false; break; }  // the rows' numbers of segment s - 2 have been read
+      if (tid < kR) {
         const int rr = kBlock * g.rb + tid, i = rr % A.n;
         rowi[set + tid] = rr < A.R && i < g.T ? i : -1;
         if (kWin) rowend[set + tid] = behind(A, g.b, i, C);
       }
-      uint64_t l[kN / 2];  // sums of this key's lane, rows in pairs
+      uint64_t l[kR / 2];  // sums of this key's lane, rows in pairs
 #pragma unroll
-      for (int r = 0; r < kN / 2; ++r) l[r] = pk2(0.f, 0.f);
-      if (!mbar_wait(&bars[kBarQFull + (s & 1)], (s >> 1) & 1) || !group_sync()) { ok = false; break; }
+      for (int r = 0; r < kR / 2; ++r) l[r] = pk2(0.f, 0.f);
+      if (!wait4(&bars[kBarQFull + (s & 1)], (s >> 1) & 1) || !group_sync()) { ok = false; break; }
       const float* f = rowf + set;
+      const uint32_t tO = tmem + lane_base + kColO + 128 * (s & 1) + 64 * H;
       const int tiles = g.t1 - g.t0, first = (j0 ^ H) & 1;  // the group's first tile of them
       for (int x = first; x < tiles; x += 2) {
         const int t = g.t0 + x, j = j0 + x;
         const int key0 = span.key0(t), key = key0 + tid;
         const bool masked = key0 + 128 > C || (kWin && key0 + 128 > A.sink && key0 < (int64_t)C + A.n - A.window);
-        if (misc[2] || !done(kBarQK, j)) { ok = false; break; }
+        if (!done(kBarQK, j)) { ok = false; break; }
         tc_fence_after();
-        uint32_t see[(kN + 31) / 32];  // masked: rows that see this key
+        uint32_t see[(kR + 31) / 32];  // masked: rows that see this key
         if (masked) {
           const int rel = key - C;
 #pragma unroll
-          for (int x = 0; x < (kN + 31) / 32; ++x) see[x] = 0;
+          for (int x = 0; x < (kR + 31) / 32; ++x) see[x] = 0;
 #pragma unroll 1
-          for (int r = 0; r < kN; ++r) {
+          for (int r = 0; r < kR; ++r) {
             const int i = rowi[set + r];
             bool in = key < g.L;
             if (in && rel >= 0)
               in = A.mask ? i >= 0 && (__ldg(A.mask + g.b * A.mask_stride + (int64_t)i * A.words + (rel >> 5)) >> (rel & 31) & 1u)
                           : rel <= i;
             if (kWin && key >= A.sink && key < rowend[set + r]) in = false;
-            if (kN > 32 && r >= 32) see[(kN - 1) / 32] |= (in ? 1u : 0u) << (r & 31);
+            if (kR > 32 && r >= 32) see[(kR - 1) / 32] |= (in ? 1u : 0u) << (r & 31);
             else see[0] |= (in ? 1u : 0u) << (r & 31);
           }
         }
-        float y[kN];
-        auto load_scores = [&]() {  // -inf where a row does not see the key
+        // kR = 64: scores by halves, read from TMEM again for each pass (all of them and the sums in registers spill)
+        constexpr int kC = kR == 64 ? 32 : kR;
+        float y[kC];
+        auto load_scores = [&](int c0) {  // of rows c0 .., -inf where a row does not see the key
 #pragma unroll
-          for (int c = 0; c < kN; c += 16)
-            tmem_ld16(tmem + lane_base + kColS + 64 * (j & 1) + c, reinterpret_cast<uint32_t*>(y) + c);
+          for (int c = 0; c < kC; c += 16) {
+            uint32_t* u = reinterpret_cast<uint32_t*>(y) + c;
+            if constexpr (kC == 8) tmem_ld8(tS + c0 + c, *reinterpret_cast<uint32_t(*)[8]>(u));
+            else tmem_ld16(tS + c0 + c, u);
+          }
           tmem_ld_wait();
           if (masked)
 #pragma unroll
-            for (int r = 0; r < kN; ++r) y[r] = (see[r >> 5] >> (r & 31) & 1u) ? y[r] : -INFINITY;
+            for (int r = 0; r < kC; ++r) y[r] = (see[c0 >> 5] >> (r & 31) & 1u) ? y[r] : -INFINITY;
         };
         // log2 of the weights; returns the largest
-        auto scale_scores = [&]() -> float {
+        auto scale_scores = [&](int c0) -> float {
           float top = -INFINITY;
 #pragma unroll
-          for (int r = 0; r < kN; r += 4) {
-            const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(f + r), b = *reinterpret_cast<const ulonglong2*>(nref + r);
+          for (int r = 0; r < kC; r += 4) {
+            const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(f + c0 + r);
+            const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(nref + c0 + r);
             up2(fma2(pk2(y[r], y[r + 1]), a.x, b.x), y[r], y[r + 1]);
             up2(fma2(pk2(y[r + 2], y[r + 3]), a.y, b.y), y[r + 2], y[r + 3]);
             top = max3f(max3f(y[r], y[r + 1], y[r + 2]), y[r + 3], top);
@@ -659,34 +766,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
         };
         auto exponentials = [&]() {
 #pragma unroll
-          for (int r = 0; r < kN; ++r) y[r] = ex2(y[r]);
+          for (int r = 0; r < kC; ++r) y[r] = ex2(y[r]);
         };
-        load_scores();
         bool far = x == first;
         if (!far) {
           // Does one of the four warps' scores pass its reference too far?  The exponentials are under way meanwhile.
-          const float top = scale_scores();
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < kR; c += kC) {
+            load_scores(c);
+            top = fmaxf(top, scale_scores(c));
+          }
           const int at = syncs;
           if (__any_sync(0xFFFFFFFFu, top > kTop + kRaise) && lane == 0) misc[4 + 2 * H + (at & 1)] = at;
           group_arrive();
-          exponentials();
+          if (kC == kR) exponentials();
           if (!group_wait()) { ok = false; break; }
           far = misc[4 + 2 * H + (at & 1)] == (uint32_t)at;
-          if (far) load_scores();
         }
         if (far) {
           // the rows' maxima over the tile, new references, and what was summed comes to them
-          float mine[(kN + 31) / 32] = {};
 #pragma unroll
-          for (int r = 0; r < kN; ++r) {
-            const float m = warp_max(y[r] * f[r]);
-            if (lane == (r & 31)) mine[r >> 5] = m;
+          for (int c = 0; c < kR; c += kC) {
+            load_scores(c);
+            float mine = 0.f;
+#pragma unroll
+            for (int r = 0; r < kC; ++r) {
+              const float m = warp_max(y[r] * f[c + r]);
+              if (lane == r) mine = m;
+            }
+            if (lane < kC) wmax[w4 * kBlock + c + lane] = mine;
           }
-#pragma unroll
-          for (int y = 0; y < (kN + 31) / 32; ++y)
-            if (32 * y + lane < kN) wmax[w4 * kBlock + 32 * y + lane] = mine[y];
           if (!group_sync()) { ok = false; break; }
-          if (tid < kN) {
+          if (tid < kR) {
             float m = m_used;
 #pragma unroll
             for (int w = 0; w < 4; ++w) m = fmaxf(m, wmax[w * kBlock + tid]);
@@ -697,105 +809,75 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
           if (!group_sync()) { ok = false; break; }
           if (x > first) {
 #pragma unroll
-            for (int r = 0; r < kN; r += 2) l[r / 2] = mul2(l[r / 2], pk2(alpha[r], alpha[r + 1]));
+            for (int r = 0; r < kR; r += 2) l[r / 2] = mul2(l[r / 2], pk2(alpha[r], alpha[r + 1]));
             if (!done(kBarPV, j - 2)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < kN; c += 16) {
-              uint32_t o[16];
-              tmem_ld16(tmem + lane_base + kColO + 64 * H + c, o);
+            for (int c = 0; c < kR; c += 8) {
+              uint32_t o[8];
+              tmem_ld8(tO + c, o);
               tmem_ld_wait();
 #pragma unroll
-              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha[c + x]);
-              tmem_st16(tmem + lane_base + kColO + 64 * H + c, o);
+              for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha[c + k]);
+              tmem_st8(tO + c, o);
             }
             tmem_st_wait();
           }
-          scale_scores();
-          exponentials();
-        }
-        tc_fence_before();  // the scores are in registers
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kBarSEmpty + (j & 1)]);
-        if (!used_before(kBarPV, j)) { ok = false; break; }
-        uint8_t* p = sm + Ly::kP + (j & 1) * Ly::kPTile;
-#pragma unroll
-        for (int r = 0; r < kN; r += 8) {
-          uint32_t w[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            w[x] = pack_f16x2(y[r + 2 * x], y[r + 2 * x + 1]);
-            l[r / 2 + x] = add2(l[r / 2 + x], pk2(y[r + 2 * x], y[r + 2 * x + 1]));
+          if (kC == kR) {
+            scale_scores(0);
+            exponentials();
           }
-          *reinterpret_cast<uint4*>(p + sw128_offset(tid, r >> 3)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (kC == kR) {
+          tc_fence_before();  // the scores are in registers
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[kBarSEmpty + H]);
+        }
+        if (!used_before(kBarPV, j)) { ok = false; break; }
+        uint8_t* p = sm + Ly::kP + H * Ly::kPTile;
+#pragma unroll
+        for (int c = 0; c < kR; c += kC) {
+          if (kC < kR) {
+            load_scores(c);
+            scale_scores(c);
+            exponentials();
+          }
+#pragma unroll
+          for (int r = 0; r < kC; r += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              w[k] = pack_f16x2(y[r + 2 * k], y[r + 2 * k + 1]);
+              uint64_t& sum = l[(c + r) / 2 + k];
+              sum = add2(sum, pk2(y[r + 2 * k], y[r + 2 * k + 1]));
+            }
+            *reinterpret_cast<uint4*>(p + sw128_offset(tid, (c + r) >> 3)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        if (kC < kR) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[kBarSEmpty + H]);
         }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kBarPFull + (j & 1)]);
+        if (lane == 0) mbar_arrive(&bars[kBarPFull + H]);
       }
       if (!ok) break;
 
       // ---- the segment's end: row sums over lanes and warps, then O^T (thread = channel)
       if (lane == 0) mbar_arrive(&bars[kBarQEmpty + (s & 1)]);  // (behind the last barrier of the group: all have read f)
-      float sums[kN];
+      float sums[kR];
 #pragma unroll
-      for (int r = 0; r < kN; r += 2) up2(l[r / 2], sums[r], sums[r + 1]);
-      lane_sums<kN, 16>(sums, lane);
-      float* own = wl + (4 * H + w4) * kBlock;
-      if constexpr (kN == 64) *reinterpret_cast<float2*>(own + 2 * lane) = make_float2(sums[0], sums[1]);
-      else if (kN == 32 || !(lane & 1)) own[kN == 32 ? lane : lane >> 1] = sums[0];
-      if (tid < kN) last[H * kBlock + tid] = m_used;
-      if (!both_sync()) { ok = false; break; }
-      const bool whole = g.r0 == 0 && g.r1 == g.tiles;
-      const int full = min(kBlock, A.R), width = min(kBlock, A.R - kBlock * g.rb);
-      const int64_t slot = 2 * (int64_t)blockIdx.x + (g.r0 > 0 ? 0 : 1);
-      const int64_t grow = (int64_t)(g.b * A.Hq + g.kvh * (A.Hq / A.Hkv)) * A.n + kBlock * g.rb;
-      if (H == 0 && tid < kN) {
-        // both groups' sums and products at the larger reference
-        const float m0 = last[tid], m1 = last[kBlock + tid], m = fmaxf(m0, m1), ref = m == -INFINITY ? 0.f : m;
-        const float f0 = ex2(m0 - ref), f1 = ex2(m1 - ref);
-        const float* x = wl + tid;
-        const float s0 = (x[0] + x[kBlock]) + (x[2 * kBlock] + x[3 * kBlock]);
-        const float s1 = (x[4 * kBlock] + x[5 * kBlock]) + (x[6 * kBlock] + x[7 * kBlock]);
-        const float sum = f0 * s0 + f1 * s1;
-        const bool some = !(sum == 0.f);
-        const float inv = whole ? (some ? X.v_scale / sum : 0.f) : X.v_scale;
-        fo[tid] = f0 * inv;
-        fo[kBlock + tid] = f1 * inv;
-        if (rowi[set + tid] >= 0) {
-          // (sums are 2^kTop times those of the reference)
-          if (!whole) A.part_ml[slot * full + tid] = make_float2(m - kTop, sum);
-          else if (A.lse) A.lse[grow + tid] = some ? (m - kTop + __log2f(sum)) * 0.69314718055994531f : -INFINITY;
-        }
-      }
-      // the last products of both groups (a segment of one tile has one of them)
-      const int end = j0 + tiles - 1;
-      const bool two = tiles > 1;
-      if (!both_sync() || !done(kBarPV, end) || (two && !done(kBarPV, end - 1))) { ok = false; break; }
-      tc_fence_after();
-      const uint32_t oA = tmem + lane_base + kColO + 64 * (end & 1), oB = tmem + lane_base + kColO + 64 * (~end & 1);
-      const float *fA = fo + kBlock * (end & 1), *fB = fo + kBlock * (~end & 1);
-      if (D == 128 || w4 < 2) {
-#pragma unroll 1
-        for (int c = 8 * H; c < kN && c < width; c += 16) {  // the groups take 8 rows in turn
-          uint32_t o[8], q[8];
-          tmem_ld8(oA + c, o);
-          tmem_ld8(oB + c, q);
-          tmem_ld_wait();
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const int r = c + x;
-            if (rowi[set + r] < 0) continue;
-            float y = __uint_as_float(o[x]) * fA[r];
-            if (two) y = fmaf(__uint_as_float(q[x]), fB[r], y);
-            if (whole) A.o[(grow + r) * D + tid] = __float2bfloat16(y);
-            else reinterpret_cast<float*>(A.part + slot * (D / 4) * full + (int64_t)(tid >> 2) * width + r)[tid & 3] = y;
-          }
-        }
-      }
-      tc_fence_before();
-      if (!both_sync()) { ok = false; break; }  // O has been read
+      for (int r = 0; r < kR; r += 2) up2(l[r / 2], sums[r], sums[r + 1]);
+      lane_sums<kR, 16>(sums, lane);
+      float* own = rows + kRowSums + 8 * set + (4 * H + w4) * kBlock;
+      if constexpr (kR == 64) *reinterpret_cast<float2*>(own + 2 * lane) = make_float2(sums[0], sums[1]);
+      else if (lane % (32 / kR) == 0) own[lane / (32 / kR)] = sums[0];
+      if (tid < kR) rows[kRowLast + 2 * set + H * kBlock + tid] = m_used;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kBarSums + (s & 1)]);
       j0 += tiles;
     }
   }
@@ -808,12 +890,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attn_kernel(const __grid_cons
   __syncthreads();
   if (misc[2]) {
     // A role gave up: copies and products that nobody waited for end before the CTA's shared memory and TMEM go.
-    if (warp == kIssuer) {
-      if (elect_one()) mma_commit(&bars[kBarDrain]);
-      mbar_wait(&bars[kBarDrain], 0, kDrainNs);
-    } else if (warp == kLoader) {
+    if (warp == Ro::kIssueQK || warp == Ro::kIssuePV) {
+      uint64_t* drained = &bars[kBarDrain + (warp == Ro::kIssueQK ? 0 : 1)];
+      if (elect_one()) mma_commit(drained);
+      wait4(drained, 0, kDrainPolls);
+    } else if (warp == Ro::kLoader) {
       const int asked = (int)misc[3];
-      for (int x = max(0, asked - kStages); x < asked; ++x) mbar_wait(&bFull[x % kStages], (x / kStages) & 1, kDrainNs);
+      for (int x = max(0, asked - kStages); x < asked; ++x) wait4(&bFull[x % kStages], (x / kStages) & 1, kDrainPolls);
     }
     __syncthreads();
   }
@@ -836,12 +919,12 @@ Ws4 kv4_ws(const msa_shape& s) {
   return w;
 }
 
-template <int D, int kN, bool kWin>
+template <int D, int kR, bool kWin>
 msa_status launch(const Kv4Args& a, bool join, cudaStream_t stream) {
-  auto kern = kv4_attn_kernel<D, kN, kWin>;
+  auto kern = kv4_attn_kernel<D, kR, kWin>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay4<D>::kAlloc) != cudaSuccess)
     return MSA_ERR_CUDA;
-  kern<<<kCtas, kThreads, Lay4<D>::kAlloc, stream>>>(a);
+  kern<<<kCtas, Roles<kR>::kThreads, Lay4<D>::kAlloc, stream>>>(a);
   note_launch();
   if (cudaGetLastError() != cudaSuccess) return MSA_ERR_CUDA;
   return join ? launch_join<D, kCtas, kBlock>(a.t, stream) : MSA_OK;
@@ -849,6 +932,7 @@ msa_status launch(const Kv4Args& a, bool join, cudaStream_t stream) {
 
 template <int D, bool kWin>
 msa_status launch_rows(const Kv4Args& a, bool join, cudaStream_t stream) {
+  if (a.t.R <= 8) return launch<D, 8, kWin>(a, join, stream);
   if (a.t.R <= 16) return launch<D, 16, kWin>(a, join, stream);
   if (a.t.R <= 32) return launch<D, 32, kWin>(a, join, stream);
   return launch<D, 64, kWin>(a, join, stream);
