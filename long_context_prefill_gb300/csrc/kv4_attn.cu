@@ -24,19 +24,20 @@
 //
 // Split: as tree.cu's (tree.cuh), one part of the line of tiles per CTA.
 //
-// A CTA (20 warps, one CTA per SM):
-//   warps 0-7    softmax (thread = key = TMEM lane) in two groups that take the
-//                tiles in turn, each with its own references, sums and O: a
-//                tile's chain (scores, exponentials, weights) is latency, two of
-//                them side by side are not.  They are joined at a segment's end
-//   warps 8-11   decode K: shared memory -> registers -> TMEM (two buffers)
-//   warps 12-15  decode V: shared memory -> registers -> shared memory (two
-//                buffers); rows that no query sees become zeros (their pages
-//                may hold anything)
-//   warp 16      loader: walks the part's segments, a bulk copy per page and
-//                head (K and V lie side by side) into a ring of tiles
-//   warp 17      issues the products
-//   warps 18-19  Q of the next segment to fp16
+// A CTA (32 warps, 24 for 64 rows; one CTA per SM):
+//   softmax (8)  thread = key = TMEM lane, in two groups that take the tiles
+//                in turn, each with its own references, sums and O: a tile's
+//                chain (scores, exponentials, weights) is latency, two of them
+//                side by side are not
+//   K (4 or 8)   decode: global memory -> registers -> TMEM (two buffers), a
+//                tile ahead
+//   V (4 or 8)   the same into shared memory (two buffers).  A row that no query
+//                sees becomes zeros (its page may hold anything)
+//   plan (1)     the part's segments
+//   scores (1), products with V (1): the issuers
+//   Q (1)        of the next segment to fp16
+//   output (4)   thread = channel: both groups' O joined, beside the softmax of
+//                the next segment
 #include "kv4.cuh"
 #include "tree.cuh"
 
@@ -45,62 +46,66 @@ namespace msa {
 namespace {
 
 constexpr int kBlock = 64;  // rows of an item
-constexpr int kSegSlots = 4;
+constexpr int kSegSlots = 16;
 
 // Warps of a CTA for blocks of up to kR rows.  With 64 rows the softmax threads' scores and sums leave the others few
 // registers, and the softmax is the longer part: K and V are decoded by one group of warps each.
 template <int kR>
 struct Roles {
-  static constexpr int kGroups = kR == 64 ? 1 : 2;  // of four warps that decode K, and V
-  static constexpr int kK = 8, kV = kK + 4 * kGroups, kLoader = kV + 4 * kGroups, kIssueQK = kLoader + 1,
-                       kIssuePV = kLoader + 2, kQ = kLoader + 3, kOut = kLoader + 4, kThreads = 32 * (kOut + 4);
+  static constexpr int kGroups = kR >= 64 ? 1 : 2;  // of four warps that decode K, and V
+  static constexpr int kK = 8, kV = kK + 4 * kGroups, kPlan = kV + 4 * kGroups, kIssueQK = kPlan + 1,
+                       kIssuePV = kPlan + 2, kQ = kPlan + 3, kOut = kPlan + 4, kThreads = 32 * (kOut + 4);
 };
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColK = 0, kColS = 128, kColO = 256;  // two of 64 columns each; O: [segment parity][group]
+constexpr int kVBufs = 2;
+// TMEM columns of products of N rows: K (four buffers of 64 columns, with N = 64 two), S [2], O [segment parity][group]
+constexpr int k_bufs(int N) { return N == 64 ? 2 : 4; }
+constexpr uint32_t col_s(int N) { return 64 * k_bufs(N); }
+constexpr uint32_t col_o(int N) { return col_s(N) + 2 * N; }
 constexpr float kTop = 7.f, kRaise = 8.f;                // log2: weight of the reference, how far a score may pass it
 
-// [2]: buffers
+// [2] of tiles j: in use j & 1, [4]: j & 3
 enum {
-  kBarKFull = 0,     // [2] K is in TMEM
-  kBarQK = 2,        // [2] scores are in TMEM, K is free
-  kBarSEmpty = 4,    // [2] scores are in registers
-  kBarVFull = 6,     // [2] V is in shared memory
-  kBarPFull = 8,     // [2] weights are in shared memory
-  kBarPV = 10,       // [2] the product is done: V and weights are free
-  kBarQFull = 12,    // [2] Q of the segment
-  kBarQEmpty = 14,   // [2] its products are done, its factors have been read
-  kBarGroup = 16,    // [2] the warps of a softmax group among themselves
-  kBarSums = 18,     // [2] a segment's references and sums are written
-  kBarODone = 20,    // [2] its products are done
-  kBarOFree = 22,    // [2] its O and sums have been read
-  kBarOut = 24,      // the output warps among themselves
-  kBarDrain = 25,    // [2] after giving up: an issuer's products are done
-  kBarSegFull = 27,  // [kSegSlots]
+  kBarKFull = 0,     // [4] K is in TMEM
+  kBarKFree = 4,     // [4] its product is done
+  kBarVFull = 8,     // [2] V is in shared memory
+  kBarQK = 16,       // [2] scores are in TMEM
+  kBarSEmpty = 18,   // [2] scores are in registers
+  kBarPFull = 20,    // [2] weights are in shared memory
+  kBarPV = 22,       // [2] the product with V is done: V and weights are free
+  kBarQFull = 24,    // [2] Q of the segment
+  kBarQEmpty = 26,   // [2] its products are done, its factors have been read
+  kBarGroup = 28,    // [2] the warps of a softmax group among themselves
+  kBarSums = 30,     // [2] a segment's references and sums are written
+  kBarODone = 32,    // [2] its products are done
+  kBarOFree = 34,    // [2] its O and sums have been read
+  kBarOut = 36,      // the output warps among themselves
+  kBarDrain = 37,    // [2] after giving up: an issuer's products are done
+  kBarSegFull = 39,  // [kSegSlots]
   kBarSegEmpty = kBarSegFull + kSegSlots,
-  kBarRing = kBarSegEmpty + kSegSlots  // full[kStages], empty[kStages]
+  kNumBars = kBarSegEmpty + kSegSlots
 };
 
 template <int D>
 struct Lay4 {
   static constexpr int kUnit = D / 2 + D / 16;   // bytes of a token, K or V
-  static constexpr int kStage = 2 * 128 * kUnit;
-  static constexpr int kStages = 4 * (128 / D);
   static constexpr int kTile = 128 * D * 2;      // a tile of V in fp16
   static constexpr int kQTile = kBlock * D * 2;
   static constexpr int kPTile = 128 * kBlock * 2;
-  static constexpr int kV = 0, kP = kV + 2 * kTile, kQ = kP + 2 * kPTile, kRaw = kQ + 2 * kQTile;
-  static constexpr int kSeg = kRaw + kStages * kStage;
+  static constexpr int kV = 0, kP = kV + kVBufs * kTile, kQ = kP + 2 * kPTile, kRaw = kQ + 2 * kQTile;
+  static constexpr int kSlot = 128 * kUnit, kDepth = 4 * (128 / D);  // codes of a tile's K or V; tiles ahead, of all groups
+  static constexpr int kSeg = kRaw + 2 * kDepth * kSlot;
   static constexpr int kRows = (kSeg + kSegSlots * (int)sizeof(Seg) + 15) / 16 * 16;
   // per row, [segment parity]: factors, rows, window ends; [group]: references, factors of a raise, maxima [warp];
-  // [segment parity][group]: factors of O, last references, sums [warp]
-  static constexpr int kWsum = kRows + (6 + 4 + 8 + 4 + 4 + 16) * kBlock * 4;
+  // [segment parity][group]: factors of O, last references, sums [warp]; [group]: the keys of a tile that it sees
+  static constexpr int kWsum = kRows + (6 + 4 + 8 + 4 + 4 + 16 + 8) * kBlock * 4;
   static constexpr int kBars = kWsum + 32 * 8;
-  static constexpr int kMisc = kBars + (kBarRing + 2 * kStages) * 8;  // [0] TMEM base, [2] abort, [3] tiles asked for, [4] flags [group][2]
+  static constexpr int kMisc = kBars + kNumBars * 8;  // [0] TMEM base, [2] abort, [4] flags [group][2]
   static constexpr int kStart = kMisc + 32;
-  static constexpr int kInfo = (kStart + 31) / 16 * 16;  // [kStages] rows of the tile that are seen: not x .. y - 1 nor from z on; w: not all
-  static constexpr int kAlloc = kInfo + kStages * 16;
-  static_assert(kRows % 16 == 0 && kWsum % 8 == 0 && kStart % 8 == 0 && kInfo % 16 == 0 && kRaw % 16 == 0, "alignment");
-  static_assert(kAlloc <= 227 * 1024 && kAlloc > 120 * 1024, "shared memory: one CTA per SM");
+  static constexpr int kNeed = kStart + 16;
+  static constexpr int kAlloc = kNeed > 120 * 1024 ? kNeed : 120 * 1024;  // one CTA per SM: its TMEM is all there is
+  static_assert(kRows % 16 == 0 && kWsum % 8 == 0 && kStart % 8 == 0, "alignment");
+  static_assert(kAlloc <= 227 * 1024, "shared memory");
 };
 
 struct Kv4Args {
@@ -115,13 +120,18 @@ constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn_major, bool b_mn_major)
   return idesc_bf16_f32(M, N, a_mn_major, b_mn_major) & ~((1u << 7) | (1u << 10));
 }
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
-          smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
-      : "memory");
+// `bytes` (16, or 8 or 4 for scales) of a thread's own to shared memory; none of them: zeros.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(uint8_t* dst, const uint8_t* src, bool there) {
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? kBytes : 0), "n"(kBytes) : "memory");
 }
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
+
 __device__ __forceinline__ float warp_max(float x) {  // a NaN among others is left out
   float m;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
@@ -157,12 +167,19 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
-// mbar_wait in five instructions: nine roles' loops share the instruction cache, so the bound is a count of polls (of 25
-// cycles at least: 0.2 s) and not a clock.
-constexpr uint32_t kPolls = 1u << 24, kDrainPolls = kPolls / 16;
+// mbar_wait in few instructions, and most of them not issued: the wait suspends for up to kSuspendNs at a time, since the
+// polls of the warps that wait would take a third of the issue slots from those that work.  Bounded by the number of polls.
+constexpr uint32_t kSuspendNs = 1000, kPolls = 1u << 21, kDrainPolls = kPolls / 16;
 __device__ __forceinline__ bool wait4(uint64_t* bar, uint32_t parity, uint32_t polls = kPolls) {
-  for (; polls; --polls)
-    if (mbar_try_wait(bar, parity)) return true;
+  for (; polls; --polls) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendNs)
+        : "memory");
+    if (ok) return true;
+  }
   return false;
 }
 
@@ -185,7 +202,6 @@ __device__ __forceinline__ void load_scales(const uint8_t* p, uint32_t (&s)[D / 
     s[0] = *reinterpret_cast<const uint32_t*>(p);
   }
 }
-
 // The scales of the next 32 channels to the front.
 template <int D>
 __device__ __forceinline__ void next_scales(uint32_t (&s)[D / 64]) {
@@ -195,11 +211,6 @@ __device__ __forceinline__ void next_scales(uint32_t (&s)[D / 64]) {
   } else {
     s[0] >>= 16;
   }
-}
-template <int D>
-__device__ __forceinline__ void store_zero_scales(uint8_t* p) {
-  if constexpr (D == 128) *reinterpret_cast<uint2*>(p) = make_uint2(0, 0);
-  else *reinterpret_cast<uint32_t*>(p) = 0;
 }
 
 // Sums l[0 .. n) over the warp; each step halves what a lane keeps: 64 rows end as rows 2 lane and 2 lane + 1 in l[0] and
@@ -225,7 +236,6 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
   using Ro = Roles<kR>;
   constexpr int kN = kR < 16 ? 16 : kR;  // rows of a product (columns behind kR hold anything)
   constexpr int kThreads = Ro::kThreads, kGroups = Ro::kGroups;
-  constexpr int kStages = Ly::kStages;
   const TreeArgs& A = X.t;
   extern __shared__ __align__(1024) uint8_t sm[];  // swizzled tiles start on 1 KB
   if (smem_u32(sm) & 1023) {
@@ -234,12 +244,9 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
     return;
   }
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Ly::kBars);
-  uint64_t* bFull = bars + kBarRing;
-  uint64_t* bEmpty = bFull + kStages;
   Seg* segs = reinterpret_cast<Seg*>(sm + Ly::kSeg);
   float* rowf = reinterpret_cast<float*>(sm + Ly::kRows);  // [2][kBlock]
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(sm + Ly::kMisc);
-  int4* infos = reinterpret_cast<int4*>(sm + Ly::kInfo);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -250,10 +257,9 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
   }
   if (threadIdx.x == 32 * Ro::kIssueQK) {
     for (int x = 0; x < 2; ++x) {
-      mbar_init(&bars[kBarKFull + x], 4);
+      mbar_init(&bars[kBarVFull + x], 4);
       mbar_init(&bars[kBarQK + x], 1);
       mbar_init(&bars[kBarSEmpty + x], 4);
-      mbar_init(&bars[kBarVFull + x], 4);
       mbar_init(&bars[kBarPFull + x], 4);
       mbar_init(&bars[kBarPV + x], 1);
       mbar_init(&bars[kBarQFull + x], 1);
@@ -264,16 +270,16 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
       mbar_init(&bars[kBarOFree + x], 4);
       mbar_init(&bars[kBarDrain + x], 1);
     }
+    for (int x = 0; x < 4; ++x) {
+      mbar_init(&bars[kBarKFull + x], 4);
+      mbar_init(&bars[kBarKFree + x], 1);
+    }
     mbar_init(&bars[kBarOut], 4);
     for (int s = 0; s < kSegSlots; ++s) {
       mbar_init(&bars[kBarSegFull + s], 1);
-      mbar_init(&bars[kBarSegEmpty + s], 8 + 2 + 1 + 4);  // softmax, issuers, Q, output
+      mbar_init(&bars[kBarSegEmpty + s], 8 + 8 * kGroups + 2 + 1 + 4);  // softmax, K and V, issuers, Q, output
     }
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&bFull[s], 1);
-      mbar_init(&bEmpty[s], 8);
-    }
-    misc[2] = misc[3] = 0;
+    misc[2] = 0;
     for (int x = 4; x < 8; ++x) misc[x] = 0xFFFFFFFFu;
     fence_mbar_init();
   }
@@ -339,57 +345,89 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
     if (lane == 0) mbar_arrive(&bars[kBarSegEmpty + slot]);
     return g.b >= 0;
   };
-  // Tile j of the part is in buffer j & 1, use number j >> 1 of it; segment s likewise.
+  // Tile j of the part is in buffer j & 1, use number j >> 1 of it (K and V: of kKBufs and kVBufs); segment s likewise.
   auto done = [&](int bar, int j) { return wait4(&bars[bar + (j & 1)], (j >> 1) & 1); };
+  constexpr int kKBufs = k_bufs(kN);
+  constexpr uint32_t kColS = col_s(kN), kColO = col_o(kN);
+  static_assert(kColO + 4 * kN <= kTmemCols, "TMEM columns");
   auto used_before = [&](int bar, int j) { return wait4(&bars[bar + (j & 1)], ((j >> 1) & 1) ^ 1); };  // (first use: at once)
   // numbers of the rows (see Lay4)
   float* rows = rowf;
   int* rowi = reinterpret_cast<int*>(rows + 2 * kBlock);    // [parity] drafted token of the row, -1: no row
   int* rowend = reinterpret_cast<int*>(rows + 4 * kBlock);  // [parity] kWin: end of the keys behind its window
   constexpr int kRowRef = 6 * kBlock, kRowAlpha = 8 * kBlock, kRowMax = 10 * kBlock, kRowFo = 18 * kBlock,
-                kRowLast = 22 * kBlock, kRowSums = 26 * kBlock;
-  // where the token of row r of a tile lies in a stage: K's codes; V's unit is one page's tokens further
+                kRowLast = 22 * kBlock, kRowSums = 26 * kBlock, kRowMask = 42 * kBlock;
   const int P = 1 << A.page_shift;
-  auto codes_at = [&](int r) { return (r >> A.page_shift) * 2 * P * Ly::kUnit + (r & (P - 1)) * 16; };
-  auto scales_at = [&](int r) { return (r >> A.page_shift) * 2 * P * Ly::kUnit + P * (D / 2) + (r & (P - 1)) * (D / 16); };
 
   // The softmax threads hold kR scores and sums, so they take registers of the others: the block starts with 8 x 128
-  // threads x 64 (kR = 64: 6 x 128 x 80), and 2 x (88, 104) + 6 x (56, 48) are within 8 x 64, 2 x 144 + 4 x 48 within 6 x 80
+  // threads x 64 (kR = 64: 6 x 128 x 80); 2 x 88 + 6 x 56 = 8 x 64, 2 x 128 + 4 x 56 = 6 x 80
   if (warp >= Ro::kK) {
-    if (kR == 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (kR == 32 || kR == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-    if (warp < Ro::kLoader) {
+    if (kR >= 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp < Ro::kPlan) {
       // ------------------------------------------------------------ K to TMEM, V to shared memory: group H the tiles
-      // j = H mod kGroups.  One loop for both (again for the instruction cache).
+      // j = H mod kGroups, thread = key.  A thread copies its key's codes into slots of its own, kDepth tiles ahead, and
+      // looks up their page one tile earlier still; nobody waits for anybody until they are decoded.  One loop for K and V.
+      constexpr int kDepth = Ly::kDepth / kGroups;
       const bool is_v = warp >= Ro::kV;
       const int H = ((warp - Ro::kK) >> 2) & (kGroups - 1), q = warp & 3, r = 32 * q + lane;
-      const uint32_t to = tmem + ((uint32_t)(32 * q) << 16) + kColK;
-      uint8_t* const codes0 = sm + Ly::kRaw + (is_v ? P * Ly::kUnit : 0) + codes_at(r);
-      uint8_t* const scales0 = sm + Ly::kRaw + (is_v ? P * Ly::kUnit : 0) + scales_at(r);
+      const uint32_t to = tmem + ((uint32_t)(32 * q) << 16);
       const uint32_t turn = (r & 7) << 4;  // the 128-byte swizzle of row r
-      const int free_bar = is_v ? kBarPV : kBarQK, full_bar = is_v ? kBarVFull : kBarKFull;
-      for (int j = H; j < cnt; j += kGroups) {
-        const int st = j % kStages;
-        if (!wait4(&bFull[st], (j / kStages) & 1)) { ok = false; break; }
-        uint8_t* codes = codes0 + st * Ly::kStage;
-        const int4 seen = infos[st];
-        if (is_v && seen.w) {
-          // a row that no query sees is zero, whatever its page holds (its codes and scales here: then it decodes as one)
-          if (r >= seen.z || (r >= seen.x && r < seen.y)) {
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) *reinterpret_cast<uint4*>(codes + c * 16 * P) = make_uint4(0, 0, 0, 0);
-            store_zero_scales<D>(scales0 + st * Ly::kStage);
-          }
+      const int free_bar = is_v ? kBarPV : kBarKFree, full_bar = is_v ? kBarVFull : kBarKFull;
+      const int bufs = is_v || kKBufs == 2 ? 2 : 4;
+      const uint8_t* const codes0 = X.data + (is_v ? P * Ly::kUnit : 0) + (r & (P - 1)) * 16;
+      const int scales_at = P * (D / 2) + (r & (P - 1)) * (D / 16 - 16);  // behind the token's codes
+      uint8_t* const slots = sm + Ly::kRaw + ((is_v ? kGroups : 0) + H) * kDepth * Ly::kSlot + r * 16;
+      const int slot_scales = 128 * (D / 2) + r * (D / 16 - 16);
+      Seg g;
+      Span span = {};
+      int s = 0, x = 0, unit = -1;  // of the tile that is looked up: its segment, its place there; its page and head, -1: not read
+      bool more = next_seg(s++, g);
+      if (more) span = span_of<kWin>(A, g.L, g.T);
+      // the next tile of this group, `by` on, and the unit that holds its row
+      auto look = [&](int by) {
+        x += by;
+        while (more && x >= g.t1 - g.t0) {
+          x -= g.t1 - g.t0;
+          more = next_seg(s++, g);
+          if (more) span = span_of<kWin>(A, g.L, g.T);
         }
-        uint32_t scales[D / 64];
-        load_scales<D>(scales0 + st * Ly::kStage, scales);
-        if (!used_before(free_bar, j)) { ok = false; break; }
-        tc_fence_after();
-        uint8_t* v = sm + Ly::kV + (j & 1) * Ly::kTile + r * 128;
+        unit = -1;
+        if (!more) return;
+        const int key = span.key0(g.t0 + x) + r;
+        if (key >= g.L || (kWin && key >= span.hole && key < span.lo)) return;  // seen by no row: zeros, whatever is there
+        const int page = A.table[(int64_t)g.b * A.max_pages + (key >> A.page_shift)];
+        if ((unsigned)page >= (unsigned)A.num_pages) atomicCAS(A.err, 0, (int)kErrIndex);  // not followed, the call has failed
+        else unit = page * A.Hkv + g.kvh;
+      };
+      auto fetch = [&](uint8_t* slot) {  // what was looked up
+        const bool there = unit >= 0;
+        const uint8_t* src = codes0 + (int64_t)max(unit, 0) * (2 * P * Ly::kUnit);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) copy_async<16>(slot + c * 2048, src + c * 16 * P, there);
+        copy_async<D / 16>(slot + slot_scales, src + scales_at, there);
+        copy_commit();
+      };
+      look(H);
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c, codes += 16 * P) {
+      for (int d = 0; d < kDepth; ++d) {
+        fetch(slots + d * Ly::kSlot);
+        look(kGroups);
+      }
+      int at = 0;  // slot of tile j
+      for (int j = H; j < cnt && ok; j += kGroups) {
+        const int buf = j & (bufs - 1), use = bufs == 4 ? j >> 2 : j >> 1;
+        uint8_t* const slot = slots + at * Ly::kSlot;
+        at = at + 1 == kDepth ? 0 : at + 1;
+        copy_wait<kDepth - 1>();
+        uint32_t scales[D / 64];
+        load_scales<D>(slot + slot_scales, scales);
+        if (!wait4(&bars[free_bar + buf], (use & 1) ^ 1)) { ok = false; break; }
+        tc_fence_after();
+        uint8_t* v = sm + Ly::kV + buf * Ly::kTile + r * 128;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
           uint32_t w[16];
-          decode32(*reinterpret_cast<const uint4*>(codes), scales[0], w);
+          decode32(*reinterpret_cast<const uint4*>(slot + c * 2048), scales[0], w);
           next_scales<D>(scales);
           if (is_v) {
             uint8_t* dst = v + (c >> 1) * 16384;
@@ -398,120 +436,59 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
             for (int y = 0; y < 4; ++y)
               *reinterpret_cast<uint4*>(dst + (at ^ (uint32_t)(y << 4))) = make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
           } else {
-            tmem_st16(to + 64 * (j & 1) + 16 * c, w);
+            tmem_st16(to + 64 * buf + 16 * c, w);
           }
         }
         if (is_v) {
-          fence_proxy_async_smem();  // V for the products; zeroed codes before the next copy into the stage
+          fence_proxy_async_smem();
         } else {
           tmem_st_wait();
           tc_fence_before();
         }
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bEmpty[st]);
-          mbar_arrive(&bars[full_bar + (j & 1)]);
-        }
+        if (lane == 0) mbar_arrive(&bars[full_bar + buf]);
+        fetch(slot);
+        look(kGroups);
       }
-    } else if (warp == Ro::kLoader) {
-      // ------------------------------------------------------------ loader
-      const uint64_t policy = A.RB == 1 ? policy_evict_first() : policy_evict_last();
-      const int pshift = 7 - A.page_shift, pp = 1 << pshift;  // pages of a tile
-      const uint32_t page_bytes = 2 * P * Ly::kUnit;
+      copy_wait<0>();  // (a CTA does not leave with copies under way)
+    } else if (warp == Ro::kPlan) {
+      // ------------------------------------------------------------ planner: the part's segments, as far ahead as the slots go
       int64_t at = start[1], pos = begin;  // first tile of request b, of the next segment
       const int64_t hi = begin + cnt;
       int b = (int)start[0], s = 0;
-      // A segment is opened while the tiles of the one before are loaded: its Q is converted meanwhile.
-      struct Open {
+      while (ok) {
         Seg g;
-        Span span;
-        int base, ids, ahead;  // lane x holds the page of entry base + x, and of base + 32 + x (along the line)
-      };
-      Open cur = {}, next = {};
-      auto publish = [&](const Seg& g) -> bool {
+        g.b = -1;  // the end's mark
+        if (pos < hi) {
+          bool bad;
+          int64_t tiles = 0;
+          for (; b < A.B; ++b) {  // pos < hi <= W: a request holding it exists
+            const bool live = request(A, b, g.L, g.T, bad);
+            g.tiles = span_of<kWin>(A, g.L, g.T).tiles;
+            tiles = live ? (int64_t)items * g.tiles : 0;
+            if (pos < at + tiles) break;
+            at += tiles;
+          }
+          if (b >= A.B) { ok = false; break; }
+          g.b = b;
+          const int item = (int)quotient(pos - at, g.tiles);
+          g.kvh = item / A.RB;
+          g.rb = item - g.kvh * A.RB;
+          g.t0 = (int)(pos - at - (int64_t)item * g.tiles);
+          const int64_t left = hi - pos;
+          g.t1 = left < g.tiles - g.t0 ? g.t0 + (int)left : g.tiles;
+          g.r0 = g.t0;
+          g.r1 = g.t1;
+          pos += g.t1 - g.t0;
+        }
         const int slot = s % kSegSlots;
-        if (misc[2] || !wait4(&bars[kBarSegEmpty + slot], ((s / kSegSlots) & 1) ^ 1)) return false;
+        if (misc[2] || !wait4(&bars[kBarSegEmpty + slot], ((s / kSegSlots) & 1) ^ 1)) { ok = false; break; }
         if (lane == 0) {
           segs[slot] = g;
           mbar_arrive(&bars[kBarSegFull + slot]);
         }
         ++s;
-        return true;
-      };
-      // -1: not read
-      auto entry = [&](const Open& o, int p) {
-        p = (o.span.tile(p >> pshift) << pshift) + (p & (pp - 1));
-        if (p >= (o.g.L + P - 1) >> A.page_shift || (kWin && o.span.gone(p, A.page_shift))) return -1;
-        const int page = A.table[(int64_t)o.g.b * A.max_pages + p];
-        if ((unsigned)page < (unsigned)A.num_pages) return page;
-        atomicCAS(A.err, 0, (int)kErrIndex);  // not followed: an existing page stands in, the call has failed
-        return 0;
-      };
-      // the segment from `pos` on, or the end's mark
-      auto open = [&](Open& o) -> bool {
-        Seg& g = o.g;
-        g.b = -1;
-        if (pos >= hi) return publish(g);
-        bool bad;
-        int64_t tiles = 0;
-        for (; b < A.B; ++b) {
-          const bool live = request(A, b, g.L, g.T, bad);
-          o.span = span_of<kWin>(A, g.L, g.T);
-          tiles = live ? (int64_t)items * o.span.tiles : 0;
-          if (pos < at + tiles) break;
-          at += tiles;
-        }
-        if (b >= A.B) return false;
-        g.b = b;
-        g.tiles = o.span.tiles;
-        const int item = (int)quotient(pos - at, g.tiles);
-        g.kvh = item / A.RB;
-        g.rb = item - g.kvh * A.RB;
-        g.t0 = (int)(pos - at - (int64_t)item * g.tiles);
-        const int64_t left = hi - pos;
-        g.t1 = left < g.tiles - g.t0 ? g.t0 + (int)left : g.tiles;
-        g.r0 = g.t0;
-        g.r1 = g.t1;
-        pos += g.t1 - g.t0;
-        if (!publish(g)) return false;
-        o.base = g.t0 << pshift;
-        o.ids = entry(o, o.base + lane);
-        o.ahead = entry(o, o.base + 32 + lane);
-        return true;
-      };
-      ok = open(next);
-      int t = 0;
-      for (int j = 0; j < cnt && ok; ++j) {
-        if (j == 0 || t == cur.g.t1) {
-          cur = next;
-          t = cur.g.t0;
-          if (!open(next)) { ok = false; break; }
-        }
-        int off = (t << pshift) - cur.base;
-        if (off >= 32) {
-          cur.base += 32;
-          off -= 32;
-          cur.ids = cur.ahead;
-          cur.ahead = entry(cur, cur.base + 32 + lane);
-        }
-        const int page = __shfl_sync(0xFFFFFFFFu, cur.ids, (off + lane) & 31);
-        const bool mine = lane < pp && page >= 0;
-        const uint32_t copies = __popc(__ballot_sync(0xFFFFFFFFu, mine));
-        const int st = j % kStages;
-        if (!wait4(&bEmpty[st], ((j / kStages) & 1) ^ 1)) { ok = false; break; }
-        if (lane == 0) {
-          const int key0 = cur.span.key0(t), z = min(128, cur.g.L - key0);
-          const int x = max(0, cur.span.hole - key0), y = min(128, cur.span.lo - key0);
-          infos[st] = make_int4(x, y, z, z < 128 || (kWin && x < y));
-          mbar_arrive_expect_tx(&bFull[st], copies * page_bytes);
-        }
-        __syncwarp();
-        if (mine)
-          bulk_load(sm + Ly::kRaw + st * Ly::kStage + lane * page_bytes,
-                    X.data + ((int64_t)page * A.Hkv + cur.g.kvh) * page_bytes, page_bytes, &bFull[st], policy);
-        __syncwarp();
-        if (lane == 0) misc[3] = j + 1;
-        ++t;
+        if (g.b < 0) break;
       }
     } else if (warp == Ro::kIssueQK) {
       // ------------------------------------------------------------ scores.  (A warp of their own: behind a product
@@ -525,14 +502,16 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
         if (!wait4(&bars[kBarQFull + (s & 1)], (s >> 1) & 1)) { ok = false; break; }
         const uint64_t q = dq + (uint64_t)((s & 1) * (Ly::kQTile >> 4));
         for (int t = g.t0; t < g.t1; ++t, ++j) {
-          if (!done(kBarKFull, j) || !used_before(kBarSEmpty, j)) { ok = false; break; }
+          const int buf = j & (kKBufs - 1), use = kKBufs == 4 ? j >> 2 : j >> 1;
+          if (!wait4(&bars[kBarKFull + buf], use & 1) || !used_before(kBarSEmpty, j)) { ok = false; break; }
           tc_fence_after();
           if (leader) {
 #pragma unroll 2
             for (int kk = 0; kk < D / 16; ++kk)
-              mma_bf16_ts(tmem + kColS + 64 * (j & 1), tmem + kColK + 64 * (j & 1) + 8 * kk,
+              mma_bf16_ts(tmem + kColS + kN * (j & 1), tmem + 64 * buf + 8 * kk,
                           q + (uint64_t)((kk >> 2) * (kBlock * 8) + (kk & 3) * 2), id, kk > 0 ? 1u : 0u);
             mma_commit(&bars[kBarQK + (j & 1)]);
+            mma_commit(&bars[kBarKFree + buf]);
             if (t + 1 == g.t1) mma_commit(&bars[kBarQEmpty + (s & 1)]);
           }
           __syncwarp();
@@ -549,7 +528,7 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
       Seg g;
       for (int s = 0; j < cnt && next_seg(s, g); ++s) {
         if (!used_before(kBarOFree, s)) { ok = false; break; }
-        const uint32_t o = tmem + kColO + 128 * (s & 1);
+        const uint32_t o = tmem + kColO + 2 * kN * (s & 1);
         for (int t = g.t0; t < g.t1; ++t, ++j) {
           if (!done(kBarVFull, j) || !done(kBarPFull, j)) { ok = false; break; }
           tc_fence_after();
@@ -558,7 +537,7 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
             const uint64_t v = dv + (uint64_t)((j & 1) * (Ly::kTile >> 4)), p = dp + (uint64_t)((j & 1) * (Ly::kPTile >> 4));
 #pragma unroll 2
             for (int kk = 0; kk < 8; ++kk)
-              mma_bf16_ss(o + 64 * (j & 1), v + (uint64_t)(kk * 128), p + (uint64_t)(kk * 128), id, (more || kk > 0) ? 1u : 0u);
+              mma_bf16_ss(o + kN * (j & 1), v + (uint64_t)(kk * 128), p + (uint64_t)(kk * 128), id, (more || kk > 0) ? 1u : 0u);
             mma_commit(&bars[kBarPV + (j & 1)]);
             if (t + 1 == g.t1) mma_commit(&bars[kBarODone + (s & 1)]);
           }
@@ -649,13 +628,13 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
         // (a segment of one tile has one group's products)
         const int end = (j0 + tiles - 1) & 1;
         const bool two = tiles > 1;
-        const uint32_t o0 = tmem + lane_base + kColO + 128 * par;
+        const uint32_t o0 = tmem + lane_base + kColO + 2 * kN * par;
         if (D == 128 || w4 < 2) {
 #pragma unroll 1
           for (int c = 0; c < kR && c < width; c += 8) {
             uint32_t o[8], q[8];
-            tmem_ld8(o0 + 64 * end + c, o);
-            tmem_ld8(o0 + 64 * (end ^ 1) + c, q);
+            tmem_ld8(o0 + kN * end + c, o);
+            tmem_ld8(o0 + kN * (end ^ 1) + c, q);
             tmem_ld_wait();
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
@@ -675,15 +654,15 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
       }
     }
   } else {
-    if (kR == 16) asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
-    if (kR == 32) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-    if (kR == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+    if (kR == 16 || kR == 32) asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+    if (kR == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
     // ------------------------------------------------------------ softmax group H: the part's tiles j = H mod 2; thread = key
     const int H = warp >> 2, w4 = warp & 3, tid = threadIdx.x & 127;
-    const uint32_t lane_base = (uint32_t)(32 * w4) << 16, tS = tmem + lane_base + kColS + 64 * H;
+    const uint32_t lane_base = (uint32_t)(32 * w4) << 16, tS = tmem + lane_base + kColS + kN * H;
     float* nref = rows + kRowRef + H * kBlock;
     float* alpha = rows + kRowAlpha + H * kBlock;
     float* wmax = rows + kRowMax + 4 * H * kBlock;
+    uint4* maskbits = reinterpret_cast<uint4*>(rows + kRowMask) + H * kBlock;
     int syncs = 0;
     auto group_arrive = [&]() {
       __syncwarp();
@@ -711,29 +690,49 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
       for (int r = 0; r < kR / 2; ++r) l[r] = pk2(0.f, 0.f);
       if (!wait4(&bars[kBarQFull + (s & 1)], (s >> 1) & 1) || !group_sync()) { ok = false; break; }
       const float* f = rowf + set;
-      const uint32_t tO = tmem + lane_base + kColO + 128 * (s & 1) + 64 * H;
+      const uint32_t tO = tmem + lane_base + kColO + 2 * kN * (s & 1) + kN * H;
       const int tiles = g.t1 - g.t0, first = (j0 ^ H) & 1;  // the group's first tile of them
       for (int x = first; x < tiles; x += 2) {
         const int t = g.t0 + x, j = j0 + x;
-        const int key0 = span.key0(t), key = key0 + tid;
+        const int key0 = span.key0(t);
         const bool masked = key0 + 128 > C || (kWin && key0 + 128 > A.sink && key0 < (int64_t)C + A.n - A.window);
         if (!done(kBarQK, j)) { ok = false; break; }
         tc_fence_after();
         uint32_t see[(kR + 31) / 32];  // masked: rows that see this key
         if (masked) {
-          const int rel = key - C;
+          // thread = row: the 128 keys that it sees, as bits; then thread = key: the rows that see it
+          if (tid < kR) {
+            const int i = rowi[set + tid], end = kWin ? rowend[set + tid] : 0;
+            const uint32_t* mrow = A.mask && i >= 0 ? A.mask + g.b * A.mask_stride + (int64_t)i * A.words : nullptr;
+            uint32_t bits[4];
 #pragma unroll
-          for (int x = 0; x < (kR + 31) / 32; ++x) see[x] = 0;
-#pragma unroll 1
-          for (int r = 0; r < kR; ++r) {
-            const int i = rowi[set + r];
-            bool in = key < g.L;
-            if (in && rel >= 0)
-              in = A.mask ? i >= 0 && (__ldg(A.mask + g.b * A.mask_stride + (int64_t)i * A.words + (rel >> 5)) >> (rel & 31) & 1u)
-                          : rel <= i;
-            if (kWin && key >= A.sink && key < rowend[set + r]) in = false;
-            if (kR > 32 && r >= 32) see[(kR - 1) / 32] |= (in ? 1u : 0u) << (r & 31);
-            else see[0] |= (in ? 1u : 0u) << (r & 31);
+            for (int c = 0; c < 4; ++c) {
+              const int rel = key0 + 32 * c - C;  // drafted index of bit 0 (negative: context)
+              uint32_t w = ~0u;
+              if (rel > -32) {
+                if (A.mask) {
+                  const int w0 = rel >> 5;  // floor for negative rel
+                  const uint32_t a = mrow && w0 >= 0 && w0 < A.words ? __ldg(mrow + w0) : 0u;
+                  const uint32_t b = mrow && w0 + 1 < A.words ? __ldg(mrow + w0 + 1) : 0u;
+                  w = __funnelshift_r(a, b, rel & 31) & low_mask32(g.T - rel);
+                  if (rel < 0) w |= low_mask32(-rel);
+                } else {
+                  w = low_mask32(min(i + 1, g.T) - rel);
+                }
+              }
+              if (kWin) w &= ~(low_mask32(end - (key0 + 32 * c)) & ~low_mask32(A.sink - (key0 + 32 * c)));
+              bits[c] = w;
+            }
+            maskbits[tid] = make_uint4(bits[0], bits[1], bits[2], bits[3]);
+          }
+          if (!group_sync()) { ok = false; break; }
+          const uint32_t* word = reinterpret_cast<const uint32_t*>(maskbits) + w4;
+#pragma unroll
+          for (int x = 0; x < (kR + 31) / 32; ++x) {
+            uint32_t bits = 0;
+#pragma unroll 8
+            for (int r = 0; r < (kR < 32 ? kR : 32); ++r) bits |= (word[4 * (32 * x + r)] >> lane & 1u) << r;
+            see[x] = bits;
           }
         }
         // kR = 64: scores by halves, read from TMEM again for each pass (all of them and the sums in registers spill)
@@ -894,9 +893,6 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
       uint64_t* drained = &bars[kBarDrain + (warp == Ro::kIssueQK ? 0 : 1)];
       if (elect_one()) mma_commit(drained);
       wait4(drained, 0, kDrainPolls);
-    } else if (warp == Ro::kLoader) {
-      const int asked = (int)misc[3];
-      for (int x = max(0, asked - kStages); x < asked; ++x) wait4(&bFull[x % kStages], (x / kStages) & 1, kDrainPolls);
     }
     __syncthreads();
   }
