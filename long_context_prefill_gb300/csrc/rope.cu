@@ -104,9 +104,9 @@ __device__ __forceinline__ void load8(const float* p, const float* q, uint64_t (
 // A block of 16 channels is held as e2m1 codes and an e4m3 scale: scale = RN(max |x| / 6), code = RN(x / scale), both
 // ties to even and of the exact x.  V is exact: a quotient x / scale of 8 by 4 significant bits is a border of two codes
 // or at least 2^-8 of it away (a border times a scale has 7 bits), so rounding it to 2^-12 gives the borders back that
-// the reciprocal's error moved.  K is rounded here in fp32 first, to 2^-19 of its pair's size (32 half steps), so its
-// blocks are rounded twice, from both ends of that range; where the two differ (0.2 % of the heads) they are computed
-// again in fp64.  What the cache holds is then what the definition gives in 64 bits, whatever order a kernel sums in.
+// the reciprocal's error moved.  K is rounded here in fp32 first, to 2^-19 of its pair's size (32 half steps), so it is
+// rounded from both ends of that range; where the two differ (a value in 0.2 % of the heads) it is computed again in
+// fp64.  What the cache holds is then what the definition gives in 64 bits, whatever order a kernel sums in.
 
 // Value `c` of the key head at `x` in fp64; r: the norm's factor.
 __device__ __noinline__ double key64(const RopeArgs& A, const __nv_bfloat16* x, int c, int pos, double r) {
@@ -129,37 +129,40 @@ __device__ __forceinline__ float sticky(double x) {
   return (double)f == x ? f : __uint_as_float(__float_as_uint(f) | 1u);
 }
 
-// Rounds the block v of 16 values to codes (two per byte) and a scale.  margin: how far off they may be.  Returns
-// whether the scale (bit 16) or a code (bits 0 .. 15) may not be that of the exact values.
-__device__ __forceinline__ uint32_t round_block(const float (&v)[16], float inv, float margin, uint2& codes,
-                                                uint32_t& scale) {
-  float a = 0.f;
+constexpr float kOff = 1.9073486328125e-06f;    // 2^-19
+constexpr float kQuot = 4.76837158203125e-07f;  // 2^-21: the rounding of a quotient by a reciprocal
+
+// The scale of a block whose largest value is a (off by up to `off`, both in units of the tensor's scale).
+__device__ __forceinline__ uint32_t block_scale(float a, float off, bool& unsure) {
+  const float q = a / 6.f, e = off * 0.25f + q * kQuot;
+  unsure = off > 0.f && e4m3_of(fmaxf(q - e, 0.f)) != e4m3_of(q + e);
+  return e4m3_of(q);
+}
+
+// Codes of 8 values v; off(x): how far value x may be off, kExact: not at all.  r: 1 / (scale of block and tensor), 0:
+// zeros.  Sets the bits of values whose code may not be that of the exact one.
+template <bool kExact, class F>
+__device__ __forceinline__ uint32_t round8(const uint64_t (&v)[4], float r, F off, uint32_t& unsure) {
+  uint32_t w = 0;
+  unsure = 0;
 #pragma unroll
-  for (int x = 0; x < 16; ++x) a = fmaxf(a, fabsf(v[x]));
-  const float step = 2.384185791015625e-07f;  // 2^-22: the quotient's rounding
-  const float q = a * inv / 6.f, off = margin * inv;
-  scale = e4m3_of(q);
-  uint32_t unsure = 0;
-  if (margin > 0.f && e4m3_of(fmaxf(q - off * 0.25f - q * step, 0.f)) != e4m3_of(q + off * 0.25f + q * step)) unsure = 1u << 16;
-  const float s = e4m3_value(scale), r = s > 0.f ? inv / s : 0.f;
-  const float e = s > 0.f ? off / s + 4.f * step : 0.f;
-  uint32_t w[2] = {0, 0};
-#pragma unroll
-  for (int x = 0; x < 16; x += 2) {
+  for (int x = 0; x < 4; ++x) {
+    float a, b;
+    up2(v[x], a, b);
     uint32_t c;
-    if (margin > 0.f) {
-      const float t0 = fabsf(v[x]) * r, t1 = fabsf(v[x + 1]) * r;
-      c = e2m1x2_of(t0 + e, t1 + e);
-      const uint32_t d = c ^ e2m1x2_of(fmaxf(t0 - e, 0.f), fmaxf(t1 - e, 0.f));
-      unsure |= (d & 0xFu ? 1u << x : 0u) | (d & 0xF0u ? 2u << x : 0u);
+    if (kExact) {
+      c = e2m1x2_of(fmaf(fabsf(a), r, 3072.f) - 3072.f, fmaf(fabsf(b), r, 3072.f) - 3072.f);
     } else {
-      c = e2m1x2_of(fmaf(fabsf(v[x]), r, 3072.f) - 3072.f, fmaf(fabsf(v[x + 1]), r, 3072.f) - 3072.f);
+      const float t0 = fabsf(a) * r, t1 = fabsf(b) * r;
+      const float e0 = fmaf(off(2 * x), r, 2.f * kQuot * t0), e1 = fmaf(off(2 * x + 1), r, 2.f * kQuot * t1);
+      c = e2m1x2_of(t0 + e0, t1 + e1);
+      const uint32_t d = c ^ e2m1x2_of(fmaxf(t0 - e0, 0.f), fmaxf(t1 - e1, 0.f));
+      unsure |= ((d & 0xFu ? 1u : 0u) | (d & 0xF0u ? 2u : 0u)) << (2 * x);
     }
-    c |= (__float_as_uint(v[x]) >> 28 & 8u) | (__float_as_uint(v[x + 1]) >> 24 & 0x80u);
-    w[x >> 3] |= c << (4 * (x & 7));
+    c |= (__float_as_uint(a) >> 28 & 8u) | (__float_as_uint(b) >> 24 & 0x80u);
+    w |= c << (8 * x);
   }
-  codes = make_uint2(w[0], w[1]);
-  return unsure;
+  return w;
 }
 
 // A lane's 16 values of a head: chunks c0 and c1 of 8.  In the rotated columns
@@ -172,7 +175,7 @@ __device__ __forceinline__ uint32_t round_block(const float (&v)[16], float inv,
 // of 32 + 8 + 8 heads of 128 into layer and cache take 151 us, 6.2 TB/s (0.92 of the
 // measured copy rate), 105K tokens 458 us (0.97), 64 tokens of a decode step 3.5 us.
 template <int D, bool kVarlen, bool kKv4>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, kKv4 ? 3 : 4)
     norm_rope_kernel(const __grid_constant__ RopeArgs A, const __grid_constant__ Seqs<kVarlen> T) {
   constexpr int kLanes = D / 16;               // lanes of a head
   constexpr int kHeads = kThreads / kLanes;    // heads in flight per CTA
@@ -181,8 +184,8 @@ __global__ void __launch_bounds__(kThreads, 4)
   __shared__ __align__(16) float cosines[kMaxTokens][D / 2], sines[kMaxTokens][D / 2];
   __shared__ __align__(16) float weights[2][2][D / 2];  // [q or k][chunk]
   __shared__ Token toks[kMaxTokens];
-  // kKv4: heads on their way from a lane's chunks to its block of 16 channels (rows apart by 4 banks)
-  __shared__ __align__(16) float blocks[kKv4 ? kHeads : 1][kKv4 ? D + 4 : 4];
+  // kKv4: the largest values of a head's chunks of 8, and how far they may be off
+  __shared__ float2 tops[kKv4 ? kHeads : 1][kKv4 ? D / 8 : 1];
   const int tid = threadIdx.x;
   const int H = A.Hq + A.Hkv * (1 + A.has_v);
   const int first = A.tok0 + blockIdx.x * A.per_cta;
@@ -282,11 +285,13 @@ __global__ void __launch_bounds__(kThreads, 4)
     const Token tk = toks[t];
     const bool is_v = h >= A.Hq + A.Hkv, is_q = h < A.Hq;
     const unsigned group = (kLanes == 8 ? 0xFFu : 0xFu) << ((tid & 31) / kLanes * kLanes);  // lanes of this head
-    float size = 0.f;  // kKv4: the largest |a| + |b| of the head's pairs
-    if (!is_v) {
-      uint64_t a[4], b[4];
+    uint64_t a[4], b[4];  // this lane's chunks
+    float size[8];        // kKv4, K: the sizes of its pairs, |first| + |second| (interleaved: 0 .. 3 of a, 4 .. 7 of b)
+    if (kKv4 || !is_v) {
       unpack8(x0, a);
       unpack8(x1, b);
+    }
+    if (!is_v) {
       if (A.norm) {
         uint64_t sum = pk2(0.f, 0.f);
 #pragma unroll
@@ -313,12 +318,15 @@ __global__ void __launch_bounds__(kThreads, 4)
           float a0, a1, b0, b1;
           up2(a[x], a0, a1);
           up2(b[x], b0, b1);
-          size = fmaxf(size, fmaxf(fabsf(a0), fabsf(a1)) + fmaxf(fabsf(b0), fabsf(b1)));
-          if (A.interleaved) size = fmaxf(size, fmaxf(fabsf(a0) + fabsf(a1), fabsf(b0) + fabsf(b1)));
+          a0 = fabsf(a0), a1 = fabsf(a1), b0 = fabsf(b0), b1 = fabsf(b1);
+          if (A.interleaved) {
+            size[x] = a0 + a1;
+            size[4 + x] = b0 + b1;
+          } else {
+            size[2 * x] = a0 + b0;
+            size[2 * x + 1] = a1 + b1;
+          }
         }
-        size *= fmaxf(1.f, fabsf(A.rot_scale));
-#pragma unroll
-        for (int o = kLanes / 2; o; o >>= 1) size = fmaxf(size, __shfl_xor_sync(group, size, o));
       }
       if (rotated) {
         uint64_t c[4], s[4];
@@ -354,14 +362,6 @@ __global__ void __launch_bounds__(kThreads, 4)
       }
       x0 = pack8(a);
       x1 = pack8(b);
-      if (kKv4 && !is_q) {
-        float* row = blocks[tid / kLanes];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          *reinterpret_cast<ulonglong2*>(row + c0 + 4 * x) = make_ulonglong2(a[2 * x], a[2 * x + 1]);
-          *reinterpret_cast<ulonglong2*>(row + c1 + 4 * x) = make_ulonglong2(b[2 * x], b[2 * x + 1]);
-        }
-      }
     }
     const int kh = is_q ? h : is_v ? h - A.Hq - A.Hkv : h - A.Hq;
     const int64_t heads = is_q ? A.Hq : A.Hkv;
@@ -372,65 +372,101 @@ __global__ void __launch_bounds__(kThreads, 4)
       __stcs(reinterpret_cast<uint4*>(dst + c1), x1);
     }
     if (kKv4 && !is_q && tk.slot >= 0) {
-      // V's chunks to blocks as well, so that a lane has channels 16 l .. 16 l + 15
-      float v[16];
-      float* row = blocks[tid / kLanes];
-      if (is_v) {
-        uint64_t a[4], b[4];
-        unpack8(x0, a);
-        unpack8(x1, b);
+      const float inv = is_v ? A.v_inv : A.k_inv, rs = fmaxf(1.f, fabsf(A.rot_scale));
+      const bool exact = is_v || (!A.norm && !rotated);  // neither normed nor turned
+      float2* top = tops[tid / kLanes];
+      // how far value x of chunk `second` may be off (a value that is not turned: by its own size)
+      auto off = [&](int second, int x, float v) {
+        if (!rotated) return A.norm ? fabsf(v) * kOff : 0.f;
+        return size[A.interleaved ? 4 * second + (x >> 1) : x] * rs * kOff;
+      };
+      auto chunk_top = [&](const uint64_t (&v)[4], int second) {
+        float m = 0.f, e = 0.f;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          *reinterpret_cast<ulonglong2*>(row + c0 + 4 * x) = make_ulonglong2(a[2 * x], a[2 * x + 1]);
-          *reinterpret_cast<ulonglong2*>(row + c1 + 4 * x) = make_ulonglong2(b[2 * x], b[2 * x + 1]);
+        for (int x = 0; x < 4; ++x) {
+          float y, z;
+          up2(v[x], y, z);
+          m = fmaxf(m, fmaxf(fabsf(y), fabsf(z)));
+          if (!exact) e = fmaxf(e, fmaxf(off(second, 2 * x, y), off(second, 2 * x + 1, z)));
         }
-      }
+        return make_float2(m * inv, e * inv);
+      };
+      top[c0 >> 3] = chunk_top(a, 0);
+      top[c1 >> 3] = chunk_top(b, 1);
       __syncwarp(group);
+      uint32_t scale[2], codes[2], unsure[2];
+      bool far[2];  // the scale may be another one
+      auto round_chunk = [&](const uint64_t (&v)[4], int second, int c) {
+        const float2 t0 = top[c >> 3], t1 = top[(c >> 3) ^ 1];  // of the block's two chunks
+        scale[second] = block_scale(fmaxf(t0.x, t1.x), fmaxf(t0.y, t1.y), far[second]);
+        const float s = e4m3_value(scale[second]), r = s > 0.f ? inv / s : 0.f;
+        float f[8];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) *reinterpret_cast<float4*>(v + 4 * x) = *reinterpret_cast<float4*>(row + 16 * l + 4 * x);
-      __syncwarp(group);
-      const float inv = is_v ? A.v_inv : A.k_inv;
-      uint2 codes;
-      uint32_t scale;
-      const bool exact = is_v || (!A.norm && 16 * l >= A.rot);  // neither normed nor turned
-      const uint32_t unsure = round_block(v, inv, exact ? 0.f : size * 1.9073486328125e-06f, codes, scale);  // 2^-19
-      if (__any_sync(group, unsure != 0)) {  // K only
+        for (int x = 0; x < 4; ++x) up2(v[x], f[2 * x], f[2 * x + 1]);
+        if (exact) codes[second] = round8<true>(v, r, [&](int) { return 0.f; }, unsure[second]);
+        else codes[second] = round8<false>(v, r, [&](int x) { return off(second, x, f[x]); }, unsure[second]);
+      };
+      round_chunk(a, 0, c0);
+      round_chunk(b, 1, c1);
+      const bool again = far[0] || far[1];
+      if (__any_sync(group, again || (unsure[0] | unsure[1]) != 0)) {  // K only
         const __nv_bfloat16* src = A.k + (first + t) * A.k_stride + kh * D;
         double ss = 0.0;
+        uint64_t f[4];
 #pragma unroll 1
-        for (int x = 0; x < 16; ++x) {
-          const double y = (double)__bfloat162float(src[16 * l + x]);
-          ss += y * y;
+        for (int k = 0; k < 2; ++k) {
+          unpack8(*reinterpret_cast<const uint4*>(src + (k ? c1 : c0)), f);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            float y, z;
+            up2(f[x], y, z);
+            ss += (double)y * (double)y + (double)z * (double)z;
+          }
         }
 #pragma unroll
         for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
-        if (unsure) {
-          const double r = A.norm ? 1.0 / sqrt(ss / D + (double)A.eps) : 1.0;
-          const int pos = tk.pos;
-          if (unsure >> 16) {
-            double a = 0.0;
+        const double r = A.norm ? 1.0 / sqrt(ss / D + (double)A.eps) : 1.0;
+        if (__any_sync(group, again)) {
+          // (quotients cut with a mark keep their order and round as the exact ones)
 #pragma unroll 1
-            for (int x = 0; x < 16; ++x) a = fmax(a, fabs(key64(A, src, 16 * l + x, pos, r)));
-            scale = e4m3_of(sticky(a * (double)inv / 6.0));
+          for (int k = 0; k < 2; ++k) {
+            double m = 0.0;
+#pragma unroll 1
+            for (int x = 0; x < 8; ++x) m = fmax(m, fabs(key64(A, src, (k ? c1 : c0) + x, tk.pos, r)));
+            top[(k ? c1 : c0) >> 3].y = sticky(m * (double)inv / 6.0);
           }
-          const float s = e4m3_value(scale);
+          __syncwarp(group);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (far[k]) {
+              const int c = (k ? c1 : c0) >> 3;
+              scale[k] = e4m3_of(fmaxf(top[c].y, top[c ^ 1].y));
+              unsure[k] = 0xFFu;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float s = e4m3_value(scale[k]);
 #pragma unroll 1
-          for (int x = 0; x < 16; ++x) {
-            if (!(unsure >> 16) && !(unsure >> x & 1u)) continue;
-            const double y = key64(A, src, 16 * l + x, pos, r);
+          for (uint32_t left = unsure[k]; left; left &= left - 1) {
+            const int x = __ffs(left) - 1;
+            const double y = key64(A, src, (k ? c1 : c0) + x, tk.pos, r);
             const uint32_t c = (e2m1x2_of(s > 0.f ? sticky(fabs(y) * (double)inv / (double)s) : 0.f, 0.f) & 7u) | (y < 0.0 ? 8u : 0u);
-            const int sh = 4 * (x & 7);
-            uint32_t& w = x < 8 ? codes.x : codes.y;
-            w = (w & ~(0xFu << sh)) | c << sh;
+            codes[k] = (codes[k] & ~(0xFu << (4 * x))) | c << (4 * x);
           }
         }
         __syncwarp(group);
       }
-      const int off = tk.slot & ((1 << A.page_shift) - 1);
+      const int row = tk.slot & ((1 << A.page_shift) - 1);
       const int64_t size4 = (int64_t)kv4_unit<D>() << A.page_shift;
       uint8_t* unit = A.kv4 + (((int64_t)(tk.slot >> A.page_shift) * A.Hkv + kh) * 2 + (is_v ? 1 : 0)) * size4;
-      *reinterpret_cast<uint2*>(unit + ((((l >> 1) << A.page_shift) + off) << 4) + 8 * (l & 1)) = codes;
-      unit[((D / 2) << A.page_shift) + off * (D / 16) + l] = (uint8_t)scale;
+      auto put = [&](int c, int k) {
+        *reinterpret_cast<uint32_t*>(unit + ((((c >> 5) << A.page_shift) + row) << 4) + (c & 31) / 2) = codes[k];
+        if (!(c & 8)) unit[((D / 2) << A.page_shift) + row * (D / 16) + (c >> 4)] = (uint8_t)scale[k];
+      };
+      put(c0, 0);
+      put(c1, 1);
+      __syncwarp(group);  // tops is the next head's
     }
     __nv_bfloat16* pages = is_v ? A.vp : A.kp;
     if (!kKv4 && !is_q && pages && tk.slot >= 0) {
