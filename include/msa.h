@@ -542,7 +542,8 @@ typedef struct {
 /* msa_qk_norm_rope and its varlen form with the 4-bit cache in place of the
  * bf16 pages (pages, slots and v_in are required; k and v, nullable, are the
  * layer's in bf16, not the cached values).  What a slot holds is what the
- * definition gives in fp64. */
+ * definition gives in exact arithmetic, but for values within 2^-40 of a
+ * border between two codes or scales. */
 MSA_API msa_status msa_qk_norm_rope_kv4(const msa_shape* shape, const msa_rope_cfg* cfg, const void* q_in,
                                         int64_t q_stride, const void* k_in, int64_t k_stride, const void* v_in,
                                         int64_t v_stride, const int32_t* positions, void* q, void* k, void* v,

@@ -43,6 +43,17 @@ __device__ __forceinline__ uint32_t e2m1x2_of(float lo, float hi) {  // saturate
   asm("{\n\t.reg .b8 c, z;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %2, %1;\n\tcvt.u32.u8 %0, c;\n\t}" : "=r"(r) : "f"(lo), "f"(hi));
   return r;
 }
+// Eight numbers as codes, the first in the lowest four bits (saturates)
+__device__ __forceinline__ uint32_t e2m1x8_of(const float (&v)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
 // Eight codes as fp16 pairs, times `scale` (twice the same fp16): exact, a product has 6 bits
 __device__ __forceinline__ void f16_of_codes(uint32_t codes, uint32_t scale, uint32_t (&r)[4]) {
   asm("{\n\t.reg .b8 a, b, c, d;\n\t.reg .b32 w, x, y, z;\n\t"

@@ -104,66 +104,207 @@ __device__ __forceinline__ void load8(const float* p, const float* q, uint64_t (
 // A block of 16 channels is held as e2m1 codes and an e4m3 scale: scale = RN(max |x| / 6), code = RN(x / scale), both
 // ties to even and of the exact x.  V is exact: a quotient x / scale of 8 by 4 significant bits is a border of two codes
 // or at least 2^-8 of it away (a border times a scale has 7 bits), so rounding it to 2^-12 gives the borders back that
-// the reciprocal's error moved.  K is rounded here in fp32 first, to 2^-19 of its pair's size (32 half steps), so it is
-// rounded from both ends of that range; where the two differ (a value in 0.2 % of the heads) it is computed again in
-// fp64.  What the cache holds is then what the definition gives in 64 bits, whatever order a kernel sums in.
+// the reciprocal's error moved.  K is rounded here in fp32 first, to kOff of its pair's size, so it is
+// rounded from both ends of that range; where the two differ (in 0.6 % of the heads) it is computed again to 42
+// bits.  What the cache holds is then what the definition gives in 64 bits, whatever order a kernel sums in.
 
-// Value `c` of the key head at `x` in fp64; r: the norm's factor.
-__device__ __noinline__ double key64(const RopeArgs& A, const __nv_bfloat16* x, int c, int pos, double r) {
+// Numbers as unevaluated sums of two floats (Dekker 1971; the exact sum is Knuth's): products and sums are good to about
+// 2^-45.  fp64 would do as well, but its instructions take 16 cycles of a whole SM each.
+struct Two {
+  float h, l;
+};
+__host__ __device__ constexpr Two two(double x) { return {(float)x, (float)(x - (double)(float)x)}; }
+__device__ __forceinline__ Two fast_sum(float a, float b) {  // |a| >= |b| or a = 0
+  const float s = __fadd_rn(a, b);
+  return {s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+__device__ __forceinline__ Two sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Two product(float a, float b) {
+  const float p = __fmul_rn(a, b);
+  return {p, __fmaf_rn(a, b, -p)};
+}
+__device__ __forceinline__ Two operator+(Two x, Two y) {
+  const Two s = sum(x.h, y.h);
+  return fast_sum(s.h, __fadd_rn(s.l, __fadd_rn(x.l, y.l)));
+}
+__device__ __forceinline__ Two operator*(Two x, Two y) {
+  const Two p = product(x.h, y.h);
+  return fast_sum(p.h, __fmaf_rn(x.h, y.l, __fmaf_rn(x.l, y.h, p.l)));
+}
+__device__ __forceinline__ Two operator*(Two x, float y) {
+  const Two p = product(x.h, y);
+  return fast_sum(p.h, __fmaf_rn(x.l, y, p.l));
+}
+__device__ __forceinline__ Two operator-(Two x) { return {-x.h, -x.l}; }
+
+// 1 / sqrt(x): a step of Newton's method from rsqrtf.
+__device__ __forceinline__ Two inverse_root(Two x) {
+  const float r = rsqrtf(x.h);
+  const Two t = x * product(r, r);
+  return fast_sum(r, 0.5f * r * __fsub_rn(__fsub_rn(1.f, t.h), t.l));
+}
+
+// Sine and cosine of `turns` 2^-64 turns: whole quarters, then Taylor's series up to pi / 4.
+__device__ __forceinline__ void sine_cosine(int64_t turns, Two& s, Two& c) {
+  const int64_t quarters = (int64_t)((uint64_t)turns + ((uint64_t)1 << 61)) >> 62;
+  const int64_t rest = (int64_t)((uint64_t)turns - ((uint64_t)quarters << 62));
+  const float h = (float)rest;
+  const Two x = fast_sum(h * 0x1p-63f, (float)(rest - (int64_t)h) * 0x1p-63f) * two(3.141592653589793);
+  const Two y = x * x;
+  Two t = {__fmaf_rn(y.h, __fmaf_rn(y.h, 1.f / 6227020800.f, -1.f / 39916800.f), 1.f / 362880.f), 0.f};
+  t = y * t + two(-1.0 / 5040);
+  t = y * t + two(1.0 / 120);
+  t = y * t + two(-1.0 / 6);
+  const Two sn = x + x * (y * t);
+  t = {__fmaf_rn(y.h, __fmaf_rn(y.h, 1.f / 479001600.f, -1.f / 3628800.f), 1.f / 40320.f), 0.f};
+  t = y * t + two(-1.0 / 720);
+  t = y * t + two(1.0 / 24);
+  t = y * t + two(-0.5);
+  const Two cs = y * t + two(1.0);
+  const bool odd = quarters & 1;
+  s = odd ? cs : sn;
+  c = odd ? sn : cs;
+  if (quarters & 2) s = -s;
+  if ((quarters + 1) & 2) c = -c;
+}
+
+// Value `c` of the key head at `x` to about 2^-40; r: the norm's factor.
+__device__ __noinline__ Two exact_key(const RopeArgs& A, const __nv_bfloat16* x, int c, int pos, Two r) {
   auto normed = [&](int i) {
-    const double v = (double)__bfloat162float(x[i]);
-    return A.norm ? v * r * (A.k_w ? (double)__bfloat162float(A.k_w[i]) : 1.0) : v;
+    const float v = __bfloat162float(x[i]);
+    return A.norm ? r * (A.k_w ? v * __bfloat162float(A.k_w[i]) : v) : Two{v, 0.f};  // (v w has 16 bits)
   };
   if (c >= A.rot) return normed(c);
   const int half = A.rot >> 1, p = A.interleaved ? c >> 1 : c % half;
   const bool second = A.interleaved ? c & 1 : c >= half;
-  const double own = normed(c), other = normed(A.interleaved ? c ^ 1 : second ? c - half : c + half);
-  double s, co;
-  sincospi((double)(int64_t)((uint64_t)(int64_t)pos * A.turn[p]) * 0x1p-63, &s, &co);
-  return (own * co + (second ? other : -other) * s) * (double)A.rot_scale;
+  const Two own = normed(c), other = normed(A.interleaved ? c ^ 1 : second ? c - half : c + half);
+  Two s, co;
+  sine_cosine((int64_t)((uint64_t)(int64_t)pos * A.turn[p]), s, co);
+  return (own * co + (second ? other : -other) * s) * A.rot_scale;
 }
 
-// x >= 0 cut to fp32 with its last bit set where something was cut: rounds to fewer bits as x itself does.
-__device__ __forceinline__ float sticky(double x) {
-  const float f = __double2float_rz(x);
-  return (double)f == x ? f : __uint_as_float(__float_as_uint(f) | 1u);
+// |x| inv / d (inv a power of two), cut to fp32 with its last bit set where something was cut: rounds to fewer bits as
+// the quotient itself does.
+__device__ __forceinline__ float sticky(Two x, float inv, float d) {
+  if (x.h < 0.f) x = -x;
+  const float a = x.h * inv, q = __fdiv_rn(a, d), left = __fadd_rn(__fmaf_rn(-q, d, a), x.l * inv);
+  if (left == 0.f) return q;
+  return __uint_as_float((__float_as_uint(q) - (left < 0.f ? 1u : 0u)) | 1u);
 }
 
-constexpr float kOff = 1.9073486328125e-06f;    // 2^-19
-constexpr float kQuot = 4.76837158203125e-07f;  // 2^-21: the rounding of a quotient by a reciprocal
+// What fp32 may be off in a turned value, in sizes of its pair (half steps of 2^-24): 13 in the sum of squares, half of
+// that in its root, 4 for rsqrtf, 2 for two products; sine and cosine 2.6 (one step, and the angle's rounding), two
+// products and their sum 2, a factor 1: below 20.
+constexpr float kOff = 1.1920928955078125e-06f;  // 20 x 2^-24
+constexpr float kQuot = 4.76837158203125e-07f;  // 2^-21: how far a quotient by a reciprocal is off, relatively
 
-// The scale of a block whose largest value is a (off by up to `off`, both in units of the tensor's scale).
+// The scale of a block whose largest value is a, off by up to `off` (both in units of the tensor's scale).
 __device__ __forceinline__ uint32_t block_scale(float a, float off, bool& unsure) {
-  const float q = a / 6.f, e = off * 0.25f + q * kQuot;
-  unsure = off > 0.f && e4m3_of(fmaxf(q - e, 0.f)) != e4m3_of(q + e);
-  return e4m3_of(q);
+  const float q = a * (1.f / 6.f);
+  if (off > 0.f) {
+    const float e = off * 0.25f + q * 0.5f * kQuot;
+    unsure = e4m3_of(fmaxf(q - e, 0.f)) != e4m3_of(q + e);
+    return e4m3_of(q);
+  }
+  // to 16 bits: exact where it is halfway between two scales (5 bits; a has 8, so else it is 2^-8 of it away at least)
+  unsure = false;
+  return e4m3_of(__uint_as_float((__float_as_uint(q) + 0x80u) & 0xFFFFFF00u));
 }
 
-// Codes of 8 values v; off(x): how far value x may be off, kExact: not at all.  r: 1 / (scale of block and tensor), 0:
-// zeros.  Sets the bits of values whose code may not be that of the exact one.
-template <bool kExact, class F>
-__device__ __forceinline__ uint32_t round8(const uint64_t (&v)[4], float r, F off, uint32_t& unsure) {
-  uint32_t w = 0;
+// Codes of the 8 values v r; e > 0: they are off by up to e, and a code that may be another one has bits set in `unsure`;
+// e = 0: they are exact.
+__device__ __forceinline__ uint32_t round8(const uint64_t (&v)[4], float r, float e, uint32_t& unsure) {
+  const uint64_t rr = pk2(r, r);
+  float f[8];
   unsure = 0;
+  if (e > 0.f) {
+    const uint64_t ee = pk2(e, e), minus = pk2(-e, -e);
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    float a, b;
-    up2(v[x], a, b);
-    uint32_t c;
-    if (kExact) {
-      c = e2m1x2_of(fmaf(fabsf(a), r, 3072.f) - 3072.f, fmaf(fabsf(b), r, 3072.f) - 3072.f);
-    } else {
-      const float t0 = fabsf(a) * r, t1 = fabsf(b) * r;
-      const float e0 = fmaf(off(2 * x), r, 2.f * kQuot * t0), e1 = fmaf(off(2 * x + 1), r, 2.f * kQuot * t1);
-      c = e2m1x2_of(t0 + e0, t1 + e1);
-      const uint32_t d = c ^ e2m1x2_of(fmaxf(t0 - e0, 0.f), fmaxf(t1 - e1, 0.f));
-      unsure |= ((d & 0xFu ? 1u : 0u) | (d & 0xF0u ? 2u : 0u)) << (2 * x);
-    }
-    c |= (__float_as_uint(a) >> 28 & 8u) | (__float_as_uint(b) >> 24 & 0x80u);
-    w |= c << (8 * x);
+    for (int x = 0; x < 4; ++x) up2(fma2(v[x], rr, ee), f[2 * x], f[2 * x + 1]);
+    const uint32_t c = e2m1x8_of(f);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) up2(fma2(v[x], rr, minus), f[2 * x], f[2 * x + 1]);
+    unsure = c ^ e2m1x8_of(f);
+    return c;
   }
-  return w;
+  const uint64_t big = pk2(3072.f, 3072.f), back = pk2(-3072.f, -3072.f);  // to 2^-12
+#pragma unroll
+  for (int x = 0; x < 4; ++x) up2(add2(fma2(v[x], rr, big), back), f[2 * x], f[2 * x + 1]);
+  return e2m1x8_of(f);
 }
+
+// A key head of which a scale or a code may not be that of the exact values: computed again.  One lane's share, in local
+// memory: a call, so that the registers it needs are not taken from the other heads' path (with the code in its place 32K
+// tokens take 276 us, reloading what was spilled for it).
+template <int D>
+struct Again {
+  const RopeArgs& A;
+  float2* top;
+  const __nv_bfloat16* src;  // the head
+  unsigned group;
+  int pos, c[2];
+  float inv, off[2];
+  uint64_t v[2][4];  // chunks, fp32
+  uint32_t scale[2], codes[2], unsure[2];
+  bool far[2];
+
+  __device__ __noinline__ void round() {
+    Two ss = {0.f, 0.f};
+#pragma unroll 1
+    for (int x = 0; x < 16; ++x) {
+      const float y = __bfloat162float(src[c[x >> 3] + (x & 7)]);
+      ss = ss + Two{y * y, 0.f};  // (squares of 8 bits are exact)
+    }
+#pragma unroll 1
+    for (int o = D / 32; o; o >>= 1)
+      ss = ss + Two{__shfl_xor_sync(group, ss.h, o), __shfl_xor_sync(group, ss.l, o)};
+    const Two r = A.norm ? inverse_root(Two{ss.h * (1.f / D), ss.l * (1.f / D)} + Two{A.eps, 0.f}) : Two{1.f, 0.f};
+    if (__any_sync(group, far[0] || far[1])) {
+      // The largest value of each block in question, of those that may be it (quotients cut with a mark keep their order
+      // and round as the exact ones), and the codes by the scale that it gives.
+      float m[2];
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) {
+        m[k] = 0.f;
+        if (!far[k]) continue;
+        const float2 t0 = top[c[k] >> 3], t1 = top[(c[k] >> 3) ^ 1];
+        const float least = fmaxf(t0.x, t1.x) - 2.f * fmaxf(t0.y, t1.y);
+#pragma unroll 1
+        for (int x = 0; x < 8; ++x) {
+          float y, z;
+          up2(v[k][x >> 1], y, z);
+          if (fabsf(x & 1 ? z : y) * inv >= least) m[k] = fmaxf(m[k], sticky(exact_key(A, src, c[k] + x, pos, r), inv, 6.f));
+        }
+      }
+      __syncwarp(group);
+      top[c[0] >> 3].x = m[0];
+      top[c[1] >> 3].x = m[1];
+      __syncwarp(group);
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k)
+        if (far[k]) {
+          scale[k] = e4m3_of(fmaxf(top[c[k] >> 3].x, top[(c[k] >> 3) ^ 1].x));
+          const float s = e4m3_value(scale[k]), q = s > 0.f ? __fdividef(inv, s) : 0.f;
+          codes[k] = round8(v[k], q, off[k] * q > 0.f ? fmaf(off[k], q, 7.f * kQuot) : 0.f, unsure[k]);
+        }
+    }
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+      const float s = e4m3_value(scale[k]);
+#pragma unroll 1
+      for (int x = 0; x < 8; ++x) {
+        if (!(unsure[k] >> (4 * x) & 0xFu)) continue;
+        const Two y = exact_key(A, src, c[k] + x, pos, r);
+        const uint32_t code = (e2m1x2_of(s > 0.f ? sticky(y, inv, s) : 0.f, 0.f) & 7u) | (y.h < 0.f ? 8u : 0u);
+        codes[k] = (codes[k] & ~(0xFu << (4 * x))) | code << (4 * x);
+      }
+    }
+    __syncwarp(group);
+  }
+};
 
 // A lane's 16 values of a head: chunks c0 and c1 of 8.  In the rotated columns
 // chunk 0 holds the first and chunk 1 the second members of 8 pairs
@@ -175,7 +316,7 @@ __device__ __forceinline__ uint32_t round8(const uint64_t (&v)[4], float r, F of
 // of 32 + 8 + 8 heads of 128 into layer and cache take 151 us, 6.2 TB/s (0.92 of the
 // measured copy rate), 105K tokens 458 us (0.97), 64 tokens of a decode step 3.5 us.
 template <int D, bool kVarlen, bool kKv4>
-__global__ void __launch_bounds__(kThreads, kKv4 ? 3 : 4)
+__global__ void __launch_bounds__(kThreads, 4)
     norm_rope_kernel(const __grid_constant__ RopeArgs A, const __grid_constant__ Seqs<kVarlen> T) {
   constexpr int kLanes = D / 16;               // lanes of a head
   constexpr int kHeads = kThreads / kLanes;    // heads in flight per CTA
@@ -286,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, kKv4 ? 3 : 4)
     const bool is_v = h >= A.Hq + A.Hkv, is_q = h < A.Hq;
     const unsigned group = (kLanes == 8 ? 0xFFu : 0xFu) << ((tid & 31) / kLanes * kLanes);  // lanes of this head
     uint64_t a[4], b[4];  // this lane's chunks
-    float size[8];        // kKv4, K: the sizes of its pairs, |first| + |second| (interleaved: 0 .. 3 of a, 4 .. 7 of b)
+    float size[2] = {0.f, 0.f};  // kKv4, K: the largest |first| + |second| of a pair that has a value in the chunk
     if (kKv4 || !is_v) {
       unpack8(x0, a);
       unpack8(x1, b);
@@ -318,13 +459,11 @@ __global__ void __launch_bounds__(kThreads, kKv4 ? 3 : 4)
           float a0, a1, b0, b1;
           up2(a[x], a0, a1);
           up2(b[x], b0, b1);
-          a0 = fabsf(a0), a1 = fabsf(a1), b0 = fabsf(b0), b1 = fabsf(b1);
           if (A.interleaved) {
-            size[x] = a0 + a1;
-            size[4 + x] = b0 + b1;
+            size[0] = fmaxf(size[0], fabsf(a0) + fabsf(a1));
+            size[1] = fmaxf(size[1], fabsf(b0) + fabsf(b1));
           } else {
-            size[2 * x] = a0 + b0;
-            size[2 * x + 1] = a1 + b1;
+            size[0] = size[1] = max3f(size[0], fabsf(a0) + fabsf(b0), fabsf(a1) + fabsf(b1));
           }
         }
       }
@@ -375,87 +514,43 @@ __global__ void __launch_bounds__(kThreads, kKv4 ? 3 : 4)
       const float inv = is_v ? A.v_inv : A.k_inv, rs = fmaxf(1.f, fabsf(A.rot_scale));
       const bool exact = is_v || (!A.norm && !rotated);  // neither normed nor turned
       float2* top = tops[tid / kLanes];
-      // how far value x of chunk `second` may be off (a value that is not turned: by its own size)
-      auto off = [&](int second, int x, float v) {
-        if (!rotated) return A.norm ? fabsf(v) * kOff : 0.f;
-        return size[A.interleaved ? 4 * second + (x >> 1) : x] * rs * kOff;
-      };
-      auto chunk_top = [&](const uint64_t (&v)[4], int second) {
-        float m = 0.f, e = 0.f;
+      // (kOff of the largest pair; a value that is not turned: of more than its own size)
+      const float off0 = exact ? 0.f : size[0] * rs * kOff, off1 = exact ? 0.f : size[1] * rs * kOff;
+      auto largest = [&](const uint64_t (&v)[4]) {
+        float m = 0.f;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           float y, z;
           up2(v[x], y, z);
-          m = fmaxf(m, fmaxf(fabsf(y), fabsf(z)));
-          if (!exact) e = fmaxf(e, fmaxf(off(second, 2 * x, y), off(second, 2 * x + 1, z)));
+          m = max3f(m, fabsf(y), fabsf(z));
         }
-        return make_float2(m * inv, e * inv);
+        return m * inv;
       };
-      top[c0 >> 3] = chunk_top(a, 0);
-      top[c1 >> 3] = chunk_top(b, 1);
+      top[c0 >> 3] = make_float2(largest(a), off0 * inv);
+      top[c1 >> 3] = make_float2(largest(b), off1 * inv);
       __syncwarp(group);
       uint32_t scale[2], codes[2], unsure[2];
       bool far[2];  // the scale may be another one
-      auto round_chunk = [&](const uint64_t (&v)[4], int second, int c) {
+      auto round_chunk = [&](const uint64_t (&v)[4], int second, int c, float off) {
         const float2 t0 = top[c >> 3], t1 = top[(c >> 3) ^ 1];  // of the block's two chunks
         scale[second] = block_scale(fmaxf(t0.x, t1.x), fmaxf(t0.y, t1.y), far[second]);
-        const float s = e4m3_value(scale[second]), r = s > 0.f ? inv / s : 0.f;
-        float f[8];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) up2(v[x], f[2 * x], f[2 * x + 1]);
-        if (exact) codes[second] = round8<true>(v, r, [&](int) { return 0.f; }, unsure[second]);
-        else codes[second] = round8<false>(v, r, [&](int x) { return off(second, x, f[x]); }, unsure[second]);
+        const float s = e4m3_value(scale[second]), r = s > 0.f ? __fdividef(inv, s) : 0.f;
+        codes[second] = round8(v, r, off * r > 0.f ? fmaf(off, r, 7.f * kQuot) : 0.f, unsure[second]);  // (quotients up to 6.4)
       };
-      round_chunk(a, 0, c0);
-      round_chunk(b, 1, c1);
+      round_chunk(a, 0, c0, off0);
+      round_chunk(b, 1, c1, off1);
       const bool again = far[0] || far[1];
       if (__any_sync(group, again || (unsure[0] | unsure[1]) != 0)) {  // K only
-        const __nv_bfloat16* src = A.k + (first + t) * A.k_stride + kh * D;
-        double ss = 0.0;
-        uint64_t f[4];
-#pragma unroll 1
-        for (int k = 0; k < 2; ++k) {
-          unpack8(*reinterpret_cast<const uint4*>(src + (k ? c1 : c0)), f);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            float y, z;
-            up2(f[x], y, z);
-            ss += (double)y * (double)y + (double)z * (double)z;
-          }
-        }
-#pragma unroll
-        for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
-        const double r = A.norm ? 1.0 / sqrt(ss / D + (double)A.eps) : 1.0;
-        if (__any_sync(group, again)) {
-          // (quotients cut with a mark keep their order and round as the exact ones)
-#pragma unroll 1
-          for (int k = 0; k < 2; ++k) {
-            double m = 0.0;
-#pragma unroll 1
-            for (int x = 0; x < 8; ++x) m = fmax(m, fabs(key64(A, src, (k ? c1 : c0) + x, tk.pos, r)));
-            top[(k ? c1 : c0) >> 3].y = sticky(m * (double)inv / 6.0);
-          }
-          __syncwarp(group);
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            if (far[k]) {
-              const int c = (k ? c1 : c0) >> 3;
-              scale[k] = e4m3_of(fmaxf(top[c].y, top[c ^ 1].y));
-              unsure[k] = 0xFFu;
-            }
-        }
+        Again<D> g = {A, top, A.k + (first + t) * A.k_stride + kh * D, group, tk.pos, {c0, c1}, inv, {off0, off1}};
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float s = e4m3_value(scale[k]);
-#pragma unroll 1
-          for (uint32_t left = unsure[k]; left; left &= left - 1) {
-            const int x = __ffs(left) - 1;
-            const double y = key64(A, src, (k ? c1 : c0) + x, tk.pos, r);
-            const uint32_t c = (e2m1x2_of(s > 0.f ? sticky(fabs(y) * (double)inv / (double)s) : 0.f, 0.f) & 7u) | (y < 0.0 ? 8u : 0u);
-            codes[k] = (codes[k] & ~(0xFu << (4 * x))) | c << (4 * x);
-          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x) g.v[k][x] = k ? b[x] : a[x];
+          g.scale[k] = scale[k], g.codes[k] = codes[k], g.unsure[k] = unsure[k], g.far[k] = far[k];
         }
-        __syncwarp(group);
+        g.round();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) scale[k] = g.scale[k], codes[k] = g.codes[k];
       }
       const int row = tk.slot & ((1 << A.page_shift) - 1);
       const int64_t size4 = (int64_t)kv4_unit<D>() << A.page_shift;
