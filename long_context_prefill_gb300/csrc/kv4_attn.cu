@@ -35,9 +35,8 @@
 //                sees becomes zeros (its page may hold anything)
 //   plan (1)     the part's segments
 //   scores (1), products with V (1): the issuers
-//   Q (1)        of the next segment to fp16
 //   output (4)   thread = channel: both groups' O joined, beside the softmax of
-//                the next segment
+//                the next segment; Q of the one behind that to fp16
 #include "kv4.cuh"
 #include "tree.cuh"
 
@@ -54,25 +53,25 @@ template <int kR>
 struct Roles {
   static constexpr int kGroups = kR >= 64 ? 1 : 2;  // of four warps that decode K, and V
   static constexpr int kK = 8, kV = kK + 4 * kGroups, kPlan = kV + 4 * kGroups, kIssueQK = kPlan + 1,
-                       kIssuePV = kPlan + 2, kQ = kPlan + 3, kOut = kPlan + 4, kThreads = 32 * (kOut + 4);
+                       kIssuePV = kPlan + 2, kOut = kPlan + 4, kThreads = 32 * (kOut + 4);
 };
 constexpr uint32_t kTmemCols = 512;
-constexpr int kVBufs = 2;
 // TMEM columns of products of N rows: K (four buffers of 64 columns, with N = 64 two), S [2], O [segment parity][group]
 constexpr int k_bufs(int N) { return N == 64 ? 2 : 4; }
 constexpr uint32_t col_s(int N) { return 64 * k_bufs(N); }
 constexpr uint32_t col_o(int N) { return col_s(N) + 2 * N; }
 constexpr float kTop = 7.f, kRaise = 8.f;                // log2: weight of the reference, how far a score may pass it
 
-// [2] of tiles j: in use j & 1, [4]: j & 3
+// of tiles j: [2] in use j & 1, [4] j & 3, [3] j % 3 (fewer with 64 rows)
 enum {
   kBarKFull = 0,     // [4] K is in TMEM
   kBarKFree = 4,     // [4] its product is done
-  kBarVFull = 8,     // [2] V is in shared memory
+  kBarVFull = 8,     // [3] V is in shared memory
+  kBarVFree = 12,    // [3]
   kBarQK = 16,       // [2] scores are in TMEM
   kBarSEmpty = 18,   // [2] scores are in registers
   kBarPFull = 20,    // [2] weights are in shared memory
-  kBarPV = 22,       // [2] the product with V is done: V and weights are free
+  kBarPV = 22,       // [2] the product with V is done: weights are free
   kBarQFull = 24,    // [2] Q of the segment
   kBarQEmpty = 26,   // [2] its products are done, its factors have been read
   kBarGroup = 28,    // [2] the warps of a softmax group among themselves
@@ -86,13 +85,14 @@ enum {
   kNumBars = kBarSegEmpty + kSegSlots
 };
 
-template <int D>
+// N: rows of a product.  Up to 32, both buffers of weights lie side by side in one tile of 64, and V has three buffers.
+template <int D, int N>
 struct Lay4 {
   static constexpr int kUnit = D / 2 + D / 16;   // bytes of a token, K or V
   static constexpr int kTile = 128 * D * 2;      // a tile of V in fp16
-  static constexpr int kQTile = kBlock * D * 2;
-  static constexpr int kPTile = 128 * kBlock * 2;
-  static constexpr int kV = 0, kP = kV + kVBufs * kTile, kQ = kP + 2 * kPTile, kRaw = kQ + 2 * kQTile;
+  static constexpr int kQTile = N * D * 2, kVBufs = N == 64 ? 2 : 3;
+  static constexpr int kPTile = N == 64 ? 128 * kBlock * 2 : 64, kPTiles = N == 64 ? 2 : 1;  // (64: half of a row of 128 bytes)
+  static constexpr int kV = 0, kP = kV + kVBufs * kTile, kQ = kP + kPTiles * 128 * kBlock * 2, kRaw = kQ + 2 * kQTile;
   static constexpr int kSlot = 128 * kUnit, kDepth = 4 * (128 / D);  // codes of a tile's K or V; tiles ahead, of all groups
   static constexpr int kSeg = kRaw + 2 * kDepth * kSlot;
   static constexpr int kRows = (kSeg + kSegSlots * (int)sizeof(Seg) + 15) / 16 * 16;
@@ -232,9 +232,10 @@ __device__ __forceinline__ void lane_sums(float* l, int lane) {
 
 template <int D, int kR, bool kWin>
 __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const __grid_constant__ Kv4Args X) {
-  using Ly = Lay4<D>;
-  using Ro = Roles<kR>;
   constexpr int kN = kR < 16 ? 16 : kR;  // rows of a product (columns behind kR hold anything)
+  using Ly = Lay4<D, kN>;
+  using Ro = Roles<kR>;
+  constexpr int kVBufs = Ly::kVBufs;
   constexpr int kThreads = Ro::kThreads, kGroups = Ro::kGroups;
   const TreeArgs& A = X.t;
   extern __shared__ __align__(1024) uint8_t sm[];  // swizzled tiles start on 1 KB
@@ -257,12 +258,11 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
   }
   if (threadIdx.x == 32 * Ro::kIssueQK) {
     for (int x = 0; x < 2; ++x) {
-      mbar_init(&bars[kBarVFull + x], 4);
       mbar_init(&bars[kBarQK + x], 1);
       mbar_init(&bars[kBarSEmpty + x], 4);
       mbar_init(&bars[kBarPFull + x], 4);
       mbar_init(&bars[kBarPV + x], 1);
-      mbar_init(&bars[kBarQFull + x], 1);
+      mbar_init(&bars[kBarQFull + x], 4);
       mbar_init(&bars[kBarQEmpty + x], 9);
       mbar_init(&bars[kBarGroup + x], 4);
       mbar_init(&bars[kBarSums + x], 8);
@@ -273,11 +273,13 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
     for (int x = 0; x < 4; ++x) {
       mbar_init(&bars[kBarKFull + x], 4);
       mbar_init(&bars[kBarKFree + x], 1);
+      mbar_init(&bars[kBarVFull + x], 4);
+      mbar_init(&bars[kBarVFree + x], 1);
     }
     mbar_init(&bars[kBarOut], 4);
     for (int s = 0; s < kSegSlots; ++s) {
       mbar_init(&bars[kBarSegFull + s], 1);
-      mbar_init(&bars[kBarSegEmpty + s], 8 + 8 * kGroups + 2 + 1 + 4);  // softmax, K and V, issuers, Q, output
+      mbar_init(&bars[kBarSegEmpty + s], 8 + 8 * kGroups + 2 + 4);  // softmax, K and V, issuers, output
     }
     misc[2] = 0;
     for (int x = 4; x < 8; ++x) misc[x] = 0xFFFFFFFFu;
@@ -372,8 +374,9 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
       const int H = ((warp - Ro::kK) >> 2) & (kGroups - 1), q = warp & 3, r = 32 * q + lane;
       const uint32_t to = tmem + ((uint32_t)(32 * q) << 16);
       const uint32_t turn = (r & 7) << 4;  // the 128-byte swizzle of row r
-      const int free_bar = is_v ? kBarPV : kBarKFree, full_bar = is_v ? kBarVFull : kBarKFull;
-      const int bufs = is_v || kKBufs == 2 ? 2 : 4;
+      const int free_bar = is_v ? kBarVFree : kBarKFree, full_bar = is_v ? kBarVFull : kBarKFull;
+      const int bufs = is_v ? kVBufs : kKBufs;
+      int buf = H, use = 0;  // of tile j: its buffer, and whose use it is
       const uint8_t* const codes0 = X.data + (is_v ? P * Ly::kUnit : 0) + (r & (P - 1)) * 16;
       const int scales_at = P * (D / 2) + (r & (P - 1)) * (D / 16 - 16);  // behind the token's codes
       uint8_t* const slots = sm + Ly::kRaw + ((is_v ? kGroups : 0) + H) * kDepth * Ly::kSlot + r * 16;
@@ -415,7 +418,6 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
       }
       int at = 0;  // slot of tile j
       for (int j = H; j < cnt && ok; j += kGroups) {
-        const int buf = j & (bufs - 1), use = bufs == 4 ? j >> 2 : j >> 1;
         uint8_t* const slot = slots + at * Ly::kSlot;
         at = at + 1 == kDepth ? 0 : at + 1;
         copy_wait<kDepth - 1>();
@@ -447,6 +449,8 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[full_bar + buf]);
+        buf += kGroups;
+        if (buf >= bufs) buf -= bufs, ++use;
         fetch(slot);
         look(kGroups);
       }
@@ -456,6 +460,8 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
       int64_t at = start[1], pos = begin;  // first tile of request b, of the next segment
       const int64_t hi = begin + cnt;
       int b = (int)start[0], s = 0;
+      if (lane == 0) note_cut<false, kCtas, kWin>(A, W, blockIdx.x, (int)start[0], start[1]);
+      __syncwarp();
       while (ok) {
         Seg g;
         g.b = -1;  // the end's mark
@@ -509,7 +515,7 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
 #pragma unroll 2
             for (int kk = 0; kk < D / 16; ++kk)
               mma_bf16_ts(tmem + kColS + kN * (j & 1), tmem + 64 * buf + 8 * kk,
-                          q + (uint64_t)((kk >> 2) * (kBlock * 8) + (kk & 3) * 2), id, kk > 0 ? 1u : 0u);
+                          q + (uint64_t)((kk >> 2) * (kN * 8) + (kk & 3) * 2), id, kk > 0 ? 1u : 0u);
             mma_commit(&bars[kBarQK + (j & 1)]);
             mma_commit(&bars[kBarKFree + buf]);
             if (t + 1 == g.t1) mma_commit(&bars[kBarQEmpty + (s & 1)]);
@@ -524,77 +530,89 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
       const uint64_t dv = sdesc_sw128(smem_u32(sm + Ly::kV), 16384, 1024);
       const uint64_t dp = sdesc_sw128(smem_u32(sm + Ly::kP), 16384, 1024);
       const bool leader = elect_one();
-      int j = 0;
+      int j = 0, buf = 0, use = 0;  // V's buffer, and whose use it is
       Seg g;
       for (int s = 0; j < cnt && next_seg(s, g); ++s) {
         if (!used_before(kBarOFree, s)) { ok = false; break; }
         const uint32_t o = tmem + kColO + 2 * kN * (s & 1);
         for (int t = g.t0; t < g.t1; ++t, ++j) {
-          if (!done(kBarVFull, j) || !done(kBarPFull, j)) { ok = false; break; }
+          if (!wait4(&bars[kBarVFull + buf], use & 1) || !done(kBarPFull, j)) { ok = false; break; }
           tc_fence_after();
           if (leader) {
             const bool more = t - g.t0 >= 2;  // not the first of its group in the segment
-            const uint64_t v = dv + (uint64_t)((j & 1) * (Ly::kTile >> 4)), p = dp + (uint64_t)((j & 1) * (Ly::kPTile >> 4));
+            const uint64_t v = dv + (uint64_t)(buf * (Ly::kTile >> 4)), p = dp + (uint64_t)((j & 1) * (Ly::kPTile >> 4));
 #pragma unroll 2
             for (int kk = 0; kk < 8; ++kk)
               mma_bf16_ss(o + kN * (j & 1), v + (uint64_t)(kk * 128), p + (uint64_t)(kk * 128), id, (more || kk > 0) ? 1u : 0u);
             mma_commit(&bars[kBarPV + (j & 1)]);
+            mma_commit(&bars[kBarVFree + buf]);
             if (t + 1 == g.t1) mma_commit(&bars[kBarODone + (s & 1)]);
           }
           __syncwarp();
+          if (++buf == kVBufs) buf = 0, ++use;
         }
         if (!ok) break;
       }
-    } else if (warp == Ro::kQ) {
-      // ------------------------------------------------------------ Q to fp16
-      constexpr int kPer = D / 32;
-      if (lane == 0) note_cut<false, kCtas, kWin>(A, W, blockIdx.x, (int)start[0], start[1]);
-      __syncwarp();
-      Seg g;
-      for (int s = 0; next_seg(s, g); ++s) {
-        if (!wait4(&bars[kBarQEmpty + (s & 1)], ((s >> 1) & 1) ^ 1)) { ok = false; break; }
+    } else if (warp >= Ro::kOut) {
+      // ------------------------------------------------------------ Q to fp16; output: both groups' O joined, thread = channel
+      const int w4 = warp & 3, tid = 32 * w4 + lane;
+      const uint32_t lane_base = (uint32_t)(32 * w4) << 16;
+      // Q of segment s: eight rows a warp at a time, all on their way before the first is used
+      auto convert = [&](int s, const Seg& g) {
+        constexpr int kPer = D / 32;
         uint8_t* to = sm + Ly::kQ + (s & 1) * Ly::kQTile;
         float* f = rowf + (s & 1) * kBlock;
         const int64_t q0 = (int64_t)(g.b * A.Hq + g.kvh * (A.Hq / A.Hkv)) * A.n + kBlock * g.rb;
         const int ch = kPer * lane;
-#pragma unroll 4
-        for (int r = 0; r < kR; ++r) {
-          const int rr = kBlock * g.rb + r;
-          if (rr >= A.R || rr % A.n >= g.T) {  // no row: whatever its column holds stays there
-            if (lane == 0) f[r] = 0x1p-126f;
-            continue;
+#pragma unroll 1
+        for (int r0 = w4; r0 < kR; r0 += 32) {
+          constexpr int kRows8 = kR < 32 ? kR / 4 : 8;  // rows r0, r0 + 4 ..
+          uint32_t u[kRows8][kPer / 2];
+          uint32_t live = 0;
+#pragma unroll
+          for (int y = 0; y < kRows8; ++y) {
+            const int r = r0 + 4 * y, rr = kBlock * g.rb + r;
+            const bool in = rr < A.R && rr % A.n < g.T;
+            live |= (in ? 1u : 0u) << y;
+            const uint32_t* src = reinterpret_cast<const uint32_t*>(X.q + (q0 + r) * D + ch);
+#pragma unroll
+            for (int x = 0; x < kPer / 2; ++x) u[y][x] = in ? __ldg(src + x) : 0u;
           }
-          const uint32_t* src = reinterpret_cast<const uint32_t*>(X.q + (q0 + r) * D + ch);
-          uint32_t u[kPer / 2];
 #pragma unroll
-          for (int x = 0; x < kPer / 2; ++x) u[x] = __ldg(src + x);
-          uint32_t top = 0;
+          for (int y = 0; y < kRows8; ++y) {
+            const int r = r0 + 4 * y;
+            if (!(live >> y & 1u)) {  // no row: whatever its column holds stays there
+              if (lane == 0) f[r] = 0x1p-126f;
+              continue;
+            }
+            uint32_t top = 0;
 #pragma unroll
-          for (int x = 0; x < kPer / 2; ++x) top = max(top, max(u[x] & 0x7FFFu, u[x] >> 16 & 0x7FFFu));
-          top = max(1u, __reduce_max_sync(0xFFFFFFFFu, top) >> 7);  // exponent of the largest value
-          const int up = 141 - (int)top, a = up / 2, c = up - a;      // to 2^14; two factors, since 2^141 is no fp32 number
-          const float fa = __uint_as_float((uint32_t)(127 + a) << 23), fc = __uint_as_float((uint32_t)(127 + c) << 23);
-          uint32_t h[kPer / 2];
+            for (int x = 0; x < kPer / 2; ++x) top = max(top, max(u[y][x] & 0x7FFFu, u[y][x] >> 16 & 0x7FFFu));
+            top = max(1u, __reduce_max_sync(0xFFFFFFFFu, top) >> 7);  // exponent of the largest value
+            const int up = 141 - (int)top, a = up / 2, c = up - a;      // to 2^14; two factors, since 2^141 is no fp32 number
+            const float fa = __uint_as_float((uint32_t)(127 + a) << 23), fc = __uint_as_float((uint32_t)(127 + c) << 23);
+            uint32_t h[kPer / 2];
 #pragma unroll
-          for (int x = 0; x < kPer / 2; ++x)
-            h[x] = pack_f16x2(__uint_as_float(u[x] << 16) * fa * fc, __uint_as_float(u[x] & 0xFFFF0000u) * fa * fc);
-          uint8_t* dst = to + (ch >> 6) * (kBlock * 128) + sw128_offset(r, (ch & 63) >> 3) + (ch & 7) * 2;
+            for (int x = 0; x < kPer / 2; ++x)
+              h[x] = pack_f16x2(__uint_as_float(u[y][x] << 16) * fa * fc, __uint_as_float(u[y][x] & 0xFFFF0000u) * fa * fc);
+            uint8_t* dst = to + (ch >> 6) * (kN * 128) + sw128_offset(r, (ch & 63) >> 3) + (ch & 7) * 2;
 #pragma unroll
-          for (int x = 0; x < kPer / 2; ++x) reinterpret_cast<uint32_t*>(dst)[x] = h[x];
-          if (lane == 0)  // (not zero: -inf times it stays -inf)
-            f[r] = fmaxf(0x1p-126f, A.scale_log2 * __uint_as_float((uint32_t)(127 - a) << 23) * __uint_as_float((uint32_t)(127 - c) << 23));
+            for (int x = 0; x < kPer / 2; ++x) reinterpret_cast<uint32_t*>(dst)[x] = h[x];
+            if (lane == 0)  // (not zero: -inf times it stays -inf)
+              f[r] = fmaxf(0x1p-126f, A.scale_log2 * __uint_as_float((uint32_t)(127 - a) << 23) * __uint_as_float((uint32_t)(127 - c) << 23));
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[kBarQFull + (s & 1)]);
-      }
-    } else {
-      // ------------------------------------------------------------ output: both groups' O joined; thread = channel
-      const int w4 = warp & 3, tid = 32 * w4 + lane;
-      const uint32_t lane_base = (uint32_t)(32 * w4) << 16;
+      };
       int outs = 0, j0 = 0;
-      Seg g;
-      for (int s = 0; j0 < cnt && next_seg(s, g); ++s) {
+      Seg g, next;
+      bool more = next_seg(0, g);
+      if (more) convert(0, g);
+      if (more) more = next_seg(1, next);
+      if (more) convert(1, next);
+      for (int s = 0; j0 < cnt && ok; ++s) {
         const int par = s & 1, set = par * kBlock, tiles = g.t1 - g.t0;
         float* fo = rows + kRowFo + 2 * set;
         const bool whole = g.r0 == 0 && g.r1 == g.tiles;
@@ -651,6 +669,11 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[kBarOFree + par]);
         j0 += tiles;
+        g = next;
+        if (more && (more = next_seg(s + 2, next))) {  // into the buffer of the segment that is done
+          if (!used_before(kBarQEmpty, s + 2)) { ok = false; break; }
+          convert(s + 2, next);
+        }
       }
     }
   } else {
@@ -833,7 +856,8 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
           if (lane == 0) mbar_arrive(&bars[kBarSEmpty + H]);
         }
         if (!used_before(kBarPV, j)) { ok = false; break; }
-        uint8_t* p = sm + Ly::kP + H * Ly::kPTile;
+        uint8_t* p = sm + Ly::kP + (kN == 64 ? H * Ly::kPTile : 0);
+        constexpr int kSide = kN == 64 ? 0 : 4;  // chunks of 16 bytes to the second buffer in the same rows
 #pragma unroll
         for (int c = 0; c < kR; c += kC) {
           if (kC < kR) {
@@ -850,7 +874,7 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
               uint64_t& sum = l[(c + r) / 2 + k];
               sum = add2(sum, pk2(y[r + 2 * k], y[r + 2 * k + 1]));
             }
-            *reinterpret_cast<uint4*>(p + sw128_offset(tid, (c + r) >> 3)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(p + sw128_offset(tid, ((c + r) >> 3) + kSide * H)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
         if (kC < kR) {
@@ -917,10 +941,11 @@ Ws4 kv4_ws(const msa_shape& s) {
 
 template <int D, int kR, bool kWin>
 msa_status launch(const Kv4Args& a, bool join, cudaStream_t stream) {
+  constexpr int kN = kR < 16 ? 16 : kR;
   auto kern = kv4_attn_kernel<D, kR, kWin>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay4<D>::kAlloc) != cudaSuccess)
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay4<D, kN>::kAlloc) != cudaSuccess)
     return MSA_ERR_CUDA;
-  kern<<<kCtas, Roles<kR>::kThreads, Lay4<D>::kAlloc, stream>>>(a);
+  kern<<<kCtas, Roles<kR>::kThreads, Lay4<D, kN>::kAlloc, stream>>>(a);
   note_launch();
   if (cudaGetLastError() != cudaSuccess) return MSA_ERR_CUDA;
   return join ? launch_join<D, kCtas, kBlock>(a.t, stream) : MSA_OK;
