@@ -383,28 +383,31 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
       const int slot_scales = 128 * (D / 2) + r * (D / 16 - 16);
       Seg g;
       Span span = {};
-      int s = 0, x = 0, unit = -1;  // of the tile that is looked up: its segment, its place there; its page and head, -1: not read
+      int s = 0, x = 0;       // of the tile that is looked up: its segment, its place there
+      int page = 0, kvh = -1;  // its page, not used before fetch (a load is on its way); its head, -1: not read
       bool more = next_seg(s++, g);
-      if (more) span = span_of<kWin>(A, g.L, g.T);
+      if (more) span = span_of<kWin>(A, g.L, g.T, g.rb);
       // the next tile of this group, `by` on, and the unit that holds its row
       auto look = [&](int by) {
         x += by;
         while (more && x >= g.t1 - g.t0) {
           x -= g.t1 - g.t0;
           more = next_seg(s++, g);
-          if (more) span = span_of<kWin>(A, g.L, g.T);
+          if (more) span = span_of<kWin>(A, g.L, g.T, g.rb);
         }
-        unit = -1;
-        if (!more) return;
+        // (no branch round the load: its value would be waited for where the paths meet)
         const int key = span.key0(g.t0 + x) + r;
-        if (key >= g.L || (kWin && key >= span.hole && key < span.lo)) return;  // seen by no row: zeros, whatever is there
-        const int page = A.table[(int64_t)g.b * A.max_pages + (key >> A.page_shift)];
-        if ((unsigned)page >= (unsigned)A.num_pages) atomicCAS(A.err, 0, (int)kErrIndex);  // not followed, the call has failed
-        else unit = page * A.Hkv + g.kvh;
+        const bool seen = more && key < g.L && !(kWin && key >= span.hole && key < span.lo);  // else zeros, whatever is there
+        page = __ldg(A.table + (int64_t)max(g.b, 0) * A.max_pages + (seen ? key >> A.page_shift : 0));
+        kvh = seen ? g.kvh : -1;
       };
       auto fetch = [&](uint8_t* slot) {  // what was looked up
-        const bool there = unit >= 0;
-        const uint8_t* src = codes0 + (int64_t)max(unit, 0) * (2 * P * Ly::kUnit);
+        bool there = kvh >= 0;
+        if (there && (unsigned)page >= (unsigned)A.num_pages) {
+          atomicCAS(A.err, 0, (int)kErrIndex);  // not followed, the call has failed
+          there = false;
+        }
+        const uint8_t* src = codes0 + (there ? (int64_t)page * A.Hkv + kvh : 0) * (2 * P * Ly::kUnit);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) copy_async<16>(slot + c * 2048, src + c * 16 * P, there);
         copy_async<D / 16>(slot + slot_scales, src + scales_at, there);
@@ -699,7 +702,7 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
     int j0 = 0;  // the segment's first tile
     Seg g;
     for (int s = 0; j0 < cnt && next_seg(s, g); ++s) {
-      const Span span = span_of<kWin>(A, g.L, g.T);
+      const Span span = span_of<kWin>(A, g.L, g.T, g.rb);
       const int C = g.L - g.T, set = (s & 1) * kBlock;
       float m_used = -INFINITY;  // of row `tid`
       if (!used_before(kBarOFree, s)) { ok = false; break; }  // the rows' numbers of segment s - 2 have been read
@@ -718,7 +721,7 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
       for (int x = first; x < tiles; x += 2) {
         const int t = g.t0 + x, j = j0 + x;
         const int key0 = span.key0(t);
-        const bool masked = key0 + 128 > C || (kWin && key0 + 128 > A.sink && key0 < (int64_t)C + A.n - A.window);
+        const bool masked = kWin ? span.masked<kWin>(key0, A.sink) : key0 + 128 > C;
         if (!done(kBarQK, j)) { ok = false; break; }
         tc_fence_after();
         uint32_t see[(kR + 31) / 32];  // masked: rows that see this key
@@ -850,11 +853,12 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
             exponentials();
           }
         }
-        if (kC == kR) {
-          tc_fence_before();  // the scores are in registers
+        auto release = [&]() {  // the scores are in registers
+          tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[kBarSEmpty + H]);
-        }
+        };
+        if (kC == kR) release();
         if (!used_before(kBarPV, j)) { ok = false; break; }
         uint8_t* p = sm + Ly::kP + (kN == 64 ? H * Ly::kPTile : 0);
         constexpr int kSide = kN == 64 ? 0 : 4;  // chunks of 16 bytes to the second buffer in the same rows
@@ -862,6 +866,7 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
         for (int c = 0; c < kR; c += kC) {
           if (kC < kR) {
             load_scores(c);
+            if (c + kC == kR) release();
             scale_scores(c);
             exponentials();
           }
@@ -876,11 +881,6 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
             }
             *reinterpret_cast<uint4*>(p + sw128_offset(tid, ((c + r) >> 3) + kSide * H)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
-        }
-        if (kC < kR) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[kBarSEmpty + H]);
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -1021,6 +1021,7 @@ extern "C" msa_status msa_attn_tree_kv4(const msa_shape* shape, const void* q, c
     t.sink = window->sink;
     t.window = window->window;
     t.depth = window->depth;
+    t.step = chain_step(t, kBlock);
   }
   t.err = device_error_word();
   if (!t.err) return MSA_ERR_CUDA;

@@ -357,6 +357,7 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
         const int item = (int)quotient(pos - at, g.tiles);
         g.kvh = item / A.RB;
         g.rb = item - g.kvh * A.RB;
+        if (kWin) span = span_of<kWin>(A, g.L, g.T, g.rb);
         g.t0 = (int)(pos - at - (int64_t)item * g.tiles);
         const int64_t left = hi - pos;
         g.t1 = left < g.tiles - g.t0 ? g.t0 + (int)left : g.tiles;
@@ -467,7 +468,7 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
           w.t = g.t0;
           w.b_end = g.t1;
           w.L = g.L;
-          w.span = span_of<kWin>(A, g.L, g.T);
+          w.span = span_of<kWin>(A, g.L, g.T, g.rb);
         }
         const int key0 = w.span.key0(w.t++), keys = w.L - key0;
         // rows of the tile that hold keys which no row sees (below 0, above 127: none)
@@ -631,7 +632,7 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
       const int C = g.L - g.T;
       const uint32_t* mrow = A.mask ? A.mask + g.b * A.mask_stride + (int64_t)i * A.words : nullptr;
       // bit k: this row attends key key0 + k (keys from the end of the context on; lanes without a row see all)
-      const Span span = span_of<kWin>(A, g.L, g.T);
+      const Span span = span_of<kWin>(A, g.L, g.T, rb);
       const int end = kWin ? behind(A, g.b, i, C) : 0;  // keys sink .. end - 1 are outside this row's window
       auto mask32 = [&](int key0) -> uint32_t {
         const int rel = key0 - C;  // drafted index of bit 0 (negative: context)
@@ -721,8 +722,7 @@ __global__ void __launch_bounds__(threads_of(kRows), 1)
         for (int t = g.t0; t < g.t1; ++t) {
           if (misc[2]) { ok = false; break; }
           const int key0 = span.key0(t);
-          // (kWin: the last row's window begins at C + n - A.window at most)
-          const bool masked = key0 + 128 > C || (kWin && key0 + 128 > A.sink && key0 < (int64_t)C + A.n - A.window);
+          const bool masked = span.masked<kWin>(key0, A.sink);
           if (!mbar_wait(&bars[kBarSFull + X], seen & 1)) { ok = false; break; }
           tc_fence_after();
           if constexpr (kPair) {
@@ -1063,6 +1063,7 @@ msa_status attn_tree(const msa_shape* shape, const void* q, const msa_kv_pages* 
     a.sink = window->sink;
     a.window = window->window;
     a.depth = window->depth;
+    a.step = chain_step(a, 256);
   }
   a.err = device_error_word();
   if (!a.err) return MSA_ERR_CUDA;

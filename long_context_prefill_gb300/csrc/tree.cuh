@@ -38,6 +38,7 @@ struct TreeArgs {
   int* err;
   int32_t sink, window;  // kWin: see msa_tree_window
   const int32_t* depth;  // kWin: [B][n] or null
+  int32_t step;  // kWin: drafted tokens of an item if those are consecutive and a chain, else 0
 };
 
 // The piece of one item that lies in a part: tiles t0 .. t1 of its `tiles`.
@@ -65,26 +66,45 @@ __device__ __forceinline__ bool request(const TreeArgs& A, int b, int& L, int& T
 __device__ __forceinline__ int key_tiles(int L) { return (L + 127) >> 7; }
 
 // The keys and tiles of a request that some row sees.  Keys hole .. lo - 1 are seen by none (lo <= hole: there are no
-// such); tile t of the request's line holds the keys from key0(t) on.
+// such); tile t of the item's line holds the keys from key0(t) on.  Items of one request have the same number of tiles.
+// Where an item is `step` tokens of a chain they are those of its own windows (a chunk of 1024 tokens in items of 256,
+// window 1024: 11 tiles an item where the chunk has 17), with what is missing to the number from the keys around them.
 struct Span {
   int tiles, head, skip;  // tiles of the line; those of the first tokens, tiles left out behind them
   int hole, lo;
+  int all0, all1;  // every row sees the keys from all0 (kWin) up to all1 - 1
   __device__ __forceinline__ int tile(int t) const { return t < head ? t : t + skip; }
   __device__ __forceinline__ int key0(int t) const { return 128 * tile(t); }
+  // some row may not see every key of the tile that begins at key0
+  template <bool kWin>
+  __device__ __forceinline__ bool masked(int key0, int sink) const {
+    return key0 + 128 > all1 || (kWin && key0 + 128 > sink && key0 < all0);
+  }
   // page p of the request, of 2^shift tokens, holds no key that is seen
   __device__ __forceinline__ bool gone(int p, int shift) const {
     return (int64_t)p << shift >= hole && (int64_t)(p + 1) << shift <= lo;
   }
 };
 template <bool kWin>
-__device__ __forceinline__ Span span_of(const TreeArgs& A, int L, int T) {
-  Span s = {key_tiles(L), 0x7FFFFFFF, 0, 0, 0};
+__device__ __forceinline__ Span span_of(const TreeArgs& A, int L, int T, int rb = 0) {
+  Span s = {key_tiles(L), 0x7FFFFFFF, 0, 0, 0, 0, L - T};
   if constexpr (kWin) {
     s.hole = min(A.sink, L);
     s.lo = max(0, L - T + 1 - A.window);  // the first row stands at L - T
     s.head = key_tiles(s.hole);
     s.skip = max(0, (s.lo >> 7) - s.head);
     s.tiles -= s.skip;
+    int end = A.n;  // the rows lie in front of it
+    if (A.step) {
+      // window - 1 + step keys, which begin anywhere in a tile, and the first tokens'
+      const int most = s.head + (int)((uint32_t)(min(A.window, L) + A.step + 253) >> 7);
+      const int i0 = min(A.step * (rb % (A.n / A.step)), T), lo = max(0, L - T + i0 + 1 - A.window);
+      s.tiles = min(s.tiles, most);
+      s.skip = max(s.skip, min((lo >> 7) - s.head, key_tiles(L) - s.tiles));
+      end = i0 + A.step;
+      s.all1 = L - T + i0 + 1;  // a chain
+    }
+    s.all0 = L - T + min(end - A.window, T);
   }
   return s;
 }
@@ -281,6 +301,9 @@ bool aligned(const void* p, size_t a, bool required) {
   if (!p) return !required;
   return reinterpret_cast<uintptr_t>(p) % a == 0;
 }
+
+// TreeArgs::step for items of `rows` rows.
+int32_t chain_step(const TreeArgs& a, int rows) { return !a.mask && a.n % rows == 0 ? rows : 0; }
 
 bool window_ok(const msa_tree_window* w, const uint32_t* mask) {
   return w->sink >= 0 && w->window >= 1 && aligned(w->depth, 4, false) && (!w->depth || mask);

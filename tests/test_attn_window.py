@@ -196,6 +196,19 @@ def test_chunk_of_a_prompt(cuda_lib, sink, window):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("sink,window", [(0, 1), (0, 129), (200, 300), (128, 1024), (3, 100000)])
+@pytest.mark.parametrize("Hq,n,d,page", [(1, 256, 64, 16), (2, 512, 128, 128), (3, 768, 64, 64), (2, 1024, 128, 32)])
+def test_items_have_their_own_windows(cuda_lib, Hq, n, d, page, sink, window):
+    """Chains whose items are 256 consecutive tokens: whole and short chunks, at the start of a prompt and far in."""
+    lens = [n, 1, n + 77, 700, 5000, n + 4000, 300]
+    tls = [n, 1, n, min(n, 600), n, 257 if n > 256 else 255, 0]
+    c = Case(Hq, 1, n, d, page, lens, sink, window, n + window, tls=tls)
+    out = c.run()
+    assert cuda_lib.poll_device_status() == 0
+    c.check(out, what=f"items {n} {sink}+{window}")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("n,d", [(1, 128), (12, 64), (30, 128), (60, 128)])
 def test_many_requests_cut_anywhere(cuda_lib, n, d):
     """More tiles than CTAs, parts that begin and end in sinks and in windows; the same bits on every run."""

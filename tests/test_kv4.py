@@ -572,6 +572,19 @@ def test_windows(cuda_lib, Hq, Hkv, n, d, page, sink, window):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("sink,window", [(0, 1), (0, 129), (200, 300), (3, 100000)])
+@pytest.mark.parametrize("Hq,n,d,page", [(1, 64, 64, 16), (2, 128, 128, 128), (3, 192, 64, 64), (2, 512, 128, 32)])
+def test_items_have_their_own_windows(cuda_lib, Hq, n, d, page, sink, window):
+    """Chains whose items are 64 consecutive tokens: whole and short chunks, at the start of a prompt and far in."""
+    lens = [n, 1, n + 77, 700, 5000, n + 4000, 300]
+    tls = [n, 1, n, min(n, 600), n, 65 if n > 64 else 63, 0]
+    c = Cache(Hq, 1, n, d, page, lens, n + window, tls=tls, sink=sink, window=window)
+    out = c.run()
+    assert cuda_lib.poll_device_status() == 0
+    c.check(out, what=f"items {n} {sink}+{window}")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("Hq,Hkv,n", [(4, 1, 1), (4, 1, 7), (4, 1, 17), (4, 1, 50), (6, 2, 100)])
 def test_long_contexts_are_cut_and_joined(cuda_lib, Hq, Hkv, n, d):
