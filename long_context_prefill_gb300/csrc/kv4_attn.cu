@@ -29,14 +29,37 @@
 //                in turn, each with its own references, sums and O: a tile's
 //                chain (scores, exponentials, weights) is latency, two of them
 //                side by side are not
-//   K (4 or 8)   decode: global memory -> registers -> TMEM (two buffers), a
-//                tile ahead
-//   V (4 or 8)   the same into shared memory (two buffers).  A row that no query
-//                sees becomes zeros (its page may hold anything)
+//   K (4 or 8)   decode: global memory -> shared memory (cp.async into slots of
+//                the thread's own) -> registers -> TMEM (four buffers, two for
+//                64 rows)
+//   V (4 or 8)   the same into shared memory (three buffers, two for 64 rows).  A
+//                row that no query sees becomes zeros (its page may hold anything)
 //   plan (1)     the part's segments
-//   scores (1), products with V (1): the issuers
+//   scores (1), products with V (1): the issuers, an elected thread each
 //   output (4)   thread = channel: both groups' O joined, beside the softmax of
 //                the next segment; Q of the one behind that to fp16
+//
+// Measured (one launch and its join, captured, inputs larger than the L2; floor =
+// bytes at 6.8 TB/s): 64 requests of 1K to 16K tokens, one row group of 4
+// (32/8 heads of 128) 114 us (floor 53; the bf16 cache's 188); one request of a
+// million tokens, 20 rows, 398 (178); 16 requests of 4K to 32K tokens with trees of
+// 48 (192 rows: three passes over the codes) 451 (66); of 16 (64 rows) 166 (34);
+// 256 requests of 100 to 1000 tokens 123 (17); heads of 64 95 (26); through 128 + 1024
+// keys 54 (13); one of 2047 tokens, 2 / 1 heads of 64, 14.
+//
+// What bounds it now: 16 warps that decode issue about 300 instructions for 32 keys of
+// K or V (16 conversions and 16 products a 32 channels, at half rate each), 600 of a
+// scheduler's 1400 cycles a tile with 8 rows; the schedulers issue 0.67 a cycle, the
+// rest is instruction fetch (eight roles) and waits for each other.  With 64 rows a
+// softmax group's chain, 3300 cycles a tile: scores 300, first pass 600, vote
+// 250, weights 900, raises 600 where references are passed often.
+//
+// Tried and slower: codes through a ring of bulk copies with a loading warp (121 us for
+// 114 in the decode case: one more hand-over a tile, and its warp's waits), or loaded into
+// registers a tile ahead (spills); one softmax group for all tiles (139 us; 64 rows and
+// 24 warps were even: 450); the chunk loop of the decode unrolled twice (118 us: fetch);
+// raising only the rows whose reference was passed (557 us for 451 with 192 rows: the
+// others follow soon after, a raise each).
 #include "kv4.cuh"
 #include "tree.cuh"
 
@@ -398,7 +421,7 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
         // (no branch round the load: its value would be waited for where the paths meet)
         const int key = span.key0(g.t0 + x) + r;
         const bool seen = more && key < g.L && !(kWin && key >= span.hole && key < span.lo);  // else zeros, whatever is there
-        page = __ldg(A.table + (int64_t)max(g.b, 0) * A.max_pages + (seen ? key >> A.page_shift : 0));
+        page = __ldg(A.table + (seen ? (int64_t)g.b * A.max_pages + (key >> A.page_shift) : 0));
         kvh = seen ? g.kvh : -1;
       };
       auto fetch = [&](uint8_t* slot) {  // what was looked up

@@ -16,8 +16,14 @@
 // is rounded to fp32 half turns in [-1, 1) for the sine and cosine: to 2^-26
 // turns at worst, and relative to the angle where that is near a whole turn.
 //
+// Into a 4-bit cache (kKv4) keys and values leave as the codes and scales of
+// "4-bit pages" below, the layer's layout as without it.
+//
 // What bounds it: HBM, every value read once and written once per
-// destination.  A lane holds both members of its pairs (two 16-byte chunks, a
+// destination.  4-bit pages: issue, 187 us for the 32K tokens that take 151 into bf16
+// pages (165 without the second computation of the heads in question, which
+// is out of line: inlined, its registers spilled and cost 70 us); 64 tokens of a decode
+// step 11 us, most of it the sines' and the exact path's chains.  A lane holds both members of its pairs (two 16-byte chunks, a
 // head in 8 lanes for d_h = 128), so the rotation needs no exchange and the
 // norm three shuffles; the cosines of a token are computed once per CTA and
 // serve all its heads.

@@ -6,6 +6,9 @@
 // context keys and the drafted keys that its mask names (none given: j <= i):
 //   o_i = Σ_j e^{s_ij} v_j / Σ_j e^{s_ij},  s_ij = scale q_i . k_j.
 //
+// Through a window (msa_attn_tree_window) row i at position p_i sees of the context
+// the keys j < sink and j > p_i - window.
+//
 // What bounds it: HBM.  A KV head's keys serve the g = Hq / Hkv query heads of
 // its group for all n drafted tokens, R = g n rows, so each byte of K and V
 // meets R multiply-adds: below about 280 rows (1925 TFLOP/s over 6.8 TB/s)
@@ -22,6 +25,13 @@
 // (launched early, waiting for the first) joins them in key order, so results
 // do not depend on timing.
 //
+// Windows (kWin, kernels of their own: the others pay nothing).  The line holds only
+// the tiles with keys that some row of an item sees (Span in tree.cuh), so an item
+// costs what its window holds, whatever the context.  Keys in those tiles that no row
+// sees may be anything: the loader puts an existing page where the table's entry need
+// not exist, and warp 8 zeroes their rows of V.  A tile that all rows see whole is not
+// masked.
+//
 // A CTA (12 warps, kMany 16 of which three have no task; one CTA per SM):
 //   warp 10    loader of group 0's part (kTwo: of the CTA's) and one more warp for
 //              group 1's: walk its segments, publish their descriptors, load Q
@@ -35,7 +45,8 @@
 //              not take the phase of a slot's earlier use for the one it waits
 //              for.  With declarations in order, the tile it saw last proves
 //              every earlier use of the slot over);
-//   warps 9/11 MMA issuers;
+//   warps 9/11 MMA issuers, an elected thread each (elect.sync: a branch on the lane
+//              makes each issue cost 66 cycles, so 15 to 40);
 //   warps 0-7  softmax groups X = 0, 1 (4 warps each, thread = row = TMEM lane).
 // Three row layouts (Rows):
 //   kFew   up to 64 rows: the groups work on parts of their own; group 1 has its
@@ -62,6 +73,10 @@
 // and slower there (against 162 to 174 us): a score tile per group with P over it
 // 194 us, turns of the groups on a scheduler 192 to 253 us, scores by halves of 64
 // keys 208 us, products held back while scores are computed 175 us.
+// Windows: decode of the same 64 requests through 128 + 1024 keys 58 us (floor 44), 16
+// trees of up to 48 through 64 + 512 35 us (floor 7.4: 8 tiles a CTA, joins 5), 1024 rows of
+// a prompt's chunk through 128 + 1024 of 128K 46 us (floor 10, of operations: 12 tiles of 256
+// rows for each of 128 items, 10 a CTA, 2.4 us a tile where the rows' ends are masked; joins 10).
 #include <type_traits>
 
 #include "tree.cuh"
