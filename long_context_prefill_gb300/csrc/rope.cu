@@ -236,7 +236,7 @@ __device__ __forceinline__ uint32_t round8(const uint64_t (&v)[4], float r, floa
     unsure = c ^ e2m1x8_of(f);
     return c;
   }
-  const uint64_t big = pk2(3072.f, 3072.f), back = pk2(-3072.f, -3072.f);  // to 2^-12
+  const uint64_t big = pk2(0x1.8p11f, 0x1.8p11f), back = pk2(-0x1.8p11f, -0x1.8p11f);  // to 2^-12
 #pragma unroll
   for (int x = 0; x < 4; ++x) up2(add2(fma2(v[x], rr, big), back), f[2 * x], f[2 * x + 1]);
   return e2m1x8_of(f);
