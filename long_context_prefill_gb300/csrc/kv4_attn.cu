@@ -42,9 +42,9 @@
 // Measured (one launch and its join, captured, inputs larger than the L2; floor =
 // bytes at 6.8 TB/s): 64 requests of 1K to 16K tokens, one row group of 4
 // (32/8 heads of 128) 114 us (floor 53; the bf16 cache's 188); one request of a
-// million tokens, 20 rows, 398 (178); 16 requests of 4K to 32K tokens with trees of
-// 48 (192 rows: three passes over the codes) 451 (66); of 16 (64 rows) 166 (34);
-// 256 requests of 100 to 1000 tokens 123 (17); heads of 64 95 (26); through 128 + 1024
+// million tokens, 20 rows, 381 (178); 16 requests of 4K to 32K tokens with trees of
+// 48 (192 rows: three passes over the codes) 451 to 460 (66); of 16 (64 rows) 166 (34),
+// of 8 (32 rows) 109 (33); 256 requests of 100 to 1000 tokens 122 (17); heads of 64 95 (26); through 128 + 1024
 // keys 54 (13); one of 2047 tokens, 2 / 1 heads of 64, 14.
 //
 // What bounds it now: 16 warps that decode issue about 300 instructions for 32 keys of
@@ -784,8 +784,10 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
             see[x] = bits;
           }
         }
-        // kR = 64: scores by halves, read from TMEM again for each pass (all of them and the sums in registers spill)
-        constexpr int kC = kR == 64 ? 32 : kR;
+        // kR = 32 and 64: scores by halves (all of them and the sums in registers spill: 32 rows 116 us for 108).  The
+        // second is read from TMEM again for its weights; of 64 rows the first is too (451 us, 475 where it is kept)
+        constexpr int kC = kR >= 32 ? kR / 2 : kR;
+        constexpr bool kKeep = kR < 64;
         float y[kC];
         auto load_scores = [&](int c0) {  // of rows c0 .., -inf where a row does not see the key
 #pragma unroll
@@ -797,7 +799,7 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
           tmem_ld_wait();
           if (masked)
 #pragma unroll
-            for (int r = 0; r < kC; ++r) y[r] = (see[c0 >> 5] >> (r & 31) & 1u) ? y[r] : -INFINITY;
+            for (int r = 0; r < kC; ++r) y[r] = (see[c0 >> 5] >> ((c0 + r) & 31) & 1u) ? y[r] : -INFINITY;
         };
         // log2 of the weights; returns the largest
         auto scale_scores = [&](int c0) -> float {
@@ -821,14 +823,14 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
           // Does one of the four warps' scores pass its reference too far?  The exponentials are under way meanwhile.
           float top = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < kR; c += kC) {
+          for (int c = kR - kC; c >= 0; c -= kC) {
             load_scores(c);
             top = fmaxf(top, scale_scores(c));
           }
           const int at = syncs;
           if (__any_sync(0xFFFFFFFFu, top > kTop + kRaise) && lane == 0) misc[4 + 2 * H + (at & 1)] = at;
           group_arrive();
-          if (kC == kR) exponentials();
+          if (kKeep) exponentials();  // (of rows 0 ..)
           if (!group_wait()) { ok = false; break; }
           far = misc[4 + 2 * H + (at & 1)] == (uint32_t)at;
         }
@@ -871,7 +873,8 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
             }
             tmem_st_wait();
           }
-          if (kC == kR) {
+          if (kKeep) {
+            if (kC < kR) load_scores(0);
             scale_scores(0);
             exponentials();
           }
@@ -887,7 +890,7 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
         constexpr int kSide = kN == 64 ? 0 : 4;  // chunks of 16 bytes to the second buffer in the same rows
 #pragma unroll
         for (int c = 0; c < kR; c += kC) {
-          if (kC < kR) {
+          if (!kKeep || c > 0) {
             load_scores(c);
             if (c + kC == kR) release();
             scale_scores(c);
