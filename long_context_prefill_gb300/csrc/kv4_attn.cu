@@ -852,9 +852,12 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
             float m = m_used;
 #pragma unroll
             for (int w = 0; w < 4; ++w) m = fmaxf(m, wmax[w * kBlock + tid]);
+            // A column without a row holds whatever shared memory held: with a reference of -inf for its scores it never
+            // asks for a raise, or the others' weights would round to what ran before
+            const bool row = rowi[set + tid] >= 0;
             alpha[tid] = m == m_used ? 1.f : ex2(m_used - m);
-            nref[tid] = fminf(kTop - m, 3e38f);  // (no key met yet: the first one is too far above)
-            m_used = m;
+            nref[tid] = row ? fminf(kTop - m, 3e38f) : -INFINITY;  // (no key met yet: the first one is too far above)
+            if (row) m_used = m;
           }
           if (!group_sync()) { ok = false; break; }
           if (x > first) {

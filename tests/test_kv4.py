@@ -886,3 +886,34 @@ def test_prompt_decode_and_continuation_together(cuda_lib):
     assert cuda_lib.poll_device_status() == 0
     assert float((got.float() - want.float()).abs().max()) <= 1.5e-2 + 2.0 ** -7 * float(V.float().abs().max())
     check_rounded(kc[0].transpose(0, 1), *norm_rope(k[0], w[1], True, 1e-6, d, _freq(d), False, pos), "layer keys")
+
+
+def _fill_shared_memory(word):
+    """Leave the 16-bit `word` in the shared memory that holds keys and values of msa_attn_tree, on every SM."""
+    Hkv, page, d, pages = 8, 128, 128, 128
+    kv = torch.full((pages, Hkv, page, d), word, dtype=torch.int16, device="cuda").view(BF)
+    q = torch.zeros(1, Hkv, 1, d, dtype=BF, device="cuda")
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    msa.attn_tree(q, kv, kv, table, torch.tensor([pages * page], dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv,n", [(4, 2, 3), (4, 1, 4), (4, 1, 8), (2, 1, 32), (4, 1, 40)])
+def test_bits_do_not_depend_on_what_ran_before(cuda_lib, Hq, Hkv, n, d):
+    """Rows that are not drafted have no say in the others' references, whatever shared memory holds in their place: fp16
+    numbers, NaN or infinities.  Their windows begin behind a group's first tile."""
+    rng = np.random.default_rng(n)
+    window = 2000  # items of 17 tiles, parts of several tiles
+    lens = [128 * int(rng.integers(8, 40)) + window + 127 - x % 4 for x in range(80)]  # the first row sees a few keys of its first tile
+    tls = [1 + x % min(n, 3) for x in range(80)]
+    for w in (0, window):
+        c = Cache(Hq, Hkv, n, d, 16, lens, n + d, tls=tls, window=w)
+        outs = []
+        for word in (0x3C00, 0x7C01, 0x7C00, -0x0400, 0):  # fp16: 1, NaN, infinity, -infinity, 0
+            _fill_shared_memory(word)
+            outs.append(c.run())
+        assert cuda_lib.poll_device_status() == 0
+        c.check(outs[0], what=f"window {w}")
+        for word, out in enumerate(outs):
+            assert torch.equal(out[0], outs[0][0]) and torch.equal(out[1], outs[0][1]), (w, word)
