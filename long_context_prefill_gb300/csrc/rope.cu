@@ -207,8 +207,17 @@ __device__ __forceinline__ float sticky(Two x, float inv, float d) {
 constexpr float kOff = 1.1920928955078125e-06f;  // 20 x 2^-24
 constexpr float kQuot = 4.76837158203125e-07f;  // 2^-21: how far a quotient by a reciprocal is off, relatively
 
-// The scale of a block whose largest value is a, off by up to `off` (both in units of the tensor's scale).
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// The scale of a block whose largest value is a, off by up to `off` (both in units of the tensor's scale).  A NaN among
+// its values makes a one, and the scale: whoever reads the block finds it, as in the bf16 cache.
 __device__ __forceinline__ uint32_t block_scale(float a, float off, bool& unsure) {
+  unsure = false;
+  if (a != a) return 0x7Fu;
   const float q = a * (1.f / 6.f);
   if (off > 0.f) {
     const float e = off * 0.25f + q * 0.5f * kQuot;
@@ -216,7 +225,6 @@ __device__ __forceinline__ uint32_t block_scale(float a, float off, bool& unsure
     return e4m3_of(q);
   }
   // to 16 bits: exact where it is halfway between two scales (5 bits; a has 8, so else it is 2^-8 of it away at least)
-  unsure = false;
   return e4m3_of(__uint_as_float((__float_as_uint(q) + 0x80u) & 0xFFFFFF00u));
 }
 
@@ -528,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 4)
         for (int x = 0; x < 4; ++x) {
           float y, z;
           up2(v[x], y, z);
-          m = max3f(m, fabsf(y), fabsf(z));
+          m = max_or_nan(m, max_or_nan(fabsf(y), fabsf(z)));
         }
         return m * inv;
       };
@@ -539,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 4)
       bool far[2];  // the scale may be another one
       auto round_chunk = [&](const uint64_t (&v)[4], int second, int c, float off) {
         const float2 t0 = top[c >> 3], t1 = top[(c >> 3) ^ 1];  // of the block's two chunks
-        scale[second] = block_scale(fmaxf(t0.x, t1.x), fmaxf(t0.y, t1.y), far[second]);
+        scale[second] = block_scale(max_or_nan(t0.x, t1.x), fmaxf(t0.y, t1.y), far[second]);
         const float s = e4m3_value(scale[second]), r = s > 0.f ? __fdividef(inv, s) : 0.f;
         codes[second] = round8(v, r, off * r > 0.f ? fmaf(off, r, 7.f * kQuot) : 0.f, unsure[second]);  // (quotients up to 6.4)
       };

@@ -917,3 +917,45 @@ def test_bits_do_not_depend_on_what_ran_before(cuda_lib, Hq, Hkv, n, d):
         c.check(outs[0], what=f"window {w}")
         for word, out in enumerate(outs):
             assert torch.equal(out[0], outs[0][0]) and torch.equal(out[1], outs[0][1]), (w, word)
+
+
+def _check_held_with_nan(data, page, d, slots, k, v, ks=1.0, vs=1.0):
+    """As _check_held for the tokens' own slots; a NaN value makes its block NaN, by its scale."""
+    rows = [t.transpose(1, 2).reshape(-1, *t.shape[1:2], d) for t in kv4_values(data, page, d, ks, vs)]
+    for got, x, s, what in ((rows[0], k, ks, "K"), (rows[1], v, vs, "V")):
+        got, want = got[slots.long()], kv4_round(x, s)[0]
+        assert torch.equal(got.isnan(), want.isnan()), f"{what}: {int((got.isnan() != want.isnan()).sum())} NaN differ"
+        assert torch.equal(got.nan_to_num(), want.nan_to_num()), f"{what}: {int((got != want).sum())} values differ"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rot,inter,norm", [(0, False, False), (None, False, False), (48, True, False), (None, False, True),
+                                            (16, True, True)])
+def test_append_keeps_nan(cuda_lib, d, rot, inter, norm):
+    """A NaN in a key or value, and what the norm makes of a head that holds one or (eps 0) of zeros alone, stays one in
+    the cache, where reading back and attention find it; other blocks and heads are as without."""
+    rot = d if rot is None else rot
+    tok, Hq, Hkv, page = 12, 4, 2, 16
+    q, k, v, w = _inputs(tok, Hq, Hkv, d, 41 + d)
+    nan = float("nan")
+    k[1, 0, 3] = k[2, 1, d - 1] = v[3, 0, 17] = v[4, 1, 0] = nan
+    k[5, 0] = 0
+    k[6, 1, :20] = nan
+    k[7], v[8] = nan, nan
+    cfg = msa.rope_cfg(rot, interleaved=inter, norm=norm, eps=0.0, q_weight=w[0], k_weight=w[1])
+    pages = msa.KV4Pages.empty(1, Hkv, page, d, "cuda")
+    slots = torch.arange(tok, dtype=torch.int32, device="cuda")
+    pos = torch.arange(5, 5 + tok, dtype=torch.int32, device="cuda")
+    qo, _, _ = msa.qk_norm_rope_kv4(q[None], k[None], v[None], cfg, pages, slots, positions=pos)
+    assert cuda_lib.poll_device_status() == 0
+    ref, _ = norm_rope(k, w[1], norm, 0.0, rot, _freq(rot), inter, pos)
+    assert bool(ref[1, 0].isnan().any()) and bool(ref[5, 0].isnan().all()) == norm
+    _check_held_with_nan(pages.data, page, d, slots, ref, v.double())
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table, lens = torch.zeros(1, 1, **i32), torch.tensor([tok], **i32)
+    hk, hv = msa.kv4_gather(pages, table, lens, tok)
+    assert bool(hk[0, 0, 1].isnan().any()) and bool(hv[0, 0, 3, 16:32].isnan().all()) and not bool(hv[0, 0, 3, :16].isnan().any())
+    o = msa.attn_tree_kv4(qo[:, :, :1].contiguous(), pages, table, lens)
+    assert bool(o[0, :2].isnan().all())  # a NaN key of their KV head
+    assert cuda_lib.poll_device_status() == 0
