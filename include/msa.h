@@ -527,7 +527,8 @@ MSA_API msa_status msa_attn_tree_window(const msa_shape* shape, const void* q, c
  * RN(x / (scale tensor scale)), to the nearest with ties to even, of the
  * exact x (a key after norm and rotation, not rounded before); a block whose
  * scale rounds to zero is held as zeros, one with a NaN by a NaN scale (0x7F):
- * all 16 values read as NaN.
+ * all 16 values read as NaN.  An infinity counts as larger than any number:
+ * the scale is 448, the code +-6.
  *
  * data: [num_pages, Hkv] units pairs, K's and V's, of page_size * (d_h / 2 +
  * d_h / 16) bytes each: codes [d_h / 32][page_size][16] (byte y of chunk c:

@@ -197,7 +197,7 @@ __device__ __noinline__ Two exact_key(const RopeArgs& A, const __nv_bfloat16* x,
 __device__ __forceinline__ float sticky(Two x, float inv, float d) {
   if (x.h < 0.f) x = -x;
   const float a = x.h * inv, q = __fdiv_rn(a, d), left = __fadd_rn(__fmaf_rn(-q, d, a), x.l * inv);
-  if (left == 0.f) return q;
+  if (left == 0.f || q == INFINITY) return q;
   return __uint_as_float((__float_as_uint(q) - (left < 0.f ? 1u : 0u)) | 1u);
 }
 
@@ -217,7 +217,7 @@ __device__ __forceinline__ float max_or_nan(float a, float b) {
 // its values makes a one, and the scale: whoever reads the block finds it, as in the bf16 cache.
 __device__ __forceinline__ uint32_t block_scale(float a, float off, bool& unsure) {
   unsure = false;
-  if (a != a) return 0x7Fu;
+  if (!(a < INFINITY)) return a != a ? 0x7Fu : 0x7Eu;
   const float q = a * (1.f / 6.f);
   if (off > 0.f) {
     const float e = off * 0.25f + q * 0.5f * kQuot;
@@ -311,6 +311,12 @@ struct Again {
 #pragma unroll 1
       for (int x = 0; x < 8; ++x) {
         if (!(unsure[k] >> (4 * x) & 0xFu)) continue;
+        float z0, z1;
+        up2(v[k][x >> 1], z0, z1);
+        if (!(fabsf(x & 1 ? z1 : z0) < INFINITY)) {  // (its neighbours' error passes fp32's range)
+          codes[k] = (codes[k] & ~(0xFu << (4 * x))) | (((x & 1 ? z1 : z0) < 0.f ? 0xFu : 7u) << (4 * x));
+          continue;
+        }
         const Two y = exact_key(A, src, c[k] + x, pos, r);
         const uint32_t code = (e2m1x2_of(s > 0.f ? sticky(y, inv, s) : 0.f, 0.f) & 7u) | (y.h < 0.f ? 8u : 0u);
         codes[k] = (codes[k] & ~(0xFu << (4 * x))) | code << (4 * x);
@@ -441,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     const bool is_v = h >= A.Hq + A.Hkv, is_q = h < A.Hq;
     const unsigned group = (kLanes == 8 ? 0xFFu : 0xFu) << ((tid & 31) / kLanes * kLanes);  // lanes of this head
     uint64_t a[4], b[4];  // this lane's chunks
-    float size[2] = {0.f, 0.f};  // kKv4, K: the largest |first| + |second| of a pair that has a value in the chunk
+    float size[2] = {0.f, 0.f};  // kKv4, K: the largest finite |first| + |second| of a pair that has a value in the chunk
     if (kKv4 || !is_v) {
       unpack8(x0, a);
       unpack8(x1, b);
@@ -473,11 +479,15 @@ __global__ void __launch_bounds__(kThreads, 4)
           float a0, a1, b0, b1;
           up2(a[x], a0, a1);
           up2(b[x], b0, b1);
+          auto pair = [](float p, float q) {  // an infinite one: NaN, which the maximum leaves out
+            const float t = fabsf(p) + fabsf(q);
+            return fmaf(t, 0.f, t);
+          };
           if (A.interleaved) {
-            size[0] = fmaxf(size[0], fabsf(a0) + fabsf(a1));
-            size[1] = fmaxf(size[1], fabsf(b0) + fabsf(b1));
+            size[0] = fmaxf(size[0], pair(a0, a1));
+            size[1] = fmaxf(size[1], pair(b0, b1));
           } else {
-            size[0] = size[1] = max3f(size[0], fabsf(a0) + fabsf(b0), fabsf(a1) + fabsf(b1));
+            size[0] = size[1] = max3f(size[0], pair(a0, b0), pair(a1, b1));
           }
         }
       }

@@ -959,3 +959,31 @@ def test_append_keeps_nan(cuda_lib, d, rot, inter, norm):
     o = msa.attn_tree_kv4(qo[:, :, :1].contiguous(), pages, table, lens)
     assert bool(o[0, :2].isnan().all())  # a NaN key of their KV head
     assert cuda_lib.poll_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ks,vs", [(1.0, 1.0), (2.0 ** -40, 2.0 ** -40), (2.0 ** 40, 2.0 ** 40)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rot,inter", [(0, False), (None, False), (48, False), (None, True), (16, True)])
+def test_append_infinities_and_values_past_any_scale(cuda_lib, d, rot, inter, ks, vs):
+    """Infinities, and finite values that the tensor's scale takes past fp32, are held as the largest number; the others
+    of their block by the largest scale, other blocks as without them."""
+    rot = d if rot is None else rot
+    tok, Hq, Hkv, page = 16, 4, 2, 16
+    q, k, v, _ = _inputs(tok, Hq, Hkv, d, 43 + d)
+    k[4:8] *= 100 * ks if ks > 1 else 300
+    v[4:8] *= 100 * vs if vs > 1 else 300
+    inf = float("inf")
+    for x in (k, v):
+        x[1, 0, 3], x[2, 1, d - 1], x[3, 0, 17] = inf, -inf, 3e38
+        x[4, 0, 9], x[5, 1, 30], x[6, 0, 0] = -3e38, inf, 2e30
+        x[6, 1, 31], x[7, 0, 2], x[7, 0, 3] = -1e27, inf, -inf
+        x[8, 0], x[9, 1] = inf, -1e38
+    cfg = msa.rope_cfg(rot, interleaved=inter)
+    pages = msa.KV4Pages.empty(1, Hkv, page, d, "cuda", ks, vs)
+    slots = torch.arange(tok, dtype=torch.int32, device="cuda")
+    pos = torch.arange(3, 3 + tok, dtype=torch.int32, device="cuda")
+    msa.qk_norm_rope_kv4(q[None], k[None], v[None], cfg, pages, slots, positions=pos)
+    assert cuda_lib.poll_device_status() == 0
+    ref, _ = norm_rope(k, None, False, 0.0, rot, _freq(rot), inter, pos)
+    _check_held_with_nan(pages.data, page, d, slots, ref, v.double(), ks, vs)
