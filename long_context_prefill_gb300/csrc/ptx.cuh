@@ -162,15 +162,6 @@ __device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr, uint32_t lbo, ui
   return d;
 }
 
-// One thread of a converged warp, the same one each time.  Products are issued under this predicate: with one that the
-// compiler cannot tell to hold for a single thread (lane == 0) it serialises each issue over the lanes, 66 cycles a
-// product where these take 15 to 40 (M = 128, N = 16 to 64).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
-  return one != 0;
-}
-
 // Instruction descriptor, kind::f16 with bf16 inputs and an fp32 accumulator.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn_major, bool b_mn_major) {
   return (1u << 4)                          // accumulator format: f32

@@ -9,6 +9,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "warps.cuh"
 
 namespace msa {
 

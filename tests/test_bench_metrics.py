@@ -23,3 +23,12 @@ def test_logical_edges_page_example():
     assert bench.logical_edges(1024, [0, 512], []) == 1536
     # a single slash at offset 0 is the diagonal: n pairs; with column 0 the pair (0, 0) is shared
     assert bench.logical_edges(10, [0], [0]) == 10 + 10 - 1
+
+
+def test_attention_traffic_is_of_the_present_sources():
+    """The captured DRAM bytes that the bench reports belong to the attention kernel's sources as they are (a change of
+    those wants a new capture)."""
+    names = ["mixed", "vs128k", "bs128k"]
+    total, per = bench.attention_traffic(names, None)
+    assert set(per) == set(names) and total == sum(per.values()) > 0
+    assert bench.attention_traffic(names, 4096) == (None, None)  # captured at the full sizes only
