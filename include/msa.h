@@ -331,11 +331,11 @@ MSA_API msa_status msa_layer_attend_stats(const msa_shape* shape, const void* q,
                                           const msa_head_cfg* table, void* o, float* lse, int64_t* edges,
                                           int64_t* tiles, void* ws, size_t ws_bytes, void* stream);
 
-/* Failure-detection check (no counterpart in the pages): launches one thread
- * that waits on a barrier nothing arrives at, with the same bounded wait the
+/* Failure-detection check (no counterpart in the pages): launches threads
+ * that wait on a barrier nothing arrives at, with the same bounded waits the
  * pipelines use but a limit of limit_ms (1..2000) milliseconds, so that the
- * next msa_poll_device_status returns MSA_ERR_DEVICE_TIMEOUT.  The context
- * stays usable.  Nothing faults, traps or hangs. */
+ * next msa_poll_device_status returns MSA_ERR_DEVICE_TIMEOUT once all have run
+ * out.  The context stays usable.  Nothing faults, traps or hangs. */
 MSA_API msa_status msa_check_wait_timeout(int32_t limit_ms, void* stream);
 
 /* Number of kernels this process has launched through the library so far

@@ -9,6 +9,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "warps.cuh"
 
 namespace msa {
 
@@ -210,16 +211,29 @@ void block_units(const msa_shape& s, const int32_t* heads, int32_t nh, std::vect
   }
 }
 
-// Failure-detection check: one thread waits on an mbarrier that nothing
-// arrives at, with a short limit, and records the timeout in the error word
-// exactly as the pipelines' bounded waits do.
+// Failure-detection check: the library's two waits, a thread each, on an
+// mbarrier that nothing arrives at, with a short limit; a third one without one
+// that another role's giving up ends.  If all run out, that is recorded in the
+// error word exactly as the pipelines do.
 __global__ void wait_timeout_check_kernel(uint64_t limit_ns, int* err) {
   __shared__ uint64_t bar;
+  __shared__ volatile uint32_t gave_up;
   if (threadIdx.x == 0) {
     mbar_init(&bar, 1);
     fence_mbar_init();
-    if (!mbar_wait(&bar, 0, limit_ns)) atomicCAS(err, 0, kErrTimeout);
+    gave_up = 0;
   }
+  __syncthreads();
+  bool reached = false;
+  if (threadIdx.x == 0) {
+    reached = mbar_wait(&bar, 0, limit_ns);
+    gave_up = 1;
+  } else if (threadIdx.x == 32) {
+    reached = mbar_wait_long(&bar, 0, nullptr, limit_ns);
+  } else if (threadIdx.x == 64) {
+    reached = mbar_wait_long(&bar, 0, &gave_up, 2 * MSA_WAIT_LIMIT_NS);
+  }
+  if (!__syncthreads_or(reached) && threadIdx.x == 0) atomicCAS(err, 0, kErrTimeout);
 }
 
 // Sequences (in token order) with their prefix sums; lens[x] tokens each.
@@ -405,7 +419,7 @@ msa_status msa_check_wait_timeout(int32_t limit_ms, void* stream) {
   if (limit_ms < 1 || limit_ms > 2000) return MSA_ERR_INVALID_ARG;
   int* err = device_error_word();
   if (!err) return MSA_ERR_CUDA;
-  wait_timeout_check_kernel<<<1, 32, 0, (cudaStream_t)stream>>>((uint64_t)limit_ms * 1000000ull, err);
+  wait_timeout_check_kernel<<<1, 96, 0, (cudaStream_t)stream>>>((uint64_t)limit_ms * 1000000ull, err);
   note_launch();
   return cudaGetLastError() == cudaSuccess ? MSA_OK : MSA_ERR_CUDA;
 }

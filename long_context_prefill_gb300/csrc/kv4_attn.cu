@@ -123,7 +123,7 @@ struct Lay4 {
   // [segment parity][group]: factors of O, last references, sums [warp]; [group]: the keys of a tile that it sees
   static constexpr int kWsum = kRows + (6 + 4 + 8 + 4 + 4 + 16 + 8) * kBlock * 4;
   static constexpr int kBars = kWsum + 32 * 8;
-  static constexpr int kMisc = kBars + kNumBars * 8;  // [0] TMEM base, [2] abort, [4] flags [group][2]
+  static constexpr int kMisc = kBars + kNumBars * 8;  // [0] TMEM base, [2] abort, [3] tiles issued, [4] flags [group][2]
   static constexpr int kStart = kMisc + 32;
   static constexpr int kNeed = kStart + 16;
   static constexpr int kAlloc = kNeed > 120 * 1024 ? kNeed : 120 * 1024;  // one CTA per SM: its TMEM is all there is
@@ -188,22 +188,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
-}
-
-// mbar_wait in few instructions, and most of them not issued: the wait suspends for up to kSuspendNs at a time, since the
-// polls of the warps that wait would take a third of the issue slots from those that work.  Bounded by the number of polls.
-constexpr uint32_t kSuspendNs = 1000, kPolls = 1u << 21, kDrainPolls = kPolls / 16;
-__device__ __forceinline__ bool wait4(uint64_t* bar, uint32_t parity, uint32_t polls = kPolls) {
-  for (; polls; --polls) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendNs)
-        : "memory");
-    if (ok) return true;
-  }
-  return false;
 }
 
 // 32 channels of a token: 16 bytes of codes and two scales, as 16 fp16 pairs.
@@ -304,7 +288,7 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
       mbar_init(&bars[kBarSegFull + s], 1);
       mbar_init(&bars[kBarSegEmpty + s], 8 + 8 * kGroups + 2 + 4);  // softmax, K and V, issuers, output
     }
-    misc[2] = 0;
+    misc[2] = misc[3] = 0;
     for (int x = 4; x < 8; ++x) misc[x] = 0xFFFFFFFFu;
     fence_mbar_init();
   }
@@ -360,22 +344,31 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
   }
   const uint32_t tmem = misc[0];
 
-  // Segment s of the part as its readers see it; false: no more, or gave up.
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_long(bar, parity, &misc[2]); };
+  // A wait for the end of a segment, of any number of tiles: again as long as tiles are issued meanwhile.
+  auto wait_segment = [&](uint64_t* bar, uint32_t parity) -> bool {
+    for (uint32_t issued = misc[3];;) {
+      if (wait(bar, parity)) return true;
+      if (misc[2] || misc[3] == issued) return false;
+      issued = misc[3];
+    }
+  };
+  // Segment s of the part as its readers see it; false: no more, or gave up.  (The planner may be waiting for a slot.)
   bool ok = true;
   auto next_seg = [&](int s, Seg& g) -> bool {
     const int slot = s % kSegSlots;
-    if (misc[2] || !wait4(&bars[kBarSegFull + slot], (s / kSegSlots) & 1)) { ok = false; return false; }
+    if (misc[2] || !wait_segment(&bars[kBarSegFull + slot], (s / kSegSlots) & 1)) { ok = false; return false; }
     g = segs[slot];
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars[kBarSegEmpty + slot]);
     return g.b >= 0;
   };
   // Tile j of the part is in buffer j & 1, use number j >> 1 of it (K and V: of kKBufs and kVBufs); segment s likewise.
-  auto done = [&](int bar, int j) { return wait4(&bars[bar + (j & 1)], (j >> 1) & 1); };
+  auto done = [&](int bar, int j) { return wait(&bars[bar + (j & 1)], (j >> 1) & 1); };
   constexpr int kKBufs = k_bufs(kN);
   constexpr uint32_t kColS = col_s(kN), kColO = col_o(kN);
   static_assert(kColO + 4 * kN <= kTmemCols, "TMEM columns");
-  auto used_before = [&](int bar, int j) { return wait4(&bars[bar + (j & 1)], ((j >> 1) & 1) ^ 1); };  // (first use: at once)
+  auto used_before = [&](int bar, int j) { return wait(&bars[bar + (j & 1)], ((j >> 1) & 1) ^ 1); };  // (first use: at once)
   // numbers of the rows (see Lay4)
   float* rows = rowf;
   int* rowi = reinterpret_cast<int*>(rows + 2 * kBlock);    // [parity] drafted token of the row, -1: no row
@@ -449,7 +442,7 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
         copy_wait<kDepth - 1>();
         uint32_t scales[D / 64];
         load_scales<D>(slot + slot_scales, scales);
-        if (!wait4(&bars[free_bar + buf], (use & 1) ^ 1)) { ok = false; break; }
+        if (!wait(&bars[free_bar + buf], (use & 1) ^ 1)) { ok = false; break; }
         tc_fence_after();
         uint8_t* v = sm + Ly::kV + buf * Ly::kTile + r * 128;
 #pragma unroll 1
@@ -514,7 +507,7 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
           pos += g.t1 - g.t0;
         }
         const int slot = s % kSegSlots;
-        if (misc[2] || !wait4(&bars[kBarSegEmpty + slot], ((s / kSegSlots) & 1) ^ 1)) { ok = false; break; }
+        if (misc[2] || !wait_segment(&bars[kBarSegEmpty + slot], ((s / kSegSlots) & 1) ^ 1)) { ok = false; break; }
         if (lane == 0) {
           segs[slot] = g;
           mbar_arrive(&bars[kBarSegFull + slot]);
@@ -531,11 +524,11 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
       int j = 0;
       Seg g;
       for (int s = 0; j < cnt && next_seg(s, g); ++s) {
-        if (!wait4(&bars[kBarQFull + (s & 1)], (s >> 1) & 1)) { ok = false; break; }
+        if (!wait(&bars[kBarQFull + (s & 1)], (s >> 1) & 1)) { ok = false; break; }
         const uint64_t q = dq + (uint64_t)((s & 1) * (Ly::kQTile >> 4));
         for (int t = g.t0; t < g.t1; ++t, ++j) {
           const int buf = j & (kKBufs - 1), use = kKBufs == 4 ? j >> 2 : j >> 1;
-          if (!wait4(&bars[kBarKFull + buf], use & 1) || !used_before(kBarSEmpty, j)) { ok = false; break; }
+          if (!wait(&bars[kBarKFull + buf], use & 1) || !used_before(kBarSEmpty, j)) { ok = false; break; }
           tc_fence_after();
           if (leader) {
 #pragma unroll 2
@@ -562,7 +555,7 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
         if (!used_before(kBarOFree, s)) { ok = false; break; }
         const uint32_t o = tmem + kColO + 2 * kN * (s & 1);
         for (int t = g.t0; t < g.t1; ++t, ++j) {
-          if (!wait4(&bars[kBarVFull + buf], use & 1) || !done(kBarPFull, j)) { ok = false; break; }
+          if (!wait(&bars[kBarVFull + buf], use & 1) || !done(kBarPFull, j)) { ok = false; break; }
           tc_fence_after();
           if (leader) {
             const bool more = t - g.t0 >= 2;  // not the first of its group in the segment
@@ -573,6 +566,7 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
             mma_commit(&bars[kBarPV + (j & 1)]);
             mma_commit(&bars[kBarVFree + buf]);
             if (t + 1 == g.t1) mma_commit(&bars[kBarODone + (s & 1)]);
+            misc[3] = j + 1;
           }
           __syncwarp();
           if (++buf == kVBufs) buf = 0, ++use;
@@ -645,7 +639,7 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
         const int full = min(kBlock, A.R), width = min(kBlock, A.R - kBlock * g.rb);
         const int64_t slot = 2 * (int64_t)blockIdx.x + (g.r0 > 0 ? 0 : 1);
         const int64_t grow = (int64_t)(g.b * A.Hq + g.kvh * (A.Hq / A.Hkv)) * A.n + kBlock * g.rb;
-        if (!done(kBarSums, s)) { ok = false; break; }
+        if (!wait_segment(&bars[kBarSums + par], (s >> 1) & 1)) { ok = false; break; }
         if (tid < kR) {
           // both groups' sums and products at the larger reference
           const float* last = rows + kRowLast + 2 * set + tid;
@@ -667,7 +661,7 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[kBarOut]);
-        if (!wait4(&bars[kBarOut], outs++ & 1) || !done(kBarODone, s)) { ok = false; break; }
+        if (!wait(&bars[kBarOut], outs++ & 1) || !done(kBarODone, s)) { ok = false; break; }
         tc_fence_after();
         // (a segment of one tile has one group's products)
         const int end = (j0 + tiles - 1) & 1;
@@ -717,7 +711,7 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kBarGroup + H]);
     };
-    auto group_wait = [&]() { return wait4(&bars[kBarGroup + H], syncs++ & 1); };
+    auto group_wait = [&]() { return wait(&bars[kBarGroup + H], syncs++ & 1); };
     auto group_sync = [&]() {
       group_arrive();
       return group_wait();
@@ -737,7 +731,7 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
       uint64_t l[kR / 2];  // sums of this key's lane, rows in pairs
 #pragma unroll
       for (int r = 0; r < kR / 2; ++r) l[r] = pk2(0.f, 0.f);
-      if (!wait4(&bars[kBarQFull + (s & 1)], (s >> 1) & 1) || !group_sync()) { ok = false; break; }
+      if (!wait(&bars[kBarQFull + (s & 1)], (s >> 1) & 1) || !group_sync()) { ok = false; break; }
       const float* f = rowf + set;
       const uint32_t tO = tmem + lane_base + kColO + 2 * kN * (s & 1) + kN * H;
       const int tiles = g.t1 - g.t0, first = (j0 ^ H) & 1;  // the group's first tile of them
@@ -945,7 +939,7 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
     if (warp == Ro::kIssueQK || warp == Ro::kIssuePV) {
       uint64_t* drained = &bars[kBarDrain + (warp == Ro::kIssueQK ? 0 : 1)];
       if (elect_one()) mma_commit(drained);
-      wait4(drained, 0, kDrainPolls);
+      mbar_wait_long(drained, 0, nullptr, MSA_WAIT_LIMIT_NS / 16);
     }
     __syncthreads();
   }

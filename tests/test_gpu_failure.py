@@ -65,3 +65,18 @@ def test_bad_block_index_reports_index_error(cuda_lib):
     cfg = dict(pattern=oracle.BLOCK, block=64, topk=topk)
     ro, rl, _ = oracle.head_rows(cfg, qn, kn, vn, np.arange(n), scale_of(d), J=J, cnt=C)
     compare_rows(f32(o[0, 0]), f32(lse[0, 0]), ro, rl, "after index error")
+
+
+@pytest.mark.parametrize("limit_ms", [40, 300])
+def test_every_wait_keeps_its_limit(cuda_lib, limit_ms):
+    """Polling waits and those that suspend run out after the time that is given, however long a poll takes, and one
+    without a short limit ends soon after another role gave up."""
+    cuda_lib.check_wait_timeout(1)  # (loads the kernel)
+    assert cuda_lib.poll_device_status() == MSA_ERR_DEVICE_TIMEOUT
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    a.record()
+    cuda_lib.check_wait_timeout(limit_ms)
+    b.record()
+    assert cuda_lib.poll_device_status() == MSA_ERR_DEVICE_TIMEOUT
+    # 16 polls of some microseconds (3.8 measured) between two looks at the clock
+    assert limit_ms <= a.elapsed_time(b) <= limit_ms + 20
