@@ -1053,9 +1053,9 @@ def kv4_gather(pages: KV4Pages, page_table, seq_len, n: int, k=None, v=None, str
     """msa_kv4_gather: the first min(seq_len[b], n) cached tokens of every
     request to (k, v) [B, Hkv, n, d] bf16; the rows behind them keep what a
     given k and v hold, and are zero otherwise."""
-    data = _kv4(pages).data
-    dev, H, d, n = data.device, data.shape[1], pages.d, int(n)
-    c = pages.view(None, d, dev)
+    data, d, n = _kv4(pages).data, pages.d, int(n)
+    c = pages.view(None, d, getattr(data, "device", None))
+    dev, H = data.device, data.shape[1]
     if n < 1 or n >> 31:
         raise ValueError(f"n: {n}")
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:

@@ -987,3 +987,20 @@ def test_append_infinities_and_values_past_any_scale(cuda_lib, d, rot, inter, ks
     assert cuda_lib.poll_device_status() == 0
     ref, _ = norm_rope(k, None, False, 0.0, rot, _freq(rot), inter, pos)
     _check_held_with_nan(pages.data, page, d, slots, ref, v.double(), ks, vs)
+
+
+def test_replaced_data_is_checked_by_every_call():
+    """KV4Pages.data in whose place something else was put: a ValueError that names it, from each of the calls."""
+    i32 = dict(dtype=torch.int32)
+    q, x = torch.zeros(2, 4, 3, 64, dtype=BF), torch.zeros(2, 5, 8, 64, dtype=BF)
+    qi, ki, vi = x.split([4, 2, 2], 2)
+    table, lens = torch.zeros(2, 4, **i32), torch.ones(2, **i32)
+    cfg, slots = msa.rope_cfg(64), torch.zeros(10, **i32)
+    pages = msa.KV4Pages.empty(9, 2, 16, 64, "cpu")
+    for data, what in ((None, "data: a 3-d"), (torch.zeros(9, dtype=torch.uint8), "data: a 3-d"),
+                       (torch.zeros(9, 2, 16 * 72), "data: dtype"), (torch.zeros(9, 2, 7, dtype=torch.uint8), "data: shape")):
+        pages.data = data
+        for call in (lambda: msa.kv4_gather(pages, table, lens, 8), lambda: msa.attn_tree_kv4(q, pages, table, lens),
+                     lambda: msa.qk_norm_rope_kv4(qi, ki, vi, cfg, pages, slots)):
+            with pytest.raises(ValueError, match=what):
+                call()
