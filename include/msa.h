@@ -544,8 +544,11 @@ typedef struct {
 /* msa_qk_norm_rope and its varlen form with the 4-bit cache in place of the
  * bf16 pages (pages, slots and v_in are required; k and v, nullable, are the
  * layer's in bf16, not the cached values).  What a slot holds is what the
- * definition gives in exact arithmetic, but for values within 2^-40 of a
- * border between two codes or scales. */
+ * definition gives in exact arithmetic, but for values so near a border
+ * between two codes or scales that (2^-40 + |position| * 2^-60) of their
+ * pair's size (the sum of both magnitudes) takes them across.  The norm's sum
+ * of squares is fp32: it has to stay within its range (|x| < 2^60; with eps
+ * below 2^-100 also a mean of squares above 2^-100), as in the layer's keys. */
 MSA_API msa_status msa_qk_norm_rope_kv4(const msa_shape* shape, const msa_rope_cfg* cfg, const void* q_in,
                                         int64_t q_stride, const void* k_in, int64_t k_stride, const void* v_in,
                                         int64_t v_stride, const int32_t* positions, void* q, void* k, void* v,

@@ -1004,3 +1004,43 @@ def test_replaced_data_is_checked_by_every_call():
                      lambda: msa.qk_norm_rope_kv4(qi, ki, vi, cfg, pages, slots)):
             with pytest.raises(ValueError, match=what):
                 call()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("inter,norm", [(False, True), (True, False)])
+def test_append_at_far_positions(cuda_lib, inter, norm):
+    """Positions up to 2^31 - 1 and negative ones.  An angle is off by |position| 2^-60 (its frequency by two units of
+    2^-64 turns: 2 pi 2^-63 < 2^-60), the sums by 2^-40 of a pair's size: codes and scales are those of a value that near
+    the exact one, and nearly all are the exact one's."""
+    tok, Hq, Hkv, d, page = 512, 4, 4, 128, 64
+    q, k, v, w = _inputs(tok, Hq, Hkv, d, 91)
+    rng = np.random.default_rng(9)
+    p = rng.integers(-(1 << 31), 1 << 31, tok)
+    p[:4] = [0, (1 << 31) - 1, -(1 << 31), -1]
+    pos = torch.from_numpy(p.astype(np.int32)).cuda()
+    # multiples of 2^-20: position * f is exact in 64 bits, so the reference has the true angle (as have its sines)
+    freq = (rng.integers(-(1 << 20), 1 << 20, d // 2) / 2.0 ** 20).tolist()
+    eps = torch.tensor(1e-6, dtype=torch.float32).double().item()
+    cfg = msa.rope_cfg(d, norm=norm, interleaved=inter, inv_freq=freq, k_weight=w[1] if norm else None)
+    pages = msa.KV4Pages.empty(tok // page, Hkv, page, d, "cuda")
+    slots = torch.arange(tok, dtype=torch.int32, device="cuda")
+    msa.qk_norm_rope_kv4(q[None], k[None], v[None], cfg, pages, slots, positions=pos)
+    assert cuda_lib.poll_device_status() == 0
+    y, slack = norm_rope(k, w[1] if norm else None, norm, eps, d, freq, inter, pos)
+    size = slack / (2.0 ** -24 * 32)  # of the value's pair
+    e = size * (2.0 ** -40 + pos.double().abs()[:, None, None] * 2.0 ** -60)
+    held = kv4_values(pages.data, page, d)[0].transpose(1, 2).reshape(tok, Hkv, d)
+    scales = pages.data[..., page * d // 2:page * (d // 2 + d // 16)].unflatten(-1, (page, d // 16)).transpose(1, 2)
+    scales = scales.contiguous().view(torch.float8_e4m3fn).double().reshape(tok, Hkv, d // 16)
+    # a block's scale lies between those of its values less and more what they may be off
+    low, high = (kv4_round(torch.copysign((y.abs() + x).clamp(min=0), y))[2].view(torch.float8_e4m3fn).double() for x in (-e, e))
+    assert bool((low <= scales).all()) and bool((scales <= high).all())
+    s = scales.repeat_interleave(16, -1)
+
+    def code(x):  # the e2m1 number nearest x / s
+        t = (x / s).clamp(-6, 6)
+        unit = torch.where(t.abs() < 2, 0.5, torch.where(t.abs() < 4, 1.0, 2.0))
+        return torch.round(t / unit) * unit
+
+    assert bool((s > 0).all()) and bool((code(y - e) <= held / s).all()) and bool((held / s <= code(y + e)).all())
+    assert float((held == kv4_round(y)[0]).double().mean()) > 0.9999
