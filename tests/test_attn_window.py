@@ -322,3 +322,24 @@ def test_streams_capture_and_workspace(cuda_lib):
         torch.cuda.synchronize()
         c.check((o, lse, o, lse), what=f"replay {lens}", lens=lens)
     assert cuda_lib.poll_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sink,window", [(0, 100), (3, 64), (200, 300), (128, 1024)])
+@pytest.mark.parametrize("Hq,Hkv,n,d,page", [(4, 1, 20, 64, 32), (8, 2, 32, 64, 16), (6, 2, 2, 64, 64), (8, 8, 100, 128, 128),
+                                             (4, 1, 16, 128, 16), (5, 1, 27, 64, 16)])
+def test_ragged_windows_of_every_row_layout(cuda_lib, Hq, Hkv, n, d, page, sink, window):
+    """6 to 135 rows a KV head, both sides of 64 and 128, heads of 64 with 65 to 128 rows among them; requests with
+    fewer drafted tokens than rows."""
+    rng = np.random.default_rng(n + window)
+    lens = n + np.array([0, 1, 130, 700, 1500, 6000])
+    tls = [n, 1, n // 2, n, 0, n - 1]
+    for masked in (False, True):
+        masks = depths = None
+        if masked:
+            masks = np.stack([tree_bits(rng, n) for _ in lens])
+            depths = masks.sum(-1) - 1
+        c = Case(Hq, Hkv, n, d, page, lens, sink, window, sink + window + d, tls=tls, masks=masks, depths=depths)
+        out = c.run()
+        assert cuda_lib.poll_device_status() == 0
+        c.check(out, what=f"window {sink}+{window} masked {masked}")

@@ -1044,3 +1044,46 @@ def test_append_at_far_positions(cuda_lib, inter, norm):
 
     assert bool((s > 0).all()) and bool((code(y - e) <= held / s).all()) and bool((held / s <= code(y + e)).all())
     assert float((held == kv4_round(y)[0]).double().mean()) > 0.9999
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sink,window", [(0, 100), (3, 64), (200, 300), (128, 1024)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv,n,page", [(6, 2, 2, 32), (8, 2, 3, 16), (4, 1, 4, 64), (4, 1, 5, 128), (4, 1, 8, 16), (4, 1, 12, 32)])
+def test_windows_of_every_row_width(cuda_lib, Hq, Hkv, n, page, d, sink, window):
+    """6, 12, 16, 20, 32 and 48 rows a KV head, whole and ragged, in products of 8, 16, 32 and 64 rows."""
+    rng = np.random.default_rng(n + window)
+    lens = n + np.array([0, 1, 130, 700, 1500, 6000])
+    for masked in (False, True):
+        masks = depths = None
+        if masked:
+            masks = np.stack([tree_bits(rng, n) for _ in lens])
+            depths = masks.sum(-1) - 1
+        tls = [n, 1, max(1, n // 2), n, 0, n - 1]
+        c = Cache(Hq, Hkv, n, d, page, lens, sink + window + d, tls=tls, masks=masks, depths=depths, sink=sink, window=window)
+        out = c.run()
+        assert cuda_lib.poll_device_status() == 0
+        c.check(out, what=f"window {sink}+{window} masked {masked}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,d", [(128, 128), (1024, 64), (200, 128)])
+def test_the_next_chunk_of_a_prompt(cuda_lib, n, d):
+    """Many tokens behind a cached prefix, without a window: every row against the definition over what the cache holds,
+    and the chunk read back and attended to by the prefill's dense kernel."""
+    Hq, Hkv, page = 4, 2, 32
+    L = 1003
+    c = Cache(Hq, Hkv, n, d, page, [L + n, n], n + d)
+    out = c.run()
+    assert cuda_lib.poll_device_status() == 0
+    c.check(out, what="chunk")
+    K, V = msa.kv4_gather(c.pages, c.table_dev, c.lens_dev, L + n)
+    Q = torch.zeros(1, Hq, L + n, d, dtype=BF, device="cuda")
+    Q[:, :, L:] = c.q[:1]
+    dense_lse = torch.zeros(1, Hq, L + n, device="cuda")
+    dense = msa.attn_dense(Q, K[:1], V[:1], list(range(Hq)), lse=dense_lse)
+    assert cuda_lib.poll_device_status() == 0
+    # the same rows by the prefill's kernel, whose weights are bf16
+    rows, lse = dense[:, :, L:].contiguous(), dense_lse[:, :, L:].contiguous()
+    check_rows(c.q[:1], lambda b, h: Hkv if h is None else K[0, h], lambda b, h: V[0, h], [L + n], [n],
+               lambda b: seen_keys(L + n, n), rows, lse, rows, lse, what="dense")
