@@ -81,8 +81,8 @@ struct Seqs<false> {};
 struct Token {
   int32_t seq0, n, i;  // first token and length of its sequence, index in it
   int32_t slot;        // cache slot, < 0: not stored
-  int32_t pos;         // kKv4
 };
+static_assert(sizeof(Token) == 16, "one load of shared memory");
 
 // 8 bf16 values (16 bytes) as four pairs
 __device__ __forceinline__ void unpack8(uint4 u, uint64_t (&f)[4]) {
@@ -344,7 +344,8 @@ __global__ void __launch_bounds__(kThreads, 4)
   // on one bank): value x of lane l at 4 (l + (x / 4) lanes) + x % 4.
   __shared__ __align__(16) float cosines[kMaxTokens][D / 2], sines[kMaxTokens][D / 2];
   __shared__ __align__(16) float weights[2][2][D / 2];  // [q or k][chunk]
-  __shared__ Token toks[kMaxTokens];
+  __shared__ __align__(16) Token toks[kMaxTokens];
+  __shared__ int32_t places[kKv4 ? kMaxTokens : 1];  // kKv4: their positions
   // kKv4: the largest values of a head's chunks of 8, and how far they may be off
   __shared__ float2 tops[kKv4 ? kHeads : 1][kKv4 ? D / 8 : 1];
   const int tid = threadIdx.x;
@@ -404,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 4)
       k.n = A.n;
     }
     k.i = tk - k.seq0;
-    if constexpr (kKv4) k.pos = A.positions ? A.positions[tk] : k.i;
+    if constexpr (kKv4) places[tid] = A.positions ? A.positions[tk] : k.i;
     k.slot = -1;
     if (A.slots) {
       k.slot = A.slots[tk];
@@ -565,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 4)
       round_chunk(b, 1, c1, off1);
       const bool again = far[0] || far[1];
       if (__any_sync(group, again || (unsure[0] | unsure[1]) != 0)) {  // K only
-        Again<D> g = {A, top, A.k + (first + t) * A.k_stride + kh * D, group, tk.pos, {c0, c1}, inv, {off0, off1}};
+        Again<D> g = {A, top, A.k + (first + t) * A.k_stride + kh * D, group, places[t], {c0, c1}, inv, {off0, off1}};
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
 #pragma unroll
