@@ -1087,3 +1087,87 @@ def test_the_next_chunk_of_a_prompt(cuda_lib, n, d):
     rows, lse = dense[:, :, L:].contiguous(), dense_lse[:, :, L:].contiguous()
     check_rows(c.q[:1], lambda b, h: Hkv if h is None else K[0, h], lambda b, h: V[0, h], [L + n], [n],
                lambda b: seen_keys(L + n, n), rows, lse, rows, lse, what="dense")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,n,B", [(2, 1, 1, 2600), (4, 1, 12, 1700)])
+@pytest.mark.parametrize("window", [0, 150])
+def test_more_requests_than_threads(cuda_lib, Hq, Hkv, n, B, window):
+    """Several requests for each thread that adds up the tiles, some of them empty."""
+    rng = np.random.default_rng(B + window)
+    tls = rng.integers(0, n + 1, B) if n > 1 else (rng.random(B) < 0.9).astype(int)
+    c = Cache(Hq, Hkv, n, 64, 16, tls + rng.integers(0, 300, B), B, tls=tls, sink=5 if window else 0, window=window)
+    out = c.run()
+    assert cuda_lib.poll_device_status() == 0
+    c.check(out, what=f"{B} requests")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,n,d", [(4, 2, 6, 128), (2, 1, 40, 64)])
+def test_masks_of_windows(cuda_lib, Hq, Hkv, n, d):
+    """One mask for all requests, depths with it and without (a row's index stands in), rows whose mask names nothing
+    and whose window holds nothing."""
+    rng = np.random.default_rng(3)
+    m = rng.random((n, n)) < 0.3
+    m[1] = m[n - 1] = False
+    lens = [n, n + 1, n + 5, n + 700, n + 130, n + 2000]
+    tls = [n, n, n - 1, n, n // 2, n]
+    for depths in (None, np.tile(rng.integers(0, n, n), (len(lens), 1))):
+        for sink, window in ((0, 1), (2, 3), (0, 300), (130, 200)):
+            c = Cache(Hq, Hkv, n, d, 16, lens, 7, tls=tls, masks=m, depths=depths, sink=sink, window=window)
+            out = c.run()
+            assert cuda_lib.poll_device_status() == 0
+            c.check(out, what=f"masks {sink}+{window}")
+    assert bool(torch.isneginf(out[1][0, :, 1]).all())  # no context, no drafted key
+
+
+@pytest.mark.gpu
+def test_two_graphs_of_one_workspace(cuda_lib):
+    """Captured calls of different shapes that share a workspace, replayed in turn, and an eager one between."""
+    a = Cache(4, 1, 8, 128, 64, [40000, 300], 1)
+    b = Cache(8, 2, 20, 64, 16, [3000, 9000, 21], 2, sink=16, window=600)
+    want = [c.run() for c in (a, b)]
+    ws = torch.empty(max(msa.attn_tree_kv4_workspace(len(c.lens), *c.q.shape[1:2], c.Hkv, *c.q.shape[2:]) for c in (a, b)),
+                     dtype=torch.uint8, device="cuda")
+    graphs, outs = [], []
+    for c in (a, b):
+        graph = torch.cuda.CUDAGraph()
+        c.run(ws=ws)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            outs.append(c.run(ws=ws))
+        graphs.append(graph)
+    for x in (0, 1, 1, 0, 0, 1, 0):
+        for t in outs[x][:2]:
+            t.zero_()
+        graphs[x].replay()
+        y = (a, b)[x ^ 1].run(ws=ws)
+        torch.cuda.synchronize()
+        for got, ref in ((outs[x], want[x]), (y, want[x ^ 1])):
+            assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1]), x
+    assert cuda_lib.poll_device_status() == 0
+
+
+@pytest.mark.gpu
+def test_append_many_sequences(cuda_lib):
+    """More packed sequences than one launch takes, empty ones among them, positions given and not."""
+    Hq, Hkv, d, page = 2, 1, 64, 16
+    rng = np.random.default_rng(2)
+    lens = rng.integers(0, 6, 2500)
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    tok = int(cu[-1])
+    q, k, v, w = _inputs(tok, Hq, Hkv, d, 8)
+    N = -(-tok // page) + 1
+    slots = torch.from_numpy(rng.permutation(N * page)[:tok].astype(np.int32)).cuda()
+    cfg = msa.rope_cfg(d, norm=True, q_weight=w[0], k_weight=w[1])
+    eps = torch.tensor(1e-6, dtype=torch.float32).double().item()
+    own = torch.from_numpy((np.arange(tok) - np.repeat(cu[:-1], lens)).astype(np.int32)).cuda()
+    for pos in (None, torch.from_numpy(rng.integers(0, 100000, tok).astype(np.int32)).cuda()):
+        pages = msa.KV4Pages.empty(N, Hkv, page, d, "cuda")
+        before = pages.data.clone()
+        qo, _, _ = msa.qk_norm_rope_varlen_kv4(q, k, v, cu, cfg, pages, slots, positions=pos)
+        want, _, _ = msa.qk_norm_rope_varlen(q, k, v, cu, cfg, positions=pos)
+        assert cuda_lib.poll_device_status() == 0
+        assert torch.equal(qo, want)
+        ref, _ = norm_rope(k, w[1], True, eps, d, _freq(d), False, own if pos is None else pos)
+        _check_held(pages.data, page, d, slots, ref, v.double(), before)
