@@ -41,21 +41,23 @@
 //
 // Measured (one launch and its join, captured, inputs larger than the L2; floor =
 // bytes at 6.8 TB/s): 64 requests of 1K to 16K tokens, one row group of 4
-// (32/8 heads of 128) 114 us (floor 53; the bf16 cache's 188); one request of a
-// million tokens, 20 rows, 381 (178); 16 requests of 4K to 32K tokens with trees of
-// 48 (192 rows: three passes over the codes) 451 to 460 (66); of 16 (64 rows) 166 (34),
-// of 8 (32 rows) 109 (33); 256 requests of 100 to 1000 tokens 122 (17); heads of 64 95 (26); through 128 + 1024
-// keys 54 (13); one of 2047 tokens, 2 / 1 heads of 64, 14.
+// (32/8 heads of 128) 110 us (floor 53; the bf16 cache's 188); one request of a
+// million tokens, 20 rows, 374 (178); 16 requests of 4K to 32K tokens with trees of
+// 48 (192 rows: three passes over the codes) 431 (66); of 16 (64 rows) 154 (34),
+// of 8 (32 rows) 100 (33); 256 requests of 100 to 1000 tokens 121 (17); heads of 64 94 (26); through 128 + 1024
+// keys 53 (13); one of 2047 tokens, 2 / 1 heads of 64, 13.4.  The next 1024 tokens behind 128K
+// (4096 rows: 64 passes) 4149 (1154, of operations; the bf16 cache 1559), behind 16K 614 (152; 245).
 //
 // What bounds it now: 16 warps that decode issue about 300 instructions for 32 keys of
 // K or V (16 conversions and 16 products a 32 channels, at half rate each), 600 of a
-// scheduler's 1400 cycles a tile with 8 rows; the schedulers issue 0.67 a cycle, the
+// scheduler's 1350 cycles a tile with 8 rows; the schedulers issue 0.72 a cycle, the
 // rest is instruction fetch (eight roles) and waits for each other.  With 64 rows a
-// softmax group's chain, 3300 cycles a tile: scores 300, first pass 600, vote
-// 250, weights 900, raises 600 where references are passed often.
+// softmax group's chain, 3300 cycles a tile (taken when 192 rows were at 451 us): scores 300,
+// first pass 600, vote 250, weights 900, raises 600 where references are passed often.
 //
-// Tried and slower: codes through a ring of bulk copies with a loading warp (121 us for
-// 114 in the decode case: one more hand-over a tile, and its warp's waits), or loaded into
+// Tried and slower (the two cases were at 114 and 451 us then): codes through a ring of bulk
+// copies with a loading warp (121 us for 114 in the decode case: one more hand-over a tile,
+// and its warp's waits), or loaded into
 // registers a tile ahead (spills); one softmax group for all tiles (139 us; 64 rows and
 // 24 warps were even: 450); the chunk loop of the decode unrolled twice (118 us: fetch);
 // raising only the rows whose reference was passed (557 us for 451 with 192 rows: the
@@ -778,7 +780,7 @@ __global__ void __launch_bounds__(Roles<kR>::kThreads, 1) kv4_attn_kernel(const 
             see[x] = bits;
           }
         }
-        // kR = 32 and 64: scores by halves (all of them and the sums in registers spill: 32 rows 116 us for 108).  The
+        // kR = 32 and 64: scores by halves (all of them and the sums in registers spill: 32 rows 116 us for 108 then).  The
         // second is read from TMEM again for its weights; of 64 rows the first is too (451 us, 475 where it is kept)
         constexpr int kC = kR >= 32 ? kR / 2 : kR;
         constexpr bool kKeep = kR < 64;

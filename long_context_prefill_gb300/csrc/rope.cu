@@ -20,10 +20,12 @@
 // "4-bit pages" below, the layer's layout as without it.
 //
 // What bounds it: HBM, every value read once and written once per
-// destination.  4-bit pages: issue, 187 us for the 32K tokens that take 151 into bf16
-// pages (165 without the second computation of the heads in question, which
-// is out of line: inlined, its registers spilled and cost 70 us); 64 tokens of a decode
-// step 11 us, most of it the sines' and the exact path's chains.  A lane holds both members of its pairs (two 16-byte chunks, a
+// destination.  4-bit pages: issue, 188 us for the 32K tokens that take 151 into bf16
+// pages (of which the second computation of the heads in question is 22; it
+// is out of line: inlined, its registers spilled and cost 70 us), 135 for 23K packed ones; 64 tokens of a decode
+// step 8.3 us one after another and 12.8 behind other kernels with the caches cold, most of it the sines' and the exact
+// path's chains (without a head in question 4.7 and 10.7, with a block's scale in question, three steps of ten, 9.2 and
+// 14.8).  A lane holds both members of its pairs (two 16-byte chunks, a
 // head in 8 lanes for d_h = 128), so the rotation needs no exchange and the
 // norm three shuffles; the cosines of a token are computed once per CTA and
 // serve all its heads.

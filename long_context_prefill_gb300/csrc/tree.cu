@@ -73,8 +73,8 @@
 // and slower there (against 162 to 174 us): a score tile per group with P over it
 // 194 us, turns of the groups on a scheduler 192 to 253 us, scores by halves of 64
 // keys 208 us, products held back while scores are computed 175 us.
-// Windows: decode of the same 64 requests through 128 + 1024 keys 58 us (floor 44), 16
-// trees of up to 48 through 64 + 512 35 us (floor 7.4: 8 tiles a CTA, joins 5), 1024 rows of
+// Windows: decode of the same 64 requests through 128 + 1024 keys 59 us (floor 44), 16
+// trees of up to 48 through 64 + 512 35 us (floor 7.4: 5.5 tiles a CTA, in items of 6 or 7, joins 5), 1024 rows of
 // a prompt's chunk through 128 + 1024 of 128K 46 us (floor 10, of operations: 12 tiles of 256
 // rows for each of 128 items, 10 a CTA, 2.4 us a tile where the rows' ends are masked; joins 10).
 #include <type_traits>
